@@ -72,6 +72,10 @@ extern "C" {
 #define PKV_STATUS_NO_FINITE_KEY      (1u << 5) /* sample: every key of a row is NaN           */
 #define PKV_STATUS_WORKSPACE_OVERFLOW (1u << 6) /* more work items than the workspace holds   */
 #define PKV_STATUS_WAIT_TIMEOUT       (1u << 7) /* a bounded in-kernel wait gave up           */
+#define PKV_STATUS_BAD_SCALE          (1u << 8) /* an e4m3 cache's scale cannot be used        */
+#define PKV_STATUS_BAD_TOKEN_ID       (1u << 9) /* logit rules: a token id >= vocab            */
+#define PKV_STATUS_BAD_PENALTY        (1u << 10) /* logit rules: a penalty is not usable       */
+#define PKV_STATUS_NO_ALLOWED_TOKEN   (1u << 11) /* logit rules: a row's mask leaves nothing   */
 
 /* One layer's KV cache geometry: k_cache/v_cache are [num_blocks, block_size,
  * num_kv_heads, head_dim] bf16. */
@@ -385,6 +389,174 @@ PKV_API int pkv_sample(const float* logits, const float* temperatures, const flo
 PKV_API int pkv_sample_philox(const float* logits, const float* temperatures, uint64_t seed,
                               uint64_t offset, int32_t batch, int32_t vocab,
                               int32_t* out_token_ids, uint32_t* status, void* stream);
+
+/*
+ * ---- an 8-bit KV cache ---------------------------------------------------
+ * (No counterpart on the pages, whose cache is bf16: half the cache bytes of
+ * a decode step and twice the tokens in the same memory.)
+ *
+ *   k_cache, v_cache  [num_blocks, block_size, num_kv_heads, head_dim] e4m3
+ *                     codes (1 sign, 4 exponent, 3 fraction bits, largest 448)
+ *   k_scale, v_scale  [num_blocks, num_kv_heads] fp32: an entry's value is its
+ *                     code times the scale of its block and kv head
+ * block_size is at most PKV_FP8_MAX_BLOCK_SIZE, head_dim 64 or 128.  Attention
+ * takes any scale in [2^-100, FLT_MAX].  A scale outside it (0 marks a block
+ * without rows) sets PKV_STATUS_BAD_SCALE where a key needs it.
+ */
+#define PKV_FP8_MAX_BLOCK_SIZE 1024
+
+/*
+ * Bytes of device workspace pkv_kv_store_fp8 needs (a pure host function; 0
+ * for small calls, which may pass a NULL workspace).
+ */
+PKV_API size_t pkv_kv_store_fp8_workspace_bytes(int32_t num_tokens, pkv_cache_desc cache);
+
+/*
+ * kv_store into an e4m3 cache.  Arguments as in pkv_kv_store (k, v bf16), with
+ * the cache's scales read and written.  For each (block, kv head) that gets rows
+ * in this call, of K and of V, with c the scale before the call:
+ *   c' = max(c, 2^e), e the least integer with max|x| <= 448 * 2^e over the
+ *        finite entries x of those rows, clamped to [-64, 119];
+ *   the rows' codes are x / c' rounded to nearest-even; magnitudes above 448
+ *        (infinities) become 448, NaN stays NaN;
+ *   if c' > c, the codes of the block's other rows become code * (c / c'),
+ *        rounded the same way.
+ * A row at offset 0 begins the block anew, as a sequence fills its blocks in
+ * order: c counts as 0 then and the block's other rows are left as they were.
+ * c = 0 likewise; any other c outside [2^-100, FLT_MAX] sets PKV_STATUS_BAD_SCALE and
+ * counts as 0.  Tokens may come in any order; of several tokens with the same
+ * slot the last one is stored.  The result does not depend on timing.
+ *   workspace      device, >= pkv_kv_store_fp8_workspace_bytes(...) bytes,
+ *                  16-byte aligned
+ * Calls that store into the same block must not overlap on the GPU.
+ */
+PKV_API int pkv_kv_store_fp8(const void* k, const void* v, void* k_cache, void* v_cache,
+                             float* k_scale, float* v_scale, const int32_t* slot_mapping,
+                             int32_t num_tokens, void* workspace, size_t workspace_bytes,
+                             pkv_cache_desc cache, uint32_t* status, void* stream);
+
+/*
+ * paged_decode over an e4m3 cache: arguments, workspace
+ * (pkv_paged_decode_workspace_bytes) and result as in pkv_paged_decode, with
+ * K and V rows code * scale.  The keys of a block whose K or V scale cannot be
+ * used are left out, as are those of a block id outside the pool.
+ */
+PKV_API int pkv_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                 const float* k_scale, const float* v_scale,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, int32_t batch,
+                                 int32_t num_q_heads, int32_t max_context_len, float scale,
+                                 void* out, void* workspace, size_t workspace_bytes,
+                                 pkv_cache_desc cache, uint32_t* status, void* stream);
+
+/*
+ * pkv_paged_decode_fp8 with the schedule that pkv_paged_decode_plan (the same
+ * one as for a bf16 cache of this geometry) wrote into the workspace; the
+ * conditions are those of pkv_paged_decode_run.
+ */
+PKV_API int pkv_paged_decode_run_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* context_lens, int32_t batch,
+                                     int32_t num_q_heads, int32_t max_context_len, float scale,
+                                     void* out, void* workspace, size_t workspace_bytes,
+                                     pkv_cache_desc cache, uint32_t* status, void* stream);
+
+/*
+ * kv_store_fp8 then paged_decode_fp8, enqueued as one call; every argument is
+ * checked before anything is enqueued.
+ */
+PKV_API size_t pkv_kv_store_paged_decode_fp8_workspace_bytes(int32_t num_tokens, int32_t batch,
+                                                             int32_t num_q_heads,
+                                                             int32_t max_context_len,
+                                                             pkv_cache_desc cache);
+PKV_API int pkv_kv_store_paged_decode_fp8(
+    const void* k, const void* v, const int32_t* slot_mapping, int32_t num_tokens,
+    const void* q, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t batch, int32_t num_q_heads, int32_t max_context_len, float scale, void* out,
+    void* workspace, size_t workspace_bytes, pkv_cache_desc cache, uint32_t* status,
+    void* stream);
+
+/*
+ * Bytes of device workspace pkv_paged_prefill_varlen_fp8 needs (pure host
+ * function): the tile schedule and the prefixes' rows as bf16, the latter
+ * sized for max_seqlen_k keys of every sequence, up to 4 GiB (beyond that the
+ * batch is attended in groups of sequences that share it; a single sequence
+ * may need more).
+ */
+PKV_API size_t pkv_paged_prefill_fp8_workspace_bytes(int32_t batch, int32_t total_q,
+                                                     int32_t num_q_heads, int32_t max_seqlen_k,
+                                                     pkv_cache_desc cache);
+
+/*
+ * paged_prefill_varlen whose cached prefix lies in an e4m3 cache: arguments
+ * and result as in pkv_paged_prefill_varlen, with prefix rows code * scale
+ * (rounded to bf16, which is exact for power-of-two scales).  The chunk's own
+ * keys are the bf16 rows of k / v.  A prefix row in a block id outside the pool
+ * (PKV_STATUS_BAD_BLOCK_ID) or with a scale that cannot be used
+ * (PKV_STATUS_BAD_SCALE) counts as zeros.  A sequence of more than max_seqlen_k keys
+ * or more cached keys than its table holds sets PKV_STATUS_BAD_SEQLENS and,
+ * where its prefix does not fit, is skipped.
+ */
+PKV_API int pkv_paged_prefill_varlen_fp8(
+    const void* q, const void* k, const void* v, const void* k_cache, const void* v_cache,
+    const float* k_scale, const float* v_scale, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int32_t batch, int32_t total_q, int32_t max_seqlen_q,
+    int32_t max_seqlen_k, int32_t num_q_heads, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, float scale, void* out, void* workspace, size_t workspace_bytes,
+    pkv_cache_desc cache, uint32_t* status, void* stream);
+
+/*
+ * ---- rules on a step's logits, ahead of pkv_sample -----------------------
+ * (No counterpart on the pages, whose sampler takes the model's logits.)
+ */
+#define PKV_FP32 0
+#define PKV_BF16 1
+#define PKV_FP16 2
+
+/* Device arrays; a NULL one (and what belongs to it) is not applied. */
+typedef struct pkv_logit_rules {
+    const int32_t* token_ids;            /* [batch, max_tokens]: prompt, then generated tokens  */
+    const int32_t* prompt_lens;          /* [batch]: prompt tokens of each row; NULL: 0         */
+    const int32_t* token_lens;           /* [batch]: all tokens of each row; NULL: max_tokens   */
+    const float* repetition_penalties;   /* [batch], > 0; NULL: 1                               */
+    const float* presence_penalties;     /* [batch]; NULL: 0                                    */
+    const float* frequency_penalties;    /* [batch]; NULL: 0                                    */
+    const int32_t* bias_offsets;         /* [batch + 1]: row b has biases [off[b], off[b + 1])  */
+    const int32_t* bias_token_ids;       /* [num_biases]                                        */
+    const float* bias_values;            /* [num_biases]                                        */
+    const uint32_t* allowed_mask;        /* [batch, ceil(vocab / 32)]: bit i % 32 of word i / 32 */
+    int32_t max_tokens;
+    int32_t num_biases;
+} pkv_logit_rules;
+
+/*
+ * apply_logit_rules -- for entry i of row b, x = logits[b, i] in fp32, in this
+ * order:
+ *   repetition  if i occurs among the row's tokens: x = x > 0 ? x / r : x * r
+ *   frequency   x -= f * n, n the occurrences among the generated tokens (those
+ *               behind the prompt)
+ *   presence    x -= p if n > 0
+ *   bias        x += the value of the row's last bias for token i
+ *   mask        x = -inf where the token is not allowed
+ *
+ *   logits       device, [batch, vocab] of logits_type (PKV_FP32, PKV_BF16 or
+ *                PKV_FP16), rows logits_stride entries apart
+ *   out          device, [batch, vocab] fp32, contiguous.  May be logits itself
+ *                (fp32, logits_stride == vocab): then entries that no rule changes
+ *                are not written.  Any other overlap is PKV_ERR_UNSUPPORTED.
+ * Token ids < 0 (padding) are skipped; one >= vocab sets PKV_STATUS_BAD_TOKEN_ID and
+ * is skipped.  Inconsistent lengths or bias offsets set PKV_STATUS_BAD_SEQLENS
+ * and that list of the row counts as empty.  A repetition penalty that is not
+ * positive and finite counts as 1, another one that is not finite as 0, and
+ * sets PKV_STATUS_BAD_PENALTY.  A row whose mask allows no token becomes -inf
+ * throughout and sets PKV_STATUS_NO_ALLOWED_TOKEN.
+ */
+PKV_API int pkv_apply_logit_rules(const void* logits, int32_t logits_type,
+                                  int64_t logits_stride, int32_t batch, int32_t vocab,
+                                  pkv_logit_rules rules, float* out, uint32_t* status,
+                                  void* stream);
 
 #ifdef __cplusplus
 }

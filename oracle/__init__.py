@@ -46,6 +46,14 @@ Functions and their pins (all pins are tests under ``tests/`` marked not-gpu):
       Salmon et al., SC 2011); the stream built on it is checked by inverting
       its round, by output statistics, and by the Gumbel-max law of its draws.
 
+  fp8_cache.encode, fp8_cache.kv_store
+      the e4m3 rounding is pinned to PyTorch's float8_e4m3fn conversion over
+      every code, every midpoint and random values; the store to its written
+      rules (bounds of a scale, the error of a stored entry, row by row == at
+      once) on tiny pools.
+  logit_rules.apply
+      pinned to values worked out by hand.
+
 Every function is pinned.
 """
-from . import attention, kv_store, sampler, slots  # noqa: F401
+from . import attention, fp8_cache, kv_store, logit_rules, sampler, slots  # noqa: F401

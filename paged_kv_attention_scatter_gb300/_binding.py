@@ -26,6 +26,10 @@ PKV_STATUS_BITS = {
     1 << 5: "NO_FINITE_KEY",
     1 << 6: "WORKSPACE_OVERFLOW",
     1 << 7: "WAIT_TIMEOUT",
+    1 << 8: "BAD_SCALE",
+    1 << 9: "BAD_TOKEN_ID",
+    1 << 10: "BAD_PENALTY",
+    1 << 11: "NO_ALLOWED_TOKEN",
 }
 STATUS = {v: k for k, v in PKV_STATUS_BITS.items()}
 
@@ -36,7 +40,11 @@ C_FUNCTIONS = ["pkv_version", "pkv_error_string", "pkv_status_string", "pkv_kv_s
                "pkv_kv_store_paged_prefill_varlen", "pkv_paged_decode_plan",
                "pkv_paged_decode_run", "pkv_paged_attention_varlen_workspace_bytes",
                "pkv_kv_store_paged_attention_varlen",
-               "pkv_layer_cache", "pkv_sample_philox", "pkv_set_wait_poll_limit"]
+               "pkv_layer_cache", "pkv_sample_philox", "pkv_set_wait_poll_limit",
+               "pkv_kv_store_fp8_workspace_bytes", "pkv_kv_store_fp8", "pkv_paged_decode_fp8",
+               "pkv_paged_decode_run_fp8", "pkv_kv_store_paged_decode_fp8_workspace_bytes",
+               "pkv_kv_store_paged_decode_fp8", "pkv_paged_prefill_fp8_workspace_bytes",
+               "pkv_paged_prefill_varlen_fp8", "pkv_apply_logit_rules"]
 
 # Size of the scratch array compiled into the library for
 # pkv_paged_decode_static_workspace (PKV_STATIC_DECODE_WORKSPACE_BYTES).
@@ -46,6 +54,14 @@ STATIC_DECODE_WORKSPACE_BYTES = 16 * 1024 * 1024
 class CacheDesc(ctypes.Structure):
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class LogitRules(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("token_ids", "prompt_lens", "token_lens", "repetition_penalties",
+                 "presence_penalties", "frequency_penalties", "bias_offsets", "bias_token_ids",
+                 "bias_values", "allowed_mask")] + \
+               [("max_tokens", ctypes.c_int32), ("num_biases", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -109,6 +125,26 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                     ctypes.POINTER(ctypes.c_void_p)]
     lib.pkv_set_wait_poll_limit.restype = ctypes.c_int
     lib.pkv_set_wait_poll_limit.argtypes = [ctypes.c_uint32]
+    lib.pkv_kv_store_fp8_workspace_bytes.restype = SZ
+    lib.pkv_kv_store_fp8_workspace_bytes.argtypes = [I32, CacheDesc]
+    lib.pkv_kv_store_fp8.restype = ctypes.c_int
+    lib.pkv_kv_store_fp8.argtypes = [P, P, P, P, P, P, P, I32, P, SZ, CacheDesc, P, P]
+    for name in ("pkv_paged_decode_fp8", "pkv_paged_decode_run_fp8"):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [P, P, P, P, P, P, I32, P, I32, I32, I32, F32, P, P, SZ, CacheDesc, P, P]
+    lib.pkv_kv_store_paged_decode_fp8_workspace_bytes.restype = SZ
+    lib.pkv_kv_store_paged_decode_fp8_workspace_bytes.argtypes = [I32, I32, I32, I32, CacheDesc]
+    lib.pkv_kv_store_paged_decode_fp8.restype = ctypes.c_int
+    lib.pkv_kv_store_paged_decode_fp8.argtypes = [P, P, P, I32, P, P, P, P, P, P, I32, P, I32, I32,
+                                                  I32, F32, P, P, SZ, CacheDesc, P, P]
+    lib.pkv_paged_prefill_fp8_workspace_bytes.restype = SZ
+    lib.pkv_paged_prefill_fp8_workspace_bytes.argtypes = [I32, I32, I32, I32, CacheDesc]
+    lib.pkv_paged_prefill_varlen_fp8.restype = ctypes.c_int
+    lib.pkv_paged_prefill_varlen_fp8.argtypes = [P, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32,
+                                                 P, I32, F32, P, P, SZ, CacheDesc, P, P]
+    lib.pkv_apply_logit_rules.restype = ctypes.c_int
+    lib.pkv_apply_logit_rules.argtypes = [P, I32, ctypes.c_int64, I32, I32, LogitRules, P, P, P]
     _LIB = lib
     return lib
 
@@ -502,3 +538,301 @@ def set_wait_poll_limit(polls: int = DEFAULT_WAIT_POLLS) -> None:
     enqueued afterwards (default DEFAULT_WAIT_POLLS).  A diagnostic: 0 makes
     every such wait give up at once, which exercises the kernels' unwinding."""
     _check(load().pkv_set_wait_poll_limit(int(polls) & 0xFFFFFFFF), "pkv_set_wait_poll_limit")
+
+
+# ----------------------------------------------------------------------------
+# The 8-bit KV cache and the logit rules.  These calls run with the tensors'
+# device current, and allocate what they make themselves under `stream` when
+# one is given, so that PyTorch's allocator hands that memory out again only
+# behind the work enqueued there.
+FP8 = torch.float8_e4m3fn
+
+
+def _on(dev, stream, call):
+    """call(raw stream) with `dev` current and, if given, `stream` current."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        with torch.cuda.stream(stream):                 # makes its device current too
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return call(torch.cuda.current_stream(dev).cuda_stream)
+    return call(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _dev(workspace, "workspace", torch.uint8, dev)
+    return workspace
+
+
+def _ws_args(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+
+
+def _fp8_cache(k_cache, v_cache, k_scale, v_scale, device=None):
+    """Checks an e4m3 cache; returns (device, the four addresses, descriptor)."""
+    dev = k_cache.device if device is None else device
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
+                         "num_kv_heads, head_dim]")
+    nb, bs, hkv, d = k_cache.shape
+    if k_scale.shape != (nb, hkv) or v_scale.shape != (nb, hkv):
+        raise ValueError("k_scale and v_scale must be [num_blocks, num_kv_heads]")
+    ptrs = (_dev(k_cache, "k_cache", FP8, dev), _dev(v_cache, "v_cache", FP8, dev),
+            _dev(k_scale, "k_scale", torch.float32, dev),
+            _dev(v_scale, "v_scale", torch.float32, dev))
+    return dev, ptrs, CacheDesc(nb, bs, hkv, d)
+
+
+def _rows_of(k, v, n, desc, dev):
+    """Checks bf16 K/V rows [n, num_kv_heads, head_dim]; returns their addresses."""
+    if k.shape != (n, desc.num_kv_heads, desc.head_dim) or v.shape != k.shape:
+        raise ValueError("k/v must be [num_tokens, num_kv_heads, head_dim] matching the cache")
+    return _dev(k, "k", torch.bfloat16, dev), _dev(v, "v", torch.bfloat16, dev)
+
+
+def _decode_batch(q, block_tables, context_lens, desc, dev):
+    """Checks a decode batch over a cache; returns (B, Hq, q, tables, lengths)."""
+    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+        raise ValueError("q must be [batch, num_q_heads, head_dim] matching the cache")
+    B, Hq, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq] and context_lens "
+                         "[batch]")
+    return (B, Hq, _dev(q, "q", torch.bfloat16, dev),
+            _dev(block_tables, "block_tables", torch.int32, dev),
+            _dev(context_lens, "context_lens", torch.int32, dev))
+
+
+def _out_like(out, q, dev):
+    if out is None:
+        return torch.empty_like(q)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _dev(out, "out", q.dtype, dev)
+    return out
+
+
+def kv_store_fp8_workspace_bytes(num_tokens, k_cache) -> int:
+    return int(load().pkv_kv_store_fp8_workspace_bytes(num_tokens, cache_desc(k_cache)))
+
+
+def kv_store_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, workspace=None,
+                 status=None, stream=None) -> None:
+    """kv_store into an 8-bit cache (in place): k, v [N, Hkv, D] bf16 rows become
+    e4m3 codes in k_cache / v_cache [NB, bs, Hkv, D] float8_e4m3fn, with one
+    scale per block and kv head in k_scale / v_scale [NB, Hkv] fp32 (value =
+    code * scale).  A block's scale is the smallest power of two that holds
+    every row stored since its offset 0 was; where it grows, the block's
+    earlier rows are re-scaled.  Of several tokens with one slot the last is
+    stored.  Start with zeroed scales."""
+    lib = load()
+    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    n = slot_mapping.numel()
+    rows = _rows_of(k, v, n, desc, dev)
+    slots = _dev(slot_mapping, "slot_mapping", torch.int32, dev)
+    st = _ptr_or_null(status, "status", torch.int32, dev)
+
+    def call(s):
+        ws = _workspace(workspace, lib.pkv_kv_store_fp8_workspace_bytes(n, desc), dev)
+        _check(lib.pkv_kv_store_fp8(*rows, *cache, slots, n, *_ws_args(ws), desc, st, s),
+               "pkv_kv_store_fp8")
+    _on(dev, stream, call)
+
+
+def _decode_fp8(name, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                max_context_len, out, workspace, status, stream):
+    lib = load()
+    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    B, Hq, qp, bt, ctx = _decode_batch(q, block_tables, context_lens, desc, dev)
+    st = _ptr_or_null(status, "status", torch.int32, dev)
+    max_len = int(max_context_len)
+
+    def call(s):
+        o = _out_like(out, q, dev)
+        ws = _workspace(workspace, lib.pkv_paged_decode_workspace_bytes(B, Hq, max_len, desc), dev)
+        _check(getattr(lib, name)(qp, *cache, bt, block_tables.shape[1], ctx, B, Hq, max_len,
+                                  float(scale), o.data_ptr(), *_ws_args(ws), desc, st, s), name)
+        return o
+    return _on(dev, stream, call)
+
+
+def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                     max_context_len, out=None, workspace=None, status=None,
+                     stream=None) -> torch.Tensor:
+    """paged_decode over an 8-bit cache (see kv_store_fp8): q [B, Hq, D] bf16 ->
+    out [B, Hq, D] bf16.  The workspace is paged_decode's."""
+    return _decode_fp8("pkv_paged_decode_fp8", q, k_cache, v_cache, k_scale, v_scale,
+                       block_tables, context_lens, scale, max_context_len, out, workspace,
+                       status, stream)
+
+
+def paged_decode_run_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                         max_context_len, workspace, out=None, status=None,
+                         stream=None) -> torch.Tensor:
+    """paged_decode_fp8 with the schedule a paged_decode_plan call (on this cache's
+    shape) wrote into `workspace`."""
+    if workspace is None:
+        raise ValueError("workspace must hold a plan")
+    return _decode_fp8("pkv_paged_decode_run_fp8", q, k_cache, v_cache, k_scale, v_scale,
+                       block_tables, context_lens, scale, max_context_len, out, workspace,
+                       status, stream)
+
+
+def kv_store_paged_decode_fp8_workspace_bytes(num_tokens, batch, num_q_heads, max_context_len,
+                                              k_cache) -> int:
+    return int(load().pkv_kv_store_paged_decode_fp8_workspace_bytes(
+        num_tokens, batch, num_q_heads, int(max_context_len), cache_desc(k_cache)))
+
+
+def kv_store_paged_decode_fp8(k, v, slot_mapping, q, k_cache, v_cache, k_scale, v_scale,
+                              block_tables, context_lens, scale, max_context_len, out=None,
+                              workspace=None, status=None, stream=None) -> torch.Tensor:
+    """kv_store_fp8 of the new tokens followed by paged_decode_fp8, in one call."""
+    lib = load()
+    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    n = slot_mapping.numel()
+    rows = _rows_of(k, v, n, desc, dev)
+    slots = _dev(slot_mapping, "slot_mapping", torch.int32, dev)
+    B, Hq, qp, bt, ctx = _decode_batch(q, block_tables, context_lens, desc, dev)
+    st = _ptr_or_null(status, "status", torch.int32, dev)
+    max_len = int(max_context_len)
+
+    def call(s):
+        o = _out_like(out, q, dev)
+        ws = _workspace(workspace, lib.pkv_kv_store_paged_decode_fp8_workspace_bytes(
+            n, B, Hq, max_len, desc), dev)
+        _check(lib.pkv_kv_store_paged_decode_fp8(
+            *rows, slots, n, qp, *cache, bt, block_tables.shape[1], ctx, B, Hq, max_len,
+            float(scale), o.data_ptr(), *_ws_args(ws), desc, st, s),
+            "pkv_kv_store_paged_decode_fp8")
+        return o
+    return _on(dev, stream, call)
+
+
+def paged_prefill_fp8_workspace_bytes(batch, total_q, num_q_heads, max_seqlen_k,
+                                      k_cache_shape) -> int:
+    nb, bs, hkv, d = k_cache_shape
+    return int(load().pkv_paged_prefill_fp8_workspace_bytes(
+        batch, total_q, num_q_heads, int(max_seqlen_k), CacheDesc(nb, bs, hkv, d)))
+
+
+def paged_prefill_varlen_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q,
+                             cu_seqlens_k, max_seqlen_q, max_seqlen_k, block_tables, scale,
+                             out=None, workspace=None, status=None,
+                             stream=None) -> torch.Tensor:
+    """paged_prefill_varlen whose cached prefix lies in an 8-bit cache (see
+    kv_store_fp8); the chunk's own k/v [Tq, Hkv, D] are bf16 rows.  block_tables is
+    required (without a cached prefix, call paged_prefill_varlen).  Output rows
+    of no sequence are left unwritten."""
+    lib = load()
+    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+        raise ValueError("q must be [total_q, num_q_heads, head_dim] matching the cache")
+    T, Hq, _ = q.shape
+    rows = _rows_of(k, v, T, desc, dev)
+    B = cu_seqlens_q.numel() - 1
+    if B < 0 or cu_seqlens_k.numel() != B + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must both be [batch + 1]")
+    if block_tables is None:
+        raise ValueError("block_tables is required")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
+    qp = _dev(q, "q", torch.bfloat16, dev)
+    cu_q = _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
+    cu_k = _dev(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev)
+    bt = _dev(block_tables, "block_tables", torch.int32, dev)
+    st = _ptr_or_null(status, "status", torch.int32, dev)
+    max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
+
+    def call(s):
+        o = _out_like(out, q, dev)
+        ws = _workspace(workspace, lib.pkv_paged_prefill_fp8_workspace_bytes(B, T, Hq, max_k, desc),
+                        dev)
+        _check(lib.pkv_paged_prefill_varlen_fp8(
+            qp, *rows, *cache, cu_q, cu_k, B, T, max_q, max_k, Hq, bt, block_tables.shape[1],
+            float(scale), o.data_ptr(), *_ws_args(ws), desc, st, s),
+            "pkv_paged_prefill_varlen_fp8")
+        return o
+    return _on(dev, stream, call)
+
+
+_LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
+                      repetition_penalties=None, presence_penalties=None,
+                      frequency_penalties=None, bias_offsets=None, bias_token_ids=None,
+                      bias_values=None, allowed_mask=None, out=None, status=None,
+                      stream=None) -> torch.Tensor:
+    """Penalties, biases and a mask on a step's logits, for sample: logits
+    [B, V] fp32, bf16 or fp16 (rows may be strided) -> [B, V] fp32.
+
+    token_ids [B, T] int32 holds each row's prompt and generated tokens, of which
+    the first prompt_lens [B] are prompt and token_lens [B] count (None: none, and
+    all T); the penalties are [B] fp32 (None: off).  Row b's biases are entries
+    bias_offsets[b] .. bias_offsets[b + 1] of bias_token_ids int32 and
+    bias_values fp32 (the last one for a token counts).  allowed_mask
+    [B, ceil(V / 32)] int32 has bit i % 32 of word i / 32 set where token i may be
+    drawn.  Pass out=logits (fp32, contiguous) to work in place."""
+    lib = load()
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dtype not in _LOGIT_TYPES:
+        raise TypeError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [batch, vocab] with contiguous rows")
+    B, V = logits.shape
+    stride = logits.stride(0) if B > 1 else V
+    if stride < V:
+        raise ValueError("rows of logits overlap")
+    r = LogitRules()
+    i32, f32 = torch.int32, torch.float32
+    if token_ids is not None:
+        if token_ids.dim() != 2 or token_ids.shape[0] != B:
+            raise ValueError("token_ids must be [batch, max_tokens]")
+        r.token_ids = _dev(token_ids, "token_ids", i32, dev)
+        r.max_tokens = token_ids.shape[1]
+    per_row = (("prompt_lens", prompt_lens, i32), ("token_lens", token_lens, i32),
+               ("repetition_penalties", repetition_penalties, f32),
+               ("presence_penalties", presence_penalties, f32),
+               ("frequency_penalties", frequency_penalties, f32))
+    for name, t, dtype in per_row:
+        if t is None:
+            continue
+        if token_ids is None:
+            raise ValueError(f"{name} needs token_ids")
+        if t.shape != (B,):
+            raise ValueError(f"{name} must be [batch]")
+        setattr(r, name, _dev(t, name, dtype, dev))
+    biases = (bias_offsets, bias_token_ids, bias_values)
+    if any(t is not None for t in biases):
+        if any(t is None for t in biases):
+            raise ValueError("bias_offsets, bias_token_ids and bias_values go together")
+        if bias_offsets.shape != (B + 1,) or bias_token_ids.dim() != 1 or \
+                bias_values.shape != bias_token_ids.shape:
+            raise ValueError("bias_offsets must be [batch + 1], the others [num_biases]")
+        r.bias_offsets = _dev(bias_offsets, "bias_offsets", i32, dev)
+        r.bias_token_ids = _dev(bias_token_ids, "bias_token_ids", i32, dev)
+        r.bias_values = _dev(bias_values, "bias_values", f32, dev)
+        r.num_biases = bias_token_ids.numel()
+    if allowed_mask is not None:
+        if allowed_mask.shape != (B, (V + 31) // 32):
+            raise ValueError("allowed_mask must be [batch, ceil(vocab / 32)]")
+        r.allowed_mask = _dev(allowed_mask, "allowed_mask", i32, dev)
+    if out is not None:
+        if out.shape != (B, V):
+            raise ValueError("out must be [batch, vocab]")
+        _dev(out, "out", f32, dev)
+    st = _ptr_or_null(status, "status", torch.int32, dev)
+
+    def call(s):
+        o = torch.empty((B, V), dtype=f32, device=dev) if out is None else out
+        _check(lib.pkv_apply_logit_rules(logits.data_ptr(), _LOGIT_TYPES[logits.dtype], stride, B,
+                                         V, r, o.data_ptr(), st, s), "pkv_apply_logit_rules")
+        return o
+    return _on(dev, stream, call)

@@ -52,6 +52,10 @@ extern "C" const char* pkv_status_string(uint32_t bits) {
     if (bits & PKV_STATUS_NO_FINITE_KEY) return "every sampling key of a row is NaN";
     if (bits & PKV_STATUS_WORKSPACE_OVERFLOW) return "more work items than the workspace holds";
     if (bits & PKV_STATUS_WAIT_TIMEOUT) return "a bounded in-kernel wait gave up";
+    if (bits & PKV_STATUS_BAD_SCALE) return "a scale of the e4m3 cache cannot be used";
+    if (bits & PKV_STATUS_BAD_TOKEN_ID) return "token id outside the vocabulary";
+    if (bits & PKV_STATUS_BAD_PENALTY) return "a logit penalty cannot be used";
+    if (bits & PKV_STATUS_NO_ALLOWED_TOKEN) return "a row's mask allows no token";
     return "unknown status bit";
 }
 

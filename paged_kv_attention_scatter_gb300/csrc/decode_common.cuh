@@ -63,3 +63,16 @@ __device__ __forceinline__ void wait_for_predecessor() {
 // programmatic dependent of the plan kernel.
 int pkv_decode_tma_supported(const pkv::DecodeArgs& a, int head_dim);
 int pkv_launch_decode_tma(pkv::DecodeArgs& a, int head_dim, cudaStream_t s);
+
+// Pieces of pkv_paged_decode (paged_decode.cu) that the decode over an e4m3
+// cache shares: the argument checks (the cache pointers are checked and stored
+// untyped), the plan kernel, and the combine kernel as a programmatic dependent
+// of the split kernel enqueued before it.
+int pkv_decode_make_args(const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                         int32_t max_context_len, float scale, void* out, void* workspace,
+                         size_t workspace_bytes, const pkv_cache_desc& cache, uint32_t* status,
+                         pkv::DecodeArgs& a);
+int pkv_launch_decode_plan(const pkv::DecodeArgs& a, cudaStream_t s);
+int pkv_launch_decode_combine(const pkv::DecodeArgs& a, int head_dim, cudaStream_t s);

@@ -1,0 +1,446 @@
+// kv_store_fp8: quantise each new token's K and V rows to e4m3 and scatter
+// them into a paged cache with one scale for each (cache block, kv head).
+//
+// For a block and head that the call stores rows into, with x the rows' entries:
+//   c' = max(c, 2^e), e the least integer with max|x| <= 448 * 2^e, in [-64, 119];
+//   a stored row's codes are e4m3(x / c'), nearest-even, saturating;
+//   every other row of the block has its codes replaced by e4m3(code * c / c').
+// c is the block's scale before the call; a row at offset 0 begins the block
+// anew (a sequence fills its blocks in order), and then c counts as 0 and the
+// other rows are left alone.  A power of two changes no significant bit of a
+// code, so x / c' is exact before its one rounding, a row re-scaled because its
+// block grew keeps its codes' bits except where they fall among the
+// subnormals, and storing a sequence row by row gives the values that storing
+// it at once does (up to those subnormals).  A scale with a full significand
+// would gain at most one bit of range and round every earlier row again
+// each time it grew.
+//
+// Design.  One CTA owns a (block, set of heads): it needs every row the call
+// stores there before it can write the first code.  It collects the rows of
+// its block -- the last token of each slot -- in shared memory, takes each
+// head's maximum while reading the rows once into registers, and writes codes
+// from the registers.  A row's head segment is read as 16 bytes a lane (D/8
+// lanes) and written as 8.  How rows find their block, by the number of tokens:
+//  * up to 2048: one launch, a CTA per token.  The CTAs of a block's first
+//    rows share its heads: one CTA for a decode step's single row, up to 2 * Hkv
+//    for a block that a prefill chunk fills; the rest of the block's CTAs leave
+//    after one look at the 16 tokens before theirs.  Each CTA that stays scans
+//    all slots (8 KB at most, from L2).
+//  * more: that scan is quadratic, so a first kernel links the runs of
+//    consecutive tokens in each block into a list per block, and the store
+//    kernel's CTAs walk the lists.
+// Bound by memory: 4 bytes read and 2 written per K/V entry pair.
+#include "fp8_common.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKeep = 8;                     // row segments a lane keeps in registers
+constexpr int32_t kScanTokens = 2048;        // largest call of the scanning form
+constexpr int kRowsPerPart = 16;             // rows for which one more CTA joins a block
+
+struct StoreArgs {
+    const uint4* k;
+    const uint4* v;
+    uint8_t* kc;
+    uint8_t* vc;
+    float* ks;
+    float* vs;
+    const int32_t* slots;
+    int32_t n, bs, Hkv, NB;
+    int64_t num_slots;
+    uint32_t* status;
+    // list form: runs linked per block
+    int32_t* count;                          // blocks in `list`, minus 1
+    int32_t* head;                           // [NB]: token that starts the block's last run, -1
+    int32_t* next;                           // [n]: start of the run linked before, -1
+    int32_t* list;                           // [min(n, NB)]: blocks that get rows
+};
+
+struct BlockRows {
+    int32_t winner[pkv::kFp8MaxBlockSize];   // offset -> last token stored there, -1
+    int32_t token[pkv::kFp8MaxBlockSize];    // the rows, in no particular order
+    int16_t offset[pkv::kFp8MaxBlockSize];
+    int32_t rows;
+    uint32_t amax[kThreads / 8];             // per lane group
+    float ratio[kThreads / 8];               // per pair in hand: old / new scale where it grew
+};
+
+// Magnitude bits of the larger finite entry of a bf16 pair and `m`.
+__device__ __forceinline__ uint32_t amax_pair(uint32_t m, uint32_t w) {
+    const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+    m = max(m, lo < 0x7f80u ? lo : 0u);
+    return max(m, hi < 0x7f80u ? hi : 0u);
+}
+
+// 2^e for the least e with (bf16 magnitude) <= 448 * 2^e, clamped.
+__device__ __forceinline__ float scale_for(uint32_t mag) {
+    const int e = (int)(mag >> 7) - 127 - ((mag & 0x7fu) <= 0x60u ? 8 : 7);  // 448 = 1.75 * 2^8
+    const int c = min(max(e, pkv::kScaleExpLo), pkv::kScaleExpHi);
+    return __int_as_float((c + 127) << 23);
+}
+
+struct Quantiser {
+    float scale, inv;
+    bool exact_inv;                          // a power of two: x * inv == x / scale
+    __device__ __forceinline__ uint32_t two(uint32_t w) const {
+        float lo = __int_as_float((int)(w << 16)), hi = __int_as_float((int)(w & 0xffff0000u));
+        if (exact_inv) {
+            lo *= inv;
+            hi *= inv;
+        } else {
+            lo = __fdiv_rn(lo, scale);
+            hi = __fdiv_rn(hi, scale);
+        }
+        return pkv::float2_to_e4m3x2(lo, hi);
+    }
+    __device__ __forceinline__ uint2 eight(const uint4& w) const {
+        return make_uint2(two(w.x) | two(w.y) << 16, two(w.z) | two(w.w) << 16);
+    }
+};
+
+__device__ __forceinline__ Quantiser quantiser(float c) {
+    return Quantiser{c, __fdiv_rn(1.f, c), (__float_as_int(c) & 0x7fffff) == 0};
+}
+
+__device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
+    uint32_t lo, hi;
+    pkv::e4m3x4_to_f16x4(codes, lo, hi);
+    const float2 a = pkv::f16x2_to_float2(lo), b = pkv::f16x2_to_float2(hi);
+    return (uint32_t)pkv::float2_to_e4m3x2(a.x * ratio, a.y * ratio) |
+           (uint32_t)pkv::float2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
+}
+
+// The winners as a compact list (any order); ends with a barrier.
+__device__ __forceinline__ void compact_rows(const StoreArgs& a, BlockRows& sm) {
+    __syncthreads();
+    for (int o = threadIdx.x; o < a.bs; o += kThreads) {
+        const int32_t t = sm.winner[o];
+        if (t >= 0) {
+            const int i = atomicAdd(&sm.rows, 1);
+            sm.token[i] = t;
+            sm.offset[i] = (int16_t)o;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void clear_rows(const StoreArgs& a, BlockRows& sm) {
+    for (int o = threadIdx.x; o < a.bs; o += kThreads) sm.winner[o] = -1;
+    if (threadIdx.x == 0) sm.rows = 0;
+    __syncthreads();
+}
+
+// Stores the collected rows of block `blk` for the (tensor, head) pairs
+// part, part + parts, ... of the 2 * Hkv.  Pair p is head p >> 1 of K (even) or V.
+template <int D>
+__device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, int32_t blk,
+                                            int part, int parts) {
+    constexpr int kLanes = D / 8;            // lanes of a row's head segment
+    constexpr int kGroups = kThreads / kLanes;
+    const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+    const int pairs = 2 * a.Hkv;
+    const int mine = (pairs - part + parts - 1) / parts;
+    // groups per pair: a power of two, so a pair's groups are aligned
+    int gpp = kGroups;
+    while (gpp > 1 && kGroups / gpp < mine) gpp >>= 1;
+    const int at_once = kGroups / gpp, sub = group % gpp;
+    const int rows = sm.rows;
+    const bool fresh = sm.winner[0] >= 0;
+    const int64_t row_codes = (int64_t)a.Hkv * D;
+    for (int i0 = 0; i0 < mine; i0 += at_once) {
+        const int i = i0 + group / gpp;
+        const bool live = i < mine;
+        const int pair = part + (live ? i : 0) * parts;
+        const int h = pair >> 1;
+        const uint4* src = ((pair & 1) ? a.v : a.k) + h * kLanes + lane;
+        uint8_t* dst = ((pair & 1) ? a.vc : a.kc) + (int64_t)blk * a.bs * row_codes + h * D +
+                       lane * 8;
+        float* scale_at = ((pair & 1) ? a.vs : a.ks) + (int64_t)blk * a.Hkv + h;
+        float old = 0.f;
+        if (live && !fresh) old = *scale_at;
+        // ---- the pair's maximum; the first kKeep rows stay in registers ----
+        uint4 keep[kKeep];
+        uint32_t m = 0;
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < kKeep; ++j) {
+                const int r = sub + j * gpp;
+                keep[j] = make_uint4(0, 0, 0, 0);
+                if (r < rows) keep[j] = __ldg(src + (int64_t)sm.token[r] * (row_codes / 8));
+            }
+#pragma unroll
+            for (int j = 0; j < kKeep; ++j)
+                m = amax_pair(amax_pair(amax_pair(amax_pair(m, keep[j].x), keep[j].y), keep[j].z),
+                              keep[j].w);
+            for (int r = sub + kKeep * gpp; r < rows; r += gpp) {
+                const uint4 w = __ldg(src + (int64_t)sm.token[r] * (row_codes / 8));
+                m = amax_pair(amax_pair(amax_pair(amax_pair(m, w.x), w.y), w.z), w.w);
+            }
+        }
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (lane == 0) sm.amax[group] = m;
+        __syncthreads();                     // every group has read its old scale too
+        for (int g = 0; g < gpp; ++g) m = max(m, sm.amax[group - sub + g]);
+        __syncthreads();                     // before the next round's maxima
+        float ratio = 0.f;
+        if (live) {
+            if (!(old == 0.f || pkv::scale_ok(old))) {
+                if (lane == 0 && sub == 0) pkv::report(a.status, PKV_STATUS_BAD_SCALE);
+                old = 0.f;
+            }
+            const float scale = fmaxf(old, scale_for(m));
+            const Quantiser quant = quantiser(scale);
+#pragma unroll
+            for (int j = 0; j < kKeep; ++j) {
+                const int r = sub + j * gpp;
+                if (r < rows)
+                    *reinterpret_cast<uint2*>(dst + sm.offset[r] * row_codes) =
+                        quant.eight(keep[j]);
+            }
+            for (int r = sub + kKeep * gpp; r < rows; r += gpp) {
+                const uint4 w = __ldg(src + (int64_t)sm.token[r] * (row_codes / 8));
+                *reinterpret_cast<uint2*>(dst + sm.offset[r] * row_codes) = quant.eight(w);
+            }
+            if (old > 0.f && scale > old) ratio = __fdiv_rn(old, scale);
+            if (lane == 0 && sub == 0) *scale_at = scale;
+        }
+        if (lane == 0 && sub == 0) sm.ratio[group / gpp] = ratio;
+        if (!__syncthreads_or(ratio > 0.f)) continue;
+        // ---- blocks that grew: their other rows, the whole CTA on one pair at a
+        // time (a decode step's pair has one lane group, and 256 rows one after
+        // another would take as long as the rest of the step) ----
+        for (int p = 0; p < at_once; ++p) {
+            const float r = sm.ratio[p];
+            if (!(r > 0.f)) continue;
+            const int pr = part + (i0 + p) * parts;
+            uint8_t* base = ((pr & 1) ? a.vc : a.kc) + (int64_t)blk * a.bs * row_codes +
+                            (pr >> 1) * D + lane * 8;
+            for (int o0 = group; o0 < a.bs; o0 += kKeep * kGroups) {
+                uint2 c[kKeep];
+#pragma unroll
+                for (int j = 0; j < kKeep; ++j) {
+                    const int o = o0 + j * kGroups;
+                    if (o < a.bs && sm.winner[o] < 0)
+                        c[j] = *reinterpret_cast<const uint2*>(base + o * row_codes);
+                }
+#pragma unroll
+                for (int j = 0; j < kKeep; ++j) {
+                    const int o = o0 + j * kGroups;
+                    if (o < a.bs && sm.winner[o] < 0)
+                        *reinterpret_cast<uint2*>(base + o * row_codes) =
+                            make_uint2(rescale4(c[j].x, r), rescale4(c[j].y, r));
+                }
+            }
+        }
+        __syncthreads();                     // sm.ratio is read before the next round
+    }
+}
+
+__device__ __forceinline__ int parts_of(int rows, int pairs) {
+    return min(max(rows / kRowsPerPart, 1), pairs);
+}
+
+// Up to kScanTokens tokens: CTA t belongs to token t.
+template <int D>
+__global__ void __launch_bounds__(kThreads) store_scan_kernel(StoreArgs a) {
+    __shared__ BlockRows sm;
+    __shared__ int32_t before, total;
+    pkv::allow_dependent_launch();
+    const int32_t t = blockIdx.x;
+    const int32_t slot = a.slots[t];
+    if (slot < 0) return;
+    if (slot >= a.num_slots) {
+        if (threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_SLOT_OUT_OF_RANGE);
+        return;
+    }
+    const int32_t blk = slot / a.bs;
+    const int32_t lo = blk * a.bs, hi = lo + a.bs;
+    const int pairs = 2 * a.Hkv;
+    // this token's rank in its block is at least the number of the block's
+    // tokens among the `pairs` before it: at `pairs` no part is left for it
+    if (pairs <= kThreads) {
+        const int32_t s = (threadIdx.x < pairs && t > (int32_t)threadIdx.x)
+                              ? a.slots[t - 1 - threadIdx.x] : -1;
+        if (__syncthreads_count(s >= lo && s < hi) >= pairs) return;
+    }
+    clear_rows(a, sm);
+    if (threadIdx.x == 0) before = total = 0;
+    __syncthreads();
+    int b = 0, all = 0;
+    for (int32_t i = threadIdx.x; i < a.n; i += kThreads) {
+        const int32_t s = a.slots[i];
+        if (s < lo || s >= hi) continue;
+        atomicMax(&sm.winner[s - lo], i);
+        ++all;
+        b += i < t;
+    }
+    if (all) {
+        atomicAdd(&total, all);
+        atomicAdd(&before, b);
+    }
+    __syncthreads();
+    const int parts = parts_of(total, pairs);
+    const int part = before;
+    if (part >= parts) return;
+    compact_rows(a, sm);
+    store_block<D>(a, sm, blk, part, parts);
+}
+
+// More tokens: each block's runs as a linked list, and the blocks as a list.
+__global__ void __launch_bounds__(kThreads) store_link_kernel(StoreArgs a) {
+    pkv::allow_dependent_launch();
+    const int32_t t = blockIdx.x * kThreads + threadIdx.x;
+    if (t >= a.n) return;
+    const int32_t slot = a.slots[t];
+    if (slot < 0) return;
+    if (slot >= a.num_slots) {
+        pkv::report(a.status, PKV_STATUS_SLOT_OUT_OF_RANGE);
+        return;
+    }
+    const int32_t blk = slot / a.bs;
+    const int32_t prev = t > 0 ? a.slots[t - 1] : -1;
+    if (prev >= 0 && prev < a.num_slots && prev / a.bs == blk) return;   // inside a run
+    const int32_t linked = atomicExch(&a.head[blk], t);
+    a.next[t] = linked;
+    if (linked < 0) a.list[atomicAdd(a.count, 1) + 1] = blk;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) store_list_kernel(StoreArgs a) {
+    __shared__ BlockRows sm;
+    pkv::wait_for_predecessor();             // the linked runs
+    pkv::allow_dependent_launch();
+    const int pairs = 2 * a.Hkv;
+    const int max_parts = parts_of(a.bs, pairs);
+    const int64_t items = (int64_t)(*a.count + 1) * max_parts;
+    int32_t have = -1;                       // block whose rows are in shared memory
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const int32_t blk = a.list[i / max_parts];
+        const int part = (int)(i % max_parts);
+        if (blk != have) {
+            __syncthreads();
+            clear_rows(a, sm);
+            const int32_t lo = blk * a.bs, hi = lo + a.bs;
+            for (int32_t run = a.head[blk]; run >= 0; run = a.next[run]) {
+                // the run's tokens: up to the first one of another block
+                for (int32_t j = run;; j += kThreads) {
+                    const int32_t t = j + (int32_t)threadIdx.x;
+                    const int32_t s = t < a.n ? a.slots[t] : -1;
+                    const bool in = s >= lo && s < hi;
+                    if (in) atomicMax(&sm.winner[s - lo], t);
+                    if (!__syncthreads_and(in)) break;
+                }
+            }
+            compact_rows(a, sm);
+            have = blk;
+        }
+        // a part beyond the rows' need has nothing to do
+        const int parts = parts_of(sm.rows, pairs);
+        if (part < parts) store_block<D>(a, sm, blk, part, parts);
+    }
+}
+
+struct StoreLayout {
+    size_t off_head, off_next, off_list, total;
+};
+
+StoreLayout store_layout(int32_t n, int32_t num_blocks) {
+    StoreLayout L{};
+    if (n <= kScanTokens) return L;
+    auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    L.off_head = 16;                         // behind the count, cleared with it
+    L.off_next = align(L.off_head + sizeof(int32_t) * (size_t)num_blocks);
+    L.off_list = align(L.off_next + sizeof(int32_t) * (size_t)n);
+    L.total = align(L.off_list + sizeof(int32_t) * (size_t)(n < num_blocks ? n : num_blocks));
+    return L;
+}
+
+template <int D>
+int launch_store(const Fp8StoreCall& c, cudaStream_t s) {
+    StoreArgs a{};
+    a.k = (const uint4*)c.k;
+    a.v = (const uint4*)c.v;
+    a.kc = (uint8_t*)c.k_cache;
+    a.vc = (uint8_t*)c.v_cache;
+    a.ks = c.k_scale;
+    a.vs = c.v_scale;
+    a.slots = c.slot_mapping;
+    a.n = c.num_tokens;
+    a.bs = c.cache.block_size;
+    a.Hkv = c.cache.num_kv_heads;
+    a.NB = c.cache.num_blocks;
+    a.num_slots = (int64_t)a.NB * a.bs;
+    a.status = c.status;
+    if (a.n <= kScanTokens) {
+        store_scan_kernel<D><<<(unsigned)a.n, kThreads, 0, s>>>(a);
+        return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
+    const StoreLayout L = store_layout(a.n, a.NB);
+    char* ws = (char*)c.workspace;
+    a.count = (int32_t*)ws;
+    a.head = (int32_t*)(ws + L.off_head);
+    a.next = (int32_t*)(ws + L.off_next);
+    a.list = (int32_t*)(ws + L.off_list);
+    if (cudaMemsetAsync(ws, 0xff, L.off_head + sizeof(int32_t) * (size_t)a.NB, s) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    store_link_kernel<<<(unsigned)((a.n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pkv_num_sms() * 8), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, store_list_kernel<D>, a) != cudaSuccess) return PKV_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+int pkv_kv_store_fp8_check(const Fp8StoreCall& c) {
+    const pkv_cache_desc& d = c.cache;
+    if (c.num_tokens < 0 || d.num_blocks <= 0 || d.block_size <= 0 || d.num_kv_heads <= 0)
+        return PKV_ERR_BAD_DIMENSION;
+    if (d.block_size > pkv::kFp8MaxBlockSize) return PKV_ERR_BAD_DIMENSION;
+    if (d.head_dim != 64 && d.head_dim != 128) return PKV_ERR_UNSUPPORTED_HEAD_DIM;
+    if ((int64_t)d.num_blocks * d.block_size >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
+    if (c.num_tokens == 0) return PKV_OK;
+    if (!c.k || !c.v || !c.k_cache || !c.v_cache || !c.k_scale || !c.v_scale || !c.slot_mapping)
+        return PKV_ERR_NULL_POINTER;
+    if (((uintptr_t)c.k | (uintptr_t)c.v | (uintptr_t)c.k_cache | (uintptr_t)c.v_cache) & 15)
+        return PKV_ERR_MISALIGNED;
+    if (((uintptr_t)c.k_scale | (uintptr_t)c.v_scale | (uintptr_t)c.slot_mapping) & 3)
+        return PKV_ERR_MISALIGNED;
+    const size_t need = store_layout(c.num_tokens, d.num_blocks).total;
+    if (need > 0) {
+        if (!c.workspace) return PKV_ERR_NULL_POINTER;
+        if ((uintptr_t)c.workspace & 15) return PKV_ERR_MISALIGNED;
+        if (c.workspace_bytes < need) return PKV_ERR_WORKSPACE_TOO_SMALL;
+    }
+    return PKV_OK;
+}
+
+int pkv_kv_store_fp8_launch(const Fp8StoreCall& c, cudaStream_t s) {
+    if (c.num_tokens == 0) return PKV_OK;
+    return c.cache.head_dim == 128 ? launch_store<128>(c, s) : launch_store<64>(c, s);
+}
+
+extern "C" size_t pkv_kv_store_fp8_workspace_bytes(int32_t num_tokens, pkv_cache_desc cache) {
+    if (num_tokens < 0 || cache.num_blocks <= 0) return 0;
+    return store_layout(num_tokens, cache.num_blocks).total;
+}
+
+extern "C" int pkv_kv_store_fp8(const void* k, const void* v, void* k_cache, void* v_cache,
+                                float* k_scale, float* v_scale, const int32_t* slot_mapping,
+                                int32_t num_tokens, void* workspace, size_t workspace_bytes,
+                                pkv_cache_desc cache, uint32_t* status, void* stream) {
+    const Fp8StoreCall c{k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, num_tokens,
+                         workspace, workspace_bytes, cache, status};
+    const int rc = pkv_kv_store_fp8_check(c);
+    return rc != PKV_OK ? rc : pkv_kv_store_fp8_launch(c, (cudaStream_t)stream);
+}

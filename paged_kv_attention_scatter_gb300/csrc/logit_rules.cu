@@ -1,0 +1,331 @@
+// apply_logit_rules: penalties for repeated tokens, biases and an allowed-token
+// mask on a step's logits, ahead of the sampler.
+//
+// For entry i of row b, x = logits[b, i] in fp32, n = occurrences of i among
+// the row's generated tokens, seen = i occurs in its prompt or generated tokens:
+//   seen:  x = x > 0 ? x / r : x * r           (repetition)
+//   x -= f * n + p * (n > 0)                    (frequency, presence)
+//   x += the row's last bias for token i        (biases)
+//   not allowed: x = -inf                       (mask)
+//
+// Design.  One pass over the logits: a CTA owns a segment of one row's
+// vocabulary and keeps a word per entry in shared memory (a bit for the prompt, a
+// count for the generated tokens), fills it from the row's whole token list with shared-memory atomics
+// (integers, so their order does not matter), then streams its segment, 16
+// bytes a lane where the rows allow.  The list is read once per segment, out of
+// L2, instead of a global table of counts being cleared, filled and read
+// (12 bytes a vocabulary entry).  Few entries have a bias, so biases are added
+// afterwards to the segment's written entries; the last entry for a token
+// is found with an integer maximum in the same shared words.
+// In place (fp32, out == logits) a vector that no rule changes is not written.
+// Bound by memory: the logits in, fp32 out, a mask bit an entry.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxSegment = 8192;            // entries per CTA (32 KB of counts)
+// A word: bit 0 says that a prompt token was this entry, the bits above count
+// the generated ones; the entry was seen if the word is not zero.
+constexpr uint32_t kInPrompt = 1, kGenerated = 2;
+
+struct RuleArgs {
+    const void* logits;
+    int64_t stride;                          // entries between rows of logits
+    float* out;
+    int32_t batch, vocab, segment;
+    pkv_logit_rules r;
+    uint32_t* status;
+    bool in_place;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+struct RowRules {
+    float rep, freq, pres;
+    bool penalties;
+};
+
+__device__ __forceinline__ float penalise(float x, uint32_t word, const RowRules& p) {
+    if (word) {
+        x = x > 0.f ? __fdiv_rn(x, p.rep) : x * p.rep;
+        const uint32_t n = word / kGenerated;
+        if (n) x -= fmaf(p.freq, (float)n, p.pres);
+    }
+    return x;
+}
+
+// kVec: every row of logits and out starts on 16 bytes.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
+    extern __shared__ uint4 smem[];
+    uint32_t* words = reinterpret_cast<uint32_t*>(smem);
+    const int32_t b = blockIdx.y;
+    const int32_t lo = blockIdx.x * a.segment;
+    const int32_t len = min(a.segment, a.vocab - lo);
+    const T* row = static_cast<const T*>(a.logits) + (int64_t)b * a.stride + lo;
+    float* out = a.out + (int64_t)b * a.vocab + lo;
+    const uint32_t* mask = nullptr;
+    const int32_t mask_words = (a.vocab + 31) / 32;
+    if (a.r.allowed_mask != nullptr)
+        mask = a.r.allowed_mask + (int64_t)b * mask_words + (lo >> 5);   // lo % 32 == 0
+
+    // ---- the row's history ----
+    RowRules p{1.f, 0.f, 0.f, false};
+    int32_t n_tokens = 0, n_prompt = 0;
+    if (a.r.token_ids != nullptr) {
+        n_tokens = a.r.token_lens != nullptr ? a.r.token_lens[b] : a.r.max_tokens;
+        n_prompt = a.r.prompt_lens != nullptr ? a.r.prompt_lens[b] : 0;
+        if (n_tokens < 0 || n_tokens > a.r.max_tokens || n_prompt < 0 || n_prompt > n_tokens) {
+            if (lo == 0 && threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
+            n_tokens = 0;
+        }
+        if (a.r.repetition_penalties != nullptr) p.rep = a.r.repetition_penalties[b];
+        if (a.r.presence_penalties != nullptr) p.pres = a.r.presence_penalties[b];
+        if (a.r.frequency_penalties != nullptr) p.freq = a.r.frequency_penalties[b];
+        const bool rep_ok = isfinite(p.rep) && p.rep > 0.f;
+        const bool add_ok = isfinite(p.freq) && isfinite(p.pres);
+        if (!(rep_ok && add_ok) && lo == 0 && threadIdx.x == 0)
+            pkv::report(a.status, PKV_STATUS_BAD_PENALTY);
+        if (!rep_ok) p.rep = 1.f;
+        if (!isfinite(p.freq)) p.freq = 0.f;
+        if (!isfinite(p.pres)) p.pres = 0.f;
+        p.penalties = n_tokens > 0 && (p.rep != 1.f || p.freq != 0.f || p.pres != 0.f);
+    }
+    if (p.penalties) {
+        for (int i = threadIdx.x; i < (len + 3) / 4; i += kThreads)
+            smem[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        const int32_t* ids = a.r.token_ids + (int64_t)b * a.r.max_tokens;
+        bool bad = false;
+#pragma unroll 4
+        for (int32_t i = threadIdx.x; i < n_tokens; i += kThreads) {
+            const int32_t id = __ldg(ids + i);
+            bad |= id >= a.vocab;
+            const uint32_t at = (uint32_t)(id - lo);
+            if (id < lo || at >= (uint32_t)len) continue;
+            if (i < n_prompt)
+                atomicOr(&words[at], kInPrompt);
+            else
+                atomicAdd(&words[at], kGenerated);
+        }
+        if (bad && lo == 0) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
+        __syncthreads();
+    }
+
+    // ---- one pass over the segment ----
+    if constexpr (kVec) {
+        constexpr int E = 16 / sizeof(T);    // entries per load
+        const int nv = len / E;
+        constexpr int U = sizeof(T) == 4 ? 4 : 2;      // loads in flight a lane
+        for (int v0 = threadIdx.x; v0 < nv; v0 += U * kThreads) {
+            uint4 raw[U];
+            uint32_t allow[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + u * kThreads;
+                if (v >= nv) continue;
+                raw[u] = __ldcs(reinterpret_cast<const uint4*>(row + v * E));
+                allow[u] = mask ? __ldg(mask + (v * E >> 5)) >> (v * E & 31) : 0xffffffffu;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = v0 + u * kThreads;
+                if (v >= nv) continue;
+                const T* in = reinterpret_cast<const T*>(&raw[u]);
+                float x[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = to_float(in[e]);
+                bool changed = !a.in_place;
+                if (p.penalties) {
+#pragma unroll
+                    for (int q = 0; q < E / 4; ++q) {
+                        const uint4 w = smem[v * (E / 4) + q];
+                        if ((w.x | w.y | w.z | w.w) == 0) continue;
+                        changed = true;
+                        x[4 * q] = penalise(x[4 * q], w.x, p);
+                        x[4 * q + 1] = penalise(x[4 * q + 1], w.y, p);
+                        x[4 * q + 2] = penalise(x[4 * q + 2], w.z, p);
+                        x[4 * q + 3] = penalise(x[4 * q + 3], w.w, p);
+                    }
+                }
+                constexpr uint32_t kAll = (1u << E) - 1u;
+                if ((allow[u] & kAll) != kAll) {
+                    changed = true;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (!(allow[u] >> e & 1u)) x[e] = -INFINITY;
+                }
+                if (changed) {
+#pragma unroll
+                    for (int q = 0; q < E / 4; ++q)
+                        *reinterpret_cast<float4*>(out + v * E + 4 * q) =
+                            make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                }
+            }
+        }
+        for (int i = nv * E + threadIdx.x; i < len; i += kThreads) {
+            float x = to_float(row[i]);
+            if (p.penalties) x = penalise(x, words[i], p);
+            if (mask && !(mask[i >> 5] >> (i & 31) & 1u)) x = -INFINITY;
+            out[i] = x;
+        }
+    } else {
+        constexpr int U = 8;
+        for (int i0 = threadIdx.x; i0 < len; i0 += U * kThreads) {
+            T raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kThreads;
+                if (i < len) raw[u] = row[i];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kThreads;
+                if (i >= len) continue;
+                float x = to_float(raw[u]);
+                if (p.penalties) x = penalise(x, words[i], p);
+                if (mask && !(__ldg(mask + (i >> 5)) >> (i & 31) & 1u)) x = -INFINITY;
+                out[i] = x;
+            }
+        }
+    }
+
+    // ---- biases of this segment's entries: the last one for a token counts ----
+    if (a.r.bias_offsets != nullptr) {
+        const int32_t e0 = a.r.bias_offsets[b], e1 = a.r.bias_offsets[b + 1];
+        if (e0 < 0 || e1 < e0 || e1 > a.r.num_biases) {
+            if (lo == 0 && threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
+        } else if (e1 > e0) {
+            __syncthreads();                 // the counts are read, the entries written
+            bool bad = false;
+            for (int32_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
+                const int32_t id = a.r.bias_token_ids[e];
+                bad |= id >= a.vocab;
+                if (id >= lo && id - lo < len) words[id - lo] = 0;
+            }
+            if (bad && lo == 0) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
+            __syncthreads();
+            for (int32_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
+                const int32_t id = a.r.bias_token_ids[e];
+                if (id >= lo && id - lo < len) atomicMax(&words[id - lo], (uint32_t)(e - e0) + 1u);
+            }
+            __syncthreads();
+            for (int32_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
+                const int32_t id = a.r.bias_token_ids[e];
+                if (id < lo || id - lo >= len || words[id - lo] != (uint32_t)(e - e0) + 1u)
+                    continue;
+                const int i = id - lo;
+                if (mask && !(mask[i >> 5] >> (i & 31) & 1u)) continue;
+                out[i] += a.r.bias_values[e];
+            }
+        }
+    }
+
+    // ---- a row whose mask leaves nothing ----
+    if (lo == 0 && mask != nullptr && a.status != nullptr) {
+        bool any = false;
+        for (int32_t w = threadIdx.x; w < mask_words; w += kThreads) {
+            const int32_t left = a.vocab - w * 32;
+            const uint32_t live = left >= 32 ? 0xffffffffu : (1u << left) - 1u;
+            any |= (__ldg(mask + w) & live) != 0;
+        }
+        if (!__syncthreads_or(any) && threadIdx.x == 0)
+            pkv::report(a.status, PKV_STATUS_NO_ALLOWED_TOKEN);
+    }
+}
+
+template <typename T>
+int launch_rules(RuleArgs& a, cudaStream_t s) {
+    // Segments: 8192 entries when the rows alone fill the GPU (each segment
+    // reads the whole history), less down to 1024 for a few rows, so that about
+    // six CTAs an SM share the work.
+    const int64_t want = (int64_t)pkv_num_sms() * 6;
+    int64_t seg = ((int64_t)a.batch * a.vocab + want - 1) / want;
+    seg = (seg + 1023) / 1024 * 1024;
+    if (seg > kMaxSegment) seg = kMaxSegment;
+    a.segment = (int32_t)seg;
+    const bool vec = (((uintptr_t)a.logits | (uintptr_t)a.out) & 15) == 0 &&
+                     (a.stride * (int64_t)sizeof(T)) % 16 == 0 && a.vocab % 4 == 0;
+    const int smem = a.r.token_ids || a.r.bias_offsets ? a.segment * 4 : 0;
+    const unsigned segs = (unsigned)((a.vocab + a.segment - 1) / a.segment);
+    for (int32_t b0 = 0; b0 < a.batch; b0 += 65535) {
+        RuleArgs sub = a;
+        const int32_t rows = a.batch - b0 < 65535 ? a.batch - b0 : 65535;
+        sub.logits = (const T*)a.logits + (int64_t)b0 * a.stride;
+        sub.out = a.out + (int64_t)b0 * a.vocab;
+        pkv_logit_rules& r = sub.r;
+        if (r.token_ids) r.token_ids += (int64_t)b0 * r.max_tokens;
+        if (r.prompt_lens) r.prompt_lens += b0;
+        if (r.token_lens) r.token_lens += b0;
+        if (r.repetition_penalties) r.repetition_penalties += b0;
+        if (r.presence_penalties) r.presence_penalties += b0;
+        if (r.frequency_penalties) r.frequency_penalties += b0;
+        if (r.bias_offsets) r.bias_offsets += b0;
+        if (r.allowed_mask) r.allowed_mask += (int64_t)b0 * ((a.vocab + 31) / 32);
+        const dim3 grid(segs, (unsigned)rows);
+        if (vec)
+            logit_rules_kernel<T, true><<<grid, kThreads, smem, s>>>(sub);
+        else
+            logit_rules_kernel<T, false><<<grid, kThreads, smem, s>>>(sub);
+        if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" int pkv_apply_logit_rules(const void* logits, int32_t logits_type,
+                                     int64_t logits_stride, int32_t batch, int32_t vocab,
+                                     pkv_logit_rules rules, float* out, uint32_t* status,
+                                     void* stream) {
+    if (batch < 0 || vocab <= 0 || logits_stride < vocab) return PKV_ERR_BAD_DIMENSION;
+    if (logits_type != PKV_FP32 && logits_type != PKV_BF16 && logits_type != PKV_FP16)
+        return PKV_ERR_UNSUPPORTED;
+    if (rules.token_ids && rules.max_tokens < 0) return PKV_ERR_BAD_DIMENSION;
+    if (rules.bias_offsets && rules.num_biases < 0) return PKV_ERR_BAD_DIMENSION;
+    if (batch == 0) return PKV_OK;
+    if (!logits || !out) return PKV_ERR_NULL_POINTER;
+    if (rules.bias_offsets && rules.num_biases > 0 && (!rules.bias_token_ids || !rules.bias_values))
+        return PKV_ERR_NULL_POINTER;
+    const uintptr_t entry = logits_type == PKV_FP32 ? 4 : 2;
+    if ((uintptr_t)logits % entry) return PKV_ERR_MISALIGNED;
+    if (((uintptr_t)out | (uintptr_t)rules.token_ids | (uintptr_t)rules.prompt_lens |
+         (uintptr_t)rules.token_lens | (uintptr_t)rules.repetition_penalties |
+         (uintptr_t)rules.presence_penalties | (uintptr_t)rules.frequency_penalties |
+         (uintptr_t)rules.bias_offsets | (uintptr_t)rules.bias_token_ids |
+         (uintptr_t)rules.bias_values | (uintptr_t)rules.allowed_mask) & 3)
+        return PKV_ERR_MISALIGNED;
+    // in place only as a whole: fp32 rows that lie where the output's do
+    const bool in_place = logits == (const void*)out;
+    if (in_place && (logits_type != PKV_FP32 || (batch > 1 && logits_stride != vocab)))
+        return PKV_ERR_UNSUPPORTED;
+    if (!in_place) {
+        const uintptr_t x0 = (uintptr_t)logits, y0 = (uintptr_t)out;
+        const uintptr_t x1 = x0 + ((uintptr_t)(batch - 1) * logits_stride + vocab) * entry;
+        const uintptr_t y1 = y0 + (uintptr_t)batch * vocab * 4;
+        if (x0 < y1 && y0 < x1) return PKV_ERR_UNSUPPORTED;
+    }
+    RuleArgs a{};
+    a.logits = logits;
+    a.stride = logits_stride;
+    a.out = out;
+    a.batch = batch;
+    a.vocab = vocab;
+    a.r = rules;
+    a.status = status;
+    a.in_place = in_place;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (logits_type == PKV_FP32) return launch_rules<float>(a, s);
+    if (logits_type == PKV_BF16) return launch_rules<__nv_bfloat16>(a, s);
+    return launch_rules<__half>(a, s);
+}

@@ -521,6 +521,21 @@ int max_resident(const void* fn) {
 // step's kv_store (`store`), or not at all (a plan already in the workspace).
 enum class PlanLaunch { kPlain, kWithStore, kNone };
 
+// The combine kernel, a programmatic dependent of the split kernel before it.
+template <int D>
+int launch_combine(const DecodeArgs& a, cudaStream_t s) {
+    for (int32_t b0 = 0; b0 < a.B; b0 += 65535) {
+        DecodeArgs sub = a;
+        const int32_t rows = a.B - b0 < 65535 ? a.B - b0 : 65535;
+        sub.b0 = b0;
+        const unsigned hblocks = (unsigned)((a.Hq + kCombineHeads - 1) / kCombineHeads);
+        if (launch_dependent(decode_combine_kernel<D>, dim3(hblocks, (unsigned)rows),
+                             dim3(32 * kCombineHeads), s, sub) != cudaSuccess)
+            return PKV_ERR_CUDA;
+    }
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 template <int D>
 int launch_decode(DecodeArgs& a, cudaStream_t s, PlanLaunch plan = PlanLaunch::kPlain,
                   const pkv::StoreRows* store = nullptr) {
@@ -548,16 +563,7 @@ int launch_decode(DecodeArgs& a, cudaStream_t s, PlanLaunch plan = PlanLaunch::k
                              a) != cudaSuccess)
             return PKV_ERR_CUDA;
     }
-    for (int32_t b0 = 0; b0 < a.B; b0 += 65535) {
-        DecodeArgs sub = a;
-        const int32_t rows = a.B - b0 < 65535 ? a.B - b0 : 65535;
-        sub.b0 = b0;
-        const unsigned hblocks = (unsigned)((a.Hq + kCombineHeads - 1) / kCombineHeads);
-        if (launch_dependent(decode_combine_kernel<D>, dim3(hblocks, (unsigned)rows),
-                             dim3(32 * kCombineHeads), s, sub) != cudaSuccess)
-            return PKV_ERR_CUDA;
-    }
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return launch_combine<D>(a, s);
 }
 
 }  // namespace
@@ -647,6 +653,26 @@ int make_decode_args(const void* q, const void* k_cache, const void* v_cache,
 }
 
 }  // namespace
+
+int pkv_decode_make_args(const void* q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                         int32_t max_context_len, float scale, void* out, void* workspace,
+                         size_t workspace_bytes, const pkv_cache_desc& cache, uint32_t* status,
+                         DecodeArgs& a) {
+    return make_decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                            batch, num_q_heads, max_context_len, scale, out, workspace,
+                            workspace_bytes, cache, status, a);
+}
+
+int pkv_launch_decode_plan(const DecodeArgs& a, cudaStream_t s) {
+    decode_plan_kernel<<<1, 1024, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_launch_decode_combine(const DecodeArgs& a, int head_dim, cudaStream_t s) {
+    return head_dim == 128 ? launch_combine<128>(a, s) : launch_combine<64>(a, s);
+}
 
 extern "C" int pkv_paged_decode(const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -240,6 +240,7 @@ int pkv_prefill_make_args(const void* q, const void* k, const void* v, const voi
     a.status = status;
     a.skip_single = 0;
     a.wait_polls = pkv_wait_polls();
+    a.max_cached = INT32_MAX;
     return PKV_OK;
 }
 

@@ -26,6 +26,7 @@ struct PrefillArgs {
     uint32_t* status;
     int32_t skip_single;             // sequences of one query are left to the decode kernels
     uint32_t wait_polls;             // polls of a bounded mbarrier wait
+    int32_t max_cached;              // cached keys a sequence may have, whatever its table holds
 };
 
 // Lengths of sequence b; returns false (and reports) when they are inconsistent.
@@ -36,7 +37,8 @@ __device__ __forceinline__ bool seq_lengths(const PrefillArgs& a, int32_t b, int
     lk = a.cu_k[b + 1] - a.cu_k[b];
     const int32_t c = lk - lq;
     bool ok = lq >= 0 && c >= 0 && q0 >= 0 && q0 + lq <= a.total_q;
-    if (c > 0) ok = ok && a.bt != nullptr && (int64_t)(c + a.bs - 1) / a.bs <= a.MB;
+    if (c > 0)
+        ok = ok && a.bt != nullptr && (int64_t)(c + a.bs - 1) / a.bs <= a.MB && c <= a.max_cached;
     if (!ok && report_bad) report(a.status, PKV_STATUS_BAD_SEQLENS);
     return ok;
 }

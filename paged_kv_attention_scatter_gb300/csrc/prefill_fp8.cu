@@ -1,0 +1,206 @@
+// paged_prefill_varlen_fp8: causal varlen prefill over chunks whose cached
+// prefix lies in an e4m3 cache (scales per cache block and kv head).
+//
+// What it computes: as paged_prefill_varlen, with the prefix rows code * scale.
+//
+// Design.  Prefill is bound by the tensor pipe, and a prefix row is read once
+// per 128-query tile and q head, so turning codes into operands inside the
+// attention kernel would repeat the conversion tens to hundreds of times
+// beside the softmax, the busiest role there.  Instead one pass writes the
+// prefix rows once as bf16 into the workspace, as cache blocks of 128 rows,
+// and the bf16 kernel attends over them: it takes its fastest path (whole-tile
+// TMA boxes) whatever the e4m3 cache's own block size.  With a power-of-two
+// scale, as kv_store_fp8 writes, the bf16 row is exact.  The pass moves 3 bytes
+// per prefix entry (1 read, 2 written), most of which the attention then finds
+// in L2.  Batches whose prefixes would exceed kExpandBytes run in groups of
+// sequences, one after another over the same workspace.
+#include "fp8_common.cuh"
+#include "prefill_common.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kChunkRows = 16;               // prefix rows per CTA
+constexpr int kBlock = 128;                  // rows per workspace cache block
+constexpr int64_t kExpandBytes = 4LL << 30;  // K and V rows of a group, where >= 1 fits
+
+struct ExpandArgs {
+    const uint8_t* kc;
+    const uint8_t* vc;
+    const float* ks;
+    const float* vs;
+    const int32_t* bt;
+    __nv_bfloat16* ko;                       // [sequences * rows_per_seq, Hkv, D]
+    __nv_bfloat16* vo;
+    int32_t* table;                          // [sequences, rows_per_seq / kBlock]
+    int32_t MB, NB, bs, Hkv, D, rows_per_seq;
+};
+
+__device__ __forceinline__ uint32_t to_bf16x2(uint32_t f16x2, float s) {
+    const float2 f = pkv::f16x2_to_float2(f16x2);
+    return pkv::pack_bf16(f.x * s, f.y * s);
+}
+
+// CTA (x, y): prefix rows 16x .. 16x + 15 of sequence y.  A row that cannot be
+// read (block id or scale out of range) is written as zeros and reported.
+__global__ void __launch_bounds__(kThreads) expand_prefix_kernel(ExpandArgs e,
+                                                                 pkv::PrefillArgs p) {
+    pkv::allow_dependent_launch();
+    const int32_t b = blockIdx.y, r0 = blockIdx.x * kChunkRows;
+    if (r0 % kBlock == 0 && threadIdx.x == 0)
+        e.table[(int64_t)b * (e.rows_per_seq / kBlock) + r0 / kBlock] =
+            (int32_t)(((int64_t)b * e.rows_per_seq + r0) / kBlock);
+    int32_t q0, lq, lk;
+    if (!pkv::seq_lengths(p, b, q0, lq, lk, false)) return;   // the plan kernel reports it
+    const int32_t rows = min(lk - lq - r0, kChunkRows);
+    if (rows <= 0) return;
+    const int32_t vecs = e.Hkv * (e.D / 16);                  // 16-code vectors per row
+    uint32_t bad = 0;
+    for (int32_t i = threadIdx.x; i < 2 * rows * vecs; i += kThreads) {
+        const int32_t j = i >> 1;                             // K and V of a vector side by side
+        const bool is_v = i & 1;
+        const int32_t r = j / vecs, c = j - r * vecs;
+        const int32_t key = r0 + r;
+        const int32_t blk = __ldg(e.bt + (int64_t)b * e.MB + key / e.bs);
+        uint4 w = make_uint4(0, 0, 0, 0);
+        float s = 0.f;
+        if ((unsigned)blk < (unsigned)e.NB) {
+            s = __ldg((is_v ? e.vs : e.ks) + (int64_t)blk * e.Hkv + c / (e.D / 16));
+            if (pkv::scale_ok(s)) {
+                w = pkv::ld_stream16((is_v ? e.vc : e.kc) +
+                                     (((int64_t)blk * e.bs + key % e.bs) * vecs + c) * 16);
+            } else {
+                s = 0.f;
+                bad |= PKV_STATUS_BAD_SCALE;
+            }
+        } else {
+            bad |= PKV_STATUS_BAD_BLOCK_ID;
+        }
+        uint32_t h[8];
+        pkv::e4m3x4_to_f16x4(w.x, h[0], h[1]);
+        pkv::e4m3x4_to_f16x4(w.y, h[2], h[3]);
+        pkv::e4m3x4_to_f16x4(w.z, h[4], h[5]);
+        pkv::e4m3x4_to_f16x4(w.w, h[6], h[7]);
+        uint4* dst = reinterpret_cast<uint4*>(is_v ? e.vo : e.ko) +
+                     (((int64_t)b * e.rows_per_seq + key) * vecs + c) * 2;
+        dst[0] = make_uint4(to_bf16x2(h[0], s), to_bf16x2(h[1], s), to_bf16x2(h[2], s),
+                            to_bf16x2(h[3], s));
+        dst[1] = make_uint4(to_bf16x2(h[4], s), to_bf16x2(h[5], s), to_bf16x2(h[6], s),
+                            to_bf16x2(h[7], s));
+    }
+    if (bad) pkv::report(p.status, bad);
+}
+
+struct Fp8PrefillLayout {
+    int64_t rows_per_seq;
+    int32_t group;                           // sequences attended at once
+    size_t off_table, off_k, off_v, total;
+};
+
+Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t max_seqlen_k,
+                                    const pkv_cache_desc& c) {
+    Fp8PrefillLayout L{};
+    auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    L.rows_per_seq = ((int64_t)max_seqlen_k + kBlock) / kBlock * kBlock;
+    const int64_t row = (int64_t)c.num_kv_heads * c.head_dim;
+    int64_t group = kExpandBytes / (L.rows_per_seq * row * 4);
+    if (group > batch) group = batch;
+    if (group > 65535) group = 65535;        // the expanding grid's y extent
+    if (group < 1) group = 1;
+    L.group = (int32_t)group;
+    L.off_table = align(pkv_prefill_layout(batch, total_q).total);
+    L.off_k = align(L.off_table + sizeof(int32_t) * (size_t)(group * (L.rows_per_seq / kBlock)));
+    L.off_v = align(L.off_k + (size_t)(group * L.rows_per_seq * row * 2));
+    L.total = align(L.off_v + (size_t)(group * L.rows_per_seq * row * 2));
+    return L;
+}
+
+struct ExpandCall {
+    ExpandArgs e;
+    pkv::PrefillArgs p;
+    int32_t sequences;
+    cudaStream_t s;
+};
+
+int enqueue_expand(void* ctx, bool* launched) {
+    const ExpandCall& c = *(const ExpandCall*)ctx;
+    const dim3 grid((unsigned)(c.e.rows_per_seq / kChunkRows), (unsigned)c.sequences);
+    expand_prefix_kernel<<<grid, kThreads, 0, c.s>>>(c.e, c.p);
+    *launched = true;
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" size_t pkv_paged_prefill_fp8_workspace_bytes(int32_t batch, int32_t total_q,
+                                                        int32_t num_q_heads,
+                                                        int32_t max_seqlen_k,
+                                                        pkv_cache_desc cache) {
+    (void)num_q_heads;
+    if (batch < 0 || total_q < 0 || max_seqlen_k < 0 || cache.num_kv_heads <= 0 ||
+        cache.head_dim <= 0)
+        return 0;
+    return fp8_prefill_layout(batch, total_q, max_seqlen_k, cache).total;
+}
+
+extern "C" int pkv_paged_prefill_varlen_fp8(
+        const void* q, const void* k, const void* v, const void* k_cache, const void* v_cache,
+        const float* k_scale, const float* v_scale, const int32_t* cu_seqlens_q,
+        const int32_t* cu_seqlens_k, int32_t batch, int32_t total_q, int32_t max_seqlen_q,
+        int32_t max_seqlen_k, int32_t num_q_heads, const int32_t* block_tables,
+        int32_t max_blocks_per_seq, float scale, void* out, void* workspace,
+        size_t workspace_bytes, pkv_cache_desc cache, uint32_t* status, void* stream) {
+    // the bf16 prefill's checks, with this call's cache and tables
+    pkv::PrefillArgs a{};
+    int rc = pkv_prefill_make_args(q, k, v, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, batch,
+                                   total_q, max_seqlen_q, max_seqlen_k, num_q_heads,
+                                   block_tables, max_blocks_per_seq, scale, out, workspace,
+                                   workspace_bytes, cache, status, a);
+    if (rc != PKV_OK || batch == 0 || total_q == 0) return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (!block_tables) return pkv_prefill_launch(a, cache.head_dim, s, nullptr);
+    if (!k_scale || !v_scale) return PKV_ERR_NULL_POINTER;
+    if (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3) return PKV_ERR_MISALIGNED;
+    if (cache.block_size > pkv::kFp8MaxBlockSize) return PKV_ERR_BAD_DIMENSION;
+    if ((int64_t)cache.num_blocks * cache.block_size >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
+    const Fp8PrefillLayout L = fp8_prefill_layout(batch, total_q, max_seqlen_k, cache);
+    if (workspace_bytes < L.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (L.group * L.rows_per_seq >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
+    char* ws = (char*)workspace;
+    ExpandCall c{};
+    c.s = s;
+    c.e.kc = (const uint8_t*)k_cache;
+    c.e.vc = (const uint8_t*)v_cache;
+    c.e.ks = k_scale;
+    c.e.vs = v_scale;
+    c.e.ko = (__nv_bfloat16*)(ws + L.off_k);
+    c.e.vo = (__nv_bfloat16*)(ws + L.off_v);
+    c.e.table = (int32_t*)(ws + L.off_table);
+    c.e.MB = max_blocks_per_seq;
+    c.e.NB = cache.num_blocks;
+    c.e.bs = cache.block_size;
+    c.e.Hkv = cache.num_kv_heads;
+    c.e.D = cache.head_dim;
+    c.e.rows_per_seq = (int32_t)L.rows_per_seq;
+    const int64_t table_keys = (int64_t)max_blocks_per_seq * cache.block_size;
+    a.kc = c.e.ko;
+    a.vc = c.e.vo;
+    a.bt = c.e.table;
+    a.MB = (int32_t)(L.rows_per_seq / kBlock);
+    a.bs = kBlock;
+    a.max_cached = table_keys < INT32_MAX ? (int32_t)table_keys : INT32_MAX;
+    const PrefillPrologue pre{enqueue_expand, &c};
+    for (int32_t b0 = 0; b0 < batch; b0 += L.group) {
+        c.sequences = batch - b0 < L.group ? batch - b0 : L.group;
+        c.e.bt = block_tables + (int64_t)b0 * max_blocks_per_seq;
+        pkv::PrefillArgs sub = a;
+        sub.cu_q = cu_seqlens_q + b0;
+        sub.cu_k = cu_seqlens_k + b0;
+        sub.B = c.sequences;
+        sub.NB = (int32_t)(c.sequences * (L.rows_per_seq / kBlock));
+        c.p = sub;
+        rc = pkv_prefill_launch(sub, cache.head_dim, s, &pre);
+        if (rc != PKV_OK) return rc;
+    }
+    return PKV_OK;
+}

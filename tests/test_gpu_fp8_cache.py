@@ -1,0 +1,571 @@
+"""The 8-bit KV cache on the GPU against the float64 oracle: the store bit for
+bit, decode and prefill within the bounds of fp8_util."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_util as F
+import gpu_util as U
+from oracle import attention as oatt
+from oracle import fp8_cache as ofp
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------
+# store
+# ----------------------------------------------------------------------------
+def _store_case(rng, n, nb, bs, hkv, d, pattern):
+    if pattern == "runs":                       # sequences in order, ragged
+        slots = []
+        perm = rng.permutation(nb)
+        at = 0
+        while len(slots) < n and at < nb:
+            take = min(int(rng.integers(1, 3 * bs + 1)), n - len(slots))
+            pos = int(rng.integers(0, bs))
+            blocks = perm[at:at + -(-(pos + take) // bs)]
+            at += len(blocks)
+            for p in range(pos, pos + take):
+                if p // bs < len(blocks):
+                    slots.append(int(blocks[p // bs]) * bs + p % bs)
+        slots += [-1] * (n - len(slots))
+    elif pattern == "shuffled":                 # any order, padding, one slot often twice
+        slots = rng.integers(-2, nb * bs, n).tolist()
+    elif pattern == "same":                     # every token to one slot
+        slots = [bs // 2] * n
+    else:                                       # one token per block, as a decode step
+        slots = (rng.permutation(nb)[:n] * bs + rng.integers(0, bs, n)).tolist()
+    return np.asarray(slots, np.int32)
+
+
+def _run_store(pkv, dev, k, v, pool, slots, expect=0, **kw):
+    kc, vc, ks, vs, _ = pool.on(dev)
+    st = pkv.new_status(dev)
+    pkv.kv_store_fp8(k.to(dev), v.to(dev), kc, vc, ks, vs, torch.from_numpy(slots).to(dev),
+                     status=st, **kw)
+    assert U.status_word(st) == expect
+    ref = ofp.kv_store(U.f64(k), U.f64(v), pool.codes["k"], pool.codes["v"], pool.scale["k"],
+                       pool.scale["v"], slots)
+    for got, want in ((ks, ref[2]), (vs, ref[3])):
+        np.testing.assert_array_equal(U.f64(got), want)
+    for got, want in ((kc, ref[0]), (vc, ref[1])):
+        got = got.view(torch.uint8).cpu().numpy()
+        same = got == want
+        # a NaN code that was re-scaled may come back with either sign
+        assert (same | ((got & 127 == 127) & (want & 127 == 127))).all()
+
+
+@pytest.mark.parametrize("n,nb,bs,hkv,d,pattern", [
+    (1, 2, 16, 1, 64, "step"), (37, 60, 256, 8, 128, "step"), (5, 9, 1, 2, 64, "step"),
+    (300, 30, 16, 8, 128, "runs"), (513, 9, 256, 2, 128, "runs"), (100, 40, 7, 3, 64, "runs"),
+    (700, 3, 1024, 1, 128, "runs"), (2048, 20, 128, 4, 64, "runs"),
+    (200, 12, 24, 5, 128, "shuffled"), (2048, 6, 48, 2, 64, "shuffled"),
+    (2049, 200, 16, 2, 128, "runs"), (3000, 40, 100, 3, 64, "shuffled"),
+    (5000, 3, 512, 20, 64, "shuffled"), (2500, 2, 8, 1, 64, "same"), (90, 2, 8, 1, 128, "same"),
+    (4097, 4500, 1, 1, 64, "step"),
+])
+def test_store_is_the_oracles(cuda, n, nb, bs, hkv, d, pattern):
+    pkv = U.lib()
+    rng = np.random.default_rng(n * 131 + bs)
+    slots = _store_case(rng, n, nb, bs, hkv, d, pattern)
+    pool = F.Pool([nb * bs - bs], bs, hkv, d, seed=n, spare=1)
+    mag = 2.0 ** rng.integers(-5, 4, (n, hkv, 1))
+    _run_store(pkv, cuda, F.bf16(rng, n, hkv, d, mag=mag), F.bf16(rng, n, hkv, d, mag=mag), pool,
+               slots)
+
+
+@pytest.mark.parametrize("n", [6, 2100])
+def test_store_special_values_and_scales(cuda, n):
+    """Infinities saturate and do not widen the scale, NaN stays; zero rows;
+    values at a power of two's edge; a scale of 0, one that is no power of two,
+    and one that cannot be used."""
+    pkv = U.lib()
+    rng = np.random.default_rng(3)
+    bs, hkv, d = 16, 4, 64
+    pool = F.Pool([16 * bs], bs, hkv, d, seed=5, arbitrary=True, spare=2200)
+    k, v = F.bf16(rng, n, hkv, d), F.bf16(rng, n, hkv, d)
+    k[0, 0, 3], k[0, 0, 4], k[1, 1, 0] = math.inf, -math.inf, math.nan
+    k[2], v[2] = 0.0, 0.0
+    v[3, 0] = 3.5                                # exactly 448 * 2^-7
+    v[3, 1] = 3.515625                           # the next bf16
+    v[3, 2, 0], v[3, 3] = 3.38e38, 1e-38
+    k[4, 0] = math.inf                           # no finite entry at all
+    slots = np.asarray([b * bs + 5 for b in range(n)], np.int32)
+    pool.scale["k"][1, 2], pool.scale["v"][1, 3] = 0.0, 0.0
+    _run_store(pkv, cuda, k, v, pool, slots)
+    pool.scale["k"][0, 1], pool.scale["v"][2, 0] = -1.0, math.inf
+    pool.scale["k"][3, 3] = math.nan
+    _run_store(pkv, cuda, k, v, pool, slots, expect=pkv.STATUS["BAD_SCALE"])
+
+
+def test_store_row_by_row_is_store_at_once(cuda):
+    """Up to the subnormals of a block's final scale."""
+    pkv = U.lib()
+    rng = np.random.default_rng(8)
+    n, bs, hkv, d = 40, 16, 2, 64
+    k = F.bf16(rng, n, hkv, d, mag=2.0 ** rng.integers(-3, 4, (n, 1, 1))).to(cuda)
+    slots = torch.arange(n, dtype=torch.int32, device=cuda) + 2 * bs
+    caches = [[torch.zeros((6, bs, hkv, d), dtype=torch.uint8, device=cuda).view(torch.float8_e4m3fn)
+               for _ in "kv"] + [torch.zeros((6, hkv), device=cuda) for _ in "kv"]
+              for _ in range(2)]
+    pkv.kv_store_fp8(k, k, *caches[0], slots)
+    for t in range(n):
+        pkv.kv_store_fp8(k[t:t + 1], k[t:t + 1], *caches[1], slots[t:t + 1])
+    assert torch.equal(caches[0][2], caches[1][2])
+    a, b = (c[0].double() * c[2].double()[:, None, :, None] for c in caches)
+    s = caches[0][2].double()[:, None, :, None]
+    assert ((a - b).abs() <= torch.where(a.abs() < s * 2.0 ** -6, s * 2.0 ** -9, 0.0)).all()
+
+
+@pytest.mark.parametrize("n", [50, 3000])
+def test_store_reports_slots_outside_the_pool(cuda, n):
+    pkv = U.lib()
+    rng = np.random.default_rng(1)
+    bs, hkv, d = 16, 2, 64
+    pool = F.Pool([300 * bs], bs, hkv, d, seed=2)
+    slots = rng.integers(0, 302 * bs, n).astype(np.int32)
+    slots[7], slots[20] = 302 * bs, 2 ** 31 - 1
+    _run_store(pkv, cuda, F.bf16(rng, n, hkv, d), F.bf16(rng, n, hkv, d), pool, slots,
+               expect=pkv.STATUS["SLOT_OUT_OF_RANGE"])
+
+
+def test_empty_store_and_padding_only(cuda):
+    pkv = U.lib()
+    pool = F.Pool([32], 16, 1, 64, seed=1)
+    none = torch.zeros((0, 1, 64), dtype=torch.bfloat16)
+    _run_store(pkv, cuda, none, none, pool, np.zeros(0, np.int32))
+    rows = torch.ones((9, 1, 64), dtype=torch.bfloat16)
+    _run_store(pkv, cuda, rows, rows, pool, np.full(9, -1, np.int32))
+
+
+# ----------------------------------------------------------------------------
+# decode
+# ----------------------------------------------------------------------------
+def _check_decode(got, pool, q, scale):
+    kv, vv = pool.values("k"), pool.values("v")
+    ref = oatt.paged_decode(U.f64(q), kv, vv, pool.bt, pool.lens, scale)
+    got = U.f64(got)
+    assert np.isfinite(got).all()
+    tol = F.bound(ref, U.f64(q), kv, vv, scale, F.RP_DECODE)
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), (err - tol).max()
+    return ref
+
+
+@pytest.mark.parametrize("lens,bs,hkv,group,d", [
+    ([1], 16, 1, 1, 64), ([1], 256, 8, 2, 128), ([0], 64, 2, 2, 128), ([1000], 256, 8, 2, 128),
+    ([0, 1, 15, 16, 17, 64, 65, 300], 16, 2, 4, 128), ([5, 700, 64, 0, 129], 64, 2, 8, 128),
+    ([5, 700, 64, 0, 129], 64, 2, 8, 64), ([33, 100, 7], 24, 3, 7, 128), ([33, 100, 7], 1, 1, 3, 64),
+    ([255, 256, 257, 1023, 1025], 256, 1, 16, 128), ([255, 256, 257, 1023], 256, 2, 9, 64),
+    ([2000, 1], 1024, 1, 4, 128), ([190, 193, 600], 192, 4, 1, 64), ([500, 13], 100, 2, 5, 128),
+    ([4100, 129, 3], 128, 1, 4, 128), ([40] * 70, 32, 2, 2, 64),
+])
+@pytest.mark.parametrize("arbitrary", [False, True])
+def test_decode_is_the_oracles(cuda, lens, bs, hkv, group, d, arbitrary):
+    pkv = U.lib()
+    rng = np.random.default_rng(len(lens) * 7 + bs)
+    pool = F.Pool(lens, bs, hkv, d, seed=bs + d, spread=4, arbitrary=arbitrary)
+    q = F.bf16(rng, len(lens), hkv * group, d)
+    st = pkv.new_status(cuda)
+    scale = 1 / math.sqrt(d)
+    out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda),
+                               torch.tensor(lens, dtype=torch.int32, device=cuda), scale,
+                               max(lens), status=st)
+    assert U.status_word(st) == 0
+    ref = _check_decode(out, pool, q, scale)
+    assert (ref[[i for i, n in enumerate(lens) if n == 0]] == 0).all()
+
+
+@pytest.mark.parametrize("bs", [16, 64, 40])
+@pytest.mark.parametrize("q_mag,vexp", [(1e25, -60), (1e-30, 100), (3e4, 0), (1.0, -90)])
+def test_decode_ranges(cuda, bs, q_mag, vexp):
+    """Queries and scales far outside f16's range: only the products count."""
+    pkv = U.lib()
+    rng = np.random.default_rng(11)
+    hkv, group, d, lens = 2, 4, 128, [200, 77]
+    pool = F.Pool(lens, bs, hkv, d, seed=4)
+    kexp = -round(math.log2(q_mag))
+    pool.scale["k"] = np.ldexp(pool.scale["k"], kexp).astype(np.float32)
+    pool.scale["v"] = np.ldexp(pool.scale["v"], vexp).astype(np.float32)
+    q = F.bf16(rng, 2, hkv * group, d, mag=q_mag)
+    q[0, 0, :5] = 0.0
+    out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda),
+                               torch.tensor(lens, dtype=torch.int32, device=cuda), 0.125, 200)
+    _check_decode(out, pool, q, 0.125)
+
+
+@pytest.mark.parametrize("bs", [16, 64, 40])
+def test_decode_values_of_very_different_scales(cuda, bs):
+    """Blocks whose V scales differ by 2^80: the small ones' keys still carry
+    their weight in the normaliser."""
+    pkv = U.lib()
+    rng = np.random.default_rng(12)
+    hkv, group, d, lens = 1, 8, 64, [10 * bs]
+    pool = F.Pool(lens, bs, hkv, d, seed=4)
+    pool.scale["v"][::2] = np.ldexp(pool.scale["v"][::2], -80)
+    q = F.bf16(rng, 1, hkv * group, d)
+    out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda),
+                               torch.tensor(lens, dtype=torch.int32, device=cuda), 0.125, lens[0])
+    _check_decode(out, pool, q, 0.125)
+
+
+@pytest.mark.parametrize("bs", [16, 64, 48, 256])
+def test_decode_leaves_out_blocks_it_cannot_read(cuda, bs):
+    """A block id outside the pool, and a block whose scale cannot be used: the
+    status says so, the other keys are attended to."""
+    pkv = U.lib()
+    rng = np.random.default_rng(13)
+    hkv, group, d = 2, 2, 128
+    n = 4 * bs + 3
+    for what in ("id", "k", "v"):
+        pool = F.Pool([n, bs + 1], bs, hkv, d, seed=6)
+        q = F.bf16(rng, 2, hkv * group, d)
+        kept = [0, 2, 3, 4]                      # blocks of sequence 0 without its second
+        bad_blk = int(pool.bt[0, 1])
+        dense = np.concatenate([pool.bt[0, kept], [-1]])
+        args = list(pool.on(cuda))
+        if what == "id":
+            args[4][0, 1] = pool.codes["k"].shape[0] if bs == 16 else -7
+        else:
+            args[2 if what == "k" else 3][bad_blk] = 0.0 if bs == 16 else math.nan
+        st = pkv.new_status(cuda)
+        out = pkv.paged_decode_fp8(q.to(cuda), *args,
+                                   torch.tensor([n, bs + 1], dtype=torch.int32, device=cuda), 0.1,
+                                   n, status=st)
+        name = "BAD_BLOCK_ID" if what == "id" else "BAD_SCALE"
+        assert U.status_word(st) == pkv.STATUS[name]
+        pool.bt[0] = dense[:pool.bt.shape[1]]
+        pool.lens[0] = n - bs
+        _check_decode(out, pool, q, 0.1)
+
+
+def test_decode_bad_context_lens(cuda):
+    pkv = U.lib()
+    rng = np.random.default_rng(14)
+    pool = F.Pool([40, 40, 40, 40], 16, 1, 64, seed=6)
+    q = F.bf16(rng, 4, 2, 64)
+    st = pkv.new_status(cuda)
+    ctx = torch.tensor([40, -1, 49, 40], dtype=torch.int32, device=cuda)
+    out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda), ctx, 0.1, 48, status=st)
+    assert U.status_word(st) == pkv.STATUS["BAD_CONTEXT_LEN"]
+    pool.lens = [40, 0, 0, 40]
+    _check_decode(out, pool, q, 0.1)
+
+
+def test_plan_and_runs_are_the_whole_call(cuda):
+    pkv = U.lib()
+    rng = np.random.default_rng(15)
+    lens = [300, 5, 0, 1000]
+    pool = F.Pool(lens, 64, 2, 128, seed=6)
+    args = pool.on(cuda)
+    ctx = torch.tensor(lens, dtype=torch.int32, device=cuda)
+    ws = pkv.paged_decode_plan(ctx, 8, 1000, args[4].shape[1], args[0])
+    for i in range(3):
+        q = F.bf16(rng, 4, 8, 128).to(cuda)
+        whole = pkv.paged_decode_fp8(q, *args, ctx, 0.1, 1000)
+        assert torch.equal(pkv.paged_decode_run_fp8(q, *args, ctx, 0.1, 1000, ws), whole)
+
+
+@pytest.mark.parametrize("n,bs", [(4, 16), (4, 256), (2200, 16)])
+def test_store_and_decode_in_one_call(cuda, n, bs):
+    """A step's fused call is its two calls, bit for bit; n = 2200 tokens is a
+    call of the store's list form (most of them padding for the decode)."""
+    pkv = U.lib()
+    rng = np.random.default_rng(16)
+    lens = [1, bs, 3 * bs + 2, 2 * bs + 1]
+    pool = F.Pool(lens, bs, 2, 128, seed=6, spare=150)
+    q, k, v = F.bf16(rng, 4, 8, 128), F.bf16(rng, n, 2, 128), F.bf16(rng, n, 2, 128)
+    free = sorted(set(range(pool.codes["k"].shape[0])) - set(pool.bt.reshape(-1).tolist()))
+    slots = [int(pool.bt[i, (m - 1) // bs]) * bs + (m - 1) % bs for i, m in enumerate(lens)]
+    slots += [free[i // bs] * bs + i % bs for i in range(n - 4)]
+    slots = torch.tensor(slots, dtype=torch.int32, device=cuda)
+    ctx = torch.tensor(lens, dtype=torch.int32, device=cuda)
+    q, k, v = q.to(cuda), k.to(cuda), v.to(cuda)
+    a, b = pool.on(cuda), pool.on(cuda)
+    pkv.kv_store_fp8(k, v, *a[:4], slots)
+    want = pkv.paged_decode_fp8(q, *a, ctx, 0.1, max(lens))
+    got = pkv.kv_store_paged_decode_fp8(k, v, slots, q, *b, ctx, 0.1, max(lens))
+    assert torch.equal(got, want)
+    for x, y in zip(a[:4], b[:4]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_cache_beyond_32_bit_offsets(cuda):
+    """Rows whose byte offset needs 33 bits, stored and attended to."""
+    pkv = U.lib()
+    rng = np.random.default_rng(17)
+    bs, hkv, d = 256, 8, 128
+    nb = (1 << 32) // (bs * hkv * d) + 40
+    small = F.Pool([600], bs, hkv, d, seed=9, spare=1)
+    kc = torch.empty((nb, bs, hkv, d), dtype=torch.uint8, device=cuda)
+    vc = torch.empty_like(kc)
+    ks = torch.ones((nb, hkv), device=cuda)
+    vs = torch.ones((nb, hkv), device=cuda)
+    far = nb - 20
+    sk, sv, sks, svs, bt = small.on(cuda)
+    for i in range(4):
+        kc[far + i], vc[far + i] = sk[i].view(torch.uint8), sv[i].view(torch.uint8)
+        ks[far + i], vs[far + i] = sks[i], svs[i]
+    args = (kc.view(torch.float8_e4m3fn), vc.view(torch.float8_e4m3fn), ks, vs)
+    bt = torch.where(bt >= 0, bt + far, bt)
+    q = F.bf16(rng, 1, 16, d)
+    ctx = torch.tensor([600], dtype=torch.int32, device=cuda)
+    row = F.bf16(rng, 1, hkv, d)
+    slot = torch.tensor([int(small.bt[0, 2]) * bs + 599 % bs + far * bs], dtype=torch.int32,
+                        device=cuda)
+    pkv.kv_store_fp8(row.to(cuda), row.to(cuda), *args, slot)
+    out = pkv.paged_decode_fp8(q.to(cuda), *args, bt, ctx, 0.1, 600)
+    ref = ofp.kv_store(U.f64(row), U.f64(row), small.codes["k"], small.codes["v"],
+                       small.scale["k"], small.scale["v"], slot.cpu().numpy() - far * bs)
+    small.codes, small.scale = {"k": ref[0], "v": ref[1]}, {"k": ref[2], "v": ref[3]}
+    _check_decode(out, small, q, 0.1)
+
+
+# ----------------------------------------------------------------------------
+# prefill
+# ----------------------------------------------------------------------------
+def _prefill(pkv, dev, lq, lp, bs, hkv, group, d, seed, max_k=None, extra=0):
+    rng = np.random.default_rng(seed)
+    pool = F.Pool(lp, bs, hkv, d, seed=seed, spread=3)
+    t = sum(lq)
+    q, k, v = (F.bf16(rng, t + extra, h, d) for h in (hkv * group, hkv, hkv))
+    cu = lambda x: np.concatenate([[0], np.cumsum(x)]).astype(np.int32)  # noqa: E731
+    cu_q, cu_k = cu(lq), cu(np.asarray(lq) + np.asarray(lp))
+    scale = 1 / math.sqrt(d)
+    st = pkv.new_status(dev)
+    kc, vc, ks, vs, bt = pool.on(dev)
+    out = torch.full((t + extra, hkv * group, d), 7.0, dtype=torch.bfloat16, device=dev)
+    pkv.paged_prefill_varlen_fp8(q.to(dev), k.to(dev), v.to(dev), kc, vc, ks, vs,
+                                 torch.from_numpy(cu_q).to(dev), torch.from_numpy(cu_k).to(dev),
+                                 max(lq), max_k or int((np.asarray(lq) + lp).max()), bt, scale,
+                                 out=out, status=st)
+    assert U.status_word(st) == 0
+    assert (out[t:] == 7.0).all()                # rows of no sequence: left as they were
+    kv, vv = pool.values("k"), pool.values("v")
+    ref = oatt.paged_prefill_varlen(U.f64(q[:t]), U.f64(k), U.f64(v), kv, vv, cu_q, cu_k, pool.bt,
+                                    scale)
+    everything = [np.concatenate([a.reshape(-1, d), U.f64(b).reshape(-1, d)])
+                  for a, b in ((kv, k), (vv, v))]
+    tol = F.bound(ref, U.f64(q[:t]), everything[0], everything[1], scale, F.RP_PREFILL)
+    err = np.abs(U.f64(out[:t]) - ref)
+    assert (err <= tol).all(), (err - tol).max()
+
+
+@pytest.mark.parametrize("lq,lp,bs,hkv,group,d", [
+    ([1], [1], 16, 1, 1, 64), ([1], [300], 256, 2, 4, 128), ([130], [0], 16, 2, 2, 128),
+    ([5, 1, 140], [128, 127, 129], 16, 2, 2, 128), ([5, 0, 70], [0, 50, 513], 64, 1, 8, 64),
+    ([33, 200], [100, 7], 24, 3, 3, 64), ([17, 3], [1000, 1], 1024, 1, 4, 128),
+    ([129, 1, 1], [255, 256, 257], 128, 2, 1, 128), ([10, 11], [37, 5], 1, 1, 2, 64),
+])
+def test_prefill_is_the_oracles(cuda, lq, lp, bs, hkv, group, d):
+    _prefill(U.lib(), cuda, lq, lp, bs, hkv, group, d, seed=bs + sum(lq), extra=3)
+
+
+def test_prefill_in_groups_of_sequences(cuda):
+    """max_seqlen_k so large that the prefixes' workspace holds two of the five
+    sequences at a time."""
+    pkv = U.lib()
+    need = [pkv.paged_prefill_fp8_workspace_bytes(b, 300, 8, 500000, (64, 16, 8, 128))
+            for b in (1, 2, 3, 5)]
+    assert need[0] < need[1] <= need[2] <= need[3] < 2 * need[1] < 9 << 30
+    _prefill(pkv, cuda, [60, 1, 90, 100, 49], [130, 400, 0, 7, 256], 16, 8, 1, 128, seed=3,
+             max_k=500000)
+
+
+def test_prefill_skips_inconsistent_sequences(cuda):
+    """More cached keys than the table holds (the table's last block ends inside
+    the workspace's), fewer keys than queries, a prefix beyond max_seqlen_k."""
+    pkv = U.lib()
+    rng = np.random.default_rng(2)
+    bs, hkv, d = 16, 1, 64
+    pool = F.Pool([48, 48, 48, 48], bs, hkv, d, seed=1)
+    lq, lk = [4, 4, 4, 4], [4 + 48, 4 + 49, 3, 4 + 48]
+    cu = lambda x: torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32,  # noqa: E731,E501
+                                device=cuda)
+    q, k = F.bf16(rng, 16, 2, d), F.bf16(rng, 16, hkv, d)
+    kc, vc, ks, vs, bt = pool.on(cuda)
+    st = pkv.new_status(cuda)
+    out = torch.full((16, 2, d), 7.0, dtype=torch.bfloat16, device=cuda)
+    pkv.paged_prefill_varlen_fp8(q.to(cuda), k.to(cuda), k.to(cuda), kc, vc, ks, vs, cu(lq),
+                                 cu(lk), 4, 53, bt, 0.125, out=out, status=st)
+    assert U.status_word(st) == pkv.STATUS["BAD_SEQLENS"]
+    assert (out[4:12] == 7.0).all()
+    kv, vv = pool.values("k"), pool.values("v")
+    for i in (0, 3):
+        rows = slice(4 * i, 4 * i + 4)
+        ref = oatt.paged_prefill_varlen(U.f64(q[rows]), U.f64(k[rows]), U.f64(k[rows]), kv, vv,
+                                        [0, 4], [0, 52], pool.bt[i:i + 1], 0.125)
+        tol = F.bound(ref, U.f64(q[rows]), np.concatenate([kv.reshape(-1, d),
+                                                           U.f64(k).reshape(-1, d)]),
+                      np.concatenate([vv.reshape(-1, d), U.f64(k).reshape(-1, d)]), 0.125,
+                      F.RP_PREFILL)
+        assert (np.abs(U.f64(out[rows]) - ref) <= tol).all()
+
+
+def test_prefill_unreadable_prefix_rows_are_zeros(cuda):
+    pkv = U.lib()
+    rng = np.random.default_rng(2)
+    bs, hkv, d = 16, 1, 64
+    for what, bit in (("id", "BAD_BLOCK_ID"), ("scale", "BAD_SCALE")):
+        pool = F.Pool([48], bs, hkv, d, seed=1)
+        q, k = F.bf16(rng, 3, 2, d), F.bf16(rng, 3, hkv, d)
+        kc, vc, ks, vs, bt = pool.on(cuda)
+        blk = int(pool.bt[0, 1])
+        if what == "id":
+            bt[0, 1] = 10 ** 6
+        else:
+            ks[blk], vs[blk] = 0.0, math.inf
+        cu = lambda n: torch.tensor([0, n], dtype=torch.int32, device=cuda)  # noqa: E731
+        st = pkv.new_status(cuda)
+        out = pkv.paged_prefill_varlen_fp8(q.to(cuda), k.to(cuda), k.to(cuda), kc, vc, ks, vs,
+                                           cu(3), cu(51), 3, 51, bt, 0.125, status=st)
+        assert U.status_word(st) == pkv.STATUS[bit]
+        for c in pool.codes.values():
+            c[blk] = 0
+        kv, vv = pool.values("k"), pool.values("v")
+        ref = oatt.paged_prefill_varlen(U.f64(q), U.f64(k), U.f64(k), kv, vv, [0, 3], [0, 51],
+                                        pool.bt, 0.125)
+        tol = F.bound(ref, U.f64(q), np.concatenate([kv.reshape(-1, d), U.f64(k).reshape(-1, d)]),
+                      np.concatenate([vv.reshape(-1, d), U.f64(k).reshape(-1, d)]), 0.125,
+                      F.RP_PREFILL)
+        assert (np.abs(U.f64(out) - ref) <= tol).all()
+
+
+# ----------------------------------------------------------------------------
+# together, streams and graphs
+# ----------------------------------------------------------------------------
+def test_a_conversation_in_the_8_bit_cache(cuda):
+    """Two prompts prefilled in two chunks each, then decode steps and sampling
+    with penalties, every step against the oracle's own cache."""
+    pkv = U.lib()
+    rng = np.random.default_rng(20)
+    bs, hkv, hq, d, vocab = 16, 2, 6, 64, 300
+    scale = 1 / math.sqrt(d)
+    tables = np.asarray([[3, 7, 1, 9], [0, 5, 8, 2]], np.int32)
+    codes = [np.full((10, bs, hkv, d), 0x7F, np.uint8) for _ in "kv"]
+    scales = [np.zeros((10, hkv), np.float32) for _ in "kv"]
+    gpu = [torch.from_numpy(c).to(cuda).view(torch.float8_e4m3fn) for c in codes] + \
+          [torch.from_numpy(s).to(cuda) for s in scales]
+    bt = torch.from_numpy(tables).to(cuda)
+    st = pkv.new_status(cuda)
+    slots_of = lambda b, a, n: [int(tables[b, p // bs]) * bs + p % bs  # noqa: E731
+                                for p in range(a, a + n)]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda)  # noqa: E731
+    state = (*codes, *scales)
+    done = [0, 0]
+    for new in ([20, 9], [14, 22]):
+        t = sum(new)
+        q, k, v = (F.bf16(rng, t, h, d) for h in (hq, hkv, hkv))
+        cu_q = np.concatenate([[0], np.cumsum(new)])
+        cu_k = np.concatenate([[0], np.cumsum(np.asarray(new) + done)])
+        out = pkv.paged_prefill_varlen_fp8(q.to(cuda), k.to(cuda), v.to(cuda), *gpu, i32(cu_q),
+                                           i32(cu_k), max(new), 60, bt, scale, status=st)
+        kv, vv = ofp.decode_values(state[0], state[2]), ofp.decode_values(state[1], state[3])
+        ref = oatt.paged_prefill_varlen(U.f64(q), U.f64(k), U.f64(v), kv, vv, cu_q, cu_k, tables,
+                                        scale)
+        tol = F.bound(ref, U.f64(q), np.full((1, d), 6.0), np.full((1, d), 6.0), scale,
+                      F.RP_PREFILL)
+        assert (np.abs(U.f64(out) - ref) <= tol).all()
+        slots = slots_of(0, done[0], new[0]) + slots_of(1, done[1], new[1])
+        pkv.kv_store_fp8(k.to(cuda), v.to(cuda), *gpu, i32(slots), status=st)
+        state = ofp.kv_store(U.f64(k), U.f64(v), *state, slots)[:4]
+        done = [a + n for a, n in zip(done, new)]
+    for _ in range(4):
+        q, k, v = (F.bf16(rng, 2, h, d) for h in (hq, hkv, hkv))
+        slots = slots_of(0, done[0], 1) + slots_of(1, done[1], 1)
+        done = [n + 1 for n in done]
+        out = pkv.kv_store_paged_decode_fp8(k.to(cuda), v.to(cuda), i32(slots), q.to(cuda), *gpu,
+                                            bt, i32(done), scale, 64, status=st)
+        state = ofp.kv_store(U.f64(k), U.f64(v), *state, slots)[:4]
+        kv, vv = ofp.decode_values(state[0], state[2]), ofp.decode_values(state[1], state[3])
+        ref = oatt.paged_decode(U.f64(q), kv, vv, tables, done, scale)
+        tol = F.bound(ref, U.f64(q), np.full((1, d), 6.0), np.full((1, d), 6.0), scale,
+                      F.RP_DECODE)
+        assert (np.abs(U.f64(out) - ref) <= tol).all()
+        # the sampler's part of the step: every token but one forbidden or used up
+        logits = torch.from_numpy(rng.normal(size=(2, vocab)).astype(np.float32)).to(cuda)
+        want = rng.integers(0, vocab, 2)
+        mask = np.zeros((2, -(-vocab // 32)), np.uint32)
+        for b in range(2):
+            mask[b, want[b] // 32] |= np.uint32(1 << (want[b] % 32))
+        ruled = pkv.apply_logit_rules(logits, allowed_mask=torch.from_numpy(
+            mask.view(np.int32)).to(cuda), status=st)
+        ids = pkv.sample(ruled, torch.ones(2, device=cuda),
+                         torch.ones((2, vocab), device=cuda), status=st)
+        assert ids.tolist() == want.tolist()
+    assert U.status_word(st) == 0
+    for got, ref in zip(gpu[:2], state[:2]):
+        np.testing.assert_array_equal(got.view(torch.uint8).cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+def test_captured_step_replays(cuda, bs):
+    """Store, decode and prefill captured in one graph, replayed with new
+    contents, equal the eager calls; run on a side stream."""
+    pkv = U.lib()
+    rng = np.random.default_rng(21)
+    lens = [bs + 1, 3 * bs, 7]
+    pool = F.Pool(lens, bs, 2, 128, seed=6)
+    args = pool.on(cuda)
+    twin = [a.clone() for a in args]
+    slots = torch.tensor([int(pool.bt[i, (n - 1) // bs]) * bs + (n - 1) % bs
+                          for i, n in enumerate(lens)], dtype=torch.int32, device=cuda)
+    ctx = torch.tensor(lens, dtype=torch.int32, device=cuda)
+    cu_q = torch.tensor([0, 1, 3, 6], dtype=torch.int32, device=cuda)
+    cu_k = torch.cumsum(torch.tensor([0] + [n + m for n, m in zip(lens, (1, 2, 3))]), 0).to(
+        device=cuda, dtype=torch.int32)
+    q, k, v = (torch.zeros((n, h, 128), dtype=torch.bfloat16, device=cuda)
+               for n, h in ((6, 4), (6, 2), (6, 2)))
+
+    def step(c, stream=None):
+        a = pkv.kv_store_paged_decode_fp8(k[:3], v[:3], slots, q[:3], *c, ctx, 0.1, max(lens),
+                                          stream=stream)
+        b = pkv.paged_prefill_varlen_fp8(q, k, v, *c[:4], cu_q, cu_k, 3, max(lens) + 3, c[4], 0.1,
+                                         stream=stream)
+        return a, b
+
+    def refill(seed):
+        r = np.random.default_rng(seed)
+        for t in (q, k, v):
+            t.copy_(F.bf16(r, *t.shape))
+    refill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    warm = [a.clone() for a in args]
+    torch.cuda.current_stream().synchronize()
+    step(warm, side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(args)
+    for seed in (1, 2):
+        refill(seed)
+        graph.replay()
+        want = step(twin)
+        torch.cuda.synchronize()
+        for x, y in zip(held, want):
+            assert torch.equal(x, y)
+        for x, y in zip(args, twin):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_random_cases(cuda):
+    """Seeded random geometries of store, decode and prefill."""
+    pkv = U.lib()
+    rng = np.random.default_rng(99)
+    for i in range(30):
+        bs = int(rng.choice([1, 3, 8, 16, 20, 32, 64, 96, 128, 256]))
+        hkv, group, d = (int(rng.choice(c)) for c in ([1, 2, 3, 8], [1, 2, 5, 8, 12], [64, 128]))
+        lens = rng.integers(0, 400, int(rng.integers(1, 6))).tolist()
+        pool = F.Pool(lens, bs, hkv, d, seed=1000 + i, spread=6, arbitrary=bool(i % 2))
+        q = F.bf16(rng, len(lens), hkv * group, d, mag=2.0)
+        out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda),
+                                   torch.tensor(lens, dtype=torch.int32, device=cuda), 0.09,
+                                   max(max(lens), 1))
+        _check_decode(out, pool, q, 0.09)
+        n = int(rng.choice([1, 9, 300, 2100]))
+        slots = _store_case(rng, n, pool.codes["k"].shape[0], bs, hkv, d,
+                            str(rng.choice(["runs", "shuffled"])))
+        _run_store(pkv, cuda, F.bf16(rng, n, hkv, d), F.bf16(rng, n, hkv, d), pool, slots)
