@@ -126,6 +126,11 @@ struct Fp8DecodeArgs {
 
 }  // namespace pkv
 
+// The TMA split kernel (paged_decode_fp8_tma.cu): whether the shapes are its own,
+// and its launch as a programmatic dependent of the plan kernel.
+bool pkv_decode_fp8_tma_supported(const pkv::Fp8DecodeArgs& fa);
+int pkv_launch_decode_fp8_tma(const pkv::Fp8DecodeArgs& fa, int head_dim, cudaStream_t s);
+
 // kv_store_fp8.cu: argument checks (enqueue nothing) and the launch.
 struct Fp8StoreCall {
     const void* k;

@@ -270,7 +270,10 @@ int launch_split(const Fp8DecodeArgs& fa, cudaStream_t s) {
 int launch_decode(Fp8DecodeArgs& fa, int head_dim, bool plan, cudaStream_t s) {
     int rc = plan ? pkv_launch_decode_plan(fa.d, s) : PKV_OK;
     if (rc != PKV_OK) return rc;
-    rc = head_dim == 128 ? launch_split<128>(fa, s) : launch_split<64>(fa, s);
+    if (pkv_decode_fp8_tma_supported(fa))
+        rc = pkv_launch_decode_fp8_tma(fa, head_dim, s);
+    else
+        rc = head_dim == 128 ? launch_split<128>(fa, s) : launch_split<64>(fa, s);
     if (rc != PKV_OK) return rc;
     return pkv_launch_decode_combine(fa.d, head_dim, s);
 }

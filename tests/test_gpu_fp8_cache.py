@@ -569,3 +569,30 @@ def test_random_cases(cuda):
         slots = _store_case(rng, n, pool.codes["k"].shape[0], bs, hkv, d,
                             str(rng.choice(["runs", "shuffled"])))
         _run_store(pkv, cuda, F.bf16(rng, n, hkv, d), F.bf16(rng, n, hkv, d), pool, slots)
+
+
+def test_decode_gives_up_then_recovers(cuda):
+    """The TMA split kernel's bounded waits run out: it reports, lets its copies
+    land and returns; the next call is the oracle's."""
+    pkv = U.lib()
+    rng = np.random.default_rng(31)
+    lens = [700, 64, 1500, 1]
+    pool = F.Pool(lens, 64, 2, 128, seed=6)
+    q = F.bf16(rng, 4, 8, 128)
+    args = (q.to(cuda), *pool.on(cuda), torch.tensor(lens, dtype=torch.int32, device=cuda), 0.1,
+            1500)
+    try:
+        for polls in (0, 2):
+            pkv.set_wait_poll_limit(polls)
+            st = pkv.new_status(cuda)
+            pkv.paged_decode_fp8(*args, status=st)
+            word = U.status_word(st)
+            if polls == 0:
+                assert word & pkv.STATUS["WAIT_TIMEOUT"]
+            assert word & ~pkv.STATUS["WAIT_TIMEOUT"] == 0
+    finally:
+        pkv.set_wait_poll_limit()
+    st = pkv.new_status(cuda)
+    out = pkv.paged_decode_fp8(*args, status=st)
+    assert U.status_word(st) == 0
+    _check_decode(out, pool, q, 0.1)
