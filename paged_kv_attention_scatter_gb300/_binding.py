@@ -9,6 +9,7 @@ a missing library is an error, never a fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -548,71 +549,88 @@ def set_wait_poll_limit(polls: int = DEFAULT_WAIT_POLLS) -> None:
 FP8 = torch.float8_e4m3fn
 
 
-def _on(dev, stream, call):
-    """call(raw stream) with `dev` current and, if given, `stream` current."""
+def _on(index, stream, call):
+    """call(raw stream) with CUDA device `index` current and, if given, `stream`."""
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, expected cuda:{index}")
         with torch.cuda.stream(stream):                 # makes its device current too
             return call(stream.cuda_stream)
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return call(torch.cuda.current_stream(dev).cuda_stream)
-    return call(torch.cuda.current_stream(dev).cuda_stream)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index))
+    return call(torch._C._cuda_getCurrentRawStream(index))
 
 
-def _workspace(workspace, need, dev):
+def _at(t, name, dtype, index) -> int:
+    """_dev for a tensor that must be on CUDA device `index`; when it is as it
+    must be, a few attribute reads: a small call's time is mostly the host's."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and \
+            t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, dtype, torch.device("cuda", max(index, 0)))
+
+
+def _maybe(t, name, dtype, index):
+    return None if t is None else _at(t, name, dtype, index)
+
+
+@functools.lru_cache(maxsize=256)
+def _desc(*shape) -> CacheDesc:
+    return CacheDesc(*shape)
+
+
+def _workspace(workspace, need, index):
+    """(address, bytes, what keeps them alive) of the caller's workspace or a new one."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _dev(workspace, "workspace", torch.uint8, dev)
-    return workspace
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+        return workspace.data_ptr(), need, workspace
+    return _at(workspace, "workspace", torch.uint8, index), workspace.numel(), workspace
 
 
-def _ws_args(workspace):
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-
-
-def _fp8_cache(k_cache, v_cache, k_scale, v_scale, device=None):
-    """Checks an e4m3 cache; returns (device, the four addresses, descriptor)."""
-    dev = k_cache.device if device is None else device
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+def _fp8_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks an e4m3 cache; returns (device index, the four addresses, descriptor)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
                          "num_kv_heads, head_dim]")
-    nb, bs, hkv, d = k_cache.shape
-    if k_scale.shape != (nb, hkv) or v_scale.shape != (nb, hkv):
+    if k_scale.shape != (shape[0], shape[2]) or v_scale.shape != k_scale.shape:
         raise ValueError("k_scale and v_scale must be [num_blocks, num_kv_heads]")
-    ptrs = (_dev(k_cache, "k_cache", FP8, dev), _dev(v_cache, "v_cache", FP8, dev),
-            _dev(k_scale, "k_scale", torch.float32, dev),
-            _dev(v_scale, "v_scale", torch.float32, dev))
-    return dev, ptrs, CacheDesc(nb, bs, hkv, d)
+    index = k_cache.get_device()
+    return index, (_at(k_cache, "k_cache", FP8, index), _at(v_cache, "v_cache", FP8, index),
+                   _at(k_scale, "k_scale", torch.float32, index),
+                   _at(v_scale, "v_scale", torch.float32, index)), _desc(*shape)
 
 
-def _rows_of(k, v, n, desc, dev):
+def _rows_of(k, v, n, desc, index):
     """Checks bf16 K/V rows [n, num_kv_heads, head_dim]; returns their addresses."""
     if k.shape != (n, desc.num_kv_heads, desc.head_dim) or v.shape != k.shape:
         raise ValueError("k/v must be [num_tokens, num_kv_heads, head_dim] matching the cache")
-    return _dev(k, "k", torch.bfloat16, dev), _dev(v, "v", torch.bfloat16, dev)
+    return _at(k, "k", torch.bfloat16, index), _at(v, "v", torch.bfloat16, index)
 
 
-def _decode_batch(q, block_tables, context_lens, desc, dev):
-    """Checks a decode batch over a cache; returns (B, Hq, q, tables, lengths)."""
-    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+def _decode_batch(q, block_tables, context_lens, desc, index):
+    """Checks a decode batch over a cache; returns (B, Hq, table width, addresses)."""
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != desc.head_dim:
         raise ValueError("q must be [batch, num_q_heads, head_dim] matching the cache")
-    B, Hq, _ = q.shape
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+    width = block_tables.shape
+    if len(width) != 2 or width[0] != shape[0] or context_lens.shape != shape[:1]:
         raise ValueError("block_tables must be [batch, max_blocks_per_seq] and context_lens "
                          "[batch]")
-    return (B, Hq, _dev(q, "q", torch.bfloat16, dev),
-            _dev(block_tables, "block_tables", torch.int32, dev),
-            _dev(context_lens, "context_lens", torch.int32, dev))
+    return (shape[0], shape[1], width[1], _at(q, "q", torch.bfloat16, index),
+            _at(block_tables, "block_tables", torch.int32, index),
+            _at(context_lens, "context_lens", torch.int32, index))
 
 
-def _out_like(out, q, dev):
+def _out_like(out, q, index):
     if out is None:
         return torch.empty_like(q)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    _dev(out, "out", q.dtype, dev)
+    _at(out, "out", q.dtype, index)
     return out
 
 
@@ -630,34 +648,36 @@ def kv_store_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, workspa
     earlier rows are re-scaled.  Of several tokens with one slot the last is
     stored.  Start with zeroed scales."""
     lib = load()
-    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    index, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
     n = slot_mapping.numel()
-    rows = _rows_of(k, v, n, desc, dev)
-    slots = _dev(slot_mapping, "slot_mapping", torch.int32, dev)
-    st = _ptr_or_null(status, "status", torch.int32, dev)
+    rows = _rows_of(k, v, n, desc, index)
+    slots = _at(slot_mapping, "slot_mapping", torch.int32, index)
+    st = _maybe(status, "status", torch.int32, index)
 
     def call(s):
-        ws = _workspace(workspace, lib.pkv_kv_store_fp8_workspace_bytes(n, desc), dev)
-        _check(lib.pkv_kv_store_fp8(*rows, *cache, slots, n, *_ws_args(ws), desc, st, s),
+        ws, size, _keep = _workspace(workspace, lib.pkv_kv_store_fp8_workspace_bytes(n, desc),
+                                     index)
+        _check(lib.pkv_kv_store_fp8(*rows, *cache, slots, n, ws, size, desc, st, s),
                "pkv_kv_store_fp8")
-    _on(dev, stream, call)
+    _on(index, stream, call)
 
 
 def _decode_fp8(name, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
                 max_context_len, out, workspace, status, stream):
     lib = load()
-    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
-    B, Hq, qp, bt, ctx = _decode_batch(q, block_tables, context_lens, desc, dev)
-    st = _ptr_or_null(status, "status", torch.int32, dev)
+    index, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    B, Hq, width, qp, bt, ctx = _decode_batch(q, block_tables, context_lens, desc, index)
+    st = _maybe(status, "status", torch.int32, index)
     max_len = int(max_context_len)
 
     def call(s):
-        o = _out_like(out, q, dev)
-        ws = _workspace(workspace, lib.pkv_paged_decode_workspace_bytes(B, Hq, max_len, desc), dev)
-        _check(getattr(lib, name)(qp, *cache, bt, block_tables.shape[1], ctx, B, Hq, max_len,
-                                  float(scale), o.data_ptr(), *_ws_args(ws), desc, st, s), name)
+        o = _out_like(out, q, index)
+        ws, size, _keep = _workspace(
+            workspace, lib.pkv_paged_decode_workspace_bytes(B, Hq, max_len, desc), index)
+        _check(getattr(lib, name)(qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
+                                  o.data_ptr(), ws, size, desc, st, s), name)
         return o
-    return _on(dev, stream, call)
+    return _on(index, stream, call)
 
 
 def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
@@ -693,24 +713,23 @@ def kv_store_paged_decode_fp8(k, v, slot_mapping, q, k_cache, v_cache, k_scale, 
                               workspace=None, status=None, stream=None) -> torch.Tensor:
     """kv_store_fp8 of the new tokens followed by paged_decode_fp8, in one call."""
     lib = load()
-    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    index, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
     n = slot_mapping.numel()
-    rows = _rows_of(k, v, n, desc, dev)
-    slots = _dev(slot_mapping, "slot_mapping", torch.int32, dev)
-    B, Hq, qp, bt, ctx = _decode_batch(q, block_tables, context_lens, desc, dev)
-    st = _ptr_or_null(status, "status", torch.int32, dev)
+    rows = _rows_of(k, v, n, desc, index)
+    slots = _at(slot_mapping, "slot_mapping", torch.int32, index)
+    B, Hq, width, qp, bt, ctx = _decode_batch(q, block_tables, context_lens, desc, index)
+    st = _maybe(status, "status", torch.int32, index)
     max_len = int(max_context_len)
 
     def call(s):
-        o = _out_like(out, q, dev)
-        ws = _workspace(workspace, lib.pkv_kv_store_paged_decode_fp8_workspace_bytes(
-            n, B, Hq, max_len, desc), dev)
+        o = _out_like(out, q, index)
+        ws, size, _keep = _workspace(workspace, lib.pkv_kv_store_paged_decode_fp8_workspace_bytes(
+            n, B, Hq, max_len, desc), index)
         _check(lib.pkv_kv_store_paged_decode_fp8(
-            *rows, slots, n, qp, *cache, bt, block_tables.shape[1], ctx, B, Hq, max_len,
-            float(scale), o.data_ptr(), *_ws_args(ws), desc, st, s),
-            "pkv_kv_store_paged_decode_fp8")
+            *rows, slots, n, qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
+            o.data_ptr(), ws, size, desc, st, s), "pkv_kv_store_paged_decode_fp8")
         return o
-    return _on(dev, stream, call)
+    return _on(index, stream, call)
 
 
 def paged_prefill_fp8_workspace_bytes(batch, total_q, num_q_heads, max_seqlen_k,
@@ -729,11 +748,11 @@ def paged_prefill_varlen_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, cu_seq
     required (without a cached prefix, call paged_prefill_varlen).  Output rows
     of no sequence are left unwritten."""
     lib = load()
-    dev, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
+    index, cache, desc = _fp8_cache(k_cache, v_cache, k_scale, v_scale)
     if q.dim() != 3 or q.shape[2] != desc.head_dim:
         raise ValueError("q must be [total_q, num_q_heads, head_dim] matching the cache")
     T, Hq, _ = q.shape
-    rows = _rows_of(k, v, T, desc, dev)
+    rows = _rows_of(k, v, T, desc, index)
     B = cu_seqlens_q.numel() - 1
     if B < 0 or cu_seqlens_k.numel() != B + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must both be [batch + 1]")
@@ -741,23 +760,22 @@ def paged_prefill_varlen_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, cu_seq
         raise ValueError("block_tables is required")
     if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
-    qp = _dev(q, "q", torch.bfloat16, dev)
-    cu_q = _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
-    cu_k = _dev(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev)
-    bt = _dev(block_tables, "block_tables", torch.int32, dev)
-    st = _ptr_or_null(status, "status", torch.int32, dev)
-    max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
+    qp = _at(q, "q", torch.bfloat16, index)
+    cu_q = _at(cu_seqlens_q, "cu_seqlens_q", torch.int32, index)
+    cu_k = _at(cu_seqlens_k, "cu_seqlens_k", torch.int32, index)
+    bt = _at(block_tables, "block_tables", torch.int32, index)
+    st = _maybe(status, "status", torch.int32, index)
+    max_q, max_k, width = int(max_seqlen_q), int(max_seqlen_k), block_tables.shape[1]
 
     def call(s):
-        o = _out_like(out, q, dev)
-        ws = _workspace(workspace, lib.pkv_paged_prefill_fp8_workspace_bytes(B, T, Hq, max_k, desc),
-                        dev)
+        o = _out_like(out, q, index)
+        ws, size, _keep = _workspace(
+            workspace, lib.pkv_paged_prefill_fp8_workspace_bytes(B, T, Hq, max_k, desc), index)
         _check(lib.pkv_paged_prefill_varlen_fp8(
-            qp, *rows, *cache, cu_q, cu_k, B, T, max_q, max_k, Hq, bt, block_tables.shape[1],
-            float(scale), o.data_ptr(), *_ws_args(ws), desc, st, s),
-            "pkv_paged_prefill_varlen_fp8")
+            qp, *rows, *cache, cu_q, cu_k, B, T, max_q, max_k, Hq, bt, width, float(scale),
+            o.data_ptr(), ws, size, desc, st, s), "pkv_paged_prefill_varlen_fp8")
         return o
-    return _on(dev, stream, call)
+    return _on(index, stream, call)
 
 
 _LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -779,10 +797,10 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
     [B, ceil(V / 32)] int32 has bit i % 32 of word i / 32 set where token i may be
     drawn.  Pass out=logits (fp32, contiguous) to work in place."""
     lib = load()
-    dev = logits.device
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
-    if logits.dtype not in _LOGIT_TYPES:
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
     if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError("logits must be [batch, vocab] with contiguous rows")
@@ -790,12 +808,13 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
     stride = logits.stride(0) if B > 1 else V
     if stride < V:
         raise ValueError("rows of logits overlap")
+    index = logits.get_device()
     r = LogitRules()
     i32, f32 = torch.int32, torch.float32
     if token_ids is not None:
         if token_ids.dim() != 2 or token_ids.shape[0] != B:
             raise ValueError("token_ids must be [batch, max_tokens]")
-        r.token_ids = _dev(token_ids, "token_ids", i32, dev)
+        r.token_ids = _at(token_ids, "token_ids", i32, index)
         r.max_tokens = token_ids.shape[1]
     per_row = (("prompt_lens", prompt_lens, i32), ("token_lens", token_lens, i32),
                ("repetition_penalties", repetition_penalties, f32),
@@ -808,7 +827,7 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
             raise ValueError(f"{name} needs token_ids")
         if t.shape != (B,):
             raise ValueError(f"{name} must be [batch]")
-        setattr(r, name, _dev(t, name, dtype, dev))
+        setattr(r, name, _at(t, name, dtype, index))
     biases = (bias_offsets, bias_token_ids, bias_values)
     if any(t is not None for t in biases):
         if any(t is None for t in biases):
@@ -816,23 +835,23 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
         if bias_offsets.shape != (B + 1,) or bias_token_ids.dim() != 1 or \
                 bias_values.shape != bias_token_ids.shape:
             raise ValueError("bias_offsets must be [batch + 1], the others [num_biases]")
-        r.bias_offsets = _dev(bias_offsets, "bias_offsets", i32, dev)
-        r.bias_token_ids = _dev(bias_token_ids, "bias_token_ids", i32, dev)
-        r.bias_values = _dev(bias_values, "bias_values", f32, dev)
+        r.bias_offsets = _at(bias_offsets, "bias_offsets", i32, index)
+        r.bias_token_ids = _at(bias_token_ids, "bias_token_ids", i32, index)
+        r.bias_values = _at(bias_values, "bias_values", f32, index)
         r.num_biases = bias_token_ids.numel()
     if allowed_mask is not None:
         if allowed_mask.shape != (B, (V + 31) // 32):
             raise ValueError("allowed_mask must be [batch, ceil(vocab / 32)]")
-        r.allowed_mask = _dev(allowed_mask, "allowed_mask", i32, dev)
+        r.allowed_mask = _at(allowed_mask, "allowed_mask", i32, index)
     if out is not None:
         if out.shape != (B, V):
             raise ValueError("out must be [batch, vocab]")
-        _dev(out, "out", f32, dev)
-    st = _ptr_or_null(status, "status", torch.int32, dev)
+        _at(out, "out", f32, index)
+    st = _maybe(status, "status", torch.int32, index)
 
     def call(s):
-        o = torch.empty((B, V), dtype=f32, device=dev) if out is None else out
-        _check(lib.pkv_apply_logit_rules(logits.data_ptr(), _LOGIT_TYPES[logits.dtype], stride, B,
-                                         V, r, o.data_ptr(), st, s), "pkv_apply_logit_rules")
+        o = torch.empty((B, V), dtype=f32, device=logits.device) if out is None else out
+        _check(lib.pkv_apply_logit_rules(logits.data_ptr(), kind, stride, B, V, r, o.data_ptr(),
+                                         st, s), "pkv_apply_logit_rules")
         return o
-    return _on(dev, stream, call)
+    return _on(index, stream, call)

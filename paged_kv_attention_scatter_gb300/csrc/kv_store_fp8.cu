@@ -16,16 +16,18 @@
 // each time it grew.
 //
 // Design.  One CTA owns a (block, set of heads): it needs every row the call
-// stores there before it can write the first code.  It collects the rows of
-// its block -- the last token of each slot -- in shared memory, takes each
-// head's maximum while reading the rows once into registers, and writes codes
-// from the registers.  A row's head segment is read as 16 bytes a lane (D/8
-// lanes) and written as 8.  How rows find their block, by the number of tokens:
-//  * up to 2048: one launch, a CTA per token.  The CTAs of a block's first
-//    rows share its heads: one CTA for a decode step's single row, up to 2 * Hkv
-//    for a block that a prefill chunk fills; the rest of the block's CTAs leave
-//    after one look at the 16 tokens before theirs.  Each CTA that stays scans
-//    all slots (8 KB at most, from L2).
+// stores there before it can write the first code.  It takes each head's
+// maximum while reading the rows once into registers, and writes codes from the
+// registers.  A row's head segment is read as 16 bytes a lane (D/8 lanes) and
+// written as 8.  Rows that are consecutive tokens in consecutive slots, as a
+// sequence's always are, are addressed by their first; any others (duplicates:
+// the last token of a slot is stored) through a list in shared memory.  How
+// rows find their block, by the number of tokens:
+//  * up to 2048: one launch, a CTA per token.  Each scans all slots (8 KB at
+//    most, out of L2, in one round of loads) for its block's tokens; the CTAs of
+//    the first of them share the block's heads, one CTA for a decode step's
+//    single row, up to 2 * Hkv for a block that a prefill chunk fills, and the
+//    others leave.
 //  * more: that scan is quadratic, so a first kernel links the runs of
 //    consecutive tokens in each block into a list per block, and the store
 //    kernel's CTAs walk the lists.
@@ -35,7 +37,9 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKeep = 8;                     // row segments a lane keeps in registers
+// Row segments a lane keeps in registers: a decode step has one row a block, a
+// prefill chunk 256 over 16 lane groups.
+constexpr int kKeepScan = 4, kKeepList = 16;
 constexpr int32_t kScanTokens = 2048;        // largest call of the scanning form
 constexpr int kRowsPerPart = 16;             // rows for which one more CTA joins a block
 
@@ -54,23 +58,39 @@ struct StoreArgs {
     int32_t* count;                          // blocks in `list`, minus 1
     int32_t* head;                           // [NB]: token that starts the block's last run, -1
     int32_t* next;                           // [n]: start of the run linked before, -1
-    int32_t* list;                           // [min(n, NB)]: blocks that get rows
+    int2* list;                              // [min(n, NB)]: blocks that get rows, a run of each
 };
 
+constexpr int kScanLoads = kScanTokens / kThreads;
+
+// The rows that a call stores into one block: `rows` of them, tokens
+// token0 + i at offsets offset0 + i (dense), or as listed.
 struct BlockRows {
     int32_t winner[pkv::kFp8MaxBlockSize];   // offset -> last token stored there, -1
     int32_t token[pkv::kFp8MaxBlockSize];    // the rows, in no particular order
     int16_t offset[pkv::kFp8MaxBlockSize];
-    int32_t rows;
+    int32_t rows, token0, offset0;
+    bool dense;
     uint32_t amax[kThreads / 8];             // per lane group
     float ratio[kThreads / 8];               // per pair in hand: old / new scale where it grew
 };
 
-// Magnitude bits of the larger finite entry of a bf16 pair and `m`.
-__device__ __forceinline__ uint32_t amax_pair(uint32_t m, uint32_t w) {
-    const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
-    m = max(m, lo < 0x7f80u ? lo : 0u);
-    return max(m, hi < 0x7f80u ? hi : 0u);
+// Larger magnitudes of the bf16 pairs of a vector and of `m`, two 16-bit lanes.
+__device__ __forceinline__ uint32_t amax8(uint32_t m, const uint4& w) {
+    m = __vmaxu2(m, w.x & 0x7fff7fffu);
+    m = __vmaxu2(m, w.y & 0x7fff7fffu);
+    m = __vmaxu2(m, w.z & 0x7fff7fffu);
+    return __vmaxu2(m, w.w & 0x7fff7fffu);
+}
+
+// The same of finite entries only.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+    const uint32_t lo = w & 0x7fffu, hi = w & 0x7fff0000u;
+    return (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f800000u ? hi : 0u);
+}
+__device__ __forceinline__ uint32_t finite_amax8(uint32_t m, const uint4& w) {
+    return amax8(m, make_uint4(finite_pair(w.x), finite_pair(w.y), finite_pair(w.z),
+                               finite_pair(w.w)));
 }
 
 // 2^e for the least e with (bf16 magnitude) <= 448 * 2^e, clamped.
@@ -111,9 +131,15 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
            (uint32_t)pkv::float2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
 }
 
-// The winners as a compact list (any order); ends with a barrier.
-__device__ __forceinline__ void compact_rows(const StoreArgs& a, BlockRows& sm) {
+__device__ __forceinline__ void clear_rows(const StoreArgs& a, BlockRows& sm) {
+    for (int o = threadIdx.x; o < a.bs; o += kThreads) sm.winner[o] = -1;
+    if (threadIdx.x == 0) sm.rows = 0;
+}
+
+// The winners as a compact list (any order), between barriers.
+__device__ __forceinline__ void list_rows(const StoreArgs& a, BlockRows& sm) {
     __syncthreads();
+    if (threadIdx.x == 0) sm.dense = false;
     for (int o = threadIdx.x; o < a.bs; o += kThreads) {
         const int32_t t = sm.winner[o];
         if (t >= 0) {
@@ -125,15 +151,9 @@ __device__ __forceinline__ void compact_rows(const StoreArgs& a, BlockRows& sm) 
     __syncthreads();
 }
 
-__device__ __forceinline__ void clear_rows(const StoreArgs& a, BlockRows& sm) {
-    for (int o = threadIdx.x; o < a.bs; o += kThreads) sm.winner[o] = -1;
-    if (threadIdx.x == 0) sm.rows = 0;
-    __syncthreads();
-}
-
-// Stores the collected rows of block `blk` for the (tensor, head) pairs
-// part, part + parts, ... of the 2 * Hkv.  Pair p is head p >> 1 of K (even) or V.
-template <int D>
+// Stores the rows of block `blk` for the (tensor, head) pairs part, part +
+// parts, ... of the 2 * Hkv.  Pair p is head p >> 1 of K (even) or V.
+template <int D, int kKeep>
 __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, int32_t blk,
                                             int part, int parts) {
     constexpr int kLanes = D / 8;            // lanes of a row's head segment
@@ -146,8 +166,16 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
     while (gpp > 1 && kGroups / gpp < mine) gpp >>= 1;
     const int at_once = kGroups / gpp, sub = group % gpp;
     const int rows = sm.rows;
-    const bool fresh = sm.winner[0] >= 0;
+    const bool dense = sm.dense;
+    const int32_t token0 = sm.token0, offset0 = sm.offset0;
+    const bool fresh = dense ? offset0 == 0 : sm.winner[0] >= 0;
     const int64_t row_codes = (int64_t)a.Hkv * D;
+    auto token_of = [&](int r) { return dense ? token0 + r : sm.token[r]; };
+    auto offset_of = [&](int r) { return dense ? offset0 + r : (int)sm.offset[r]; };
+    // rows of the block that this call does not store
+    auto other = [&](int o) {
+        return dense ? o < offset0 || o >= offset0 + rows : sm.winner[o] < 0;
+    };
     for (int i0 = 0; i0 < mine; i0 += at_once) {
         const int i = i0 + group / gpp;
         const bool live = i < mine;
@@ -157,34 +185,38 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
         uint8_t* dst = ((pair & 1) ? a.vc : a.kc) + (int64_t)blk * a.bs * row_codes + h * D +
                        lane * 8;
         float* scale_at = ((pair & 1) ? a.vs : a.ks) + (int64_t)blk * a.Hkv + h;
+        auto load = [&](int r) { return __ldg(src + (int64_t)token_of(r) * (row_codes / 8)); };
+        // ---- the pair's maximum; the first kKeep rows stay in registers ----
+        const int n = live ? rows : 0;
+        uint4 keep[kKeep];
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j) {
+            keep[j] = make_uint4(0, 0, 0, 0);
+            if (sub + j * gpp < n) keep[j] = load(sub + j * gpp);
+        }
         float old = 0.f;
         if (live && !fresh) old = *scale_at;
-        // ---- the pair's maximum; the first kKeep rows stay in registers ----
-        uint4 keep[kKeep];
         uint32_t m = 0;
-        if (live) {
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j) {
-                const int r = sub + j * gpp;
-                keep[j] = make_uint4(0, 0, 0, 0);
-                if (r < rows) keep[j] = __ldg(src + (int64_t)sm.token[r] * (row_codes / 8));
-            }
+        for (int j = 0; j < kKeep; ++j) m = amax8(m, keep[j]);
+        const int rest = sub + kKeep * gpp;
+#pragma unroll 4
+        for (int r = rest; r < n; r += gpp) m = amax8(m, load(r));
+        if ((m & 0x7fffu) >= 0x7f80u || m >= 0x7f800000u) {      // infinities or NaN
+            m = 0;
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j)
-                m = amax_pair(amax_pair(amax_pair(amax_pair(m, keep[j].x), keep[j].y), keep[j].z),
-                              keep[j].w);
-            for (int r = sub + kKeep * gpp; r < rows; r += gpp) {
-                const uint4 w = __ldg(src + (int64_t)sm.token[r] * (row_codes / 8));
-                m = amax_pair(amax_pair(amax_pair(amax_pair(m, w.x), w.y), w.z), w.w);
-            }
+            for (int j = 0; j < kKeep; ++j) m = finite_amax8(m, keep[j]);
+            for (int r = rest; r < n; r += gpp) m = finite_amax8(m, load(r));
         }
+        m = max(m & 0xffffu, m >> 16);
 #pragma unroll
         for (int off = kLanes / 2; off > 0; off >>= 1)
             m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-        if (lane == 0) sm.amax[group] = m;
-        __syncthreads();                     // every group has read its old scale too
-        for (int g = 0; g < gpp; ++g) m = max(m, sm.amax[group - sub + g]);
-        __syncthreads();                     // before the next round's maxima
+        if (gpp > 1) {
+            if (lane == 0) sm.amax[group] = m;
+            __syncthreads();                 // every group has read its old scale too
+            for (int g = 0; g < gpp; ++g) m = max(m, sm.amax[group - sub + g]);
+        }
         float ratio = 0.f;
         if (live) {
             if (!(old == 0.f || pkv::scale_ok(old))) {
@@ -193,21 +225,19 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
             }
             const float scale = fmaxf(old, scale_for(m));
             const Quantiser quant = quantiser(scale);
+            auto store = [&](int r, const uint4& w) {
+                *reinterpret_cast<uint2*>(dst + offset_of(r) * row_codes) = quant.eight(w);
+            };
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j) {
-                const int r = sub + j * gpp;
-                if (r < rows)
-                    *reinterpret_cast<uint2*>(dst + sm.offset[r] * row_codes) =
-                        quant.eight(keep[j]);
-            }
-            for (int r = sub + kKeep * gpp; r < rows; r += gpp) {
-                const uint4 w = __ldg(src + (int64_t)sm.token[r] * (row_codes / 8));
-                *reinterpret_cast<uint2*>(dst + sm.offset[r] * row_codes) = quant.eight(w);
-            }
+            for (int j = 0; j < kKeep; ++j)
+                if (sub + j * gpp < n) store(sub + j * gpp, keep[j]);
+#pragma unroll 4
+            for (int r = rest; r < n; r += gpp) store(r, load(r));
             if (old > 0.f && scale > old) ratio = __fdiv_rn(old, scale);
             if (lane == 0 && sub == 0) *scale_at = scale;
         }
         if (lane == 0 && sub == 0) sm.ratio[group / gpp] = ratio;
+        // (this barrier also lets the next round's maxima be written)
         if (!__syncthreads_or(ratio > 0.f)) continue;
         // ---- blocks that grew: their other rows, the whole CTA on one pair at a
         // time (a decode step's pair has one lane group, and 256 rows one after
@@ -218,18 +248,19 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
             const int pr = part + (i0 + p) * parts;
             uint8_t* base = ((pr & 1) ? a.vc : a.kc) + (int64_t)blk * a.bs * row_codes +
                             (pr >> 1) * D + lane * 8;
-            for (int o0 = group; o0 < a.bs; o0 += kKeep * kGroups) {
-                uint2 c[kKeep];
+            constexpr int kBatch = 8;
+            for (int o0 = group; o0 < a.bs; o0 += kBatch * kGroups) {
+                uint2 c[kBatch];
 #pragma unroll
-                for (int j = 0; j < kKeep; ++j) {
+                for (int j = 0; j < kBatch; ++j) {
                     const int o = o0 + j * kGroups;
-                    if (o < a.bs && sm.winner[o] < 0)
+                    if (o < a.bs && other(o))
                         c[j] = *reinterpret_cast<const uint2*>(base + o * row_codes);
                 }
 #pragma unroll
-                for (int j = 0; j < kKeep; ++j) {
+                for (int j = 0; j < kBatch; ++j) {
                     const int o = o0 + j * kGroups;
-                    if (o < a.bs && sm.winner[o] < 0)
+                    if (o < a.bs && other(o))
                         *reinterpret_cast<uint2*>(base + o * row_codes) =
                             make_uint2(rescale4(c[j].x, r), rescale4(c[j].y, r));
                 }
@@ -247,9 +278,15 @@ __device__ __forceinline__ int parts_of(int rows, int pairs) {
 template <int D>
 __global__ void __launch_bounds__(kThreads) store_scan_kernel(StoreArgs a) {
     __shared__ BlockRows sm;
-    __shared__ int32_t before, total;
+    __shared__ int32_t before, total, first_token, first_slot;
     pkv::allow_dependent_launch();
     const int32_t t = blockIdx.x;
+    int32_t s[kScanLoads];
+#pragma unroll
+    for (int j = 0; j < kScanLoads; ++j) {
+        const int32_t i = threadIdx.x + j * kThreads;
+        s[j] = i < a.n ? __ldg(a.slots + i) : -1;
+    }
     const int32_t slot = a.slots[t];
     if (slot < 0) return;
     if (slot >= a.num_slots) {
@@ -258,35 +295,57 @@ __global__ void __launch_bounds__(kThreads) store_scan_kernel(StoreArgs a) {
     }
     const int32_t blk = slot / a.bs;
     const int32_t lo = blk * a.bs, hi = lo + a.bs;
-    const int pairs = 2 * a.Hkv;
-    // this token's rank in its block is at least the number of the block's
-    // tokens among the `pairs` before it: at `pairs` no part is left for it
-    if (pairs <= kThreads) {
-        const int32_t s = (threadIdx.x < pairs && t > (int32_t)threadIdx.x)
-                              ? a.slots[t - 1 - threadIdx.x] : -1;
-        if (__syncthreads_count(s >= lo && s < hi) >= pairs) return;
+    if (threadIdx.x == 0) {
+        before = total = 0;
+        first_token = INT_MAX;
     }
-    clear_rows(a, sm);
-    if (threadIdx.x == 0) before = total = 0;
     __syncthreads();
     int b = 0, all = 0;
-    for (int32_t i = threadIdx.x; i < a.n; i += kThreads) {
-        const int32_t s = a.slots[i];
-        if (s < lo || s >= hi) continue;
-        atomicMax(&sm.winner[s - lo], i);
+    int32_t first = INT_MAX;
+#pragma unroll
+    for (int j = kScanLoads - 1; j >= 0; --j) {
+        if (s[j] < lo || s[j] >= hi) continue;
+        const int32_t i = threadIdx.x + j * kThreads;
+        first = i;
         ++all;
         b += i < t;
     }
     if (all) {
         atomicAdd(&total, all);
         atomicAdd(&before, b);
+        atomicMin(&first_token, first);
     }
     __syncthreads();
-    const int parts = parts_of(total, pairs);
-    const int part = before;
+    const int rows = total, part = before, parts = parts_of(rows, 2 * a.Hkv);
     if (part >= parts) return;
-    compact_rows(a, sm);
-    store_block<D>(a, sm, blk, part, parts);
+    if (threadIdx.x == first_token % kThreads) first_slot = a.slots[first_token];
+    __syncthreads();
+    // dense: the block's tokens are first_token + i in slots first_slot + i
+    bool in_line = true;
+#pragma unroll
+    for (int j = 0; j < kScanLoads; ++j) {
+        const int32_t i = threadIdx.x + j * kThreads;
+        if (s[j] >= lo && s[j] < hi)
+            in_line = in_line && i - first_token == s[j] - first_slot && i - first_token < rows;
+    }
+    if (__syncthreads_and(in_line)) {
+        if (threadIdx.x == 0) {
+            sm.dense = true;
+            sm.rows = rows;
+            sm.token0 = first_token;
+            sm.offset0 = first_slot - lo;
+        }
+        __syncthreads();
+    } else {
+        clear_rows(a, sm);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kScanLoads; ++j)
+            if (s[j] >= lo && s[j] < hi)
+                atomicMax(&sm.winner[s[j] - lo], (int32_t)threadIdx.x + j * kThreads);
+        list_rows(a, sm);
+    }
+    store_block<D, kKeepScan>(a, sm, blk, part, parts);
 }
 
 // More tokens: each block's runs as a linked list, and the blocks as a list.
@@ -305,41 +364,69 @@ __global__ void __launch_bounds__(kThreads) store_link_kernel(StoreArgs a) {
     if (prev >= 0 && prev < a.num_slots && prev / a.bs == blk) return;   // inside a run
     const int32_t linked = atomicExch(&a.head[blk], t);
     a.next[t] = linked;
-    if (linked < 0) a.list[atomicAdd(a.count, 1) + 1] = blk;
+    if (linked < 0) a.list[atomicAdd(a.count, 1) + 1] = make_int2(blk, t);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) store_list_kernel(StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) store_list_kernel(StoreArgs a) {
     __shared__ BlockRows sm;
     pkv::wait_for_predecessor();             // the linked runs
     pkv::allow_dependent_launch();
     const int pairs = 2 * a.Hkv;
     const int max_parts = parts_of(a.bs, pairs);
     const int64_t items = (int64_t)(*a.count + 1) * max_parts;
-    int32_t have = -1;                       // block whose rows are in shared memory
+    int32_t have = -1;                       // block whose rows are in hand
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-        const int32_t blk = a.list[i / max_parts];
+        const int2 entry = a.list[i / max_parts];
+        const int32_t blk = entry.x, run = entry.y;
         const int part = (int)(i % max_parts);
         if (blk != have) {
-            __syncthreads();
-            clear_rows(a, sm);
             const int32_t lo = blk * a.bs, hi = lo + a.bs;
-            for (int32_t run = a.head[blk]; run >= 0; run = a.next[run]) {
-                // the run's tokens: up to the first one of another block
-                for (int32_t j = run;; j += kThreads) {
-                    const int32_t t = j + (int32_t)threadIdx.x;
-                    const int32_t s = t < a.n ? a.slots[t] : -1;
-                    const bool in = s >= lo && s < hi;
-                    if (in) atomicMax(&sm.winner[s - lo], t);
-                    if (!__syncthreads_and(in)) break;
-                }
+            const int32_t head = a.head[blk], slot0 = a.slots[run];
+            // the block's only run, one row a slot, no longer than the block?
+            int32_t rows = 0;
+            bool ok = head == run;
+            for (int32_t j = 0;; j += kThreads) {
+                const int32_t k = j + (int32_t)threadIdx.x;
+                const int32_t s = k < a.n - run ? a.slots[run + k] : -1;
+                const bool in = s >= lo && s < hi;
+                ok = ok && (!in || s == slot0 + k);
+                const int in_run = __syncthreads_count(in);
+                rows += in_run;
+                if (in_run < kThreads) break;
             }
-            compact_rows(a, sm);
+            // a token of this block behind the run's end would be another run's
+            // (head != run), and is not read as one of this run
+            ok = __syncthreads_and(ok);
+            if (ok) {
+                if (threadIdx.x == 0) {
+                    sm.dense = true;
+                    sm.rows = rows;
+                    sm.token0 = run;
+                    sm.offset0 = slot0 - lo;
+                }
+                __syncthreads();
+            } else {
+                clear_rows(a, sm);
+                __syncthreads();
+                for (int32_t r = head; r >= 0; r = a.next[r]) {
+                    // the run's tokens: up to the first one of another block
+                    for (int32_t j = r;; j += kThreads) {
+                        const int32_t t = j + (int32_t)threadIdx.x;
+                        const int32_t s = t < a.n ? a.slots[t] : -1;
+                        const bool in = s >= lo && s < hi;
+                        if (in) atomicMax(&sm.winner[s - lo], t);
+                        if (!__syncthreads_and(in)) break;
+                    }
+                }
+                list_rows(a, sm);
+            }
             have = blk;
         }
         // a part beyond the rows' need has nothing to do
         const int parts = parts_of(sm.rows, pairs);
-        if (part < parts) store_block<D>(a, sm, blk, part, parts);
+        if (part < parts) store_block<D, kKeepList>(a, sm, blk, part, parts);
+        __syncthreads();                     // the rows in hand are read to the end
     }
 }
 
@@ -354,7 +441,7 @@ StoreLayout store_layout(int32_t n, int32_t num_blocks) {
     L.off_head = 16;                         // behind the count, cleared with it
     L.off_next = align(L.off_head + sizeof(int32_t) * (size_t)num_blocks);
     L.off_list = align(L.off_next + sizeof(int32_t) * (size_t)n);
-    L.total = align(L.off_list + sizeof(int32_t) * (size_t)(n < num_blocks ? n : num_blocks));
+    L.total = align(L.off_list + sizeof(int2) * (size_t)(n < num_blocks ? n : num_blocks));
     return L;
 }
 
@@ -383,7 +470,7 @@ int launch_store(const Fp8StoreCall& c, cudaStream_t s) {
     a.count = (int32_t*)ws;
     a.head = (int32_t*)(ws + L.off_head);
     a.next = (int32_t*)(ws + L.off_next);
-    a.list = (int32_t*)(ws + L.off_list);
+    a.list = (int2*)(ws + L.off_list);
     if (cudaMemsetAsync(ws, 0xff, L.off_head + sizeof(int32_t) * (size_t)a.NB, s) != cudaSuccess)
         return PKV_ERR_CUDA;
     store_link_kernel<<<(unsigned)((a.n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);

@@ -79,19 +79,46 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
     if (a.r.allowed_mask != nullptr)
         mask = a.r.allowed_mask + (int64_t)b * mask_words + (lo >> 5);   // lo % 32 == 0
 
+    // ---- the segment's logits, all in flight while the history is counted ----
+    constexpr int E = 16 / sizeof(T);        // entries per load
+    constexpr int U = kMaxSegment / E / kThreads;
+    const int nv = kVec ? len / E : 0;
+    uint4 raw[kVec ? U : 1];
+    uint32_t allow[kVec ? U : 1];
+    if constexpr (kVec) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = threadIdx.x + u * kThreads;
+            if (v < nv) raw[u] = __ldcs(reinterpret_cast<const uint4*>(row) + v);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = threadIdx.x + u * kThreads;
+            allow[u] = v < nv && mask ? __ldg(mask + (v * E >> 5)) : 0xffffffffu;
+        }
+    }
+
+    int32_t e0 = 0, e1 = 0;                  // the row's biases
+    if (a.r.bias_offsets != nullptr) {
+        e0 = a.r.bias_offsets[b];
+        e1 = a.r.bias_offsets[b + 1];
+    }
+
     // ---- the row's history ----
     RowRules p{1.f, 0.f, 0.f, false};
     int32_t n_tokens = 0, n_prompt = 0;
     if (a.r.token_ids != nullptr) {
-        n_tokens = a.r.token_lens != nullptr ? a.r.token_lens[b] : a.r.max_tokens;
-        n_prompt = a.r.prompt_lens != nullptr ? a.r.prompt_lens[b] : 0;
+        n_tokens = a.r.max_tokens;
+        // one round trip for all of them
+        if (a.r.token_lens != nullptr) n_tokens = a.r.token_lens[b];
+        if (a.r.prompt_lens != nullptr) n_prompt = a.r.prompt_lens[b];
+        if (a.r.repetition_penalties != nullptr) p.rep = a.r.repetition_penalties[b];
+        if (a.r.presence_penalties != nullptr) p.pres = a.r.presence_penalties[b];
+        if (a.r.frequency_penalties != nullptr) p.freq = a.r.frequency_penalties[b];
         if (n_tokens < 0 || n_tokens > a.r.max_tokens || n_prompt < 0 || n_prompt > n_tokens) {
             if (lo == 0 && threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
             n_tokens = 0;
         }
-        if (a.r.repetition_penalties != nullptr) p.rep = a.r.repetition_penalties[b];
-        if (a.r.presence_penalties != nullptr) p.pres = a.r.presence_penalties[b];
-        if (a.r.frequency_penalties != nullptr) p.freq = a.r.frequency_penalties[b];
         const bool rep_ok = isfinite(p.rep) && p.rep > 0.f;
         const bool add_ok = isfinite(p.freq) && isfinite(p.pres);
         if (!(rep_ok && add_ok) && lo == 0 && threadIdx.x == 0)
@@ -107,16 +134,24 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
         __syncthreads();
         const int32_t* ids = a.r.token_ids + (int64_t)b * a.r.max_tokens;
         bool bad = false;
-#pragma unroll 4
-        for (int32_t i = threadIdx.x; i < n_tokens; i += kThreads) {
-            const int32_t id = __ldg(ids + i);
-            bad |= id >= a.vocab;
-            const uint32_t at = (uint32_t)(id - lo);
-            if (id < lo || at >= (uint32_t)len) continue;
-            if (i < n_prompt)
-                atomicOr(&words[at], kInPrompt);
-            else
-                atomicAdd(&words[at], kGenerated);
+        constexpr int kIds = 8;              // loads in flight a lane
+        for (int32_t i0 = threadIdx.x; i0 < n_tokens; i0 += kIds * kThreads) {
+            int32_t id[kIds];
+#pragma unroll
+            for (int u = 0; u < kIds; ++u) {
+                const int32_t i = i0 + u * kThreads;
+                id[u] = i < n_tokens ? __ldg(ids + i) : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < kIds; ++u) {
+                bad |= id[u] >= a.vocab;
+                const uint32_t at = (uint32_t)(id[u] - lo);
+                if (id[u] < lo || at >= (uint32_t)len) continue;
+                if (i0 + u * kThreads < n_prompt)
+                    atomicOr(&words[at], kInPrompt);
+                else
+                    atomicAdd(&words[at], kGenerated);
+            }
         }
         if (bad && lo == 0) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
         __syncthreads();
@@ -124,53 +159,40 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
 
     // ---- one pass over the segment ----
     if constexpr (kVec) {
-        constexpr int E = 16 / sizeof(T);    // entries per load
-        const int nv = len / E;
-        constexpr int U = sizeof(T) == 4 ? 4 : 2;      // loads in flight a lane
-        for (int v0 = threadIdx.x; v0 < nv; v0 += U * kThreads) {
-            uint4 raw[U];
-            uint32_t allow[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int v = v0 + u * kThreads;
-                if (v >= nv) continue;
-                raw[u] = __ldcs(reinterpret_cast<const uint4*>(row + v * E));
-                allow[u] = mask ? __ldg(mask + (v * E >> 5)) >> (v * E & 31) : 0xffffffffu;
-            }
+        for (int u = 0; u < U; ++u) {
+            const int v = threadIdx.x + u * kThreads;
+            if (v >= nv) continue;
+            const T* in = reinterpret_cast<const T*>(&raw[u]);
+            float x[E];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int v = v0 + u * kThreads;
-                if (v >= nv) continue;
-                const T* in = reinterpret_cast<const T*>(&raw[u]);
-                float x[E];
+            for (int e = 0; e < E; ++e) x[e] = to_float(in[e]);
+            bool changed = !a.in_place;
+            if (p.penalties) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = to_float(in[e]);
-                bool changed = !a.in_place;
-                if (p.penalties) {
-#pragma unroll
-                    for (int q = 0; q < E / 4; ++q) {
-                        const uint4 w = smem[v * (E / 4) + q];
-                        if ((w.x | w.y | w.z | w.w) == 0) continue;
-                        changed = true;
-                        x[4 * q] = penalise(x[4 * q], w.x, p);
-                        x[4 * q + 1] = penalise(x[4 * q + 1], w.y, p);
-                        x[4 * q + 2] = penalise(x[4 * q + 2], w.z, p);
-                        x[4 * q + 3] = penalise(x[4 * q + 3], w.w, p);
-                    }
-                }
-                constexpr uint32_t kAll = (1u << E) - 1u;
-                if ((allow[u] & kAll) != kAll) {
+                for (int q = 0; q < E / 4; ++q) {
+                    const uint4 w = smem[v * (E / 4) + q];
+                    if ((w.x | w.y | w.z | w.w) == 0) continue;
                     changed = true;
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (!(allow[u] >> e & 1u)) x[e] = -INFINITY;
+                    x[4 * q] = penalise(x[4 * q], w.x, p);
+                    x[4 * q + 1] = penalise(x[4 * q + 1], w.y, p);
+                    x[4 * q + 2] = penalise(x[4 * q + 2], w.z, p);
+                    x[4 * q + 3] = penalise(x[4 * q + 3], w.w, p);
                 }
-                if (changed) {
+            }
+            constexpr uint32_t kAll = (1u << E) - 1u;
+            const uint32_t bits = allow[u] >> (v * E & 31) & kAll;
+            if (bits != kAll) {
+                changed = true;
 #pragma unroll
-                    for (int q = 0; q < E / 4; ++q)
-                        *reinterpret_cast<float4*>(out + v * E + 4 * q) =
-                            make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-                }
+                for (int e = 0; e < E; ++e)
+                    if (!(bits >> e & 1u)) x[e] = -INFINITY;
+            }
+            if (changed) {
+#pragma unroll
+                for (int q = 0; q < E / 4; ++q)
+                    *reinterpret_cast<float4*>(out + v * E + 4 * q) =
+                        make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             }
         }
         for (int i = nv * E + threadIdx.x; i < len; i += kThreads) {
@@ -180,19 +202,19 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
             out[i] = x;
         }
     } else {
-        constexpr int U = 8;
-        for (int i0 = threadIdx.x; i0 < len; i0 += U * kThreads) {
-            T raw[U];
+        constexpr int kLoads = 8;
+        for (int i0 = threadIdx.x; i0 < len; i0 += kLoads * kThreads) {
+            T one[kLoads];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < kLoads; ++u) {
                 const int i = i0 + u * kThreads;
-                if (i < len) raw[u] = row[i];
+                if (i < len) one[u] = row[i];
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < kLoads; ++u) {
                 const int i = i0 + u * kThreads;
                 if (i >= len) continue;
-                float x = to_float(raw[u]);
+                float x = to_float(one[u]);
                 if (p.penalties) x = penalise(x, words[i], p);
                 if (mask && !(__ldg(mask + (i >> 5)) >> (i & 31) & 1u)) x = -INFINITY;
                 out[i] = x;
@@ -202,7 +224,6 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
 
     // ---- biases of this segment's entries: the last one for a token counts ----
     if (a.r.bias_offsets != nullptr) {
-        const int32_t e0 = a.r.bias_offsets[b], e1 = a.r.bias_offsets[b + 1];
         if (e0 < 0 || e1 < e0 || e1 > a.r.num_biases) {
             if (lo == 0 && threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
         } else if (e1 > e0) {
