@@ -270,7 +270,9 @@ int launch_split(const Fp8DecodeArgs& fa, cudaStream_t s) {
 int launch_decode(Fp8DecodeArgs& fa, int head_dim, bool plan, cudaStream_t s) {
     int rc = plan ? pkv_launch_decode_plan(fa.d, s) : PKV_OK;
     if (rc != PKV_OK) return rc;
-    if (pkv_decode_fp8_tma_supported(fa))
+    if (head_dim == 128)
+        rc = pkv_launch_decode_fp8_tc(fa, s);
+    else if (pkv_decode_fp8_tma_supported(fa))
         rc = pkv_launch_decode_fp8_tma(fa, head_dim, s);
     else
         rc = head_dim == 128 ? launch_split<128>(fa, s) : launch_split<64>(fa, s);

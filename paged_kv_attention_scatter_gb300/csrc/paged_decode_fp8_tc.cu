@@ -1,0 +1,851 @@
+// paged_decode_fp8 split kernel on the 5th-generation tensor cores (head_dim
+// 128, any block size).
+//
+// The sums are those stated in paged_decode_fp8.cu.  Here the codes are never
+// converted: tcgen05.mma takes them as they lie in shared memory, keys (for S)
+// and head_dim (for O) as its 128 rows, and the at most 8 q heads of a unit as
+// its 16 columns:
+//   S[key, n] = K8[key, :] . Q[n, :]      A = K, K-major;   B = Q, K-major
+//   O[d, n]   = sum_key V8[key, d] P[key, n]   A = V, MN-major;  B = P, MN-major
+// Q and P have to be e4m3 as well, whose significand is 4 bits; each is the sum
+// of two e4m3 values, in a column of its own each, H columns apart:
+//   q * up = q1 + q2 / 16, up the power of two that brings a row's largest entry
+//     to [2^7, 2^8).  A bf16 has 8 significant bits, so q1 rounds to the first 4
+//     and q2 holds the rest exactly, down to 2^-22 of the row's largest entry.
+//   p = 2^(y - M + 8) <= 256 likewise: off by 2^-9 of itself, or 2^-22 of the
+//     row's largest weight.
+// M is the running maximum over all keys of the unit: the four softmax warps
+// exchange their maxima each stage, so no p exceeds 256.  (A reference that
+// lags, redone when it is passed, needs headroom that e4m3 lacks: 448 / 256.)
+//
+// Roles, one CTA per SM, a ring of 128-key stages (32 KB):
+//   warps 0-3  softmax: thread i has key i of a stage (TMEM lane i).  It reads
+//              the key's S columns, exchanges maxima, writes the key's 16 bytes of
+//              P (one 16-byte store: B, MN-major, 16 columns wide) and zeroes the V
+//              row of a key that does not count (0 * NaN is NaN).  Then it takes the
+//              stage before's O, thread i being head_dim entry i now, and adds it
+//              to fp32 registers: O = (O + O') alpha.  TMEM accumulates within a
+//              stage only, so nothing in it is ever rescaled, and a unit's output
+//              needs no merge but the sum of L.
+//   warp 4     S issuer, up to two stages ahead of the softmax (two S buffers).
+//   warp 5     P V issuer; its completion frees the stage's slot.
+//   warp 6     Q: scales, splits and lays out the next unit's rows.
+//   warp 7     producer, block sizes that are multiples of 64: per stage two
+//              64-key TMA boxes of K and two of V, each in one cache block, with
+//              its scales in the stage's record.
+//   warps 7-10 producers, other block sizes: lane l of a warp looks up its key's
+//              block and scales (a stage ahead), the warp gathers the 32 rows with
+//              16-byte cp.async into the layout the boxes would have; rows that do
+//              not count are filled with zeros.  Three stages are in flight.
+// What the HMMA kernels of the other cases spend their issue slots on -- the
+// conversions, two thirds idle MMAs, the per-warp partial outputs -- is gone: a
+// stage costs a softmax warp about 200 instructions.  Every mbarrier wait is
+// bounded; on expiry the CTA unwinds as in paged_decode_tma.cu, and TMEM is
+// freed after its last MMA.
+#include <cudaTypedefs.h>
+
+#include "fp8_common.cuh"
+#include "tc_utils.cuh"
+#include "tma_host.cuh"
+
+using pkv::Fp8DecodeArgs;
+using pkv::kMaxGroup;
+
+namespace {
+
+namespace tc = pkv::tc;
+
+constexpr int D = 128;
+constexpr int kBoxKeys = 64;
+constexpr int kStageKeys = 128;
+constexpr int kTileBytes = kStageKeys * D;       // K or V of a stage
+constexpr int kStages = 6;
+constexpr int kCols = 16;                        // MMA N
+constexpr int kSoftmaxWarps = 4;
+constexpr int kFirstProducer = 7;
+constexpr int kGatherWarps = 4;
+constexpr int kTmemCols = 64;                    // S, S, O, O buffers of 16
+
+enum : int32_t { kFirst = 1, kLast = 2, kEnd = 4 };
+
+struct StageMeta {
+    int32_t flags, keys;                         // keys from the stage's first to the chunk's end
+    int32_t row, h0, nh, nch;                    // row: of part_o, or of out if nch is 1
+};
+
+struct Smem {
+    uint8_t kv[kStages][2 * kTileBytes];         // K tile, V tile; 1024-byte aligned
+    uint8_t q[2][kCols * D];                     // by unit parity, 128-byte swizzle
+    uint8_t p[2][kStageKeys * kCols];            // by stage parity
+    float ks[kStages][kStageKeys];               // per key (gathered) or box: K scale,
+    float lv[kStages][kStageKeys];               // log2 of V's (-inf: does not count),
+    float iv[kStages][kStageKeys];               // its inverse
+    StageMeta meta[kStages];
+    float q_pow[2][kMaxGroup];
+    float warp_max[2][kSoftmaxWarps][kMaxGroup];
+    float warp_sum[2][kSoftmaxWarps][kMaxGroup];
+    uint64_t full[kStages], empty[kStages];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t max_bar, sum_bar, drain_s, drain_o;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+// Instruction descriptor of tcgen05.mma.kind::f8f6f4: e4m3 A and B, fp32 D, 128 x 16.
+__host__ __device__ constexpr uint32_t idesc_e4m3(bool mn_major) {
+    return (1u << 4) | ((mn_major ? 3u : 0u) << 15) | ((uint32_t)(kCols >> 3) << 17) |
+           ((uint32_t)(128 >> 4) << 24);
+}
+
+// Descriptor of P: MN-major without swizzle.  A core matrix is 8 keys of 16
+// columns (16 bytes), and the operand is one core matrix wide, so the only
+// stride is the one along the keys, 128 bytes.
+__device__ __forceinline__ uint64_t p_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 |
+           (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// N consecutive fp32 columns of this thread's TMEM lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float* v) {
+    uint32_t r[N];
+    if constexpr (N == 4) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr));
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+              "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+              "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(addr));
+    }
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+
+// x16 = 16 x (f16x2, |x| <= 256) as x = hi + lo / 16, both pairs of e4m3: the
+// first four significant bits and what they leave, which 16 x - 16 hi gives
+// exactly.
+__device__ __forceinline__ void split_e4m3(uint32_t x16, uint16_t& hi, uint16_t& lo) {
+    hi = f16x2_to_e4m3x2(mul_f16x2(x16, 0x2c002c00u));                     // 1/16
+    lo = f16x2_to_e4m3x2(fma_f16x2(pkv::e4m3x2_to_f16x2(hi), 0xcc00cc00u, x16));  // -16
+}
+
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::saddr(smem)),
+                 "l"(gmem), "r"(bytes)
+                 : "memory");
+}
+
+// The CTA's units in order: unit u is (chunk u / units_per_sc, kv head, group of
+// q heads), its stages every 128 keys of the chunk.  `info` of the unit after
+// is loaded a unit ahead.
+struct Units {
+    int64_t u, count;
+    int4 info, ahead;
+    int32_t per_sc, n_hg;
+    const int4* records;
+    int64_t step;
+    __device__ __forceinline__ Units(const pkv::DecodeArgs& a) {
+        per_sc = a.Hkv * a.n_hg;
+        n_hg = a.n_hg;
+        records = a.chunk_info;
+        count = (int64_t)a.chunk_prefix[a.B] * per_sc;
+        u = blockIdx.x;
+        step = gridDim.x;
+        if (u < count) info = records[u / per_sc];
+        if (u + step < count) ahead = records[(u + step) / per_sc];
+    }
+    __device__ __forceinline__ bool live() const { return u < count; }
+    __device__ __forceinline__ bool more() const { return u + step < count; }
+    __device__ __forceinline__ void next() {
+        u += step;
+        info = ahead;
+        if (u + step < count) ahead = records[(u + step) / per_sc];
+    }
+    __device__ __forceinline__ int32_t sc() const { return (int32_t)(u / per_sc); }
+    __device__ __forceinline__ int32_t kv_head(int64_t unit) const {
+        return (int32_t)(unit % per_sc) / n_hg;
+    }
+    __device__ __forceinline__ int32_t head_group() const {
+        return (int32_t)(u % per_sc) % n_hg;
+    }
+};
+
+// A ring position that several roles walk alike.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == kStages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// kHeads: q heads a unit may have (2, 4 or 8).  kGather: any block size.
+template <int kHeads, bool kGather, bool kPolls>
+__global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)) * 32, 1)
+    decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, Fp8DecodeArgs fa) {
+    const pkv::DecodeArgs& a = fa.d;
+    const uint32_t polls = kPolls ? a.wait_polls : (uint32_t)PKV_DEFAULT_WAIT_POLLS;
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(&sm.full[s], kGather ? kGatherWarps : 1);
+            tc::mbar_init(&sm.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sm.s_full[i], 1);
+            tc::mbar_init(&sm.p_full[i], kSoftmaxWarps);
+            tc::mbar_init(&sm.o_full[i], 1);
+            tc::mbar_init(&sm.q_full[i], 1);
+            tc::mbar_init(&sm.q_empty[i], 1 + kSoftmaxWarps);
+        }
+        tc::mbar_init(&sm.max_bar, kSoftmaxWarps);
+        tc::mbar_init(&sm.sum_bar, kSoftmaxWarps);
+        tc::mbar_init(&sm.drain_s, 1);
+        tc::mbar_init(&sm.drain_o, 1);
+        sm.abort_flag = 0;
+        tc::mbar_init_fence();
+    }
+    // the Q rows that no head fills, once
+    for (int i = threadIdx.x; i < (int)sizeof(sm.q) / 16; i += blockDim.x)
+        reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
+    if (warp == 4) tc::tmem_alloc(&sm.tmem, kTmemCols);
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    pkv::wait_for_predecessor();                 // the plan kernel's chunk records
+    pkv::allow_dependent_launch();
+
+    auto give_up = [&]() {
+        *(volatile int*)&sm.abort_flag = 1;
+        pkv::report(a.status, PKV_STATUS_WAIT_TIMEOUT);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return tc::mbar_wait(bar, parity, &sm.abort_flag, polls);
+    };
+    // the same for a whole warp: one outcome for all its lanes
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+    };
+
+    if (warp < kSoftmaxWarps) {
+        // ------------------------------------------------------------- softmax
+        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        const int key = threadIdx.x;             // of S; head_dim entry of O
+        const int mine = kGather ? key : key / kBoxKeys;
+        Ring ring;
+        uint32_t it = 0, units = 0;              // stages and units so far
+        float m[kHeads], l[kHeads], o[kHeads], xs[kHeads];
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) m[h] = l[h] = o[h] = xs[h] = 0.f;
+        bool ok = true;
+        while (true) {
+            const uint32_t buf = it & 1, par = (it >> 1) & 1;
+            if (!(ok = wait_warp(&sm.full[ring.slot], ring.phase))) break;
+            const StageMeta meta = sm.meta[ring.slot];
+            if (meta.flags & kEnd) break;
+            const float ks = sm.ks[ring.slot][mine], lv = sm.lv[ring.slot][mine];
+            const float iv = sm.iv[ring.slot][mine];
+            const bool counts = lv != -INFINITY && (kGather || key < meta.keys);
+            if (meta.flags & kFirst) {
+                if (!(ok = wait_warp(&sm.q_full[units & 1], (units >> 1) & 1))) break;
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    xs[h] = a.scale_log2 * sm.q_pow[units & 1][h];
+                    m[h] = -INFINITY;
+                    l[h] = o[h] = 0.f;
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.q_empty[units & 1]);
+            }
+            if (!(ok = wait_warp(&sm.s_full[buf], par))) break;
+            tc::tc_fence_after();
+            float s[2 * kHeads], y[kHeads];
+            tmem_ld<2 * kHeads>(lane_base + buf * kCols, s);
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                const float dot = fmaf(s[kHeads + h], 0.0625f, s[h]);
+                y[h] = counts ? fmaf(dot, ks * xs[h], lv) : -INFINITY;
+            }
+            // ---- the stage's maxima ----
+            float top[kHeads];
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) top[h] = warp_max(y[h]);
+            if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < kHeads; h += 2)
+                    *reinterpret_cast<float2*>(&sm.warp_max[buf][warp][h]) =
+                        make_float2(top[h], top[h + 1]);
+                tc::mbar_arrive(&sm.max_bar);
+            }
+            if (!(ok = wait_warp(&sm.max_bar, it & 1))) break;
+            float alpha[kHeads];
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                float mn = m[h];
+#pragma unroll
+                for (int w = 0; w < kSoftmaxWarps; ++w) mn = fmaxf(mn, sm.warp_max[buf][w][h]);
+                const float use = mn == -INFINITY ? 0.f : mn;
+                alpha[h] = pkv::fast_exp2(m[h] - use);       // 0 from -inf
+                m[h] = mn;
+                const float p = pkv::fast_exp2(y[h] - (use - 8.f));
+                l[h] = fmaf(p, iv, l[h] * alpha[h]);
+                y[h] = p;
+            }
+            // ---- the key's row of P ----
+            uint32_t w[4] = {0, 0, 0, 0};        // bytes h: first parts, kHeads + h: second
+            uint16_t hi[kHeads / 2], lo[kHeads / 2];
+#pragma unroll
+            for (int h = 0; h < kHeads; h += 2)
+                split_e4m3(pkv::pack_f16(y[h] * 16.f, y[h + 1] * 16.f), hi[h / 2], lo[h / 2]);
+#pragma unroll
+            for (int i = 0; i < kHeads / 2; ++i) {
+                w[(2 * i) / 4] |= (uint32_t)hi[i] << ((2 * i) % 4 * 8);
+                w[(kHeads + 2 * i) / 4] |= (uint32_t)lo[i] << ((kHeads + 2 * i) % 4 * 8);
+            }
+            *reinterpret_cast<uint4*>(sm.p[buf] + key * kCols) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (!counts) {
+                uint4* v = reinterpret_cast<uint4*>(sm.kv[ring.slot] + kTileBytes + key * D);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.p_full[buf]);
+            // ---- the stage before's O, and at a unit's end this one's ----
+            float t[2 * kHeads];
+            if (!(meta.flags & kFirst)) {
+                if (!(ok = wait_warp(&sm.o_full[buf ^ 1], ((it - 1) >> 1) & 1))) break;
+                tc::tc_fence_after();
+                tmem_ld<2 * kHeads>(lane_base + (2 + (buf ^ 1)) * kCols, t);
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    o[h] = (o[h] + fmaf(t[kHeads + h], 0.0625f, t[h])) * alpha[h];
+            }
+            if (meta.flags & kLast) {
+                if (!(ok = wait_warp(&sm.o_full[buf], par))) break;
+                tc::tc_fence_after();
+                tmem_ld<2 * kHeads>(lane_base + (2 + buf) * kCols, t);
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    o[h] += fmaf(t[kHeads + h], 0.0625f, t[h]);
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int h = 0; h < kHeads; h += 2)
+                        *reinterpret_cast<float2*>(&sm.warp_sum[units & 1][warp][h]) =
+                            make_float2(l[h], l[h + 1]);
+                    tc::mbar_arrive(&sm.sum_bar);
+                }
+                if (!(ok = wait_warp(&sm.sum_bar, units & 1))) break;
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    if (h >= meta.nh) continue;
+                    float L = 0.f;
+#pragma unroll
+                    for (int x = 0; x < kSoftmaxWarps; ++x) L += sm.warp_sum[units & 1][x][h];
+                    if (meta.nch == 1) {
+                        a.out[((int64_t)meta.row + meta.h0 + h) * D + key] =
+                            __float2bfloat16_rn(L > 0.f ? o[h] / L : 0.f);
+                    } else {
+                        const int64_t at = (int64_t)meta.row + meta.h0 + h;
+                        a.part_o[at * D + key] = o[h];
+                        if (key == 0) a.part_ml[at] = make_float2(m[h], L);
+                    }
+                }
+                ++units;
+            }
+            ++it;
+            ring.next();
+        }
+        if (!ok) give_up();
+    } else if (warp == 4) {
+        // ------------------------------------------------------------ S issuer
+        if (lane == 0) {
+            Ring ring;
+            uint32_t units = 0;
+            bool ok = true;
+            for (uint32_t it = 0;; ++it, ring.next()) {
+                const uint32_t buf = it & 1;
+                if (!(ok = wait(&sm.full[ring.slot], ring.phase))) break;
+                const int32_t flags = sm.meta[ring.slot].flags;
+                if (flags & kEnd) break;
+                // the buffer's last S is read once its P is written
+                if (it >= 2 && !(ok = wait(&sm.p_full[buf], ((it - 2) >> 1) & 1))) break;
+                if ((flags & kFirst) &&
+                    !(ok = wait(&sm.q_full[units & 1], (units >> 1) & 1)))
+                    break;
+                tc::tc_fence_after();
+                const uint64_t kd = tc::umma_desc_sw128(tc::saddr(sm.kv[ring.slot]), 16, 1024);
+                const uint64_t qd = tc::umma_desc_sw128(tc::saddr(sm.q[units & 1]), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)             // 32 codes = 32 bytes a step
+                    mma_e4m3(tmem + buf * kCols, kd + k * 2, qd + k * 2, idesc_e4m3(false), k > 0);
+                tc::umma_commit(&sm.s_full[buf]);
+                if (flags & kLast) {
+                    tc::umma_commit(&sm.q_empty[units & 1]);
+                    ++units;
+                }
+            }
+            if (!ok) give_up();
+            tc::umma_commit(&sm.drain_s);                    // every MMA issued here is done
+            tc::mbar_drain(&sm.drain_s, 0);
+        }
+    } else if (warp == 5) {
+        // ---------------------------------------------------------- P V issuer
+        if (lane == 0) {
+            Ring ring;
+            bool ok = true;
+            for (uint32_t it = 0;; ++it, ring.next()) {
+                const uint32_t buf = it & 1;
+                if (!(ok = wait(&sm.full[ring.slot], ring.phase))) break;
+                if (sm.meta[ring.slot].flags & kEnd) break;
+                if (!(ok = wait(&sm.p_full[buf], (it >> 1) & 1))) break;
+                tc::tc_fence_after();
+                const uint64_t vd =
+                    tc::umma_desc_sw128(tc::saddr(sm.kv[ring.slot]) + kTileBytes, 1024, 1024);
+                const uint64_t pd = p_desc(tc::saddr(sm.p[buf]));
+#pragma unroll
+                for (int k = 0; k < kStageKeys / 32; ++k)    // 32 keys: 4 KB of V, 512 bytes of P
+                    mma_e4m3(tmem + (2 + buf) * kCols, vd + k * (4096 >> 4), pd + k * (512 >> 4),
+                             idesc_e4m3(true), k > 0);
+                tc::umma_commit(&sm.empty[ring.slot]);
+                tc::umma_commit(&sm.o_full[buf]);
+            }
+            if (!ok) give_up();
+            tc::umma_commit(&sm.drain_o);
+            tc::mbar_drain(&sm.drain_o, 0);
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------------------------- Q
+        // lane l: quarter l % 4 (32 entries) of head l / 4
+        const int h = lane >> 2, part = lane & 3;
+        Units un(a);
+        uint32_t units = 0;
+        bool ok = true;
+        for (; un.live(); un.next(), ++units) {
+            const int32_t hg = un.head_group(), kvh = un.kv_head(un.u);
+            const int32_t h0 = kvh * a.G + hg * kMaxGroup;
+            const bool there = h < kHeads && h < min(kMaxGroup, a.G - hg * kMaxGroup);
+            uint4 raw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (there)
+                    raw[i] = __ldg(reinterpret_cast<const uint4*>(
+                                       a.q + ((int64_t)un.info.x * a.Hq + h0 + h) * D + part * 32) +
+                                   i);
+            }
+            uint32_t mag = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t x = pkv::word(raw[i >> 2], i & 3);
+                const uint32_t lo = x & 0x7fffu, hi = (x >> 16) & 0x7fffu;
+                mag = max(mag, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            }
+            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+            // largest entry 1.f * 2^(E - 127) to 1.f * 2^7, where that power and its
+            // inverse are normal fp32 numbers
+            const int e = min(max(7 - ((int)(mag >> 7) - 127), -113), 113);
+            const float up16 = __int_as_float((e + 4 + 127) << 23);
+            uint32_t hi[8], lo[8];               // 32 codes of either part
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                uint16_t a0, b0, a1, b1;
+                const uint32_t x = pkv::word(raw[i >> 2], i & 3);
+                const uint32_t z = pkv::word(raw[i >> 2], (i & 3) + 1);
+                split_e4m3(pkv::pack_f16(__int_as_float((int)(x << 16)) * up16,
+                                         __int_as_float((int)(x & 0xffff0000u)) * up16),
+                           a0, b0);
+                split_e4m3(pkv::pack_f16(__int_as_float((int)(z << 16)) * up16,
+                                         __int_as_float((int)(z & 0xffff0000u)) * up16),
+                           a1, b1);
+                hi[i >> 1] = (uint32_t)a0 | (uint32_t)a1 << 16;
+                lo[i >> 1] = (uint32_t)b0 | (uint32_t)b1 << 16;
+            }
+            if (units >= 2 &&
+                !(ok = wait_warp(&sm.q_empty[units & 1], ((units - 2) >> 1) & 1)))
+                break;
+            if (h < kHeads) {
+                uint8_t* q = sm.q[units & 1];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int chunk = part * 2 + c;
+                    const int r1 = h, r2 = kHeads + h;
+                    *reinterpret_cast<uint4*>(q + r1 * D + ((chunk ^ (r1 & 7)) << 4)) =
+                        make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                    *reinterpret_cast<uint4*>(q + r2 * D + ((chunk ^ (r2 & 7)) << 4)) =
+                        make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                }
+                if (part == 0) sm.q_pow[units & 1][h] = __int_as_float((127 - e) << 23);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.q_full[units & 1]);
+        }
+        // the last arrivals on the two buffers' barriers come before the CTA ends
+        for (uint32_t i = 1; ok && i <= 2 && i <= units; ++i)
+            ok = wait_warp(&sm.q_empty[(units - i) & 1], ((units - i) >> 1) & 1);
+        if (!ok && lane == 0) give_up();
+    } else if constexpr (!kGather) {
+        // -------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            tc::tma_prefetch_desc(&kmap);
+            tc::tma_prefetch_desc(&vmap);
+        }
+        Ring ring;
+        int issued = 0;
+        bool ok = true;
+        Units un(a);
+        // lane l holds the id and scales of the unit's l-th cache block (at most
+        // 1024 keys: 17 blocks), loaded while the unit before is streamed
+        auto load_block = [&](const int4& i) {
+            const int32_t blk0 = i.y / a.bs, nblk = (i.z - 1) / a.bs - blk0 + 1;
+            return lane < nblk ? a.bt[(int64_t)i.x * a.MB + blk0 + lane] : -1;
+        };
+        auto load_scale = [&](const float* scales, int32_t blk, int32_t kvh) {
+            return (unsigned)blk < (unsigned)a.NB ? __ldg(scales + (int64_t)blk * a.Hkv + kvh)
+                                                  : 0.f;
+        };
+        int32_t blk_next = -1;
+        float ks_next = 0.f, vs_next = 0.f;
+        if (un.live()) {
+            blk_next = load_block(un.info);
+            ks_next = load_scale(fa.ks, blk_next, un.kv_head(un.u));
+            vs_next = load_scale(fa.vs, blk_next, un.kv_head(un.u));
+        }
+        for (; un.live() && ok; un.next()) {
+            const int32_t kvh = un.kv_head(un.u), hg = un.head_group(), sc = un.sc();
+            const int32_t my_blk = blk_next;
+            const float my_ks = ks_next, my_vs = vs_next;
+            const bool my_scales = pkv::scale_ok(my_ks) && pkv::scale_ok(my_vs);
+            const float my_lv = __log2f(my_vs), my_iv = __frcp_rn(my_vs);
+            const int32_t b = un.info.x, key0 = un.info.y, key_end = un.info.z, nch = un.info.w;
+            const int32_t blk0 = key0 / a.bs;
+            for (int32_t k = key0; k < key_end; k += kStageKeys) {
+                if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
+                int32_t blk[2], at[2], scales[2];
+                float ks[2], lv[2], iv[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int32_t i = min(k + j * kBoxKeys, key_end - 1) / a.bs;
+                    at[j] = (k + j * kBoxKeys) - i * a.bs;
+                    blk[j] = __shfl_sync(0xffffffffu, my_blk, i - blk0);
+                    scales[j] = __shfl_sync(0xffffffffu, (int)my_scales, i - blk0);
+                    ks[j] = __shfl_sync(0xffffffffu, my_ks, i - blk0);
+                    lv[j] = __shfl_sync(0xffffffffu, my_lv, i - blk0);
+                    iv[j] = __shfl_sync(0xffffffffu, my_iv, i - blk0);
+                }
+                if (lane == 0) {
+                    uint32_t bytes = 0;
+                    bool good[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const bool there = k + j * kBoxKeys < key_end;
+                        const bool inside = (unsigned)blk[j] < (unsigned)a.NB;
+                        good[j] = there && inside && scales[j];
+                        if (good[j])
+                            bytes += 2 * kBoxKeys * D;
+                        else if (there)
+                            pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE
+                                                         : PKV_STATUS_BAD_BLOCK_ID);
+                        sm.ks[ring.slot][j] = ks[j];
+                        sm.lv[ring.slot][j] = good[j] ? lv[j] : -INFINITY;
+                        sm.iv[ring.slot][j] = good[j] ? iv[j] : 0.f;
+                    }
+                    StageMeta m;
+                    m.keys = key_end - k;
+                    m.flags = (k == key0 ? kFirst : 0) | (k + kStageKeys >= key_end ? kLast : 0);
+                    m.h0 = kvh * a.G + hg * kMaxGroup;
+                    m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
+                    m.nch = nch;
+                    m.row = (nch == 1 ? b : sc) * a.Hq;
+                    sm.meta[ring.slot] = m;
+                    if (bytes == 0) {
+                        tc::mbar_arrive(&sm.full[ring.slot]);
+                    } else {
+                        tc::mbar_expect_tx(&sm.full[ring.slot], bytes);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (!good[j]) continue;
+                            const int32_t row = blk[j] * a.bs + at[j];
+                            uint8_t* kt = sm.kv[ring.slot] + j * kBoxKeys * D;
+                            tc::tma_load_3d(kt, &kmap, &sm.full[ring.slot], 0, kvh, row);
+                            tc::tma_load_3d(kt + kTileBytes, &vmap, &sm.full[ring.slot], 0, kvh,
+                                            row);
+                        }
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                ring.next();
+                if (un.more()) {                 // the next unit's blocks, then their scales
+                    const int32_t next_head = un.kv_head(un.u + un.step);
+                    if (k == key0) blk_next = load_block(un.ahead);
+                    if (k == key0 + kStageKeys || (k == key0 && k + kStageKeys >= key_end)) {
+                        ks_next = load_scale(fa.ks, blk_next, next_head);
+                        vs_next = load_scale(fa.vs, blk_next, next_head);
+                    }
+                }
+            }
+        }
+        bool ended = false;
+        if (ok && (ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) {
+            if (lane == 0) {
+                sm.meta[ring.slot].flags = kEnd;
+                tc::mbar_arrive(&sm.full[ring.slot]);
+            }
+            __syncwarp();
+            ended = true;
+        }
+        if (!ok && lane == 0) give_up();
+        // every copy issued has landed, and every slot's last release has arrived
+        // (or, where a role gave up, never will), before the CTA ends.  The slot of
+        // the end mark was released before the mark; its barrier has moved on.
+        for (int i = 1; i <= min(issued, ended ? kStages - 1 : kStages); ++i) {
+            int s = ring.slot - i;
+            uint32_t ph = ring.phase;
+            if (s < 0) {
+                s += kStages;
+                ph ^= 1;
+            }
+            tc::mbar_drain(&sm.full[s], ph);
+            if (ok && !(ok = wait_warp(&sm.empty[s], ph)) && lane == 0) give_up();
+        }
+    } else {
+        // ------------------------------------------------- gathering producers
+        const int row0 = (warp - kFirstProducer) * 32;
+        Ring ring, landed;                       // the stage being filled; the next to hand over
+        int pending = 0;                         // stages between the two
+        bool ok = true;
+        Units un(a);
+        // this lane's key of a stage: its block, loaded a stage ahead
+        auto load_block = [&](const int4& i, int32_t k) {
+            const int32_t kk = k + row0 + lane;
+            return kk < i.z ? a.bt[(int64_t)i.x * a.MB + kk / a.bs] : -2;      // -2: past the end
+        };
+        auto hand_over = [&]() {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.full[landed.slot]);
+            landed.next();
+            --pending;
+        };
+        // a stage's scales, written to its record a stage later, when they are there
+        struct Late {
+            int slot = -1;
+            int32_t blk;
+            float ks, vs;
+        } late;
+        auto write_scales = [&]() {
+            if (late.slot < 0) return;
+            const bool inside = late.blk >= 0;
+            const bool good = inside && pkv::scale_ok(late.ks) && pkv::scale_ok(late.vs);
+            if (!good && late.blk != -2)
+                pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE : PKV_STATUS_BAD_BLOCK_ID);
+            sm.ks[late.slot][row0 + lane] = good ? late.ks : 0.f;
+            sm.lv[late.slot][row0 + lane] = good ? __log2f(late.vs) : -INFINITY;
+            sm.iv[late.slot][row0 + lane] = good ? __frcp_rn(late.vs) : 0.f;
+        };
+        int32_t k = 0, blk = -2, issued = 0;
+        if (un.live()) {
+            k = un.info.y;
+            blk = load_block(un.info, k);
+        }
+        while (un.live()) {
+            if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
+            const int32_t kvh = un.kv_head(un.u), key_end = un.info.z;
+            if (blk != -2 && (unsigned)blk >= (unsigned)a.NB) blk = -1;
+            Late mine;
+            mine.slot = ring.slot;
+            mine.blk = blk;
+            mine.ks = mine.vs = 0.f;
+            int32_t row = -1;                    // cache row (slot) of this lane's key
+            if (blk >= 0) {
+                const int64_t at = (int64_t)blk * a.Hkv + kvh;
+                mine.ks = __ldg(fa.ks + at);
+                mine.vs = __ldg(fa.vs + at);
+                row = blk * a.bs + (k + row0 + lane) % a.bs;
+            }
+            if (row0 == 0 && lane == 0) {
+                StageMeta m;
+                m.keys = key_end - k;
+                m.flags = (k == un.info.y ? kFirst : 0) | (k + kStageKeys >= key_end ? kLast : 0);
+                const int32_t hg = un.head_group();
+                m.h0 = kvh * a.G + hg * kMaxGroup;
+                m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
+                m.nch = un.info.w;
+                m.row = (un.info.w == 1 ? un.info.x : un.sc()) * a.Hq;
+                sm.meta[ring.slot] = m;
+            }
+            uint8_t* kt = sm.kv[ring.slot] + row0 * D;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {        // rows 4j .. 4j + 3, 8 chunks each
+                const int r = 4 * j + (lane >> 3), c = lane & 7;
+                const int32_t src = __shfl_sync(0xffffffffu, row, r);
+                const int dst = r * D + ((c ^ (r & 7)) << 4);
+                const int64_t off = src >= 0 ? ((int64_t)src * a.Hkv + kvh) * D + c * 16 : 0;
+                cp_async16(kt + dst, fa.kc + off, src >= 0 ? 16 : 0);
+                cp_async16(kt + kTileBytes + dst, fa.vc + off, src >= 0 ? 16 : 0);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            ++pending;
+            ++issued;
+            write_scales();                      // of the stage before
+            late = mine;
+            ring.next();
+            k += kStageKeys;
+            if (k >= key_end) {
+                un.next();
+                if (un.live()) k = un.info.y;
+            }
+            blk = un.live() ? load_block(un.info, k) : -2;
+            if (pending > 2) {
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                hand_over();
+            }
+        }
+        write_scales();
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        while (pending > 0) hand_over();
+        if (ok && (ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) {
+            if (row0 == 0 && lane == 0) sm.meta[ring.slot].flags = kEnd;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.full[ring.slot]);
+        }
+        // every slot's last release has arrived before the CTA ends
+        for (int i = 1; ok && i <= min(issued, kStages - 1); ++i) {
+            const int s = ring.slot - i;
+            ok = wait_warp(&sm.empty[s < 0 ? s + kStages : s],
+                           s < 0 ? ring.phase ^ 1 : ring.phase);
+        }
+        if (!ok && lane == 0) give_up();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 4) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Rows of [rows, heads, D] codes, one head of kBoxKeys rows a box.
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int heads) {
+    auto enc = pkv::tma_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)heads * D};
+    cuuint32_t box[3] = {(cuuint32_t)D, 1, (cuuint32_t)kBoxKeys};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kHeads, bool kGather, bool kPolls>
+int launch(const Fp8DecodeArgs& fa, cudaStream_t s) {
+    const pkv::DecodeArgs& a = fa.d;
+    CUtensorMap kmap{}, vmap{};
+    const int64_t rows = (int64_t)a.NB * a.bs;
+    if (!kGather && (!encode_rows(&kmap, fa.kc, rows, a.Hkv) ||
+                     !encode_rows(&vmap, fa.vc, rows, a.Hkv)))
+        return PKV_ERR_CUDA;
+    const int smem = (int)sizeof(Smem) + 1024;
+    static std::atomic<uint64_t> configured{0};
+    void (*kernel)(const CUtensorMap, const CUtensorMap, Fp8DecodeArgs) =
+        decode_fp8_tc_kernel<kHeads, kGather, kPolls>;
+    if (!pkv_dynamic_smem_once((const void*)kernel, smem, configured)) return PKV_ERR_CUDA;
+    int64_t grid = pkv_num_sms();
+    const int64_t upper = (int64_t)a.cap * a.Hkv * a.n_hg;
+    if (grid > upper) grid = upper;
+    if (grid < 1) grid = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((kFirstProducer + (kGather ? kGatherWarps : 1)) * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, fa) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <int kHeads, bool kGather>
+int launch_polls(const Fp8DecodeArgs& fa, cudaStream_t s) {
+    return fa.d.wait_polls != (uint32_t)PKV_DEFAULT_WAIT_POLLS ? launch<kHeads, kGather, true>(fa, s)
+                                                               : launch<kHeads, kGather, false>(fa, s);
+}
+
+template <bool kGather>
+int launch_heads(const Fp8DecodeArgs& fa, cudaStream_t s) {
+    if (fa.d.G <= 2) return launch_polls<2, kGather>(fa, s);
+    if (fa.d.G <= 4) return launch_polls<4, kGather>(fa, s);
+    return launch_polls<8, kGather>(fa, s);
+}
+
+}  // namespace
+
+int pkv_launch_decode_fp8_tc(const Fp8DecodeArgs& fa, cudaStream_t s) {
+    return fa.d.bs % kBoxKeys == 0 && fa.d.chunk_keys % kBoxKeys == 0 &&
+                   pkv::tma_encode_fn() != nullptr
+               ? launch_heads<false>(fa, s)
+               : launch_heads<true>(fa, s);
+}

@@ -596,3 +596,27 @@ def test_decode_gives_up_then_recovers(cuda):
     out = pkv.paged_decode_fp8(*args, status=st)
     assert U.status_word(st) == 0
     _check_decode(out, pool, q, 0.1)
+
+
+@pytest.mark.parametrize("bs", [16, 256])
+@pytest.mark.parametrize("group", [2, 4, 8])
+def test_decode_many_stages_a_cta(cuda, bs, group):
+    """Enough keys that every CTA's ring goes round several times; the call
+    reports nothing (a wait at the kernel's end that ran out would)."""
+    pkv = U.lib()
+    rng = np.random.default_rng(41)
+    nb, hkv, d, B = 8192 // bs * 4, 8, 128, 32
+    kc = torch.randint(0, 127, (nb, bs, hkv, d), dtype=torch.uint8, device=cuda).view(
+        torch.float8_e4m3fn)
+    ks = torch.full((nb, hkv), 2.0 ** -9, device=cuda)
+    bt = torch.from_numpy(np.stack([rng.permutation(nb)[:8192 // bs] for _ in range(B)]).astype(
+        np.int32)).to(cuda)
+    ctx = torch.from_numpy(rng.integers(6000, 8193, B).astype(np.int32)).to(cuda)
+    q = F.bf16(rng, B, hkv * group, d).to(cuda)
+    st = pkv.new_status(cuda)
+    out = pkv.paged_decode_fp8(q, kc, kc, ks, ks, bt, ctx, 0.05, 8192, status=st)
+    assert U.status_word(st) == 0
+    # the same rows attended to through the bf16 decode (exact rows, another kernel)
+    rows = (kc.float() * ks[:, None, :, None]).to(torch.bfloat16)
+    ref = pkv.paged_decode(q, rows, rows, bt, ctx, 0.05, 8192)
+    U.assert_close(U.f64(out), U.f64(ref), "fp8 against bf16 decode")
