@@ -33,9 +33,8 @@
 //   warp 7     producer, block sizes that are multiples of 64: per stage two
 //              64-key TMA boxes of K and two of V, each in one cache block, with
 //              its scales in the stage's record.
-//   warps 7-10 producers, other block sizes: lane l of a warp looks up its key's
-//              block and scales (a stage ahead), the warp gathers the 32 rows with
-//              16-byte cp.async into the layout the boxes would have; rows that do
+//   warps 7-14 producers, other block sizes: a lane looks up a key's block and
+//              scales (a stage ahead), the warp gathers its 16 rows with 16-byte cp.async into the layout the boxes would have; rows that do
 //              not count are filled with zeros.  Three stages are in flight.
 // What the HMMA kernels of the other cases spend their issue slots on -- the
 // conversions, two thirds idle MMAs, the per-warp partial outputs -- is gone: a
@@ -63,7 +62,8 @@ constexpr int kStages = 6;
 constexpr int kCols = 16;                        // MMA N
 constexpr int kSoftmaxWarps = 4;
 constexpr int kFirstProducer = 7;
-constexpr int kGatherWarps = 4;
+constexpr int kGatherWarps = 8;
+constexpr int kGatherRows = kStageKeys / kGatherWarps;   // rows of a stage per warp
 constexpr int kTmemCols = 64;                    // S, S, O, O buffers of 16
 
 enum : int32_t { kFirst = 1, kLast = 2, kEnd = 4 };
@@ -555,17 +555,18 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         int issued = 0;
         bool ok = true;
         Units un(a);
-        // lane l holds the id and scales of the unit's l-th cache block (at most
-        // 1024 keys: 17 blocks), loaded while the unit before is streamed
+        // Lane l has box l of the unit (at most 1024 keys: 16 boxes): its block's id
+        // and scales, loaded while the unit before is streamed.  Lanes 2j and
+        // 2j + 1 fill stage j, so a stage costs no shuffles or divisions.
         auto load_block = [&](const int4& i) {
-            const int32_t blk0 = i.y / a.bs, nblk = (i.z - 1) / a.bs - blk0 + 1;
-            return lane < nblk ? a.bt[(int64_t)i.x * a.MB + blk0 + lane] : -1;
+            const int32_t kk = i.y + lane * kBoxKeys;
+            return kk < i.z ? a.bt[(int64_t)i.x * a.MB + kk / a.bs] : -2;      // -2: past the end
         };
         auto load_scale = [&](const float* scales, int32_t blk, int32_t kvh) {
             return (unsigned)blk < (unsigned)a.NB ? __ldg(scales + (int64_t)blk * a.Hkv + kvh)
                                                   : 0.f;
         };
-        int32_t blk_next = -1;
+        int32_t blk_next = -2;
         float ks_next = 0.f, vs_next = 0.f;
         if (un.live()) {
             blk_next = load_block(un.info);
@@ -573,74 +574,58 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             vs_next = load_scale(fa.vs, blk_next, un.kv_head(un.u));
         }
         for (; un.live() && ok; un.next()) {
-            const int32_t kvh = un.kv_head(un.u), hg = un.head_group(), sc = un.sc();
-            const int32_t my_blk = blk_next;
-            const float my_ks = ks_next, my_vs = vs_next;
-            const bool my_scales = pkv::scale_ok(my_ks) && pkv::scale_ok(my_vs);
-            const float my_lv = __log2f(my_vs), my_iv = __frcp_rn(my_vs);
-            const int32_t b = un.info.x, key0 = un.info.y, key_end = un.info.z, nch = un.info.w;
-            const int32_t blk0 = key0 / a.bs;
-            for (int32_t k = key0; k < key_end; k += kStageKeys) {
+            const int32_t kvh = un.kv_head(un.u);
+            const int32_t key0 = un.info.y, keys = un.info.z - key0;
+            const int32_t blk = blk_next;
+            const bool inside = (unsigned)blk < (unsigned)a.NB;
+            const bool good = inside && pkv::scale_ok(ks_next) && pkv::scale_ok(vs_next);
+            if (!good && blk != -2)
+                pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE : PKV_STATUS_BAD_BLOCK_ID);
+            const float ks = good ? ks_next : 0.f;
+            const float lv = good ? __log2f(vs_next) : -INFINITY;
+            const float iv = good ? __frcp_rn(vs_next) : 0.f;
+            const uint32_t goods = __ballot_sync(0xffffffffu, good);
+            const int32_t row = blk * a.bs + (key0 + lane * kBoxKeys) % a.bs;
+            StageMeta m;
+            const int32_t hg = un.head_group();
+            m.h0 = kvh * a.G + hg * kMaxGroup;
+            m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
+            m.nch = un.info.w;
+            m.row = (un.info.w == 1 ? un.info.x : un.sc()) * a.Hq;
+            const int32_t next_head = un.more() ? un.kv_head(un.u + un.step) : 0;
+            for (int j = 0; j * kStageKeys < keys; ++j) {
                 if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
-                int32_t blk[2], at[2], scales[2];
-                float ks[2], lv[2], iv[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int32_t i = min(k + j * kBoxKeys, key_end - 1) / a.bs;
-                    at[j] = (k + j * kBoxKeys) - i * a.bs;
-                    blk[j] = __shfl_sync(0xffffffffu, my_blk, i - blk0);
-                    scales[j] = __shfl_sync(0xffffffffu, (int)my_scales, i - blk0);
-                    ks[j] = __shfl_sync(0xffffffffu, my_ks, i - blk0);
-                    lv[j] = __shfl_sync(0xffffffffu, my_lv, i - blk0);
-                    iv[j] = __shfl_sync(0xffffffffu, my_iv, i - blk0);
-                }
-                if (lane == 0) {
-                    uint32_t bytes = 0;
-                    bool good[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const bool there = k + j * kBoxKeys < key_end;
-                        const bool inside = (unsigned)blk[j] < (unsigned)a.NB;
-                        good[j] = there && inside && scales[j];
-                        if (good[j])
-                            bytes += 2 * kBoxKeys * D;
-                        else if (there)
-                            pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE
-                                                         : PKV_STATUS_BAD_BLOCK_ID);
-                        sm.ks[ring.slot][j] = ks[j];
-                        sm.lv[ring.slot][j] = good[j] ? lv[j] : -INFINITY;
-                        sm.iv[ring.slot][j] = good[j] ? iv[j] : 0.f;
-                    }
-                    StageMeta m;
-                    m.keys = key_end - k;
-                    m.flags = (k == key0 ? kFirst : 0) | (k + kStageKeys >= key_end ? kLast : 0);
-                    m.h0 = kvh * a.G + hg * kMaxGroup;
-                    m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
-                    m.nch = nch;
-                    m.row = (nch == 1 ? b : sc) * a.Hq;
-                    sm.meta[ring.slot] = m;
-                    if (bytes == 0) {
-                        tc::mbar_arrive(&sm.full[ring.slot]);
-                    } else {
-                        tc::mbar_expect_tx(&sm.full[ring.slot], bytes);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (!good[j]) continue;
-                            const int32_t row = blk[j] * a.bs + at[j];
-                            uint8_t* kt = sm.kv[ring.slot] + j * kBoxKeys * D;
-                            tc::tma_load_3d(kt, &kmap, &sm.full[ring.slot], 0, kvh, row);
-                            tc::tma_load_3d(kt + kTileBytes, &vmap, &sm.full[ring.slot], 0, kvh,
-                                            row);
-                        }
+                const int i = lane - 2 * j;      // 0, 1: this lane's box is in the stage
+                if (i == 0 || i == 1) {
+                    sm.ks[ring.slot][i] = ks;
+                    sm.lv[ring.slot][i] = lv;
+                    sm.iv[ring.slot][i] = iv;
+                    if (i == 0) {
+                        m.keys = keys - j * kStageKeys;
+                        m.flags = (j == 0 ? kFirst : 0) |
+                                  ((j + 1) * kStageKeys >= keys ? kLast : 0);
+                        sm.meta[ring.slot] = m;
                     }
                 }
                 __syncwarp();
+                const uint32_t bytes = __popc(goods >> (2 * j) & 3u) * (2 * kBoxKeys * D);
+                if (i == 0) {
+                    if (bytes == 0)
+                        tc::mbar_arrive(&sm.full[ring.slot]);
+                    else
+                        tc::mbar_expect_tx(&sm.full[ring.slot], bytes);
+                }
+                __syncwarp();
+                if ((i == 0 || i == 1) && good) {
+                    uint8_t* kt = sm.kv[ring.slot] + i * kBoxKeys * D;
+                    tc::tma_load_3d(kt, &kmap, &sm.full[ring.slot], 0, kvh, row);
+                    tc::tma_load_3d(kt + kTileBytes, &vmap, &sm.full[ring.slot], 0, kvh, row);
+                }
                 ++issued;
                 ring.next();
-                if (un.more()) {                 // the next unit's blocks, then their scales
-                    const int32_t next_head = un.kv_head(un.u + un.step);
-                    if (k == key0) blk_next = load_block(un.ahead);
-                    if (k == key0 + kStageKeys || (k == key0 && k + kStageKeys >= key_end)) {
+                if (un.more()) {                 // the next unit's boxes, then their scales
+                    if (j == 0) blk_next = load_block(un.ahead);
+                    if (j == 1 || (j == 0 && keys <= kStageKeys)) {
                         ks_next = load_scale(fa.ks, blk_next, next_head);
                         vs_next = load_scale(fa.vs, blk_next, next_head);
                     }
@@ -672,15 +657,19 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         }
     } else {
         // ------------------------------------------------- gathering producers
-        const int row0 = (warp - kFirstProducer) * 32;
+        // Lane l of a warp looks up row l % 16 of the warp's 16.
+        const int row0 = (warp - kFirstProducer) * kGatherRows;
+        const int my_key = row0 + (lane & (kGatherRows - 1));
         Ring ring, landed;                       // the stage being filled; the next to hand over
         int pending = 0;                         // stages between the two
         bool ok = true;
         Units un(a);
-        // this lane's key of a stage: its block, loaded a stage ahead
+        // this lane's key of a stage, as table entry and offset; a stage on is 128
+        // keys on (no division by the block size outside a unit's start)
+        const int32_t step_blocks = kStageKeys / a.bs, step_off = kStageKeys % a.bs;
+        int32_t at_block = 0, at_off = 0;
         auto load_block = [&](const int4& i, int32_t k) {
-            const int32_t kk = k + row0 + lane;
-            return kk < i.z ? a.bt[(int64_t)i.x * a.MB + kk / a.bs] : -2;      // -2: past the end
+            return k + my_key < i.z ? a.bt[(int64_t)i.x * a.MB + at_block] : -2;   // -2: past the end
         };
         auto hand_over = [&]() {
             tc::fence_proxy_async_smem();
@@ -701,13 +690,19 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             const bool good = inside && pkv::scale_ok(late.ks) && pkv::scale_ok(late.vs);
             if (!good && late.blk != -2)
                 pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE : PKV_STATUS_BAD_BLOCK_ID);
-            sm.ks[late.slot][row0 + lane] = good ? late.ks : 0.f;
-            sm.lv[late.slot][row0 + lane] = good ? __log2f(late.vs) : -INFINITY;
-            sm.iv[late.slot][row0 + lane] = good ? __frcp_rn(late.vs) : 0.f;
+            if (lane >= kGatherRows) return;
+            sm.ks[late.slot][my_key] = good ? late.ks : 0.f;
+            sm.lv[late.slot][my_key] = good ? __log2f(late.vs) : -INFINITY;
+            sm.iv[late.slot][my_key] = good ? __frcp_rn(late.vs) : 0.f;
         };
         int32_t k = 0, blk = -2, issued = 0;
-        if (un.live()) {
+        auto start_unit = [&]() {
             k = un.info.y;
+            at_block = (k + my_key) / a.bs;
+            at_off = (k + my_key) % a.bs;
+        };
+        if (un.live()) {
+            start_unit();
             blk = load_block(un.info, k);
         }
         while (un.live()) {
@@ -718,12 +713,15 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             mine.slot = ring.slot;
             mine.blk = blk;
             mine.ks = mine.vs = 0.f;
-            int32_t row = -1;                    // cache row (slot) of this lane's key
+            // the key's row in 128-byte units: a tensor within the GPU's memory has
+            // fewer than 2^32 - 1 of them
+            uint32_t row = 0xffffffffu;
             if (blk >= 0) {
                 const int64_t at = (int64_t)blk * a.Hkv + kvh;
                 mine.ks = __ldg(fa.ks + at);
                 mine.vs = __ldg(fa.vs + at);
-                row = blk * a.bs + (k + row0 + lane) % a.bs;
+                row = ((uint32_t)blk * (uint32_t)a.bs + (uint32_t)at_off) * (uint32_t)a.Hkv +
+                      (uint32_t)kvh;
             }
             if (row0 == 0 && lane == 0) {
                 StageMeta m;
@@ -738,13 +736,14 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             }
             uint8_t* kt = sm.kv[ring.slot] + row0 * D;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {        // rows 4j .. 4j + 3, 8 chunks each
+            for (int j = 0; j < kGatherRows / 4; ++j) {          // rows 4j .. 4j + 3, 8 chunks each
                 const int r = 4 * j + (lane >> 3), c = lane & 7;
-                const int32_t src = __shfl_sync(0xffffffffu, row, r);
+                const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                const bool there = src != 0xffffffffu;
                 const int dst = r * D + ((c ^ (r & 7)) << 4);
-                const int64_t off = src >= 0 ? ((int64_t)src * a.Hkv + kvh) * D + c * 16 : 0;
-                cp_async16(kt + dst, fa.kc + off, src >= 0 ? 16 : 0);
-                cp_async16(kt + kTileBytes + dst, fa.vc + off, src >= 0 ? 16 : 0);
+                const uint64_t off = there ? (uint64_t)src * D + c * 16 : 0;
+                cp_async16(kt + dst, fa.kc + off, there ? 16 : 0);
+                cp_async16(kt + kTileBytes + dst, fa.vc + off, there ? 16 : 0);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             ++pending;
@@ -753,9 +752,15 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             late = mine;
             ring.next();
             k += kStageKeys;
+            at_block += step_blocks;
+            at_off += step_off;
+            if (at_off >= a.bs) {
+                at_off -= a.bs;
+                ++at_block;
+            }
             if (k >= key_end) {
                 un.next();
-                if (un.live()) k = un.info.y;
+                if (un.live()) start_unit();
             }
             blk = un.live() ? load_block(un.info, k) : -2;
             if (pending > 2) {
