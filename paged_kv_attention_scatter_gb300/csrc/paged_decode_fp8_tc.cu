@@ -35,7 +35,7 @@
 //              its scales in the stage's record.
 //   warps 7-14 producers, other block sizes: a lane looks up a key's block and
 //              scales (a stage ahead), the warp gathers its 16 rows with 16-byte cp.async into the layout the boxes would have; rows that do
-//              not count are filled with zeros.  Three stages are in flight.
+//              not count are filled with zeros.  Four stages are in flight.
 // What the HMMA kernels of the other cases spend their issue slots on -- the
 // conversions, two thirds idle MMAs, the per-warp partial outputs -- is gone: a
 // stage costs a softmax warp about 200 instructions.  Every mbarrier wait is
@@ -63,6 +63,7 @@ constexpr int kCols = 16;                        // MMA N
 constexpr int kSoftmaxWarps = 4;
 constexpr int kFirstProducer = 7;
 constexpr int kGatherWarps = 8;
+constexpr int kPending = 4;                      // gathered stages in flight
 constexpr int kGatherRows = kStageKeys / kGatherWarps;   // rows of a stage per warp
 constexpr int kTmemCols = 64;                    // S, S, O, O buffers of 16
 
@@ -81,9 +82,9 @@ struct Smem {
     float lv[kStages][kStageKeys];               // log2 of V's (-inf: does not count),
     float iv[kStages][kStageKeys];               // its inverse
     StageMeta meta[kStages];
-    float q_pow[2][kMaxGroup];
-    float warp_max[2][kSoftmaxWarps][kMaxGroup];
-    float warp_sum[2][kSoftmaxWarps][kMaxGroup];
+    alignas(16) float q_pow[2][kMaxGroup];
+    alignas(16) float warp_max[2][kSoftmaxWarps][kMaxGroup];
+    alignas(16) float warp_sum[2][kSoftmaxWarps][kMaxGroup];
     uint64_t full[kStages], empty[kStages];
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t q_full[2], q_empty[2];
@@ -179,39 +180,37 @@ __device__ __forceinline__ void cp_async16(void* smem, const void* gmem, uint32_
                  : "memory");
 }
 
-// The CTA's units in order: unit u is (chunk u / units_per_sc, kv head, group of
-// q heads), its stages every 128 keys of the chunk.  `info` of the unit after
-// is loaded a unit ahead.
+// A CTA's units in order: unit u is (chunk u / per_sc, kv head, group of q
+// heads).  The CTA takes u = blockIdx.x, + gridDim.x, ...; a step is an addition
+// with carry, not a division.
 struct Units {
-    int64_t u, count;
-    int4 info, ahead;
-    int32_t per_sc, n_hg;
+    int32_t sc, rem, chunks, per_sc, n_hg, step_sc, step_rem;
     const int4* records;
-    int64_t step;
-    __device__ __forceinline__ Units(const pkv::DecodeArgs& a) {
+    __device__ __forceinline__ explicit Units(const pkv::DecodeArgs& a) {
         per_sc = a.Hkv * a.n_hg;
         n_hg = a.n_hg;
         records = a.chunk_info;
-        count = (int64_t)a.chunk_prefix[a.B] * per_sc;
-        u = blockIdx.x;
-        step = gridDim.x;
-        if (u < count) info = records[u / per_sc];
-        if (u + step < count) ahead = records[(u + step) / per_sc];
+        chunks = a.chunk_prefix[a.B];
+        sc = (int32_t)blockIdx.x / per_sc;
+        rem = (int32_t)blockIdx.x % per_sc;
+        step_sc = (int32_t)gridDim.x / per_sc;
+        step_rem = (int32_t)gridDim.x % per_sc;
     }
-    __device__ __forceinline__ bool live() const { return u < count; }
-    __device__ __forceinline__ bool more() const { return u + step < count; }
+    __device__ __forceinline__ bool live() const { return sc < chunks; }
     __device__ __forceinline__ void next() {
-        u += step;
-        info = ahead;
-        if (u + step < count) ahead = records[(u + step) / per_sc];
+        sc += step_sc;
+        rem += step_rem;
+        if (rem >= per_sc) {
+            rem -= per_sc;
+            ++sc;
+        }
     }
-    __device__ __forceinline__ int32_t sc() const { return (int32_t)(u / per_sc); }
-    __device__ __forceinline__ int32_t kv_head(int64_t unit) const {
-        return (int32_t)(unit % per_sc) / n_hg;
+    // (sequence, first key, end key, chunks of the sequence); no keys past the end
+    __device__ __forceinline__ int4 record() const {
+        return live() ? records[sc] : make_int4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ int32_t head_group() const {
-        return (int32_t)(u % per_sc) % n_hg;
-    }
+    __device__ __forceinline__ int32_t kv_head() const { return n_hg == 1 ? rem : rem / n_hg; }
+    __device__ __forceinline__ int32_t head_group() const { return n_hg == 1 ? 0 : rem % n_hg; }
 };
 
 // A ring position that several roles walk alike.
@@ -480,8 +479,12 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         Units un(a);
         uint32_t units = 0;
         bool ok = true;
-        for (; un.live(); un.next(), ++units) {
-            const int32_t hg = un.head_group(), kvh = un.kv_head(un.u);
+        int32_t sequence = un.record().x;        // of the unit after: loaded a unit ahead
+        for (; un.live(); ++units) {
+            const int32_t hg = un.head_group(), kvh = un.kv_head();
+            const int32_t b = sequence;
+            un.next();
+            sequence = un.record().x;
             const int32_t h0 = kvh * a.G + hg * kMaxGroup;
             const bool there = h < kHeads && h < min(kMaxGroup, a.G - hg * kMaxGroup);
             uint4 raw[4];
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 raw[i] = make_uint4(0, 0, 0, 0);
                 if (there)
                     raw[i] = __ldg(reinterpret_cast<const uint4*>(
-                                       a.q + ((int64_t)un.info.x * a.Hq + h0 + h) * D + part * 32) +
+                                       a.q + ((int64_t)b * a.Hq + h0 + h) * D + part * 32) +
                                    i);
             }
             uint32_t mag = 0;
@@ -554,10 +557,11 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         Ring ring;
         int issued = 0;
         bool ok = true;
-        Units un(a);
-        // Lane l has box l of the unit (at most 1024 keys: 16 boxes): its block's id
-        // and scales, loaded while the unit before is streamed.  Lanes 2j and
-        // 2j + 1 fill stage j, so a stage costs no shuffles or divisions.
+        // Lane l has box l of the unit (at most 1024 keys: 16 boxes).  Lanes 2j and
+        // 2j + 1 fill stage j, so a stage costs no shuffles or divisions.  A unit
+        // needs its record, then its boxes' block ids, then their scales: at a
+        // unit's start the next one's scales, the ids of the one after and the
+        // record of the third are requested, and have that unit's time to arrive.
         auto load_block = [&](const int4& i) {
             const int32_t kk = i.y + lane * kBoxKeys;
             return kk < i.z ? a.bt[(int64_t)i.x * a.MB + kk / a.bs] : -2;      // -2: past the end
@@ -566,33 +570,41 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             return (unsigned)blk < (unsigned)a.NB ? __ldg(scales + (int64_t)blk * a.Hkv + kvh)
                                                   : 0.f;
         };
-        int32_t blk_next = -2;
-        float ks_next = 0.f, vs_next = 0.f;
-        if (un.live()) {
-            blk_next = load_block(un.info);
-            ks_next = load_scale(fa.ks, blk_next, un.kv_head(un.u));
-            vs_next = load_scale(fa.vs, blk_next, un.kv_head(un.u));
-        }
-        for (; un.live() && ok; un.next()) {
-            const int32_t kvh = un.kv_head(un.u);
-            const int32_t key0 = un.info.y, keys = un.info.z - key0;
-            const int32_t blk = blk_next;
+        Units un(a), next_un = un, third = un;
+        int4 info = un.record();
+        next_un.next();
+        int4 next_info = next_un.record();
+        third.next();
+        third.next();
+        int4 third_info = third.record();
+        int32_t blk = load_block(info), next_blk = load_block(next_info);
+        float ks_in = load_scale(fa.ks, blk, un.kv_head());
+        float vs_in = load_scale(fa.vs, blk, un.kv_head());
+        while (un.live() && ok) {
+            const int32_t kvh = un.kv_head();
+            const int32_t key0 = info.y, keys = info.z - key0;
             const bool inside = (unsigned)blk < (unsigned)a.NB;
-            const bool good = inside && pkv::scale_ok(ks_next) && pkv::scale_ok(vs_next);
+            const bool good = inside && pkv::scale_ok(ks_in) && pkv::scale_ok(vs_in);
             if (!good && blk != -2)
                 pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE : PKV_STATUS_BAD_BLOCK_ID);
-            const float ks = good ? ks_next : 0.f;
-            const float lv = good ? __log2f(vs_next) : -INFINITY;
-            const float iv = good ? __frcp_rn(vs_next) : 0.f;
+            const float ks = good ? ks_in : 0.f;
+            const float lv = good ? __log2f(vs_in) : -INFINITY;
+            const float iv = good ? __frcp_rn(vs_in) : 0.f;
             const uint32_t goods = __ballot_sync(0xffffffffu, good);
             const int32_t row = blk * a.bs + (key0 + lane * kBoxKeys) % a.bs;
             StageMeta m;
             const int32_t hg = un.head_group();
             m.h0 = kvh * a.G + hg * kMaxGroup;
             m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
-            m.nch = un.info.w;
-            m.row = (un.info.w == 1 ? un.info.x : un.sc()) * a.Hq;
-            const int32_t next_head = un.more() ? un.kv_head(un.u + un.step) : 0;
+            m.nch = info.w;
+            m.row = (info.w == 1 ? info.x : un.sc) * a.Hq;
+            // requests for the units after
+            ks_in = load_scale(fa.ks, next_blk, next_un.kv_head());
+            vs_in = load_scale(fa.vs, next_blk, next_un.kv_head());
+            const int32_t third_blk = load_block(third_info);
+            Units fourth = third;
+            fourth.next();
+            const int4 fourth_info = fourth.record();
             for (int j = 0; j * kStageKeys < keys; ++j) {
                 if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
                 const int i = lane - 2 * j;      // 0, 1: this lane's box is in the stage
@@ -623,14 +635,15 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 }
                 ++issued;
                 ring.next();
-                if (un.more()) {                 // the next unit's boxes, then their scales
-                    if (j == 0) blk_next = load_block(un.ahead);
-                    if (j == 1 || (j == 0 && keys <= kStageKeys)) {
-                        ks_next = load_scale(fa.ks, blk_next, next_head);
-                        vs_next = load_scale(fa.vs, blk_next, next_head);
-                    }
-                }
             }
+            un = next_un;
+            info = next_info;
+            blk = next_blk;
+            next_un = third;
+            next_info = third_info;
+            next_blk = third_blk;
+            third = fourth;
+            third_info = fourth_info;
         }
         bool ended = false;
         if (ok && (ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) {
@@ -661,15 +674,40 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         const int row0 = (warp - kFirstProducer) * kGatherRows;
         const int my_key = row0 + (lane & (kGatherRows - 1));
         Ring ring, landed;                       // the stage being filled; the next to hand over
-        int pending = 0;                         // stages between the two
+        int pending = 0, issued = 0;             // stages between the two; stages so far
         bool ok = true;
-        Units un(a);
-        // this lane's key of a stage, as table entry and offset; a stage on is 128
-        // keys on (no division by the block size outside a unit's start)
+        // A walk over the stages, with this lane's key of each as table entry and
+        // offset; a stage on is 128 keys on (divisions only at a unit's start).
         const int32_t step_blocks = kStageKeys / a.bs, step_off = kStageKeys % a.bs;
-        int32_t at_block = 0, at_off = 0;
-        auto load_block = [&](const int4& i, int32_t k) {
-            return k + my_key < i.z ? a.bt[(int64_t)i.x * a.MB + at_block] : -2;   // -2: past the end
+        struct Walk {
+            Units un;
+            int4 info, ahead;                    // this unit's record and the next one's
+            int32_t k, block, off;
+        };
+        auto start_unit = [&](Walk& w) {
+            w.k = w.info.y;
+            w.block = (w.k + my_key) / a.bs;
+            w.off = (w.k + my_key) % a.bs;
+        };
+        auto step = [&](Walk& w) {
+            w.k += kStageKeys;
+            w.block += step_blocks;
+            w.off += step_off;
+            if (w.off >= a.bs) {
+                w.off -= a.bs;
+                ++w.block;
+            }
+            if (w.k >= w.info.z) {
+                w.un.next();
+                w.info = w.ahead;
+                Units after = w.un;
+                after.next();
+                w.ahead = after.record();
+                start_unit(w);
+            }
+        };
+        auto load_block = [&](const Walk& w) {
+            return w.k + my_key < w.info.z ? a.bt[(int64_t)w.info.x * a.MB + w.block] : -2;
         };
         auto hand_over = [&]() {
             tc::fence_proxy_async_smem();
@@ -695,19 +733,24 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             sm.lv[late.slot][my_key] = good ? __log2f(late.vs) : -INFINITY;
             sm.iv[late.slot][my_key] = good ? __frcp_rn(late.vs) : 0.f;
         };
-        int32_t k = 0, blk = -2, issued = 0;
-        auto start_unit = [&]() {
-            k = un.info.y;
-            at_block = (k + my_key) / a.bs;
-            at_off = (k + my_key) % a.bs;
-        };
-        if (un.live()) {
-            start_unit();
-            blk = load_block(un.info, k);
-        }
-        while (un.live()) {
+        // `fill` is the stage being filled; its keys' blocks were requested two
+        // stages before, when `fetch` was there
+        Walk fill{Units(a)};
+        fill.info = fill.un.record();
+        Units second = fill.un;
+        second.next();
+        fill.ahead = second.record();
+        start_unit(fill);
+        Walk fetch = fill;
+        int32_t blk = load_block(fetch);
+        step(fetch);
+        int32_t blk1 = load_block(fetch);
+        step(fetch);
+        while (fill.un.live()) {
             if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
-            const int32_t kvh = un.kv_head(un.u), key_end = un.info.z;
+            const int32_t blk2 = load_block(fetch);
+            step(fetch);
+            const int32_t kvh = fill.un.kv_head();
             if (blk != -2 && (unsigned)blk >= (unsigned)a.NB) blk = -1;
             Late mine;
             mine.slot = ring.slot;
@@ -720,18 +763,19 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 const int64_t at = (int64_t)blk * a.Hkv + kvh;
                 mine.ks = __ldg(fa.ks + at);
                 mine.vs = __ldg(fa.vs + at);
-                row = ((uint32_t)blk * (uint32_t)a.bs + (uint32_t)at_off) * (uint32_t)a.Hkv +
+                row = ((uint32_t)blk * (uint32_t)a.bs + (uint32_t)fill.off) * (uint32_t)a.Hkv +
                       (uint32_t)kvh;
             }
             if (row0 == 0 && lane == 0) {
                 StageMeta m;
-                m.keys = key_end - k;
-                m.flags = (k == un.info.y ? kFirst : 0) | (k + kStageKeys >= key_end ? kLast : 0);
-                const int32_t hg = un.head_group();
+                m.keys = fill.info.z - fill.k;
+                m.flags = (fill.k == fill.info.y ? kFirst : 0) |
+                          (fill.k + kStageKeys >= fill.info.z ? kLast : 0);
+                const int32_t hg = fill.un.head_group();
                 m.h0 = kvh * a.G + hg * kMaxGroup;
                 m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
-                m.nch = un.info.w;
-                m.row = (un.info.w == 1 ? un.info.x : un.sc()) * a.Hq;
+                m.nch = fill.info.w;
+                m.row = (fill.info.w == 1 ? fill.info.x : fill.un.sc) * a.Hq;
                 sm.meta[ring.slot] = m;
             }
             uint8_t* kt = sm.kv[ring.slot] + row0 * D;
@@ -751,20 +795,11 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             write_scales();                      // of the stage before
             late = mine;
             ring.next();
-            k += kStageKeys;
-            at_block += step_blocks;
-            at_off += step_off;
-            if (at_off >= a.bs) {
-                at_off -= a.bs;
-                ++at_block;
-            }
-            if (k >= key_end) {
-                un.next();
-                if (un.live()) start_unit();
-            }
-            blk = un.live() ? load_block(un.info, k) : -2;
-            if (pending > 2) {
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
+            step(fill);
+            blk = blk1;
+            blk1 = blk2;
+            if (pending > kPending) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
                 hand_over();
             }
         }
