@@ -14,28 +14,32 @@
 //     and q2 holds the rest exactly, down to 2^-22 of the row's largest entry.
 //   p = 2^(y - M + 8) <= 256 likewise: off by 2^-9 of itself, or 2^-22 of the
 //     row's largest weight.
-// M is the running maximum over all keys of the unit: the four softmax warps
-// exchange their maxima each stage, so no p exceeds 256.  (A reference that
+// M is the running maximum over all keys of the unit that a softmax group has seen: its four
+// warps exchange their maxima each stage, so no p exceeds 256.  (A reference that
 // lags, redone when it is passed, needs headroom that e4m3 lacks: 448 / 256.)
 //
 // Roles, one CTA per SM, a ring of 128-key stages (32 KB):
-//   warps 0-3  softmax: thread i has key i of a stage (TMEM lane i).  It reads
+//   warps 0-7  softmax, two groups of four that take a CTA's stages in turn (a
+//              stage's chain of steps is longer than its bytes take to arrive).
+//              Thread i of a group has key i of a stage (TMEM lane i).  It reads
 //              the key's S columns, exchanges maxima, writes the key's 16 bytes of
 //              P (one 16-byte store: B, MN-major, 16 columns wide) and zeroes the V
 //              row of a key that does not count (0 * NaN is NaN).  Then it takes the
-//              stage before's O, thread i being head_dim entry i now, and adds it
-//              to fp32 registers: O = (O + O') alpha.  TMEM accumulates within a
-//              stage only, so nothing in it is ever rescaled, and a unit's output
-//              needs no merge but the sum of L.
-//   warp 4     S issuer, up to two stages ahead of the softmax (two S buffers).
-//   warp 5     P V issuer; its completion frees the stage's slot.
-//   warp 6     Q: scales, splits and lays out the next unit's rows.
-//   warp 7     producer, block sizes that are multiples of 64: per stage two
+//              O of its group's stage before, thread i being head_dim entry i now,
+//              and adds it to fp32 registers: O = (O + O') alpha.  TMEM accumulates
+//              within a stage only, so nothing in it is ever rescaled.  The group
+//              with a unit's last stage merges the other's share and writes it.
+//   warp 8     S issuer, up to three stages ahead of the softmax (two S buffers a
+//              group).
+//   warp 9     P V issuer; its completion frees the stage's slot.
+//   warp 10    Q: scales, splits and lays out the next units' rows.
+//   warp 11    producer, block sizes that are multiples of 64: per stage two
 //              64-key TMA boxes of K and two of V, each in one cache block, with
 //              its scales in the stage's record.
-//   warps 7-14 producers, other block sizes: a lane looks up a key's block and
-//              scales (a stage ahead), the warp gathers its 16 rows with 16-byte cp.async into the layout the boxes would have; rows that do
-//              not count are filled with zeros.  Four stages are in flight.
+//   warps 11-18 producers, other block sizes: a lane looks up a key's block and
+//              scales, the warp gathers its 16 rows with 16-byte cp.async into the
+//              layout the boxes would have; rows that do not count are filled with
+//              zeros.  Four stages are in flight.
 // What the HMMA kernels of the other cases spend their issue slots on -- the
 // conversions, two thirds idle MMAs, the per-warp partial outputs -- is gone: a
 // stage costs a softmax warp about 200 instructions.  Every mbarrier wait is
@@ -60,35 +64,42 @@ constexpr int kStageKeys = 128;
 constexpr int kTileBytes = kStageKeys * D;       // K or V of a stage
 constexpr int kStages = 6;
 constexpr int kCols = 16;                        // MMA N
-constexpr int kSoftmaxWarps = 4;
-constexpr int kFirstProducer = 7;
+constexpr int kGroups = 2, kGroupWarps = 4;     // softmax groups of 128 threads
+constexpr int kSWarp = kGroups * kGroupWarps, kPvWarp = kSWarp + 1, kQWarp = kSWarp + 2;
+constexpr int kFirstProducer = kSWarp + 3;
+constexpr int kBufs = 2 * kGroups;               // S, P and O buffers: two a group
+constexpr int kQPow = 8;                         // a power of two; see the Q role
 constexpr int kGatherWarps = 8;
 constexpr int kPending = 4;                      // gathered stages in flight
 constexpr int kGatherRows = kStageKeys / kGatherWarps;   // rows of a stage per warp
-constexpr int kTmemCols = 64;                    // S, S, O, O buffers of 16
+constexpr int kTmemCols = 2 * kBufs * 16;        // the S buffers, then the O buffers
 
-enum : int32_t { kFirst = 1, kLast = 2, kEnd = 4 };
-
-struct StageMeta {
-    int32_t flags, keys;                         // keys from the stage's first to the chunk's end
+struct alignas(16) StageMeta {
+    int32_t j, n;                                // stage j of the unit's n; n 0: no more stages
+    int32_t keys;                                // from the stage's first to the chunk's end
+    int32_t unit;                                // of this CTA, counted up
     int32_t row, h0, nh, nch;                    // row: of part_o, or of out if nch is 1
 };
 
 struct Smem {
     uint8_t kv[kStages][2 * kTileBytes];         // K tile, V tile; 1024-byte aligned
     uint8_t q[2][kCols * D];                     // by unit parity, 128-byte swizzle
-    uint8_t p[2][kStageKeys * kCols];            // by stage parity
+    uint8_t p[kBufs][kStageKeys * kCols];
     float ks[kStages][kStageKeys];               // per key (gathered) or box: K scale,
     float lv[kStages][kStageKeys];               // log2 of V's (-inf: does not count),
     float iv[kStages][kStageKeys];               // its inverse
     StageMeta meta[kStages];
-    alignas(16) float q_pow[2][kMaxGroup];
-    alignas(16) float warp_max[2][kSoftmaxWarps][kMaxGroup];
-    alignas(16) float warp_sum[2][kSoftmaxWarps][kMaxGroup];
+    alignas(16) float q_pow[kQPow][kMaxGroup];
+    alignas(16) float warp_max[kBufs][kGroupWarps][kMaxGroup];
+    alignas(16) float warp_sum[kGroups][2][kGroupWarps][kMaxGroup];
+    // one group's share of a unit, for the group that finishes it
+    alignas(16) float ex_o[kMaxGroup][D];
+    alignas(16) float ex_l[kGroupWarps][kMaxGroup];
+    alignas(16) float ex_m[kMaxGroup];
     uint64_t full[kStages], empty[kStages];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[kBufs], p_full[kBufs], o_full[kBufs];
     uint64_t q_full[2], q_empty[2];
-    uint64_t max_bar, sum_bar, drain_s, drain_o;
+    uint64_t max_bar[kGroups], sum_bar[kGroups], ex_full, ex_free, drain_s, drain_o;
     uint32_t tmem;
     int abort_flag;
 };
@@ -217,9 +228,10 @@ struct Units {
 struct Ring {
     int slot = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == kStages) {
-            slot = 0;
+    __device__ __forceinline__ void next(int by = 1) {
+        slot += by;
+        if (slot >= kStages) {
+            slot -= kStages;
             phase ^= 1;
         }
     }
@@ -242,15 +254,19 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             tc::mbar_init(&sm.full[s], kGather ? kGatherWarps : 1);
             tc::mbar_init(&sm.empty[s], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             tc::mbar_init(&sm.s_full[i], 1);
-            tc::mbar_init(&sm.p_full[i], kSoftmaxWarps);
+            tc::mbar_init(&sm.p_full[i], kGroupWarps);
             tc::mbar_init(&sm.o_full[i], 1);
-            tc::mbar_init(&sm.q_full[i], 1);
-            tc::mbar_init(&sm.q_empty[i], 1 + kSoftmaxWarps);
         }
-        tc::mbar_init(&sm.max_bar, kSoftmaxWarps);
-        tc::mbar_init(&sm.sum_bar, kSoftmaxWarps);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sm.q_full[i], 1);
+            tc::mbar_init(&sm.q_empty[i], 1);
+            tc::mbar_init(&sm.max_bar[i], kGroupWarps);
+            tc::mbar_init(&sm.sum_bar[i], kGroupWarps);
+        }
+        tc::mbar_init(&sm.ex_full, kGroupWarps);
+        tc::mbar_init(&sm.ex_free, kGroupWarps);
         tc::mbar_init(&sm.drain_s, 1);
         tc::mbar_init(&sm.drain_o, 1);
         sm.abort_flag = 0;
@@ -259,7 +275,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
     // the Q rows that no head fills, once
     for (int i = threadIdx.x; i < (int)sizeof(sm.q) / 16; i += blockDim.x)
         reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0, 0, 0, 0);
-    if (warp == 4) tc::tmem_alloc(&sm.tmem, kTmemCols);
+    if (warp == kSWarp) tc::tmem_alloc(&sm.tmem, kTmemCols);
     tc::fence_proxy_async_smem();
     tc::tc_fence_before();
     __syncthreads();
@@ -280,40 +296,41 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
     };
 
-    if (warp < kSoftmaxWarps) {
+    if (warp < kSWarp) {
         // ------------------------------------------------------------- softmax
-        const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-        const int key = threadIdx.x;             // of S; head_dim entry of O
+        const int group = warp / kGroupWarps, gw = warp % kGroupWarps;
+        const uint32_t lane_base = tmem + ((uint32_t)(gw * 32) << 16);
+        const int key = threadIdx.x % kStageKeys;            // of S; head_dim entry of O
         const int mine = kGather ? key : key / kBoxKeys;
         Ring ring;
-        uint32_t it = 0, units = 0;              // stages and units so far
+        ring.next(group);
+        uint32_t shared = 0, units = 0;          // units of both groups; units of this one
         float m[kHeads], l[kHeads], o[kHeads], xs[kHeads];
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) m[h] = l[h] = o[h] = xs[h] = 0.f;
         bool ok = true;
-        while (true) {
-            const uint32_t buf = it & 1, par = (it >> 1) & 1;
+        for (uint32_t c = 0;; ++c, ring.next(kGroups)) {     // this group's stages
+            const int buf = 2 * group + (c & 1), before = 2 * group + ((c & 1) ^ 1);
+            const uint32_t par = (c >> 1) & 1;
             if (!(ok = wait_warp(&sm.full[ring.slot], ring.phase))) break;
             const StageMeta meta = sm.meta[ring.slot];
-            if (meta.flags & kEnd) break;
+            if (meta.n == 0) break;
+            const bool first = meta.j < kGroups, last = meta.j + kGroups >= meta.n;
             const float ks = sm.ks[ring.slot][mine], lv = sm.lv[ring.slot][mine];
             const float iv = sm.iv[ring.slot][mine];
             const bool counts = lv != -INFINITY && (kGather || key < meta.keys);
-            if (meta.flags & kFirst) {
-                if (!(ok = wait_warp(&sm.q_full[units & 1], (units >> 1) & 1))) break;
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h) {
-                    xs[h] = a.scale_log2 * sm.q_pow[units & 1][h];
-                    m[h] = -INFINITY;
-                    l[h] = o[h] = 0.f;
-                }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sm.q_empty[units & 1]);
-            }
             if (!(ok = wait_warp(&sm.s_full[buf], par))) break;
             tc::tc_fence_after();
             float s[2 * kHeads], y[kHeads];
             tmem_ld<2 * kHeads>(lane_base + buf * kCols, s);
+            if (first) {                         // (the S issuer has waited for Q)
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    xs[h] = a.scale_log2 * sm.q_pow[meta.unit % kQPow][h];
+                    m[h] = -INFINITY;
+                    l[h] = o[h] = 0.f;
+                }
+            }
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 const float dot = fmaf(s[kHeads + h], 0.0625f, s[h]);
@@ -326,21 +343,29 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             if (lane == 0) {
 #pragma unroll
                 for (int h = 0; h < kHeads; h += 2)
-                    *reinterpret_cast<float2*>(&sm.warp_max[buf][warp][h]) =
+                    *reinterpret_cast<float2*>(&sm.warp_max[buf][gw][h]) =
                         make_float2(top[h], top[h + 1]);
-                tc::mbar_arrive(&sm.max_bar);
+                tc::mbar_arrive(&sm.max_bar[group]);
             }
-            if (!(ok = wait_warp(&sm.max_bar, it & 1))) break;
-            float alpha[kHeads];
+            if (!(ok = wait_warp(&sm.max_bar[group], c & 1))) break;
+            float alpha[kHeads], use[kHeads];
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) use[h] = m[h];
+#pragma unroll
+            for (int w = 0; w < kGroupWarps; ++w)
+#pragma unroll
+                for (int h = 0; h < kHeads; h += 2) {
+                    const float2 x = *reinterpret_cast<const float2*>(&sm.warp_max[buf][w][h]);
+                    use[h] = fmaxf(use[h], x.x);
+                    use[h + 1] = fmaxf(use[h + 1], x.y);
+                }
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
-                float mn = m[h];
-#pragma unroll
-                for (int w = 0; w < kSoftmaxWarps; ++w) mn = fmaxf(mn, sm.warp_max[buf][w][h]);
-                const float use = mn == -INFINITY ? 0.f : mn;
-                alpha[h] = pkv::fast_exp2(m[h] - use);       // 0 from -inf
+                const float mn = use[h];
+                const float u = mn == -INFINITY ? 0.f : mn;
+                alpha[h] = pkv::fast_exp2(m[h] - u);         // 0 from -inf
                 m[h] = mn;
-                const float p = pkv::fast_exp2(y[h] - (use - 8.f));
+                const float p = pkv::fast_exp2(y[h] - (u - 8.f));
                 l[h] = fmaf(p, iv, l[h] * alpha[h]);
                 y[h] = p;
             }
@@ -365,105 +390,131 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sm.p_full[buf]);
-            // ---- the stage before's O, and at a unit's end this one's ----
+            // ---- the O of the group's stage before, and at a unit's end this one's ----
             float t[2 * kHeads];
-            if (!(meta.flags & kFirst)) {
-                if (!(ok = wait_warp(&sm.o_full[buf ^ 1], ((it - 1) >> 1) & 1))) break;
+            if (!first) {
+                if (!(ok = wait_warp(&sm.o_full[before], ((c - 1) >> 1) & 1))) break;
                 tc::tc_fence_after();
-                tmem_ld<2 * kHeads>(lane_base + (2 + (buf ^ 1)) * kCols, t);
+                tmem_ld<2 * kHeads>(lane_base + (kBufs + before) * kCols, t);
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h)
                     o[h] = (o[h] + fmaf(t[kHeads + h], 0.0625f, t[h])) * alpha[h];
             }
-            if (meta.flags & kLast) {
-                if (!(ok = wait_warp(&sm.o_full[buf], par))) break;
-                tc::tc_fence_after();
-                tmem_ld<2 * kHeads>(lane_base + (2 + buf) * kCols, t);
+            if (!last) continue;
+            if (!(ok = wait_warp(&sm.o_full[buf], par))) break;
+            tc::tc_fence_after();
+            tmem_ld<2 * kHeads>(lane_base + (kBufs + buf) * kCols, t);
 #pragma unroll
-                for (int h = 0; h < kHeads; ++h) {
-                    o[h] += fmaf(t[kHeads + h], 0.0625f, t[h]);
+            for (int h = 0; h < kHeads; ++h) {
+                o[h] += fmaf(t[kHeads + h], 0.0625f, t[h]);
 #pragma unroll
-                    for (int off = 16; off > 0; off >>= 1)
-                        l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-                }
-                if (lane == 0) {
-#pragma unroll
-                    for (int h = 0; h < kHeads; h += 2)
-                        *reinterpret_cast<float2*>(&sm.warp_sum[units & 1][warp][h]) =
-                            make_float2(l[h], l[h + 1]);
-                    tc::mbar_arrive(&sm.sum_bar);
-                }
-                if (!(ok = wait_warp(&sm.sum_bar, units & 1))) break;
-#pragma unroll
-                for (int h = 0; h < kHeads; ++h) {
-                    if (h >= meta.nh) continue;
-                    float L = 0.f;
-#pragma unroll
-                    for (int x = 0; x < kSoftmaxWarps; ++x) L += sm.warp_sum[units & 1][x][h];
-                    if (meta.nch == 1) {
-                        a.out[((int64_t)meta.row + meta.h0 + h) * D + key] =
-                            __float2bfloat16_rn(L > 0.f ? o[h] / L : 0.f);
-                    } else {
-                        const int64_t at = (int64_t)meta.row + meta.h0 + h;
-                        a.part_o[at * D + key] = o[h];
-                        if (key == 0) a.part_ml[at] = make_float2(m[h], L);
-                    }
-                }
-                ++units;
+                for (int off = 16; off > 0; off >>= 1)
+                    l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
             }
-            ++it;
-            ring.next();
+            if (meta.j + 1 < meta.n) {
+                // the other group has the unit's last stage: hand this share over
+                // once the share before has been read
+                if (shared > 0 && !(ok = wait_warp(&sm.ex_free, (shared - 1) & 1))) break;
+                ++shared;
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    sm.ex_o[h][key] = o[h];
+                    if (lane == 0) sm.ex_l[gw][h] = l[h];
+                    if (key == 0) sm.ex_m[h] = m[h];
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.ex_full);
+                continue;
+            }
+            float (*sums)[kMaxGroup] = sm.warp_sum[group][units & 1];
+            if (lane == 0) {
+#pragma unroll
+                for (int h = 0; h < kHeads; h += 2)
+                    *reinterpret_cast<float2*>(&sums[gw][h]) = make_float2(l[h], l[h + 1]);
+                tc::mbar_arrive(&sm.sum_bar[group]);
+            }
+            if (!(ok = wait_warp(&sm.sum_bar[group], units & 1))) break;
+            ++units;
+            const bool both = meta.n > 1;
+            if (both && !(ok = wait_warp(&sm.ex_full, shared & 1))) break;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                float L = 0.f, M = m[h], O = o[h];
+#pragma unroll
+                for (int x = 0; x < kGroupWarps; ++x) L += sums[x][h];
+                if (both) {
+                    float L2 = 0.f;
+#pragma unroll
+                    for (int x = 0; x < kGroupWarps; ++x) L2 += sm.ex_l[x][h];
+                    const float m2 = sm.ex_m[h];
+                    M = fmaxf(M, m2);
+                    const float u = M == -INFINITY ? 0.f : M;
+                    const float f1 = pkv::fast_exp2(m[h] - u), f2 = pkv::fast_exp2(m2 - u);
+                    L = fmaf(L, f1, L2 * f2);
+                    O = fmaf(O, f1, sm.ex_o[h][key] * f2);
+                }
+                if (h >= meta.nh) continue;
+                const int64_t at = (int64_t)meta.row + meta.h0 + h;
+                if (meta.nch == 1) {
+                    a.out[at * D + key] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
+                } else {
+                    a.part_o[at * D + key] = O;
+                    if (key == 0) a.part_ml[at] = make_float2(M, L);
+                }
+            }
+            if (both) {
+                ++shared;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.ex_free);
+            }
         }
         if (!ok) give_up();
-    } else if (warp == 4) {
+    } else if (warp == kSWarp) {
         // ------------------------------------------------------------ S issuer
         if (lane == 0) {
             Ring ring;
-            uint32_t units = 0;
             bool ok = true;
             for (uint32_t it = 0;; ++it, ring.next()) {
-                const uint32_t buf = it & 1;
+                const uint32_t c = it / kGroups;             // of the stage's group
+                const uint32_t buf = 2 * (it % kGroups) + (c & 1);
                 if (!(ok = wait(&sm.full[ring.slot], ring.phase))) break;
-                const int32_t flags = sm.meta[ring.slot].flags;
-                if (flags & kEnd) break;
+                const int32_t j = sm.meta[ring.slot].j, n = sm.meta[ring.slot].n;
+                const uint32_t unit = sm.meta[ring.slot].unit;
+                if (n == 0) break;
                 // the buffer's last S is read once its P is written
-                if (it >= 2 && !(ok = wait(&sm.p_full[buf], ((it - 2) >> 1) & 1))) break;
-                if ((flags & kFirst) &&
-                    !(ok = wait(&sm.q_full[units & 1], (units >> 1) & 1)))
-                    break;
+                if (c >= 2 && !(ok = wait(&sm.p_full[buf], ((c - 2) >> 1) & 1))) break;
+                if (j == 0 && !(ok = wait(&sm.q_full[unit & 1], (unit >> 1) & 1))) break;
                 tc::tc_fence_after();
                 const uint64_t kd = tc::umma_desc_sw128(tc::saddr(sm.kv[ring.slot]), 16, 1024);
-                const uint64_t qd = tc::umma_desc_sw128(tc::saddr(sm.q[units & 1]), 16, 1024);
+                const uint64_t qd = tc::umma_desc_sw128(tc::saddr(sm.q[unit & 1]), 16, 1024);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)             // 32 codes = 32 bytes a step
                     mma_e4m3(tmem + buf * kCols, kd + k * 2, qd + k * 2, idesc_e4m3(false), k > 0);
                 tc::umma_commit(&sm.s_full[buf]);
-                if (flags & kLast) {
-                    tc::umma_commit(&sm.q_empty[units & 1]);
-                    ++units;
-                }
+                if (j + 1 == n) tc::umma_commit(&sm.q_empty[unit & 1]);
             }
             if (!ok) give_up();
             tc::umma_commit(&sm.drain_s);                    // every MMA issued here is done
             tc::mbar_drain(&sm.drain_s, 0);
         }
-    } else if (warp == 5) {
+    } else if (warp == kPvWarp) {
         // ---------------------------------------------------------- P V issuer
         if (lane == 0) {
             Ring ring;
             bool ok = true;
             for (uint32_t it = 0;; ++it, ring.next()) {
-                const uint32_t buf = it & 1;
+                const uint32_t c = it / kGroups;
+                const uint32_t buf = 2 * (it % kGroups) + (c & 1);
                 if (!(ok = wait(&sm.full[ring.slot], ring.phase))) break;
-                if (sm.meta[ring.slot].flags & kEnd) break;
-                if (!(ok = wait(&sm.p_full[buf], (it >> 1) & 1))) break;
+                if (sm.meta[ring.slot].n == 0) break;
+                if (!(ok = wait(&sm.p_full[buf], (c >> 1) & 1))) break;
                 tc::tc_fence_after();
                 const uint64_t vd =
                     tc::umma_desc_sw128(tc::saddr(sm.kv[ring.slot]) + kTileBytes, 1024, 1024);
                 const uint64_t pd = p_desc(tc::saddr(sm.p[buf]));
 #pragma unroll
                 for (int k = 0; k < kStageKeys / 32; ++k)    // 32 keys: 4 KB of V, 512 bytes of P
-                    mma_e4m3(tmem + (2 + buf) * kCols, vd + k * (4096 >> 4), pd + k * (512 >> 4),
+                    mma_e4m3(tmem + (kBufs + buf) * kCols, vd + k * (4096 >> 4), pd + k * (512 >> 4),
                              idesc_e4m3(true), k > 0);
                 tc::umma_commit(&sm.empty[ring.slot]);
                 tc::umma_commit(&sm.o_full[buf]);
@@ -472,9 +523,12 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             tc::umma_commit(&sm.drain_o);
             tc::mbar_drain(&sm.drain_o, 0);
         }
-    } else if (warp == 6) {
+    } else if (warp == kQWarp) {
         // ------------------------------------------------------------------- Q
-        // lane l: quarter l % 4 (32 entries) of head l / 4
+        // lane l: quarter l % 4 (32 entries) of head l / 4.  The operand has two
+        // buffers, freed by the unit's last S.  The powers are read by the softmax,
+        // up to three stages behind the S issuer and so up to three units; this
+        // role is up to two units ahead of it: 8 buffers are enough.
         const int h = lane >> 2, part = lane & 3;
         Units un(a);
         uint32_t units = 0;
@@ -538,7 +592,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     *reinterpret_cast<uint4*>(q + r2 * D + ((chunk ^ (r2 & 7)) << 4)) =
                         make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
                 }
-                if (part == 0) sm.q_pow[units & 1][h] = __int_as_float((127 - e) << 23);
+                if (part == 0) sm.q_pow[units % kQPow][h] = __int_as_float((127 - e) << 23);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -555,7 +609,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             tc::tma_prefetch_desc(&vmap);
         }
         Ring ring;
-        int issued = 0;
+        int issued = 0, units = 0;
         bool ok = true;
         // Lane l has box l of the unit (at most 1024 keys: 16 boxes).  Lanes 2j and
         // 2j + 1 fill stage j, so a stage costs no shuffles or divisions.  A unit
@@ -598,6 +652,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
             m.nch = info.w;
             m.row = (info.w == 1 ? info.x : un.sc) * a.Hq;
+            m.n = (keys + kStageKeys - 1) / kStageKeys;
+            m.unit = units++;
             // requests for the units after
             ks_in = load_scale(fa.ks, next_blk, next_un.kv_head());
             vs_in = load_scale(fa.vs, next_blk, next_un.kv_head());
@@ -613,9 +669,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     sm.lv[ring.slot][i] = lv;
                     sm.iv[ring.slot][i] = iv;
                     if (i == 0) {
+                        m.j = j;
                         m.keys = keys - j * kStageKeys;
-                        m.flags = (j == 0 ? kFirst : 0) |
-                                  ((j + 1) * kStageKeys >= keys ? kLast : 0);
                         sm.meta[ring.slot] = m;
                     }
                 }
@@ -645,20 +700,22 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             third = fourth;
             third_info = fourth_info;
         }
-        bool ended = false;
-        if (ok && (ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) {
+        int ended = 0;                           // an end mark for either group
+        for (; ok && ended < kGroups; ++ended) {
+            Ring mark = ring;
+            mark.next(ended);
+            if (!(ok = wait_warp(&sm.empty[mark.slot], mark.phase ^ 1))) break;
             if (lane == 0) {
-                sm.meta[ring.slot].flags = kEnd;
-                tc::mbar_arrive(&sm.full[ring.slot]);
+                sm.meta[mark.slot].n = 0;
+                tc::mbar_arrive(&sm.full[mark.slot]);
             }
             __syncwarp();
-            ended = true;
         }
         if (!ok && lane == 0) give_up();
         // every copy issued has landed, and every slot's last release has arrived
-        // (or, where a role gave up, never will), before the CTA ends.  The slot of
-        // the end mark was released before the mark; its barrier has moved on.
-        for (int i = 1; i <= min(issued, ended ? kStages - 1 : kStages); ++i) {
+        // (or, where a role gave up, never will), before the CTA ends.  A marked
+        // slot was released before its mark, and its barrier has moved on.
+        for (int i = 1; i <= min(issued, kStages - ended); ++i) {
             int s = ring.slot - i;
             uint32_t ph = ring.phase;
             if (s < 0) {
@@ -674,7 +731,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         const int row0 = (warp - kFirstProducer) * kGatherRows;
         const int my_key = row0 + (lane & (kGatherRows - 1));
         Ring ring, landed;                       // the stage being filled; the next to hand over
-        int pending = 0, issued = 0;             // stages between the two; stages so far
+        int pending = 0, issued = 0, units = 0;  // stages between the two; stages and units so far
         bool ok = true;
         // A walk over the stages, with this lane's key of each as table entry and
         // offset; a stage on is 128 keys on (divisions only at a unit's start).
@@ -768,9 +825,10 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             }
             if (row0 == 0 && lane == 0) {
                 StageMeta m;
+                m.j = (fill.k - fill.info.y) / kStageKeys;
+                m.n = (fill.info.z - fill.info.y + kStageKeys - 1) / kStageKeys;
                 m.keys = fill.info.z - fill.k;
-                m.flags = (fill.k == fill.info.y ? kFirst : 0) |
-                          (fill.k + kStageKeys >= fill.info.z ? kLast : 0);
+                m.unit = m.j + 1 == m.n ? units++ : units;
                 const int32_t hg = fill.un.head_group();
                 m.h0 = kvh * a.G + hg * kMaxGroup;
                 m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
@@ -806,13 +864,16 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         write_scales();
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         while (pending > 0) hand_over();
-        if (ok && (ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) {
-            if (row0 == 0 && lane == 0) sm.meta[ring.slot].flags = kEnd;
+        for (int i = 0; ok && i < kGroups; ++i) {            // an end mark for either group
+            Ring mark = ring;
+            mark.next(i);
+            if (!(ok = wait_warp(&sm.empty[mark.slot], mark.phase ^ 1))) break;
+            if (row0 == 0 && lane == 0) sm.meta[mark.slot].n = 0;
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.full[ring.slot]);
+            if (lane == 0) tc::mbar_arrive(&sm.full[mark.slot]);
         }
         // every slot's last release has arrived before the CTA ends
-        for (int i = 1; ok && i <= min(issued, kStages - 1); ++i) {
+        for (int i = 1; ok && i <= min(issued, kStages - kGroups); ++i) {
             const int s = ring.slot - i;
             ok = wait_warp(&sm.empty[s < 0 ? s + kStages : s],
                            s < 0 ? ring.phase ^ 1 : ring.phase);
@@ -821,7 +882,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 4) tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == kSWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 // Rows of [rows, heads, D] codes, one head of kBoxKeys rows a box.
