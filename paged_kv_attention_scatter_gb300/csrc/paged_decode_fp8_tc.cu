@@ -36,10 +36,10 @@
 //   warp 11    producer, block sizes that are multiples of 64: per stage two
 //              64-key TMA boxes of K and two of V, each in one cache block, with
 //              its scales in the stage's record.
-//   warps 11-18 producers, other block sizes: a lane looks up a key's block and
-//              scales, the warp gathers its 16 rows with 16-byte cp.async into the
-//              layout the boxes would have; rows that do not count are filled with
-//              zeros.  Four stages are in flight.
+//   warps 11-18 producers, other block sizes, four teams of two that fill stages
+//              in turn: a lane looks up two keys' blocks and scales, the warp
+//              gathers its 64 rows with 16-byte cp.async into the layout the boxes
+//              would have; rows that do not count are filled with zeros.
 // What the HMMA kernels of the other cases spend their issue slots on -- the
 // conversions, two thirds idle MMAs, the per-warp partial outputs -- is gone: a
 // stage costs a softmax warp about 200 instructions.  Every mbarrier wait is
@@ -69,9 +69,9 @@ constexpr int kSWarp = kGroups * kGroupWarps, kPvWarp = kSWarp + 1, kQWarp = kSW
 constexpr int kFirstProducer = kSWarp + 3;
 constexpr int kBufs = 2 * kGroups;               // S, P and O buffers: two a group
 constexpr int kQPow = 8;                         // a power of two; see the Q role
-constexpr int kGatherWarps = 8;
-constexpr int kPending = 4;                      // gathered stages in flight
-constexpr int kGatherRows = kStageKeys / kGatherWarps;   // rows of a stage per warp
+constexpr int kTeams = 4, kTeamWarps = 2;        // gathering warps: a team fills a stage
+constexpr int kGatherWarps = kTeams * kTeamWarps;
+constexpr int kGatherRows = kStageKeys / kTeamWarps;     // rows of a stage per warp
 constexpr int kTmemCols = 2 * kBufs * 16;        // the S buffers, then the O buffers
 
 struct alignas(16) StageMeta {
@@ -227,12 +227,13 @@ struct Units {
 // A ring position that several roles walk alike.
 struct Ring {
     int slot = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, laps = 0;
     __device__ __forceinline__ void next(int by = 1) {
         slot += by;
         if (slot >= kStages) {
             slot -= kStages;
             phase ^= 1;
+            ++laps;
         }
     }
 };
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            tc::mbar_init(&sm.full[s], kGather ? kGatherWarps : 1);
+            tc::mbar_init(&sm.full[s], kGather ? kTeamWarps : 1);
             tc::mbar_init(&sm.empty[s], 1);
         }
         for (int i = 0; i < kBufs; ++i) {
@@ -727,156 +728,144 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         }
     } else {
         // ------------------------------------------------- gathering producers
-        // Lane l of a warp looks up row l % 16 of the warp's 16.
-        const int row0 = (warp - kFirstProducer) * kGatherRows;
-        const int my_key = row0 + (lane & (kGatherRows - 1));
-        Ring ring, landed;                       // the stage being filled; the next to hand over
-        int pending = 0, issued = 0, units = 0;  // stages between the two; stages and units so far
+        // Team t takes stages t, t + kTeams, ...; a team's warp has 64 rows of each,
+        // lane l looks up rows l and l + 32 of them.  A team hands a stage over when
+        // its copies have landed; meanwhile the other teams' are in flight.
+        const int team = (warp - kFirstProducer) / kTeamWarps;
+        const int row0 = (warp - kFirstProducer) % kTeamWarps * kGatherRows;
+        constexpr int kRows = kGatherRows / 32;  // rows that a lane looks up
+        Ring ring;
+        int units = 0;
         bool ok = true;
-        // A walk over the stages, with this lane's key of each as table entry and
+        // A walk over the stages, with this lane's keys of each as table entry and
         // offset; a stage on is 128 keys on (divisions only at a unit's start).
         const int32_t step_blocks = kStageKeys / a.bs, step_off = kStageKeys % a.bs;
-        struct Walk {
-            Units un;
-            int4 info, ahead;                    // this unit's record and the next one's
-            int32_t k, block, off;
-        };
-        auto start_unit = [&](Walk& w) {
-            w.k = w.info.y;
-            w.block = (w.k + my_key) / a.bs;
-            w.off = (w.k + my_key) % a.bs;
-        };
-        auto step = [&](Walk& w) {
-            w.k += kStageKeys;
-            w.block += step_blocks;
-            w.off += step_off;
-            if (w.off >= a.bs) {
-                w.off -= a.bs;
-                ++w.block;
-            }
-            if (w.k >= w.info.z) {
-                w.un.next();
-                w.info = w.ahead;
-                Units after = w.un;
-                after.next();
-                w.ahead = after.record();
-                start_unit(w);
+        Units un(a);
+        int4 info = un.record(), ahead;          // this unit's record and the next one's
+        int32_t k = 0, block[kRows], off[kRows];
+        auto start_unit = [&]() {
+            Units after = un;
+            after.next();
+            ahead = after.record();
+            k = info.y;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                block[i] = (k + row0 + lane + 32 * i) / a.bs;
+                off[i] = (k + row0 + lane + 32 * i) % a.bs;
             }
         };
-        auto load_block = [&](const Walk& w) {
-            return w.k + my_key < w.info.z ? a.bt[(int64_t)w.info.x * a.MB + w.block] : -2;
+        auto step = [&]() {                      // to the CTA's next stage
+            ring.next();
+            k += kStageKeys;
+            if (k >= info.z) {
+                un.next();
+                info = ahead;
+                ++units;
+                start_unit();
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                block[i] += step_blocks;
+                off[i] += step_off;
+                if (off[i] >= a.bs) {
+                    off[i] -= a.bs;
+                    ++block[i];
+                }
+            }
         };
-        auto hand_over = [&]() {
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.full[landed.slot]);
-            landed.next();
-            --pending;
+        int32_t blk[kRows];                      // block ids; -2: past the end
+        auto load_blocks = [&]() {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                blk[i] = k + row0 + lane + 32 * i < info.z
+                             ? a.bt[(int64_t)info.x * a.MB + block[i]] : -2;
         };
-        // a stage's scales, written to its record a stage later, when they are there
-        struct Late {
-            int slot = -1;
-            int32_t blk;
-            float ks, vs;
-        } late;
-        auto write_scales = [&]() {
-            if (late.slot < 0) return;
-            const bool inside = late.blk >= 0;
-            const bool good = inside && pkv::scale_ok(late.ks) && pkv::scale_ok(late.vs);
-            if (!good && late.blk != -2)
-                pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE : PKV_STATUS_BAD_BLOCK_ID);
-            if (lane >= kGatherRows) return;
-            sm.ks[late.slot][my_key] = good ? late.ks : 0.f;
-            sm.lv[late.slot][my_key] = good ? __log2f(late.vs) : -INFINITY;
-            sm.iv[late.slot][my_key] = good ? __frcp_rn(late.vs) : 0.f;
-        };
-        // `fill` is the stage being filled; its keys' blocks were requested two
-        // stages before, when `fetch` was there
-        Walk fill{Units(a)};
-        fill.info = fill.un.record();
-        Units second = fill.un;
-        second.next();
-        fill.ahead = second.record();
-        start_unit(fill);
-        Walk fetch = fill;
-        int32_t blk = load_block(fetch);
-        step(fetch);
-        int32_t blk1 = load_block(fetch);
-        step(fetch);
-        while (fill.un.live()) {
+        start_unit();
+        for (int i = 0; i < team && un.live(); ++i) step();
+        load_blocks();
+        while (un.live()) {
+            const int32_t kvh = un.kv_head();
+            float ks[kRows], vs[kRows];
+            // rows in 128-byte units: a tensor within the GPU's memory has fewer
+            // than 2^32 - 1 of them
+            uint32_t row[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                ks[i] = vs[i] = 0.f;
+                row[i] = 0xffffffffu;
+                if ((unsigned)blk[i] < (unsigned)a.NB) {
+                    const int64_t at = (int64_t)blk[i] * a.Hkv + kvh;
+                    ks[i] = __ldg(fa.ks + at);
+                    vs[i] = __ldg(fa.vs + at);
+                    row[i] = ((uint32_t)blk[i] * (uint32_t)a.bs + (uint32_t)off[i]) *
+                                 (uint32_t)a.Hkv + (uint32_t)kvh;
+                }
+            }
             if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
-            const int32_t blk2 = load_block(fetch);
-            step(fetch);
-            const int32_t kvh = fill.un.kv_head();
-            if (blk != -2 && (unsigned)blk >= (unsigned)a.NB) blk = -1;
-            Late mine;
-            mine.slot = ring.slot;
-            mine.blk = blk;
-            mine.ks = mine.vs = 0.f;
-            // the key's row in 128-byte units: a tensor within the GPU's memory has
-            // fewer than 2^32 - 1 of them
-            uint32_t row = 0xffffffffu;
-            if (blk >= 0) {
-                const int64_t at = (int64_t)blk * a.Hkv + kvh;
-                mine.ks = __ldg(fa.ks + at);
-                mine.vs = __ldg(fa.vs + at);
-                row = ((uint32_t)blk * (uint32_t)a.bs + (uint32_t)fill.off) * (uint32_t)a.Hkv +
-                      (uint32_t)kvh;
-            }
-            if (row0 == 0 && lane == 0) {
-                StageMeta m;
-                m.j = (fill.k - fill.info.y) / kStageKeys;
-                m.n = (fill.info.z - fill.info.y + kStageKeys - 1) / kStageKeys;
-                m.keys = fill.info.z - fill.k;
-                m.unit = m.j + 1 == m.n ? units++ : units;
-                const int32_t hg = fill.un.head_group();
-                m.h0 = kvh * a.G + hg * kMaxGroup;
-                m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
-                m.nch = fill.info.w;
-                m.row = (fill.info.w == 1 ? fill.info.x : fill.un.sc) * a.Hq;
-                sm.meta[ring.slot] = m;
-            }
-            uint8_t* kt = sm.kv[ring.slot] + row0 * D;
+            const int slot = ring.slot;
+            uint8_t* kt = sm.kv[slot] + row0 * D;
 #pragma unroll
             for (int j = 0; j < kGatherRows / 4; ++j) {          // rows 4j .. 4j + 3, 8 chunks each
                 const int r = 4 * j + (lane >> 3), c = lane & 7;
-                const uint32_t src = __shfl_sync(0xffffffffu, row, r);
+                const uint32_t src = __shfl_sync(0xffffffffu, row[j / 8], r & 31);
                 const bool there = src != 0xffffffffu;
                 const int dst = r * D + ((c ^ (r & 7)) << 4);
-                const uint64_t off = there ? (uint64_t)src * D + c * 16 : 0;
-                cp_async16(kt + dst, fa.kc + off, there ? 16 : 0);
-                cp_async16(kt + kTileBytes + dst, fa.vc + off, there ? 16 : 0);
+                const uint64_t at = there ? (uint64_t)src * D + c * 16 : 0;
+                cp_async16(kt + dst, fa.kc + at, there ? 16 : 0);
+                cp_async16(kt + kTileBytes + dst, fa.vc + at, there ? 16 : 0);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            ++pending;
-            ++issued;
-            write_scales();                      // of the stage before
-            late = mine;
-            ring.next();
-            step(fill);
-            blk = blk1;
-            blk1 = blk2;
-            if (pending > kPending) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-                hand_over();
+            if (row0 == 0 && lane == 0) {
+                StageMeta m;
+                m.j = (k - info.y) / kStageKeys;
+                m.n = (info.z - info.y + kStageKeys - 1) / kStageKeys;
+                m.keys = info.z - k;
+                m.unit = units;
+                const int32_t hg = un.head_group();
+                m.h0 = kvh * a.G + hg * kMaxGroup;
+                m.nh = min(kMaxGroup, a.G - hg * kMaxGroup);
+                m.nch = info.w;
+                m.row = (info.w == 1 ? info.x : un.sc) * a.Hq;
+                sm.meta[slot] = m;
             }
-        }
-        write_scales();
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        while (pending > 0) hand_over();
-        for (int i = 0; ok && i < kGroups; ++i) {            // an end mark for either group
-            Ring mark = ring;
-            mark.next(i);
-            if (!(ok = wait_warp(&sm.empty[mark.slot], mark.phase ^ 1))) break;
-            if (row0 == 0 && lane == 0) sm.meta[mark.slot].n = 0;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const bool inside = (unsigned)blk[i] < (unsigned)a.NB;
+                const bool good = inside && pkv::scale_ok(ks[i]) && pkv::scale_ok(vs[i]);
+                if (!good && blk[i] != -2)
+                    pkv::report(a.status,
+                                inside ? PKV_STATUS_BAD_SCALE : PKV_STATUS_BAD_BLOCK_ID);
+                const int key = row0 + lane + 32 * i;
+                sm.ks[slot][key] = good ? ks[i] : 0.f;
+                sm.lv[slot][key] = good ? __log2f(vs[i]) : -INFINITY;
+                sm.iv[slot][key] = good ? __frcp_rn(vs[i]) : 0.f;
+            }
+            // the team's next stage: its block ids arrive while the copies land
+            for (int i = 0; i < kTeams && un.live(); ++i) step();
+            load_blocks();
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sm.full[mark.slot]);
+            if (lane == 0) tc::mbar_arrive(&sm.full[slot]);
         }
-        // every slot's last release has arrived before the CTA ends
-        for (int i = 1; ok && i <= min(issued, kStages - kGroups); ++i) {
-            const int s = ring.slot - i;
-            ok = wait_warp(&sm.empty[s < 0 ? s + kStages : s],
-                           s < 0 ? ring.phase ^ 1 : ring.phase);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        // past the last stage: the ring stands behind it for every team.  The first
+        // team marks the end for either group, and waits for the slots' last release.
+        if (ok && team == 0) {
+            for (int i = 0; ok && i < kGroups; ++i) {
+                Ring mark = ring;
+                mark.next(i);
+                if (!(ok = wait_warp(&sm.empty[mark.slot], mark.phase ^ 1))) break;
+                if (row0 == 0 && lane == 0) sm.meta[mark.slot].n = 0;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.full[mark.slot]);
+            }
+            for (int i = 1; ok && i <= kStages - kGroups; ++i) {
+                const int s = ring.slot - i;
+                const uint32_t phase = s < 0 ? ring.phase ^ 1 : ring.phase;
+                if (s < 0 && ring.laps == 0) break;          // never filled
+                ok = wait_warp(&sm.empty[s < 0 ? s + kStages : s], phase);
+            }
         }
         if (!ok && lane == 0) give_up();
     }

@@ -138,6 +138,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int units_per_sc = a.Hkv * a.n_hg;
     const int64_t units = (int64_t)a.chunk_prefix[a.B] * units_per_sc;
+    // a bounded wait with one outcome for the whole warp
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &sm.abort_flag, polls)) != 0;
+    };
 
     if (warp == kConsumerWarps) {
         // ------------------------------------------------------------ producer
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t h0 = kvh * a.G + hg * kMaxGroup;
             const int32_t nh = min(kMaxGroup, a.G - hg * kMaxGroup);
             for (int32_t k = key0; k < key_end; k += kStageKeys) {
-                if (!tc::mbar_wait(&sm.empty[slot], phase ^ 1, &sm.abort_flag, polls)) {
+                if (!wait_warp(&sm.empty[slot], phase ^ 1)) {
                     ok = false;
                     break;
                 }
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             u = un;
         }
-        if (ok && tc::mbar_wait(&sm.empty[slot], phase ^ 1, &sm.abort_flag, polls)) {
+        if (ok && wait_warp(&sm.empty[slot], phase ^ 1)) {
             if (lane == 0) {
                 sm.meta[slot].flags = kEnd;
                 tc::mbar_arrive(&sm.full[slot]);
@@ -326,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     uint32_t merged = 0;                         // units merged so far
     while (true) {
-        if (!tc::mbar_wait(&sm.full[slot], phase, &sm.abort_flag, polls)) {
+        if (!wait_warp(&sm.full[slot], phase)) {
             if (lane == 0) {
                 sm.abort_flag = 1;
                 pkv::report(a.status, PKV_STATUS_WAIT_TIMEOUT);
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- end of a unit: merge the warps (bounded mbarrier waits, so a warp
         // that gave up can never leave the others blocked) ----
         if (merged > 0 &&
-            !tc::mbar_wait(&sm.merge_free, (merged - 1) & 1, &sm.abort_flag, polls)) {
+            !wait_warp(&sm.merge_free, (merged - 1) & 1)) {
             sm.abort_flag = 1;
             pkv::report(a.status, PKV_STATUS_WAIT_TIMEOUT);
             break;
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_float2(o[mt][e], o[mt][2 + e]);
         }
         tc::mbar_arrive(&sm.merge_full);
-        if (!tc::mbar_wait(&sm.merge_full, merged & 1, &sm.abort_flag, polls)) {
+        if (!wait_warp(&sm.merge_full, merged & 1)) {
             sm.abort_flag = 1;
             pkv::report(a.status, PKV_STATUS_WAIT_TIMEOUT);
             break;

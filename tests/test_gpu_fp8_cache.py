@@ -571,18 +571,19 @@ def test_random_cases(cuda):
         _run_store(pkv, cuda, F.bf16(rng, n, hkv, d), F.bf16(rng, n, hkv, d), pool, slots)
 
 
-def test_decode_gives_up_then_recovers(cuda):
-    """The TMA split kernel's bounded waits run out: it reports, lets its copies
-    land and returns; the next call is the oracle's."""
+@pytest.mark.parametrize("bs,d", [(64, 128), (16, 128), (64, 64)])
+def test_decode_gives_up_then_recovers(cuda, bs, d):
+    """The split kernels' bounded waits run out: they report, let their copies
+    and MMAs finish and return; the next call is the oracle's."""
     pkv = U.lib()
     rng = np.random.default_rng(31)
     lens = [700, 64, 1500, 1]
-    pool = F.Pool(lens, 64, 2, 128, seed=6)
-    q = F.bf16(rng, 4, 8, 128)
+    pool = F.Pool(lens, bs, 2, d, seed=6)
+    q = F.bf16(rng, 4, 8, d)
     args = (q.to(cuda), *pool.on(cuda), torch.tensor(lens, dtype=torch.int32, device=cuda), 0.1,
             1500)
     try:
-        for polls in (0, 2):
+        for polls in (0, 1, 2, 3, 5):
             pkv.set_wait_poll_limit(polls)
             st = pkv.new_status(cuda)
             pkv.paged_decode_fp8(*args, status=st)
