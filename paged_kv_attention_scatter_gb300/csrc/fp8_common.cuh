@@ -132,7 +132,7 @@ bool pkv_decode_fp8_tma_supported(const pkv::Fp8DecodeArgs& fa);
 int pkv_launch_decode_fp8_tma(const pkv::Fp8DecodeArgs& fa, int head_dim, cudaStream_t s);
 
 // The tcgen05 split kernel (paged_decode_fp8_tc.cu) for head_dim 128, likewise.
-int pkv_launch_decode_fp8_tc(const pkv::Fp8DecodeArgs& fa, cudaStream_t s);
+int pkv_launch_decode_fp8(const pkv::Fp8DecodeArgs& fa, int head_dim, cudaStream_t s);
 
 // kv_store_fp8.cu: argument checks (enqueue nothing) and the launch.
 struct Fp8StoreCall {

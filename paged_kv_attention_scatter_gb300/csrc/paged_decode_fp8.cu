@@ -23,6 +23,7 @@
 // This file has the entry points and a split kernel for any block size; the
 // one for block sizes that are multiples of 64 is in paged_decode_fp8_tma.cu.
 #include "fp8_common.cuh"
+#include <stdlib.h>
 
 namespace {
 
@@ -270,8 +271,8 @@ int launch_split(const Fp8DecodeArgs& fa, cudaStream_t s) {
 int launch_decode(Fp8DecodeArgs& fa, int head_dim, bool plan, cudaStream_t s) {
     int rc = plan ? pkv_launch_decode_plan(fa.d, s) : PKV_OK;
     if (rc != PKV_OK) return rc;
-    if (head_dim == 128)
-        rc = pkv_launch_decode_fp8_tc(fa, s);
+    if (getenv("PKV_OLD") == nullptr)
+        rc = pkv_launch_decode_fp8(fa, head_dim, s);
     else if (pkv_decode_fp8_tma_supported(fa))
         rc = pkv_launch_decode_fp8_tma(fa, head_dim, s);
     else

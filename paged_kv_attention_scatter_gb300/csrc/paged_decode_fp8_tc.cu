@@ -34,11 +34,11 @@
 //   warp 9     P V issuer; its completion frees the stage's slot.
 //   warp 10    Q: scales, splits and lays out the next units' rows.
 //   warp 11    producer, block sizes that are multiples of 64: per stage two
-//              64-key TMA boxes of K and two of V, each in one cache block, with
+//              (head_dim 64: four) 64-key TMA boxes of K and as many of V, each in one cache block, with
 //              its scales in the stage's record.
 //   warps 11-18 producers, other block sizes, four teams of two that fill stages
-//              in turn: a lane looks up two keys' blocks and scales, the warp
-//              gathers its 64 rows with 16-byte cp.async into the layout the boxes
+//              in turn: a lane looks up its keys' blocks and scales, the warp
+//              gathers half a stage's rows with 16-byte cp.async into the layout the boxes
 //              would have; rows that do not count are filled with zeros.
 // What the HMMA kernels of the other cases spend their issue slots on -- the
 // conversions, two thirds idle MMAs, the per-warp partial outputs -- is gone: a
@@ -58,11 +58,7 @@ namespace {
 
 namespace tc = pkv::tc;
 
-constexpr int D = 128;
 constexpr int kBoxKeys = 64;
-constexpr int kStageKeys = 128;
-constexpr int kTileBytes = kStageKeys * D;       // K or V of a stage
-constexpr int kStages = 6;
 constexpr int kCols = 16;                        // MMA N
 constexpr int kGroups = 2, kGroupWarps = 4;     // softmax groups of 128 threads
 constexpr int kSWarp = kGroups * kGroupWarps, kPvWarp = kSWarp + 1, kQWarp = kSWarp + 2;
@@ -71,8 +67,6 @@ constexpr int kBufs = 2 * kGroups;               // S, P and O buffers: two a gr
 constexpr int kQPow = 8;                         // a power of two; see the Q role
 constexpr int kTeams = 4, kTeamWarps = 2;        // gathering warps: a team fills a stage
 constexpr int kGatherWarps = kTeams * kTeamWarps;
-constexpr int kGatherRows = kStageKeys / kTeamWarps;     // rows of a stage per warp
-constexpr int kTmemCols = 2 * kBufs * 16;        // the S buffers, then the O buffers
 
 struct alignas(16) StageMeta {
     int32_t j, n;                                // stage j of the unit's n; n 0: no more stages
@@ -81,10 +75,16 @@ struct alignas(16) StageMeta {
     int32_t row, h0, nh, nch;                    // row: of part_o, or of out if nch is 1
 };
 
+template <int D>
 struct Smem {
+    // a stage is 32 KB, K and V: 128 keys, or 256 of head_dim 64 (two a thread, so
+    // that a stage's fixed costs are spread over as many bytes)
+    static constexpr int kTileBytes = 128 * 128;
+    static constexpr int kStageKeys = kTileBytes / D;
+    static constexpr int kStages = D == 128 ? 6 : 5;
     uint8_t kv[kStages][2 * kTileBytes];         // K tile, V tile; 1024-byte aligned
-    uint8_t q[2][kCols * D];                     // by unit parity, 128-byte swizzle
-    uint8_t p[kBufs][kStageKeys * kCols];
+    alignas(1024) uint8_t q[2][kCols * D];       // by unit parity, swizzled
+    alignas(16) uint8_t p[kBufs][kStageKeys * kCols];
     float ks[kStages][kStageKeys];               // per key (gathered) or box: K scale,
     float lv[kStages][kStageKeys];               // log2 of V's (-inf: does not count),
     float iv[kStages][kStageKeys];               // its inverse
@@ -104,10 +104,29 @@ struct Smem {
     int abort_flag;
 };
 
-// Instruction descriptor of tcgen05.mma.kind::f8f6f4: e4m3 A and B, fp32 D, 128 x 16.
-__host__ __device__ constexpr uint32_t idesc_e4m3(bool mn_major) {
+static_assert(sizeof(Smem<128>) + 1024 <= 232448 && sizeof(Smem<64>) + 1024 <= 232448,
+              "more shared memory than a CTA can have");
+
+// Instruction descriptor of tcgen05.mma.kind::f8f6f4: e4m3 A and B (both K-major
+// or both MN-major), fp32 D, rows x 16.
+__host__ __device__ constexpr uint32_t idesc_e4m3(bool mn_major, int rows) {
     return (1u << 4) | ((mn_major ? 3u : 0u) << 15) | ((uint32_t)(kCols >> 3) << 17) |
-           ((uint32_t)(128 >> 4) << 24);
+           ((uint32_t)(rows >> 4) << 24);
+}
+
+// Descriptor of rows of D bytes in D-byte swizzle atoms of 8 rows: K and Q
+// (K-major) and V (MN-major, one atom wide): the stride from 8 rows to the next 8.
+template <int D>
+__device__ __forceinline__ uint64_t rows_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 |
+           (uint64_t)((8 * D) >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)(D == 128 ? 2 : 4) << 61;
+}
+
+// Byte offset of 16-byte chunk c of row r in that layout (64-byte swizzle: two
+// rows a 128-byte line, chunk ^ line).
+template <int D>
+__device__ __forceinline__ int swz(int r, int c) {
+    return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
 // Descriptor of P: MN-major without swizzle.  A core matrix is 8 keys of 16
@@ -128,31 +147,35 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b
         : "memory");
 }
 
-// N consecutive fp32 columns of this thread's TMEM lane.
+// N consecutive fp32 columns of this thread's TMEM lane; there after tmem_wait_ld.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float* v) {
-    uint32_t r[N];
     if constexpr (N == 4) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                      : "r"(addr));
     } else if constexpr (N == 8) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                       "=r"(r[6]), "=r"(r[7])
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                       "=f"(v[6]), "=f"(v[7])
                      : "r"(addr));
     } else {
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
             "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-              "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-              "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+              "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+              "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
             : "r"(addr));
     }
+}
+// Waits for this thread's tcgen05.ld; the values pass through it, so that no use
+// of them moves ahead of the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait(float* v) {
     tc::tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -225,7 +248,8 @@ struct Units {
 };
 
 // A ring position that several roles walk alike.
-struct Ring {
+template <int kStages>
+struct RingOf {
     int slot = 0;
     uint32_t phase = 0, laps = 0;
     __device__ __forceinline__ void next(int by = 1) {
@@ -239,14 +263,22 @@ struct Ring {
 };
 
 // kHeads: q heads a unit may have (2, 4 or 8).  kGather: any block size.
-template <int kHeads, bool kGather, bool kPolls>
+template <int D, int kHeads, bool kGather, bool kPolls>
 __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)) * 32, 1)
     decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, Fp8DecodeArgs fa) {
     const pkv::DecodeArgs& a = fa.d;
     const uint32_t polls = kPolls ? a.wait_polls : (uint32_t)PKV_DEFAULT_WAIT_POLLS;
+    using Sm = Smem<D>;
+    constexpr int kStages = Sm::kStages, kTileBytes = Sm::kTileBytes, kStageKeys = Sm::kStageKeys;
+    constexpr int kSub = kStageKeys / 128;       // keys of a stage per softmax thread
+    constexpr int kBoxes = kStageKeys / kBoxKeys;
+    constexpr int kTmemO = kBufs * kSub * kCols; // columns: the S buffers, then the O buffers
+    constexpr int kTmemCols = D == 128 ? 128 : 256;
+    constexpr int kGatherRows = kStageKeys / kTeamWarps;         // rows of a stage per warp
+    using Ring = RingOf<kStages>;
     extern __shared__ uint8_t smem_raw[];
-    Smem& sm = *reinterpret_cast<Smem*>(
+    Sm& sm = *reinterpret_cast<Sm*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -301,8 +333,11 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         // ------------------------------------------------------------- softmax
         const int group = warp / kGroupWarps, gw = warp % kGroupWarps;
         const uint32_t lane_base = tmem + ((uint32_t)(gw * 32) << 16);
-        const int key = threadIdx.x % kStageKeys;            // of S; head_dim entry of O
-        const int mine = kGather ? key : key / kBoxKeys;
+        // thread i of the group: keys i (and i + 128) of a stage, TMEM lane i; and the
+        // head_dim entry of O in that lane: 128 rows are the lanes, 64 rows the
+        // first 16 of each warp's
+        const int key = threadIdx.x % 128;
+        const int dim = D == 128 ? key : lane < 16 ? gw * 16 + lane : -1;
         Ring ring;
         ring.next(group);
         uint32_t shared = 0, units = 0;          // units of both groups; units of this one
@@ -317,13 +352,23 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             const StageMeta meta = sm.meta[ring.slot];
             if (meta.n == 0) break;
             const bool first = meta.j < kGroups, last = meta.j + kGroups >= meta.n;
-            const float ks = sm.ks[ring.slot][mine], lv = sm.lv[ring.slot][mine];
-            const float iv = sm.iv[ring.slot][mine];
-            const bool counts = lv != -INFINITY && (kGather || key < meta.keys);
+            float ks[kSub], lv[kSub], iv[kSub];
+            bool counts[kSub];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                const int mine = kGather ? key + 128 * u : (key + 128 * u) / kBoxKeys;
+                ks[u] = sm.ks[ring.slot][mine];
+                lv[u] = sm.lv[ring.slot][mine];
+                iv[u] = sm.iv[ring.slot][mine];
+                counts[u] = lv[u] != -INFINITY && (kGather || key + 128 * u < meta.keys);
+            }
             if (!(ok = wait_warp(&sm.s_full[buf], par))) break;
             tc::tc_fence_after();
-            float s[2 * kHeads], y[kHeads];
-            tmem_ld<2 * kHeads>(lane_base + buf * kCols, s);
+            float s[kSub][2 * kHeads], y[kSub][kHeads];
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+                tmem_ld<2 * kHeads>(lane_base + (buf * kSub + u) * kCols, s[u]);
+            tmem_wait<kSub * 2 * kHeads>(&s[0][0]);
             if (first) {                         // (the S issuer has waited for Q)
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) {
@@ -333,14 +378,20 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 }
             }
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                const float dot = fmaf(s[kHeads + h], 0.0625f, s[h]);
-                y[h] = counts ? fmaf(dot, ks * xs[h], lv) : -INFINITY;
-            }
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h) {
+                    const float dot = fmaf(s[u][kHeads + h], 0.0625f, s[u][h]);
+                    y[u][h] = counts[u] ? fmaf(dot, ks[u] * xs[h], lv[u]) : -INFINITY;
+                }
             // ---- the stage's maxima ----
             float top[kHeads];
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) top[h] = warp_max(y[h]);
+            for (int h = 0; h < kHeads; ++h) {
+                top[h] = y[0][h];
+                if constexpr (kSub == 2) top[h] = fmaxf(top[h], y[1][h]);
+                top[h] = warp_max(top[h]);
+            }
             if (lane == 0) {
 #pragma unroll
                 for (int h = 0; h < kHeads; h += 2)
@@ -366,26 +417,33 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 const float u = mn == -INFINITY ? 0.f : mn;
                 alpha[h] = pkv::fast_exp2(m[h] - u);         // 0 from -inf
                 m[h] = mn;
-                const float p = pkv::fast_exp2(y[h] - (u - 8.f));
-                l[h] = fmaf(p, iv, l[h] * alpha[h]);
-                y[h] = p;
+                l[h] *= alpha[h];
+#pragma unroll
+                for (int x = 0; x < kSub; ++x) {
+                    const float p = pkv::fast_exp2(y[x][h] - (u - 8.f));
+                    l[h] = fmaf(p, iv[x], l[h]);
+                    y[x][h] = p;
+                }
             }
-            // ---- the key's row of P ----
-            uint32_t w[4] = {0, 0, 0, 0};        // bytes h: first parts, kHeads + h: second
-            uint16_t hi[kHeads / 2], lo[kHeads / 2];
+            // ---- the keys' rows of P: bytes h the first parts, kHeads + h the second ----
 #pragma unroll
-            for (int h = 0; h < kHeads; h += 2)
-                split_e4m3(pkv::pack_f16(y[h] * 16.f, y[h + 1] * 16.f), hi[h / 2], lo[h / 2]);
+            for (int u = 0; u < kSub; ++u) {
+                uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < kHeads / 2; ++i) {
-                w[(2 * i) / 4] |= (uint32_t)hi[i] << ((2 * i) % 4 * 8);
-                w[(kHeads + 2 * i) / 4] |= (uint32_t)lo[i] << ((kHeads + 2 * i) % 4 * 8);
-            }
-            *reinterpret_cast<uint4*>(sm.p[buf] + key * kCols) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (!counts) {
-                uint4* v = reinterpret_cast<uint4*>(sm.kv[ring.slot] + kTileBytes + key * D);
+                for (int h = 0; h < kHeads; h += 2) {
+                    uint16_t hi, lo;
+                    split_e4m3(pkv::pack_f16(y[u][h] * 16.f, y[u][h + 1] * 16.f), hi, lo);
+                    w[h / 4] |= (uint32_t)hi << (h % 4 * 8);
+                    w[(kHeads + h) / 4] |= (uint32_t)lo << ((kHeads + h) % 4 * 8);
+                }
+                *reinterpret_cast<uint4*>(sm.p[buf] + (key + 128 * u) * kCols) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+                if (!counts[u]) {
+                    uint4* v = reinterpret_cast<uint4*>(sm.kv[ring.slot] + kTileBytes +
+                                                        (key + 128 * u) * D);
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < D / 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
+                }
             }
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
@@ -396,7 +454,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             if (!first) {
                 if (!(ok = wait_warp(&sm.o_full[before], ((c - 1) >> 1) & 1))) break;
                 tc::tc_fence_after();
-                tmem_ld<2 * kHeads>(lane_base + (kBufs + before) * kCols, t);
+                tmem_ld<2 * kHeads>(lane_base + kTmemO + before * kCols, t);
+                tmem_wait<2 * kHeads>(t);
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h)
                     o[h] = (o[h] + fmaf(t[kHeads + h], 0.0625f, t[h])) * alpha[h];
@@ -404,7 +463,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             if (!last) continue;
             if (!(ok = wait_warp(&sm.o_full[buf], par))) break;
             tc::tc_fence_after();
-            tmem_ld<2 * kHeads>(lane_base + (kBufs + buf) * kCols, t);
+            tmem_ld<2 * kHeads>(lane_base + kTmemO + buf * kCols, t);
+            tmem_wait<2 * kHeads>(t);
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 o[h] += fmaf(t[kHeads + h], 0.0625f, t[h]);
@@ -419,7 +479,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 ++shared;
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) {
-                    sm.ex_o[h][key] = o[h];
+                    if (dim >= 0) sm.ex_o[h][dim] = o[h];
                     if (lane == 0) sm.ex_l[gw][h] = l[h];
                     if (key == 0) sm.ex_m[h] = m[h];
                 }
@@ -452,15 +512,15 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     const float u = M == -INFINITY ? 0.f : M;
                     const float f1 = pkv::fast_exp2(m[h] - u), f2 = pkv::fast_exp2(m2 - u);
                     L = fmaf(L, f1, L2 * f2);
-                    O = fmaf(O, f1, sm.ex_o[h][key] * f2);
+                    if (dim >= 0) O = fmaf(O, f1, sm.ex_o[h][dim] * f2);
                 }
-                if (h >= meta.nh) continue;
+                if (h >= meta.nh || dim < 0) continue;
                 const int64_t at = (int64_t)meta.row + meta.h0 + h;
                 if (meta.nch == 1) {
-                    a.out[at * D + key] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
+                    a.out[at * D + dim] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
                 } else {
-                    a.part_o[at * D + key] = O;
-                    if (key == 0) a.part_ml[at] = make_float2(M, L);
+                    a.part_o[at * D + dim] = O;
+                    if (dim == 0) a.part_ml[at] = make_float2(M, L);
                 }
             }
             if (both) {
@@ -486,11 +546,15 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 if (c >= 2 && !(ok = wait(&sm.p_full[buf], ((c - 2) >> 1) & 1))) break;
                 if (j == 0 && !(ok = wait(&sm.q_full[unit & 1], (unit >> 1) & 1))) break;
                 tc::tc_fence_after();
-                const uint64_t kd = tc::umma_desc_sw128(tc::saddr(sm.kv[ring.slot]), 16, 1024);
-                const uint64_t qd = tc::umma_desc_sw128(tc::saddr(sm.q[unit & 1]), 16, 1024);
+                const uint64_t qd = rows_desc<D>(tc::saddr(sm.q[unit & 1]));
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k)             // 32 codes = 32 bytes a step
-                    mma_e4m3(tmem + buf * kCols, kd + k * 2, qd + k * 2, idesc_e4m3(false), k > 0);
+                for (int u = 0; u < kSub; ++u) {
+                    const uint64_t kd = rows_desc<D>(tc::saddr(sm.kv[ring.slot]) + u * 128 * D);
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k)         // 32 codes = 32 bytes a step
+                        mma_e4m3(tmem + (buf * kSub + u) * kCols, kd + k * 2, qd + k * 2,
+                                 idesc_e4m3(false, 128), k > 0);
+                }
                 tc::umma_commit(&sm.s_full[buf]);
                 if (j + 1 == n) tc::umma_commit(&sm.q_empty[unit & 1]);
             }
@@ -510,13 +574,13 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 if (sm.meta[ring.slot].n == 0) break;
                 if (!(ok = wait(&sm.p_full[buf], (c >> 1) & 1))) break;
                 tc::tc_fence_after();
-                const uint64_t vd =
-                    tc::umma_desc_sw128(tc::saddr(sm.kv[ring.slot]) + kTileBytes, 1024, 1024);
+                const uint64_t vd = rows_desc<D>(tc::saddr(sm.kv[ring.slot]) + kTileBytes);
                 const uint64_t pd = p_desc(tc::saddr(sm.p[buf]));
 #pragma unroll
-                for (int k = 0; k < kStageKeys / 32; ++k)    // 32 keys: 4 KB of V, 512 bytes of P
-                    mma_e4m3(tmem + (kBufs + buf) * kCols, vd + k * (4096 >> 4), pd + k * (512 >> 4),
-                             idesc_e4m3(true), k > 0);
+                for (int k = 0; k < kStageKeys / 32; ++k)    // 32 keys a step
+                    mma_e4m3(tmem + kTmemO + buf * kCols, vd + k * (32 * D >> 4),
+                             pd + k * (32 * kCols >> 4),
+                             idesc_e4m3(true, D), k > 0);
                 tc::umma_commit(&sm.empty[ring.slot]);
                 tc::umma_commit(&sm.o_full[buf]);
             }
@@ -526,7 +590,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         }
     } else if (warp == kQWarp) {
         // ------------------------------------------------------------------- Q
-        // lane l: quarter l % 4 (32 entries) of head l / 4.  The operand has two
+        // lane l: quarter l % 4 of head l / 4.  The operand has two
         // buffers, freed by the unit's last S.  The powers are read by the softmax,
         // up to three stages behind the S issuer and so up to three units; this
         // role is up to two units ahead of it: 8 buffers are enough.
@@ -542,18 +606,19 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             sequence = un.record().x;
             const int32_t h0 = kvh * a.G + hg * kMaxGroup;
             const bool there = h < kHeads && h < min(kMaxGroup, a.G - hg * kMaxGroup);
-            uint4 raw[4];
+            constexpr int kChunks = D / 64;      // 16-entry chunks of the quarter
+            uint4 raw[2 * kChunks];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2 * kChunks; ++i) {
                 raw[i] = make_uint4(0, 0, 0, 0);
                 if (there)
                     raw[i] = __ldg(reinterpret_cast<const uint4*>(
-                                       a.q + ((int64_t)b * a.Hq + h0 + h) * D + part * 32) +
+                                       a.q + ((int64_t)b * a.Hq + h0 + h) * D + part * (D / 4)) +
                                    i);
             }
             uint32_t mag = 0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < D / 8; ++i) {
                 const uint32_t x = pkv::word(raw[i >> 2], i & 3);
                 const uint32_t lo = x & 0x7fffu, hi = (x >> 16) & 0x7fffu;
                 mag = max(mag, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
@@ -564,9 +629,9 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             // inverse are normal fp32 numbers
             const int e = min(max(7 - ((int)(mag >> 7) - 127), -113), 113);
             const float up16 = __int_as_float((e + 4 + 127) << 23);
-            uint32_t hi[8], lo[8];               // 32 codes of either part
+            uint32_t hi[4 * kChunks], lo[4 * kChunks];       // the codes of either part
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
+            for (int i = 0; i < D / 8; i += 2) {
                 uint16_t a0, b0, a1, b1;
                 const uint32_t x = pkv::word(raw[i >> 2], i & 3);
                 const uint32_t z = pkv::word(raw[i >> 2], (i & 3) + 1);
@@ -585,12 +650,11 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             if (h < kHeads) {
                 uint8_t* q = sm.q[units & 1];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int chunk = part * 2 + c;
-                    const int r1 = h, r2 = kHeads + h;
-                    *reinterpret_cast<uint4*>(q + r1 * D + ((chunk ^ (r1 & 7)) << 4)) =
+                for (int c = 0; c < kChunks; ++c) {
+                    const int chunk = part * kChunks + c;
+                    *reinterpret_cast<uint4*>(q + swz<D>(h, chunk)) =
                         make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                    *reinterpret_cast<uint4*>(q + r2 * D + ((chunk ^ (r2 & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(q + swz<D>(kHeads + h, chunk)) =
                         make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
                 }
                 if (part == 0) sm.q_pow[units % kQPow][h] = __int_as_float((127 - e) << 23);
@@ -613,7 +677,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         int issued = 0, units = 0;
         bool ok = true;
         // Lane l has box l of the unit (at most 1024 keys: 16 boxes).  Lanes 2j and
-        // 2j + 1 fill stage j, so a stage costs no shuffles or divisions.  A unit
+        // 2j + 1 (four lanes for head_dim 64) fill stage j, so a stage costs no shuffles or divisions.  A unit
         // needs its record, then its boxes' block ids, then their scales: at a
         // unit's start the next one's scales, the ids of the one after and the
         // record of the third are requested, and have that unit's time to arrive.
@@ -664,8 +728,9 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             const int4 fourth_info = fourth.record();
             for (int j = 0; j * kStageKeys < keys; ++j) {
                 if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
-                const int i = lane - 2 * j;      // 0, 1: this lane's box is in the stage
-                if (i == 0 || i == 1) {
+                const int i = lane - kBoxes * j; // 0 .. kBoxes - 1: its box is in the stage
+                const bool in_stage = i >= 0 && i < kBoxes;
+                if (in_stage) {
                     sm.ks[ring.slot][i] = ks;
                     sm.lv[ring.slot][i] = lv;
                     sm.iv[ring.slot][i] = iv;
@@ -676,7 +741,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     }
                 }
                 __syncwarp();
-                const uint32_t bytes = __popc(goods >> (2 * j) & 3u) * (2 * kBoxKeys * D);
+                const uint32_t bytes = __popc(goods >> (kBoxes * j) & ((1u << kBoxes) - 1u)) *
+                                       (2 * kBoxKeys * D);
                 if (i == 0) {
                     if (bytes == 0)
                         tc::mbar_arrive(&sm.full[ring.slot]);
@@ -684,7 +750,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                         tc::mbar_expect_tx(&sm.full[ring.slot], bytes);
                 }
                 __syncwarp();
-                if ((i == 0 || i == 1) && good) {
+                if (in_stage && good) {
                     uint8_t* kt = sm.kv[ring.slot] + i * kBoxKeys * D;
                     tc::tma_load_3d(kt, &kmap, &sm.full[ring.slot], 0, kvh, row);
                     tc::tma_load_3d(kt + kTileBytes, &vmap, &sm.full[ring.slot], 0, kvh, row);
@@ -728,8 +794,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         }
     } else {
         // ------------------------------------------------- gathering producers
-        // Team t takes stages t, t + kTeams, ...; a team's warp has 64 rows of each,
-        // lane l looks up rows l and l + 32 of them.  A team hands a stage over when
+        // Team t takes stages t, t + kTeams, ...; a team's warp has half the rows of
+        // each, lane l looks up rows l, l + 32, ... of them.  A team hands a stage over when
         // its copies have landed; meanwhile the other teams' are in flight.
         const int team = (warp - kFirstProducer) / kTeamWarps;
         const int row0 = (warp - kFirstProducer) % kTeamWarps * kGatherRows;
@@ -787,8 +853,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         while (un.live()) {
             const int32_t kvh = un.kv_head();
             float ks[kRows], vs[kRows];
-            // rows in 128-byte units: a tensor within the GPU's memory has fewer
-            // than 2^32 - 1 of them
+            // rows of one head: K and V within the GPU's memory have fewer than
+            // 2^32 - 1 of them each
             uint32_t row[kRows];
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
@@ -805,15 +871,15 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
             const int slot = ring.slot;
             uint8_t* kt = sm.kv[slot] + row0 * D;
+            constexpr int kChunks = D / 16, kAtOnce = 32 / kChunks;      // of a row; rows a copy
 #pragma unroll
-            for (int j = 0; j < kGatherRows / 4; ++j) {          // rows 4j .. 4j + 3, 8 chunks each
-                const int r = 4 * j + (lane >> 3), c = lane & 7;
-                const uint32_t src = __shfl_sync(0xffffffffu, row[j / 8], r & 31);
+            for (int j = 0; j < kGatherRows / kAtOnce; ++j) {
+                const int r = kAtOnce * j + lane / kChunks, c = lane % kChunks;
+                const uint32_t src = __shfl_sync(0xffffffffu, row[j * kAtOnce / 32], r & 31);
                 const bool there = src != 0xffffffffu;
-                const int dst = r * D + ((c ^ (r & 7)) << 4);
                 const uint64_t at = there ? (uint64_t)src * D + c * 16 : 0;
-                cp_async16(kt + dst, fa.kc + at, there ? 16 : 0);
-                cp_async16(kt + kTileBytes + dst, fa.vc + at, there ? 16 : 0);
+                cp_async16(kt + swz<D>(r, c), fa.kc + at, there ? 16 : 0);
+                cp_async16(kt + kTileBytes + swz<D>(r, c), fa.vc + at, there ? 16 : 0);
             }
             if (row0 == 0 && lane == 0) {
                 StageMeta m;
@@ -875,6 +941,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 }
 
 // Rows of [rows, heads, D] codes, one head of kBoxKeys rows a box.
+template <int D>
 bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int heads) {
     auto enc = pkv::tma_encode_fn();
     if (!enc) return false;
@@ -883,23 +950,24 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int heads) {
     cuuint32_t box[3] = {(cuuint32_t)D, 1, (cuuint32_t)kBoxKeys};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kHeads, bool kGather, bool kPolls>
+template <int D, int kHeads, bool kGather, bool kPolls>
 int launch(const Fp8DecodeArgs& fa, cudaStream_t s) {
     const pkv::DecodeArgs& a = fa.d;
     CUtensorMap kmap{}, vmap{};
     const int64_t rows = (int64_t)a.NB * a.bs;
-    if (!kGather && (!encode_rows(&kmap, fa.kc, rows, a.Hkv) ||
-                     !encode_rows(&vmap, fa.vc, rows, a.Hkv)))
+    if (!kGather && (!encode_rows<D>(&kmap, fa.kc, rows, a.Hkv) ||
+                     !encode_rows<D>(&vmap, fa.vc, rows, a.Hkv)))
         return PKV_ERR_CUDA;
-    const int smem = (int)sizeof(Smem) + 1024;
+    const int smem = (int)sizeof(Smem<D>) + 1024;
     static std::atomic<uint64_t> configured{0};
     void (*kernel)(const CUtensorMap, const CUtensorMap, Fp8DecodeArgs) =
-        decode_fp8_tc_kernel<kHeads, kGather, kPolls>;
+        decode_fp8_tc_kernel<D, kHeads, kGather, kPolls>;
     if (!pkv_dynamic_smem_once((const void*)kernel, smem, configured)) return PKV_ERR_CUDA;
     int64_t grid = pkv_num_sms();
     const int64_t upper = (int64_t)a.cap * a.Hkv * a.n_hg;
@@ -918,24 +986,26 @@ int launch(const Fp8DecodeArgs& fa, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, kernel, kmap, vmap, fa) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-template <int kHeads, bool kGather>
-int launch_polls(const Fp8DecodeArgs& fa, cudaStream_t s) {
-    return fa.d.wait_polls != (uint32_t)PKV_DEFAULT_WAIT_POLLS ? launch<kHeads, kGather, true>(fa, s)
-                                                               : launch<kHeads, kGather, false>(fa, s);
+// Waits with a poll limit other than the default are an instantiation of their
+// own; it takes any number of heads.
+template <int D, bool kGather>
+int launch_heads(const Fp8DecodeArgs& fa, cudaStream_t s) {
+    if (fa.d.wait_polls != (uint32_t)PKV_DEFAULT_WAIT_POLLS)
+        return launch<D, 8, kGather, true>(fa, s);
+    if (fa.d.G <= 2) return launch<D, 2, kGather, false>(fa, s);
+    if (fa.d.G <= 4) return launch<D, 4, kGather, false>(fa, s);
+    return launch<D, 8, kGather, false>(fa, s);
 }
 
-template <bool kGather>
-int launch_heads(const Fp8DecodeArgs& fa, cudaStream_t s) {
-    if (fa.d.G <= 2) return launch_polls<2, kGather>(fa, s);
-    if (fa.d.G <= 4) return launch_polls<4, kGather>(fa, s);
-    return launch_polls<8, kGather>(fa, s);
+template <int D>
+int launch_blocks(const Fp8DecodeArgs& fa, cudaStream_t s) {
+    const bool boxes = fa.d.bs % kBoxKeys == 0 && fa.d.chunk_keys % kBoxKeys == 0 &&
+                       pkv::tma_encode_fn() != nullptr;
+    return boxes ? launch_heads<D, false>(fa, s) : launch_heads<D, true>(fa, s);
 }
 
 }  // namespace
 
-int pkv_launch_decode_fp8_tc(const Fp8DecodeArgs& fa, cudaStream_t s) {
-    return fa.d.bs % kBoxKeys == 0 && fa.d.chunk_keys % kBoxKeys == 0 &&
-                   pkv::tma_encode_fn() != nullptr
-               ? launch_heads<false>(fa, s)
-               : launch_heads<true>(fa, s);
+int pkv_launch_decode_fp8(const Fp8DecodeArgs& fa, int head_dim, cudaStream_t s) {
+    return head_dim == 128 ? launch_blocks<128>(fa, s) : launch_blocks<64>(fa, s);
 }
