@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libpagedattn.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "kv_store.cu", "paged_decode.cu", "paged_decode_tma.cu", "prefill.cu",
            "prefill_tc.cu",
-           "sample.cu", "kv_store_fp8.cu", "paged_decode_fp8.cu", "paged_decode_fp8_tma.cu", "paged_decode_fp8_tc.cu",
+           "sample.cu", "kv_store_fp8.cu", "paged_decode_fp8.cu", "paged_decode_fp8_tc.cu",
            "prefill_fp8.cu",
            "logit_rules.cu"]
 

@@ -2,18 +2,25 @@
 
 Bounds, from the kernels' roundings (a value rounded to t is off by at most
 finfo(t).eps / 2 relative: bf16 2^-8, f16 2^-11, fp32 2^-24):
-  * q . K: operands are exact (q times a power of two in f16, codes in f16);
-    fp32 sums of at most 128 products, each partial sum off by at most 2^-23 of
-    the magnitudes summed (a tensor core may cut instead of round), so the
-    exponent x is off by at most dx = 128 * 2^-23 * X with X = scale * max_j
-    sum |q K_j|, and by 4 * 2^-24 * X from the fp32 steps behind it;
-  * p is rounded to f16 (decode) or bf16 (prefill) for the product with V, and
-    to bf16 the result; exp2 is good to 2^-22.
+  * q . K: codes are exact.  The decode takes a q row, scaled so that its largest
+    entry lies in [2^7, 2^8), as two e4m3 parts of 4 significant bits, the second
+    16 times finer: exact for bf16's 8 bits down to the second part's smallest
+    step, 2^-9 / 16, so off by 2^-14 < 2^-21 of the largest entry.  fp32 sums of at
+    most 128 products, each partial sum off by at most 2^-23 of the magnitudes
+    summed (a tensor core may cut instead of round).  With
+    X = scale * max_j sum |q K_j| the exponent is off by at most
+    dx = 128 * 2^-23 X + 2^-21 * scale * sum_d max|q| max_j |K_jd|,
+    and by 4 * 2^-24 X from the fp32 steps behind it;
+  * p is rounded for the product with V: in the prefill to bf16, 2^-8 of itself; in
+    the decode to f16 and then to two parts as q is, 2^-11 + 2^-9 of itself (the
+    first part leaves at most 2^-4 of [1, 2), the second rounds that to 4 bits)
+    or 2^-14 / 2^8 of the row's largest p, whichever is more;
+  * the result is rounded to bf16; exp2 is good to 2^-22.
 With A = max |V| over the row's keys, an error d in every log weight moves the
-output by at most 2 d A (a weighted mean of values within A), and the rounding
-of p by its half step times A.  So
-    |out - ref| <= 2^-8 |ref| + A (rp + 2 (dx + 2^-21 X + 2^-21)),
-rp = 2^-11 or 2^-8.  The bound is taken against the largest sums of the case."""
+output by at most 2 d A (a weighted mean of values within A), a rounding of
+every p by r of itself by r A, and one of n weights by f of the largest by n f A.
+    |out - ref| <= 2^-8 |ref| + A (r + n f + 2 (dx + 2^-21 X + 2^-21)).
+The bound is taken against the largest sums of the case."""
 from __future__ import annotations
 
 import numpy as np
@@ -21,17 +28,19 @@ import torch
 
 from oracle import fp8_cache as ofp
 
-RP_DECODE, RP_PREFILL = 2.0 ** -11, 2.0 ** -8
+DECODE, PREFILL = (2.0 ** -9 + 2.0 ** -11, 2.0 ** -22), (2.0 ** -8, 0.0)      # r, f
 
 
-def bound(ref, q, k_values, v_values, scale, rp):
+def bound(ref, q, k_values, v_values, scale, rounding, n):
     """Elementwise error bound for outputs `ref` [.., D] of queries q [.., D]
-    over the finite entries of the given key and value rows [.., D]."""
+    over at most n of the finite entries of the given key and value rows [.., D]."""
+    r, f = rounding
     kmax = np.abs(np.where(np.isfinite(k_values), k_values, 0.0)).reshape(-1, q.shape[-1]).max(0)
     big_x = abs(scale) * (np.abs(q) * kmax).sum(-1).max()
+    worst_q = abs(scale) * np.abs(q).max() * kmax.sum()
     a = np.abs(np.where(np.isfinite(v_values), v_values, 0.0)).max()
-    d = (128 * 2.0 ** -23 + 2.0 ** -21) * big_x + 2.0 ** -21
-    return 2.0 ** -8 * np.abs(ref) + a * (rp + 2 * d)
+    d = (128 * 2.0 ** -23 + 2.0 ** -21) * big_x + 2.0 ** -21 * worst_q + 2.0 ** -21
+    return 2.0 ** -8 * np.abs(ref) + a * (r + n * f + 2 * d)
 
 
 class Pool:

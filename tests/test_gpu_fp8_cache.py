@@ -148,7 +148,7 @@ def _check_decode(got, pool, q, scale):
     ref = oatt.paged_decode(U.f64(q), kv, vv, pool.bt, pool.lens, scale)
     got = U.f64(got)
     assert np.isfinite(got).all()
-    tol = F.bound(ref, U.f64(q), kv, vv, scale, F.RP_DECODE)
+    tol = F.bound(ref, U.f64(q), kv, vv, scale, F.DECODE, max(pool.lens))
     err = np.abs(got - ref)
     assert (err <= tol).all(), (err - tol).max()
     return ref
@@ -348,7 +348,7 @@ def _prefill(pkv, dev, lq, lp, bs, hkv, group, d, seed, max_k=None, extra=0):
                                     scale)
     everything = [np.concatenate([a.reshape(-1, d), U.f64(b).reshape(-1, d)])
                   for a, b in ((kv, k), (vv, v))]
-    tol = F.bound(ref, U.f64(q[:t]), everything[0], everything[1], scale, F.RP_PREFILL)
+    tol = F.bound(ref, U.f64(q[:t]), everything[0], everything[1], scale, F.PREFILL, 0)
     err = np.abs(U.f64(out[:t]) - ref)
     assert (err <= tol).all(), (err - tol).max()
 
@@ -400,7 +400,7 @@ def test_prefill_skips_inconsistent_sequences(cuda):
         tol = F.bound(ref, U.f64(q[rows]), np.concatenate([kv.reshape(-1, d),
                                                            U.f64(k).reshape(-1, d)]),
                       np.concatenate([vv.reshape(-1, d), U.f64(k).reshape(-1, d)]), 0.125,
-                      F.RP_PREFILL)
+                      F.PREFILL, 0)
         assert (np.abs(U.f64(out[rows]) - ref) <= tol).all()
 
 
@@ -429,7 +429,7 @@ def test_prefill_unreadable_prefix_rows_are_zeros(cuda):
                                         pool.bt, 0.125)
         tol = F.bound(ref, U.f64(q), np.concatenate([kv.reshape(-1, d), U.f64(k).reshape(-1, d)]),
                       np.concatenate([vv.reshape(-1, d), U.f64(k).reshape(-1, d)]), 0.125,
-                      F.RP_PREFILL)
+                      F.PREFILL, 0)
         assert (np.abs(U.f64(out) - ref) <= tol).all()
 
 
@@ -466,7 +466,7 @@ def test_a_conversation_in_the_8_bit_cache(cuda):
         ref = oatt.paged_prefill_varlen(U.f64(q), U.f64(k), U.f64(v), kv, vv, cu_q, cu_k, tables,
                                         scale)
         tol = F.bound(ref, U.f64(q), np.full((1, d), 6.0), np.full((1, d), 6.0), scale,
-                      F.RP_PREFILL)
+                      F.PREFILL, 0)
         assert (np.abs(U.f64(out) - ref) <= tol).all()
         slots = slots_of(0, done[0], new[0]) + slots_of(1, done[1], new[1])
         pkv.kv_store_fp8(k.to(cuda), v.to(cuda), *gpu, i32(slots), status=st)
@@ -482,7 +482,7 @@ def test_a_conversation_in_the_8_bit_cache(cuda):
         kv, vv = ofp.decode_values(state[0], state[2]), ofp.decode_values(state[1], state[3])
         ref = oatt.paged_decode(U.f64(q), kv, vv, tables, done, scale)
         tol = F.bound(ref, U.f64(q), np.full((1, d), 6.0), np.full((1, d), 6.0), scale,
-                      F.RP_DECODE)
+                      F.DECODE, 64)
         assert (np.abs(U.f64(out) - ref) <= tol).all()
         # the sampler's part of the step: every token but one forbidden or used up
         logits = torch.from_numpy(rng.normal(size=(2, vocab)).astype(np.float32)).to(cuda)
