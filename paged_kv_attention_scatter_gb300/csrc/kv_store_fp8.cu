@@ -100,27 +100,18 @@ __device__ __forceinline__ float scale_for(uint32_t mag) {
     return __int_as_float((c + 127) << 23);
 }
 
-struct Quantiser {
-    float scale, inv;
-    bool exact_inv;                          // a power of two: x * inv == x / scale
-    __device__ __forceinline__ uint32_t two(uint32_t w) const {
-        float lo = __int_as_float((int)(w << 16)), hi = __int_as_float((int)(w & 0xffff0000u));
-        if (exact_inv) {
-            lo *= inv;
-            hi *= inv;
-        } else {
-            lo = __fdiv_rn(lo, scale);
-            hi = __fdiv_rn(hi, scale);
-        }
-        return pkv::float2_to_e4m3x2(lo, hi);
-    }
-    __device__ __forceinline__ uint2 eight(const uint4& w) const {
-        return make_uint2(two(w.x) | two(w.y) << 16, two(w.z) | two(w.w) << 16);
-    }
-};
-
-__device__ __forceinline__ Quantiser quantiser(float c) {
-    return Quantiser{c, __fdiv_rn(1.f, c), (__float_as_int(c) & 0x7fffff) == 0};
+// The codes of eight entries divided by the scale.  For a power of two that is
+// a multiplication by its inverse; kDivide is for the scales of other writers.
+template <bool kDivide>
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, float s) {
+    const float lo = __int_as_float((int)(w << 16)), hi = __int_as_float((int)(w & 0xffff0000u));
+    if constexpr (kDivide) return pkv::float2_to_e4m3x2(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
+    return pkv::float2_to_e4m3x2(lo * s, hi * s);
+}
+template <bool kDivide>
+__device__ __forceinline__ uint2 eight_codes(const uint4& w, float s) {
+    return make_uint2(two_codes<kDivide>(w.x, s) | two_codes<kDivide>(w.y, s) << 16,
+                      two_codes<kDivide>(w.z, s) | two_codes<kDivide>(w.w, s) << 16);
 }
 
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
@@ -153,7 +144,7 @@ __device__ __forceinline__ void list_rows(const StoreArgs& a, BlockRows& sm) {
 
 // Stores the rows of block `blk` for the (tensor, head) pairs part, part +
 // parts, ... of the 2 * Hkv.  Pair p is head p >> 1 of K (even) or V.
-template <int D, int kKeep>
+template <int D, int kKeep, bool kDense>
 __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, int32_t blk,
                                             int part, int parts) {
     constexpr int kLanes = D / 8;            // lanes of a row's head segment
@@ -166,15 +157,14 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
     while (gpp > 1 && kGroups / gpp < mine) gpp >>= 1;
     const int at_once = kGroups / gpp, sub = group % gpp;
     const int rows = sm.rows;
-    const bool dense = sm.dense;
     const int32_t token0 = sm.token0, offset0 = sm.offset0;
-    const bool fresh = dense ? offset0 == 0 : sm.winner[0] >= 0;
+    const bool fresh = kDense ? offset0 == 0 : sm.winner[0] >= 0;
     const int64_t row_codes = (int64_t)a.Hkv * D;
-    auto token_of = [&](int r) { return dense ? token0 + r : sm.token[r]; };
-    auto offset_of = [&](int r) { return dense ? offset0 + r : (int)sm.offset[r]; };
+    auto token_of = [&](int r) { return kDense ? token0 + r : sm.token[r]; };
+    auto offset_of = [&](int r) { return kDense ? offset0 + r : (int)sm.offset[r]; };
     // rows of the block that this call does not store
     auto other = [&](int o) {
-        return dense ? o < offset0 || o >= offset0 + rows : sm.winner[o] < 0;
+        return kDense ? o < offset0 || o >= offset0 + rows : sm.winner[o] < 0;
     };
     for (int i0 = 0; i0 < mine; i0 += at_once) {
         const int i = i0 + group / gpp;
@@ -204,9 +194,8 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
         for (int r = rest; r < n; r += gpp) m = amax8(m, load(r));
         if ((m & 0x7fffu) >= 0x7f80u || m >= 0x7f800000u) {      // infinities or NaN
             m = 0;
-#pragma unroll
-            for (int j = 0; j < kKeep; ++j) m = finite_amax8(m, keep[j]);
-            for (int r = rest; r < n; r += gpp) m = finite_amax8(m, load(r));
+#pragma unroll 1
+            for (int r = sub; r < n; r += gpp) m = finite_amax8(m, load(r));
         }
         m = max(m & 0xffffu, m >> 16);
 #pragma unroll
@@ -224,15 +213,20 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
                 old = 0.f;
             }
             const float scale = fmaxf(old, scale_for(m));
-            const Quantiser quant = quantiser(scale);
-            auto store = [&](int r, const uint4& w) {
-                *reinterpret_cast<uint2*>(dst + offset_of(r) * row_codes) = quant.eight(w);
+            auto at = [&](int r) {
+                return reinterpret_cast<uint2*>(dst + offset_of(r) * row_codes);
             };
+            if ((__float_as_int(scale) & 0x7fffff) == 0) {
+                const float inv = __fdiv_rn(1.f, scale);
 #pragma unroll
-            for (int j = 0; j < kKeep; ++j)
-                if (sub + j * gpp < n) store(sub + j * gpp, keep[j]);
+                for (int j = 0; j < kKeep; ++j)
+                    if (sub + j * gpp < n) *at(sub + j * gpp) = eight_codes<false>(keep[j], inv);
 #pragma unroll 4
-            for (int r = rest; r < n; r += gpp) store(r, load(r));
+                for (int r = rest; r < n; r += gpp) *at(r) = eight_codes<false>(load(r), inv);
+            } else {
+#pragma unroll 1
+                for (int r = sub; r < n; r += gpp) *at(r) = eight_codes<true>(load(r), scale);
+            }
             if (old > 0.f && scale > old) ratio = __fdiv_rn(old, scale);
             if (lane == 0 && sub == 0) *scale_at = scale;
         }
@@ -276,7 +270,7 @@ __device__ __forceinline__ int parts_of(int rows, int pairs) {
 
 // Up to kScanTokens tokens: CTA t belongs to token t.
 template <int D>
-__global__ void __launch_bounds__(kThreads) store_scan_kernel(StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) store_scan_kernel(StoreArgs a) {
     __shared__ BlockRows sm;
     __shared__ int32_t before, total, first_token, first_slot;
     pkv::allow_dependent_launch();
@@ -345,7 +339,10 @@ __global__ void __launch_bounds__(kThreads) store_scan_kernel(StoreArgs a) {
                 atomicMax(&sm.winner[s[j] - lo], (int32_t)threadIdx.x + j * kThreads);
         list_rows(a, sm);
     }
-    store_block<D, kKeepScan>(a, sm, blk, part, parts);
+    if (sm.dense)
+        store_block<D, kKeepScan, true>(a, sm, blk, part, parts);
+    else
+        store_block<D, kKeepScan, false>(a, sm, blk, part, parts);
 }
 
 // More tokens: each block's runs as a linked list, and the blocks as a list.
@@ -425,7 +422,12 @@ __global__ void __launch_bounds__(kThreads, 2) store_list_kernel(StoreArgs a) {
         }
         // a part beyond the rows' need has nothing to do
         const int parts = parts_of(sm.rows, pairs);
-        if (part < parts) store_block<D, kKeepList>(a, sm, blk, part, parts);
+        if (part < parts) {
+            if (sm.dense)
+                store_block<D, kKeepList, true>(a, sm, blk, part, parts);
+            else
+                store_block<D, kKeepScan, false>(a, sm, blk, part, parts);
+        }
         __syncthreads();                     // the rows in hand are read to the end
     }
 }
@@ -478,7 +480,14 @@ int launch_store(const Fp8StoreCall& c, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pkv_num_sms() * 8), 1, 1);
+    // about a CTA an item (blocks filled to half on average, at least): the
+    // scheduler evens them out better than a loop does, and a CTA without one
+    // leaves at once
+    const int pairs = 2 * a.Hkv, most = a.bs / kRowsPerPart;
+    int64_t grid = 2LL * (a.n / a.bs + 1) * (most < 1 ? 1 : most > pairs ? pairs : most);
+    if (grid < pkv_num_sms() * 8) grid = pkv_num_sms() * 8;
+    if (grid > 1 << 20) grid = 1 << 20;
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
