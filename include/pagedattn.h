@@ -520,7 +520,7 @@ typedef struct pkv_logit_rules {
     const int32_t* token_ids;            /* [batch, max_tokens]: prompt, then generated tokens  */
     const int32_t* prompt_lens;          /* [batch]: prompt tokens of each row; NULL: 0         */
     const int32_t* token_lens;           /* [batch]: all tokens of each row; NULL: max_tokens   */
-    const float* repetition_penalties;   /* [batch], > 0; NULL: 1                               */
+    const float* repetition_penalties;   /* [batch], in [2^-100, 2^100]; NULL: 1                 */
     const float* presence_penalties;     /* [batch]; NULL: 0                                    */
     const float* frequency_penalties;    /* [batch]; NULL: 0                                    */
     const int32_t* bias_offsets;         /* [batch + 1]: row b has biases [off[b], off[b + 1])  */
@@ -548,9 +548,9 @@ typedef struct pkv_logit_rules {
  *                are not written.  Any other overlap is PKV_ERR_UNSUPPORTED.
  * Token ids < 0 (padding) are skipped; one >= vocab sets PKV_STATUS_BAD_TOKEN_ID and
  * is skipped.  Inconsistent lengths or bias offsets set PKV_STATUS_BAD_SEQLENS
- * and that list of the row counts as empty.  A repetition penalty that is not
- * positive and finite counts as 1, another one that is not finite as 0, and
- * sets PKV_STATUS_BAD_PENALTY.  A row whose mask allows no token becomes -inf
+ * and that list of the row counts as empty.  A repetition penalty outside
+ * [2^-100, 2^100] counts as 1, another penalty that is not finite as 0, and sets
+ * PKV_STATUS_BAD_PENALTY.  A row whose mask allows no token becomes -inf
  * throughout and sets PKV_STATUS_NO_ALLOWED_TOKEN.
  */
 PKV_API int pkv_apply_logit_rules(const void* logits, int32_t logits_type,

@@ -51,13 +51,13 @@ template <>
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
 struct RowRules {
-    float rep, freq, pres;
+    float rep, inv_rep, freq, pres;          // inv_rep = 1 / rep, rounded
     bool penalties;
 };
 
 __device__ __forceinline__ float penalise(float x, uint32_t word, const RowRules& p) {
     if (word) {
-        x = x > 0.f ? __fdiv_rn(x, p.rep) : x * p.rep;
+        x *= x > 0.f ? p.inv_rep : p.rep;
         const uint32_t n = word / kGenerated;
         if (n) x -= fmaf(p.freq, (float)n, p.pres);
     }
@@ -98,14 +98,36 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
         }
     }
 
-    int32_t e0 = 0, e1 = 0;                  // the row's biases
+    // the row's first tokens, before its lengths are known (the row has max_tokens
+    // entries whatever they are)
+    constexpr int kIds = 8;                  // loads in flight a lane
+    const int32_t* ids = a.r.token_ids + (int64_t)b * a.r.max_tokens;
+    int32_t first_ids[kIds];
+    if (a.r.token_ids != nullptr) {
+#pragma unroll
+        for (int u = 0; u < kIds; ++u) {
+            const int32_t i = threadIdx.x + u * kThreads;
+            if (i < a.r.max_tokens) first_ids[u] = __ldg(ids + i);
+        }
+    }
+    // the row's biases, and this thread's first one
+    int32_t e0 = 0, e1 = 0, bias_id = -1;
+    float bias_value = 0.f;
     if (a.r.bias_offsets != nullptr) {
         e0 = a.r.bias_offsets[b];
         e1 = a.r.bias_offsets[b + 1];
+        if (e0 < 0 || e1 < e0 || e1 > a.r.num_biases) {
+            if (lo == 0 && threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
+            e0 = e1 = 0;
+        }
+        if (e0 + (int)threadIdx.x < e1) {
+            bias_id = __ldg(a.r.bias_token_ids + e0 + threadIdx.x);
+            bias_value = __ldg(a.r.bias_values + e0 + threadIdx.x);
+        }
     }
 
     // ---- the row's history ----
-    RowRules p{1.f, 0.f, 0.f, false};
+    RowRules p{1.f, 1.f, 0.f, 0.f, false};
     int32_t n_tokens = 0, n_prompt = 0;
     if (a.r.token_ids != nullptr) {
         n_tokens = a.r.max_tokens;
@@ -119,11 +141,12 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
             if (lo == 0 && threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
             n_tokens = 0;
         }
-        const bool rep_ok = isfinite(p.rep) && p.rep > 0.f;
+        const bool rep_ok = p.rep >= 0x1p-100f && p.rep <= 0x1p100f;     // 1 / rep is as good
         const bool add_ok = isfinite(p.freq) && isfinite(p.pres);
         if (!(rep_ok && add_ok) && lo == 0 && threadIdx.x == 0)
             pkv::report(a.status, PKV_STATUS_BAD_PENALTY);
         if (!rep_ok) p.rep = 1.f;
+        p.inv_rep = __frcp_rn(p.rep);
         if (!isfinite(p.freq)) p.freq = 0.f;
         if (!isfinite(p.pres)) p.pres = 0.f;
         p.penalties = n_tokens > 0 && (p.rep != 1.f || p.freq != 0.f || p.pres != 0.f);
@@ -132,26 +155,31 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
         for (int i = threadIdx.x; i < (len + 3) / 4; i += kThreads)
             smem[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        const int32_t* ids = a.r.token_ids + (int64_t)b * a.r.max_tokens;
         bool bad = false;
-        constexpr int kIds = 8;              // loads in flight a lane
-        for (int32_t i0 = threadIdx.x; i0 < n_tokens; i0 += kIds * kThreads) {
+        auto count = [&](int32_t i, int32_t id) {
+            bad |= id >= a.vocab;
+            const uint32_t at = (uint32_t)(id - lo);
+            if (id < lo || at >= (uint32_t)len) return;
+            if (i < n_prompt)
+                atomicOr(&words[at], kInPrompt);
+            else
+                atomicAdd(&words[at], kGenerated);
+        };
+#pragma unroll
+        for (int u = 0; u < kIds; ++u) {
+            const int32_t i = threadIdx.x + u * kThreads;
+            if (i < n_tokens) count(i, first_ids[u]);
+        }
+        for (int32_t i0 = kIds * kThreads + threadIdx.x; i0 < n_tokens; i0 += kIds * kThreads) {
             int32_t id[kIds];
 #pragma unroll
             for (int u = 0; u < kIds; ++u) {
                 const int32_t i = i0 + u * kThreads;
-                id[u] = i < n_tokens ? __ldg(ids + i) : -1;
+                if (i < n_tokens) id[u] = __ldg(ids + i);
             }
 #pragma unroll
-            for (int u = 0; u < kIds; ++u) {
-                bad |= id[u] >= a.vocab;
-                const uint32_t at = (uint32_t)(id[u] - lo);
-                if (id[u] < lo || at >= (uint32_t)len) continue;
-                if (i0 + u * kThreads < n_prompt)
-                    atomicOr(&words[at], kInPrompt);
-                else
-                    atomicAdd(&words[at], kGenerated);
-            }
+            for (int u = 0; u < kIds; ++u)
+                if (i0 + u * kThreads < n_tokens) count(i0 + u * kThreads, id[u]);
         }
         if (bad && lo == 0) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
         __syncthreads();
@@ -223,32 +251,36 @@ __global__ void __launch_bounds__(kThreads) logit_rules_kernel(RuleArgs a) {
     }
 
     // ---- biases of this segment's entries: the last one for a token counts ----
-    if (a.r.bias_offsets != nullptr) {
-        if (e0 < 0 || e1 < e0 || e1 > a.r.num_biases) {
-            if (lo == 0 && threadIdx.x == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
-        } else if (e1 > e0) {
-            __syncthreads();                 // the counts are read, the entries written
-            bool bad = false;
-            for (int32_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
-                const int32_t id = a.r.bias_token_ids[e];
-                bad |= id >= a.vocab;
-                if (id >= lo && id - lo < len) words[id - lo] = 0;
-            }
-            if (bad && lo == 0) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
+    if (e1 > e0) {
+        // f(entry of the row, token, value) of this thread's biases
+        auto each = [&](auto f) {
+            if (bias_id >= 0) f((uint32_t)threadIdx.x, bias_id, bias_value);
+            for (int32_t e = e0 + kThreads + threadIdx.x; e < e1; e += kThreads)
+                f((uint32_t)(e - e0), __ldg(a.r.bias_token_ids + e), __ldg(a.r.bias_values + e));
+        };
+        auto here = [&](int32_t id) { return id >= lo && id - lo < len; };
+        bool bad = false, some = false;
+        each([&](uint32_t, int32_t id, float) {
+            bad |= id >= a.vocab;
+            some |= here(id);
+        });
+        if (bad && lo == 0) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
+        // (the barrier: the counts are read, the entries written)
+        if (__syncthreads_or(some)) {
+            each([&](uint32_t, int32_t id, float) {
+                if (here(id)) words[id - lo] = 0;
+            });
             __syncthreads();
-            for (int32_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
-                const int32_t id = a.r.bias_token_ids[e];
-                if (id >= lo && id - lo < len) atomicMax(&words[id - lo], (uint32_t)(e - e0) + 1u);
-            }
+            each([&](uint32_t e, int32_t id, float) {
+                if (here(id)) atomicMax(&words[id - lo], e + 1);
+            });
             __syncthreads();
-            for (int32_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
-                const int32_t id = a.r.bias_token_ids[e];
-                if (id < lo || id - lo >= len || words[id - lo] != (uint32_t)(e - e0) + 1u)
-                    continue;
+            each([&](uint32_t e, int32_t id, float value) {
+                if (!here(id) || words[id - lo] != e + 1) return;
                 const int i = id - lo;
-                if (mask && !(mask[i >> 5] >> (i & 31) & 1u)) continue;
-                out[i] += a.r.bias_values[e];
-            }
+                if (mask && !(mask[i >> 5] >> (i & 31) & 1u)) return;
+                out[i] += value;
+            });
         }
     }
 

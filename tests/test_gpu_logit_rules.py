@@ -1,9 +1,10 @@
 """apply_logit_rules on the GPU against the float64 oracle.
 
-Bound of an entry: the repetition product or quotient, f * n + p, its
-subtraction and the bias are four fp32 roundings, each off by at most 2^-24 of
-a value no larger than the sum of the magnitudes that went in (the oracle's
-second result); logits of any type are exact in fp32."""
+Bound of an entry: the repetition product (a quotient is a product with a
+rounded inverse: two roundings), f * n + p, its subtraction and the bias are at
+most five fp32 roundings, each off by at most 2^-24 of a value no larger than the
+sum of the magnitudes that went in (the oracle's second result); logits of any
+type are exact in fp32.  A sixth covers their products."""
 import math
 
 import numpy as np
@@ -75,7 +76,7 @@ def _check(got, c):
     np.testing.assert_array_equal(np.isneginf(got), np.isneginf(ref))
     fine = np.isfinite(ref)
     assert np.isfinite(got[fine]).all()
-    assert (np.abs(got[fine] - ref[fine]) <= 4 * 2.0 ** -24 * spread[fine]).all()
+    assert (np.abs(got[fine] - ref[fine]) <= 6 * 2.0 ** -24 * spread[fine]).all()
 
 
 @pytest.mark.parametrize("B,V,T,bias,mask", [
@@ -122,7 +123,7 @@ def test_several_segments_of_a_row(cuda, V):
     got = U.f64(out)
     np.testing.assert_array_equal(np.isneginf(got), np.isneginf(want))
     fine = np.isfinite(want)
-    assert (np.abs(got[fine] - want[fine]) <= 3 * 2.0 ** -24 * (np.abs(want[fine]) + 2)).all()
+    assert (np.abs(got[fine] - want[fine]) <= 4 * 2.0 ** -24 * (np.abs(want[fine]) + 2)).all()
 
 
 @pytest.mark.parametrize("V", [96, 97, 20000])
@@ -188,7 +189,7 @@ def test_status_bits_and_what_is_left_out(cuda):
                       bias_values=f32([1.0, 1.0, 1.0]))
         assert st == S["BAD_SEQLENS"] and (out[0] == 1).all()
     # penalties
-    for name, bad in (("repetition_penalties", [0.0, -1.0, math.inf, math.nan]),
+    for name, bad in (("repetition_penalties", [0.0, -1.0, 1e-31, 1e31, math.inf, math.nan]),
                       ("presence_penalties", [math.inf, math.nan]),
                       ("frequency_penalties", [-math.inf, math.nan])):
         for v in bad:
