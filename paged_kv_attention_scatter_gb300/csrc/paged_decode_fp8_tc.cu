@@ -188,6 +188,31 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -363,7 +388,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 const int mine = kGather ? key + 128 * u : (key + 128 * u) / kBoxKeys;
                 ks[u] = sm.ks[ring.slot][mine];
                 lv[u] = sm.lv[ring.slot][mine];
-                iv[u] = sm.iv[ring.slot][mine];
+                iv[u] = sm.iv[ring.slot][mine] * 0.0625f;
                 counts[u] = lv[u] != -INFINITY && (kGather || key + 128 * u < meta.keys);
             }
             if (!(ok = wait_warp(&sm.s_full[buf], par))) break;
@@ -381,13 +406,25 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     l[h] = o[h] = 0.f;
                 }
             }
+            // y = dot ks xs + lv, the heads two by two; -inf where the key does not
+            // count, whose dot may be anything
 #pragma unroll
-            for (int u = 0; u < kSub; ++u)
+            for (int u = 0; u < kSub; ++u) {
 #pragma unroll
-                for (int h = 0; h < kHeads; ++h) {
-                    const float dot = fmaf(s[u][kHeads + h], 0.0625f, s[u][h]);
-                    y[u][h] = counts[u] ? fmaf(dot, ks[u] * xs[h], lv[u]) : -INFINITY;
+                for (int h = 0; h < kHeads; h += 2) {
+                    const float2 dot = fma2(make_float2(s[u][kHeads + h], s[u][kHeads + h + 1]),
+                                            both(0.0625f), make_float2(s[u][h], s[u][h + 1]));
+                    const float2 k = mul2(both(ks[u]), make_float2(xs[h], xs[h + 1]));
+                    const float2 x = fma2(dot, k, both(lv[u]));
+                    y[u][h] = x.x;
+                    y[u][h + 1] = x.y;
                 }
+                if (!__all_sync(0xffffffffu, counts[u])) {
+#pragma unroll
+                    for (int h = 0; h < kHeads; ++h)
+                        if (!counts[u]) y[u][h] = -INFINITY;
+                }
+            }
             // ---- the stage's maxima ----
             float top[kHeads];
 #pragma unroll
@@ -408,13 +445,22 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) use[h] = m[h];
 #pragma unroll
-            for (int w = 0; w < kGroupWarps; ++w)
+            for (int w = 0; w < kGroupWarps; ++w) {
+                if constexpr (kHeads == 2) {
+                    const float2 x = *reinterpret_cast<const float2*>(sm.warp_max[buf][w]);
+                    use[0] = fmaxf(use[0], x.x);
+                    use[1] = fmaxf(use[1], x.y);
+                } else {
 #pragma unroll
-                for (int h = 0; h < kHeads; h += 2) {
-                    const float2 x = *reinterpret_cast<const float2*>(&sm.warp_max[buf][w][h]);
-                    use[h] = fmaxf(use[h], x.x);
-                    use[h + 1] = fmaxf(use[h + 1], x.y);
+                    for (int h = 0; h < kHeads; h += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(&sm.warp_max[buf][w][h]);
+                        use[h] = fmaxf(use[h], x.x);
+                        use[h + 1] = fmaxf(use[h + 1], x.y);
+                        use[h + 2] = fmaxf(use[h + 2], x.z);
+                        use[h + 3] = fmaxf(use[h + 3], x.w);
+                    }
                 }
+            }
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 const float mn = use[h];
@@ -424,9 +470,9 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 l[h] *= alpha[h];
 #pragma unroll
                 for (int x = 0; x < kSub; ++x) {
-                    const float p = pkv::fast_exp2(y[x][h] - (u - 8.f));
-                    l[h] = fmaf(p, iv[x], l[h]);
-                    y[x][h] = p;
+                    // 16 p, as split_e4m3 takes it; l is summed in sixteenths of iv
+                    y[x][h] = pkv::fast_exp2(y[x][h] - (u - 12.f));
+                    l[h] = fmaf(y[x][h], iv[x], l[h]);
                 }
             }
             // ---- the keys' rows of P: bytes h the first parts, kHeads + h the second ----
@@ -436,7 +482,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 #pragma unroll
                 for (int h = 0; h < kHeads; h += 2) {
                     uint16_t hi, lo;
-                    split_e4m3(pkv::pack_f16(y[u][h] * 16.f, y[u][h + 1] * 16.f), hi, lo);
+                    split_e4m3(pkv::pack_f16(y[u][h], y[u][h + 1]), hi, lo);
                     w[h / 4] |= (uint32_t)hi << (h % 4 * 8);
                     w[(kHeads + h) / 4] |= (uint32_t)lo << ((kHeads + h) % 4 * 8);
                 }
@@ -461,8 +507,14 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 tmem_ld<2 * kHeads>(lane_base + kTmemO + before * kCols, t);
                 tmem_wait<2 * kHeads>(t);
 #pragma unroll
-                for (int h = 0; h < kHeads; ++h)
-                    o[h] = (o[h] + fmaf(t[kHeads + h], 0.0625f, t[h])) * alpha[h];
+                for (int h = 0; h < kHeads; h += 2) {
+                    const float2 x = fma2(make_float2(t[kHeads + h], t[kHeads + h + 1]),
+                                          both(0.0625f), make_float2(t[h], t[h + 1]));
+                    const float2 sum = mul2(add2(make_float2(o[h], o[h + 1]), x),
+                                            make_float2(alpha[h], alpha[h + 1]));
+                    o[h] = sum.x;
+                    o[h + 1] = sum.y;
+                }
             }
             if (!last) continue;
             if (!(ok = wait_warp(&sm.o_full[buf], par))) break;
