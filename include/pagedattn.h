@@ -436,9 +436,16 @@ PKV_API int pkv_kv_store_fp8(const void* k, const void* v, void* k_cache, void* 
                              pkv_cache_desc cache, uint32_t* status, void* stream);
 
 /*
- * paged_decode over an e4m3 cache: arguments, workspace
- * (pkv_paged_decode_workspace_bytes) and result as in pkv_paged_decode, with
- * K and V rows code * scale.  The keys of a block whose K or V scale cannot be
+ * Bytes of device workspace pkv_paged_decode_fp8 needs (as
+ * pkv_paged_decode_workspace_bytes; its chunks are longer).
+ */
+PKV_API size_t pkv_paged_decode_fp8_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                                    int32_t max_context_len,
+                                                    pkv_cache_desc cache);
+
+/*
+ * paged_decode over an e4m3 cache: arguments and result as in
+ * pkv_paged_decode, with K and V rows code * scale.  The keys of a block whose K or V scale cannot be
  * used are left out, as are those of a block id outside the pool.
  */
 PKV_API int pkv_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
@@ -450,10 +457,14 @@ PKV_API int pkv_paged_decode_fp8(const void* q, const void* k_cache, const void*
                                  pkv_cache_desc cache, uint32_t* status, void* stream);
 
 /*
- * pkv_paged_decode_fp8 with the schedule that pkv_paged_decode_plan (the same
- * one as for a bf16 cache of this geometry) wrote into the workspace; the
- * conditions are those of pkv_paged_decode_run.
+ * paged_decode_fp8 split into a plan and a run, as pkv_paged_decode_plan and
+ * pkv_paged_decode_run split pkv_paged_decode, under the same conditions.
  */
+PKV_API int pkv_paged_decode_plan_fp8(const int32_t* context_lens, int32_t batch,
+                                      int32_t num_q_heads, int32_t max_context_len,
+                                      int32_t max_blocks_per_seq, void* workspace,
+                                      size_t workspace_bytes, pkv_cache_desc cache,
+                                      uint32_t* status, void* stream);
 PKV_API int pkv_paged_decode_run_fp8(const void* q, const void* k_cache, const void* v_cache,
                                      const float* k_scale, const float* v_scale,
                                      const int32_t* block_tables, int32_t max_blocks_per_seq,

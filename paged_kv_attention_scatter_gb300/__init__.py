@@ -29,6 +29,7 @@ from ._binding import (STATUS, cache_desc, kv_store, kv_store_paged_attention_va
                        set_wait_poll_limit, status_names, apply_logit_rules, kv_store_fp8,
                        kv_store_fp8_workspace_bytes, kv_store_paged_decode_fp8,
                        kv_store_paged_decode_fp8_workspace_bytes, paged_decode_fp8,
+                       paged_decode_fp8_workspace_bytes, paged_decode_plan_fp8,
                        paged_decode_run_fp8, paged_prefill_fp8_workspace_bytes,
                        paged_prefill_varlen_fp8)
 from ._build import build  # noqa: F401
@@ -40,5 +41,6 @@ __all__ = ["kv_store", "paged_decode", "paged_prefill_varlen", "sample", "build"
            "paged_decode_workspace_bytes", "paged_prefill_workspace_bytes", "new_status",
            "status_names", "STATUS", "cache_desc", "library_path", "set_wait_poll_limit",
            "kv_store_fp8", "paged_decode_fp8", "paged_prefill_varlen_fp8", "apply_logit_rules",
-           "kv_store_paged_decode_fp8", "paged_decode_run_fp8", "kv_store_fp8_workspace_bytes",
+           "kv_store_paged_decode_fp8", "paged_decode_plan_fp8", "paged_decode_run_fp8",
+           "paged_decode_fp8_workspace_bytes", "kv_store_fp8_workspace_bytes",
            "kv_store_paged_decode_fp8_workspace_bytes", "paged_prefill_fp8_workspace_bytes"]

@@ -43,6 +43,7 @@ C_FUNCTIONS = ["pkv_version", "pkv_error_string", "pkv_status_string", "pkv_kv_s
                "pkv_kv_store_paged_attention_varlen",
                "pkv_layer_cache", "pkv_sample_philox", "pkv_set_wait_poll_limit",
                "pkv_kv_store_fp8_workspace_bytes", "pkv_kv_store_fp8", "pkv_paged_decode_fp8",
+               "pkv_paged_decode_fp8_workspace_bytes", "pkv_paged_decode_plan_fp8",
                "pkv_paged_decode_run_fp8", "pkv_kv_store_paged_decode_fp8_workspace_bytes",
                "pkv_kv_store_paged_decode_fp8", "pkv_paged_prefill_fp8_workspace_bytes",
                "pkv_paged_prefill_varlen_fp8", "pkv_apply_logit_rules"]
@@ -130,6 +131,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.pkv_kv_store_fp8_workspace_bytes.argtypes = [I32, CacheDesc]
     lib.pkv_kv_store_fp8.restype = ctypes.c_int
     lib.pkv_kv_store_fp8.argtypes = [P, P, P, P, P, P, P, I32, P, SZ, CacheDesc, P, P]
+    lib.pkv_paged_decode_fp8_workspace_bytes.restype = SZ
+    lib.pkv_paged_decode_fp8_workspace_bytes.argtypes = [I32, I32, I32, CacheDesc]
+    lib.pkv_paged_decode_plan_fp8.restype = ctypes.c_int
+    lib.pkv_paged_decode_plan_fp8.argtypes = [P, I32, I32, I32, I32, P, SZ, CacheDesc, P, P]
     for name in ("pkv_paged_decode_fp8", "pkv_paged_decode_run_fp8"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
@@ -543,9 +548,9 @@ def set_wait_poll_limit(polls: int = DEFAULT_WAIT_POLLS) -> None:
 
 # ----------------------------------------------------------------------------
 # The 8-bit KV cache and the logit rules.  These calls run with the tensors'
-# device current, and allocate what they make themselves under `stream` when
-# one is given, so that PyTorch's allocator hands that memory out again only
-# behind the work enqueued there.
+# device current, and allocate what they make themselves on `stream` when one is
+# given, so that PyTorch's allocator hands that memory out again only behind the
+# work enqueued there.
 FP8 = torch.float8_e4m3fn
 
 
@@ -580,14 +585,28 @@ def _desc(*shape) -> CacheDesc:
     return CacheDesc(*shape)
 
 
-def _workspace(workspace, need, index):
-    """(address, bytes, what keeps them alive) of the caller's workspace or a new one."""
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-        return workspace.data_ptr(), need, workspace
-    return _at(workspace, "workspace", torch.uint8, index), workspace.numel(), workspace
+class _Scratch:
+    """(address, bytes) of the caller's workspace, or of one that lives for the
+    call: taken from PyTorch's allocator on the call's stream and given back
+    behind the work enqueued there (no tensor is made for it, which would cost
+    as much as the call's launches)."""
+
+    def __init__(self, workspace, need, index, stream):
+        self.own = None
+        if workspace is not None:
+            self.at = _at(workspace, "workspace", torch.uint8, index), workspace.numel()
+        elif need == 0:
+            self.at = None, 0
+        else:
+            self.own = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
+            self.at = self.own, need
+
+    def __enter__(self):
+        return self.at
+
+    def __exit__(self, *exc):
+        if self.own is not None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(self.own)
 
 
 def _fp8_cache(k_cache, v_cache, k_scale, v_scale):
@@ -655,10 +674,10 @@ def kv_store_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, workspa
     st = _maybe(status, "status", torch.int32, index)
 
     def call(s):
-        ws, size, _keep = _workspace(workspace, lib.pkv_kv_store_fp8_workspace_bytes(n, desc),
-                                     index)
-        _check(lib.pkv_kv_store_fp8(*rows, *cache, slots, n, ws, size, desc, st, s),
-               "pkv_kv_store_fp8")
+        need = lib.pkv_kv_store_fp8_workspace_bytes(n, desc)
+        with _Scratch(workspace, need, index, s) as ws:
+            _check(lib.pkv_kv_store_fp8(*rows, *cache, slots, n, *ws, desc, st, s),
+                   "pkv_kv_store_fp8")
     _on(index, stream, call)
 
 
@@ -672,10 +691,10 @@ def _decode_fp8(name, q, k_cache, v_cache, k_scale, v_scale, block_tables, conte
 
     def call(s):
         o = _out_like(out, q, index)
-        ws, size, _keep = _workspace(
-            workspace, lib.pkv_paged_decode_workspace_bytes(B, Hq, max_len, desc), index)
-        _check(getattr(lib, name)(qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
-                                  o.data_ptr(), ws, size, desc, st, s), name)
+        need = lib.pkv_paged_decode_fp8_workspace_bytes(B, Hq, max_len, desc)
+        with _Scratch(workspace, need, index, s) as ws:
+            _check(getattr(lib, name)(qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
+                                      o.data_ptr(), *ws, desc, st, s), name)
         return o
     return _on(index, stream, call)
 
@@ -684,17 +703,48 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, contex
                      max_context_len, out=None, workspace=None, status=None,
                      stream=None) -> torch.Tensor:
     """paged_decode over an 8-bit cache (see kv_store_fp8): q [B, Hq, D] bf16 ->
-    out [B, Hq, D] bf16.  The workspace is paged_decode's."""
+    out [B, Hq, D] bf16."""
     return _decode_fp8("pkv_paged_decode_fp8", q, k_cache, v_cache, k_scale, v_scale,
                        block_tables, context_lens, scale, max_context_len, out, workspace,
                        status, stream)
 
 
+def paged_decode_fp8_workspace_bytes(batch, num_q_heads, max_context_len, k_cache) -> int:
+    return int(load().pkv_paged_decode_fp8_workspace_bytes(batch, num_q_heads,
+                                                           int(max_context_len),
+                                                           cache_desc(k_cache)))
+
+
+def paged_decode_plan_fp8(context_lens, num_q_heads, max_context_len, max_blocks_per_seq, k_cache,
+                          workspace=None, status=None, stream=None) -> torch.Tensor:
+    """The chunk schedule of a decode batch over an 8-bit cache of k_cache's shape,
+    for any number of paged_decode_run_fp8 calls (as paged_decode_plan is for
+    paged_decode_run).  Returns the workspace."""
+    lib = load()
+    index = k_cache.get_device()
+    _at(k_cache, "k_cache", FP8, index)
+    ctx = _at(context_lens, "context_lens", torch.int32, index)
+    st = _maybe(status, "status", torch.int32, index)
+    desc = _desc(*k_cache.shape)
+    B, Hq, max_len = context_lens.numel(), int(num_q_heads), int(max_context_len)
+
+    def call(s):
+        ws = workspace
+        if ws is None:
+            need = lib.pkv_paged_decode_fp8_workspace_bytes(B, Hq, max_len, desc)
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=k_cache.device)
+        _check(lib.pkv_paged_decode_plan_fp8(ctx, B, Hq, max_len, int(max_blocks_per_seq),
+                                             _at(ws, "workspace", torch.uint8, index), ws.numel(),
+                                             desc, st, s), "pkv_paged_decode_plan_fp8")
+        return ws
+    return _on(index, stream, call)
+
+
 def paged_decode_run_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
                          max_context_len, workspace, out=None, status=None,
                          stream=None) -> torch.Tensor:
-    """paged_decode_fp8 with the schedule a paged_decode_plan call (on this cache's
-    shape) wrote into `workspace`."""
+    """paged_decode_fp8 with the schedule a paged_decode_plan_fp8 call wrote into
+    `workspace` (same context lengths and sizes)."""
     if workspace is None:
         raise ValueError("workspace must hold a plan")
     return _decode_fp8("pkv_paged_decode_run_fp8", q, k_cache, v_cache, k_scale, v_scale,
@@ -723,11 +773,11 @@ def kv_store_paged_decode_fp8(k, v, slot_mapping, q, k_cache, v_cache, k_scale, 
 
     def call(s):
         o = _out_like(out, q, index)
-        ws, size, _keep = _workspace(workspace, lib.pkv_kv_store_paged_decode_fp8_workspace_bytes(
-            n, B, Hq, max_len, desc), index)
-        _check(lib.pkv_kv_store_paged_decode_fp8(
-            *rows, slots, n, qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
-            o.data_ptr(), ws, size, desc, st, s), "pkv_kv_store_paged_decode_fp8")
+        need = lib.pkv_kv_store_paged_decode_fp8_workspace_bytes(n, B, Hq, max_len, desc)
+        with _Scratch(workspace, need, index, s) as ws:
+            _check(lib.pkv_kv_store_paged_decode_fp8(
+                *rows, slots, n, qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
+                o.data_ptr(), *ws, desc, st, s), "pkv_kv_store_paged_decode_fp8")
         return o
     return _on(index, stream, call)
 
@@ -769,11 +819,11 @@ def paged_prefill_varlen_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, cu_seq
 
     def call(s):
         o = _out_like(out, q, index)
-        ws, size, _keep = _workspace(
-            workspace, lib.pkv_paged_prefill_fp8_workspace_bytes(B, T, Hq, max_k, desc), index)
-        _check(lib.pkv_paged_prefill_varlen_fp8(
-            qp, *rows, *cache, cu_q, cu_k, B, T, max_q, max_k, Hq, bt, width, float(scale),
-            o.data_ptr(), ws, size, desc, st, s), "pkv_paged_prefill_varlen_fp8")
+        need = lib.pkv_paged_prefill_fp8_workspace_bytes(B, T, Hq, max_k, desc)
+        with _Scratch(workspace, need, index, s) as ws:
+            _check(lib.pkv_paged_prefill_varlen_fp8(
+                qp, *rows, *cache, cu_q, cu_k, B, T, max_q, max_k, Hq, bt, width, float(scale),
+                o.data_ptr(), *ws, desc, st, s), "pkv_paged_prefill_varlen_fp8")
         return o
     return _on(index, stream, call)
 

@@ -65,14 +65,21 @@ int pkv_decode_tma_supported(const pkv::DecodeArgs& a, int head_dim);
 int pkv_launch_decode_tma(pkv::DecodeArgs& a, int head_dim, cudaStream_t s);
 
 // Pieces of pkv_paged_decode (paged_decode.cu) that the decode over an e4m3
-// cache shares: the argument checks (the cache pointers are checked and stored
-// untyped), the plan kernel, and the combine kernel as a programmatic dependent
-// of the split kernel enqueued before it.
+// cache shares, with a chunk length of its own: the workspace, the argument checks
+// (the cache pointers are checked and stored untyped), the plan kernel, and the
+// combine kernel as a programmatic dependent of the split kernel before it.
+size_t pkv_decode_workspace(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
+                            const pkv_cache_desc& cache, int32_t chunk_keys);
+int pkv_decode_make_plan_args(const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                              int32_t max_context_len, int32_t max_blocks_per_seq,
+                              void* workspace, size_t workspace_bytes,
+                              const pkv_cache_desc& cache, uint32_t* status, pkv::DecodeArgs& a,
+                              int32_t chunk_keys);
 int pkv_decode_make_args(const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* block_tables, int32_t max_blocks_per_seq,
                          const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
                          int32_t max_context_len, float scale, void* out, void* workspace,
                          size_t workspace_bytes, const pkv_cache_desc& cache, uint32_t* status,
-                         pkv::DecodeArgs& a);
+                         pkv::DecodeArgs& a, int32_t chunk_keys);
 int pkv_launch_decode_plan(const pkv::DecodeArgs& a, cudaStream_t s);
 int pkv_launch_decode_combine(const pkv::DecodeArgs& a, int head_dim, cudaStream_t s);

@@ -481,12 +481,14 @@ struct DecodeLayout {
     size_t off_prefix, off_info, off_ml, off_o, total;
 };
 
+// chunk_keys 0: the choice above.
 DecodeLayout decode_layout(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
-                           const pkv_cache_desc& c) {
+                           const pkv_cache_desc& c, int32_t chunk_keys = 0) {
     DecodeLayout L{};
     const int32_t G = num_q_heads / (c.num_kv_heads > 0 ? c.num_kv_heads : 1);
     const int32_t n_hg = (G + kMaxGroup - 1) / kMaxGroup;
-    L.chunk_keys = choose_chunk_keys(batch, c.num_kv_heads * n_hg, max_ctx);
+    L.chunk_keys = chunk_keys > 0 ? chunk_keys
+                                  : choose_chunk_keys(batch, c.num_kv_heads * n_hg, max_ctx);
     const int64_t per_seq = ((int64_t)max_ctx + L.chunk_keys - 1) / L.chunk_keys;
     L.cap = (int32_t)((int64_t)batch * per_seq);
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -584,7 +586,7 @@ namespace {
 int make_plan_args(const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
                    int32_t max_context_len, int32_t max_blocks_per_seq, void* workspace,
                    size_t workspace_bytes, const pkv_cache_desc& cache, uint32_t* status,
-                   DecodeArgs& a) {
+                   DecodeArgs& a, int32_t chunk_keys = 0) {
     if (batch < 0 || max_context_len < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0 ||
         cache.num_blocks <= 0 || cache.block_size <= 0 || cache.num_kv_heads <= 0)
         return PKV_ERR_BAD_DIMENSION;
@@ -593,7 +595,7 @@ int make_plan_args(const int32_t* context_lens, int32_t batch, int32_t num_q_hea
     if (!context_lens || !workspace) return PKV_ERR_NULL_POINTER;
     if ((uintptr_t)workspace & 15) return PKV_ERR_MISALIGNED;
     if ((uintptr_t)context_lens & 3) return PKV_ERR_MISALIGNED;
-    const DecodeLayout L = decode_layout(batch, num_q_heads, max_context_len, cache);
+    const DecodeLayout L = decode_layout(batch, num_q_heads, max_context_len, cache, chunk_keys);
     if (workspace_bytes < L.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
     char* ws = (char*)workspace;
     a.ctx = context_lens;
@@ -627,7 +629,7 @@ int make_decode_args(const void* q, const void* k_cache, const void* v_cache,
                      const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
                      int32_t max_context_len, float scale, void* out, void* workspace,
                      size_t workspace_bytes, const pkv_cache_desc& cache, uint32_t* status,
-                     DecodeArgs& a) {
+                     DecodeArgs& a, int32_t chunk_keys = 0) {
     if (batch < 0 || max_context_len < 0 || max_blocks_per_seq <= 0 || num_q_heads <= 0 ||
         cache.num_blocks <= 0 || cache.block_size <= 0 || cache.num_kv_heads <= 0)
         return PKV_ERR_BAD_DIMENSION;
@@ -641,7 +643,7 @@ int make_decode_args(const void* q, const void* k_cache, const void* v_cache,
     if (((uintptr_t)block_tables | (uintptr_t)context_lens) & 3) return PKV_ERR_MISALIGNED;
     const int rc = make_plan_args(context_lens, batch, num_q_heads, max_context_len,
                                   max_blocks_per_seq, workspace, workspace_bytes, cache, status,
-                                  a);
+                                  a, chunk_keys);
     if (rc != PKV_OK) return rc;
     a.q = (const __nv_bfloat16*)q;
     a.kc = (const __nv_bfloat16*)k_cache;
@@ -654,15 +656,29 @@ int make_decode_args(const void* q, const void* k_cache, const void* v_cache,
 
 }  // namespace
 
+size_t pkv_decode_workspace(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
+                            const pkv_cache_desc& cache, int32_t chunk_keys) {
+    return decode_layout(batch, num_q_heads, max_context_len, cache, chunk_keys).total;
+}
+
+int pkv_decode_make_plan_args(const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
+                              int32_t max_context_len, int32_t max_blocks_per_seq,
+                              void* workspace, size_t workspace_bytes,
+                              const pkv_cache_desc& cache, uint32_t* status, DecodeArgs& a,
+                              int32_t chunk_keys) {
+    return make_plan_args(context_lens, batch, num_q_heads, max_context_len, max_blocks_per_seq,
+                          workspace, workspace_bytes, cache, status, a, chunk_keys);
+}
+
 int pkv_decode_make_args(const void* q, const void* k_cache, const void* v_cache,
                          const int32_t* block_tables, int32_t max_blocks_per_seq,
                          const int32_t* context_lens, int32_t batch, int32_t num_q_heads,
                          int32_t max_context_len, float scale, void* out, void* workspace,
                          size_t workspace_bytes, const pkv_cache_desc& cache, uint32_t* status,
-                         DecodeArgs& a) {
+                         DecodeArgs& a, int32_t chunk_keys) {
     return make_decode_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
                             batch, num_q_heads, max_context_len, scale, out, workspace,
-                            workspace_bytes, cache, status, a);
+                            workspace_bytes, cache, status, a, chunk_keys);
 }
 
 int pkv_launch_decode_plan(const DecodeArgs& a, cudaStream_t s) {

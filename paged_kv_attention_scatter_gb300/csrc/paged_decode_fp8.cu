@@ -19,6 +19,25 @@
 namespace {
 
 using pkv::Fp8DecodeArgs;
+using pkv::kMaxGroup;
+
+// Keys per work unit, from the sizes alone: the multiple of 128 (a stage of
+// head_dim 128) nearest to the length that gives about two units per SM for a
+// typical context of half the stated maximum, within 128..1024.  A unit's end
+// -- its last stage's P V waited for, the two softmax groups' shares merged --
+// costs about a stage, so units are longer than the bf16 decode's, whose rule
+// aims at sixteen a SM (measured, us: 64 sequences of 16/8 heads and 512..4096
+// keys 59 at 256, 57 at 512, 57 at 1024; 8 of 32/8 and 4000..8192 39 at 128, 28 at
+// 512, 27 at 1024; 2 of 30000..32768 60, 35, 33).
+int32_t choose_chunk_keys(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
+                          const pkv_cache_desc& c) {
+    const int32_t hkv = c.num_kv_heads > 0 ? c.num_kv_heads : 1;
+    const int32_t n_hg = (num_q_heads / hkv + kMaxGroup - 1) / kMaxGroup;
+    const double keys = (double)max_ctx / 2.0 * batch * hkv * n_hg / (2.0 * 152);
+    const double chunk = keys / 128.0 + 0.5;
+    if (chunk < 1.0) return 128;
+    return chunk >= 8.0 ? 1024 : (int32_t)chunk * 128;
+}
 
 // Plan (unless a plan is in the workspace), split, combine.
 int launch_decode(Fp8DecodeArgs& fa, int head_dim, bool plan, cudaStream_t s) {
@@ -37,7 +56,9 @@ int make_args(const void* q, const void* k_cache, const void* v_cache, const flo
               Fp8DecodeArgs& fa) {
     const int rc = pkv_decode_make_args(q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                         context_lens, batch, num_q_heads, max_context_len, scale,
-                                        out, workspace, workspace_bytes, cache, status, fa.d);
+                                        out, workspace, workspace_bytes, cache, status, fa.d,
+                                        choose_chunk_keys(batch, num_q_heads, max_context_len,
+                                                          cache));
     if (rc != PKV_OK) return rc;
     if (!k_scale || !v_scale) return PKV_ERR_NULL_POINTER;
     if (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3) return PKV_ERR_MISALIGNED;
@@ -51,6 +72,30 @@ int make_args(const void* q, const void* k_cache, const void* v_cache, const flo
 }
 
 }  // namespace
+
+extern "C" size_t pkv_paged_decode_fp8_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                                       int32_t max_context_len,
+                                                       pkv_cache_desc cache) {
+    if (batch < 0 || num_q_heads <= 0 || max_context_len < 0 || cache.num_kv_heads <= 0 ||
+        cache.head_dim <= 0)
+        return 0;
+    return pkv_decode_workspace(batch, num_q_heads, max_context_len, cache,
+                                choose_chunk_keys(batch, num_q_heads, max_context_len, cache));
+}
+
+extern "C" int pkv_paged_decode_plan_fp8(const int32_t* context_lens, int32_t batch,
+                                         int32_t num_q_heads, int32_t max_context_len,
+                                         int32_t max_blocks_per_seq, void* workspace,
+                                         size_t workspace_bytes, pkv_cache_desc cache,
+                                         uint32_t* status, void* stream) {
+    if (batch == 0 && max_context_len >= 0 && num_q_heads > 0) return PKV_OK;
+    pkv::DecodeArgs a{};
+    const int rc = pkv_decode_make_plan_args(
+        context_lens, batch, num_q_heads, max_context_len, max_blocks_per_seq, workspace,
+        workspace_bytes, cache, status, a,
+        choose_chunk_keys(batch, num_q_heads, max_context_len, cache));
+    return rc != PKV_OK ? rc : pkv_launch_decode_plan(a, (cudaStream_t)stream);
+}
 
 extern "C" int pkv_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
                                     const float* k_scale, const float* v_scale,
@@ -90,7 +135,8 @@ namespace {
 // The store's list of runs lies behind the decode's workspace.
 size_t store_at(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
                 const pkv_cache_desc& cache) {
-    return (pkv_paged_decode_workspace_bytes(batch, num_q_heads, max_context_len, cache) + 255) &
+    return (pkv_paged_decode_fp8_workspace_bytes(batch, num_q_heads, max_context_len, cache) +
+            255) &
            ~(size_t)255;
 }
 

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunkRows = 16;               // prefix rows per CTA
+constexpr int kBatch = 4;                    // vectors a lane has in flight
 constexpr int kBlock = 128;                  // rows per workspace cache block
 constexpr int64_t kExpandBytes = 4LL << 30;  // K and V rows of a group, where >= 1 fits
 
@@ -41,6 +42,13 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint32_t f16x2, float s) {
     return pkv::pack_bf16(f.x * s, f.y * s);
 }
 
+// 32 bytes to global memory in one instruction (address 32-byte aligned).
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // CTA (x, y): prefix rows 16x .. 16x + 15 of sequence y.  A row that cannot be
 // read (block id or scale out of range) is written as zeros and reported.
 __global__ void __launch_bounds__(kThreads) expand_prefix_kernel(ExpandArgs e,
@@ -55,38 +63,58 @@ __global__ void __launch_bounds__(kThreads) expand_prefix_kernel(ExpandArgs e,
     const int32_t rows = min(lk - lq - r0, kChunkRows);
     if (rows <= 0) return;
     const int32_t vecs = e.Hkv * (e.D / 16);                  // 16-code vectors per row
+    const int32_t half = rows * vecs, per_head = e.D / 16;   // K's vectors, then V's
     uint32_t bad = 0;
-    for (int32_t i = threadIdx.x; i < 2 * rows * vecs; i += kThreads) {
-        const int32_t j = i >> 1;                             // K and V of a vector side by side
-        const bool is_v = i & 1;
-        const int32_t r = j / vecs, c = j - r * vecs;
-        const int32_t key = r0 + r;
-        const int32_t blk = __ldg(e.bt + (int64_t)b * e.MB + key / e.bs);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        float s = 0.f;
-        if ((unsigned)blk < (unsigned)e.NB) {
-            s = __ldg((is_v ? e.vs : e.ks) + (int64_t)blk * e.Hkv + c / (e.D / 16));
-            if (pkv::scale_ok(s)) {
-                w = pkv::ld_stream16((is_v ? e.vc : e.kc) +
-                                     (((int64_t)blk * e.bs + key % e.bs) * vecs + c) * 16);
-            } else {
-                s = 0.f;
-                bad |= PKV_STATUS_BAD_SCALE;
+    // kBatch vectors a lane at once: a vector is three loads, of which the scale's
+    // and the codes' addresses need the block id
+    for (int32_t i0 = threadIdx.x; i0 < 2 * half; i0 += kBatch * kThreads) {
+        int32_t blk[kBatch], row[kBatch], col[kBatch];       // row of the chunk; vector of the row
+        float s[kBatch];
+        uint4 w[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int32_t i = i0 + u * kThreads;
+            const int32_t j = i < half ? i : i - half;
+            row[u] = j / vecs;
+            col[u] = j - row[u] * vecs;
+            blk[u] = i < 2 * half ? __ldg(e.bt + (int64_t)b * e.MB + (r0 + row[u]) / e.bs) : -1;
+            if (i < 2 * half && (unsigned)blk[u] >= (unsigned)e.NB) {
+                bad |= PKV_STATUS_BAD_BLOCK_ID;
+                blk[u] = -1;
             }
-        } else {
-            bad |= PKV_STATUS_BAD_BLOCK_ID;
         }
-        uint32_t h[8];
-        pkv::e4m3x4_to_f16x4(w.x, h[0], h[1]);
-        pkv::e4m3x4_to_f16x4(w.y, h[2], h[3]);
-        pkv::e4m3x4_to_f16x4(w.z, h[4], h[5]);
-        pkv::e4m3x4_to_f16x4(w.w, h[6], h[7]);
-        uint4* dst = reinterpret_cast<uint4*>(is_v ? e.vo : e.ko) +
-                     (((int64_t)b * e.rows_per_seq + key) * vecs + c) * 2;
-        dst[0] = make_uint4(to_bf16x2(h[0], s), to_bf16x2(h[1], s), to_bf16x2(h[2], s),
-                            to_bf16x2(h[3], s));
-        dst[1] = make_uint4(to_bf16x2(h[4], s), to_bf16x2(h[5], s), to_bf16x2(h[6], s),
-                            to_bf16x2(h[7], s));
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const bool is_v = i0 + u * kThreads >= half;
+            s[u] = 0.f;
+            w[u] = make_uint4(0, 0, 0, 0);
+            if (blk[u] < 0) continue;
+            s[u] = __ldg((is_v ? e.vs : e.ks) + (int64_t)blk[u] * e.Hkv + col[u] / per_head);
+            w[u] = pkv::ld_stream16((is_v ? e.vc : e.kc) +
+                                    (((int64_t)blk[u] * e.bs + (r0 + row[u]) % e.bs) * vecs +
+                                     col[u]) * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int32_t i = i0 + u * kThreads;
+            if (i >= 2 * half) continue;
+            float sc = s[u];
+            if (!pkv::scale_ok(sc)) {
+                if (blk[u] >= 0) bad |= PKV_STATUS_BAD_SCALE;
+                sc = 0.f;
+                w[u] = make_uint4(0, 0, 0, 0);
+            }
+            uint32_t h[8];
+            pkv::e4m3x4_to_f16x4(w[u].x, h[0], h[1]);
+            pkv::e4m3x4_to_f16x4(w[u].y, h[2], h[3]);
+            pkv::e4m3x4_to_f16x4(w[u].z, h[4], h[5]);
+            pkv::e4m3x4_to_f16x4(w[u].w, h[6], h[7]);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) h[x] = to_bf16x2(h[x], sc);
+            st_global_32b((i >= half ? e.vo : e.ko) +
+                              (((int64_t)b * e.rows_per_seq + r0 + row[u]) * vecs + col[u]) * 16,
+                          h);
+        }
     }
     if (bad) pkv::report(p.status, bad);
 }
@@ -111,7 +139,8 @@ Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t max_
     L.off_table = align(pkv_prefill_layout(batch, total_q).total);
     L.off_k = align(L.off_table + sizeof(int32_t) * (size_t)(group * (L.rows_per_seq / kBlock)));
     L.off_v = align(L.off_k + (size_t)(group * L.rows_per_seq * row * 2));
-    L.total = align(L.off_v + (size_t)(group * L.rows_per_seq * row * 2));
+    // 256 bytes more: the workspace is 16-byte aligned, the rows are written by 32
+    L.total = align(L.off_v + (size_t)(group * L.rows_per_seq * row * 2)) + 256;
     return L;
 }
 
@@ -166,7 +195,7 @@ extern "C" int pkv_paged_prefill_varlen_fp8(
     const Fp8PrefillLayout L = fp8_prefill_layout(batch, total_q, max_seqlen_k, cache);
     if (workspace_bytes < L.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
     if (L.group * L.rows_per_seq >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
-    char* ws = (char*)workspace;
+    char* ws = (char*)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
     ExpandCall c{};
     c.s = s;
     c.e.kc = (const uint8_t*)k_cache;

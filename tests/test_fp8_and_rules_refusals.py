@@ -62,14 +62,28 @@ def test_decode(lib):
         for name in ("q", "kc", "vc", "ks", "vs", "bt", "ctx", "out", "ws"):
             assert decode(**{name: None}) == -1
             assert decode(**{name: ODD}) == -4
-        need = lib.pkv_paged_decode_workspace_bytes(2, 4, 64, _desc())
-        assert decode(size=need - 1) == -5
+        need = lib.pkv_paged_decode_fp8_workspace_bytes(2, 4, 64, _desc())
+        assert need > 0 and decode(size=need - 1) == -5
+
+
+def test_decode_plan(lib):
+    f = lib.pkv_paged_decode_plan_fp8
+
+    def plan(ctx=OK, batch=2, hq=4, max_ctx=64, ws=OK, size=BIG, desc=None):
+        return f(ctx, batch, hq, max_ctx, 4, ws, size, desc or _desc(), None, None)
+    assert plan(batch=0, ctx=None, ws=None) == 0
+    assert plan(ctx=None) == -1 and plan(ws=None) == -1
+    assert plan(ctx=ODD) == -4 and plan(ws=ODD) == -4
+    assert plan(hq=3) == -2 and plan(desc=_desc(d=80)) == -3
+    need = lib.pkv_paged_decode_fp8_workspace_bytes(2, 4, 64, _desc())
+    assert plan(size=need - 1) == -5
+    assert lib.pkv_paged_decode_fp8_workspace_bytes(2, 0, 64, _desc()) == 0
 
 
 def test_store_and_decode(lib):
     f = lib.pkv_kv_store_paged_decode_fp8
     query = lib.pkv_kv_store_paged_decode_fp8_workspace_bytes
-    dec = lib.pkv_paged_decode_workspace_bytes(2, 4, 64, _desc())
+    dec = lib.pkv_paged_decode_fp8_workspace_bytes(2, 4, 64, _desc())
     assert query(3, 2, 4, 64, _desc()) >= dec > 0
     assert query(5000, 2, 4, 64, _desc()) >= dec + lib.pkv_kv_store_fp8_workspace_bytes(5000,
                                                                                         _desc())

@@ -261,7 +261,8 @@ def test_plan_and_runs_are_the_whole_call(cuda):
     pool = F.Pool(lens, 64, 2, 128, seed=6)
     args = pool.on(cuda)
     ctx = torch.tensor(lens, dtype=torch.int32, device=cuda)
-    ws = pkv.paged_decode_plan(ctx, 8, 1000, args[4].shape[1], args[0])
+    ws = pkv.paged_decode_plan_fp8(ctx, 8, 1000, args[4].shape[1], args[0])
+    assert ws.numel() >= pkv.paged_decode_fp8_workspace_bytes(4, 8, 1000, args[0])
     for i in range(3):
         q = F.bf16(rng, 4, 8, 128).to(cuda)
         whole = pkv.paged_decode_fp8(q, *args, ctx, 0.1, 1000)
