@@ -33,6 +33,44 @@ struct DecodeArgs {
     int32_t total_q;                 // rows of q / out (varlen batch only)
     int32_t b0;                      // first sequence of a combine launch
     uint32_t wait_polls;             // polls of a bounded mbarrier wait
+    // No plan in the workspace: the kernels take the schedule of a batch of at
+    // most 32 sequences from `ctx` themselves (WarpPlan).
+    int32_t inline_plan;
+};
+
+// The chunk schedule of at most 32 sequences, held by a warp: lane b has sequence
+// b's length, chunks and the chunks up to and with it.  What the plan kernel
+// writes for any number, without its launch.
+struct WarpPlan {
+    int32_t len, n, incl;
+    bool bad;                        // this lane's length is out of range (it gets no chunks)
+    __device__ __forceinline__ explicit WarpPlan(const DecodeArgs& a) {
+        const int lane = threadIdx.x & 31;
+        len = lane < a.B ? a.ctx[lane] : 0;
+        bad = len < 0 || len > (int64_t)a.MB * a.bs || len > a.max_ctx;
+        n = bad ? 0 : (len + a.chunk_keys - 1) / a.chunk_keys;
+        incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
+        }
+    }
+    __device__ __forceinline__ int32_t total() const {
+        return __shfl_sync(0xffffffffu, incl, 31);
+    }
+    // (first chunk, chunks) of sequence b
+    __device__ __forceinline__ int2 of(int32_t b) const {
+        const int32_t nb = __shfl_sync(0xffffffffu, n, b);
+        return make_int2(__shfl_sync(0xffffffffu, incl, b) - nb, nb);
+    }
+    // (sequence, first key, end key, chunks of the sequence) of chunk sc < total()
+    __device__ __forceinline__ int4 record(int32_t sc, int32_t chunk_keys) const {
+        const int32_t b = __popc(__ballot_sync(0xffffffffu, incl <= sc));
+        const int2 f = of(b);
+        const int32_t i = sc - f.x, l = __shfl_sync(0xffffffffu, len, b);
+        return make_int4(b, i * chunk_keys, min(l, (i + 1) * chunk_keys), f.y);
+    }
 };
 
 // q / out row of sequence b

@@ -68,6 +68,8 @@ struct Fp8DecodeArgs {
     const uint8_t* vc;
     const float* ks;                 // [num_blocks, num_kv_heads]
     const float* vs;
+    int32_t no_combine;              // every sequence is one chunk at most: the split kernel
+                                     // writes all output rows
 };
 
 }  // namespace pkv

@@ -383,7 +383,15 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
     // The plan's prefix is final before this grid launches (the split kernels
     // allow it only after their own wait for the plan), so it is read ahead
     // of the wait for the split kernel's partials.
-    const int32_t p0 = a.chunk_prefix[b], n = a.chunk_prefix[b + 1] - p0;
+    int32_t p0, n;
+    if (a.inline_plan) {
+        const int2 f = pkv::WarpPlan(a).of(b);
+        p0 = f.x;
+        n = f.y;
+    } else {
+        p0 = a.chunk_prefix[b];
+        n = a.chunk_prefix[b + 1] - p0;
+    }
     wait_for_predecessor();                  // the split kernel's partials
     if (h >= a.Hq) return;
     if (n == 1) return;                                  // written by the split kernel
@@ -620,6 +628,7 @@ int make_plan_args(const int32_t* context_lens, int32_t batch, int32_t num_q_hea
     a.total_q = 0;
     a.b0 = 0;
     a.wait_polls = pkv_wait_polls();
+    a.inline_plan = 0;
     return PKV_OK;
 }
 

@@ -35,16 +35,23 @@ int32_t choose_chunk_keys(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
     const int32_t n_hg = (num_q_heads / hkv + kMaxGroup - 1) / kMaxGroup;
     const double keys = (double)max_ctx / 2.0 * batch * hkv * n_hg / (2.0 * 152);
     const double chunk = keys / 128.0 + 0.5;
+    // short contexts: one unit a sequence and head, so that nothing is left to combine
+    if (max_ctx <= 512) return max_ctx <= 128 ? 128 : (max_ctx + 127) / 128 * 128;
     if (chunk < 1.0) return 128;
     return chunk >= 8.0 ? 1024 : (int32_t)chunk * 128;
 }
 
-// Plan (unless a plan is in the workspace), split, combine.
+// Plan, split, combine.  A batch of at most 32 sequences needs no plan kernel (nor
+// has one if a plan is in the workspace), and one of single chunks no combine: a
+// small call's time is mostly its launches'.
 int launch_decode(Fp8DecodeArgs& fa, int head_dim, bool plan, cudaStream_t s) {
-    int rc = plan ? pkv_launch_decode_plan(fa.d, s) : PKV_OK;
+    int rc = PKV_OK;
+    fa.d.inline_plan = plan && fa.d.B <= 32;
+    fa.no_combine = fa.d.max_ctx <= fa.d.chunk_keys;
+    if (plan && !fa.d.inline_plan) rc = pkv_launch_decode_plan(fa.d, s);
     if (rc != PKV_OK) return rc;
     rc = pkv_launch_decode_fp8(fa, head_dim, s);
-    if (rc != PKV_OK) return rc;
+    if (rc != PKV_OK || fa.no_combine) return rc;
     return pkv_launch_decode_combine(fa.d, head_dim, s);
 }
 

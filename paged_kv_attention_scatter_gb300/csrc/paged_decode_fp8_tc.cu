@@ -243,23 +243,44 @@ __device__ __forceinline__ void cp_async16(void* smem, const void* gmem, uint32_
                  : "memory");
 }
 
+// The chunk records, as a warp reads them: from the plan kernel's list, or from
+// the warp's own plan.
+struct Schedule {
+    pkv::WarpPlan plan;
+    const int4* records;
+    int32_t chunks, chunk_keys;
+    bool own;
+    __device__ __forceinline__ explicit Schedule(const pkv::DecodeArgs& a)
+        : plan(own_args(a)), records(a.chunk_info), chunk_keys(a.chunk_keys),
+          own(a.inline_plan != 0) {
+        chunks = own ? plan.total() : a.chunk_prefix[a.B];
+    }
+    // (a plan of no sequences where the list is used)
+    __device__ __forceinline__ static pkv::DecodeArgs own_args(const pkv::DecodeArgs& a) {
+        pkv::DecodeArgs x = a;
+        if (!a.inline_plan) x.B = 0;
+        return x;
+    }
+    // no keys past the last chunk
+    __device__ __forceinline__ int4 record(int32_t sc) const {
+        if (sc >= chunks) return make_int4(0, 0, 0, 0);
+        return own ? plan.record(sc, chunk_keys) : records[sc];
+    }
+};
+
 // A CTA's units in order: unit u is (chunk u / per_sc, kv head, group of q
 // heads).  The CTA takes u = blockIdx.x, + gridDim.x, ...; a step is an addition
 // with carry, not a division.
 struct Units {
-    int32_t sc, rem, chunks, per_sc, n_hg, step_sc, step_rem;
-    const int4* records;
+    int32_t sc, rem, per_sc, n_hg, step_sc, step_rem;
     __device__ __forceinline__ explicit Units(const pkv::DecodeArgs& a) {
         per_sc = a.Hkv * a.n_hg;
         n_hg = a.n_hg;
-        records = a.chunk_info;
-        chunks = a.chunk_prefix[a.B];
         sc = (int32_t)blockIdx.x / per_sc;
         rem = (int32_t)blockIdx.x % per_sc;
         step_sc = (int32_t)gridDim.x / per_sc;
         step_rem = (int32_t)gridDim.x % per_sc;
     }
-    __device__ __forceinline__ bool live() const { return sc < chunks; }
     __device__ __forceinline__ void next() {
         sc += step_sc;
         rem += step_rem;
@@ -267,10 +288,6 @@ struct Units {
             rem -= per_sc;
             ++sc;
         }
-    }
-    // (sequence, first key, end key, chunks of the sequence); no keys past the end
-    __device__ __forceinline__ int4 record() const {
-        return live() ? records[sc] : make_int4(0, 0, 0, 0);
     }
     __device__ __forceinline__ int32_t kv_head() const { return n_hg == 1 ? rem : rem / n_hg; }
     __device__ __forceinline__ int32_t head_group() const { return n_hg == 1 ? 0 : rem % n_hg; }
@@ -651,15 +668,27 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         // up to three stages behind the S issuer and so up to three units; this
         // role is up to two units ahead of it: 8 buffers are enough.
         const int h = lane >> 2, part = lane & 3;
+        const Schedule sched(a);
+        if (sched.own && blockIdx.x == 0 && sched.plan.bad)
+            pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
+        if (fa.no_combine) {                     // the rows of sequences without keys
+            for (int32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
+                const int32_t n = sched.own ? sched.plan.of(b).y
+                                            : a.chunk_prefix[b + 1] - a.chunk_prefix[b];
+                if (n > 0) continue;
+                uint4* row = reinterpret_cast<uint4*>(a.out + (int64_t)b * a.Hq * D);
+                for (int32_t i = lane; i < a.Hq * (D / 8); i += 32) row[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
         Units un(a);
         uint32_t units = 0;
         bool ok = true;
-        int32_t sequence = un.record().x;        // of the unit after: loaded a unit ahead
-        for (; un.live(); ++units) {
+        int32_t sequence = sched.record(un.sc).x;        // of the unit after: loaded a unit ahead
+        for (; un.sc < sched.chunks; ++units) {
             const int32_t hg = un.head_group(), kvh = un.kv_head();
             const int32_t b = sequence;
             un.next();
-            sequence = un.record().x;
+            sequence = sched.record(un.sc).x;
             const int32_t h0 = kvh * a.G + hg * kMaxGroup;
             const bool there = h < kHeads && h < min(kMaxGroup, a.G - hg * kMaxGroup);
             constexpr int kChunks = D / 64;      // 16-entry chunks of the quarter
@@ -745,17 +774,18 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             return (unsigned)blk < (unsigned)a.NB ? __ldg(scales + (int64_t)blk * a.Hkv + kvh)
                                                   : 0.f;
         };
+        const Schedule sched(a);
         Units un(a), next_un = un, third = un;
-        int4 info = un.record();
+        int4 info = sched.record(un.sc);
         next_un.next();
-        int4 next_info = next_un.record();
+        int4 next_info = sched.record(next_un.sc);
         third.next();
         third.next();
-        int4 third_info = third.record();
+        int4 third_info = sched.record(third.sc);
         int32_t blk = load_block(info), next_blk = load_block(next_info);
         float ks_in = load_scale(fa.ks, blk, un.kv_head());
         float vs_in = load_scale(fa.vs, blk, un.kv_head());
-        while (un.live() && ok) {
+        while (un.sc < sched.chunks && ok) {
             const int32_t kvh = un.kv_head();
             const int32_t key0 = info.y, keys = info.z - key0;
             const bool inside = (unsigned)blk < (unsigned)a.NB;
@@ -781,7 +811,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             const int32_t third_blk = load_block(third_info);
             Units fourth = third;
             fourth.next();
-            const int4 fourth_info = fourth.record();
+            const int4 fourth_info = sched.record(fourth.sc);
             for (int j = 0; j * kStageKeys < keys; ++j) {
                 if (!(ok = wait_warp(&sm.empty[ring.slot], ring.phase ^ 1))) break;
                 const int i = lane - kBoxes * j; // 0 .. kBoxes - 1: its box is in the stage
@@ -862,13 +892,14 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         // A walk over the stages, with this lane's keys of each as table entry and
         // offset; a stage on is 128 keys on (divisions only at a unit's start).
         const int32_t step_blocks = kStageKeys / a.bs, step_off = kStageKeys % a.bs;
+        const Schedule sched(a);
         Units un(a);
-        int4 info = un.record(), ahead;          // this unit's record and the next one's
+        int4 info = sched.record(un.sc), ahead;          // this unit's record and the next one's
         int32_t k = 0, block[kRows], off[kRows];
         auto start_unit = [&]() {
             Units after = un;
             after.next();
-            ahead = after.record();
+            ahead = sched.record(after.sc);
             k = info.y;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
@@ -904,9 +935,9 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                              ? a.bt[(int64_t)info.x * a.MB + block[i]] : -2;
         };
         start_unit();
-        for (int i = 0; i < team && un.live(); ++i) step();
+        for (int i = 0; i < team && un.sc < sched.chunks; ++i) step();
         load_blocks();
-        while (un.live()) {
+        while (un.sc < sched.chunks) {
             const int32_t kvh = un.kv_head();
             float ks[kRows], vs[kRows];
             // rows of one head: K and V within the GPU's memory have fewer than
@@ -963,7 +994,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 sm.iv[slot][key] = good ? __frcp_rn(vs[i]) : 0.f;
             }
             // the team's next stage: its block ids arrive while the copies land
-            for (int i = 0; i < kTeams && un.live(); ++i) step();
+            for (int i = 0; i < kTeams && un.sc < sched.chunks; ++i) step();
             load_blocks();
             asm volatile("cp.async.wait_all;" ::: "memory");
             tc::fence_proxy_async_smem();
