@@ -400,7 +400,7 @@ PKV_API int pkv_sample_philox(const float* logits, const float* temperatures, ui
  *   k_scale, v_scale  [num_blocks, num_kv_heads] fp32: an entry's value is its
  *                     code times the scale of its block and kv head
  * block_size is at most PKV_FP8_MAX_BLOCK_SIZE, head_dim 64 or 128.  Attention
- * takes any scale in [2^-100, FLT_MAX].  A scale outside it (0 marks a block
+ * takes any scale in [2^-96, FLT_MAX].  A scale outside it (0 marks a block
  * without rows) sets PKV_STATUS_BAD_SCALE where a key needs it.
  */
 #define PKV_FP8_MAX_BLOCK_SIZE 1024
@@ -423,7 +423,7 @@ PKV_API size_t pkv_kv_store_fp8_workspace_bytes(int32_t num_tokens, pkv_cache_de
  *        rounded the same way.
  * A row at offset 0 begins the block anew, as a sequence fills its blocks in
  * order: c counts as 0 then and the block's other rows are left as they were.
- * c = 0 likewise; any other c outside [2^-100, FLT_MAX] sets PKV_STATUS_BAD_SCALE and
+ * c = 0 likewise; any other c outside [2^-96, FLT_MAX] sets PKV_STATUS_BAD_SCALE and
  * counts as 0.  Tokens may come in any order; of several tokens with the same
  * slot the last one is stored.  The result does not depend on timing.
  *   workspace      device, >= pkv_kv_store_fp8_workspace_bytes(...) bytes,

@@ -55,7 +55,7 @@ def scale_for(amax: float) -> float:
 
 
 def usable(scale: float) -> bool:
-    return bool(2.0 ** -100 <= scale <= np.finfo(np.float32).max)
+    return bool(2.0 ** -96 <= scale <= np.finfo(np.float32).max)
 
 
 def kv_store(k, v, k_codes, v_codes, k_scale, v_scale, slot_mapping):

@@ -561,7 +561,7 @@ def _on(index, stream, call):
             raise ValueError(f"stream is on {stream.device}, expected cuda:{index}")
         with torch.cuda.stream(stream):                 # makes its device current too
             return call(stream.cuda_stream)
-    if torch.cuda.current_device() != index:
+    if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
             return call(torch._C._cuda_getCurrentRawStream(index))
     return call(torch._C._cuda_getCurrentRawStream(index))
@@ -585,28 +585,29 @@ def _desc(*shape) -> CacheDesc:
     return CacheDesc(*shape)
 
 
-class _Scratch:
-    """(address, bytes) of the caller's workspace, or of one that lives for the
-    call: taken from PyTorch's allocator on the call's stream and given back
-    behind the work enqueued there (no tensor is made for it, which would cost
-    as much as the call's launches)."""
+def _scratch(workspace, need, index, stream):
+    """(address, bytes, address to give back) of the caller's workspace, or of one
+    that lives for the call: taken from PyTorch's allocator on the call's stream
+    and given back, by _done, behind the work enqueued there (no tensor is made
+    for it, which would cost as much as the call's launches)."""
+    if workspace is not None:
+        return _at(workspace, "workspace", torch.uint8, index), workspace.numel(), None
+    if need == 0:
+        return None, 0, None
+    p = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
+    return p, need, p
 
-    def __init__(self, workspace, need, index, stream):
-        self.own = None
-        if workspace is not None:
-            self.at = _at(workspace, "workspace", torch.uint8, index), workspace.numel()
-        elif need == 0:
-            self.at = None, 0
-        else:
-            self.own = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, stream)
-            self.at = self.own, need
 
-    def __enter__(self):
-        return self.at
+def _done(scratch) -> None:
+    if scratch is not None:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
 
-    def __exit__(self, *exc):
-        if self.own is not None:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(self.own)
+
+@functools.lru_cache(maxsize=1024)
+def _need(name, *args) -> int:
+    """A workspace query (a pure function of the sizes); the last four arguments
+    are the cache's."""
+    return int(getattr(load(), name)(*args[:-4], CacheDesc(*args[-4:])))
 
 
 def _fp8_cache(k_cache, v_cache, k_scale, v_scale):
@@ -674,10 +675,14 @@ def kv_store_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, workspa
     st = _maybe(status, "status", torch.int32, index)
 
     def call(s):
-        need = lib.pkv_kv_store_fp8_workspace_bytes(n, desc)
-        with _Scratch(workspace, need, index, s) as ws:
-            _check(lib.pkv_kv_store_fp8(*rows, *cache, slots, n, *ws, desc, st, s),
+        need = 0 if workspace is not None else _need("pkv_kv_store_fp8_workspace_bytes", n,
+                                                     *k_cache.shape)
+        ws, size, own = _scratch(workspace, need, index, s)
+        try:
+            _check(lib.pkv_kv_store_fp8(*rows, *cache, slots, n, ws, size, desc, st, s),
                    "pkv_kv_store_fp8")
+        finally:
+            _done(own)
     _on(index, stream, call)
 
 
@@ -691,10 +696,14 @@ def _decode_fp8(name, q, k_cache, v_cache, k_scale, v_scale, block_tables, conte
 
     def call(s):
         o = _out_like(out, q, index)
-        need = lib.pkv_paged_decode_fp8_workspace_bytes(B, Hq, max_len, desc)
-        with _Scratch(workspace, need, index, s) as ws:
+        need = 0 if workspace is not None else _need("pkv_paged_decode_fp8_workspace_bytes", B, Hq,
+                                                     max_len, *k_cache.shape)
+        ws, size, own = _scratch(workspace, need, index, s)
+        try:
             _check(getattr(lib, name)(qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
-                                      o.data_ptr(), *ws, desc, st, s), name)
+                                      o.data_ptr(), ws, size, desc, st, s), name)
+        finally:
+            _done(own)
         return o
     return _on(index, stream, call)
 
@@ -773,11 +782,15 @@ def kv_store_paged_decode_fp8(k, v, slot_mapping, q, k_cache, v_cache, k_scale, 
 
     def call(s):
         o = _out_like(out, q, index)
-        need = lib.pkv_kv_store_paged_decode_fp8_workspace_bytes(n, B, Hq, max_len, desc)
-        with _Scratch(workspace, need, index, s) as ws:
+        need = 0 if workspace is not None else _need(
+            "pkv_kv_store_paged_decode_fp8_workspace_bytes", n, B, Hq, max_len, *k_cache.shape)
+        ws, size, own = _scratch(workspace, need, index, s)
+        try:
             _check(lib.pkv_kv_store_paged_decode_fp8(
                 *rows, slots, n, qp, *cache, bt, width, ctx, B, Hq, max_len, float(scale),
-                o.data_ptr(), *ws, desc, st, s), "pkv_kv_store_paged_decode_fp8")
+                o.data_ptr(), ws, size, desc, st, s), "pkv_kv_store_paged_decode_fp8")
+        finally:
+            _done(own)
         return o
     return _on(index, stream, call)
 
@@ -819,11 +832,15 @@ def paged_prefill_varlen_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, cu_seq
 
     def call(s):
         o = _out_like(out, q, index)
-        need = lib.pkv_paged_prefill_fp8_workspace_bytes(B, T, Hq, max_k, desc)
-        with _Scratch(workspace, need, index, s) as ws:
+        need = 0 if workspace is not None else _need("pkv_paged_prefill_fp8_workspace_bytes", B, T,
+                                                     Hq, max_k, *k_cache.shape)
+        ws, size, own = _scratch(workspace, need, index, s)
+        try:
             _check(lib.pkv_paged_prefill_varlen_fp8(
                 qp, *rows, *cache, cu_q, cu_k, B, T, max_q, max_k, Hq, bt, width, float(scale),
-                o.data_ptr(), *ws, desc, st, s), "pkv_paged_prefill_varlen_fp8")
+                o.data_ptr(), ws, size, desc, st, s), "pkv_paged_prefill_varlen_fp8")
+        finally:
+            _done(own)
         return o
     return _on(index, stream, call)
 
@@ -866,11 +883,10 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
             raise ValueError("token_ids must be [batch, max_tokens]")
         r.token_ids = _at(token_ids, "token_ids", i32, index)
         r.max_tokens = token_ids.shape[1]
-    per_row = (("prompt_lens", prompt_lens, i32), ("token_lens", token_lens, i32),
-               ("repetition_penalties", repetition_penalties, f32),
-               ("presence_penalties", presence_penalties, f32),
-               ("frequency_penalties", frequency_penalties, f32))
-    for name, t, dtype in per_row:
+    for name, t, dtype in (("prompt_lens", prompt_lens, i32), ("token_lens", token_lens, i32),
+                           ("repetition_penalties", repetition_penalties, f32),
+                           ("presence_penalties", presence_penalties, f32),
+                           ("frequency_penalties", frequency_penalties, f32)):
         if t is None:
             continue
         if token_ids is None:
@@ -878,9 +894,8 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
         if t.shape != (B,):
             raise ValueError(f"{name} must be [batch]")
         setattr(r, name, _at(t, name, dtype, index))
-    biases = (bias_offsets, bias_token_ids, bias_values)
-    if any(t is not None for t in biases):
-        if any(t is None for t in biases):
+    if not (bias_offsets is None and bias_token_ids is None and bias_values is None):
+        if bias_offsets is None or bias_token_ids is None or bias_values is None:
             raise ValueError("bias_offsets, bias_token_ids and bias_values go together")
         if bias_offsets.shape != (B + 1,) or bias_token_ids.dim() != 1 or \
                 bias_values.shape != bias_token_ids.shape:

@@ -36,6 +36,8 @@ struct DecodeArgs {
     // No plan in the workspace: the kernels take the schedule of a batch of at
     // most 32 sequences from `ctx` themselves (WarpPlan).
     int32_t inline_plan;
+    // The combine kernel: a row whose weights are NaN comes out as NaN (else as zeros).
+    int32_t keep_nan;
 };
 
 // The chunk schedule of at most 32 sequences, held by a warp: lane b has sequence

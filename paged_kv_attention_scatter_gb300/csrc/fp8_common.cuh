@@ -13,10 +13,10 @@ constexpr int kFp8MaxBlockSize = 1024;       // largest cache block (see kv_stor
 // for attention.
 constexpr int kScaleExpLo = -64, kScaleExpHi = 119;
 
-// A scale that attention can use.  The lower bound keeps 1 / scale, summed
-// over any number of keys, finite in fp32.
+// A scale that attention can use.  The lower bound keeps 2^8 / scale, summed
+// over 2^23 keys, finite in fp32.
 __device__ __forceinline__ bool scale_ok(float s) {
-    return s >= 7.888609052210118e-31f && s <= 3.4028234663852886e38f;   // [2^-100, max]
+    return s >= 0x1p-96f && s <= 3.4028234663852886e38f;
 }
 
 // Two e4m3 codes (low byte first) -> f16x2.  Exact: every e4m3 value is an f16.

@@ -42,6 +42,8 @@
 //    stalls the K/V stream.)
 //  * Keys past ctx_b are never loaded (their registers are zero and their
 //    scores -inf), so NaN in unused cache slots cannot reach the output.
+#include <math_constants.h>
+
 #include "decode_common.cuh"
 #include "prefill_common.cuh"
 
@@ -398,6 +400,7 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
     if (n == 0 && a.cu_q != nullptr) return;             // not a decode row of a varlen batch
     const int d0 = lane * E;
     float M = -INFINITY, L = 0.f, O[E];
+    bool nan = false;                        // a chunk's sum of weights is NaN
 #pragma unroll
     for (int e = 0; e < E; ++e) O[e] = 0.f;
     for (int32_t c0 = 0; c0 < n; c0 += kCombineBatch) {
@@ -428,7 +431,10 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
         }
         float mb = M;
 #pragma unroll
-        for (int c = 0; c < kCombineBatch; ++c) mb = fmaxf(mb, ml[c].x);
+        for (int c = 0; c < kCombineBatch; ++c) {
+            mb = fmaxf(mb, ml[c].x);
+            nan = nan || ml[c].y != ml[c].y;
+        }
         if (mb == -INFINITY) continue;                   // nothing visible yet
         const float r = (M == -INFINITY) ? 0.f : pkv::fast_exp2(M - mb);
         L *= r;
@@ -444,11 +450,13 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
         }
         M = mb;
     }
+    if (a.keep_nan && nan) L = CUDART_NAN_F;
+    const bool some = L > 0.f || (a.keep_nan && L != L);
     __nv_bfloat16* dst = a.out + (pkv::row_of(a, b) * a.Hq + h) * D + d0;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t*>(dst + e) =
-            pkv::pack_bf16(L > 0.f ? O[e] / L : 0.f, L > 0.f ? O[e + 1] / L : 0.f);
+            pkv::pack_bf16(some ? O[e] / L : 0.f, some ? O[e + 1] / L : 0.f);
 }
 
 template <typename... Args>
@@ -629,6 +637,7 @@ int make_plan_args(const int32_t* context_lens, int32_t batch, int32_t num_q_hea
     a.b0 = 0;
     a.wait_polls = pkv_wait_polls();
     a.inline_plan = 0;
+    a.keep_nan = 0;
     return PKV_OK;
 }
 

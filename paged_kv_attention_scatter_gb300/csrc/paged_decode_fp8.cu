@@ -47,6 +47,7 @@ int32_t choose_chunk_keys(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
 int launch_decode(Fp8DecodeArgs& fa, int head_dim, bool plan, cudaStream_t s) {
     int rc = PKV_OK;
     fa.d.inline_plan = plan && fa.d.B <= 32;
+    fa.d.keep_nan = 1;
     fa.no_combine = fa.d.max_ctx <= fa.d.chunk_keys;
     if (plan && !fa.d.inline_plan) rc = pkv_launch_decode_plan(fa.d, s);
     if (rc != PKV_OK) return rc;

@@ -590,7 +590,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 if (h >= meta.nh || dim < 0) continue;
                 const int64_t at = (int64_t)meta.row + meta.h0 + h;
                 if (meta.nch == 1) {
-                    a.out[at * D + dim] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
+                    a.out[at * D + dim] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
                 } else {
                     a.part_o[at * D + dim] = O;
                     if (dim == 0) a.part_ml[at] = make_float2(M, L);
@@ -710,6 +710,13 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             }
             mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
             mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+            // an infinite entry makes the head's weights NaN; e4m3 has no infinity, so
+            // it goes in as NaN
+            auto no_inf = [](uint32_t x) {
+                if ((x & 0x7fffu) == 0x7f80u) x |= 0x40u;
+                if ((x & 0x7fff0000u) == 0x7f800000u) x |= 0x400000u;
+                return x;
+            };
             // largest entry 1.f * 2^(E - 127) to 1.f * 2^7, where that power and its
             // inverse are normal fp32 numbers
             const int e = min(max(7 - ((int)(mag >> 7) - 127), -113), 113);
@@ -718,8 +725,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 #pragma unroll
             for (int i = 0; i < D / 8; i += 2) {
                 uint16_t a0, b0, a1, b1;
-                const uint32_t x = pkv::word(raw[i >> 2], i & 3);
-                const uint32_t z = pkv::word(raw[i >> 2], (i & 3) + 1);
+                const uint32_t x = no_inf(pkv::word(raw[i >> 2], i & 3));
+                const uint32_t z = no_inf(pkv::word(raw[i >> 2], (i & 3) + 1));
                 split_e4m3(pkv::pack_f16(__int_as_float((int)(x << 16)) * up16,
                                          __int_as_float((int)(x & 0xffff0000u)) * up16),
                            a0, b0);

@@ -179,7 +179,7 @@ def test_decode_is_the_oracles(cuda, lens, bs, hkv, group, d, arbitrary):
 
 
 @pytest.mark.parametrize("bs", [16, 64, 40])
-@pytest.mark.parametrize("q_mag,vexp", [(1e25, -60), (1e-30, 100), (3e4, 0), (1.0, -90)])
+@pytest.mark.parametrize("q_mag,vexp", [(1e25, -60), (1e-30, 100), (3e4, 0), (1.0, -86)])
 def test_decode_ranges(cuda, bs, q_mag, vexp):
     """Queries and scales far outside f16's range: only the products count."""
     pkv = U.lib()
@@ -194,6 +194,31 @@ def test_decode_ranges(cuda, bs, q_mag, vexp):
     out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda),
                                torch.tensor(lens, dtype=torch.int32, device=cuda), 0.125, 200)
     _check_decode(out, pool, q, 0.125)
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("most", [100, 5000])          # with and without a combine
+def test_decode_infinities_and_nan(cuda, bs, d, most):
+    """NaN or an infinity in a head's query: NaN for that head alone.  A NaN code in
+    a key that counts: NaN for its kv head; in a value: for that entry."""
+    pkv = U.lib()
+    rng = np.random.default_rng(19)
+    pool = F.Pool([most, 90], bs, 2, d, seed=4)
+    blk = int(pool.bt[1, 0])
+    pool.codes["k"][blk, 3, 0, 5] = 0x7F
+    pool.codes["v"][blk, 3, 1, 7] = 0xFF
+    q = F.bf16(rng, 2, 8, d)
+    ctx = torch.tensor([most, 90], dtype=torch.int32, device=cuda)
+    clean = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda), ctx, 0.125, most)
+    q[0, 1, 0], q[0, 2, 9], q[0, 6, d - 1] = math.inf, math.nan, -math.inf
+    out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda), ctx, 0.125, most)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[0, [1, 2, 6]] = True
+    bad[1, :4] = True                            # kv head 0
+    bad[1, 4:, 7] = True
+    assert torch.equal(torch.isnan(out), bad)
+    assert torch.equal(out[~bad], clean[~bad])
 
 
 @pytest.mark.parametrize("bs", [16, 64, 40])
