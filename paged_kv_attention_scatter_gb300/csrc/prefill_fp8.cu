@@ -35,6 +35,7 @@ struct ExpandArgs {
     __nv_bfloat16* vo;
     int32_t* table;                          // [sequences, rows_per_seq / kBlock]
     int32_t MB, NB, bs, Hkv, D, rows_per_seq;
+    int32_t vec_shift;                       // log2 of the vectors of a row, -1: not a power of two
 };
 
 __device__ __forceinline__ uint32_t to_bf16x2(uint32_t f16x2, float s) {
@@ -63,7 +64,12 @@ __global__ void __launch_bounds__(kThreads) expand_prefix_kernel(ExpandArgs e,
     const int32_t rows = min(lk - lq - r0, kChunkRows);
     if (rows <= 0) return;
     const int32_t vecs = e.Hkv * (e.D / 16);                  // 16-code vectors per row
-    const int32_t half = rows * vecs, per_head = e.D / 16;   // K's vectors, then V's
+    const int32_t half = rows * vecs;                         // K's vectors, then V's
+    const int head_shift = e.D == 128 ? 3 : 2;                // vectors of a head, log2
+    // a chunk of 16 rows lies in one cache block where the block size allows
+    const bool one_block = e.bs % kChunkRows == 0;
+    const int32_t blk0 = one_block ? __ldg(e.bt + (int64_t)b * e.MB + r0 / e.bs) : 0;
+    const int32_t off0 = r0 % e.bs;
     uint32_t bad = 0;
     // kBatch vectors a lane at once: a vector is three loads, of which the scale's
     // and the codes' addresses need the block id
@@ -75,9 +81,11 @@ __global__ void __launch_bounds__(kThreads) expand_prefix_kernel(ExpandArgs e,
         for (int u = 0; u < kBatch; ++u) {
             const int32_t i = i0 + u * kThreads;
             const int32_t j = i < half ? i : i - half;
-            row[u] = j / vecs;
+            row[u] = e.vec_shift >= 0 ? j >> e.vec_shift : j / vecs;
             col[u] = j - row[u] * vecs;
-            blk[u] = i < 2 * half ? __ldg(e.bt + (int64_t)b * e.MB + (r0 + row[u]) / e.bs) : -1;
+            blk[u] = i >= 2 * half ? -1
+                     : one_block   ? blk0
+                                   : __ldg(e.bt + (int64_t)b * e.MB + (r0 + row[u]) / e.bs);
             if (i < 2 * half && (unsigned)blk[u] >= (unsigned)e.NB) {
                 bad |= PKV_STATUS_BAD_BLOCK_ID;
                 blk[u] = -1;
@@ -89,9 +97,10 @@ __global__ void __launch_bounds__(kThreads) expand_prefix_kernel(ExpandArgs e,
             s[u] = 0.f;
             w[u] = make_uint4(0, 0, 0, 0);
             if (blk[u] < 0) continue;
-            s[u] = __ldg((is_v ? e.vs : e.ks) + (int64_t)blk[u] * e.Hkv + col[u] / per_head);
+            s[u] = __ldg((is_v ? e.vs : e.ks) + (int64_t)blk[u] * e.Hkv + (col[u] >> head_shift));
             w[u] = pkv::ld_stream16((is_v ? e.vc : e.kc) +
-                                    (((int64_t)blk[u] * e.bs + (r0 + row[u]) % e.bs) * vecs +
+                                    (((int64_t)blk[u] * e.bs +
+                                      (one_block ? off0 + row[u] : (r0 + row[u]) % e.bs)) * vecs +
                                      col[u]) * 16);
         }
 #pragma unroll
@@ -211,6 +220,8 @@ extern "C" int pkv_paged_prefill_varlen_fp8(
     c.e.Hkv = cache.num_kv_heads;
     c.e.D = cache.head_dim;
     c.e.rows_per_seq = (int32_t)L.rows_per_seq;
+    const int32_t vecs = cache.num_kv_heads * (cache.head_dim / 16);
+    c.e.vec_shift = (vecs & (vecs - 1)) == 0 ? __builtin_ctz((unsigned)vecs) : -1;
     const int64_t table_keys = (int64_t)max_blocks_per_seq * cache.block_size;
     a.kc = c.e.ko;
     a.vc = c.e.vo;
