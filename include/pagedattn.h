@@ -491,10 +491,11 @@ PKV_API int pkv_kv_store_paged_decode_fp8(
 
 /*
  * Bytes of device workspace pkv_paged_prefill_varlen_fp8 needs (pure host
- * function): the tile schedule and the prefixes' rows as bf16, the latter
- * sized for max_seqlen_k keys of every sequence, up to 4 GiB (beyond that the
- * batch is attended in groups of sequences that share it; a single sequence
- * may need more).
+ * function): the tile schedule, partial results where few queries' keys are
+ * split over several work items, and the prefixes' rows as bf16.  The latter are
+ * sized for max_seqlen_k keys of every sequence, up to 4 GiB; beyond that the
+ * batch is attended in groups of sequences that share it (a single sequence may
+ * need more).
  */
 PKV_API size_t pkv_paged_prefill_fp8_workspace_bytes(int32_t batch, int32_t total_q,
                                                      int32_t num_q_heads, int32_t max_seqlen_k,
@@ -507,8 +508,8 @@ PKV_API size_t pkv_paged_prefill_fp8_workspace_bytes(int32_t batch, int32_t tota
  * keys are the bf16 rows of k / v.  A prefix row in a block id outside the pool
  * (PKV_STATUS_BAD_BLOCK_ID) or with a scale that cannot be used
  * (PKV_STATUS_BAD_SCALE) counts as zeros.  A sequence of more than max_seqlen_k keys
- * or more cached keys than its table holds sets PKV_STATUS_BAD_SEQLENS and,
- * where its prefix does not fit, is skipped.
+ * or more cached keys than its table holds sets PKV_STATUS_BAD_SEQLENS and is
+ * skipped (its output rows are not written), as an inconsistent one is.
  */
 PKV_API int pkv_paged_prefill_varlen_fp8(
     const void* q, const void* k, const void* v, const void* k_cache, const void* v_cache,

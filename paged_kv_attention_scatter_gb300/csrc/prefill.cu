@@ -43,6 +43,11 @@ __device__ __forceinline__ void load_lengths(const PrefillArgs& a, int32_t base,
     s_lk[threadIdx.x] = lk;
 }
 
+// Key tiles of split s of a q tile with `tiles` of them.
+__device__ __forceinline__ int32_t split_cost(const PrefillArgs& a, int32_t tiles, int32_t s) {
+    return min(min(a.split_tiles, tiles - s * a.split_tiles), kBins - 1);
+}
+
 // One CTA: the (sequence, q tile) list ordered by decreasing number of key
 // tiles (a counting sort), so the longest tiles start first.  Each pass reads
 // the lengths of up to 1024 sequences at once, then a warp takes a sequence
@@ -69,11 +74,18 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(PrefillArgs 
             const int32_t c = lk - lq;
             const int32_t nt = (lq + a.tile_m - 1) / a.tile_m;
             for (int32_t m = lane; m < nt; m += 32) {
+                if (a.split_tiles > 0) {
+                    const int32_t tiles = pkv::key_tiles(c, m), ns = pkv::key_splits(a, tiles);
+                    for (int32_t s = 0; s < ns; ++s)
+                        atomicAdd(&hist[kBins - 1 - split_cost(a, tiles, s)], 1);
+                    atomicAdd(&total, ns);
+                    continue;
+                }
                 const int32_t lim = min(lk, c + (m + 1) * a.tile_m);
                 const int32_t cost = min((lim + a.tile_n - 1) / a.tile_n, kBins - 1);
                 atomicAdd(&hist[kBins - 1 - cost], 1);
             }
-            if (lane == 0) atomicAdd(&total, nt);
+            if (lane == 0 && a.split_tiles == 0) atomicAdd(&total, nt);
         }
         __syncthreads();
     }
@@ -122,6 +134,16 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(PrefillArgs 
             const int32_t c = lk - lq;
             const int32_t nt = (lq + a.tile_m - 1) / a.tile_m;
             for (int32_t m = lane; m < nt; m += 32) {
+                if (a.split_tiles > 0) {
+                    const int32_t tiles = pkv::key_tiles(c, m), ns = pkv::key_splits(a, tiles);
+                    for (int32_t s = 0; s < ns; ++s) {
+                        const int32_t pos =
+                            atomicAdd(&hist[kBins - 1 - split_cost(a, tiles, s)], 1);
+                        if (pos < a.max_tiles) a.tiles[pos] = make_int2(base + i, m | s << 16);
+                        else overflow = true;
+                    }
+                    continue;
+                }
                 const int32_t lim = min(lk, c + (m + 1) * a.tile_m);
                 const int32_t cost = min((lim + a.tile_n - 1) / a.tile_n, kBins - 1);
                 const int32_t pos = atomicAdd(&hist[kBins - 1 - cost], 1);
@@ -241,6 +263,10 @@ int pkv_prefill_make_args(const void* q, const void* k, const void* v, const voi
     a.skip_single = 0;
     a.wait_polls = pkv_wait_polls();
     a.max_cached = INT32_MAX;
+    a.skip_long = 0;
+    a.split_tiles = 0;
+    a.part_o = nullptr;
+    a.part_ml = nullptr;
     return PKV_OK;
 }
 

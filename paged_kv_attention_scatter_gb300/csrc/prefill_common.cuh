@@ -27,7 +27,22 @@ struct PrefillArgs {
     int32_t skip_single;             // sequences of one query are left to the decode kernels
     uint32_t wait_polls;             // polls of a bounded mbarrier wait
     int32_t max_cached;              // cached keys a sequence may have, whatever its table holds
+    int32_t skip_long;               // a sequence of more than max_sk keys is inconsistent
+    // Few q tiles over many keys: a tile's keys in splits of split_tiles key tiles,
+    // each a work item of its own with partial results, merged by a combine kernel
+    // (0: no splits).  The list's entries are (sequence, q tile | split << 16).
+    int32_t split_tiles;
+    float* part_o;                   // [splits, total_q, Hq, D], unnormalised
+    float2* part_ml;                 // [splits, total_q, Hq]: (max, sum) in base 2
 };
+
+// Key tiles and splits of q tile m of a sequence with c cached keys.
+__device__ __forceinline__ int32_t key_tiles(int32_t c, int32_t m) {
+    return (c + kPrefillTileK - 1) / kPrefillTileK + m + 1;
+}
+__device__ __forceinline__ int32_t key_splits(const PrefillArgs& a, int32_t tiles) {
+    return a.split_tiles > 0 ? (tiles + a.split_tiles - 1) / a.split_tiles : 1;
+}
 
 // Lengths of sequence b; returns false (and reports) when they are inconsistent.
 __device__ __forceinline__ bool seq_lengths(const PrefillArgs& a, int32_t b, int32_t& q0,
@@ -37,6 +52,7 @@ __device__ __forceinline__ bool seq_lengths(const PrefillArgs& a, int32_t b, int
     lk = a.cu_k[b + 1] - a.cu_k[b];
     const int32_t c = lk - lq;
     bool ok = lq >= 0 && c >= 0 && q0 >= 0 && q0 + lq <= a.total_q;
+    if (a.skip_long) ok = ok && lk <= a.max_sk;
     if (c > 0)
         ok = ok && a.bt != nullptr && (int64_t)(c + a.bs - 1) / a.bs <= a.MB && c <= a.max_cached;
     if (!ok && report_bad) report(a.status, PKV_STATUS_BAD_SEQLENS);

@@ -14,6 +14,12 @@
 // per prefix entry (1 read, 2 written), most of which the attention then finds
 // in L2.  Batches whose prefixes would exceed kExpandBytes run in groups of
 // sequences, one after another over the same workspace.
+//
+// A chunk of few queries on a long prefix has few (q tile, head) work items, each
+// a serial walk over its key tiles.  Where they could not fill the GPU, a tile's
+// keys are split into work items of their own, whose partial results a combine
+// kernel merges (3 chunks of 20..301 queries on 500..6000 cached keys, 16 heads:
+// 40 us for the attention without splits).
 #include "fp8_common.cuh"
 #include "prefill_common.cuh"
 
@@ -128,14 +134,93 @@ __global__ void __launch_bounds__(kThreads) expand_prefix_kernel(ExpandArgs e,
     if (bad) pkv::report(p.status, bad);
 }
 
+// CTA r: query row r, a warp a head at a time: merges the row's splits.  Rows of
+// unsplit tiles are the attention kernel's.
+constexpr int kCombineWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kCombineWarps * 32) combine_splits_kernel(pkv::PrefillArgs p) {
+    constexpr int E = D / 32;
+    __shared__ int32_t owner;                // sequence whose row this is
+    const int32_t r = blockIdx.x;
+    if (threadIdx.x == 0) owner = -1;
+    __syncthreads();
+    int32_t q0, lq, lk;
+    for (int32_t b = threadIdx.x; b < p.B; b += kCombineWarps * 32)
+        if (pkv::seq_lengths(p, b, q0, lq, lk, false) && r >= q0 && r < q0 + lq) owner = b;
+    __syncthreads();
+    if (owner < 0) return;
+    pkv::seq_lengths(p, owner, q0, lq, lk, false);
+    const int32_t n = pkv::key_splits(p, pkv::key_tiles(lk - lq, (r - q0) / pkv::kPrefillTileQ));
+    if (n == 1) return;
+    pkv::wait_for_predecessor();             // the attention kernel's partial results
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int32_t h = warp; h < p.Hq; h += kCombineWarps) {
+        const int64_t at = (int64_t)r * p.Hq + h, step = (int64_t)p.total_q * p.Hq;
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int32_t s = 0; s < n; ++s) M = fmaxf(M, p.part_ml[at + s * step].x);
+        const float use = M == -INFINITY ? 0.f : M;
+        float L = 0.f, O[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] = 0.f;
+#pragma unroll 4
+        for (int32_t s = 0; s < n; ++s) {
+            const float2 ml = p.part_ml[at + s * step];
+            const float f = pkv::fast_exp2(ml.x - use);
+            L = fmaf(ml.y, f, L);
+            const float* o = p.part_o + (at + s * step) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 v = *reinterpret_cast<const float2*>(o + e);
+                O[e] = fmaf(v.x, f, O[e]);
+                O[e + 1] = fmaf(v.y, f, O[e + 1]);
+            }
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;           // as for unsplit rows
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(p.out + at * D + lane * E + e) =
+                pkv::pack_bf16(O[e] * inv, O[e + 1] * inv);
+    }
+}
+
+template <int D>
+int launch_combine(const pkv::PrefillArgs& p, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.total_q, 1, 1);
+    cfg.blockDim = dim3(kCombineWarps * 32, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_splits_kernel<D>, p) == cudaSuccess ? PKV_OK
+                                                                                : PKV_ERR_CUDA;
+}
+
 struct Fp8PrefillLayout {
     int64_t rows_per_seq;
     int32_t group;                           // sequences attended at once
-    size_t off_table, off_k, off_v, total;
+    int32_t split_tiles, max_tiles;          // key tiles of a split (0: none); list entries
+    size_t off_table, off_tiles, off_ml, off_o, off_k, off_v, total;
 };
 
-Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t max_seqlen_k,
-                                    const pkv_cache_desc& c) {
+constexpr int kSms = 152;
+
+// Key tiles of a split, 0 for none: where the (q tile, head) items, at most
+// `items`, could leave SMs idle at the end (fewer than two a SM), the length
+// that gives about four items a SM if every one of them had all `key_tiles`.
+int32_t choose_split(int64_t items, int64_t key_tiles) {
+    if (items >= 2 * kSms) return 0;
+    int64_t split = (items * key_tiles + 4 * kSms - 1) / (4 * kSms);
+    if (split < 4) split = 4;
+    return split < key_tiles ? (int32_t)split : 0;
+}
+
+Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t num_q_heads,
+                                    int32_t max_seqlen_k, const pkv_cache_desc& c) {
     Fp8PrefillLayout L{};
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
     L.rows_per_seq = ((int64_t)max_seqlen_k + kBlock) / kBlock * kBlock;
@@ -146,7 +231,18 @@ Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t max_
     if (group < 1) group = 1;
     L.group = (int32_t)group;
     L.off_table = align(pkv_prefill_layout(batch, total_q).total);
-    L.off_k = align(L.off_table + sizeof(int32_t) * (size_t)(group * (L.rows_per_seq / kBlock)));
+    L.off_tiles = align(L.off_table + sizeof(int32_t) * (size_t)(group * (L.rows_per_seq / kBlock)));
+    // a sequence's cached and own keys together are max_seqlen_k at most, each part
+    // rounded up to tiles
+    const int64_t tiles = pkv_prefill_layout(batch, total_q).max_tiles;
+    const int64_t key_tiles = L.rows_per_seq / kBlock + 1;
+    L.split_tiles = choose_split(tiles * num_q_heads, key_tiles);
+    const int64_t splits = L.split_tiles > 0 ? (key_tiles + L.split_tiles - 1) / L.split_tiles : 0;
+    L.max_tiles = (int32_t)(tiles * splits);
+    const size_t rows = (size_t)splits * total_q * num_q_heads;
+    L.off_ml = align(L.off_tiles + sizeof(int2) * (size_t)L.max_tiles);
+    L.off_o = align(L.off_ml + sizeof(float2) * rows);
+    L.off_k = align(L.off_o + sizeof(float) * rows * c.head_dim);
     L.off_v = align(L.off_k + (size_t)(group * L.rows_per_seq * row * 2));
     // 256 bytes more: the workspace is 16-byte aligned, the rows are written by 32
     L.total = align(L.off_v + (size_t)(group * L.rows_per_seq * row * 2)) + 256;
@@ -174,11 +270,10 @@ extern "C" size_t pkv_paged_prefill_fp8_workspace_bytes(int32_t batch, int32_t t
                                                         int32_t num_q_heads,
                                                         int32_t max_seqlen_k,
                                                         pkv_cache_desc cache) {
-    (void)num_q_heads;
-    if (batch < 0 || total_q < 0 || max_seqlen_k < 0 || cache.num_kv_heads <= 0 ||
+    if (batch < 0 || total_q < 0 || num_q_heads <= 0 || max_seqlen_k < 0 || cache.num_kv_heads <= 0 ||
         cache.head_dim <= 0)
         return 0;
-    return fp8_prefill_layout(batch, total_q, max_seqlen_k, cache).total;
+    return fp8_prefill_layout(batch, total_q, num_q_heads, max_seqlen_k, cache).total;
 }
 
 extern "C" int pkv_paged_prefill_varlen_fp8(
@@ -201,7 +296,8 @@ extern "C" int pkv_paged_prefill_varlen_fp8(
     if (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3) return PKV_ERR_MISALIGNED;
     if (cache.block_size > pkv::kFp8MaxBlockSize) return PKV_ERR_BAD_DIMENSION;
     if ((int64_t)cache.num_blocks * cache.block_size >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
-    const Fp8PrefillLayout L = fp8_prefill_layout(batch, total_q, max_seqlen_k, cache);
+    const Fp8PrefillLayout L =
+        fp8_prefill_layout(batch, total_q, num_q_heads, max_seqlen_k, cache);
     if (workspace_bytes < L.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
     if (L.group * L.rows_per_seq >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
     char* ws = (char*)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
@@ -229,6 +325,14 @@ extern "C" int pkv_paged_prefill_varlen_fp8(
     a.MB = (int32_t)(L.rows_per_seq / kBlock);
     a.bs = kBlock;
     a.max_cached = table_keys < INT32_MAX ? (int32_t)table_keys : INT32_MAX;
+    a.skip_long = 1;                         // the workspace has no room for such a sequence
+    if (L.split_tiles > 0) {
+        a.split_tiles = L.split_tiles;
+        a.tiles = (int2*)(ws + L.off_tiles);
+        a.max_tiles = L.max_tiles;
+        a.part_ml = (float2*)(ws + L.off_ml);
+        a.part_o = (float*)(ws + L.off_o);
+    }
     const PrefillPrologue pre{enqueue_expand, &c};
     for (int32_t b0 = 0; b0 < batch; b0 += L.group) {
         c.sequences = batch - b0 < L.group ? batch - b0 : L.group;
@@ -240,6 +344,8 @@ extern "C" int pkv_paged_prefill_varlen_fp8(
         sub.NB = (int32_t)(c.sequences * (L.rows_per_seq / kBlock));
         c.p = sub;
         rc = pkv_prefill_launch(sub, cache.head_dim, s, &pre);
+        if (rc == PKV_OK && L.split_tiles > 0)
+            rc = cache.head_dim == 128 ? launch_combine<128>(sub, s) : launch_combine<64>(sub, s);
         if (rc != PKV_OK) return rc;
     }
     return PKV_OK;

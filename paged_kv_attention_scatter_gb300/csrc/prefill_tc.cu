@@ -126,15 +126,17 @@ struct TcMaps {
 
 struct Item {
     int32_t b, m, h, q0, lq, lk, c, n_cached, n_tiles, rows;
+    int32_t first, end, split, splits;   // its key tiles [first, end); split of splits
 };
 
+template <bool kSplit>
 __device__ __forceinline__ Item item_at(const PrefillArgs& a, int64_t it) {
     Item x;
     const int32_t tile = (int32_t)(it / a.Hq);
     x.h = (int32_t)(it - (int64_t)tile * a.Hq);
     const int2 tm = a.tiles[tile];
     x.b = tm.x;
-    x.m = tm.y;
+    x.m = kSplit ? tm.y & 0xffff : tm.y;
     x.q0 = a.cu_q[x.b];
     x.lq = a.cu_q[x.b + 1] - x.q0;
     x.lk = a.cu_k[x.b + 1] - a.cu_k[x.b];
@@ -142,6 +144,16 @@ __device__ __forceinline__ Item item_at(const PrefillArgs& a, int64_t it) {
     x.n_cached = (x.c + kBN - 1) / kBN;
     x.n_tiles = x.n_cached + x.m + 1;
     x.rows = min(kBM, x.lq - x.m * kBM);
+    x.first = 0;
+    x.end = x.n_tiles;
+    x.split = 0;
+    x.splits = 1;
+    if constexpr (kSplit) {
+        x.split = tm.y >> 16;
+        x.splits = pkv::key_splits(a, x.n_tiles);
+        x.first = x.split * a.split_tiles;
+        x.end = min(x.n_tiles, x.first + a.split_tiles);
+    }
     return x;
 }
 
@@ -316,7 +328,7 @@ __device__ __forceinline__ void mbar_expect_tx_only(uint64_t* bar, uint32_t byte
                  : "memory");
 }
 
-template <int D, int kLoad, bool kPolls>
+template <int D, int kLoad, bool kPolls, bool kSplit = false>
 __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
         const __grid_constant__ TcMaps maps, const PrefillArgs a) {
     constexpr bool kGather = kLoad != kLoadTile;  // the producer warps' lanes gather
@@ -415,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                 if (!(ok = next_item(s, I, it, polls, true))) break;
                 if (it < 0) break;
             }
-            const Item x = item_at(a, it);
+            const Item x = item_at<kSplit>(a, it);
             const int32_t kvh = x.h / a.G;
             if (k_side) {
                 if (I > 0 && !(ok = warp_wait(&s.q_free, (I - 1) & 1, &s.abort_flag, polls)))
@@ -428,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                 }
                 ++q_issued;
             }
-            for (int32_t j = 0; j < x.n_tiles; ++j, ++T) {
+            for (int32_t j = x.first; j < x.end; ++j, ++T) {
                 const int st = T % kStages;
                 const uint32_t use = T / kStages;
                 if (use > 0 && !(ok = warp_wait(&empty[st], (use - 1) & 1, &s.abort_flag, polls)))
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                 s.item_ring[qs] = it < n_items ? it : -1;
                 mbar_arrive(&s.item_full[qs]);
                 if (it >= n_items) break;
-                const Item x = item_at(a, it);
+                const Item x = item_at<kSplit>(a, it);
                 const int32_t kvh = x.h / a.G;
                 if (I > 0 && !(ok = mbar_wait(&s.q_free, (I - 1) & 1,
                         &s.abort_flag, polls))) break;
@@ -554,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                     tma_load_3d(s.q + hf * kHalf, &maps.q, &s.q_full, hf * 64, x.h,
                                 x.q0 + x.m * kBM);
                 ++q_issued;
-                for (int32_t j = 0; j < x.n_tiles; ++j, ++T) {
+                for (int32_t j = x.first; j < x.end; ++j, ++T) {
                     const int st = T % kStages;
                     const uint32_t use = T / kStages;
                     if (use > 0 && !(ok = mbar_wait(&s.k_empty[st], (use - 1) & 1,
@@ -581,9 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                 int32_t it = -1;
                 if (!(ok = next_item(s, I, it, polls))) break;
                 if (it < 0) break;
-                const Item x = item_at(a, it);
+                const Item x = item_at<kSplit>(a, it);
                 const int32_t kvh = x.h / a.G;
-                for (int32_t j = 0; j < x.n_tiles; ++j, ++T) {
+                for (int32_t j = x.first; j < x.end; ++j, ++T) {
                     const int st = T % kStages;
                     const uint32_t use = T / kStages;
                     if (use > 0 && !(ok = mbar_wait(&s.v_empty[st], (use - 1) & 1,
@@ -613,11 +625,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                 int32_t it = -1;
                 if (!(ok = next_item(s, I, it, polls))) break;
                 if (it < 0) break;
-                const Item x = item_at(a, it);
+                const Item x = item_at<kSplit>(a, it);
                 if (warp == 5) {
                     if (!(ok = mbar_wait(&s.q_full, I & 1, &s.abort_flag, polls))) break;
-                    for (int32_t j = 0; j < x.n_tiles; ++j) {
-                        const uint32_t t = T + j;
+                    for (int32_t j = x.first; j < x.end; ++j) {
+                        const uint32_t t = T + (j - x.first);
                         const int st = t % kStages;
                         if (!(ok = mbar_wait(&s.k_full[st], (t / kStages) & 1,
                                 &s.abort_flag, polls))) break;
@@ -640,12 +652,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                     if (!ok) break;
                     umma_commit(&s.q_free);              // every Q K^T of the item issued
                 } else {
-                    for (int32_t j = 0; j < x.n_tiles; ++j) {
-                        const uint32_t t = T + j;
+                    for (int32_t j = x.first; j < x.end; ++j) {
+                        const uint32_t t = T + (j - x.first);
                         const int st = t % kStages;
                         if (!(ok = mbar_wait(&s.p_full[st], (t / kStages) & 1,
                                 &s.abort_flag, polls))) break;
-                        if (j == 0 && I > 0 && !(ok = mbar_wait(&s.o_free, (I - 1) & 1,
+                        if (j == x.first && I > 0 && !(ok = mbar_wait(&s.o_free, (I - 1) & 1,
                                 &s.abort_flag, polls)))
                             break;
                         if (!(ok = mbar_wait(&s.v_full[st], (t / kStages) & 1,
@@ -653,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                         tc_fence_after();
                         const uint64_t vd = vd0 + (uint64_t)(st * (kTile >> 4));
                         const uint32_t a_p = tmem + kColS0 + st * kBN;
-                        const uint32_t acc0 = j > 0 ? 1u : 0u;
+                        const uint32_t acc0 = j > x.first ? 1u : 0u;
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
                             umma_bf16_tmem_a(tmem + kColO, a_p + kk * 8, vd + (kk * 2048 >> 4), id_pv,
@@ -663,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                     }
                     if (!ok) break;
                 }
-                T += x.n_tiles;
+                T += x.end - x.first;
             }
             if (!ok) give_up(s, a.status);
             // every MMA of both issuers has finished before TMEM is freed
@@ -680,10 +692,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
             int32_t it = -1;
             if (!(ok = next_item(s, I, it, polls, true))) break;
             if (it < 0) break;
-            const Item x = item_at(a, it);
+            const Item x = item_at<kSplit>(a, it);
             float m_run = -INFINITY, l_run = 0.f;
-            for (int32_t j = 0; j < x.n_tiles && ok; ++j) {
-                const uint32_t t = T + j;
+            for (int32_t j = x.first; j < x.end && ok; ++j) {
+                const uint32_t t = T + (j - x.first);
                 const int st = t % kStages;
                 const uint32_t s_col = lane_base + kColS0 + st * kBN;
                 if (!(ok = warp_wait(&s.s_full[st], (t / kStages) & 1,
@@ -739,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                 // (rare: the maximum grew by more than 2^9) is the tile's
                 // maximum taken and P recomputed.  The first tile of an item
                 // takes the maximum first.
-                bool redo = j == 0;
+                bool redo = j == x.first;
                 if (!redo) {
                     exp_pass(-m_run);
                     const float lt = (ls[0] + ls[1]) + (ls[2] + ls[3]);
@@ -767,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                         m_run = mx;
                         l_run *= alpha;
                     }
-                    if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                    if (j > x.first && __any_sync(0xffffffffu, raise)) {
                         // O may only be rescaled once the previous P V has finished
                         const uint32_t tp = t - 1;
                         if (!(ok = warp_wait(&s.pv_done[tp % kStages], (tp / kStages) & 1,
@@ -808,11 +820,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
             }
             if (!ok) break;
             // ---- epilogue: O / l to global ----
-            const uint32_t tl = T + x.n_tiles - 1;
+            const uint32_t tl = T + (x.end - x.first) - 1;
             if (!(ok = warp_wait(&s.pv_done[tl % kStages], (tl / kStages) & 1,
                     &s.abort_flag, polls)))
                 break;
             tc_fence_after();
+            if constexpr (kSplit) {
+                if (x.splits > 1) {
+                    // this split's share, for the combine kernel
+                    const int64_t at = ((int64_t)x.split * a.total_q + x.q0 + x.m * kBM + i) * a.Hq +
+                                       x.h;
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        float ov[32];
+                        tmem_ld32(lane_base + kColO + cc * 32, ov);
+                        tmem_wait_ld();
+                        if (i >= x.rows) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w8[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w8[k] = __float_as_uint(ov[e + k]);
+                            st_global_32b(a.part_o + at * D + cc * 32 + e, w8);
+                        }
+                    }
+                    if (i < x.rows) a.part_ml[at] = make_float2(m_run, l_run);
+                    tc_fence_before();
+                    mbar_arrive(&s.o_free);
+                    T += x.end - x.first;
+                    continue;
+                }
+            }
             const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
             __nv_bfloat16* orow = a.out + ((int64_t)(x.q0 + x.m * kBM + i) * a.Hq + x.h) * D;
             // a row is 32-byte aligned when `out` is (rows are D*2 bytes):
@@ -851,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
             }
             tc_fence_before();
             mbar_arrive(&s.o_free);
-            T += x.n_tiles;
+            T += x.end - x.first;
         }
         if (!ok) give_up(s, a.status);
     }
@@ -896,12 +934,17 @@ int launch_tc(PrefillArgs& a, const TcMaps& maps, cudaStream_t s, const PrefillP
         {prefill_tc_kernel<D, kLoadGather, false>, prefill_tc_kernel<D, kLoadGather, true>},
         {prefill_tc_kernel<D, kLoadSplit64, false>, prefill_tc_kernel<D, kLoadSplit64, true>},
         {prefill_tc_kernel<D, kLoadSplit96, false>, prefill_tc_kernel<D, kLoadSplit96, true>}};
+    // splits come with tile boxes only (their caller lays the cache out for them)
+    static const Kernel split_kernels[2] = {prefill_tc_kernel<D, kLoadTile, false, true>,
+                                            prefill_tc_kernel<D, kLoadTile, true, true>};
     const int smem = (int)sizeof(TcSmem<D>) + 1024;
     const int mode = load_mode(a);
     const int custom = a.wait_polls != (uint32_t)PKV_DEFAULT_WAIT_POLLS ? 1 : 0;
-    const Kernel kernel = kernels[mode][custom];
-    static std::atomic<uint64_t> configured[8];
-    if (!pkv_dynamic_smem_once((const void*)kernel, smem, configured[mode * 2 + custom]))
+    const bool split = a.split_tiles > 0 && mode == kLoadTile;
+    const Kernel kernel = split ? split_kernels[custom] : kernels[mode][custom];
+    static std::atomic<uint64_t> configured[10];
+    if (!pkv_dynamic_smem_once((const void*)kernel, smem,
+                               configured[split ? 8 + custom : mode * 2 + custom]))
         return PKV_ERR_CUDA;
     a.tile_m = kBM;
     a.tile_n = kBN;
