@@ -493,9 +493,10 @@ PKV_API int pkv_kv_store_paged_decode_fp8(
  * Bytes of device workspace pkv_paged_prefill_varlen_fp8 needs (pure host
  * function): the tile schedule, partial results where few queries' keys are
  * split over several work items, and the prefixes' rows as bf16.  The latter are
- * sized for max_seqlen_k keys of every sequence, up to 4 GiB; beyond that the
+ * sized for max_seqlen_k keys of every sequence, up to 4.1 GB; beyond that the
  * batch is attended in groups of sequences that share it (a single sequence may
- * need more).
+ * need more).  The answer grows with batch, total_q and max_seqlen_k: a workspace
+ * for the largest call serves the smaller ones.
  */
 PKV_API size_t pkv_paged_prefill_fp8_workspace_bytes(int32_t batch, int32_t total_q,
                                                      int32_t num_q_heads, int32_t max_seqlen_k,

@@ -19,7 +19,7 @@
 // a serial walk over its key tiles.  Where they could not fill the GPU, a tile's
 // keys are split into work items of their own, whose partial results a combine
 // kernel merges (3 chunks of 20..301 queries on 500..6000 cached keys, 16 heads:
-// 40 us for the attention without splits).
+// 40 us for the attention without splits, 22 with them).
 #include "fp8_common.cuh"
 #include "prefill_common.cuh"
 
@@ -29,7 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kChunkRows = 16;               // prefix rows per CTA
 constexpr int kBatch = 4;                    // vectors a lane has in flight
 constexpr int kBlock = 128;                  // rows per workspace cache block
-constexpr int64_t kExpandBytes = 4LL << 30;  // K and V rows of a group, where >= 1 fits
+constexpr int64_t kExpandBytes = 4100000000; // K and V rows of a group, where >= 1 fits
 
 struct ExpandArgs {
     const uint8_t* kc;
@@ -149,11 +149,13 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_splits_kernel(pkv:
     for (int32_t b = threadIdx.x; b < p.B; b += kCombineWarps * 32)
         if (pkv::seq_lengths(p, b, q0, lq, lk, false) && r >= q0 && r < q0 + lq) owner = b;
     __syncthreads();
+    // the attention kernel's partial results; every CTA waits, so that this grid
+    // never ends before that one
+    pkv::wait_for_predecessor();
     if (owner < 0) return;
     pkv::seq_lengths(p, owner, q0, lq, lk, false);
     const int32_t n = pkv::key_splits(p, pkv::key_tiles(lk - lq, (r - q0) / pkv::kPrefillTileQ));
     if (n == 1) return;
-    pkv::wait_for_predecessor();             // the attention kernel's partial results
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int32_t h = warp; h < p.Hq; h += kCombineWarps) {
         const int64_t at = (int64_t)r * p.Hq + h, step = (int64_t)p.total_q * p.Hq;
@@ -209,14 +211,17 @@ struct Fp8PrefillLayout {
 
 constexpr int kSms = 152;
 
-// Key tiles of a split, 0 for none: where the (q tile, head) items, at most
-// `items`, could leave SMs idle at the end (fewer than two a SM), the length
-// that gives about four items a SM if every one of them had all `key_tiles`.
+// Key tiles of a split, 0 for none: as many splits of a tile's keys as bring the
+// (q tile, head) items, at most `items`, to two an SM, but none under 16 tiles: a
+// split's start and end, its partial rows and the combine cost about as much as
+// eight (measured, us, unsplit and at 4, 8, 14, 20 tiles: 64 queries of 32 heads on
+// 8000 cached keys 58, 54, 41, 40, 36; 200 on 2000 25, 33, 28, 28, 26; two chunks of
+// 100 on 1000 18, 25, 25, 20, 20).
 int32_t choose_split(int64_t items, int64_t key_tiles) {
-    if (items >= 2 * kSms) return 0;
-    int64_t split = (items * key_tiles + 4 * kSms - 1) / (4 * kSms);
-    if (split < 4) split = 4;
-    return split < key_tiles ? (int32_t)split : 0;
+    if (items <= 0) return 0;
+    int64_t splits = (2 * kSms + items - 1) / items;
+    if (splits > key_tiles / 16) splits = key_tiles / 16;
+    return splits < 2 ? 0 : (int32_t)((key_tiles + splits - 1) / splits);
 }
 
 Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t num_q_heads,
@@ -225,13 +230,22 @@ Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t num_
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
     L.rows_per_seq = ((int64_t)max_seqlen_k + kBlock) / kBlock * kBlock;
     const int64_t row = (int64_t)c.num_kv_heads * c.head_dim;
-    int64_t group = kExpandBytes / (L.rows_per_seq * row * 4);
+    if ((double)L.rows_per_seq * row * 4 > 0x1p60) {         // more than any memory
+        L.total = SIZE_MAX;
+        return L;
+    }
+    const int64_t seq_bytes = L.rows_per_seq * row * 4;      // K and V as bf16
+    int64_t group = kExpandBytes / seq_bytes;
     if (group > batch) group = batch;
     if (group > 65535) group = 65535;        // the expanding grid's y extent
     if (group < 1) group = 1;
     L.group = (int32_t)group;
     L.off_table = align(pkv_prefill_layout(batch, total_q).total);
-    L.off_tiles = align(L.off_table + sizeof(int32_t) * (size_t)(group * (L.rows_per_seq / kBlock)));
+    // The sizes reserved below grow with every argument, so that a workspace for the
+    // largest call holds the smaller ones; the group and the splits do not.
+    int64_t kv_bytes = kExpandBytes > seq_bytes ? kExpandBytes : seq_bytes;
+    if (kv_bytes / seq_bytes >= batch) kv_bytes = batch * seq_bytes;
+    L.off_tiles = align(L.off_table + sizeof(int32_t) * (size_t)(kv_bytes / (row * 4 * kBlock) + 1));
     // a sequence's cached and own keys together are max_seqlen_k at most, each part
     // rounded up to tiles
     const int64_t tiles = pkv_prefill_layout(batch, total_q).max_tiles;
@@ -239,13 +253,19 @@ Fp8PrefillLayout fp8_prefill_layout(int32_t batch, int32_t total_q, int32_t num_
     L.split_tiles = choose_split(tiles * num_q_heads, key_tiles);
     const int64_t splits = L.split_tiles > 0 ? (key_tiles + L.split_tiles - 1) / L.split_tiles : 0;
     L.max_tiles = (int32_t)(tiles * splits);
-    const size_t rows = (size_t)splits * total_q * num_q_heads;
-    L.off_ml = align(L.off_tiles + sizeof(int2) * (size_t)L.max_tiles);
-    L.off_o = align(L.off_ml + sizeof(float2) * rows);
-    L.off_k = align(L.off_o + sizeof(float) * rows * c.head_dim);
-    L.off_v = align(L.off_k + (size_t)(group * L.rows_per_seq * row * 2));
+    // splits * items < 2 * kSms + items where there are any, and items < 2 * kSms
+    int64_t items = tiles * num_q_heads;
+    if (items > 2 * kSms) items = 2 * kSms;
+    int64_t rows = kBlock * (2 * kSms + items);
+    const double most = (double)(key_tiles / 16) * num_q_heads * total_q;
+    if (most < (double)rows) rows = (int64_t)most;
+    if (key_tiles < 32) rows = 0;
+    L.off_ml = align(L.off_tiles + sizeof(int2) * 4 * kSms);
+    L.off_o = align(L.off_ml + sizeof(float2) * (size_t)rows);
+    L.off_k = align(L.off_o + sizeof(float) * (size_t)rows * c.head_dim);
+    L.off_v = align(L.off_k + (size_t)(kv_bytes / 2));
     // 256 bytes more: the workspace is 16-byte aligned, the rows are written by 32
-    L.total = align(L.off_v + (size_t)(group * L.rows_per_seq * row * 2)) + 256;
+    L.total = align(L.off_v + (size_t)(kv_bytes / 2)) + 256;
     return L;
 }
 

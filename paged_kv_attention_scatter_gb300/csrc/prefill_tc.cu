@@ -26,6 +26,9 @@
 //     swizzle atom;
 //   * new tiles t = 0 .. m: the chunk's own k/v rows q0 + 128t ..; tile t == m
 //     is the diagonal (causal mask col <= row), tiles t > m are never visible.
+// With kSplit a tile's keys are cut into runs of split_tiles key tiles, each a
+// work item that leaves its unnormalised O, row maximum and row sum for a
+// combine kernel (few queries on long prefixes, see prefill_fp8.cu).
 // Masked keys get -inf scores; V rows of masked cached keys are zeroed in
 // shared memory because unused cache slots may hold NaN.
 //

@@ -127,6 +127,29 @@ def test_prefill(lib):
     assert lib.pkv_paged_prefill_fp8_workspace_bytes(1, 4, 4, -1, _desc()) == 0
 
 
+def test_prefill_workspace_grows_with_the_call(lib):
+    """A workspace for the largest call holds every smaller one."""
+    need = lib.pkv_paged_prefill_fp8_workspace_bytes
+    sizes = ([0, 1, 2, 3, 7, 40, 600], [0, 1, 100, 128, 129, 1000, 4000, 20000],
+             [0, 1, 127, 128, 3900, 4000, 9000, 50000, 400000, 3000000])
+    for hq, desc in ((8, _desc(hkv=8, d=128)), (3, _desc(hkv=1, d=64))):
+        at = {(b, n, k): need(b, n, hq, k, desc) for b in sizes[0] for n in sizes[1]
+              for k in sizes[2]}
+        for (b, n, k), bytes_ in at.items():
+            for axis, x in enumerate((b, n, k)):
+                bigger = [s for s in sizes[axis] if s > x]
+                if bigger:
+                    key = [b, n, k]
+                    key[axis] = bigger[0]
+                    assert at[tuple(key)] >= bytes_, (b, n, k, axis)
+
+
+def test_prefill_sizes_beyond_any_memory(lib):
+    """The product of the sizes passes 64 bits."""
+    desc = _desc(hkv=1 << 28, d=128)
+    assert lib.pkv_paged_prefill_fp8_workspace_bytes(1, 4, 1 << 28, (1 << 31) - 1, desc) > 1 << 60
+
+
 def test_rules(lib):
     from paged_kv_attention_scatter_gb300._binding import LogitRules
 

@@ -387,6 +387,8 @@ def _prefill(pkv, dev, lq, lp, bs, hkv, group, d, seed, max_k=None, extra=0):
     # few queries on long prefixes: keys split over work items, some rows unsplit
     ([1], [3000], 64, 1, 2, 128), ([20, 160, 5, 300], [2500, 900, 0, 17], 16, 2, 2, 128),
     ([130, 7], [511, 4000], 256, 1, 3, 64), ([1] * 20, [700] * 19 + [5000], 32, 1, 1, 64),
+    ([1], [5000], 64, 1, 2, 128), ([20, 160, 5, 300], [6500, 4600, 0, 17], 16, 1, 2, 128),
+    ([130, 7], [511, 9000], 256, 1, 3, 64), ([65, 128], [4096, 3968], 128, 2, 1, 128),
 ])
 def test_prefill_is_the_oracles(cuda, lq, lp, bs, hkv, group, d):
     _prefill(U.lib(), cuda, lq, lp, bs, hkv, group, d, seed=bs + sum(lq), extra=3)
@@ -473,6 +475,45 @@ def test_split_prefill_gives_up_then_recovers(cuda):
     finally:
         pkv.set_wait_poll_limit()
     _prefill(pkv, cuda, [20, 160], [2500, 900], 16, 2, 2, 128, seed=4)
+
+
+def test_split_prefill_skips_a_sequence_beyond_max_seqlen_k(cuda):
+    # 4340 keys: two splits of 17 tiles; the longer sequence's rows have no room in them
+    pkv = U.lib()
+    rng = np.random.default_rng(3)
+    hkv, d = 1, 128
+    pool = F.Pool([4300, 4300], 64, hkv, d, seed=1)
+    q, k = F.bf16(rng, 340, 2, d), F.bf16(rng, 340, hkv, d)
+    cu_q = torch.tensor([0, 300, 340], dtype=torch.int32, device=cuda)
+    cu_k = torch.tensor([0, 4600, 8940], dtype=torch.int32, device=cuda)
+    kc, vc, ks, vs, bt = pool.on(cuda)
+    st = pkv.new_status(cuda)
+    out = torch.full((340, 2, d), 7.0, dtype=torch.bfloat16, device=cuda)
+    pkv.paged_prefill_varlen_fp8(q.to(cuda), k.to(cuda), k.to(cuda), kc, vc, ks, vs, cu_q, cu_k, 300,
+                                 4340, bt, 0.09, out=out, status=st)
+    assert U.status_word(st) == pkv.STATUS["BAD_SEQLENS"]
+    assert (out[:300] == 7.0).all()
+    kv, vv = pool.values("k"), pool.values("v")
+    ref = oatt.paged_prefill_varlen(U.f64(q[300:]), U.f64(k[300:]), U.f64(k[300:]), kv, vv, [0, 40],
+                                    [0, 4340], pool.bt[1:], 0.09)
+    both = [np.concatenate([x.reshape(-1, d), U.f64(k).reshape(-1, d)]) for x in (kv, vv)]
+    tol = F.bound(ref, U.f64(q[300:]), *both, 0.09, F.PREFILL, 0)
+    assert (np.abs(U.f64(out[300:]) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("polls", [0, 2, 4])
+def test_long_split_prefill_gives_up_then_recovers(cuda, polls):
+    pkv = U.lib()
+    case = ([20, 160], [5500, 900], 16, 1, 2, 128)
+    pkv.set_wait_poll_limit(polls)
+    try:
+        _prefill(pkv, cuda, *case, seed=4)
+    except AssertionError:
+        pass                                     # the status said so (or too few polls were few)
+    finally:
+        pkv.set_wait_poll_limit()
+    torch.cuda.synchronize()
+    _prefill(pkv, cuda, *case, seed=4)
 
 
 def test_prefill_unreadable_prefix_rows_are_zeros(cuda):
