@@ -17,8 +17,10 @@
 //
 // Design.  One CTA owns a (block, set of heads): it needs every row the call
 // stores there before it can write the first code.  It takes each head's
-// maximum while reading the rows once into registers, and writes codes from the
-// registers.  A row's head segment is read as 16 bytes a lane (D/8 lanes) and
+// maximum while reading the rows once, into registers or shared memory, and
+// writes codes from there; a block is shared by as many CTAs as let each keep
+// all of its rows (a CTA with twice the rows it can keep takes three times as
+// long, and is the launch's last).  A row's head segment is read as 16 bytes a lane (D/8 lanes) and
 // written as 8.  Rows that are consecutive tokens in consecutive slots, as a
 // sequence's always are, are addressed by their first; any others (duplicates:
 // the last token of a slot is stored) through a list in shared memory.  How
@@ -26,12 +28,20 @@
 //  * up to 2048: one launch, a CTA per token.  Each scans all slots (8 KB at
 //    most, out of L2, in one round of loads) for its block's tokens; the CTAs of
 //    the first of them share the block's heads, one CTA for a decode step's
-//    single row, up to 2 * Hkv for a block that a prefill chunk fills, and the
+//    few rows, up to 2 * Hkv for a block that a prefill chunk fills, and the
 //    others leave.
 //  * more: that scan is quadratic, so a first kernel links the runs of
-//    consecutive tokens in each block into a list per block, and the store
-//    kernel's CTAs walk the lists.
-// Bound by memory: 4 bytes read and 2 written per K/V entry pair.
+//    consecutive tokens in each block into a list per block, and notes whether a
+//    block's rows are one token after another in one slot after another, and the
+//    last of them.  The store kernel's CTAs then know their rows after two round
+//    trips, or walk the lists.  Blocks of few and of many rows are listed apart, so
+//    that a call of many sequences with a token each has one CTA a block (43 us
+//    for 4096; 305 with the CTAs of full blocks).
+// Memory's part: 4 bytes read and 2 written per K/V entry pair.  16384 tokens of 16
+// prompts (8 heads of 128, blocks of 256) take 25 us, 4.1 TB/s: three waves of CTAs,
+// each waiting 1.5 us for its rows' place, 3-4 for the rows at the copy rate, and
+// converting for 2; three CTAs an SM with their rows in shared memory against two
+// with them in registers.
 #include "fp8_common.cuh"
 
 namespace {
@@ -41,7 +51,6 @@ constexpr int kThreads = 256;
 // prefill chunk 256 over 16 lane groups.
 constexpr int kKeepScan = 4, kKeepList = 16;
 constexpr int32_t kScanTokens = 2048;        // largest call of the scanning form
-constexpr int kRowsPerPart = 16;             // rows for which one more CTA joins a block
 
 struct StoreArgs {
     const uint4* k;
@@ -55,20 +64,43 @@ struct StoreArgs {
     int64_t num_slots;
     uint32_t* status;
     // list form: runs linked per block
-    int32_t* count;                          // blocks in `list`, minus 1
+    int32_t* count;                          // [2]: blocks of few rows, of many; minus 1
     int32_t* head;                           // [NB]: token that starts the block's last run, -1
+    int8_t* in_line;                         // [NB]: 0 if a run has tokens not slot after slot
+    int32_t* last;                           // [NB]: last token of a run (of the only one)
     int32_t* next;                           // [n]: start of the run linked before, -1
-    int2* list;                              // [min(n, NB)]: blocks that get rows, a run of each
+    int2* list;                              // [list_size]: blocks that get rows, a run of each;
+    int32_t list_size;                       //  few rows from the front, many from the back
+    int32_t few, most;                       // CTAs of a block of few rows; most of one of many
 };
 
 constexpr int kScanLoads = kScanTokens / kThreads;
 
+__device__ __forceinline__ void cp_async16(uint4* to, const uint4* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits for all but the last `pending` groups.
+__device__ __forceinline__ void cp_async_wait(int pending) {
+    if (pending >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // The rows that a call stores into one block: `rows` of them, tokens
 // token0 + i at offsets offset0 + i (dense), or as listed.
-struct BlockRows {
+struct RowLists {
     int32_t winner[pkv::kFp8MaxBlockSize];   // offset -> last token stored there, -1
     int32_t token[pkv::kFp8MaxBlockSize];    // the rows, in no particular order
     int16_t offset[pkv::kFp8MaxBlockSize];
+};
+struct BlockRows {
     int32_t rows, token0, offset0;
     bool dense;
     uint32_t amax[kThreads / 8];             // per lane group
@@ -122,21 +154,21 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
            (uint32_t)pkv::float2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
 }
 
-__device__ __forceinline__ void clear_rows(const StoreArgs& a, BlockRows& sm) {
-    for (int o = threadIdx.x; o < a.bs; o += kThreads) sm.winner[o] = -1;
+__device__ __forceinline__ void clear_rows(const StoreArgs& a, BlockRows& sm, RowLists& l) {
+    for (int o = threadIdx.x; o < a.bs; o += kThreads) l.winner[o] = -1;
     if (threadIdx.x == 0) sm.rows = 0;
 }
 
 // The winners as a compact list (any order), between barriers.
-__device__ __forceinline__ void list_rows(const StoreArgs& a, BlockRows& sm) {
+__device__ __forceinline__ void list_rows(const StoreArgs& a, BlockRows& sm, RowLists& l) {
     __syncthreads();
     if (threadIdx.x == 0) sm.dense = false;
     for (int o = threadIdx.x; o < a.bs; o += kThreads) {
-        const int32_t t = sm.winner[o];
+        const int32_t t = l.winner[o];
         if (t >= 0) {
             const int i = atomicAdd(&sm.rows, 1);
-            sm.token[i] = t;
-            sm.offset[i] = (int16_t)o;
+            l.token[i] = t;
+            l.offset[i] = (int16_t)o;
         }
     }
     __syncthreads();
@@ -144,9 +176,11 @@ __device__ __forceinline__ void list_rows(const StoreArgs& a, BlockRows& sm) {
 
 // Stores the rows of block `blk` for the (tensor, head) pairs part, part +
 // parts, ... of the 2 * Hkv.  Pair p is head p >> 1 of K (even) or V.
-template <int D, int kKeep, bool kDense>
-__device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, int32_t blk,
-                                            int part, int parts) {
+// A lane's first kKeep row segments stay in registers, or in `staged` if that is given
+// (a place of its own there, so no barrier).
+template <int D, int kKeep, bool kDense, bool kStaged>
+__device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, const RowLists& l,
+                                            uint4* staged, int32_t blk, int part, int parts) {
     constexpr int kLanes = D / 8;            // lanes of a row's head segment
     constexpr int kGroups = kThreads / kLanes;
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
@@ -158,13 +192,13 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
     const int at_once = kGroups / gpp, sub = group % gpp;
     const int rows = sm.rows;
     const int32_t token0 = sm.token0, offset0 = sm.offset0;
-    const bool fresh = kDense ? offset0 == 0 : sm.winner[0] >= 0;
+    const bool fresh = kDense ? offset0 == 0 : l.winner[0] >= 0;
     const int64_t row_codes = (int64_t)a.Hkv * D;
-    auto token_of = [&](int r) { return kDense ? token0 + r : sm.token[r]; };
-    auto offset_of = [&](int r) { return kDense ? offset0 + r : (int)sm.offset[r]; };
+    auto token_of = [&](int r) { return kDense ? token0 + r : l.token[r]; };
+    auto offset_of = [&](int r) { return kDense ? offset0 + r : (int)l.offset[r]; };
     // rows of the block that this call does not store
     auto other = [&](int o) {
-        return kDense ? o < offset0 || o >= offset0 + rows : sm.winner[o] < 0;
+        return kDense ? o < offset0 || o >= offset0 + rows : l.winner[o] < 0;
     };
     for (int i0 = 0; i0 < mine; i0 += at_once) {
         const int i = i0 + group / gpp;
@@ -178,17 +212,34 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
         auto load = [&](int r) { return __ldg(src + (int64_t)token_of(r) * (row_codes / 8)); };
         // ---- the pair's maximum; the first kKeep rows stay in registers ----
         const int n = live ? rows : 0;
-        uint4 keep[kKeep];
+        uint4 keep[kStaged ? 1 : kKeep];
+        uint4* const mine_at = staged + threadIdx.x;
+        constexpr int kPart = kKeep / 4;     // rows waited for at once
+        const uint4* from = src + (int64_t)(token0 + sub) * (row_codes / 8);   // dense rows
 #pragma unroll
         for (int j = 0; j < kKeep; ++j) {
-            keep[j] = make_uint4(0, 0, 0, 0);
-            if (sub + j * gpp < n) keep[j] = load(sub + j * gpp);
+            const bool there = sub + j * gpp < n;
+            if constexpr (kStaged) {
+                if (there) cp_async16(mine_at + j * kThreads, from);
+                if (j % kPart == kPart - 1) cp_async_commit();
+            } else {
+                keep[j] = make_uint4(0, 0, 0, 0);
+                if (there) keep[j] = kDense ? __ldg(from) : load(sub + j * gpp);
+            }
+            from += gpp * (row_codes / 8);
         }
         float old = 0.f;
         if (live && !fresh) old = *scale_at;
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < kKeep; ++j) m = amax8(m, keep[j]);
+        for (int j = 0; j < kKeep; ++j) {
+            if constexpr (kStaged) {
+                if (j % kPart == 0) cp_async_wait(kKeep / kPart - 1 - j / kPart);
+                if (sub + j * gpp < n) m = amax8(m, mine_at[j * kThreads]);
+            } else {
+                m = amax8(m, keep[j]);
+            }
+        }
         const int rest = sub + kKeep * gpp;
 #pragma unroll 4
         for (int r = rest; r < n; r += gpp) m = amax8(m, load(r));
@@ -218,9 +269,15 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
             };
             if ((__float_as_int(scale) & 0x7fffff) == 0) {
                 const float inv = __fdiv_rn(1.f, scale);
+                uint8_t* to = dst + (offset0 + sub) * row_codes;
 #pragma unroll
-                for (int j = 0; j < kKeep; ++j)
-                    if (sub + j * gpp < n) *at(sub + j * gpp) = eight_codes<false>(keep[j], inv);
+                for (int j = 0; j < kKeep; ++j) {
+                    if (sub + j * gpp < n)
+                        *(kDense ? reinterpret_cast<uint2*>(to) : at(sub + j * gpp)) =
+                            eight_codes<false>(kStaged ? mine_at[j * kThreads] : keep[kStaged ? 0 : j],
+                                               inv);
+                    to += gpp * row_codes;
+                }
 #pragma unroll 4
                 for (int r = rest; r < n; r += gpp) *at(r) = eight_codes<false>(load(r), inv);
             } else {
@@ -264,14 +321,21 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, i
     }
 }
 
-__device__ __forceinline__ int parts_of(int rows, int pairs) {
-    return min(max(rows / kRowsPerPart, 1), pairs);
+// CTAs that share a block's pairs: as many as let each keep all of its rows.
+template <int D, int kKeep>
+__host__ __device__ __forceinline__ int parts_of(int rows, int pairs) {
+    constexpr int kGroups = kThreads / (D / 8);
+    int gpp = 1;                             // lane groups a pair needs
+    while (gpp < kGroups && gpp * kKeep < rows) gpp <<= 1;
+    const int mine = kGroups / gpp;
+    return (pairs + mine - 1) / mine;
 }
 
 // Up to kScanTokens tokens: CTA t belongs to token t.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) store_scan_kernel(StoreArgs a) {
     __shared__ BlockRows sm;
+    __shared__ RowLists lists;
     __shared__ int32_t before, total, first_token, first_slot;
     pkv::allow_dependent_launch();
     const int32_t t = blockIdx.x;
@@ -310,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 4) store_scan_kernel(StoreArgs a) {
         atomicMin(&first_token, first);
     }
     __syncthreads();
-    const int rows = total, part = before, parts = parts_of(rows, 2 * a.Hkv);
+    const int rows = total, part = before, parts = min(rows, parts_of<D, kKeepScan>(rows, 2 * a.Hkv));
     if (part >= parts) return;
     if (threadIdx.x == first_token % kThreads) first_slot = a.slots[first_token];
     __syncthreads();
@@ -331,18 +395,18 @@ __global__ void __launch_bounds__(kThreads, 4) store_scan_kernel(StoreArgs a) {
         }
         __syncthreads();
     } else {
-        clear_rows(a, sm);
+        clear_rows(a, sm, lists);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kScanLoads; ++j)
             if (s[j] >= lo && s[j] < hi)
-                atomicMax(&sm.winner[s[j] - lo], (int32_t)threadIdx.x + j * kThreads);
-        list_rows(a, sm);
+                atomicMax(&lists.winner[s[j] - lo], (int32_t)threadIdx.x + j * kThreads);
+        list_rows(a, sm, lists);
     }
     if (sm.dense)
-        store_block<D, kKeepScan, true>(a, sm, blk, part, parts);
+        store_block<D, kKeepScan, true, false>(a, sm, lists, nullptr, blk, part, parts);
     else
-        store_block<D, kKeepScan, false>(a, sm, blk, part, parts);
+        store_block<D, kKeepScan, false, false>(a, sm, lists, nullptr, blk, part, parts);
 }
 
 // More tokens: each block's runs as a linked list, and the blocks as a list.
@@ -351,97 +415,109 @@ __global__ void __launch_bounds__(kThreads) store_link_kernel(StoreArgs a) {
     const int32_t t = blockIdx.x * kThreads + threadIdx.x;
     if (t >= a.n) return;
     const int32_t slot = a.slots[t];
+    const int32_t prev = t > 0 ? a.slots[t - 1] : -1, next = t < a.n - 1 ? a.slots[t + 1] : -1;
+    const int32_t ahead = t < a.n - kKeepList ? a.slots[t + kKeepList] : -1;
     if (slot < 0) return;
     if (slot >= a.num_slots) {
         pkv::report(a.status, PKV_STATUS_SLOT_OUT_OF_RANGE);
         return;
     }
-    const int32_t blk = slot / a.bs;
-    const int32_t prev = t > 0 ? a.slots[t - 1] : -1;
-    if (prev >= 0 && prev < a.num_slots && prev / a.bs == blk) return;   // inside a run
+    const int32_t blk = slot / a.bs, lo = blk * a.bs, hi = lo + a.bs;
+    if (next < lo || next >= hi) a.last[blk] = t;
+    if (prev >= lo && prev < hi) {           // inside a run
+        if (slot != prev + 1) a.in_line[blk] = 0;
+        return;
+    }
     const int32_t linked = atomicExch(&a.head[blk], t);
     a.next[t] = linked;
-    if (linked < 0) a.list[atomicAdd(a.count, 1) + 1] = make_int2(blk, t);
+    if (linked >= 0) return;
+    // more rows than a lane group keeps, if the run is in line
+    const bool many = ahead >= 0 && ahead < hi && ahead - slot == kKeepList;
+    const int32_t at = atomicAdd(a.count + many, 1) + 1;
+    a.list[many ? a.list_size - 1 - at : at] = make_int2(blk, t);
+}
+
+constexpr int kListSmem = kKeepList * kThreads * 16;
+constexpr int kListCtas = 3;
+static_assert(kListSmem >= (int)sizeof(RowLists), "the lists take the staged rows' place");
+
+// (out of line: its registers are not the dense rows' to give)
+template <int D>
+__device__ __noinline__ void store_listed(const StoreArgs& a, BlockRows& sm, const RowLists& l,
+                                          int32_t blk, int part, int parts) {
+    store_block<D, kKeepScan, false, false>(a, sm, l, nullptr, blk, part, parts);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) store_list_kernel(StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, kListCtas) store_list_kernel(StoreArgs a) {
+    extern __shared__ __align__(16) char dynamic[];          // staged rows, or the lists
     __shared__ BlockRows sm;
+    uint4* const staged = reinterpret_cast<uint4*>(dynamic);
+    RowLists& lists = *reinterpret_cast<RowLists*>(dynamic);
     pkv::wait_for_predecessor();             // the linked runs
     pkv::allow_dependent_launch();
-    const int pairs = 2 * a.Hkv;
-    const int max_parts = parts_of(a.bs, pairs);
-    const int64_t items = (int64_t)(*a.count + 1) * max_parts;
-    int32_t have = -1;                       // block whose rows are in hand
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-        const int2 entry = a.list[i / max_parts];
+    const uint32_t few = a.few, most = a.most;
+    // (read beside the counts, and not used if there is no such entry)
+    int2 entry = a.list[max(a.list_size - 1 - (int32_t)(blockIdx.x / most), 0)];
+    // blocks * parts < 2^32, as the rows of n tokens fit a GPU's memory
+    const uint32_t from_many = (uint32_t)(a.count[1] + 1) * most;
+    const uint32_t items = from_many + (uint32_t)(a.count[0] + 1) * few;
+    for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const bool many = i < from_many;
+        const uint32_t j = many ? i : i - from_many, of = many ? most : few;
+        if (!many) entry = a.list[j / of];
+        else if (i != blockIdx.x) entry = a.list[a.list_size - 1 - (int32_t)(j / of)];
         const int32_t blk = entry.x, run = entry.y;
-        const int part = (int)(i % max_parts);
-        if (blk != have) {
-            const int32_t lo = blk * a.bs, hi = lo + a.bs;
-            const int32_t head = a.head[blk], slot0 = a.slots[run];
-            // the block's only run, one row a slot, no longer than the block?
-            int32_t rows = 0;
-            bool ok = head == run;
-            for (int32_t j = 0;; j += kThreads) {
-                const int32_t k = j + (int32_t)threadIdx.x;
-                const int32_t s = k < a.n - run ? a.slots[run + k] : -1;
-                const bool in = s >= lo && s < hi;
-                ok = ok && (!in || s == slot0 + k);
-                const int in_run = __syncthreads_count(in);
-                rows += in_run;
-                if (in_run < kThreads) break;
+        const int part = (int)(j % of);
+        const int32_t lo = blk * a.bs, hi = lo + a.bs;
+        const int32_t head = a.head[blk], slot0 = a.slots[run], last = a.last[blk];
+        if (head == run && a.in_line[blk] != 0) {        // the block's only run
+            if (threadIdx.x == 0) {
+                sm.dense = true;
+                sm.rows = last - run + 1;
+                sm.token0 = run;
+                sm.offset0 = slot0 - lo;
             }
-            // a token of this block behind the run's end would be another run's
-            // (head != run), and is not read as one of this run
-            ok = __syncthreads_and(ok);
-            if (ok) {
-                if (threadIdx.x == 0) {
-                    sm.dense = true;
-                    sm.rows = rows;
-                    sm.token0 = run;
-                    sm.offset0 = slot0 - lo;
+            __syncthreads();
+        } else {
+            clear_rows(a, sm, lists);
+            __syncthreads();
+            for (int32_t r = head; r >= 0; r = a.next[r]) {
+                // the run's tokens: up to the first one of another block
+                for (int32_t j = r;; j += kThreads) {
+                    const int32_t t = j + (int32_t)threadIdx.x;
+                    const int32_t s = t < a.n ? a.slots[t] : -1;
+                    const bool in = s >= lo && s < hi;
+                    if (in) atomicMax(&lists.winner[s - lo], t);
+                    if (!__syncthreads_and(in)) break;
                 }
-                __syncthreads();
-            } else {
-                clear_rows(a, sm);
-                __syncthreads();
-                for (int32_t r = head; r >= 0; r = a.next[r]) {
-                    // the run's tokens: up to the first one of another block
-                    for (int32_t j = r;; j += kThreads) {
-                        const int32_t t = j + (int32_t)threadIdx.x;
-                        const int32_t s = t < a.n ? a.slots[t] : -1;
-                        const bool in = s >= lo && s < hi;
-                        if (in) atomicMax(&sm.winner[s - lo], t);
-                        if (!__syncthreads_and(in)) break;
-                    }
-                }
-                list_rows(a, sm);
             }
-            have = blk;
+            list_rows(a, sm, lists);
         }
         // a part beyond the rows' need has nothing to do
-        const int parts = parts_of(sm.rows, pairs);
+        const int parts = many ? parts_of<D, kKeepList>(sm.rows, 2 * a.Hkv) : (int)few;
         if (part < parts) {
             if (sm.dense)
-                store_block<D, kKeepList, true>(a, sm, blk, part, parts);
+                store_block<D, kKeepList, true, true>(a, sm, lists, staged, blk, part, parts);
             else
-                store_block<D, kKeepScan, false>(a, sm, blk, part, parts);
+                store_listed<D>(a, sm, lists, blk, part, parts);
         }
         __syncthreads();                     // the rows in hand are read to the end
     }
 }
 
 struct StoreLayout {
-    size_t off_head, off_next, off_list, total;
+    size_t off_head, off_in_line, off_last, off_next, off_list, total;
 };
 
 StoreLayout store_layout(int32_t n, int32_t num_blocks) {
     StoreLayout L{};
     if (n <= kScanTokens) return L;
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    L.off_head = 16;                         // behind the count, cleared with it
-    L.off_next = align(L.off_head + sizeof(int32_t) * (size_t)num_blocks);
+    L.off_head = 16;                         // behind the counts, cleared with them
+    L.off_in_line = L.off_head + sizeof(int32_t) * (size_t)num_blocks;   // cleared with them
+    L.off_last = align(L.off_in_line + (size_t)num_blocks);
+    L.off_next = align(L.off_last + sizeof(int32_t) * (size_t)num_blocks);
     L.off_list = align(L.off_next + sizeof(int32_t) * (size_t)n);
     L.total = align(L.off_list + sizeof(int2) * (size_t)(n < num_blocks ? n : num_blocks));
     return L;
@@ -471,11 +547,19 @@ int launch_store(const Fp8StoreCall& c, cudaStream_t s) {
     char* ws = (char*)c.workspace;
     a.count = (int32_t*)ws;
     a.head = (int32_t*)(ws + L.off_head);
+    a.in_line = (int8_t*)(ws + L.off_in_line);
+    a.last = (int32_t*)(ws + L.off_last);
     a.next = (int32_t*)(ws + L.off_next);
     a.list = (int2*)(ws + L.off_list);
-    if (cudaMemsetAsync(ws, 0xff, L.off_head + sizeof(int32_t) * (size_t)a.NB, s) != cudaSuccess)
+    a.list_size = a.n < a.NB ? a.n : a.NB;
+    a.few = parts_of<D, kKeepList>(1, 2 * a.Hkv);
+    a.most = parts_of<D, kKeepList>(a.bs, 2 * a.Hkv);
+    if (cudaMemsetAsync(ws, 0xff, L.off_in_line + (size_t)a.NB, s) != cudaSuccess)
         return PKV_ERR_CUDA;
     store_link_kernel<<<(unsigned)((a.n + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+    static std::atomic<uint64_t> configured;
+    if (!pkv_dynamic_smem_once((const void*)store_list_kernel<D>, kListSmem, configured))
+        return PKV_ERR_CUDA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -483,12 +567,12 @@ int launch_store(const Fp8StoreCall& c, cudaStream_t s) {
     // about a CTA an item (blocks filled to half on average, at least): the
     // scheduler evens them out better than a loop does, and a CTA without one
     // leaves at once
-    const int pairs = 2 * a.Hkv, most = a.bs / kRowsPerPart;
-    int64_t grid = 2LL * (a.n / a.bs + 1) * (most < 1 ? 1 : most > pairs ? pairs : most);
+    int64_t grid = 2LL * (a.n / a.bs + 1) * a.most;
     if (grid < pkv_num_sms() * 8) grid = pkv_num_sms() * 8;
     if (grid > 1 << 20) grid = 1 << 20;
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kListSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

@@ -76,6 +76,54 @@ def test_store_is_the_oracles(cuda, n, nb, bs, hkv, d, pattern):
                slots)
 
 
+def _run_edges(rng, nb, bs):
+    """Runs of 1 to bs rows around the 16 that a lane group keeps: in line, with two rows
+    swapped, a slot left out or stored twice, padding inside, and two runs of one block
+    with another block's rows between them."""
+    slots, perm = [], rng.permutation(nb)
+    for i in range(0, nb - 1, 2):
+        b, c = int(perm[i]) * bs, int(perm[i + 1]) * bs
+        rows = int(rng.choice([1, 2, 15, 16, 17, 18, 33, bs]))
+        rows = min(rows, bs)
+        pos = int(rng.integers(0, bs - rows + 1))
+        run = list(range(b + pos, b + pos + rows))
+        kind = int(rng.integers(0, 6))
+        at = int(rng.integers(0, rows))
+        if kind == 1 and rows > 2:
+            run[at - 1], run[at - 2] = run[at - 2], run[at - 1]
+        elif kind == 2 and rows > 1:
+            del run[at]
+        elif kind == 3:
+            run.insert(at, run[-1])
+        elif kind == 4:
+            run.insert(at, -1)
+        elif kind == 5 and rows > 6:            # slot after slot again sixteen tokens on
+            run[2:5] = [c, c + bs // 2, c + bs - 1]
+        slots += run
+    return np.asarray(slots, np.int32)
+
+
+@pytest.mark.parametrize("nb,bs,hkv,d", [(260, 48, 8, 128), (700, 20, 3, 64), (120, 256, 2, 128),
+                                         (150, 200, 20, 64)])
+def test_store_runs_of_few_and_many_rows(cuda, nb, bs, hkv, d):
+    rng = np.random.default_rng(bs)
+    slots = _run_edges(rng, nb, bs)
+    n = len(slots)
+    assert n > 2048
+    pool = F.Pool([nb * bs - bs], bs, hkv, d, seed=n, spare=1)
+    mag = 2.0 ** rng.integers(-5, 4, (n, hkv, 1))
+    _run_store(U.lib(), cuda, F.bf16(rng, n, hkv, d, mag=mag), F.bf16(rng, n, hkv, d, mag=mag),
+               pool, slots)
+
+
+def test_store_one_row_each_of_many_sequences(cuda):
+    rng = np.random.default_rng(4)
+    n, nb, bs, hkv, d = 2500, 2600, 64, 2, 128
+    slots = _store_case(rng, n, nb, bs, hkv, d, "step")
+    pool = F.Pool([nb * bs - bs], bs, hkv, d, seed=n, spare=1)
+    _run_store(U.lib(), cuda, F.bf16(rng, n, hkv, d), F.bf16(rng, n, hkv, d), pool, slots)
+
+
 @pytest.mark.parametrize("n", [6, 2100])
 def test_store_special_values_and_scales(cuda, n):
     """Infinities saturate and do not widen the scale, NaN stays; zero rows;
