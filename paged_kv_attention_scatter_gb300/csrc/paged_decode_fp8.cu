@@ -23,12 +23,16 @@ using pkv::kMaxGroup;
 
 // Keys per work unit, from the sizes alone: the multiple of 128 (a stage of
 // head_dim 128) nearest to the length that gives about two units per SM for a
-// typical context of half the stated maximum, within 128..1024.  A unit's end
+// typical context of half the stated maximum, within 128..1024, and 2048 (a lane of
+// the producer has one of a unit's 64-key boxes) where a SM has sixteen such units or
+// where a stage of head_dim 64 has eight heads' softmax.  A unit's end
 // -- its last stage's P V waited for, the two softmax groups' shares merged --
 // costs about a stage, so units are longer than the bf16 decode's, whose rule
 // aims at sixteen a SM (measured, us: 64 sequences of 16/8 heads and 512..4096
 // keys 59 at 256, 57 at 512, 57 at 1024; 8 of 32/8 and 4000..8192 39 at 128, 28 at
-// 512, 27 at 1024; 2 of 30000..32768 60, 35, 33).
+// 512, 27 at 1024; 2 of 30000..32768 60, 35, 33; and at 1024 and 2048: 64 of 16/8 as
+// above 57, 61; 96 of 64/8 and 128..32768 200, 196; head_dim 64, 64 of 64/8 and
+// 512..4096 51, 48, in blocks of 16 75, 66; of 16/8 37, 39).
 int32_t choose_chunk_keys(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
                           const pkv_cache_desc& c) {
     const int32_t hkv = c.num_kv_heads > 0 ? c.num_kv_heads : 1;
@@ -38,6 +42,7 @@ int32_t choose_chunk_keys(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
     // short contexts: one unit a sequence and head, so that nothing is left to combine
     if (max_ctx <= 512) return max_ctx <= 128 ? 128 : (max_ctx + 127) / 128 * 128;
     if (chunk < 1.0) return 128;
+    if (chunk >= 128.0 || (chunk >= 16.0 && c.head_dim == 64 && num_q_heads / hkv > 4)) return 2048;
     return chunk >= 8.0 ? 1024 : (int32_t)chunk * 128;
 }
 

@@ -768,7 +768,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         Ring ring;
         int issued = 0, units = 0;
         bool ok = true;
-        // Lane l has box l of the unit (at most 1024 keys: 16 boxes).  Lanes 2j and
+        // Lane l has box l of the unit (at most 2048 keys: 32 boxes).  Lanes 2j and
         // 2j + 1 (four lanes for head_dim 64) fill stage j, so a stage costs no shuffles or divisions.  A unit
         // needs its record, then its boxes' block ids, then their scales: at a
         // unit's start the next one's scales, the ids of the one after and the

@@ -226,6 +226,23 @@ def test_decode_is_the_oracles(cuda, lens, bs, hkv, group, d, arbitrary):
     assert (ref[[i for i, n in enumerate(lens) if n == 0]] == 0).all()
 
 
+@pytest.mark.parametrize("lens", [[2047, 2049, 0, 1985, 6200], [4097] + [130] * 32 + [2048]])
+@pytest.mark.parametrize("bs,d", [(16, 128), (64, 128), (256, 64), (24, 64)])
+def test_decode_longest_units(cuda, lens, bs, d):
+    """A stated maximum so large that units have 2048 keys, with and without a plan
+    kernel."""
+    pkv = U.lib()
+    rng = np.random.default_rng(bs)
+    pool = F.Pool(lens, bs, 2, d, seed=bs + d, spread=4)
+    q = F.bf16(rng, len(lens), 16, d)
+    st = pkv.new_status(cuda)
+    out = pkv.paged_decode_fp8(q.to(cuda), *pool.on(cuda),
+                               torch.tensor(lens, dtype=torch.int32, device=cuda), 0.09, 1 << 20,
+                               status=st)
+    assert U.status_word(st) == 0
+    _check_decode(out, pool, q, 0.09)
+
+
 @pytest.mark.parametrize("bs", [16, 64, 40])
 @pytest.mark.parametrize("q_mag,vexp", [(1e25, -60), (1e-30, 100), (3e4, 0), (1.0, -86)])
 def test_decode_ranges(cuda, bs, q_mag, vexp):
