@@ -95,6 +95,28 @@ def test_rules_are_the_oracles(cuda, B, V, T, bias, mask, dtype, pad):
     _check(out, c)
 
 
+@pytest.mark.parametrize("T", [32766, 32767, 32768, 70000])
+@pytest.mark.parametrize("V,dtype", [(72, "fp32"), (73, "fp32"), (72, "bf16")])
+def test_long_histories(cuda, T, V, dtype):
+    """Nearly every generated token is the same, next to entries with prompt tokens,
+    single ones and none: counts up to and beyond what 16 bits hold."""
+    pkv = U.lib()
+    rng = np.random.default_rng(T)
+    ids = np.stack([np.full(T, 40), np.full(T, 41), np.full(T, V - 1)]).astype(np.int32)
+    ids[:, :4] = [42, 39, 5, V - 2]
+    ids[:, -1] = 38
+    x = torch.from_numpy(rng.normal(size=(3, V)).astype(np.float32)).to(TYPES[dtype])
+    c = {"logits": x, "token_ids": ids, "token_lens": np.full(3, T, np.int32),
+         "prompt_lens": np.asarray([4, 0, 2], np.int32),
+         "repetition": np.asarray([1.5, 1.0, 0.7], np.float32),
+         "presence": np.asarray([0.25, 0.5, 0.0], np.float32),
+         "frequency": np.asarray([0.001, 0.01, 0.3], np.float32)}
+    st = pkv.new_status(cuda)
+    out = pkv.apply_logit_rules(x.to(cuda), **_args(c, cuda), status=st)
+    assert U.status_word(st) == 0
+    _check(out, c)
+
+
 @pytest.mark.parametrize("V", [9000, 9003, 40000])
 def test_several_segments_of_a_row(cuda, V):
     """Rows of more than one CTA's segment, tokens near every segment's edge
