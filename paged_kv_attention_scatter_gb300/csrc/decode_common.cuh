@@ -34,44 +34,73 @@ struct DecodeArgs {
     int32_t b0;                      // first sequence of a combine launch
     uint32_t wait_polls;             // polls of a bounded mbarrier wait
     // No plan in the workspace: the kernels take the schedule of a batch of at
-    // most 32 sequences from `ctx` themselves (WarpPlan).
+    // most kMaxInline sequences from `ctx` themselves (WarpPlan).
     int32_t inline_plan;
     // The combine kernel: a row whose weights are NaN comes out as NaN (else as zeros).
     int32_t keep_nan;
 };
 
-// The chunk schedule of at most 32 sequences, held by a warp: lane b has sequence
-// b's length, chunks and the chunks up to and with it.  What the plan kernel
-// writes for any number, without its launch.
+// The chunk schedule of at most kMaxInline sequences, held by a warp: lane l has
+// sequence 32 i + l's length, chunks and the chunks up to and with it.  What the
+// plan kernel writes for any number, without its launch.
+constexpr int kInlinePerLane = 4, kMaxInline = 32 * kInlinePerLane;
+
 struct WarpPlan {
-    int32_t len, n, incl;
-    bool bad;                        // this lane's length is out of range (it gets no chunks)
+    int32_t len[kInlinePerLane], n[kInlinePerLane], incl[kInlinePerLane];
+    int32_t batch, sum;              // chunks of all
+    bool bad;                        // one of this lane's lengths is out of range (no chunks)
     __device__ __forceinline__ explicit WarpPlan(const DecodeArgs& a) {
         const int lane = threadIdx.x & 31;
-        len = lane < a.B ? a.ctx[lane] : 0;
-        bad = len < 0 || len > (int64_t)a.MB * a.bs || len > a.max_ctx;
-        n = bad ? 0 : (len + a.chunk_keys - 1) / a.chunk_keys;
-        incl = n;
+        bad = false;
+        batch = a.B;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int32_t x = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += x;
+        for (int i = 0; i < kInlinePerLane; ++i)
+            len[i] = 32 * i + lane < batch ? a.ctx[32 * i + lane] : 0;
+        int32_t before = 0;
+#pragma unroll
+        for (int i = 0; i < kInlinePerLane; ++i) {
+            n[i] = 0;
+            incl[i] = before;
+            if (i > 0 && 32 * i >= batch) continue;
+            const bool out = len[i] < 0 || len[i] > (int64_t)a.MB * a.bs || len[i] > a.max_ctx;
+            bad |= out;
+            int32_t x = n[i] = out ? 0 : (len[i] + a.chunk_keys - 1) / a.chunk_keys;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off) x += y;
+            }
+            incl[i] += x;
+            before = __shfl_sync(0xffffffffu, incl[i], 31);
         }
+        sum = before;
     }
-    __device__ __forceinline__ int32_t total() const {
-        return __shfl_sync(0xffffffffu, incl, 31);
+    __device__ __forceinline__ int32_t total() const { return sum; }
+    // a sequence's value (b alike in every lane)
+    __device__ __forceinline__ static int32_t get(const int32_t (&x)[kInlinePerLane], int32_t b) {
+        if (b < 32) return __shfl_sync(0xffffffffu, x[0], b);
+        int32_t mine = x[1];
+#pragma unroll
+        for (int i = 2; i < kInlinePerLane; ++i)
+            if (b >= 32 * i) mine = x[i];
+        return __shfl_sync(0xffffffffu, mine, b & 31);
     }
     // (first chunk, chunks) of sequence b
     __device__ __forceinline__ int2 of(int32_t b) const {
-        const int32_t nb = __shfl_sync(0xffffffffu, n, b);
-        return make_int2(__shfl_sync(0xffffffffu, incl, b) - nb, nb);
+        const int32_t nb = get(n, b);
+        return make_int2(get(incl, b) - nb, nb);
     }
     // (sequence, first key, end key, chunks of the sequence) of chunk sc < total()
     __device__ __forceinline__ int4 record(int32_t sc, int32_t chunk_keys) const {
-        const int32_t b = __popc(__ballot_sync(0xffffffffu, incl <= sc));
+        int32_t b = __popc(__ballot_sync(0xffffffffu, incl[0] <= sc));
+        if (batch > 32) {
+#pragma unroll
+            for (int i = 1; i < kInlinePerLane; ++i)
+                b += __popc(__ballot_sync(0xffffffffu, incl[i] <= sc));
+        }
         const int2 f = of(b);
-        const int32_t i = sc - f.x, l = __shfl_sync(0xffffffffu, len, b);
-        return make_int4(b, i * chunk_keys, min(l, (i + 1) * chunk_keys), f.y);
+        const int32_t i = sc - f.x;
+        return make_int4(b, i * chunk_keys, min(get(len, b), (i + 1) * chunk_keys), f.y);
     }
 };
 

@@ -344,6 +344,33 @@ def test_decode_bad_context_lens(cuda):
     _check_decode(out, pool, q, 0.1)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 64, 65, 127, 128, 129, 200])
+@pytest.mark.parametrize("bs,most", [(16, 300), (64, 1500)])      # without and with a combine
+def test_decode_batches_around_a_warps_lanes(cuda, B, bs, most):
+    """With and without a plan kernel: many sequences, some without keys, some of a
+    length that is out of range (reported, zero rows), some of several chunks."""
+    pkv = U.lib()
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 40, B).tolist()
+    for i in (0, 5, B // 2, B - 1):
+        lens[i] = most
+    pool = F.Pool(lens, bs, 1, 64, seed=B)
+    q = F.bf16(rng, B, 3, 64)
+    st = pkv.new_status(cuda)
+    run = lambda ctx: pkv.paged_decode_fp8(  # noqa: E731
+        q.to(cuda), *pool.on(cuda), torch.tensor(ctx, dtype=torch.int32, device=cuda), 0.1, most,
+        status=st)
+    out = run(lens)
+    assert U.status_word(st) == 0
+    _check_decode(out, pool, q, 0.1)
+    bad = list(lens)
+    bad[B - 2], bad[3] = -5, most + 1
+    out = run(bad)
+    assert U.status_word(st) == pkv.STATUS["BAD_CONTEXT_LEN"]
+    pool.lens[B - 2] = pool.lens[3] = 0
+    _check_decode(out, pool, q, 0.1)
+
+
 def test_plan_and_runs_are_the_whole_call(cuda):
     pkv = U.lib()
     rng = np.random.default_rng(15)
