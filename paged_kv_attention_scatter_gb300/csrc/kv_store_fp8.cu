@@ -274,8 +274,8 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, c
                 for (int j = 0; j < kKeep; ++j) {
                     if (sub + j * gpp < n)
                         *(kDense ? reinterpret_cast<uint2*>(to) : at(sub + j * gpp)) =
-                            eight_codes<false>(kStaged ? mine_at[j * kThreads] : keep[kStaged ? 0 : j],
-                                               inv);
+                            eight_codes<false>(
+                                kStaged ? mine_at[j * kThreads] : keep[kStaged ? 0 : j], inv);
                     to += gpp * row_codes;
                 }
 #pragma unroll 4
@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 4) store_scan_kernel(StoreArgs a) {
         atomicMin(&first_token, first);
     }
     __syncthreads();
-    const int rows = total, part = before, parts = min(rows, parts_of<D, kKeepScan>(rows, 2 * a.Hkv));
+    const int rows = total, part = before;
+    const int parts = min(rows, parts_of<D, kKeepScan>(rows, 2 * a.Hkv));
     if (part >= parts) return;
     if (threadIdx.x == first_token % kThreads) first_slot = a.slots[first_token];
     __syncthreads();

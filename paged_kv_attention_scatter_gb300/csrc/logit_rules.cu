@@ -350,8 +350,9 @@ int launch_rules(RuleArgs& a, cudaStream_t s) {
     const bool wide = a.r.token_ids && a.r.max_tokens > 32767;
     const int smem = a.segment * ((int)sizeof(T) + (wide ? 4 : 2));
     void (*const kernel)(RuleArgs) =
-        vec ? (wide ? logit_rules_kernel<T, true, uint32_t> : logit_rules_kernel<T, true, uint16_t>)
-            : (wide ? logit_rules_kernel<T, false, uint32_t> : logit_rules_kernel<T, false, uint16_t>);
+        vec ? wide ? logit_rules_kernel<T, true, uint32_t> : logit_rules_kernel<T, true, uint16_t>
+        : wide ? logit_rules_kernel<T, false, uint32_t>
+               : logit_rules_kernel<T, false, uint16_t>;
     static std::atomic<uint64_t> configured[4];
     if (!pkv_dynamic_smem_once((const void*)kernel, kMaxSegment * ((int)sizeof(T) + (wide ? 4 : 2)),
                                configured[vec * 2 + wide]))

@@ -34,8 +34,8 @@
 //   warp 9     P V issuer; its completion frees the stage's slot.
 //   warp 10    Q: scales, splits and lays out the next units' rows.
 //   warp 11    producer, block sizes that are multiples of 64: per stage two
-//              (head_dim 64: four) 64-key TMA boxes of K and as many of V, each in one cache block, with
-//              its scales in the stage's record.
+//              (head_dim 64: four) 64-key TMA boxes of K and as many of V, each in one
+//              cache block, with its scales in the stage's record.
 //   warps 11-18 producers, other block sizes, four teams of two that fill stages
 //              in turn: a lane looks up its keys' blocks and scales, the warp
 //              gathers half a stage's rows with 16-byte cp.async into the layout the boxes
@@ -769,10 +769,10 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         int issued = 0, units = 0;
         bool ok = true;
         // Lane l has box l of the unit (at most 2048 keys: 32 boxes).  Lanes 2j and
-        // 2j + 1 (four lanes for head_dim 64) fill stage j, so a stage costs no shuffles or divisions.  A unit
-        // needs its record, then its boxes' block ids, then their scales: at a
-        // unit's start the next one's scales, the ids of the one after and the
-        // record of the third are requested, and have that unit's time to arrive.
+        // 2j + 1 (four lanes for head_dim 64) fill stage j, so a stage costs no shuffles
+        // or divisions.  A unit needs its record, then its boxes' block ids, then their
+        // scales: at a unit's start the next one's scales, the ids of the one after and
+        // the record of the third are requested, and have that unit's time to arrive.
         auto load_block = [&](const int4& i) {
             const int32_t kk = i.y + lane * kBoxKeys;
             return kk < i.z ? a.bt[(int64_t)i.x * a.MB + kk / a.bs] : -2;      // -2: past the end
