@@ -95,10 +95,10 @@ struct Smem {
     StageMeta meta[kStages];
     alignas(16) float q_pow[kQPow][kMaxGroup];
     alignas(16) float warp_max[kBufs][kGroupWarps][kMaxGroup];
-    alignas(16) float warp_sum[kGroups][2][kGroupWarps][kMaxGroup];
+    alignas(16) float warp_sum[kGroups][2][kMaxGroup][kGroupWarps];
     // one group's share of a unit, for the group that finishes it
     alignas(16) float ex_o[kMaxGroup][D];
-    alignas(16) float ex_l[kGroupWarps][kMaxGroup];
+    alignas(16) float ex_l[kMaxGroup][kGroupWarps];
     alignas(16) float ex_m[kMaxGroup];
     uint64_t full[kStages], empty[kStages];
     uint64_t s_full[kBufs], p_full[kBufs], o_full[kBufs];
@@ -534,17 +534,30 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 }
             }
             if (!last) continue;
+            // the warp's sums, while the last P V runs: a lane passes on half of its heads
+            // at a step and ends with the sum of head lane / (32 / kHeads)
+#pragma unroll
+            for (int left = kHeads / 2, off = 16; off > 0; left >>= 1, off >>= 1) {
+                if (left > 0) {
+                    const bool upper = lane & off;
+#pragma unroll
+                    for (int h = 0; h < left; ++h) {
+                        const float give = upper ? l[h] : l[left + h];
+                        const float keep = upper ? l[left + h] : l[h];
+                        l[h] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+                    }
+                } else {
+                    l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
+                }
+            }
+            const int l_head = lane / (32 / kHeads);
+            const bool l_mine = lane % (32 / kHeads) == 0;
             if (!(ok = wait_warp(&sm.o_full[buf], par))) break;
             tc::tc_fence_after();
             tmem_ld<2 * kHeads>(lane_base + kTmemO + buf * kCols, t);
             tmem_wait<2 * kHeads>(t);
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                o[h] += fmaf(t[kHeads + h], 0.0625f, t[h]);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-            }
+            for (int h = 0; h < kHeads; ++h) o[h] += fmaf(t[kHeads + h], 0.0625f, t[h]);
             if (meta.j + 1 < meta.n) {
                 // the other group has the unit's last stage: hand this share over
                 // once the share before has been read
@@ -553,33 +566,28 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) {
                     if (dim >= 0) sm.ex_o[h][dim] = o[h];
-                    if (lane == 0) sm.ex_l[gw][h] = l[h];
                     if (key == 0) sm.ex_m[h] = m[h];
                 }
+                if (l_mine) sm.ex_l[l_head][gw] = l[0];
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sm.ex_full);
                 continue;
             }
-            float (*sums)[kMaxGroup] = sm.warp_sum[group][units & 1];
-            if (lane == 0) {
-#pragma unroll
-                for (int h = 0; h < kHeads; h += 2)
-                    *reinterpret_cast<float2*>(&sums[gw][h]) = make_float2(l[h], l[h + 1]);
-                tc::mbar_arrive(&sm.sum_bar[group]);
-            }
+            float (*sums)[kGroupWarps] = sm.warp_sum[group][units & 1];
+            if (l_mine) sums[l_head][gw] = l[0];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sm.sum_bar[group]);
             if (!(ok = wait_warp(&sm.sum_bar[group], units & 1))) break;
             ++units;
             const bool both = meta.n > 1;
             if (both && !(ok = wait_warp(&sm.ex_full, shared & 1))) break;
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
-                float L = 0.f, M = m[h], O = o[h];
-#pragma unroll
-                for (int x = 0; x < kGroupWarps; ++x) L += sums[x][h];
+                const float4 mine = *reinterpret_cast<const float4*>(sums[h]);
+                float L = (mine.x + mine.y) + (mine.z + mine.w), M = m[h], O = o[h];
                 if (both) {
-                    float L2 = 0.f;
-#pragma unroll
-                    for (int x = 0; x < kGroupWarps; ++x) L2 += sm.ex_l[x][h];
+                    const float4 other = *reinterpret_cast<const float4*>(sm.ex_l[h]);
+                    const float L2 = (other.x + other.y) + (other.z + other.w);
                     const float m2 = sm.ex_m[h];
                     M = fmaxf(M, m2);
                     const float u = M == -INFINITY ? 0.f : M;
