@@ -825,3 +825,102 @@ def test_decode_many_stages_a_cta(cuda, bs, group):
     rows = (kc.float() * ks[:, None, :, None]).to(torch.bfloat16)
     ref = pkv.paged_decode(q, rows, rows, bt, ctx, 0.05, 8192)
     U.assert_close(U.f64(out), U.f64(ref), "fp8 against bf16 decode")
+
+
+def _work(cuda, seed):
+    """Calls that take every kernel: the list form of the store, a decode with a plan
+    kernel and a combine, a prefill whose keys are split.  (inputs, call)"""
+    pkv = U.lib()
+    rng = np.random.default_rng(seed)
+    hkv, d, bs = 2, 128, 16
+    lens = [5000, 4600] + rng.integers(0, 60, 130).tolist()
+    pool = F.Pool(lens, bs, hkv, d, seed=seed)
+    cache = pool.on(cuda)
+    n = 2300
+    slots = torch.from_numpy(rng.permutation(pool.bt[0][:n // bs + 1])[:, None] * bs +
+                             np.arange(bs)).flatten()[:n].to(cuda, torch.int32)
+    x = [F.bf16(rng, n, hkv, d).to(cuda) for _ in "kv"]
+    qd = F.bf16(rng, len(lens), 4, d).to(cuda)
+    ctx = torch.tensor(lens, dtype=torch.int32, device=cuda)
+    qp = F.bf16(rng, 150, 4, d).to(cuda)
+    cu_q = torch.tensor([0, 130, 150], dtype=torch.int32, device=cuda)
+    cu_k = torch.tensor([0, 5130, 9750], dtype=torch.int32, device=cuda)
+
+    def call(c, stream=None):
+        pkv.kv_store_fp8(*x, *c[:4], slots, stream=stream)
+        a = pkv.paged_decode_fp8(qd, *c, ctx, 0.1, 5000, stream=stream)
+        b = pkv.paged_prefill_varlen_fp8(qp, x[0][:150], x[1][:150], *c[:4], cu_q, cu_k, 130, 5130,
+                                         c[4][:2].contiguous(), 0.1, stream=stream)
+        return a, b
+    return cache, call
+
+
+def test_calls_on_two_streams_at_once(cuda):
+    """Their scratch is their own: the results are those of one after the other."""
+    work = [_work(cuda, s) for s in (1, 2)]
+    want = []
+    for cache, call in work:
+        c = [t.clone() for t in cache]
+        want.append((call(c), c))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        caches = [[t.clone() for t in cache] for cache, _ in work]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in work]
+        got = [call(c, s) for (_, call), c, s in zip(work, caches, streams)]
+        torch.cuda.synchronize()
+        for g, c, (w, wc) in zip(got, caches, want):
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+                       for x, y in zip(c, wc))
+
+
+def test_captured_calls_replay_between_eager_ones(cuda):
+    work = [_work(cuda, s) for s in (3, 4)]
+    want = []
+    for cache, call in work:
+        c = [t.clone() for t in cache]
+        want.append(call(c))
+    graphs, held = [], []
+    caches = [[t.clone() for t in cache] for cache, _ in work]
+    torch.cuda.synchronize()
+    for (_, call), c in zip(work, caches):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(call(c))
+        graphs.append(g)
+    for _ in range(3):
+        for i in (0, 1):
+            for x in held[i]:
+                x.zero_()
+            graphs[i].replay()
+            eager = work[1 - i][1]([t.clone() for t in work[1 - i][0]])
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(held[i], want[i]))
+            assert all(torch.equal(x, y) for x, y in zip(eager, want[1 - i]))
+
+
+def test_split_prefill_infinities_and_nan(cuda):
+    """As the unsplit kernel: a query's NaN or infinity is its head's alone."""
+    pkv = U.lib()
+    rng = np.random.default_rng(6)
+    pool = F.Pool([4600], 64, 1, 128, seed=3)
+    kc, vc, ks, vs, bt = pool.on(cuda)
+    q = F.bf16(rng, 140, 2, 128).to(cuda)
+    k = F.bf16(rng, 140, 1, 128).to(cuda)
+    cu = [torch.tensor([0, n], dtype=torch.int32, device=cuda) for n in (140, 4740)]
+    run = lambda: pkv.paged_prefill_varlen_fp8(  # noqa: E731
+        q, k, k, kc, vc, ks, vs, *cu, 140, 4740, bt, 0.1)
+    clean = run()
+    q[3, 1, 0], q[131, 0, 77] = math.nan, math.inf
+    out = run()
+    touched = torch.zeros((140, 2), dtype=torch.bool, device=cuda)
+    touched[3, 1] = touched[131, 0] = True
+    assert torch.equal(out[~touched], clean[~touched])
+    assert out[touched].isnan().all()
+
+
+@pytest.mark.parametrize("bs", [16, 128])
+def test_split_prefill_of_short_sequences(cuda, bs):
+    """A stated maximum that asks for splits, and sequences that have none."""
+    _prefill(U.lib(), cuda, [3, 200, 1], [50, 0, 700], bs, 1, 2, 64, seed=bs, max_k=100000, extra=2)
