@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxSegment = 8192;            // entries per CTA
+constexpr int kSlack = 16;                   // entries more in shared memory, see in_at, out_at
 constexpr int kCtas = 4;                     // an SM, 48 KB of fp32 logits and words each
 // A word: bit 0 says that a prompt token was this entry, the bits above count
 // the generated ones; the entry was seen if the word is not zero.
@@ -99,14 +100,15 @@ __device__ __forceinline__ float penalise(float x, uint32_t word, const RowRules
     return x;
 }
 
-// kVec: every row of logits and out starts on 16 bytes.
+// kVec: every row of logits and out starts on 16 bytes (so that a thread reads only
+// what it staged, and a mask word holds a vector's bits).
 template <typename T, bool kVec, typename Word>
 __global__ void __launch_bounds__(kThreads, kCtas) logit_rules_kernel(RuleArgs a) {
     // the segment's logits, its words; at the end a 32-bit word an entry for the biases
     extern __shared__ uint4 smem[];
     uint4* const staged = smem;
-    uint4* const counts = reinterpret_cast<uint4*>(reinterpret_cast<T*>(smem) + a.segment);
-    Word* const words = reinterpret_cast<Word*>(counts);
+    uint4* const counts =
+        reinterpret_cast<uint4*>(reinterpret_cast<T*>(smem) + a.segment + kSlack);
     uint32_t* const last_bias = reinterpret_cast<uint32_t*>(smem);
     const int32_t b = blockIdx.y;
     const int32_t lo = blockIdx.x * a.segment;
@@ -118,22 +120,36 @@ __global__ void __launch_bounds__(kThreads, kCtas) logit_rules_kernel(RuleArgs a
     if (a.r.allowed_mask != nullptr)
         mask = a.r.allowed_mask + (int64_t)b * mask_words + (lo >> 5);   // lo % 32 == 0
 
-    // ---- the segment's logits, all in flight while the history is counted ----
+    // Rows that do not start on 16 bytes: entry i of the segment is staged at
+    // in_at + i, as far from 16 bytes as it is in memory; out's first 16 bytes begin
+    // with entry out_at, and the words are moved so that its word begins four.
     constexpr int E = 16 / sizeof(T);        // entries per load
+    const int in_at = kVec ? 0 : (int)((uintptr_t)row % 16 / sizeof(T));
+    const int out_at = kVec ? 0 : min(len, (int)(-((uintptr_t)out >> 2) & 3));
+    const int word_at = kVec ? 0 : -out_at & 3;
+    Word* const words = reinterpret_cast<Word*>(counts);     // entry i's at word_at + i
+    T* const entries = reinterpret_cast<T*>(smem) + in_at;
+
+    // ---- the segment's logits, all in flight while the history is counted ----
     constexpr int U = (kMaxSegment / E + kThreads - 1) / kThreads;
-    const int nv = kVec ? len / E : 0;
+    const int head = kVec ? 0 : min(len, -in_at & (E - 1));  // entries ahead of 16 bytes
+    const int nv = (len - head) / E;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int v = threadIdx.x + u * kThreads;
+        if (v < nv) cp_async16(entries + head + v * E, row + head + v * E);
+    }
     uint32_t allow[kVec ? U : 1];
     if constexpr (kVec) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int v = threadIdx.x + u * kThreads;
-            if (v < nv) cp_async16(staged + v, reinterpret_cast<const uint4*>(row) + v);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = threadIdx.x + u * kThreads;
             allow[u] = v < nv && mask ? __ldg(mask + (v * E >> 5)) : 0xffffffffu;
         }
+    } else {
+        const int i = threadIdx.x, j = head + nv * E + threadIdx.x;
+        if (i < head) entries[i] = row[i];
+        if (j < len) entries[j] = row[j];
     }
 
     // the row's first tokens, before its lengths are known (the row has max_tokens
@@ -190,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logit_rules_kernel(RuleArgs a
         p.penalties = n_tokens > 0 && (p.rep != 1.f || p.freq != 0.f || p.pres != 0.f);
     }
     if (p.penalties) {
-        for (int i = threadIdx.x; i < (len * (int)sizeof(Word) + 15) / 16; i += kThreads)
+        for (int i = threadIdx.x; i < ((len + 3) * (int)sizeof(Word) + 15) / 16; i += kThreads)
             counts[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         bool bad = false;
@@ -198,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logit_rules_kernel(RuleArgs a
             bad |= id >= a.vocab;
             const uint32_t at = (uint32_t)(id - lo);
             if (id < lo || at >= (uint32_t)len) return;
-            count_token(words, at, i < n_prompt);
+            count_token(words, at + word_at, i < n_prompt);
         };
 #pragma unroll
         for (int u = 0; u < kIds; ++u) {
@@ -262,28 +278,53 @@ __global__ void __launch_bounds__(kThreads, kCtas) logit_rules_kernel(RuleArgs a
         }
         for (int i = nv * E + threadIdx.x; i < len; i += kThreads) {
             float x = to_float(row[i]);
-            if (p.penalties) x = penalise(x, words[i], p);
+            if (p.penalties) x = penalise(x, words[word_at + i], p);
             if (mask && !(mask[i >> 5] >> (i & 31) & 1u)) x = -INFINITY;
             out[i] = x;
         }
     } else {
-        constexpr int kLoads = 8;
-        for (int i0 = threadIdx.x; i0 < len; i0 += kLoads * kThreads) {
-            T one[kLoads];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();                     // a vector of out lies across two of the row's
+        auto bits_at = [&](int i) {          // 32 entries' bits from i on
+            const uint32_t lo_bits = __ldg(mask + (i >> 5));
+            const int next = min((i >> 5) + 1, mask_words - 1 - (lo >> 5));
+            return __funnelshift_r(lo_bits, __ldg(mask + next), i & 31);
+        };
+        const int n4 = (len - out_at) / 4;
+#pragma unroll 4
+        for (int v = threadIdx.x; v < n4; v += kThreads) {
+            const int i = out_at + 4 * v;
+            float x[4];
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const int i = i0 + u * kThreads;
-                if (i < len) one[u] = row[i];
+            for (int e = 0; e < 4; ++e) x[e] = to_float(entries[i + e]);
+            bool changed = !a.in_place;
+            if (p.penalties) {
+                const uint4 w = four_words(words, word_at + i);
+                if ((w.x | w.y | w.z | w.w) != 0) {
+                    changed = true;
+                    x[0] = penalise(x[0], w.x, p);
+                    x[1] = penalise(x[1], w.y, p);
+                    x[2] = penalise(x[2], w.z, p);
+                    x[3] = penalise(x[3], w.w, p);
+                }
             }
+            const uint32_t bits = mask ? bits_at(i) & 15u : 15u;
+            if (bits != 15u) {
+                changed = true;
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const int i = i0 + u * kThreads;
-                if (i >= len) continue;
-                float x = to_float(one[u]);
-                if (p.penalties) x = penalise(x, words[i], p);
-                if (mask && !(__ldg(mask + (i >> 5)) >> (i & 31) & 1u)) x = -INFINITY;
-                out[i] = x;
+                for (int e = 0; e < 4; ++e)
+                    if (!(bits >> e & 1u)) x[e] = -INFINITY;
             }
+            if (changed) *reinterpret_cast<float4*>(out + i) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+        // ahead of the vectors and behind them
+        const int rest = out_at + len - (out_at + 4 * n4);
+        if ((int)threadIdx.x < rest) {
+            const int i = (int)threadIdx.x < out_at ? threadIdx.x : threadIdx.x + 4 * n4;
+            float x = to_float(entries[i]);
+            if (p.penalties) x = penalise(x, words[word_at + i], p);
+            if (mask && !(mask[i >> 5] >> (i & 31) & 1u)) x = -INFINITY;
+            out[i] = x;
         }
     }
 
@@ -348,13 +389,14 @@ int launch_rules(RuleArgs& a, cudaStream_t s) {
                      (a.stride * (int64_t)sizeof(T)) % 16 == 0 && a.vocab % 4 == 0;
     // 16-bit words hold a count of up to 32767 tokens (with a prompt's bit)
     const bool wide = a.r.token_ids && a.r.max_tokens > 32767;
-    const int smem = a.segment * ((int)sizeof(T) + (wide ? 4 : 2));
+    const int smem = (a.segment + kSlack) * ((int)sizeof(T) + (wide ? 4 : 2));
     void (*const kernel)(RuleArgs) =
         vec ? wide ? logit_rules_kernel<T, true, uint32_t> : logit_rules_kernel<T, true, uint16_t>
         : wide ? logit_rules_kernel<T, false, uint32_t>
                : logit_rules_kernel<T, false, uint16_t>;
     static std::atomic<uint64_t> configured[4];
-    if (!pkv_dynamic_smem_once((const void*)kernel, kMaxSegment * ((int)sizeof(T) + (wide ? 4 : 2)),
+    if (!pkv_dynamic_smem_once((const void*)kernel,
+                               (kMaxSegment + kSlack) * ((int)sizeof(T) + (wide ? 4 : 2)),
                                configured[vec * 2 + wide]))
         return PKV_ERR_CUDA;
     const unsigned segs = (unsigned)((a.vocab + a.segment - 1) / a.segment);

@@ -95,6 +95,29 @@ def test_rules_are_the_oracles(cuda, B, V, T, bias, mask, dtype, pad):
     _check(out, c)
 
 
+@pytest.mark.parametrize("V", [*range(1, 24), 8191, 8193, 9217])
+@pytest.mark.parametrize("dtype,skew,pad", [("fp32", 0, 0), ("fp32", 1, 2), ("fp32", 3, 5),
+                                            ("bf16", 5, 0), ("bf16", 0, 3), ("fp16", 7, 1)])
+def test_rows_anywhere_in_their_16_bytes(cuda, V, dtype, skew, pad):
+    """Rows of logits and of out that begin at every offset from 16 bytes, alike or not:
+    what lies around them is neither written nor read into the result."""
+    pkv = U.lib()
+    B = 9 if V < 1000 else 2
+    c = _case(V + skew, B, V, 12 if V < 1000 else 3, 3, V % 2 == 1, dtype, 0)
+    stride = V + pad
+    room = torch.full((skew + B * stride + 16,), math.nan, dtype=TYPES[dtype], device=cuda)
+    logits = room[skew:skew + B * stride].view(B, stride)[:, :V]
+    logits.copy_(c["logits"])
+    for lead in range(4):
+        wide = torch.full((lead + B * V + 8,), 7.0, device=cuda)
+        out = wide[lead:lead + B * V].view(B, V)
+        st = pkv.new_status(cuda)
+        pkv.apply_logit_rules(logits, **_args(c, cuda), out=out, status=st)
+        assert U.status_word(st) in (0, pkv.STATUS["NO_ALLOWED_TOKEN"])
+        _check(out, c)
+        assert (wide[:lead] == 7.0).all() and (wide[lead + B * V:] == 7.0).all()
+
+
 @pytest.mark.parametrize("T", [32766, 32767, 32768, 70000])
 @pytest.mark.parametrize("V,dtype", [(72, "fp32"), (73, "fp32"), (72, "bf16")])
 def test_long_histories(cuda, T, V, dtype):
