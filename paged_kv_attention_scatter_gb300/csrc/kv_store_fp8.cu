@@ -104,7 +104,8 @@ struct BlockRows {
     int32_t rows, token0, offset0;
     bool dense;
     uint32_t amax[kThreads / 8];             // per lane group
-    float ratio[kThreads / 8];               // per pair in hand: old / new scale where it grew
+    float ratio[kThreads / 8];               // per pair in hand: old / new scale where it grew,
+                                             // else -1 (the quotient may round to 0)
 };
 
 // Larger magnitudes of the bf16 pairs of a vector and of `m`, two 16-bit lanes.
@@ -257,7 +258,7 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, c
             __syncthreads();                 // every group has read its old scale too
             for (int g = 0; g < gpp; ++g) m = max(m, sm.amax[group - sub + g]);
         }
-        float ratio = 0.f;
+        float ratio = -1.f;
         if (live) {
             if (!(old == 0.f || pkv::scale_ok(old))) {
                 if (lane == 0 && sub == 0) pkv::report(a.status, PKV_STATUS_BAD_SCALE);
@@ -289,13 +290,13 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, BlockRows& sm, c
         }
         if (lane == 0 && sub == 0) sm.ratio[group / gpp] = ratio;
         // (this barrier also lets the next round's maxima be written)
-        if (!__syncthreads_or(ratio > 0.f)) continue;
+        if (!__syncthreads_or(ratio >= 0.f)) continue;
         // ---- blocks that grew: their other rows, the whole CTA on one pair at a
         // time (a decode step's pair has one lane group, and 256 rows one after
         // another would take as long as the rest of the step) ----
         for (int p = 0; p < at_once; ++p) {
             const float r = sm.ratio[p];
-            if (!(r > 0.f)) continue;
+            if (!(r >= 0.f)) continue;
             const int pr = part + (i0 + p) * parts;
             uint8_t* base = ((pr & 1) ? a.vc : a.kc) + (int64_t)blk * a.bs * row_codes +
                             (pr >> 1) * D + lane * 8;
