@@ -487,8 +487,10 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 l[h] *= alpha[h];
 #pragma unroll
                 for (int x = 0; x < kSub; ++x) {
-                    // 16 p, as split_e4m3 takes it; l is summed in sixteenths of iv
-                    y[x][h] = pkv::fast_exp2(y[x][h] - (u - 12.f));
+                    // 16 p, as split_e4m3 takes it; l is summed in sixteenths of iv.  (The
+                    // difference first: u - 12 is rounded where u is large, and 16 p
+                    // would be 2^16 for the largest key of scores around 2^27.)
+                    y[x][h] = pkv::fast_exp2((y[x][h] - u) + 12.f);
                     l[h] = fmaf(y[x][h], iv[x], l[h]);
                 }
             }
