@@ -727,9 +727,11 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 if ((x & 0x7fff0000u) == 0x7f800000u) x |= 0x400000u;
                 return x;
             };
-            // largest entry 1.f * 2^(E - 127) to 1.f * 2^7, where that power and its
-            // inverse are normal fp32 numbers
-            const int e = min(max(7 - ((int)(mag >> 7) - 127), -113), 113);
+            // largest entry 1.f * 2^(E - 127) to 1.f * 2^7: e >= -120, as E <= 254.  At
+            // most 2^120, so that 16 times it and its inverse are normal fp32 numbers:
+            // rows below 2^-113 stay below 2^7, but 2^120 takes bf16's smallest step,
+            // 2^-133, to the second part's, 2^-13, so they are held exactly too.
+            const int e = min(7 - ((int)(mag >> 7) - 127), 120);
             const float up16 = __int_as_float((e + 4 + 127) << 23);
             uint32_t hi[4 * kChunks], lo[4 * kChunks];       // the codes of either part
 #pragma unroll

@@ -60,3 +60,26 @@ def test_scores_of_any_size(cuda, bs, d, n, most, group):
         got = _decode(pkv, cuda, q, pool, scale, most)
         want = pool.values("v")[pool.bt[0, at // bs], at % bs, 0]
         np.testing.assert_array_equal(got, np.broadcast_to(want, got.shape), err_msg=str(top))
+
+
+@pytest.mark.parametrize("bs,d", [(16, 128), (64, 128), (40, 64)])
+@pytest.mark.parametrize("q_mag", [6e37, 1e37, 1e36, 1e-31, 1e-33, 1e-35, 1e-37, 1e-39])
+def test_queries_of_any_size(cuda, bs, d, q_mag):
+    """Down to bf16's subnormals and up to its largest values, with key scales and a
+    softmax scale that make the scores ordinary."""
+    pkv = U.lib()
+    rng = np.random.default_rng(11)
+    hkv, group, lens = 2, 4, [200, 77]
+    pool = F.Pool(lens, bs, hkv, d, seed=4)
+    # the keys' scales take what they can of it (2^-96 .. 2^127), the softmax scale the rest
+    exp = -round(math.log2(q_mag))
+    k_exp = min(max(exp, -80), 120)
+    pool.scale["k"] = np.ldexp(pool.scale["k"], k_exp).astype(np.float32)
+    scale = math.ldexp(0.125, exp - k_exp)
+    q = F.bf16(rng, 2, hkv * group, d, mag=q_mag)
+    assert torch.isfinite(q).all() and (q != 0).float().mean() > 0.9
+    q[0, 0, :5] = 0.0
+    q[1, 3] = 0.0
+    if q_mag > 1:
+        q[1, 0, 7] = -torch.finfo(torch.bfloat16).max
+    _check(_decode(pkv, cuda, q, pool, scale), q, pool, scale)
