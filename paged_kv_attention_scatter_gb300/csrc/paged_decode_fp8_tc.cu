@@ -390,6 +390,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         float m[kHeads], l[kHeads], o[kHeads], xs[kHeads];
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) m[h] = l[h] = o[h] = xs[h] = 0.f;
+        bool wide = false;                       // some |xs| > 1: ks xs may overflow
         bool ok = true;
         for (uint32_t c = 0;; ++c, ring.next(kGroups)) {     // this group's stages
             const int buf = 2 * group + (c & 1), before = 2 * group + ((c & 1) ^ 1);
@@ -416,9 +417,11 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 tmem_ld<2 * kHeads>(lane_base + (buf * kSub + u) * kCols, s[u]);
             tmem_wait<kSub * 2 * kHeads>(&s[0][0]);
             if (first) {                         // (the S issuer has waited for Q)
+                wide = false;
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) {
                     xs[h] = a.scale_log2 * sm.q_pow[meta.unit % kQPow][h];
+                    wide = wide || fabsf(xs[h]) > 1.f;
                     m[h] = -INFINITY;
                     l[h] = o[h] = 0.f;
                 }
@@ -435,6 +438,13 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     const float2 x = fma2(dot, k, both(lv[u]));
                     y[u][h] = x.x;
                     y[u][h + 1] = x.y;
+                    // queries past 2^7 / scale: a dot of zero stays zero whatever the
+                    // scales, and a product overflows only where the score does
+                    if (wide) {
+                        if (fabsf(xs[h]) > 1.f) y[u][h] = fmaf(dot.x * ks[u], xs[h], lv[u]);
+                        if (fabsf(xs[h + 1]) > 1.f)
+                            y[u][h + 1] = fmaf(dot.y * ks[u], xs[h + 1], lv[u]);
+                    }
                 }
                 if (!__all_sync(0xffffffffu, counts[u])) {
 #pragma unroll

@@ -83,3 +83,22 @@ def test_queries_of_any_size(cuda, bs, d, q_mag):
     if q_mag > 1:
         q[1, 0, 7] = -torch.finfo(torch.bfloat16).max
     _check(_decode(pkv, cuda, q, pool, scale), q, pool, scale)
+
+
+@pytest.mark.parametrize("bs,d", [(16, 128), (64, 128), (24, 64)])
+@pytest.mark.parametrize("q_exp", [20, 60])
+def test_zero_keys_under_a_large_scale(cuda, bs, d, q_exp):
+    """A block of zero K codes under a scale of 2^125 beside queries of 2^20 and more: the scores
+    of its keys are zero, not zero times an overflow."""
+    pkv = U.lib()
+    rng = np.random.default_rng(bs + q_exp)
+    lens = [4 * bs + 5, 3 * bs]
+    pool = F.Pool(lens, bs, 1, d, seed=bs)
+    pool.scale["k"] = np.ldexp(pool.scale["k"], -q_exp).astype(np.float32)
+    for row in pool.bt:
+        blk = int(row[1])
+        pool.scale["k"][blk] = 2.0 ** 125
+        pool.codes["k"][blk] = rng.choice(np.asarray([0, 0x80], np.uint8), pool.codes["k"][blk].shape)
+    q = F.bf16(rng, 2, 8, d, mag=2.0 ** q_exp)
+    q[:, ::3] = F.bf16(rng, 2, 3, d)             # heads of ordinary size in the same unit
+    _check(_decode(pkv, cuda, q, pool, 0.125), q, pool, 0.125)
