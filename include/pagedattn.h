@@ -447,6 +447,11 @@ PKV_API size_t pkv_paged_decode_fp8_workspace_bytes(int32_t batch, int32_t num_q
  * paged_decode over an e4m3 cache: arguments and result as in
  * pkv_paged_decode, with K and V rows code * scale.  The keys of a block whose K or V scale cannot be
  * used are left out, as are those of a block id outside the pool.
+ * V scales may differ by any factor within a sequence: every key counts in the softmax's sum.
+ * In the sum of V rows a key's share (its weight times its V scale) is held to 2^-9 + 2^-11
+ * of itself or to 2^-22 of the largest share among the keys attended together (2048 at most),
+ * whichever is more: beside keys of the same weight and a V scale 2^13 larger, a small block's
+ * values keep 9 bits, beside 2^20 two.
  */
 PKV_API int pkv_paged_decode_fp8(const void* q, const void* k_cache, const void* v_cache,
                                  const float* k_scale, const float* v_scale,

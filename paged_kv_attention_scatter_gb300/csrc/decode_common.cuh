@@ -36,8 +36,6 @@ struct DecodeArgs {
     // No plan in the workspace: the kernels take the schedule of a batch of at
     // most kMaxInline sequences from `ctx` themselves (WarpPlan).
     int32_t inline_plan;
-    // The combine kernel: a row whose weights are NaN comes out as NaN (else as zeros).
-    int32_t keep_nan;
 };
 
 // The chunk schedule of at most kMaxInline sequences, held by a warp: lane l has
@@ -135,7 +133,7 @@ int pkv_launch_decode_tma(pkv::DecodeArgs& a, int head_dim, cudaStream_t s);
 
 // Pieces of pkv_paged_decode (paged_decode.cu) that the decode over an e4m3
 // cache shares, with a chunk length of its own: the workspace, the argument checks
-// (the cache pointers are checked and stored untyped), the plan kernel, and the
+// (the cache pointers are checked and stored untyped), the plan kernel, and its
 // combine kernel as a programmatic dependent of the split kernel before it.
 size_t pkv_decode_workspace(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
                             const pkv_cache_desc& cache, int32_t chunk_keys);

@@ -376,8 +376,12 @@ constexpr int kCombineHeads = 4;     // q heads per combine CTA, one warp each
 // One warp per (sequence, q head); lane l owns head_dim elements
 // [l*D/32, (l+1)*D/32).  The chunks' (max, sum) pairs and partial outputs of up
 // to 16 chunks are loaded at once and merged online (base 2), so a sequence of
-// up to 16 chunks costs one round trip; no block-wide reduction.
-template <int D>
+// up to 16 chunks costs one round trip; no block-wide reduction.  kScales: partials of
+// the decode over an e4m3 cache, whose maxima hold V's scales (paged_decode_fp8.cu).
+// Chunks' sums then count although their maxima are hundreds of powers of two
+// apart, so a sum is scaled in two steps of half the power; a row whose weights are
+// NaN is NaN (else zeros); and there may be no plan in the workspace.
+template <int D, bool kScales>
 __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(DecodeArgs a) {
     constexpr int E = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
     // allow it only after their own wait for the plan), so it is read ahead
     // of the wait for the split kernel's partials.
     int32_t p0, n;
-    if (a.inline_plan) {
+    if (kScales && a.inline_plan) {
         const int2 f = pkv::WarpPlan(a).of(b);
         p0 = f.x;
         n = f.y;
@@ -433,25 +437,39 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
 #pragma unroll
         for (int c = 0; c < kCombineBatch; ++c) {
             mb = fmaxf(mb, ml[c].x);
-            nan = nan || ml[c].y != ml[c].y;
+            if (kScales) nan = nan || ml[c].y != ml[c].y;
         }
         if (mb == -INFINITY) continue;                   // nothing visible yet
-        const float r = (M == -INFINITY) ? 0.f : pkv::fast_exp2(M - mb);
-        L *= r;
+        float r, half = 0.f;                 // half * half: r
+        if constexpr (kScales) {
+            half = (M == -INFINITY) ? 0.f : pkv::fast_exp2(0.5f * (M - mb));
+            r = half * half;
+            L = L * half * half;
+        } else {
+            r = (M == -INFINITY) ? 0.f : pkv::fast_exp2(M - mb);
+            L *= r;
+        }
 #pragma unroll
         for (int e = 0; e < E; ++e) O[e] *= r;
 #pragma unroll
         for (int c = 0; c < kCombineBatch; ++c) {
             if (ml[c].x == -INFINITY) continue;
-            const float f = pkv::fast_exp2(ml[c].x - mb);
-            L += ml[c].y * f;
+            float f;
+            if constexpr (kScales) {
+                half = pkv::fast_exp2(0.5f * (ml[c].x - mb));
+                f = half * half;
+                L = fmaf(ml[c].y * half, half, L);
+            } else {
+                f = pkv::fast_exp2(ml[c].x - mb);
+                L += ml[c].y * f;
+            }
 #pragma unroll
             for (int e = 0; e < E; ++e) O[e] += ov[c][e] * f;
         }
         M = mb;
     }
-    if (a.keep_nan && nan) L = CUDART_NAN_F;
-    const bool some = L > 0.f || (a.keep_nan && L != L);
+    if (kScales && nan) L = CUDART_NAN_F;
+    const bool some = L > 0.f || (kScales && L != L);
     __nv_bfloat16* dst = a.out + (pkv::row_of(a, b) * a.Hq + h) * D + d0;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
@@ -540,14 +558,14 @@ int max_resident(const void* fn) {
 enum class PlanLaunch { kPlain, kWithStore, kNone };
 
 // The combine kernel, a programmatic dependent of the split kernel before it.
-template <int D>
+template <int D, bool kScales>
 int launch_combine(const DecodeArgs& a, cudaStream_t s) {
     for (int32_t b0 = 0; b0 < a.B; b0 += 65535) {
         DecodeArgs sub = a;
         const int32_t rows = a.B - b0 < 65535 ? a.B - b0 : 65535;
         sub.b0 = b0;
         const unsigned hblocks = (unsigned)((a.Hq + kCombineHeads - 1) / kCombineHeads);
-        if (launch_dependent(decode_combine_kernel<D>, dim3(hblocks, (unsigned)rows),
+        if (launch_dependent(decode_combine_kernel<D, kScales>, dim3(hblocks, (unsigned)rows),
                              dim3(32 * kCombineHeads), s, sub) != cudaSuccess)
             return PKV_ERR_CUDA;
     }
@@ -581,7 +599,7 @@ int launch_decode(DecodeArgs& a, cudaStream_t s, PlanLaunch plan = PlanLaunch::k
                              a) != cudaSuccess)
             return PKV_ERR_CUDA;
     }
-    return launch_combine<D>(a, s);
+    return launch_combine<D, false>(a, s);
 }
 
 }  // namespace
@@ -637,7 +655,6 @@ int make_plan_args(const int32_t* context_lens, int32_t batch, int32_t num_q_hea
     a.b0 = 0;
     a.wait_polls = pkv_wait_polls();
     a.inline_plan = 0;
-    a.keep_nan = 0;
     return PKV_OK;
 }
 
@@ -705,7 +722,7 @@ int pkv_launch_decode_plan(const DecodeArgs& a, cudaStream_t s) {
 }
 
 int pkv_launch_decode_combine(const DecodeArgs& a, int head_dim, cudaStream_t s) {
-    return head_dim == 128 ? launch_combine<128>(a, s) : launch_combine<64>(a, s);
+    return head_dim == 128 ? launch_combine<128, true>(a, s) : launch_combine<64, true>(a, s);
 }
 
 extern "C" int pkv_paged_decode(const void* q, const void* k_cache, const void* v_cache,

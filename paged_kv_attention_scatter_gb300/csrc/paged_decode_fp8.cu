@@ -11,9 +11,15 @@
 //   p_j = 2^(y_j - M) = 2^(x_j - M) vs_j,
 //   O = sum p_j V8_j,   L = sum p_j / vs_j,   out = O / L,
 // so p is at most 1 whatever the scales, one exponential serves both sums, and a
-// (M, L, O) triple merges across chunks as in the bf16 decode: the plan and
-// the combine kernel are that decode's.  The split kernel is in
-// paged_decode_fp8_tc.cu; this file has the entry points.
+// (M, L, O) triple merges across chunks as in the bf16 decode, with that decode's plan
+// kernel.  The scales span 2^224, more than fp32's exponent does below 1: a key of a
+// small scale beside one of a large scale may have no p left, but its share of L has
+// to count.  So p is squared up from g = 2^((y - M) / 2), which is normal down to
+// y - M = -252, and L sums (g / sqrt(vs))^2; where M rises or triples merge, L is
+// scaled by half the power twice.  O loses nothing that shows: a key's part of it is
+// held to 2^-9 of itself or 2^-22 of the largest p (paged_decode_fp8_tc.cu), that is of
+// the largest product of a weight and a V scale among the at most 2048 keys of a unit.
+// The split kernel is in paged_decode_fp8_tc.cu; this file has the entry points.
 #include "fp8_common.cuh"
 
 namespace {
@@ -54,7 +60,6 @@ int32_t choose_chunk_keys(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
 int launch_decode(Fp8DecodeArgs& fa, int head_dim, bool plan, cudaStream_t s) {
     int rc = PKV_OK;
     fa.d.inline_plan = plan && fa.d.B <= pkv::kMaxInline;
-    fa.d.keep_nan = 1;
     fa.no_combine = fa.d.max_ctx <= fa.d.chunk_keys;
     if (plan && !fa.d.inline_plan) rc = pkv_launch_decode_plan(fa.d, s);
     if (rc != PKV_OK) return rc;

@@ -91,7 +91,7 @@ struct Smem {
     alignas(16) uint8_t p[kBufs][kStageKeys * kCols];
     float ks[kStages][kStageKeys];               // per key (gathered) or box: K scale,
     float lv[kStages][kStageKeys];               // log2 of V's (-inf: does not count),
-    float iv[kStages][kStageKeys];               // its inverse
+    float rv[kStages][kStageKeys];               // 16 / sqrt(V's)
     StageMeta meta[kStages];
     alignas(16) float q_pow[kQPow][kMaxGroup];
     alignas(16) float warp_max[kBufs][kGroupWarps][kMaxGroup];
@@ -399,14 +399,14 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             const StageMeta meta = sm.meta[ring.slot];
             if (meta.n == 0) break;
             const bool first = meta.j < kGroups, last = meta.j + kGroups >= meta.n;
-            float ks[kSub], lv[kSub], iv[kSub];
+            float ks[kSub], lv[kSub], rv[kSub];
             bool counts[kSub];
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
                 const int mine = kGather ? key + 128 * u : (key + 128 * u) / kBoxKeys;
                 ks[u] = sm.ks[ring.slot][mine];
                 lv[u] = sm.lv[ring.slot][mine];
-                iv[u] = sm.iv[ring.slot][mine] * 0.0625f;
+                rv[u] = sm.rv[ring.slot][mine];
                 counts[u] = lv[u] != -INFINITY && (kGather || key + 128 * u < meta.keys);
             }
             if (!(ok = wait_warp(&sm.s_full[buf], par))) break;
@@ -488,21 +488,36 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     }
                 }
             }
+            // Weights by their square roots: g = 2^((y - u) / 2) is normal down to y - u =
+            // -252 and l's term is (g rv)^2 = 256 g^2 / vs, so a key counts there however
+            // small its V scale is beside the largest (p itself may vanish, and may: it
+            // is its share of O).  The difference is rounded once: an offset in the
+            // exponent would be lost in scores around 2^27.
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                const float mn = use[h];
-                const float u = mn == -INFINITY ? 0.f : mn;
-                alpha[h] = pkv::fast_exp2(m[h] - u);         // 0 from -inf
-                m[h] = mn;
-                l[h] *= alpha[h];
+            for (int h = 0; h < kHeads; h += 2) {
+                const float2 u = make_float2(use[h] == -INFINITY ? 0.f : use[h],
+                                             use[h + 1] == -INFINITY ? 0.f : use[h + 1]);
+                const float2 a2 = make_float2(pkv::fast_exp2(0.5f * (m[h] - u.x)),    // 0 from -inf
+                                              pkv::fast_exp2(0.5f * (m[h + 1] - u.y)));
+                const float2 squared = mul2(a2, a2);
+                float2 sum = mul2(mul2(make_float2(l[h], l[h + 1]), a2), a2);
+                alpha[h] = squared.x;
+                alpha[h + 1] = squared.y;
+                m[h] = use[h];
+                m[h + 1] = use[h + 1];
 #pragma unroll
                 for (int x = 0; x < kSub; ++x) {
-                    // 16 p, as split_e4m3 takes it; l is summed in sixteenths of iv.  (The
-                    // difference first: u - 12 is rounded where u is large, and 16 p
-                    // would be 2^16 for the largest key of scores around 2^27.)
-                    y[x][h] = pkv::fast_exp2((y[x][h] - u) + 12.f);
-                    l[h] = fmaf(y[x][h], iv[x], l[h]);
+                    const float2 e = fma2(make_float2(y[x][h], y[x][h + 1]), both(0.5f),
+                                          mul2(u, both(-0.5f)));
+                    const float2 g = make_float2(pkv::fast_exp2(e.x), pkv::fast_exp2(e.y));
+                    const float2 t = mul2(g, both(rv[x]));
+                    sum = fma2(t, t, sum);
+                    const float2 p16 = mul2(mul2(g, g), both(4096.f));   // as split_e4m3 takes it
+                    y[x][h] = p16.x;
+                    y[x][h + 1] = p16.y;
                 }
+                l[h] = sum.x;
+                l[h + 1] = sum.y;
             }
             // ---- the keys' rows of P: bytes h the first parts, kHeads + h the second ----
 #pragma unroll
@@ -603,9 +618,10 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     const float m2 = sm.ex_m[h];
                     M = fmaxf(M, m2);
                     const float u = M == -INFINITY ? 0.f : M;
-                    const float f1 = pkv::fast_exp2(m[h] - u), f2 = pkv::fast_exp2(m2 - u);
-                    L = fmaf(L, f1, L2 * f2);
-                    if (dim >= 0) O = fmaf(O, f1, sm.ex_o[h][dim] * f2);
+                    const float f1 = pkv::fast_exp2(0.5f * (m[h] - u));
+                    const float f2 = pkv::fast_exp2(0.5f * (m2 - u));
+                    L = fmaf(L * f1, f1, L2 * f2 * f2);
+                    if (dim >= 0) O = fmaf(O, f1 * f1, sm.ex_o[h][dim] * (f2 * f2));
                 }
                 if (h >= meta.nh || dim < 0) continue;
                 const int64_t at = (int64_t)meta.row + meta.h0 + h;
@@ -823,7 +839,8 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 pkv::report(a.status, inside ? PKV_STATUS_BAD_SCALE : PKV_STATUS_BAD_BLOCK_ID);
             const float ks = good ? ks_in : 0.f;
             const float lv = good ? __log2f(vs_in) : -INFINITY;
-            const float iv = good ? __frcp_rn(vs_in) : 0.f;
+            // (good to 2^-22; __frsqrt_rn cost 1.5 us of 77 where every key has one)
+            const float rv = good ? 16.f * rsqrtf(vs_in) : 0.f;
             const uint32_t goods = __ballot_sync(0xffffffffu, good);
             const int32_t row = blk * a.bs + (key0 + lane * kBoxKeys) % a.bs;
             StageMeta m;
@@ -848,7 +865,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 if (in_stage) {
                     sm.ks[ring.slot][i] = ks;
                     sm.lv[ring.slot][i] = lv;
-                    sm.iv[ring.slot][i] = iv;
+                    sm.rv[ring.slot][i] = rv;
                     if (i == 0) {
                         m.j = j;
                         m.keys = keys - j * kStageKeys;
@@ -1020,7 +1037,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 const int key = row0 + lane + 32 * i;
                 sm.ks[slot][key] = good ? ks[i] : 0.f;
                 sm.lv[slot][key] = good ? __log2f(vs[i]) : -INFINITY;
-                sm.iv[slot][key] = good ? __frcp_rn(vs[i]) : 0.f;
+                sm.rv[slot][key] = good ? 16.f * rsqrtf(vs[i]) : 0.f;
             }
             // the team's next stage: its block ids arrive while the copies land
             for (int i = 0; i < kTeams && un.sc < sched.chunks; ++i) step();

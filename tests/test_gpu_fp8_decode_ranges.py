@@ -102,3 +102,67 @@ def test_zero_keys_under_a_large_scale(cuda, bs, d, q_exp):
     q = F.bf16(rng, 2, 8, d, mag=2.0 ** q_exp)
     q[:, ::3] = F.bf16(rng, 2, 3, d)             # heads of ordinary size in the same unit
     _check(_decode(pkv, cuda, q, pool, 0.125), q, pool, 0.125)
+
+
+# the V scales' exponents by block
+SPREADS = [(-64, 110), (110, -64), (-96, 112), (-75, 75), (100, -40), (0, 13), (13, 0), (-7, -20)]
+
+
+@pytest.mark.parametrize("bs,d", [(16, 128), (64, 128), (256, 64), (24, 64)])
+# one unit of several stages, units of one stage, units of 2048 keys
+@pytest.mark.parametrize("lens,most", [([500, 90], 500), ([3000, 1300], 3000),
+                                       ([5000, 1300], 1 << 20)])
+@pytest.mark.parametrize("halves", [False, True])    # small and large blocks in two halves, in turn
+def test_value_scales_far_apart(cuda, bs, d, lens, most, halves):
+    """Blocks whose V scales differ by up to 2^208: the small ones' keys carry their weight
+    in the normaliser, whether they come before the large ones or behind them."""
+    pkv = U.lib()
+    rng = np.random.default_rng(bs)
+    for lo, hi in SPREADS:
+        pool = F.Pool(lens, bs, 1, d, seed=bs, spread=0)
+        exps = np.full(pool.scale["v"].shape[0], hi)
+        for row, n in zip(pool.bt, lens):
+            used = row[:-(-n // bs)]
+            exps[used[:len(used) // 2] if halves else used[::2]] = lo
+        pool.scale["v"] = np.ldexp(np.ones_like(pool.scale["v"]), exps[:, None]).astype(np.float32)
+        q = F.bf16(rng, len(lens), 8, d)
+        _check(_decode(pkv, cuda, q, pool, 0.125, most), q, pool, 0.125)
+
+
+@pytest.mark.parametrize("bs,d", [(16, 128), (64, 128), (24, 64)])
+@pytest.mark.parametrize("apart", [0, 6, 13])
+@pytest.mark.parametrize("n,most", [(500, 500), (5000, 1 << 20)])
+def test_small_values_beside_large_ones(cuda, bs, d, apart, n, most):
+    """Every second block's V scale is 2^apart larger, but its codes are zero in half of the
+    entries, where the output is made of the small blocks' values alone.  Entry by entry, with
+    s_j = w_j vs_j the share of a key (its weight times its V scale) and C its codes:
+    each share is kept to r of itself (2^-9 + 2^-11) or 2^-22 of the largest, and the
+    log weights to d as in fp8_util, so
+      |out - ref| <= 2^-8 |ref| + sum_j |C_j| (s_j (r + 2 d) + 2^-22 max s)."""
+    pkv = U.lib()
+    rng = np.random.default_rng(bs + apart)
+    pool = F.Pool([n], bs, 1, d, seed=bs, spread=0)
+    large = pool.bt[0, ::2]
+    pool.scale["v"][large] *= np.float32(2.0 ** apart)
+    zeros = pool.codes["v"][large][..., :d // 2]
+    pool.codes["v"][np.ix_(large, range(bs), [0], range(d // 2))] = np.where(zeros == 0x7F, 0x7F, 0)
+    q = F.bf16(rng, 1, 4, d)
+    scale = 0.125
+    got = _decode(pkv, cuda, q, pool, scale, most)
+    rows = lambda x: x[pool.bt[0, np.arange(n) // bs], np.arange(n) % bs, 0]  # noqa: E731
+    K, V = rows(pool.values("k")), rows(pool.values("v"))
+    vs = pool.scale["v"].astype(np.float64)[pool.bt[0, np.arange(n) // bs], 0]
+    C = np.abs(V) / vs[:, None]
+    for h in range(4):
+        qh = U.f64(q)[0, h]
+        x = scale * (K @ qh)
+        w = np.exp(x - x.max())
+        s = w / w.sum() * vs
+        ref = (w / w.sum()) @ V
+        big_x = scale * (np.abs(K) @ np.abs(qh)).max()
+        worst_q = scale * np.abs(qh).max() * np.abs(K).sum(1).max()
+        dx = (128 * 2.0 ** -23 + 2.0 ** -21) * big_x + 2.0 ** -21 * worst_q + 2.0 ** -20
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -9 + 2.0 ** -11 + 2 * dx) * (s @ C) + \
+            2.0 ** -22 * s.max() * C.sum(0)
+        err = np.abs(got[0, h] - ref)
+        assert (err <= tol).all(), (err / tol).max()
