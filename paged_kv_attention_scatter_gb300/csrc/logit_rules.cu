@@ -244,6 +244,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) logit_rules_kernel(RuleArgs a
         }
         if (bad && lo == 0) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
         __syncthreads();
+    } else if (lo == 0 && a.status != nullptr) {
+        // penalties that change nothing: the tokens are only checked
+        bool bad = false;
+        for (int32_t i = threadIdx.x; i < n_tokens; i += kThreads)
+            bad |= __ldg(ids + i) >= a.vocab;
+        if (bad) pkv::report(a.status, PKV_STATUS_BAD_TOKEN_ID);
     }
 
     // ---- one pass over the segment ----
