@@ -19,7 +19,7 @@ struct DecodeArgs {
     __nv_bfloat16* out;
     int32_t* chunk_prefix;           // [B+1] exclusive prefix of chunk counts
     int4* chunk_info;                // [cap]: (sequence, first key, end key, chunks of it)
-    float2* part_ml;                 // [cap * Hq]: (max, sum) in base 2
+    float2* part_ml;                 // [cap * Hq]: (max, sum) in base 2 (e4m3 cache: max halved)
     float* part_o;                   // [cap * Hq * D]
     int32_t B, Hq, Hkv, G, n_hg, MB, NB, bs, max_ctx, chunk_keys, cap;
     float scale_log2;

@@ -379,8 +379,9 @@ constexpr int kCombineHeads = 4;     // q heads per combine CTA, one warp each
 // up to 16 chunks costs one round trip; no block-wide reduction.  kScales: partials of
 // the decode over an e4m3 cache, whose maxima hold V's scales (paged_decode_fp8.cu).
 // Chunks' sums then count although their maxima are hundreds of powers of two
-// apart, so a sum is scaled in two steps of half the power; a row whose weights are
-// NaN is NaN (else zeros); and there may be no plan in the workspace.
+// apart: the maxima come halved, and a sum is scaled in two steps of half the power.
+// A row whose weights are NaN is NaN (else zeros), and there may be no plan in the
+// workspace.
 template <int D, bool kScales>
 __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(DecodeArgs a) {
     constexpr int E = D / 32;
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
         if (mb == -INFINITY) continue;                   // nothing visible yet
         float r, half = 0.f;                 // half * half: r
         if constexpr (kScales) {
-            half = (M == -INFINITY) ? 0.f : pkv::fast_exp2(0.5f * (M - mb));
+            half = (M == -INFINITY) ? 0.f : pkv::fast_exp2(M - mb);
             r = half * half;
             L = L * half * half;
         } else {
@@ -453,13 +454,13 @@ __global__ void __launch_bounds__(32 * kCombineHeads) decode_combine_kernel(Deco
         for (int e = 0; e < E; ++e) O[e] *= r;
 #pragma unroll
         for (int c = 0; c < kCombineBatch; ++c) {
-            if (ml[c].x == -INFINITY) continue;
             float f;
             if constexpr (kScales) {
-                half = pkv::fast_exp2(0.5f * (ml[c].x - mb));
+                half = pkv::fast_exp2(ml[c].x - mb);         // 0 for a chunk without keys
                 f = half * half;
                 L = fmaf(ml[c].y * half, half, L);
             } else {
+                if (ml[c].x == -INFINITY) continue;
                 f = pkv::fast_exp2(ml[c].x - mb);
                 L += ml[c].y * f;
             }

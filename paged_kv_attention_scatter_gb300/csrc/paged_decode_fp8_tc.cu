@@ -13,7 +13,8 @@
 //     to [2^7, 2^8).  A bf16 has 8 significant bits, so q1 rounds to the first 4
 //     and q2 holds the rest exactly, down to 2^-22 of the row's largest entry.
 //   p = 2^(y - M + 8) <= 256 likewise: off by 2^-9 of itself, or 2^-22 of the
-//     row's largest weight.
+//     row's largest weight.  (Scores past 2^20 have a step of their own of 2^-3 and
+//     more; M may be rounded up there by up to 12, and p smaller by as much.)
 // M is the running maximum over all keys of the unit that a softmax group has seen: its four
 // warps exchange their maxima each stage, so no p exceeds 256.  (A reference that
 // lags, redone when it is passed, needs headroom that e4m3 lacks: 448 / 256.)
@@ -91,15 +92,15 @@ struct Smem {
     alignas(16) uint8_t p[kBufs][kStageKeys * kCols];
     float ks[kStages][kStageKeys];               // per key (gathered) or box: K scale,
     float lv[kStages][kStageKeys];               // log2 of V's (-inf: does not count),
-    float rv[kStages][kStageKeys];               // 16 / sqrt(V's)
+    float rv[kStages][kStageKeys];               // 1 / (4 sqrt(V's))
     StageMeta meta[kStages];
     alignas(16) float q_pow[kQPow][kMaxGroup];
-    alignas(16) float warp_max[kBufs][kGroupWarps][kMaxGroup];
+    alignas(16) float warp_ref[kBufs][kGroupWarps][kMaxGroup];
     alignas(16) float warp_sum[kGroups][2][kMaxGroup][kGroupWarps];
     // one group's share of a unit, for the group that finishes it
     alignas(16) float ex_o[kMaxGroup][D];
     alignas(16) float ex_l[kMaxGroup][kGroupWarps];
-    alignas(16) float ex_m[kMaxGroup];
+    alignas(16) float ex_c[kMaxGroup];
     uint64_t full[kStages], empty[kStages];
     uint64_t s_full[kBufs], p_full[kBufs], o_full[kBufs];
     uint64_t q_full[2], q_empty[2];
@@ -212,6 +213,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A factor in fp32's range, NaN if it is NaN.
+__device__ __forceinline__ float saturate(float x) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(3.4028234663852886e38f));
+    return r;
+}
+
+// 6 - m / 2 rounded down, so that m / 2 and it add up to at most 6 (and at least 0, as
+// -m / 2 is a number itself): the reference of weights whose largest score is m.  +inf
+// for a maximum over nothing.
+__device__ __forceinline__ float half_ref(float m) { return __fmaf_rd(m, -0.5f, 6.f); }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -387,10 +400,9 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
         Ring ring;
         ring.next(group);
         uint32_t shared = 0, units = 0;          // units of both groups; units of this one
-        float m[kHeads], l[kHeads], o[kHeads], xs[kHeads];
+        float c_run[kHeads], l[kHeads], o[kHeads], xs[kHeads];       // c_run: half_ref(M)
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) m[h] = l[h] = o[h] = xs[h] = 0.f;
-        bool wide = false;                       // some |xs| > 1: ks xs may overflow
+        for (int h = 0; h < kHeads; ++h) c_run[h] = l[h] = o[h] = xs[h] = 0.f;
         bool ok = true;
         for (uint32_t c = 0;; ++c, ring.next(kGroups)) {     // this group's stages
             const int buf = 2 * group + (c & 1), before = 2 * group + ((c & 1) ^ 1);
@@ -417,34 +429,27 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 tmem_ld<2 * kHeads>(lane_base + (buf * kSub + u) * kCols, s[u]);
             tmem_wait<kSub * 2 * kHeads>(&s[0][0]);
             if (first) {                         // (the S issuer has waited for Q)
-                wide = false;
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) {
-                    xs[h] = a.scale_log2 * sm.q_pow[meta.unit % kQPow][h];
-                    wide = wide || fabsf(xs[h]) > 1.f;
-                    m[h] = -INFINITY;
+                    xs[h] = fabsf(a.scale_log2) * sm.q_pow[meta.unit % kQPow][h];
+                    c_run[h] = INFINITY;
                     l[h] = o[h] = 0.f;
                 }
             }
             // y = dot ks xs + lv, the heads two by two; -inf where the key does not
-            // count, whose dot may be anything
+            // count, whose dot may be anything.  The factor saturates, so that a dot
+            // of zero beside it stays zero (any other is a score past 2^100 then).
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
 #pragma unroll
                 for (int h = 0; h < kHeads; h += 2) {
                     const float2 dot = fma2(make_float2(s[u][kHeads + h], s[u][kHeads + h + 1]),
                                             both(0.0625f), make_float2(s[u][h], s[u][h + 1]));
-                    const float2 k = mul2(both(ks[u]), make_float2(xs[h], xs[h + 1]));
+                    float2 k = mul2(both(ks[u]), make_float2(xs[h], xs[h + 1]));
+                    k = make_float2(saturate(k.x), saturate(k.y));
                     const float2 x = fma2(dot, k, both(lv[u]));
                     y[u][h] = x.x;
                     y[u][h + 1] = x.y;
-                    // queries past 2^7 / scale: a dot of zero stays zero whatever the
-                    // scales, and a product overflows only where the score does
-                    if (wide) {
-                        if (fabsf(xs[h]) > 1.f) y[u][h] = fmaf(dot.x * ks[u], xs[h], lv[u]);
-                        if (fabsf(xs[h + 1]) > 1.f)
-                            y[u][h + 1] = fmaf(dot.y * ks[u], xs[h + 1], lv[u]);
-                    }
                 }
                 if (!__all_sync(0xffffffffu, counts[u])) {
 #pragma unroll
@@ -452,67 +457,67 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                         if (!counts[u]) y[u][h] = -INFINITY;
                 }
             }
-            // ---- the stage's maxima ----
+            // ---- the stage's maxima, as half references (half_ref falls with its argument) ----
             float top[kHeads];
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 top[h] = y[0][h];
                 if constexpr (kSub == 2) top[h] = fmaxf(top[h], y[1][h]);
-                top[h] = warp_max(top[h]);
+                top[h] = half_ref(warp_max(top[h]));
             }
             if (lane == 0) {
 #pragma unroll
                 for (int h = 0; h < kHeads; h += 2)
-                    *reinterpret_cast<float2*>(&sm.warp_max[buf][gw][h]) =
+                    *reinterpret_cast<float2*>(&sm.warp_ref[buf][gw][h]) =
                         make_float2(top[h], top[h + 1]);
                 tc::mbar_arrive(&sm.max_bar[group]);
             }
             if (!(ok = wait_warp(&sm.max_bar[group], c & 1))) break;
             float alpha[kHeads], use[kHeads];
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) use[h] = m[h];
+            for (int h = 0; h < kHeads; ++h) use[h] = c_run[h];
 #pragma unroll
             for (int w = 0; w < kGroupWarps; ++w) {
                 if constexpr (kHeads == 2) {
-                    const float2 x = *reinterpret_cast<const float2*>(sm.warp_max[buf][w]);
-                    use[0] = fmaxf(use[0], x.x);
-                    use[1] = fmaxf(use[1], x.y);
+                    const float2 x = *reinterpret_cast<const float2*>(sm.warp_ref[buf][w]);
+                    use[0] = fminf(use[0], x.x);
+                    use[1] = fminf(use[1], x.y);
                 } else {
 #pragma unroll
                     for (int h = 0; h < kHeads; h += 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(&sm.warp_max[buf][w][h]);
-                        use[h] = fmaxf(use[h], x.x);
-                        use[h + 1] = fmaxf(use[h + 1], x.y);
-                        use[h + 2] = fmaxf(use[h + 2], x.z);
-                        use[h + 3] = fmaxf(use[h + 3], x.w);
+                        const float4 x = *reinterpret_cast<const float4*>(&sm.warp_ref[buf][w][h]);
+                        use[h] = fminf(use[h], x.x);
+                        use[h + 1] = fminf(use[h + 1], x.y);
+                        use[h + 2] = fminf(use[h + 2], x.z);
+                        use[h + 3] = fminf(use[h + 3], x.w);
                     }
                 }
             }
-            // Weights by their square roots: g = 2^((y - u) / 2) is normal down to y - u =
-            // -252 and l's term is (g rv)^2 = 256 g^2 / vs, so a key counts there however
-            // small its V scale is beside the largest (p itself may vanish, and may: it
-            // is its share of O).  The difference is rounded once: an offset in the
-            // exponent would be lost in scores around 2^27.
+            // Weights by their square roots, against c = 6 - M / 2 rounded down (half_ref):
+            // g = 2^(y / 2 + c) is at most 2^6 and normal down to 2^-264 of the largest
+            // weight.  16 p = g^2, and l's term is (g rv)^2 = 256 / vs of the weight, so a
+            // key counts there however small its V scale is beside the largest (its p
+            // may vanish: that is its share of O).  Every step and merge takes the
+            // difference of two c, so what their rounding leaves out cancels.
 #pragma unroll
             for (int h = 0; h < kHeads; h += 2) {
-                const float2 u = make_float2(use[h] == -INFINITY ? 0.f : use[h],
-                                             use[h + 1] == -INFINITY ? 0.f : use[h + 1]);
-                const float2 a2 = make_float2(pkv::fast_exp2(0.5f * (m[h] - u.x)),    // 0 from -inf
-                                              pkv::fast_exp2(0.5f * (m[h + 1] - u.y)));
+                const float2 c2 = make_float2(use[h] == INFINITY ? 6.f : use[h],
+                                              use[h + 1] == INFINITY ? 6.f : use[h + 1]);
+                const float2 a2 = make_float2(pkv::fast_exp2(c2.x - c_run[h]),       // 0 from +inf
+                                              pkv::fast_exp2(c2.y - c_run[h + 1]));
                 const float2 squared = mul2(a2, a2);
                 float2 sum = mul2(mul2(make_float2(l[h], l[h + 1]), a2), a2);
                 alpha[h] = squared.x;
                 alpha[h + 1] = squared.y;
-                m[h] = use[h];
-                m[h + 1] = use[h + 1];
+                c_run[h] = use[h];
+                c_run[h + 1] = use[h + 1];
 #pragma unroll
                 for (int x = 0; x < kSub; ++x) {
-                    const float2 e = fma2(make_float2(y[x][h], y[x][h + 1]), both(0.5f),
-                                          mul2(u, both(-0.5f)));
+                    const float2 e = fma2(make_float2(y[x][h], y[x][h + 1]), both(0.5f), c2);
                     const float2 g = make_float2(pkv::fast_exp2(e.x), pkv::fast_exp2(e.y));
                     const float2 t = mul2(g, both(rv[x]));
                     sum = fma2(t, t, sum);
-                    const float2 p16 = mul2(mul2(g, g), both(4096.f));   // as split_e4m3 takes it
+                    const float2 p16 = mul2(g, g);           // as split_e4m3 takes it
                     y[x][h] = p16.x;
                     y[x][h + 1] = p16.y;
                 }
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) {
                     if (dim >= 0) sm.ex_o[h][dim] = o[h];
-                    if (key == 0) sm.ex_m[h] = m[h];
+                    if (key == 0) sm.ex_c[h] = c_run[h];
                 }
                 if (l_mine) sm.ex_l[l_head][gw] = l[0];
                 __syncwarp();
@@ -611,17 +616,16 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 const float4 mine = *reinterpret_cast<const float4*>(sums[h]);
-                float L = (mine.x + mine.y) + (mine.z + mine.w), M = m[h], O = o[h];
+                float L = (mine.x + mine.y) + (mine.z + mine.w), O = o[h], c1 = c_run[h];
                 if (both) {
                     const float4 other = *reinterpret_cast<const float4*>(sm.ex_l[h]);
                     const float L2 = (other.x + other.y) + (other.z + other.w);
-                    const float m2 = sm.ex_m[h];
-                    M = fmaxf(M, m2);
-                    const float u = M == -INFINITY ? 0.f : M;
-                    const float f1 = pkv::fast_exp2(0.5f * (m[h] - u));
-                    const float f2 = pkv::fast_exp2(0.5f * (m2 - u));
+                    const float c2 = sm.ex_c[h], cm = fminf(c1, c2);
+                    const float to = cm == INFINITY ? 0.f : cm;
+                    const float f1 = pkv::fast_exp2(to - c1), f2 = pkv::fast_exp2(to - c2);
                     L = fmaf(L * f1, f1, L2 * f2 * f2);
                     if (dim >= 0) O = fmaf(O, f1 * f1, sm.ex_o[h][dim] * (f2 * f2));
+                    c1 = cm;
                 }
                 if (h >= meta.nh || dim < 0) continue;
                 const int64_t at = (int64_t)meta.row + meta.h0 + h;
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                     a.out[at * D + dim] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
                 } else {
                     a.part_o[at * D + dim] = O;
-                    if (dim == 0) a.part_ml[at] = make_float2(M, L);
+                    if (dim == 0) a.part_ml[at] = make_float2(-c1, L);         // M / 2 - 6, see the combine
                 }
             }
             if (both) {
@@ -747,8 +751,9 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
             mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
             // an infinite entry makes the head's weights NaN; e4m3 has no infinity, so
-            // it goes in as NaN
-            auto no_inf = [](uint32_t x) {
+            // it goes in as NaN.  A negative softmax scale's sign goes with q.
+            auto no_inf = [&](uint32_t x) {
+                x ^= a.scale_log2 < 0.f ? 0x80008000u : 0u;
                 if ((x & 0x7fffu) == 0x7f80u) x |= 0x40u;
                 if ((x & 0x7fff0000u) == 0x7f800000u) x |= 0x400000u;
                 return x;
@@ -840,7 +845,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
             const float ks = good ? ks_in : 0.f;
             const float lv = good ? __log2f(vs_in) : -INFINITY;
             // (good to 2^-22; __frsqrt_rn cost 1.5 us of 77 where every key has one)
-            const float rv = good ? 16.f * rsqrtf(vs_in) : 0.f;
+            const float rv = good ? 0.25f * rsqrtf(vs_in) : 0.f;
             const uint32_t goods = __ballot_sync(0xffffffffu, good);
             const int32_t row = blk * a.bs + (key0 + lane * kBoxKeys) % a.bs;
             StageMeta m;
@@ -1037,7 +1042,7 @@ __global__ void __launch_bounds__((kFirstProducer + (kGather ? kGatherWarps : 1)
                 const int key = row0 + lane + 32 * i;
                 sm.ks[slot][key] = good ? ks[i] : 0.f;
                 sm.lv[slot][key] = good ? __log2f(vs[i]) : -INFINITY;
-                sm.rv[slot][key] = good ? 16.f * rsqrtf(vs[i]) : 0.f;
+                sm.rv[slot][key] = good ? 0.25f * rsqrtf(vs[i]) : 0.f;
             }
             // the team's next stage: its block ids arrive while the copies land
             for (int i = 0; i < kTeams && un.sc < sched.chunks; ++i) step();

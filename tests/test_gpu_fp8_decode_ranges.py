@@ -166,3 +166,13 @@ def test_small_values_beside_large_ones(cuda, bs, d, apart, n, most):
             2.0 ** -22 * s.max() * C.sum(0)
         err = np.abs(got[0, h] - ref)
         assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("bs,d", [(16, 128), (64, 64)])
+@pytest.mark.parametrize("scale", [-0.125, 0.0, -1e-20])
+def test_softmax_scales_of_either_sign(cuda, bs, d, scale):
+    pkv = U.lib()
+    rng = np.random.default_rng(bs)
+    pool = F.Pool([700, 33], bs, 2, d, seed=bs)
+    q = F.bf16(rng, 2, 8, d)
+    _check(_decode(pkv, cuda, q, pool, scale), q, pool, scale)
