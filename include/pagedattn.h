@@ -553,6 +553,7 @@ typedef struct pkv_logit_rules {
  * apply_logit_rules -- for entry i of row b, x = logits[b, i] in fp32, in this
  * order:
  *   repetition  if i occurs among the row's tokens: x = x > 0 ? x / r : x * r
+ *               (x / r as x times the rounded 1 / r, one rounding more)
  *   frequency   x -= f * n, n the occurrences among the generated tokens (those
  *               behind the prompt)
  *   presence    x -= p if n > 0

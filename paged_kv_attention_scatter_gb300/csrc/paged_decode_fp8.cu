@@ -27,7 +27,8 @@ namespace {
 using pkv::Fp8DecodeArgs;
 using pkv::kMaxGroup;
 
-// Keys per work unit, from the sizes alone: the multiple of 128 (a stage of
+// Keys per work unit, from the sizes alone (152 SMs, a GB300's, are written down because
+// the workspace's size follows): the multiple of 128 (a stage of
 // head_dim 128) nearest to the length that gives about two units per SM for a
 // typical context of half the stated maximum, within 128..1024, and 2048 (a lane of
 // the producer has one of a unit's 64-key boxes) where a SM has sixteen such units or
@@ -35,10 +36,10 @@ using pkv::kMaxGroup;
 // -- its last stage's P V waited for, the two softmax groups' shares merged --
 // costs about a stage, so units are longer than the bf16 decode's, whose rule
 // aims at sixteen a SM (measured, us: 64 sequences of 16/8 heads and 512..4096
-// keys 59 at 256, 57 at 512, 57 at 1024; 8 of 32/8 and 4000..8192 39 at 128, 28 at
-// 512, 27 at 1024; 2 of 30000..32768 60, 35, 33; and at 1024 and 2048: 64 of 16/8 as
-// above 57, 61; 96 of 64/8 and 128..32768 200, 196; head_dim 64, 64 of 64/8 and
-// 512..4096 51, 48, in blocks of 16 75, 66; of 16/8 37, 39).
+// keys 61 at 256, 56 at 512, 55 at 1024; 8 of 32/8 and 4000..8192 43 at 128, 27 at
+// 512, 25 at 1024; 2 of 30000..32768 68, 34, 32; and at 1024 and 2048: 64 of 16/8 as
+// above 55, 60; 96 of 64/8 and 128..32768 198, 196; head_dim 64, 64 of 64/8 and
+// 512..4096 50, 48, in blocks of 16 67, 62; of 16/8 36, 38).
 int32_t choose_chunk_keys(int32_t batch, int32_t num_q_heads, int32_t max_ctx,
                           const pkv_cache_desc& c) {
     const int32_t hkv = c.num_kv_heads > 0 ? c.num_kv_heads : 1;

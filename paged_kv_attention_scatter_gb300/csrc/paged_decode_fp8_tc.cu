@@ -48,7 +48,7 @@
 // each MMA idle, the warps' partial outputs merged per unit) took 91 and 265 us
 // where this one takes 54 and 190 (64 sequences of 16/8 heads, 512..4096 keys; 96
 // of 64/8 heads, 128..32768 keys, block size 256), and one loading registers
-// straight from the cache 179 us where this one takes 73 (48 of 32/8 heads,
+// straight from the cache 179 us where this one takes 74 (48 of 32/8 heads,
 // 1..8192 keys, block size 16).
 #include <cudaTypedefs.h>
 

@@ -3,14 +3,17 @@
 //
 // What it computes: as paged_prefill_varlen, with the prefix rows code * scale.
 //
-// Design.  Prefill is bound by the tensor pipe, and a prefix row is read once
-// per 128-query tile and q head, so turning codes into operands inside the
+// Design.  Prefill of long chunks is bound by the tensor pipe, and a prefix row is read
+// once per 128-query tile and q head, so turning codes into operands inside the
 // attention kernel would repeat the conversion tens to hundreds of times
-// beside the softmax, the busiest role there.  Instead one pass writes the
+// beside the softmax, the busiest role there.  (For one to three tiles a sequence it
+// would not; those calls pay for the pass: 12 us of 37 for 3 chunks of 20..301 queries.)
+// Instead one pass writes the
 // prefix rows once as bf16 into the workspace, as cache blocks of 128 rows,
 // and the bf16 kernel attends over them: it takes its fastest path (whole-tile
 // TMA boxes) whatever the e4m3 cache's own block size.  With a power-of-two
-// scale, as kv_store_fp8 writes, the bf16 row is exact.  The pass moves 3 bytes
+// scale, as kv_store_fp8 writes, the bf16 row is exact; the weights are rounded to bf16
+// for the product with V, as that kernel does.  The pass moves 3 bytes
 // per prefix entry (1 read, 2 written), most of which the attention then finds
 // in L2.  Batches whose prefixes would exceed kExpandBytes run in groups of
 // sequences, one after another over the same workspace.
@@ -209,6 +212,8 @@ struct Fp8PrefillLayout {
     size_t off_table, off_tiles, off_ml, off_o, off_k, off_v, total;
 };
 
+// Of a GB300; not asked of the device, because the workspace's size follows from it and
+// is a function of the call's sizes alone.
 constexpr int kSms = 152;
 
 // Key tiles of a split, 0 for none: as many splits of a tile's keys as bring the
