@@ -577,6 +577,94 @@ PKV_API int pkv_apply_logit_rules(const void* logits, int32_t logits_type,
                                   pkv_logit_rules rules, float* out, uint32_t* status,
                                   void* stream);
 
+/*
+ * ---- norms of q and k heads, and the rotation of their positions ----------
+ * (No counterpart on the pages, whose attention takes rotated rows: the steps
+ * between a layer's projections and its kv_store.)
+ *
+ * The first rotary_dim entries of a head are rotated in pairs: entries i and
+ * i + rotary_dim / 2, or 2i and 2i + 1 where `interleaved` is not 0.  Pair i of
+ * a token at position p turns by p * frequency[i] radians.  `turns` holds each
+ * frequency as the fraction of a turn a position adds, in units of 2^-64
+ * (pkv_rotary_turns), so that angles are exact to |p| * 2^-65 turns for any int32 p.
+ */
+typedef struct pkv_rotary {
+    const uint64_t* turns;   /* device, [rotary_dim / 2]; NULL where rotary_dim is 0 */
+    int32_t rotary_dim;      /* even, 0 (no rotation) .. head_dim */
+    int32_t interleaved;
+    float magnitude;         /* factor of the rotated entries */
+} pkv_rotary;
+
+/* How frequencies are stretched to positions beyond a model's training. */
+#define PKV_ROPE_PLAIN  0    /* w_i = base^(-2i / rotary_dim)                              */
+#define PKV_ROPE_LINEAR 1    /* w_i / factor                                               */
+#define PKV_ROPE_NTK    2    /* base * factor^(rotary_dim / (rotary_dim - 2)) as the base   */
+#define PKV_ROPE_YARN   3    /* w_i up to the pair that makes `high` turns within
+                                original_max_position positions, w_i / factor from the one
+                                that makes `low`, a ramp over the pairs between them;
+                                magnitude 0.1 ln(factor) + 1                               */
+#define PKV_ROPE_BANDS  4    /* by the turns w_i makes within original_max_position
+                                positions: w_i from `high` on, w_i / factor up to `low`,
+                                linear in the turns between them                           */
+typedef struct pkv_rotary_scaling {
+    int32_t kind;            /* PKV_ROPE_* */
+    int32_t original_max_position;
+    double factor;           /* >= 1 */
+    double low, high;        /* turns: usually 1 and 32 (YARN), 1 and 4 (BANDS) */
+} pkv_rotary_scaling;
+
+/*
+ * Host functions.  pkv_rotary_frequencies writes the rotary_dim / 2 frequencies
+ * (radians a position) of a base (> 1) and a scaling to host memory, and the
+ * magnitude that belongs to them.  pkv_rotary_turns turns any frequencies in
+ * [0, 65536] into the units that pkv_rotary takes (to half a unit), in host memory;
+ * the caller copies them to the device.
+ */
+PKV_API int pkv_rotary_frequencies(int32_t rotary_dim, double base, pkv_rotary_scaling scaling,
+                                   double* frequencies, float* magnitude);
+PKV_API int pkv_rotary_turns(const double* frequencies, int32_t count, uint64_t* turns);
+
+/*
+ * qk_norm_rope -- RMS norm and rotation of every q and k head: for a head x,
+ *   y = x * weight / sqrt(mean(x^2) + eps)   (y = x where the weights are NULL),
+ *   then y's first rotary_dim entries rotated by its token's position, pairs
+ *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin).
+ * Computed in fp32 and rounded once to the rows' type.
+ *
+ *   q, k         device, [num_tokens, heads, head_dim] of `type` (PKV_FP32, PKV_BF16
+ *                or PKV_FP16), tokens q_stride / k_stride elements apart (a packed
+ *                projection's rows)
+ *   q_weight, k_weight  device, [head_dim] of weight_type, or NULL
+ *   positions    device, [num_tokens] int32, any value
+ *   q_out, k_out device, as q and k, with strides of their own.  Either may be its own
+ *                input (same stride); any other overlap is PKV_ERR_UNSUPPORTED.
+ * head_dim a multiple of 8, at most 256; rows 16-byte aligned.  A norm or a
+ * rotation is needed (PKV_ERR_BAD_DIMENSION otherwise).  Strides are not read when
+ * num_tokens is 1.
+ */
+PKV_API int pkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             int32_t type, const void* q_weight, const void* k_weight,
+                             int32_t weight_type, float eps, const int32_t* positions,
+                             pkv_rotary rotary, int32_t num_tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, void* q_out,
+                             int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                             void* stream);
+
+/*
+ * qk_norm_rope of bf16 rows and kv_store in one pass: q rows to q_out, k rows
+ * normed and rotated to their slots of k_cache (and to k_out unless it is
+ * NULL, e.g. for pkv_paged_prefill_varlen), v rows [num_tokens, num_kv_heads,
+ * head_dim], v_stride elements apart, to their slots of v_cache as they are.
+ * slot_mapping as in pkv_kv_store; a token without a slot still gets its q_out
+ * and k_out rows.  The caches must not overlap the other tensors.
+ */
+PKV_API int pkv_qk_norm_rope_kv_store(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, const void* q_weight, const void* k_weight, int32_t weight_type, float eps,
+    const int32_t* positions, pkv_rotary rotary, const int32_t* slot_mapping, int32_t num_tokens,
+    int32_t num_q_heads, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+    void* k_cache, void* v_cache, pkv_cache_desc cache, uint32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

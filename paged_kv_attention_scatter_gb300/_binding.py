@@ -46,7 +46,9 @@ C_FUNCTIONS = ["pkv_version", "pkv_error_string", "pkv_status_string", "pkv_kv_s
                "pkv_paged_decode_fp8_workspace_bytes", "pkv_paged_decode_plan_fp8",
                "pkv_paged_decode_run_fp8", "pkv_kv_store_paged_decode_fp8_workspace_bytes",
                "pkv_kv_store_paged_decode_fp8", "pkv_paged_prefill_fp8_workspace_bytes",
-               "pkv_paged_prefill_varlen_fp8", "pkv_apply_logit_rules"]
+               "pkv_paged_prefill_varlen_fp8", "pkv_apply_logit_rules",
+               "pkv_rotary_frequencies", "pkv_rotary_turns", "pkv_qk_norm_rope",
+               "pkv_qk_norm_rope_kv_store"]
 
 # Size of the scratch array compiled into the library for
 # pkv_paged_decode_static_workspace (PKV_STATIC_DECODE_WORKSPACE_BYTES).
@@ -64,6 +66,16 @@ class LogitRules(ctypes.Structure):
                  "presence_penalties", "frequency_penalties", "bias_offsets", "bias_token_ids",
                  "bias_values", "allowed_mask")] + \
                [("max_tokens", ctypes.c_int32), ("num_biases", ctypes.c_int32)]
+
+
+class RotaryScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original_max_position", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -151,6 +163,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                                  P, I32, F32, P, P, SZ, CacheDesc, P, P]
     lib.pkv_apply_logit_rules.restype = ctypes.c_int
     lib.pkv_apply_logit_rules.argtypes = [P, I32, ctypes.c_int64, I32, I32, LogitRules, P, P, P]
+    I64, F64 = ctypes.c_int64, ctypes.c_double
+    lib.pkv_rotary_frequencies.restype = ctypes.c_int
+    lib.pkv_rotary_frequencies.argtypes = [I32, F64, RotaryScaling, P, ctypes.POINTER(F32)]
+    lib.pkv_rotary_turns.restype = ctypes.c_int
+    lib.pkv_rotary_turns.argtypes = [P, I32, P]
+    lib.pkv_qk_norm_rope.restype = ctypes.c_int
+    lib.pkv_qk_norm_rope.argtypes = [P, I64, P, I64, I32, P, P, I32, F32, P, RotaryDesc, I32, I32,
+                                     I32, I32, P, I64, P, I64, P]
+    lib.pkv_qk_norm_rope_kv_store.restype = ctypes.c_int
+    lib.pkv_qk_norm_rope_kv_store.argtypes = [P, I64, P, I64, P, I64, P, P, I32, F32, P,
+                                              RotaryDesc, P, I32, I32, P, I64, P, I64, P, P,
+                                              CacheDesc, P, P]
     _LIB = lib
     return lib
 
@@ -845,7 +869,7 @@ def paged_prefill_varlen_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, cu_seq
     return _on(index, stream, call)
 
 
-_LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}      # PKV_FP32, ...
 
 
 def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
@@ -866,7 +890,7 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
     lib = load()
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
-    kind = _LOGIT_TYPES.get(logits.dtype)
+    kind = _TYPES.get(logits.dtype)
     if kind is None:
         raise TypeError(f"logits must be fp32, bf16 or fp16, got {logits.dtype}")
     if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
@@ -919,4 +943,180 @@ def apply_logit_rules(logits, token_ids=None, prompt_lens=None, token_lens=None,
         _check(lib.pkv_apply_logit_rules(logits.data_ptr(), kind, stride, B, V, r, o.data_ptr(),
                                          st, s), "pkv_apply_logit_rules")
         return o
+    return _on(index, stream, call)
+
+
+# ----------------------------------------------------------------------------
+# Norms of q and k heads and the rotation of their positions.
+_ROPE_SCALINGS = {None: (0, 1.0, 1.0), "linear": (1, 1.0, 1.0), "ntk": (2, 1.0, 1.0),
+                  "yarn": (3, 1.0, 32.0), "bands": (4, 1.0, 4.0)}      # kind, usual low and high
+
+
+class Rotary:
+    """The rotation of a model's positions, made by rotary(): its frequencies on
+    one device, for any number of calls there."""
+
+    def __init__(self, turns, rotary_dim, interleaved, magnitude):
+        self.turns = turns                              # [rotary_dim / 2] int64 (uint64 bits)
+        self.rotary_dim = rotary_dim
+        self.interleaved = bool(interleaved)
+        self.magnitude = float(magnitude)
+        self.desc = RotaryDesc(turns.data_ptr(), rotary_dim, int(self.interleaved),
+                               self.magnitude)
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
+                       original_max_position=0, low=None, high=None):
+    """(frequencies, magnitude): the rotary_dim / 2 radians a position as a list, and
+    the factor of rotated entries, of a base and a scaling: None, "linear", "ntk",
+    "yarn" or "bands" (see pkv_rotary_scaling in include/pagedattn.h)."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(k for k in _ROPE_SCALINGS if k)} or "
+                         f"None, got {scaling!r}")
+    kind, usual_low, usual_high = _ROPE_SCALINGS[scaling]
+    spec = RotaryScaling(kind, int(original_max_position), float(factor),
+                         usual_low if low is None else float(low),
+                         usual_high if high is None else float(high))
+    out = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+    magnitude = ctypes.c_float()
+    _check(load().pkv_rotary_frequencies(int(rotary_dim), float(base), spec, out,
+                                         ctypes.byref(magnitude)), "pkv_rotary_frequencies")
+    return list(out), magnitude.value
+
+
+def rotary(rotary_dim, base=10000.0, interleaved=False, scaling=None, factor=1.0,
+           original_max_position=0, low=None, high=None, frequencies=None, magnitude=None,
+           device=None) -> Rotary:
+    """The rotation qk_norm_rope applies to the first rotary_dim entries of a head:
+    entries i and i + rotary_dim / 2 in pairs, or 2i and 2i + 1 (interleaved), at the
+    frequencies of a base and a scaling (see rotary_frequencies) or at those
+    given (radians a position, [rotary_dim / 2]).  `magnitude` replaces the scaling's.
+    Copies the frequencies to `device` (default: the current one) and waits for that."""
+    rotary_dim = int(rotary_dim)
+    if frequencies is None:
+        frequencies, usual = rotary_frequencies(rotary_dim, base, scaling, factor,
+                                                original_max_position, low, high)
+    else:
+        if scaling is not None:
+            raise ValueError("scaling and frequencies exclude each other")
+        frequencies, usual = [float(f) for f in frequencies], 1.0
+        if rotary_dim != 2 * len(frequencies):
+            raise ValueError("frequencies must be [rotary_dim / 2]")
+    n = len(frequencies)
+    turns = (ctypes.c_int64 * n)()
+    _check(load().pkv_rotary_turns((ctypes.c_double * n)(*frequencies), n, turns),
+           "pkv_rotary_turns")
+    on = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return Rotary(torch.tensor(list(turns), dtype=torch.int64).to(on), rotary_dim, interleaved,
+                  usual if magnitude is None else magnitude)
+
+
+def _heads(t, name, dtype, index, like=None):
+    """Address and token stride of rows [tokens, heads, head_dim] whose heads are
+    contiguous (a view of a packed projection, say)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be on cuda:{max(index, 0)}, got {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or (like is not None and shape != like):
+        raise ValueError(f"{name} must be {'[tokens, heads, head_dim]' if like is None else like}"
+                         f", got {list(shape)}")
+    stride = t.stride()
+    if (stride[2] != 1 and shape[2] > 1) or (stride[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"the heads of {name} must be contiguous")
+    return t.data_ptr(), stride[0]
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, positions, rope):
+    """What both calls check alike: (index, tokens, the arguments of q and k, of
+    the weights, positions, rotation)."""
+    index, dtype = q.get_device(), q.dtype
+    if dtype not in _TYPES:
+        raise TypeError(f"q must be fp32, bf16 or fp16, got {dtype}")
+    rows = (*_heads(q, "q", dtype, index), *_heads(k, "k", dtype, index))
+    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q and k must have the same tokens and head_dim")
+    n, _, d = q.shape
+    wp, wtype = [None, None], dtype
+    for i, (name, w) in enumerate((("q_weight", q_weight), ("k_weight", k_weight))):
+        if w is None:
+            continue
+        if w.shape != (d,):
+            raise ValueError(f"{name} must be [head_dim]")
+        if wp[0] is not None and w.dtype is not wtype:
+            raise TypeError("q_weight and k_weight must have the same dtype")
+        wtype = w.dtype
+        if wtype not in _TYPES:
+            raise TypeError(f"{name} must be fp32, bf16 or fp16, got {wtype}")
+        wp[i] = _at(w, name, wtype, index)
+    if rope is None:
+        return index, n, rows, (*wp, _TYPES[wtype]), None, _NO_ROTARY
+    if not isinstance(rope, Rotary):
+        raise TypeError("rope must come from rotary()")
+    if rope.turns.get_device() != index:
+        raise ValueError(f"rope is on {rope.turns.device}, expected cuda:{index}")
+    if positions is None or positions.shape != (n,):
+        raise ValueError("positions must be [tokens]")
+    return (index, n, rows, (*wp, _TYPES[wtype]), _at(positions, "positions", torch.int32, index),
+            rope.desc)
+
+
+_NO_ROTARY = RotaryDesc(None, 0, 0, 1.0)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, eps, positions, rope, q_out=None, k_out=None,
+                 stream=None):
+    """RMS norm (weights [D], or None for no norm) and position rotation (rotary(), or
+    None) of every head of q [T, Hq, D] and k [T, Hkv, D], fp32, bf16 or fp16; tokens
+    may be strided (views of a packed projection).  positions [T] int32.  Returns
+    (q_out, k_out), contiguous unless given; pass q_out=q, k_out=k to work in place."""
+    lib = load()
+    index, n, rows, weights, pos, desc = _norm_rope_args(q, k, q_weight, k_weight, positions, rope)
+    dtype, hq, d = q.dtype, q.shape[1], q.shape[2]
+
+    def call(s):
+        qo = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
+        ko = torch.empty(k.shape, dtype=dtype, device=q.device) if k_out is None else k_out
+        _check(lib.pkv_qk_norm_rope(*rows, _TYPES[dtype], *weights, float(eps), pos, desc, n, hq,
+                                    k.shape[1], d, *_heads(qo, "q_out", dtype, index, q.shape),
+                                    *_heads(ko, "k_out", dtype, index, k.shape), s),
+               "pkv_qk_norm_rope")
+        return qo, ko
+    return _on(index, stream, call)
+
+
+def qk_norm_rope_kv_store(q, k, v, q_weight, k_weight, eps, positions, rope, k_cache, v_cache,
+                          slot_mapping, q_out=None, k_out=None, status=None,
+                          stream=None) -> torch.Tensor:
+    """qk_norm_rope of bf16 rows with its k rows, and v [T, Hkv, D] as it is, stored in
+    the paged cache as kv_store stores them (slot_mapping [T] int32, negative =
+    skip).  Returns q_out; the k rows are also written to k_out when given (for
+    paged_prefill_varlen)."""
+    lib = load()
+    index, n, rows, weights, pos, desc = _norm_rope_args(q, k, q_weight, k_weight, positions, rope)
+    bf16 = torch.bfloat16
+    if q.dtype is not bf16:
+        raise TypeError(f"q must be {bf16}, got {q.dtype}")
+    vrow = _heads(v, "v", bf16, index, k.shape)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or shape[2:] != k.shape[1:]:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
+                         "num_kv_heads, head_dim] matching k")
+    if slot_mapping.shape != (n,):
+        raise ValueError("slot_mapping must hold one slot per token")
+    slots = _at(slot_mapping, "slot_mapping", torch.int32, index)
+    caches = _at(k_cache, "k_cache", bf16, index), _at(v_cache, "v_cache", bf16, index)
+    st = _maybe(status, "status", torch.int32, index)
+    ko = (None, 0) if k_out is None else _heads(k_out, "k_out", bf16, index, k.shape)
+
+    def call(s):
+        qo = torch.empty(q.shape, dtype=bf16, device=q.device) if q_out is None else q_out
+        _check(lib.pkv_qk_norm_rope_kv_store(
+            *rows, *vrow, *weights, float(eps), pos, desc, slots, n, q.shape[1],
+            *_heads(qo, "q_out", bf16, index, q.shape), *ko, *caches, _desc(*shape), st, s),
+            "pkv_qk_norm_rope_kv_store")
+        return qo
     return _on(index, stream, call)
