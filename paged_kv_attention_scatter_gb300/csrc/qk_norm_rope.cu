@@ -30,7 +30,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kBatch = 4;                    // heads a lane has in flight
 constexpr int kMaxDim = 256;
 
@@ -44,7 +44,7 @@ struct HeadArgs {
     const int32_t* positions;
     const uint64_t* turns;
     int32_t rotary_dim, interleaved;
-    float magnitude, eps;
+    float magnitude, eps, inv_dim;           // inv_dim: 1 / D
     int32_t num_tokens, Hq, Hkv, D;
     // the cache
     const int32_t* slots;
@@ -53,85 +53,92 @@ struct HeadArgs {
     uint32_t* status;
 };
 
-// Where a lane finds the partner entries of its eight: nowhere (no rotation), among
-// them, in another lane, in memory.
-enum Partner : int { kNone, kPairs, kLane, kMemory };
+// Where a lane finds the partner entries of its sixteen: nowhere (no rotation), next to
+// them, at the same place of its other chunk, or through shared memory.
+enum Partner : int { kNone, kPairs, kChunks, kShared };
 
+// Eight entries as four packed pairs of fp32; arithmetic on pairs is one instruction.
+struct Pairs {
+    uint64_t v[4];
+};
+
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 up2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+    const float2 f = up2(v);
+    return pk2(f.y, f.x);
+}
+
+__device__ __forceinline__ uint64_t two(uint32_t w, __nv_bfloat16) {
+    return pk2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t two(uint32_t w, __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pk2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t pack(float2 f, __nv_bfloat16) {
+    return pkv::pack_bf16(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t pack(float2 f, __half) {
+    const __half2 v = __floats2half2_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Eight entries as they lie in memory.
 template <typename T>
-struct Eight;
+struct Eight {
+    uint4 v;
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const T* p) { v = pkv::ld_stream16(p); }
+    __device__ __forceinline__ Pairs get() const {
+        return {{two(v.x, T()), two(v.y, T()), two(v.z, T()), two(v.w, T())}};
+    }
+    static __device__ __forceinline__ void store(T* p, const Pairs& y) {
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(pack(up2(y.v[0]), T()), pack(up2(y.v[1]), T()), pack(up2(y.v[2]), T()),
+                       pack(up2(y.v[3]), T()));
+    }
+    __device__ __forceinline__ void put(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
+};
 template <>
 struct Eight<float> {
     float4 a, b;
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float* p) {
         a = pkv::ld_stream16f(p);
         b = pkv::ld_stream16f(p + 4);
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    __device__ __forceinline__ Pairs get() const {
+        return {{pk2(a.x, a.y), pk2(a.z, a.w), pk2(b.x, b.y), pk2(b.z, b.w)}};
     }
-    __device__ __forceinline__ Eight from(int lane) const {
-        Eight r;
-        r.a = make_float4(__shfl_sync(~0u, a.x, lane), __shfl_sync(~0u, a.y, lane),
-                          __shfl_sync(~0u, a.z, lane), __shfl_sync(~0u, a.w, lane));
-        r.b = make_float4(__shfl_sync(~0u, b.x, lane), __shfl_sync(~0u, b.y, lane),
-                          __shfl_sync(~0u, b.z, lane), __shfl_sync(~0u, b.w, lane));
-        return r;
-    }
-    static __device__ __forceinline__ void store(float* p, const float (&y)[8]) {
-        *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(y[4], y[5], y[6], y[7]);
+    static __device__ __forceinline__ void store(float* p, const Pairs& y) {
+        const float2 f0 = up2(y.v[0]), f1 = up2(y.v[1]), f2 = up2(y.v[2]), f3 = up2(y.v[3]);
+        *reinterpret_cast<float4*>(p) = make_float4(f0.x, f0.y, f1.x, f1.y);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(f2.x, f2.y, f3.x, f3.y);
     }
     __device__ __forceinline__ void put(float* p) const {
         *reinterpret_cast<float4*>(p) = a;
         *reinterpret_cast<float4*>(p + 4) = b;
     }
 };
-
-__device__ __forceinline__ float2 two(uint32_t w, __nv_bfloat16) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ float2 two(uint32_t w, __half) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
-    return pkv::pack_bf16(lo, hi);
-}
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-template <typename T>
-struct Eight {
-    uint4 v;
-    __device__ __forceinline__ void load(const T* p) { v = pkv::ld_stream16(p); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = two(w[i], T());
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    }
-    __device__ __forceinline__ Eight from(int lane) const {
-        Eight r;
-        r.v = make_uint4(__shfl_sync(~0u, v.x, lane), __shfl_sync(~0u, v.y, lane),
-                         __shfl_sync(~0u, v.z, lane), __shfl_sync(~0u, v.w, lane));
-        return r;
-    }
-    static __device__ __forceinline__ void store(T* p, const float (&y)[8]) {
-        *reinterpret_cast<uint4*>(p) =
-            make_uint4(pack(y[0], y[1], T()), pack(y[2], y[3], T()), pack(y[4], y[5], T()),
-                       pack(y[6], y[7], T()));
-    }
-    __device__ __forceinline__ void put(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
-};
-
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 
 __device__ __forceinline__ float weight_at(const HeadArgs& a, int which, int e) {
     const void* w = a.weight[which];
@@ -183,19 +190,56 @@ __device__ __forceinline__ void fill_tables(const HeadArgs& g, int32_t token, Ta
         }
 }
 
-// kLanes: lanes of a head (8 kLanes >= D).  kStore: k and v rows go into the cache.
+__device__ __forceinline__ Pairs table_at(const float* p) {
+    const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(p);
+    const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(p + 4);
+    return {{lo.x, lo.y, hi.x, hi.y}};
+}
+
+// r (A x + B x') of eight entries from e0 on; `rotated` of them have a partner.
+template <Partner kPartner>
+__device__ __forceinline__ Pairs turned(const float* a, const float* b, const Pairs& x,
+                                        const Pairs& partner, int e0, int rotary_dim,
+                                        uint64_t r2) {
+    const Pairs ta = table_at(a + e0);
+    Pairs y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.v[i] = mul2(ta.v[i], x.v[i]);
+    if constexpr (kPartner != kNone) {
+        // entries behind the rotated ones have none: an infinite one beside them, times
+        // the table's zero, would make them NaN
+        if (e0 < rotary_dim) {
+            const Pairs tb = table_at(b + e0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (e0 + 2 * i < rotary_dim) y.v[i] = fma2(tb.v[i], partner.v[i], y.v[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.v[i] = mul2(y.v[i], r2);
+    return y;
+}
+
+// kLanes: lanes of a head (16 kLanes >= D), each with two chunks of eight entries.
+// kStore: k and v rows go into the cache.
 template <typename T, int kLanes, Partner kPartner, bool kStore>
 __global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
     constexpr int kHeads = kThreads / kLanes;            // heads of a pass
     __shared__ __align__(16) Tables tab;
+    // a pass's rows as fp32, for partners that lie across chunks
+    __shared__ __align__(16) float rows[kPartner == kShared ? kThreads * 16 : 1];
     const int32_t token = blockIdx.x;
-    const int c = threadIdx.x % kLanes, lane = threadIdx.x & 31;
-    const bool in_row = c * 8 < g.D;
+    const int j = threadIdx.x % kLanes, head = threadIdx.x / kLanes;
     const int32_t qk = g.Hq + g.Hkv, heads = kStore ? qk + g.Hkv : qk;
-    const int half = g.rotary_dim / 2;
-    // the half layout's partner lane (in whole chunks)
-    const int away = half / 8;
-    const int other = lane + (c < away ? away : c < 2 * away ? -away : 0);
+    // this lane's chunks: where they are partners (half layout, whole chunks) chunk j and
+    // the one half the rotated part away, and behind those as elsewhere: j and j + as many
+    // as there are lanes with a first chunk
+    const int chunks = g.D / 8, away = kPartner == kChunks ? g.rotary_dim / 16 : 0;
+    const int left = chunks - 2 * away;                  // chunks not in such pairs
+    const int c0 = j < away ? j : j + away, c1 = j < away ? j + away : j + away + (left + 1) / 2;
+    const bool has0 = j < away + (left + 1) / 2;
+    const bool has1 = j < away || (has0 && c1 < chunks);
+    const int e0 = c0 * 8, e1 = has1 ? c1 * 8 : 0;
     int32_t slot = -1;
     if constexpr (kStore) {
         slot = __ldg(g.slots + token);
@@ -205,26 +249,19 @@ __global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
         }
     }
     for (int32_t base = 0; base < heads; base += kBatch * kHeads) {
-        Eight<T> x[kBatch];
-        float xp[kPartner == kMemory ? kBatch : 1][8];
+        Eight<T> x0[kBatch], x1[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int32_t h = base + u * kHeads + threadIdx.x / kLanes;
-            x[u] = Eight<T>{};
-            if (h < heads && in_row) {
+            const int32_t h = base + u * kHeads + head;
+            x0[u].zero();
+            x1[u].zero();
+            if (h < heads) {
                 const int which = h < g.Hq ? 0 : h < qk ? 1 : 2;
                 const int32_t hh = h - (which == 0 ? 0 : which == 1 ? g.Hq : qk);
                 const T* row = (const T*)g.in[which] + token * g.in_stride[which] +
                                (int64_t)hh * g.D;
-                x[u].load(row + c * 8);
-                if constexpr (kPartner == kMemory)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int e = c * 8 + k;
-                        xp[u][k] = e < half             ? as_float(row[e + half])
-                                   : e < g.rotary_dim ? as_float(row[e - half])
-                                                      : 0.f;
-                    }
+                if (has0) x0[u].load(row + e0);
+                if (has1) x1[u].load(row + e1);
             }
         }
         if (base == 0) {
@@ -234,45 +271,78 @@ __global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (base + u * kHeads >= heads) break;           // alike in every thread
-            const int32_t h = base + u * kHeads + threadIdx.x / kLanes;
-            const int which = h < g.Hq ? 0 : 1;
-            float y[8], p[8], o[8];
-            x[u].get(y);
-            float ss = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(y[k], y[k], ss);
-#pragma unroll
-            for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(~0u, ss, off);
-            const float r = g.weight[which] ? rsqrtf(ss / (float)g.D + g.eps) : 1.f;
-            if constexpr (kPartner == kLane) x[u].from(other).get(p);
-            __syncwarp();                    // the row is read: it may be written in place
-            if (h >= heads || !in_row) continue;
-            if (kStore && h >= qk) {         // a v row, as it is
-                if (slot >= 0)
-                    x[u].put((T*)g.cache[1] + ((int64_t)slot * g.Hkv + (h - qk)) * g.D + c * 8);
-                continue;
-            }
-            const float* ta = tab.a[which] + c * 8;
-            const float* tb = tab.b[which] + c * 8;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                o[k] = ta[k] * y[k];
-                if constexpr (kPartner != kNone) {
-                    const float partner = kPartner == kPairs  ? y[k ^ 1]
-                                          : kPartner == kLane ? p[k]
-                                                              : xp[kPartner == kMemory ? u : 0][k];
-                    // entries behind the rotated ones have none
-                    if (c * 8 + k < g.rotary_dim) o[k] = fmaf(tb[k], partner, o[k]);
+            const int32_t h = base + u * kHeads + head;
+            if (kStore && h >= qk) {                         // a v row, as it is
+                if (slot >= 0 && h < heads) {
+                    T* to = (T*)g.cache[1] + ((int64_t)slot * g.Hkv + (h - qk)) * g.D;
+                    if (has0) x0[u].put(to + e0);
+                    if (has1) x1[u].put(to + e1);
                 }
-                o[k] *= r;
             }
+            if (kStore && __all_sync(~0u, h >= qk)) continue;
+            const int which = h < g.Hq ? 0 : 1;
+            const Pairs a = x0[u].get(), b = x1[u].get();
+            float r = 1.f;
+            if (g.weight[0] || g.weight[1]) {
+                uint64_t s2 = mul2(a.v[0], a.v[0]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) s2 = fma2(a.v[i], a.v[i], s2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s2 = fma2(b.v[i], b.v[i], s2);
+                const float2 s = up2(s2);
+                float ss = s.x + s.y;
+#pragma unroll
+                for (int off = kLanes / 2; off > 0; off >>= 1)
+                    ss += __shfl_xor_sync(~0u, ss, off);
+                if (g.weight[which]) r = rsqrtf(ss * g.inv_dim + g.eps);
+            }
+            const uint64_t r2 = pk2(r, r);
+            Pairs pa = a, pb = b;                            // partners
+            if constexpr (kPartner == kPairs) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pa.v[i] = swapped(a.v[i]);
+                    pb.v[i] = swapped(b.v[i]);
+                }
+            } else if constexpr (kPartner == kChunks) {
+                pa = b;
+                pb = a;
+            } else if constexpr (kPartner == kShared) {
+                float* mine = rows + head * (kLanes * 16);
+                const int half = g.rotary_dim / 2;
+                __syncwarp();                                // the last rows are read
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (has0) *reinterpret_cast<uint64_t*>(mine + e0 + 2 * i) = a.v[i];
+                    if (has1) *reinterpret_cast<uint64_t*>(mine + e1 + 2 * i) = b.v[i];
+                }
+                __syncwarp();
+                auto at = [&](int e) {                       // the partner of entry e
+                    return e < half ? mine[e + half] : e < g.rotary_dim ? mine[e - half] : 0.f;
+                };
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    pa.v[i] = pk2(at(e0 + 2 * i), at(e0 + 2 * i + 1));
+                    pb.v[i] = pk2(at(e1 + 2 * i), at(e1 + 2 * i + 1));
+                }
+            }
+            __syncwarp();                    // the rows are read: they may be written in place
+            if (h >= qk || !has0) continue;
             const int32_t hh = which ? h - g.Hq : h;
-            if (g.out[which])
-                Eight<T>::store((T*)g.out[which] + token * g.out_stride[which] +
-                                    (int64_t)hh * g.D + c * 8,
-                                o);
-            if (kStore && which == 1 && slot >= 0)
-                Eight<T>::store((T*)g.cache[0] + ((int64_t)slot * g.Hkv + hh) * g.D + c * 8, o);
+            const Pairs y0 = turned<kPartner>(tab.a[which], tab.b[which], a, pa, e0,
+                                              g.rotary_dim, r2);
+            const Pairs y1 = turned<kPartner>(tab.a[which], tab.b[which], b, pb, e1,
+                                              g.rotary_dim, r2);
+            if (g.out[which]) {
+                T* to = (T*)g.out[which] + token * g.out_stride[which] + (int64_t)hh * g.D;
+                Eight<T>::store(to + e0, y0);
+                if (has1) Eight<T>::store(to + e1, y1);
+            }
+            if (kStore && which == 1 && slot >= 0) {
+                T* to = (T*)g.cache[0] + ((int64_t)slot * g.Hkv + hh) * g.D;
+                Eight<T>::store(to + e0, y0);
+                if (has1) Eight<T>::store(to + e1, y1);
+            }
         }
     }
 }
@@ -282,17 +352,17 @@ int launch(const HeadArgs& g, cudaStream_t s) {
     void (*kernel)(const HeadArgs) =
         g.rotary_dim == 0        ? head_kernel<T, kLanes, kNone, kStore>
         : g.interleaved          ? head_kernel<T, kLanes, kPairs, kStore>
-        : g.rotary_dim % 16 == 0 ? head_kernel<T, kLanes, kLane, kStore>
-                                 : head_kernel<T, kLanes, kMemory, kStore>;
+        : g.rotary_dim % 16 == 0 ? head_kernel<T, kLanes, kChunks, kStore>
+                                 : head_kernel<T, kLanes, kShared, kStore>;
     kernel<<<(unsigned)g.num_tokens, kThreads, 0, s>>>(g);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 template <typename T, bool kStore>
 int launch(const HeadArgs& g, cudaStream_t s) {
-    return g.D <= 64    ? launch<T, 8, kStore>(g, s)
-           : g.D <= 128 ? launch<T, 16, kStore>(g, s)
-                        : launch<T, 32, kStore>(g, s);
+    return g.D <= 64    ? launch<T, 4, kStore>(g, s)
+           : g.D <= 128 ? launch<T, 8, kStore>(g, s)
+                        : launch<T, 16, kStore>(g, s);
 }
 
 // A [tokens, heads, D] view whose tokens are `stride` elements apart.
@@ -380,6 +450,7 @@ int make_args(const void* q, int64_t q_stride, const void* k, int64_t k_stride, 
     g.interleaved = rotary.interleaved != 0;
     g.magnitude = rotary.magnitude;
     g.eps = eps;
+    g.inv_dim = 1.f / (float)head_dim;
     g.num_tokens = num_tokens;
     g.Hq = num_q_heads;
     g.Hkv = num_kv_heads;
