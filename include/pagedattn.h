@@ -665,6 +665,63 @@ PKV_API int pkv_qk_norm_rope_kv_store(
     int32_t num_q_heads, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
     void* k_cache, void* v_cache, pkv_cache_desc cache, uint32_t* status, void* stream);
 
+/*
+ * ---- decode attention over shared prefixes --------------------------------
+ * (No counterpart on the pages, whose prefix cache lets sequences share blocks;
+ * here their attention shares the work on them too.)
+ *
+ * Bytes of device workspace the calls below need (a pure host function).  As
+ * with pkv_paged_decode_workspace_bytes, a workspace shared by several batch
+ * sizes must be as large as the largest of their answers.
+ */
+PKV_API size_t pkv_paged_decode_shared_workspace_bytes(int32_t batch, int32_t num_q_heads,
+                                                       int32_t max_context_len,
+                                                       pkv_cache_desc cache);
+
+/*
+ * paged_decode for sequences in groups whose first keys are the same: arguments
+ * and result as in pkv_paged_decode, and
+ *   group_offsets device, [num_groups + 1] int32, increasing, within [0, batch]:
+ *                 group g is the sequences group_offsets[g] .. group_offsets[g+1] - 1.
+ *                 Sequences outside every group attend by themselves.
+ *   prefix_lens   device, [num_groups] int32: the first prefix_lens[g] keys of every
+ *                 sequence of group g (of its context_lens[b] in all) are those that
+ *                 any one of its block-table rows names.  Read once for the group.
+ * num_groups 0 takes NULL for both.  scale must be positive and finite.
+ * A context length of 0 gives zeros.  One below its group's prefix, or out of
+ * range as in pkv_paged_decode, sets PKV_STATUS_BAD_CONTEXT_LEN and gives zeros.
+ * Offsets that decrease or leave the batch set PKV_STATUS_BAD_SEQLENS and no group
+ * is used; a prefix < 0 or longer than max_context_len or the block table sets it
+ * and counts as 0.  Keys in a block id outside the pool are left out.  A query
+ * row whose scores are NaN or +inf gives NaN.  num_blocks*block_size must be below
+ * 2^31 (PKV_ERR_UNSUPPORTED).
+ */
+PKV_API int pkv_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* context_lens, const int32_t* group_offsets,
+                                    const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                                    int32_t num_q_heads, int32_t max_context_len, float scale,
+                                    void* out, void* workspace, size_t workspace_bytes,
+                                    pkv_cache_desc cache, uint32_t* status, void* stream);
+
+/*
+ * paged_decode_shared split into a plan (of the lengths alone, once a step) and a
+ * run (once a layer), as pkv_paged_decode_plan and pkv_paged_decode_run split
+ * pkv_paged_decode, under the same conditions.
+ */
+PKV_API int pkv_paged_decode_plan_shared(const int32_t* context_lens, const int32_t* group_offsets,
+                                         const int32_t* prefix_lens, int32_t num_groups,
+                                         int32_t batch, int32_t num_q_heads,
+                                         int32_t max_context_len, int32_t max_blocks_per_seq,
+                                         void* workspace, size_t workspace_bytes,
+                                         pkv_cache_desc cache, uint32_t* status, void* stream);
+PKV_API int pkv_paged_decode_run_shared(const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                        int32_t batch, int32_t num_q_heads,
+                                        int32_t max_context_len, float scale, void* out,
+                                        void* workspace, size_t workspace_bytes,
+                                        pkv_cache_desc cache, uint32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,9 @@ from ._binding import (STATUS, cache_desc, kv_store, kv_store_paged_attention_va
                        paged_decode_fp8_workspace_bytes, paged_decode_plan_fp8,
                        paged_decode_run_fp8, paged_prefill_fp8_workspace_bytes,
                        paged_prefill_varlen_fp8, Rotary, qk_norm_rope, qk_norm_rope_kv_store,
-                       rotary, rotary_frequencies)
+                       rotary, rotary_frequencies, paged_decode_plan_shared,
+                       paged_decode_run_shared, paged_decode_shared,
+                       paged_decode_shared_workspace_bytes)
 from ._build import build  # noqa: F401
 
 __all__ = ["kv_store", "paged_decode", "paged_prefill_varlen", "sample", "build", "load",
@@ -45,4 +47,6 @@ __all__ = ["kv_store", "paged_decode", "paged_prefill_varlen", "sample", "build"
            "kv_store_paged_decode_fp8", "paged_decode_plan_fp8", "paged_decode_run_fp8",
            "paged_decode_fp8_workspace_bytes", "kv_store_fp8_workspace_bytes",
            "kv_store_paged_decode_fp8_workspace_bytes", "paged_prefill_fp8_workspace_bytes",
-           "Rotary", "rotary", "rotary_frequencies", "qk_norm_rope", "qk_norm_rope_kv_store"]
+           "Rotary", "rotary", "rotary_frequencies", "qk_norm_rope", "qk_norm_rope_kv_store",
+           "paged_decode_shared", "paged_decode_plan_shared", "paged_decode_run_shared",
+           "paged_decode_shared_workspace_bytes"]

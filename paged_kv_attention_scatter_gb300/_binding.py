@@ -48,7 +48,9 @@ C_FUNCTIONS = ["pkv_version", "pkv_error_string", "pkv_status_string", "pkv_kv_s
                "pkv_kv_store_paged_decode_fp8", "pkv_paged_prefill_fp8_workspace_bytes",
                "pkv_paged_prefill_varlen_fp8", "pkv_apply_logit_rules",
                "pkv_rotary_frequencies", "pkv_rotary_turns", "pkv_qk_norm_rope",
-               "pkv_qk_norm_rope_kv_store"]
+               "pkv_qk_norm_rope_kv_store", "pkv_paged_decode_shared_workspace_bytes",
+               "pkv_paged_decode_shared", "pkv_paged_decode_plan_shared",
+               "pkv_paged_decode_run_shared"]
 
 # Size of the scratch array compiled into the library for
 # pkv_paged_decode_static_workspace (PKV_STATIC_DECODE_WORKSPACE_BYTES).
@@ -175,6 +177,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.pkv_qk_norm_rope_kv_store.argtypes = [P, I64, P, I64, P, I64, P, P, I32, F32, P,
                                               RotaryDesc, P, I32, I32, P, I64, P, I64, P, P,
                                               CacheDesc, P, P]
+    lib.pkv_paged_decode_shared_workspace_bytes.restype = SZ
+    lib.pkv_paged_decode_shared_workspace_bytes.argtypes = [I32, I32, I32, CacheDesc]
+    lib.pkv_paged_decode_shared.restype = ctypes.c_int
+    lib.pkv_paged_decode_shared.argtypes = [P, P, P, P, I32, P, P, P, I32, I32, I32, I32, F32, P,
+                                            P, SZ, CacheDesc, P, P]
+    lib.pkv_paged_decode_plan_shared.restype = ctypes.c_int
+    lib.pkv_paged_decode_plan_shared.argtypes = [P, P, P, I32, I32, I32, I32, I32, P, SZ,
+                                                 CacheDesc, P, P]
+    lib.pkv_paged_decode_run_shared.restype = ctypes.c_int
+    lib.pkv_paged_decode_run_shared.argtypes = [P, P, P, P, I32, I32, I32, I32, F32, P, P, SZ,
+                                                CacheDesc, P, P]
     _LIB = lib
     return lib
 
@@ -1119,4 +1132,124 @@ def qk_norm_rope_kv_store(q, k, v, q_weight, k_weight, eps, positions, rope, k_c
             *_heads(qo, "q_out", bf16, index, q.shape), *ko, *caches, _desc(*shape), st, s),
             "pkv_qk_norm_rope_kv_store")
         return qo
+    return _on(index, stream, call)
+
+
+# ----------------------------------------------------------------------------
+# Decode attention over shared prefixes.
+def paged_decode_shared_workspace_bytes(batch, num_q_heads, max_context_len, k_cache) -> int:
+    return int(load().pkv_paged_decode_shared_workspace_bytes(batch, num_q_heads,
+                                                              int(max_context_len),
+                                                              cache_desc(k_cache)))
+
+
+def _bf16_cache(k_cache, v_cache):
+    """Checks a bf16 cache; returns (device index, the two addresses, descriptor)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
+                         "num_kv_heads, head_dim]")
+    index = k_cache.get_device()
+    return index, (_at(k_cache, "k_cache", torch.bfloat16, index),
+                   _at(v_cache, "v_cache", torch.bfloat16, index)), _desc(*shape)
+
+
+def _groups(context_lens, group_offsets, prefix_lens, index):
+    """Addresses of a batch's lengths and groups, and the number of groups."""
+    ctx = _at(context_lens, "context_lens", torch.int32, index)
+    if group_offsets is None and prefix_lens is None:
+        return ctx, None, None, 0
+    if group_offsets is None or prefix_lens is None:
+        raise ValueError("group_offsets and prefix_lens go together")
+    n = prefix_lens.numel()
+    if prefix_lens.dim() != 1 or group_offsets.shape != (n + 1,):
+        raise ValueError("group_offsets must be [groups + 1] and prefix_lens [groups]")
+    return (ctx, _at(group_offsets, "group_offsets", torch.int32, index),
+            _at(prefix_lens, "prefix_lens", torch.int32, index), n)
+
+
+def paged_decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_offsets,
+                        prefix_lens, scale, max_context_len, out=None, workspace=None, status=None,
+                        stream=None) -> torch.Tensor:
+    """paged_decode of sequences in groups with their first keys in common, which are
+    read and multiplied once for a group: sequences group_offsets[g] ..
+    group_offsets[g + 1] - 1 (int32, [groups + 1], increasing) share the first prefix_lens[g]
+    ([groups] int32) of their keys, so that their block tables name the same blocks
+    there.  Other sequences attend by themselves.  Both may be None: no groups."""
+    lib = load()
+    index, cache, desc = _bf16_cache(k_cache, v_cache)
+    B, Hq, width, qp, bt, _ = _decode_batch(q, block_tables, context_lens, desc, index)
+    lens = _groups(context_lens, group_offsets, prefix_lens, index)
+    st = _maybe(status, "status", torch.int32, index)
+    max_len = int(max_context_len)
+
+    def call(s):
+        o = _out_like(out, q, index)
+        need = 0 if workspace is not None else _need("pkv_paged_decode_shared_workspace_bytes", B,
+                                                     Hq, max_len, *k_cache.shape)
+        ws, size, own = _scratch(workspace, need, index, s)
+        try:
+            _check(lib.pkv_paged_decode_shared(qp, *cache, bt, width, *lens, B, Hq, max_len,
+                                               float(scale), o.data_ptr(), ws, size, desc, st, s),
+                   "pkv_paged_decode_shared")
+        finally:
+            _done(own)
+        return o
+    return _on(index, stream, call)
+
+
+def paged_decode_plan_shared(context_lens, group_offsets, prefix_lens, num_q_heads,
+                             max_context_len, max_blocks_per_seq, k_cache, workspace=None,
+                             status=None, stream=None) -> torch.Tensor:
+    """The schedule of a batch of paged_decode_shared over a cache of k_cache's shape, for
+    any number of paged_decode_run_shared calls (one a layer).  Returns the workspace."""
+    lib = load()
+    index = k_cache.get_device()
+    _at(k_cache, "k_cache", torch.bfloat16, index)
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be [batch]")
+    lens = _groups(context_lens, group_offsets, prefix_lens, index)
+    st = _maybe(status, "status", torch.int32, index)
+    desc = _desc(*k_cache.shape)
+    B, Hq, max_len = context_lens.numel(), int(num_q_heads), int(max_context_len)
+
+    def call(s):
+        ws = workspace
+        if ws is None:
+            need = _need("pkv_paged_decode_shared_workspace_bytes", B, Hq, max_len,
+                         *k_cache.shape)
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=k_cache.device)
+        _check(lib.pkv_paged_decode_plan_shared(*lens, B, Hq, max_len, int(max_blocks_per_seq),
+                                                _at(ws, "workspace", torch.uint8, index),
+                                                ws.numel(), desc, st, s),
+               "pkv_paged_decode_plan_shared")
+        return ws
+    return _on(index, stream, call)
+
+
+def paged_decode_run_shared(q, k_cache, v_cache, block_tables, scale, max_context_len, workspace,
+                            out=None, status=None, stream=None) -> torch.Tensor:
+    """paged_decode_shared with the schedule a paged_decode_plan_shared call wrote into
+    `workspace` (same sizes)."""
+    lib = load()
+    index, cache, desc = _bf16_cache(k_cache, v_cache)
+    if len(q.shape) != 3 or q.shape[2] != desc.head_dim:
+        raise ValueError("q must be [batch, num_q_heads, head_dim] matching the cache")
+    B, Hq, _ = q.shape
+    if len(block_tables.shape) != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq]")
+    if workspace is None:
+        raise ValueError("workspace must hold a plan")
+    qp = _at(q, "q", torch.bfloat16, index)
+    bt = _at(block_tables, "block_tables", torch.int32, index)
+    ws = _at(workspace, "workspace", torch.uint8, index)
+    st = _maybe(status, "status", torch.int32, index)
+
+    def call(s):
+        o = _out_like(out, q, index)
+        _check(lib.pkv_paged_decode_run_shared(qp, *cache, bt, block_tables.shape[1], B, Hq,
+                                               int(max_context_len), float(scale), o.data_ptr(),
+                                               ws, workspace.numel(), desc, st, s),
+               "pkv_paged_decode_run_shared")
+        return o
     return _on(index, stream, call)

@@ -22,7 +22,7 @@ SOURCES = ["api.cu", "kv_store.cu", "paged_decode.cu", "paged_decode_tma.cu", "p
            "prefill_tc.cu",
            "sample.cu", "kv_store_fp8.cu", "paged_decode_fp8.cu", "paged_decode_fp8_tc.cu",
            "prefill_fp8.cu",
-           "logit_rules.cu", "qk_norm_rope.cu"]
+           "logit_rules.cu", "qk_norm_rope.cu", "paged_decode_shared.cu"]
 
 
 def nvcc_path() -> str:

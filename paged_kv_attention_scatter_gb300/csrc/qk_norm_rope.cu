@@ -317,13 +317,28 @@ __global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
                     if (has1) *reinterpret_cast<uint64_t*>(mine + e1 + 2 * i) = b.v[i];
                 }
                 __syncwarp();
-                auto at = [&](int e) {                       // the partner of entry e
-                    return e < half ? mine[e + half] : e < g.rotary_dim ? mine[e - half] : 0.f;
-                };
+                if (half % 4 == 0) {         // four entries have their partners in a row
+                    auto at = [&](int e, Pairs& to, int i) {
+                        ulonglong2 v = make_ulonglong2(0, 0);
+                        if (e < g.rotary_dim)
+                            v = *reinterpret_cast<const ulonglong2*>(
+                                mine + (e < half ? e + half : e - half));
+                        to.v[i] = v.x;
+                        to.v[i + 1] = v.y;
+                    };
+                    at(e0, pa, 0);
+                    at(e0 + 4, pa, 2);
+                    at(e1, pb, 0);
+                    at(e1 + 4, pb, 2);
+                } else {
+                    auto at = [&](int e) {
+                        return e < half ? mine[e + half] : e < g.rotary_dim ? mine[e - half] : 0.f;
+                    };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    pa.v[i] = pk2(at(e0 + 2 * i), at(e0 + 2 * i + 1));
-                    pb.v[i] = pk2(at(e1 + 2 * i), at(e1 + 2 * i + 1));
+                    for (int i = 0; i < 4; ++i) {
+                        pa.v[i] = pk2(at(e0 + 2 * i), at(e0 + 2 * i + 1));
+                        pb.v[i] = pk2(at(e1 + 2 * i), at(e1 + 2 * i + 1));
+                    }
                 }
             }
             __syncwarp();                    // the rows are read: they may be written in place
