@@ -11,30 +11,27 @@
 // sum l and an unnormalised o over some of the keys, and
 //   M = max m,  out = sum 2^(m - M) o / sum 2^(m - M) l.
 //
-// Work item = (record, kv head, tile of q heads).  A record is a run of keys for up to 256
-// rows: either common keys of a group's sequences, or own keys of one sequence.  Both go
-// through the same kernel, so that items bound by the tensor cores (many rows on the same
+// Work item = (record, kv head, tile of q heads).  A record is a run of keys for up to 128
+// rows: either common keys of some of a group's sequences, or own keys of one sequence.  Both
+// go through the same kernel, so that items bound by the tensor cores (many rows on the same
 // keys) and items bound by HBM (a few rows on keys of their own) run side by side.  One CTA
 // of plan_kernel sizes the records from the lengths and lays them out; CTAs of the
 // persistent attention kernel, one an SM, draw items from a counter.
 //
-// A CTA attends 128-row tiles against 128-key tiles:
-//   warps 0-3, 4-7  two softmax groups; thread i of a group owns row i = TMEM lane i.
-//                   P = exp2(S scale - m) is computed against the running maximum straight
-//                   away, and again, with the maximum taken and O and l rescaled, only
-//                   where its row sum passes 2^16 (and for the first tile).  P stays in
-//                   registers until then and goes over S in TMEM as bf16, unnormalised:
-//                   its relative rounding of 2^-9 is that of a bf16 softmax, l is summed
-//                   from the unrounded values.
-//   warp 8          the producer: draws items, loads Q tiles, K and V tiles (TMA, one box per
-//                   run of a cache block, or rows gathered with cp.async where the block
-//                   size is no multiple of 8)
-//   warp 9, 10      issue Q K^T and P V (tcgen05.mma, accumulators in TMEM)
-// An item of two row tiles gives each group its own: both multiply the same K and V
-// tiles, which halves what is read from L2 for each product.  An item of one row tile has
-// its key tiles dealt to the two groups in turn, each with a maximum, sum and O of its
-// own (two parts), so that one group's softmax runs beside the other's products.
-// TMEM columns: S0 [0,128), S1 [128,256), O0 [256,256+D), O1 [384,384+D).
+// A CTA attends a 128-row tile against 128-key tiles, with the roles of the prefill's
+// kernel (prefill_tc.cu, where the figures behind them stand):
+//   warps 0-3  softmax: thread i owns row i = TMEM lane i.  P = exp2(S scale - m) is
+//              computed against the running maximum straight away and goes over S in TMEM
+//              as bf16, unnormalised: its rounding of 2^-8 of itself is that of a bf16
+//              softmax, l is summed from the unrounded values.  Only for an item's first
+//              tile, and where a row's sum passes 2^16, the maximum is taken, O and l are
+//              rescaled and P computed again.
+//   warp 4     producer: draws items, loads Q and K tiles (TMA, one box a run of a cache
+//              block, or rows gathered with cp.async where the block size is no multiple
+//              of 8) into a ring of three
+//   warp 7     producer of the V tiles, likewise
+//   warp 5, 6  issue Q K^T into one of three S buffers, and P V (tcgen05.mma)
+// TMEM columns: S0 [0,128), S1 [128,256), S2 [256,384), O [384,384+D).
 //
 // Keys outside a tile's run and keys of a block id outside the pool have weight 0, and
 // their V rows are zeroed in shared memory, because unused cache slots may hold NaN.
@@ -54,18 +51,20 @@ namespace {
 constexpr int kRows = 128;               // rows of a tile (TMEM lanes)
 constexpr int kKeys = 128;               // key rows of a tile in shared memory
 constexpr int kHalf = kKeys * 128;       // bytes of a tile's 64-column block
-constexpr int kThreads = 384;
-constexpr int kItemRing = 4, kItemReaders = 10;
-constexpr int kMaskRing = 16;            // more tiles than are between producer and softmax
+constexpr int kThreads = 256;
+constexpr int kStages = 3;               // K, V and S buffers
+constexpr int kItemRing = 4, kItemReaders = 7;
+constexpr int kMaskRing = 8;             // more tiles than are between producer and softmax
+constexpr uint32_t kColO = 384;
 constexpr float kRescaleThreshold = 8.0f;   // log2 of the tolerated growth of a maximum
 constexpr float kSumTrigger = 65536.0f;
 constexpr int kSms = 152;                // of a GB300: sizes follow from the arguments alone
 
-// A run of keys for `seqs` sequences from b0 on (1: own keys of b0, read through its own
-// table; more: common keys, read through that of sequence `table`).
+// A run of keys for `seqs` sequences from b0 on, read through the table of sequence `table`
+// (own keys: one sequence, and its table).
 struct Record {
     int32_t b0, seqs, table, key_lo, key_hi;
-    int32_t part;                        // place of its (first) part among a sequence's
+    int32_t part;                        // place of its part among a sequence's
     int32_t pad0, pad1;
 };
 
@@ -77,7 +76,7 @@ struct SharedArgs {
     __nv_bfloat16* out;
     int32_t* ctrl;                       // [0] records, [1] items drawn
     int32_t* part_prefix;                // [B + 1]: parts of the sequences before
-    int32_t* group;                      // [B]: the sequence's group, -1: none
+    int2* sequences;                     // [B]: the plan's notes (see Sequence)
     int32_t* table;                      // [B], at a group's first sequence: whose table
     Record* records;
     float2* part_ml;                     // [cap_parts, Hq]: (max halved, sum)
@@ -102,11 +101,12 @@ __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) {
 
 // ---------------------------------------------------------------------- plan
 constexpr int kPlanThreads = 1024;
+constexpr int kStaged = 1024;            // groups held in shared memory
 // Fewer common keys than this are attended by each sequence itself.
 constexpr int kMinShared = 64;
-// What the plan expects, in ns: a key tile for two row tiles and for one, the start and end
-// of an item, and the bytes a ns of parts written and read again.
-constexpr int kPairTile = 1150, kTileCost = 1450, kItemCost = 2000, kPartBytes = 3500;
+// What the plan expects, in ns: a key tile of common keys and of own ones (which come from
+// HBM), the start and end of an item; and the bytes a ns of parts written and read again.
+constexpr float kCommonTile = 750, kOwnTile = 1450, kItemCost = 2500, kPartBytes = 3500;
 
 struct Group {
     int32_t first, seqs;
@@ -114,279 +114,281 @@ struct Group {
     int32_t keys;                        // those attended together: all of them, or 0
 };
 
-// Group g of the call; `ok`: the offsets are increasing and within the batch.
-__device__ __forceinline__ Group group_at(const SharedArgs& a, int32_t g, bool report) {
-    Group x{a.offsets[g], 0, a.prefix[g], 0};
-    x.seqs = a.offsets[g + 1] - x.first;
-    if (x.prefix < 0 || x.prefix > (int64_t)a.MB * a.bs || x.prefix > a.max_ctx) {
-        if (report) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
-        x.prefix = 0;
+// What a sequence attends: keys [0, prefix) with its group, [prefix, ctx) on its own.
+struct Sequence {
+    int32_t ctx, prefix;                 // ctx 0: nothing
+};
+
+// Groups as the plan reads them, the first kStaged from shared memory.
+struct Groups {
+    const SharedArgs& a;
+    const int32_t* offsets;
+    const int32_t* prefix;
+    __device__ __forceinline__ Group at(int32_t g, bool report) const {
+        Group x{offsets[g], 0, prefix[g], 0};
+        x.seqs = offsets[g + 1] - x.first;
+        if (x.prefix < 0 || x.prefix > (int64_t)a.MB * a.bs || x.prefix > a.max_ctx) {
+            if (report) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
+            x.prefix = 0;
+        }
+        if (x.seqs >= 2 && x.prefix >= kMinShared) x.keys = x.prefix;
+        return x;
     }
-    if (x.seqs >= 2 && x.prefix >= kMinShared) x.keys = x.prefix;
-    return x;
-}
+    // the group of sequence b among the first n, -1: none
+    __device__ __forceinline__ int32_t of(int32_t b, int32_t n) const {
+        int32_t lo = 0, hi = n;              // groups that begin at b or before
+        while (lo < hi) {
+            const int32_t mid = (lo + hi) / 2;
+            if (offsets[mid] <= b) lo = mid + 1;
+            else hi = mid;
+        }
+        return lo > 0 && b < offsets[lo] ? lo - 1 : -1;
+    }
+};
 
 // The first key tile of a run begins at a box of the cache block that key_lo lies in.
 __device__ __forceinline__ int32_t tile_origin(const SharedArgs& a, int32_t key_lo) {
     return key_lo / a.box * a.box;
 }
 __device__ __forceinline__ int32_t key_tiles(const SharedArgs& a, int32_t lo, int32_t hi) {
-    return ceil_div(hi - tile_origin(a, lo), a.tile_keys);
-}
-
-// Block-wide sum of v.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(~0u, v, off);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = scratch[threadIdx.x & 31];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(~0u, v, off);
-    return v;
+    return hi > lo ? ceil_div(hi - tile_origin(a, lo), a.tile_keys) : 0;
 }
 
 // Block-wide exclusive prefix of v, over `carry` (updated to the sum).
-__device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t& carry, int32_t* scratch) {
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t& carry, int64_t* scratch) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int32_t x = v;
+    int64_t x = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int32_t y = __shfl_up_sync(~0u, x, off);
+        const int64_t y = __shfl_up_sync(~0u, x, off);
         if (lane >= off) x += y;
     }
     __syncthreads();
     if (lane == 31) scratch[w] = x;
     __syncthreads();
-    int32_t s = scratch[lane];
+    int64_t s = scratch[lane];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int32_t y = __shfl_up_sync(~0u, s, off);
+        const int64_t y = __shfl_up_sync(~0u, s, off);
         if (lane >= off) s += y;
     }
-    const int32_t before = w > 0 ? __shfl_sync(~0u, s, w - 1) : 0;
-    const int32_t all = __shfl_sync(~0u, s, 31);
-    const int32_t r = carry + before + x - v;
+    const int64_t up = __shfl_sync(~0u, s, w > 0 ? w - 1 : 0);
+    const int64_t all = __shfl_sync(~0u, s, 31);
+    const int64_t r = carry + (w > 0 ? up : 0) + x - v;
     carry += all;
     return r;
 }
 
-// Parts of `tiles` key tiles cut every `len`: two of a run where its tiles are dealt to two
-// softmax groups, one where each group has rows of its own.
-__device__ __forceinline__ int32_t parts_of(int32_t tiles, int32_t len, bool dealt) {
-    const int32_t runs = ceil_div(tiles, len);
-    if (!dealt || runs == 0) return runs;
-    const int32_t last = tiles - (runs - 1) * len;
-    return (runs - 1) * min(2, len) + min(2, last);
-}
-
-// What a sequence attends: keys [0, prefix) with its group, [prefix, ctx) on its own.
-struct Sequence {
-    int32_t ctx, prefix, own_tiles;
-    bool dealt;                          // its row tile is the last, without another beside it
-    int32_t prefix_tiles;
-};
-
-__device__ __forceinline__ Sequence sequence_at(const SharedArgs& a, int32_t b, bool report) {
-    Sequence s{0, 0, 0, true, 0};
-    int32_t c = a.ctx[b];
-    if (c < 0 || c > (int64_t)a.MB * a.bs || c > a.max_ctx) {
-        if (report) pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
-        return s;
-    }
-    if (c == 0) return s;
-    const int32_t g = a.group[b];
-    if (g >= 0) {
-        const Group x = group_at(a, g, false);
-        if (x.prefix > c) {                  // a member without all of its group's keys
-            if (report) pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
-            return s;
-        }
-        if (x.keys > 0) {
-            s.prefix = x.keys;
-            s.prefix_tiles = key_tiles(a, 0, x.keys);
-            const int32_t tiles = ceil_div(x.seqs, a.tile_seqs);
-            s.dealt = (tiles & 1) && (b - x.first) / a.tile_seqs == tiles - 1;
-        }
-    }
-    s.ctx = c;
-    s.own_tiles = c > s.prefix ? key_tiles(a, s.prefix, c) : 0;
-    return s;
-}
-
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedArgs a) {
     pkv::allow_dependent_launch();
-    __shared__ int64_t sums[32];
-    __shared__ int32_t scans[32];
+    __shared__ int64_t scratch[32];
+    // common tiles of row tiles, of sequences; own tiles; row tiles; sequences with own keys;
+    // common records, own records
+    __shared__ unsigned long long sum[7];
     __shared__ int32_t run_len[2];           // key tiles of a common run, of an own run
-    const int tid = threadIdx.x;
+    __shared__ int32_t staged_offsets[kStaged + 1], staged_prefix[kStaged];
+    const int tid = threadIdx.x, lane = tid & 31;
     const int32_t units = a.Hkv * a.head_tiles;
 
     // ---- groups: increasing offsets within the batch, or none is used
-    bool bad = false;
-    for (int32_t g = tid; g <= a.groups; g += kPlanThreads) {
-        const int32_t o = a.groups > 0 ? a.offsets[g] : 0;
-        bad |= o < 0 || o > a.B || (g > 0 && o < a.offsets[g - 1]);
-    }
-    const int32_t groups = __syncthreads_or(bad) ? 0 : a.groups;
-    if (groups != a.groups && tid == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
-    for (int32_t b = tid; b < a.B; b += kPlanThreads) {
-        int32_t lo = 0, hi = groups;         // groups that begin at b or before
-        while (lo < hi) {
-            const int32_t mid = (lo + hi) / 2;
-            if (a.offsets[mid] <= b) lo = mid + 1;
-            else hi = mid;
-        }
-        a.group[b] = lo > 0 && b < a.offsets[lo] ? lo - 1 : -1;
-        a.table[b] = INT32_MAX;
+    const bool staged = a.groups <= kStaged;
+    if (tid < 7) sum[tid] = 0;
+    if (staged && a.groups > 0) {
+        for (int32_t g = tid; g <= a.groups; g += kPlanThreads) staged_offsets[g] = a.offsets[g];
+        for (int32_t g = tid; g < a.groups; g += kPlanThreads) staged_prefix[g] = a.prefix[g];
     }
     __syncthreads();
-    // ---- how much there is: common tiles of row pairs and of lone row tiles, own tiles
-    int64_t pair_tiles = 0, lone_tiles = 0, own_tiles = 0, members = 0, runs = 0;
-    for (int32_t g = tid; g < groups; g += kPlanThreads) {
-        const Group x = group_at(a, g, true);
-        if (x.keys == 0) continue;
-        const int32_t tiles = ceil_div(x.seqs, a.tile_seqs), n = key_tiles(a, 0, x.keys);
-        pair_tiles += (int64_t)(tiles / 2) * n;
-        lone_tiles += (int64_t)(tiles & 1) * n;
-        runs += (tiles + 1) / 2;
-        members += (int64_t)x.seqs * n;
+    const Groups of{a, staged ? staged_offsets : a.offsets, staged ? staged_prefix : a.prefix};
+    bool bad = false;
+    if (a.groups > 0)
+        for (int32_t g = tid; g <= a.groups; g += kPlanThreads) {
+            const int32_t o = of.offsets[g];
+            bad |= o < 0 || o > a.B || (g > 0 && o < of.offsets[g - 1]);
+        }
+    const int32_t groups = __syncthreads_or(bad) ? 0 : a.groups;
+    if (groups != a.groups && tid == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
+
+    // ---- how much there is
+    auto add = [&](int which, int32_t v) {   // a warp's values into sum[which]
+        v = __reduce_add_sync(~0u, v);
+        if (lane == 0 && v != 0) atomicAdd(&sum[which], (unsigned long long)v);
+    };
+    for (int32_t base = 0; base < groups; base += kPlanThreads) {
+        const int32_t g = base + tid;
+        Group x{};
+        if (g < groups) x = of.at(g, true);
+        int32_t tiles = 0, n = 0;
+        if (x.keys > 0) {
+            tiles = ceil_div(x.seqs, a.tile_seqs);
+            n = key_tiles(a, 0, x.keys);
+            a.table[x.first] = INT32_MAX;
+            // these may pass 32 bits when added up
+            atomicAdd(&sum[0], (unsigned long long)tiles * n);
+            atomicAdd(&sum[1], (unsigned long long)x.seqs * n);
+        }
+        add(3, tiles);
     }
-    int32_t busy = 0;
-    for (int32_t b = tid; b < a.B; b += kPlanThreads) {
-        const Sequence s = sequence_at(a, b, true);
-        own_tiles += s.own_tiles;
-        busy += s.own_tiles > 0;
-        if (s.prefix > 0) atomicMin(&a.table[a.offsets[a.group[b]]], b);
+    __syncthreads();
+    Sequence mine{};                         // of sequence tid; the others' are noted
+    auto sequence_at = [&](int32_t b) {
+        Sequence s{0, 0};
+        const int32_t c = a.ctx[b];
+        if (c < 0 || c > (int64_t)a.MB * a.bs || c > a.max_ctx) {
+            pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
+            return s;
+        }
+        const int32_t g = c > 0 ? of.of(b, groups) : -1;
+        if (g >= 0) {
+            const Group x = of.at(g, false);
+            if (x.prefix > c) {              // a member without all of its group's keys
+                pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
+                return s;
+            }
+            s.prefix = x.keys;
+            if (x.keys > 0) atomicMin(&a.table[x.first], b);
+        }
+        s.ctx = c;
+        return s;
+    };
+    for (int32_t base = 0; base < a.B; base += kPlanThreads) {
+        const int32_t b = base + tid;
+        Sequence s{};
+        if (b < a.B) s = sequence_at(b);
+        if (base == 0) mine = s;
+        else if (b < a.B) a.sequences[b] = make_int2(s.ctx, s.prefix);
+        const int32_t own = key_tiles(a, s.prefix, s.ctx);
+        add(2, own);
+        add(4, own > 0);
     }
-    pair_tiles = block_sum(pair_tiles, sums);
-    lone_tiles = block_sum(lone_tiles, sums);
-    own_tiles = block_sum(own_tiles, sums);
-    members = block_sum(members, sums);
-    runs = block_sum(runs, sums);
-    const int32_t sequences = (int32_t)block_sum(busy, sums);
+    auto noted = [&](int32_t b) {
+        Sequence s = mine;
+        if (b >= a.B) s = Sequence{};
+        else if (b >= kPlanThreads) {
+            const int2 n = a.sequences[b];
+            s = Sequence{n.x, n.y};
+        }
+        return s;
+    };
+    __syncthreads();
 
     // ---- run lengths: lane l of the first warp weighs common runs of a length
     if (tid < 32) {
+        const float common_tiles = (float)sum[0], members = (float)sum[1];
+        const int64_t own_tiles = (int64_t)sum[2];
         // own runs: eight items an SM up to four tiles each, then up to sixteen items
-        const int64_t eight = (own_tiles * units + 8 * kSms - 1) / (8 * kSms);
-        const int64_t sixteen = (own_tiles * units + 16 * kSms - 1) / (16 * kSms);
-        const int32_t own = (int32_t)max(max(min(eight, (int64_t)4), sixteen), (int64_t)1);
-        const int64_t own_cost = (own_tiles * kTileCost +
-                                  (own_tiles / own + sequences) * kItemCost) * units;
+        const int64_t work = own_tiles * units;
+        int64_t own = (work + 8 * kSms - 1) / (8 * kSms);
+        own = own < 4 ? own : 4;
+        const int64_t sixteen = (work + 16 * kSms - 1) / (16 * kSms);
+        own = own > sixteen ? own : sixteen;
+        if (own < 1) own = 1;
+        const float own_cost = (own_tiles * kOwnTile +
+                                ((float)own_tiles / own + (float)sum[4]) * kItemCost) * units;
         // lengths 1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, ...
-        const int l = tid;
-        const int32_t len = l < 4 ? l + 1 : (4 + (l & 3)) << ((l >> 2) - 1);
-        const int64_t items = ((pair_tiles + lone_tiles) / len + runs) * units;
-        const int64_t item = (int64_t)len * (pair_tiles > 0 ? kPairTile : kTileCost) + kItemCost;
-        const int64_t rounds = (items + kSms - 1) / kSms;
-        int64_t cost = max(rounds * item, (items * item + own_cost) / kSms);
+        const int32_t len = lane < 4 ? lane + 1 : (4 + (lane & 3)) << ((lane >> 2) - 1);
+        const float items = (common_tiles / len + (float)sum[3]) * units;
+        const float item = len * kCommonTile + kItemCost;
+        float cost = fmaxf(ceilf(items / kSms) * item, (items * item + own_cost) / kSms);
         // parts: written once, read once, by all rows
         cost += members / len * a.Hq * a.D * 4 / kPartBytes;
-        if (members / len > a.common_budget) cost = INT64_MAX;
-        int64_t best = cost;
+        if ((int64_t)sum[1] / len > a.common_budget) cost = INFINITY;
+        float best = cost;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) best = min(best, __shfl_xor_sync(~0u, best, off));
+        for (int off = 16; off > 0; off >>= 1)
+            best = fminf(best, __shfl_xor_sync(~0u, best, off));
         const uint32_t who = __ballot_sync(~0u, cost == best);
         int32_t chosen = __shfl_sync(~0u, len, __ffs(who) - 1);
-        if (best == INT64_MAX)                           // longer than any of these
-            chosen = (int32_t)((members + a.common_budget - 1) / a.common_budget);
+        if (best == INFINITY)                            // longer than any of these
+            chosen = (int32_t)(((int64_t)sum[1] + a.common_budget - 1) / a.common_budget);
         if (tid == 0) {
             run_len[0] = chosen;
-            run_len[1] = own;
+            run_len[1] = (int32_t)own;
         }
     }
     __syncthreads();
     const int32_t common = run_len[0], own = run_len[1];
 
-    // ---- the sequences' parts, and how many records there are of each kind
-    int32_t carry = 0;
-    for (int32_t base = 0; base < a.B; base += kPlanThreads) {
-        const int32_t b = base + tid;
-        Sequence s{};
-        if (b < a.B) s = sequence_at(a, b, false);
-        const int32_t n = parts_of(s.prefix_tiles, common, s.dealt) +
-                          parts_of(s.own_tiles, own, true);
-        const int32_t at = block_prefix(n, carry, scans);
-        if (b < a.B) a.part_prefix[b] = at;
-    }
-    if (tid == 0) a.part_prefix[a.B] = carry;
-    int32_t n_common = 0, n_own = 0;
-    for (int32_t g = tid; g < groups; g += kPlanThreads) {
-        const Group x = group_at(a, g, false);
-        if (x.keys > 0)
-            n_common += (ceil_div(x.seqs, a.tile_seqs) + 1) / 2 *
-                        ceil_div(key_tiles(a, 0, x.keys), common);
-    }
-    for (int32_t b = tid; b < a.B; b += kPlanThreads)
-        n_own += ceil_div(sequence_at(a, b, false).own_tiles, own);
-    n_common = (int32_t)block_sum(n_common, sums);
-    n_own = (int32_t)block_sum(n_own, sums);
-    const bool fits = n_common + n_own <= a.cap_records && carry <= a.cap_parts;
-    if (!fits) {                             // cannot be: the lengths above allow for it
-        if (tid == 0) pkv::report(a.status, PKV_STATUS_WORKSPACE_OVERFLOW);
-        for (int32_t b = tid; b <= a.B; b += kPlanThreads) a.part_prefix[b] = 0;
-    }
-    if (tid == 0) {
-        a.ctrl[0] = fits ? n_common + n_own : 0;
-        a.ctrl[1] = 0;
-    }
-    if (!fits) return;
-    // ---- records: the common ones spread over the first three quarters of the own ones, so
-    // that the two kinds run side by side and short items come last
-    const int32_t spread = max(1, n_own - n_own / 4);
-    auto common_at = [&](int32_t i) {
-        return n_own == 0 ? i : i + (int32_t)((int64_t)i * spread / n_common);
-    };
-    auto own_at = [&](int32_t j) {
-        const int64_t before = ((int64_t)(j + 1) * n_common + spread - 1) / spread;
-        return j + (int32_t)min(before, (int64_t)n_common);
-    };
-    carry = 0;
+    // ---- how many records there are of each kind
     for (int32_t base = 0; base < groups; base += kPlanThreads) {
         const int32_t g = base + tid;
         Group x{};
-        int32_t pairs = 0, cuts = 0, tiles = 0;
-        if (g < groups) x = group_at(a, g, false);
+        if (g < groups) x = of.at(g, false);
+        add(5, x.keys > 0 ? ceil_div(x.seqs, a.tile_seqs) *
+                                ceil_div(key_tiles(a, 0, x.keys), common)
+                          : 0);
+    }
+    for (int32_t base = 0; base < a.B; base += kPlanThreads) {
+        const Sequence s = noted(base + tid);
+        add(6, ceil_div(key_tiles(a, s.prefix, s.ctx), own));
+    }
+    __syncthreads();
+    const int32_t n_common = (int32_t)sum[5], n_own = (int32_t)sum[6];
+    // ---- records: the common ones spread over the first three quarters of the own ones, so
+    // that the two kinds run side by side and short items come last
+    const int32_t spread = max(1, n_own - n_own / 4);
+    auto put = [&](int64_t at, const Record& r) {
+        if (at < a.cap_records) a.records[at] = r;
+    };
+    int64_t carry = 0;
+    for (int32_t base = 0; base < groups; base += kPlanThreads) {
+        const int32_t g = base + tid;
+        Group x{};
+        if (g < groups) x = of.at(g, false);
+        int32_t tiles = 0, cuts = 0;
         if (x.keys > 0) {
             tiles = ceil_div(x.seqs, a.tile_seqs);
-            pairs = (tiles + 1) / 2;
             cuts = ceil_div(key_tiles(a, 0, x.keys), common);
         }
-        const int32_t at = block_prefix(pairs * cuts, carry, scans);
-        for (int32_t i = 0; i < pairs * cuts; ++i) {
-            const int32_t cut = i / pairs, pair = i - cut * pairs;
+        const int32_t first = (int32_t)block_prefix(tiles * cuts, carry, scratch);
+        for (int32_t i = 0; i < tiles * cuts; ++i) {
+            const int32_t cut = i / tiles, tile = i - cut * tiles;
             Record r{};
-            r.b0 = x.first + pair * 2 * a.tile_seqs;
-            r.seqs = min(2 * a.tile_seqs, x.first + x.seqs - r.b0);
+            r.b0 = x.first + tile * a.tile_seqs;
+            r.seqs = min(a.tile_seqs, x.first + x.seqs - r.b0);
             r.table = a.table[x.first];
             r.key_lo = cut * common * a.tile_keys;
             r.key_hi = min(x.keys, (cut + 1) * common * a.tile_keys);
-            r.part = cut * (r.seqs <= a.tile_seqs ? min(2, common) : 1);
+            r.part = cut;
             // no member has keys: nobody's table to read
             if (r.table == INT32_MAX) r.key_hi = r.key_lo;
-            a.records[common_at(at + i)] = r;
+            const int64_t at = first + i;
+            put(n_own == 0 ? at : at + at * spread / n_common, r);
         }
     }
+    // ---- and each sequence's parts: those of its group's runs, then those of its own
     carry = 0;
     for (int32_t base = 0; base < a.B; base += kPlanThreads) {
         const int32_t b = base + tid;
-        Sequence s{};
-        if (b < a.B) s = sequence_at(a, b, false);
-        const int32_t n = ceil_div(s.own_tiles, own);
-        const int32_t at = block_prefix(n, carry, scans);
-        const int32_t first = parts_of(s.prefix_tiles, common, s.dealt);
-        const int32_t origin = tile_origin(a, s.prefix);
+        const Sequence s = noted(b);
+        const int32_t n = ceil_div(key_tiles(a, s.prefix, s.ctx), own);
+        const int32_t before = ceil_div(key_tiles(a, 0, s.prefix), common);
+        const int64_t at = block_prefix((int64_t)(before + n) << 32 | n, carry, scratch);
+        if (b < a.B) a.part_prefix[b] = (int32_t)(at >> 32);
+        const int32_t first = (int32_t)at, origin = tile_origin(a, s.prefix);
         for (int32_t i = 0; i < n; ++i) {
             Record r{};
             r.b0 = r.table = b;
             r.seqs = 1;
             r.key_lo = i == 0 ? s.prefix : origin + i * own * a.tile_keys;
             r.key_hi = min(s.ctx, origin + (i + 1) * own * a.tile_keys);
-            r.part = first + i * min(2, own);
-            a.records[own_at(at + i)] = r;
+            r.part = before + i;
+            const int64_t j = first + i;
+            const int64_t ahead = ((j + 1) * n_common + spread - 1) / spread;
+            put(j + min(ahead, (int64_t)n_common), r);
         }
+    }
+    const int32_t parts = (int32_t)(carry >> 32);
+    if (tid == 0) a.part_prefix[a.B] = parts;
+    // cannot be: the run lengths allow for it
+    const bool fits = (int64_t)n_common + n_own <= a.cap_records && parts <= a.cap_parts;
+    if (!fits) {
+        if (tid == 0) pkv::report(a.status, PKV_STATUS_WORKSPACE_OVERFLOW);
+        __syncthreads();
+        for (int32_t b = tid; b <= a.B; b += kPlanThreads) a.part_prefix[b] = 0;
+    }
+    if (tid == 0) {
+        a.ctrl[0] = fits ? n_common + n_own : 0;
+        a.ctrl[1] = 0;
     }
 }
 
@@ -394,19 +396,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedArgs a) {
 template <int D>
 struct __align__(1024) Smem {
     static constexpr int kTile = kKeys * D * 2;            // bytes of a Q, K or V tile
-    static constexpr int kSlots = D == 128 ? 5 : 12;       // K and V tiles in turn
-    unsigned char q[2][kTile];
-    unsigned char kv[kSlots][kTile];
-    uint64_t q_full[2], q_empty[2];
-    uint64_t kv_full[kSlots], kv_empty[kSlots];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+    unsigned char q[kTile];
+    unsigned char k[kStages][kTile];
+    unsigned char v[kStages][kTile];
+    uint64_t q_full, q_free;
+    uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
+    uint64_t s_full[kStages], p_full[kStages], pv_done[kStages];
+    uint64_t o_free, mma_done;
     uint64_t item_full[kItemRing], item_empty[kItemRing];
-    uint64_t mma_done;
+    uint64_t mask_full[kMaskRing];
     uint4 mask[kMaskRing];                                 // keys of a tile that count
     struct Item {
-        int32_t b0, seqs, key_lo, key_hi, origin, tiles, kvh, head_tile, part;
-        int32_t group;                                     // softmax group of the first tile
-        int32_t end;
+        int32_t b0, seqs, table, key_lo, key_hi, origin, tiles, kvh, head_tile, part, end;
     } items[kItemRing];
     uint32_t tmem_base;
     int abort_flag;
@@ -500,6 +501,62 @@ __device__ __forceinline__ void gather_rows(const int64_t (&src)[4], const __nv_
         }
 }
 
+// Where a lane finds its part of a key tile.
+struct Source {
+    uint32_t valid[4];                   // keys that count
+    int64_t rows[4];                     // kGather: element offsets of rows l, l + 32, ..., -1: none
+    int32_t row;                         // else: the pool row of this lane's box, -1: none
+    int32_t box, boxes;                  // rows of a box; boxes to load
+    bool full, bad;                      // all keys of the tile are in the run; a bad block id
+};
+
+template <int D, bool kGather>
+__device__ __forceinline__ Source find_tile(const SharedArgs& a, const int32_t* table, int32_t key_lo,
+                                            int32_t key_hi, int32_t key0, int32_t kvh, int lane) {
+    Source s;
+    const int32_t lo = max(key_lo - key0, 0), hi = min(key_hi - key0, a.tile_keys);
+    s.full = lo == 0 && hi == a.tile_keys;
+    s.box = s.full ? a.box : a.edge_box;
+    s.row = -1;
+    s.bad = false;
+    if constexpr (kGather) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int32_t i = g * 32 + lane, key = key0 + i;
+            s.rows[g] = -1;
+            if (i >= lo && i < hi) {
+                const int32_t blk = __ldg(table + key / a.bs);
+                if ((unsigned)blk < (unsigned)a.NB)
+                    s.rows[g] = (((int64_t)blk * a.bs + key % a.bs) * a.Hkv + kvh) * D;
+                else
+                    s.bad = true;
+            }
+            s.valid[g] = __ballot_sync(0xffffffffu, s.rows[g] >= 0);
+        }
+        s.boxes = 0;
+    } else {
+        const int32_t i = lane * s.box, key = key0 + i;
+        const bool wanted = i < hi && i + s.box > lo;
+        if (wanted) {
+            const int32_t blk = __ldg(table + key / a.bs);
+            if ((unsigned)blk < (unsigned)a.NB) s.row = blk * a.bs + key % a.bs;
+            else s.bad = true;
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) s.valid[w] = range_word(lo, hi, w);
+        uint32_t gone = __ballot_sync(0xffffffffu, s.bad);
+        while (gone) {
+            const int u = __ffs(gone) - 1;
+            gone &= gone - 1;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                s.valid[w] &= ~range_word(u * s.box, (u + 1) * s.box, w);
+        }
+        s.boxes = __popc(__ballot_sync(0xffffffffu, s.row >= 0));
+    }
+    return s;
+}
+
 // kGather: rows gathered (block sizes that are no multiple of 8).  kPolls: the waits take
 // their limit from the arguments (pkv_set_wait_poll_limit).
 template <int D, bool kGather, bool kPolls>
@@ -507,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     shared_kernel(const __grid_constant__ Maps maps, const SharedArgs a) {
     using S = Smem<D>;
     using Item = typename S::Item;
-    constexpr int kTile = S::kTile, kSlots = S::kSlots, kBlocks = D / 64;
+    constexpr int kTile = S::kTile, kBlocks = D / 64;
     const uint32_t polls = kPolls ? a.wait_polls : (uint32_t)PKV_DEFAULT_WAIT_POLLS;
     extern __shared__ unsigned char smem_raw[];
     S& s = *reinterpret_cast<S*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -515,38 +572,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         s.abort_flag = 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.q_full[i], 1);
-            mbar_init(&s.q_empty[i], 1);
-            mbar_init(&s.s_full[i], 2);
+        mbar_init(&s.q_full, 1);
+        mbar_init(&s.q_free, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.v_full[i], 1);
+            mbar_init(&s.k_empty[i], 1);
+            mbar_init(&s.v_empty[i], 1);
+            mbar_init(&s.s_full[i], 1);
             mbar_init(&s.p_full[i], 4);
             mbar_init(&s.pv_done[i], 1);
-            mbar_init(&s.o_free[i], 4);
         }
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&s.kv_full[i], 1);
-            mbar_init(&s.kv_empty[i], 1);
-        }
+        mbar_init(&s.o_free, 4);
         for (int i = 0; i < kItemRing; ++i) {
             mbar_init(&s.item_full[i], 1);
             mbar_init(&s.item_empty[i], kItemReaders);
         }
+        for (int i = 0; i < kMaskRing; ++i) mbar_init(&s.mask_full[i], 1);
         mbar_init(&s.mma_done, 2);
         mbar_init_fence();
     }
-    if (warp == 9) tmem_alloc(&s.tmem_base, 512);
+    if (warp == 5) tmem_alloc(&s.tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem_base;
     pkv::wait_for_predecessor();             // the plan's records
     pkv::allow_dependent_launch();           // the combine reads the plan's parts at once
-    const int32_t units = a.Hkv * a.head_tiles;
-    const int64_t n_items64 = (int64_t)a.ctrl[0] * units;
-    const uint32_t n_items = (uint32_t)n_items64;
-    uint32_t fills = 0, q_fills = 0;         // the producer's
+    const uint32_t units = (uint32_t)(a.Hkv * a.head_tiles);
+    const uint32_t n_items = (uint32_t)a.ctrl[0] * units;
+    uint32_t fills = 0, q_fills = 0;         // a producer's tiles, and Q tiles
 
-    // Item I from the producer's ring; false: none in time.
+    // Item I from the ring; false: none in time.
     auto next_item = [&](uint32_t I, Item& x, bool warp_wide) {
         const int r = I % kItemRing;
         const uint32_t par = (I / kItemRing) & 1;
@@ -559,166 +616,125 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
     };
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ producer
+    if (warp == 4 || warp == 7) {
+        // ------------------------------------------------------------ producers
+        const bool k_side = warp == 4;
+        uint64_t* full = k_side ? s.k_full : s.v_full;
+        uint64_t* empty = k_side ? s.k_empty : s.v_empty;
+        const CUtensorMap* whole_map = k_side ? &maps.k : &maps.v;
+        const CUtensorMap* edge_map = k_side ? &maps.k_edge : &maps.v_edge;
+        const __nv_bfloat16* pool = k_side ? a.kc : a.vc;
         if (lane == 0) {
-            tma_prefetch_desc(&maps.q);
-            tma_prefetch_desc(&maps.q_one);
+            if (k_side) {
+                tma_prefetch_desc(&maps.q);
+                tma_prefetch_desc(&maps.q_one);
+            }
             if (!kGather) {
-                tma_prefetch_desc(&maps.k);
-                tma_prefetch_desc(&maps.v);
-                tma_prefetch_desc(&maps.k_edge);
-                tma_prefetch_desc(&maps.v_edge);
+                tma_prefetch_desc(whole_map);
+                tma_prefetch_desc(edge_map);
             }
         }
         const uint32_t wrap = n_items + gridDim.x - 1;     // the last draw resets the counter
         auto draw = [&]() {
-            return lane == 0 ? atomicInc((unsigned int*)a.ctrl + 1, wrap) : 0u;
+            return k_side && lane == 0 ? atomicInc((unsigned int*)a.ctrl + 1, wrap) : 0u;
         };
-        uint32_t tile_no = 0, group = 0;
         bool ok = true, bad_block = false;
-        int pend = -1;                       // a gathered slot in flight
-        auto land = [&](int slot) {
+        int pend = -1;                       // a gathered stage in flight
+        auto land = [&](int st) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.kv_full[slot]);
+            if (lane == 0) mbar_arrive(&full[st]);
         };
         uint32_t next = draw(), it = __shfl_sync(0xffffffffu, next, 0);
         for (uint32_t I = 0; ok; ++I) {
-            const int ring = I % kItemRing;
-            if (I >= kItemRing && !(ok = warp_wait(&s.item_empty[ring], (I / kItemRing - 1) & 1,
-                                                   &s.abort_flag, polls)))
-                break;
-            if (it >= n_items) {
+            Item x;
+            if (k_side) {
+                const int ring = I % kItemRing;
+                if (I >= kItemRing &&
+                    !(ok = warp_wait(&s.item_empty[ring], (I / kItemRing - 1) & 1, &s.abort_flag,
+                                     polls)))
+                    break;
+                if (it >= n_items) {
+                    if (lane == 0) {
+                        s.items[ring].end = 1;
+                        mbar_arrive(&s.item_full[ring]);
+                    }
+                    break;
+                }
+                next = draw();               // needed only behind this item's loads
+                const uint32_t rec = it / units, unit = it - rec * units;
+                const int4 r0 = *reinterpret_cast<const int4*>(a.records + rec);
+                const int2 r1 = *reinterpret_cast<const int2*>(&a.records[rec].key_hi);
+                x.b0 = r0.x;
+                x.seqs = r0.y;
+                x.table = r0.z;
+                x.key_lo = r0.w;
+                x.key_hi = r1.x;
+                x.part = r1.y;
+                x.origin = tile_origin(a, x.key_lo);
+                x.tiles = key_tiles(a, x.key_lo, x.key_hi);
+                x.kvh = unit / a.head_tiles;
+                x.head_tile = unit - x.kvh * a.head_tiles;
+                x.end = 0;
                 if (lane == 0) {
-                    s.items[ring].end = 1;
+                    s.items[ring] = x;
                     mbar_arrive(&s.item_full[ring]);
                 }
-                break;
+            } else {
+                if (!(ok = next_item(I, x, true)) || x.end) break;
             }
-            next = draw();                   // needed only behind this item's loads
-            const int32_t rec = (int32_t)(it / units), unit = (int32_t)(it - rec * units);
-            const int4 r0 = *reinterpret_cast<const int4*>(a.records + rec);
-            const int2 r1 = *reinterpret_cast<const int2*>(&a.records[rec].key_hi);
-            Item x;
-            x.b0 = r0.x;
-            x.seqs = r0.y;
-            const int32_t* table = a.bt + (int64_t)r0.z * a.MB;
-            x.key_lo = r0.w;
-            x.key_hi = r1.x;
-            x.part = r1.y;
-            x.origin = tile_origin(a, x.key_lo);
-            x.tiles = x.key_hi > x.key_lo ? ceil_div(x.key_hi - x.origin, a.tile_keys) : 0;
-            x.kvh = unit / a.head_tiles;
-            x.head_tile = unit - x.kvh * a.head_tiles;
-            x.end = 0;
-            const bool pair = x.seqs > a.tile_seqs;
-            x.group = pair ? 0 : group;
-            if (lane == 0) {
-                s.items[ring] = x;
-                mbar_arrive(&s.item_full[ring]);
-            }
-            if (x.tiles > 0) {
-                // ---- Q: one or two row tiles
-                const CUtensorMap* qm = x.seqs == 1 ? &maps.q_one : &maps.q;
-                const uint32_t q_bytes =
-                    (uint32_t)(kBlocks * 128 * a.tile_heads * (x.seqs == 1 ? 1 : a.tile_seqs));
-                for (int t = 0; t < (pair ? 2 : 1); ++t) {
-                    const int slot = q_fills & 1;
-                    if (q_fills >= 2 &&
-                        !(ok = warp_wait(&s.q_empty[slot], (q_fills / 2 - 1) & 1, &s.abort_flag,
-                                         polls)))
-                        break;
-                    if (lane == 0) {
-                        mbar_expect_tx(&s.q_full[slot], q_bytes);
-                        for (int hf = 0; hf < kBlocks; ++hf)
-                            tma_load_4d(s.q[slot] + hf * kHalf, qm, &s.q_full[slot], hf * 64,
-                                        x.head_tile * a.tile_heads, x.kvh,
-                                        x.b0 + t * a.tile_seqs);
-                    }
-                    ++q_fills;
+            const int32_t* table = a.bt + (int64_t)x.table * a.MB;
+            if (k_side && x.tiles > 0) {
+                if (q_fills > 0 &&
+                    !(ok = warp_wait(&s.q_free, (q_fills - 1) & 1, &s.abort_flag, polls)))
+                    break;
+                if (lane == 0) {
+                    const CUtensorMap* m = x.seqs == 1 ? &maps.q_one : &maps.q;
+                    mbar_expect_tx(&s.q_full,
+                                   (uint32_t)(kBlocks * 128 * a.tile_heads *
+                                              (x.seqs == 1 ? 1 : a.tile_seqs)));
+                    for (int hf = 0; hf < kBlocks; ++hf)
+                        tma_load_4d(s.q + hf * kHalf, m, &s.q_full, hf * 64,
+                                    x.head_tile * a.tile_heads, x.kvh, x.b0);
                 }
-                if (!ok) break;
-                if (!pair) group ^= x.tiles & 1;
+                ++q_fills;
             }
-            // ---- K and V tiles
-            for (int32_t j = 0; j < x.tiles && ok; ++j, ++tile_no) {
-                const int32_t key0 = x.origin + j * a.tile_keys;
-                const int32_t lo = max(x.key_lo - key0, 0);
-                const int32_t hi = min(x.key_hi - key0, a.tile_keys);
-                uint32_t valid[4];
-                int64_t src[4];              // kGather: element offsets of rows, -1: none
-                int32_t row = -1;            // else: the pool row of this lane's box
-                const bool full = lo == 0 && hi == a.tile_keys;
-                const int32_t box = full ? a.box : a.edge_box;
+            for (int32_t j = 0; j < x.tiles; ++j, ++fills) {
+                const int st = fills % kStages;
+                const Source src = find_tile<D, kGather>(
+                    a, table, x.key_lo, x.key_hi, x.origin + j * a.tile_keys, x.kvh, lane);
+                bad_block |= src.bad;
+                if (fills >= kStages &&
+                    !(ok = warp_wait(&empty[st], (fills / kStages - 1) & 1, &s.abort_flag, polls)))
+                    break;
+                if (k_side && lane == 0) {
+                    s.mask[fills % kMaskRing] =
+                        make_uint4(src.valid[0], src.valid[1], src.valid[2], src.valid[3]);
+                    mbar_arrive(&s.mask_full[fills % kMaskRing]);
+                }
+                unsigned char* dst = k_side ? s.k[st] : s.v[st];
                 if constexpr (kGather) {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int32_t i = g * 32 + lane, key = key0 + i;
-                        src[g] = -1;
-                        if (i >= lo && i < hi) {
-                            const int32_t blk = __ldg(table + key / a.bs);
-                            if ((unsigned)blk < (unsigned)a.NB)
-                                src[g] = (((int64_t)blk * a.bs + key % a.bs) * a.Hkv + x.kvh) * D;
-                            else
-                                bad_block = true;
-                        }
-                        valid[g] = __ballot_sync(0xffffffffu, src[g] >= 0);
+                    gather_rows<D>(src.rows, pool, dst, lane);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (pend >= 0) {         // the tile before this one has landed
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        land(pend);
                     }
+                    pend = st;
                 } else {
-                    const int32_t i = lane * box, key = key0 + i;
-                    const bool wanted = i < hi && i + box > lo;
-                    if (wanted) {
-                        const int32_t blk = __ldg(table + key / a.bs);
-                        if ((unsigned)blk < (unsigned)a.NB) row = blk * a.bs + key % a.bs;
-                        else bad_block = true;
+                    if (lane == 0) {
+                        if (src.boxes > 0)
+                            mbar_expect_tx(&full[st],
+                                           (uint32_t)(src.boxes * src.box * 128 * kBlocks));
+                        else
+                            mbar_arrive(&full[st]);
                     }
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) valid[w] = range_word(lo, hi, w);
-                    uint32_t gone = __ballot_sync(0xffffffffu, wanted && row < 0);
-                    while (gone) {
-                        const int u = __ffs(gone) - 1;
-                        gone &= gone - 1;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            valid[w] &= ~range_word(u * box, (u + 1) * box, w);
-                    }
-                }
-                const int boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++fills) {
-                    const int slot = fills % kSlots;
-                    if (fills >= kSlots &&
-                        !(ok = warp_wait(&s.kv_empty[slot], (fills / kSlots - 1) & 1,
-                                         &s.abort_flag, polls)))
-                        break;
-                    if (kv == 0 && lane == 0)
-                        s.mask[tile_no % kMaskRing] =
-                            make_uint4(valid[0], valid[1], valid[2], valid[3]);
-                    if constexpr (kGather) {
-                        gather_rows<D>(src, kv ? a.vc : a.kc, s.kv[slot], lane);
-                        asm volatile("cp.async.commit_group;" ::: "memory");
-                        if (pend >= 0) {     // the tile before this one has landed
-                            asm volatile("cp.async.wait_group 1;" ::: "memory");
-                            land(pend);
-                        }
-                        pend = slot;
-                    } else {
-                        if (lane == 0) {
-                            if (boxes > 0)
-                                mbar_expect_tx(&s.kv_full[slot],
-                                               (uint32_t)(boxes * box * 128 * kBlocks));
-                            else
-                                mbar_arrive(&s.kv_full[slot]);
-                        }
-                        __syncwarp();
-                        if (row >= 0) {
-                            const CUtensorMap* m = full ? (kv ? &maps.v : &maps.k)
-                                                        : (kv ? &maps.v_edge : &maps.k_edge);
-                            for (int hf = 0; hf < kBlocks; ++hf)
-                                tma_load_3d(s.kv[slot] + hf * kHalf + lane * box * 128, m,
-                                            &s.kv_full[slot], hf * 64, x.kvh, row);
-                        }
+                    __syncwarp();
+                    if (src.row >= 0) {
+                        const CUtensorMap* m = src.full ? whole_map : edge_map;
+                        for (int hf = 0; hf < kBlocks; ++hf)
+                            tma_load_3d(dst + hf * kHalf + lane * src.box * 128, m, &full[st],
+                                        hf * 64, x.kvh, src.row);
                     }
                 }
             }
@@ -730,193 +746,166 @@ __global__ void __launch_bounds__(kThreads, 1)
             land(pend);
         }
         // every CTA draws until it gets nothing, so that the counter ends where it began
-        for (it = __shfl_sync(0xffffffffu, next, 0); it < n_items;)
-            it = __shfl_sync(0xffffffffu, draw(), 0);
+        if (k_side)
+            for (it = __shfl_sync(0xffffffffu, next, 0); it < n_items;)
+                it = __shfl_sync(0xffffffffu, draw(), 0);
         if (__any_sync(0xffffffffu, bad_block) && lane == 0)
             pkv::report(a.status, PKV_STATUS_BAD_BLOCK_ID);
         if (!ok && lane == 0) give_up(s, a.status);
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == 5 || warp == 6) {
         // ------------------------------------------------------------ MMA issuers
         if (lane == 0) {
             const uint32_t id_qk = umma_idesc_bf16(kRows, kKeys, false);
             const uint32_t id_pv = umma_idesc_bf16(kRows, D, true);
-            const uint64_t qd0 = umma_desc_sw128(saddr(s.q[0]), 16, 1024);
-            const uint64_t kd0 = umma_desc_sw128(saddr(s.kv[0]), 16, 1024);
-            const uint64_t vd0 = umma_desc_sw128(saddr(s.kv[0]), kHalf, 1024);
-            uint32_t n[2] = {0, 0};          // products of each group so far
-            uint32_t o_uses[2] = {0, 0};     // items each group's O was used for
-            uint32_t q_uses = 0;             // Q tiles so far
-            uint32_t tile_no = 0;
+            const uint64_t qd0 = umma_desc_sw128(saddr(s.q), 16, 1024);
+            const uint64_t kd0 = umma_desc_sw128(saddr(s.k[0]), 16, 1024);
+            const uint64_t vd0 = umma_desc_sw128(saddr(s.v[0]), kHalf, 1024);
+            uint32_t T = 0, uses = 0;        // tiles, items with tiles so far
             bool ok = true;
             for (uint32_t I = 0; ok; ++I) {
                 Item x;
                 if (!(ok = next_item(I, x, false)) || x.end) break;
                 if (x.tiles == 0) continue;
-                const bool pair = x.seqs > a.tile_seqs;
-                if (warp == 9) {
-                    for (int t = 0; t < (pair ? 2 : 1) && ok; ++t)
-                        ok = mbar_wait(&s.q_full[(q_uses + t) & 1], ((q_uses + t) / 2) & 1,
-                                       &s.abort_flag, polls);
-                    if (!ok) break;
-                    for (int32_t j = 0; j < x.tiles && ok; ++j) {
-                        const uint32_t fill = 2 * (tile_no + j), slot = fill % kSlots;
-                        if (!(ok = mbar_wait(&s.kv_full[slot], (fill / kSlots) & 1, &s.abort_flag,
+                if (warp == 5) {
+                    if (!(ok = mbar_wait(&s.q_full, uses & 1, &s.abort_flag, polls))) break;
+                    for (int32_t j = 0; j < x.tiles; ++j) {
+                        const uint32_t t = T + j;
+                        const int st = t % kStages;
+                        if (!(ok = mbar_wait(&s.k_full[st], (t / kStages) & 1, &s.abort_flag,
                                              polls)))
                             break;
-                        const uint64_t kd = kd0 + (uint64_t)(slot * (kTile >> 4));
-                        for (int t = 0; t < (pair ? 2 : 1); ++t) {
-                            const int g = pair ? t : (x.group + j) & 1;
-                            // this S still holds the group's last P until its product is done
-                            if (n[g] > 0 && !(ok = mbar_wait(&s.pv_done[g], (n[g] - 1) & 1,
-                                                             &s.abort_flag, polls)))
-                                break;
-                            tc_fence_after();
-                            const uint64_t qd =
-                                qd0 + (uint64_t)(((q_uses + t) & 1) * (kTile >> 4));
+                        // the S buffer still holds P of tile t-3 until its P V is done
+                        if (t >= kStages &&
+                            !(ok = mbar_wait(&s.pv_done[st], (t / kStages - 1) & 1,
+                                             &s.abort_flag, polls)))
+                            break;
+                        tc_fence_after();
+                        const uint64_t kd = kd0 + (uint64_t)(st * (kTile >> 4));
+                        const uint32_t d_s = tmem + st * kKeys;
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                                umma_bf16(tmem + g * kKeys, qd + off, kd + off, id_qk, kk > 0);
-                            }
-                            umma_commit(&s.s_full[g]);
-                            mbar_arrive(&s.s_full[g]);     // passes on the producer's mask
-                            ++n[g];
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                            umma_bf16(d_s, qd0 + off, kd + off, id_qk, kk > 0);
                         }
-                        if (!ok) break;
-                        umma_commit(&s.kv_empty[slot]);
+                        umma_commit(&s.s_full[st]);
+                        umma_commit(&s.k_empty[st]);
                     }
                     if (!ok) break;
-                    for (int t = 0; t < (pair ? 2 : 1); ++t)
-                        umma_commit(&s.q_empty[(q_uses + t) & 1]);
-                    q_uses += pair ? 2 : 1;
+                    umma_commit(&s.q_free);
                 } else {
-                    for (int32_t j = 0; j < x.tiles && ok; ++j) {
-                        const uint32_t fill = 2 * (tile_no + j) + 1, slot = fill % kSlots;
-                        const uint64_t vd = vd0 + (uint64_t)(slot * (kTile >> 4));
-                        const int steps =
-                            (min(x.key_hi - x.origin - j * a.tile_keys, a.tile_keys) + 15) / 16;
-                        for (int t = 0; t < (pair ? 2 : 1); ++t) {
-                            const int g = pair ? t : (x.group + j) & 1;
-                            const bool first = pair ? j == 0 : j < 2;
-                            if (!(ok = mbar_wait(&s.p_full[g], n[g] & 1, &s.abort_flag, polls)))
-                                break;
-                            if (first) {
-                                if (o_uses[g] > 0 &&
-                                    !(ok = mbar_wait(&s.o_free[g], (o_uses[g] - 1) & 1,
-                                                     &s.abort_flag, polls)))
-                                    break;
-                                ++o_uses[g];
-                            }
-                            if (!(ok = mbar_wait(&s.kv_full[slot], (fill / kSlots) & 1,
-                                                 &s.abort_flag, polls)))
-                                break;
-                            tc_fence_after();
-                            for (int kk = 0; kk < steps; ++kk)
-                                umma_bf16_tmem_a(tmem + 256 + g * 128, tmem + g * kKeys + kk * 8,
-                                                 vd + (kk * 2048 >> 4), id_pv,
-                                                 kk > 0 || !first ? 1u : 0u);
-                            umma_commit(&s.pv_done[g]);
-                            ++n[g];
-                        }
-                        if (!ok) break;
-                        umma_commit(&s.kv_empty[slot]);
+                    for (int32_t j = 0; j < x.tiles; ++j) {
+                        const uint32_t t = T + j;
+                        const int st = t % kStages;
+                        if (!(ok = mbar_wait(&s.p_full[st], (t / kStages) & 1, &s.abort_flag,
+                                             polls)))
+                            break;
+                        if (j == 0 && uses > 0 &&
+                            !(ok = mbar_wait(&s.o_free, (uses - 1) & 1, &s.abort_flag, polls)))
+                            break;
+                        if (!(ok = mbar_wait(&s.v_full[st], (t / kStages) & 1, &s.abort_flag,
+                                             polls)))
+                            break;
+                        tc_fence_after();
+                        const uint64_t vd = vd0 + (uint64_t)(st * (kTile >> 4));
+                        const uint32_t a_p = tmem + st * kKeys;
+                        const uint32_t acc0 = j > 0 ? 1u : 0u;
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            umma_bf16_tmem_a(tmem + kColO, a_p + kk * 8, vd + (kk * 2048 >> 4),
+                                             id_pv, kk > 0 ? 1u : acc0);
+                        umma_commit(&s.pv_done[st]);
+                        umma_commit(&s.v_empty[st]);
                     }
+                    if (!ok) break;
                 }
-                tile_no += x.tiles;
+                T += x.tiles;
+                ++uses;
             }
             if (!ok) give_up(s, a.status);
             // every product of both issuers has finished before TMEM is freed
             umma_commit(&s.mma_done);
             mbar_drain(&s.mma_done, 0);
         }
-    } else if (warp < 8) {
+    } else {
         // ------------------------------------------------------------ softmax
-        const int g = warp >> 2, i = tid & 127;            // group; row = TMEM lane
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_col = tmem + lanes + g * kKeys, o_col = tmem + lanes + 256 + g * 128;
+        const int i = tid;                                 // row = TMEM lane
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const int32_t my_seq = i / a.tile_heads, my_head = i - my_seq * a.tile_heads;
-        uint32_t n = 0, tile_no = 0;         // this group's products; the CTA's tiles
+        uint32_t T = 0;
         bool ok = true;
         for (uint32_t I = 0; ok; ++I) {
             Item x;
             if (!(ok = next_item(I, x, true)) || x.end) break;
-            const bool pair = x.seqs > a.tile_seqs;
-            const int32_t j0 = pair ? 0 : (x.group == g ? 0 : 1), step = pair ? 1 : 2;
-            if (j0 >= x.tiles) {
-                tile_no += x.tiles;
-                continue;
-            }
-            const int32_t seqs = pair ? (g == 0 ? a.tile_seqs : x.seqs - a.tile_seqs) : x.seqs;
+            if (x.tiles == 0) continue;
             const int32_t head = x.head_tile * a.tile_heads + my_head;
-            const bool mine = my_seq < seqs && my_seq < a.tile_seqs && head < a.G;
-            const bool active = (warp & 3) * 32 < min(seqs, a.tile_seqs) * a.tile_heads;
+            const bool mine = my_seq < x.seqs && head < a.G;
+            const bool active = warp * 32 < x.seqs * a.tile_heads;
             float m_run = -INFINITY, l_run = 0.f;
-            for (int32_t j = j0; j < x.tiles; j += step, ++n) {
-                const uint32_t t = tile_no + j;
-                if (!(ok = warp_wait(&s.s_full[g], n & 1, &s.abort_flag, polls))) break;
+            for (int32_t j = 0; j < x.tiles && ok; ++j) {
+                const uint32_t t = T + j;
+                const int st = t % kStages;
+                const uint32_t s_col = lanes + st * kKeys;
+                if (!(ok = warp_wait(&s.s_full[st], (t / kStages) & 1, &s.abort_flag, polls)))
+                    break;
+                if (!(ok = warp_wait(&s.mask_full[t % kMaskRing], (t / kMaskRing) & 1,
+                                     &s.abort_flag, polls)))
+                    break;
                 tc_fence_after();
                 const uint4 mk = s.mask[t % kMaskRing];
                 const uint32_t mask[4] = {mk.x, mk.y, mk.z, mk.w};
                 const bool whole = (mk.x & mk.y & mk.z & mk.w) == ~0u;
                 if (active) {
-                    uint32_t pw[64];
+                    float sv[kKeys];
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc) tmem_ld32(s_col + cc * 32, sv + cc * 32);
+                    tmem_wait_ld();
+                    if (!whole) {
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c)
+                            sv[c] = (mask[c >> 5] >> (c & 31)) & 1 ? sv[c] : -INFINITY;
+                    }
                     float sum = 0.f;
-                    // P against `neg_m`, 32 columns at a time, and its sum
+                    // P against `neg_m` over the first 64 columns of S, and its sum
                     auto exp_pass = [&](float neg_m) {
                         const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
                         const uint64_t neg2 = pk2(neg_m, neg_m);
-                        uint64_t l2[2] = {0, 0};
+                        uint64_t l2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
-                            float sv[32];
-                            tmem_ld32(s_col + cc * 32, sv);
-                            tmem_wait_ld();
-                            if (!whole) {
+                        for (int half = 0; half < 2; ++half) {
+                            float pw[32];
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    sv[e] = (mask[cc] >> e) & 1 ? sv[e] : -INFINITY;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 32; ++e) {
+                                const int c = half * 64 + 2 * e;
                                 float x0, x1;
-                                up2(fma2(pk2(sv[2 * e], sv[2 * e + 1]), scale2, neg2), x0, x1);
+                                up2(fma2(pk2(sv[c], sv[c + 1]), scale2, neg2), x0, x1);
                                 const float p0 = pkv::fast_exp2(x0), p1 = pkv::fast_exp2(x1);
                                 l2[e & 1] = add2(l2[e & 1], pk2(p0, p1));
-                                pw[cc * 16 + e] = pkv::pack_bf16(p0, p1);
+                                pw[e] = __uint_as_float(pkv::pack_bf16(p0, p1));
                             }
+                            tmem_st32(s_col + half * 32, pw);
                         }
                         float s0, s1, s2, s3;
                         up2(l2[0], s0, s1);
                         up2(l2[1], s2, s3);
                         sum = (s0 + s1) + (s2 + s3);
                     };
-                    bool redo = j == j0;
+                    bool redo = j == 0;
                     if (!redo) {
                         exp_pass(-m_run);
                         redo = __any_sync(0xffffffffu, mine && !(sum <= kSumTrigger));
+                        if (redo) tmem_wait_st();          // before P is stored again
                     }
                     if (redo) {
-                        float mx = -INFINITY;
+                        float part[8];
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
-                            float sv[32];
-                            tmem_ld32(s_col + cc * 32, sv);
-                            tmem_wait_ld();
-                            if (!whole) {
+                        for (int e = 0; e < 8; ++e) part[e] = fmaxf(sv[e], sv[8 + e]);
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    sv[e] = (mask[cc] >> e) & 1 ? sv[e] : -INFINITY;
-                            }
-                            float part[4];
+                        for (int c = 16; c < kKeys; c += 16)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) part[e] = fmaxf(sv[e], sv[4 + e]);
-#pragma unroll
-                            for (int c = 8; c < 32; c += 8)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    part[e] = max3(part[e], sv[c + e], sv[c + 4 + e]);
-                            mx = max3(mx, fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-                        }
+                            for (int e = 0; e < 8; ++e)
+                                part[e] = max3(part[e], sv[c + e], sv[c + 8 + e]);
+                        float mx = fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
+                                         fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
                         mx *= a.scale_log2;                // scale > 0 keeps the order
                         const bool raise = mine && mx > m_run + kRescaleThreshold;
                         float alpha = 1.f;
@@ -925,66 +914,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                             m_run = mx;
                             l_run *= alpha;
                         }
-                        // this S was computed behind the group's last P V: O is at rest
-                        if (j > j0 && __any_sync(0xffffffffu, raise)) {
+                        if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                            // O may only be rescaled once the last P V has finished
+                            const uint32_t tp = t - 1;
+                            if (!(ok = warp_wait(&s.pv_done[tp % kStages], (tp / kStages) & 1,
+                                                 &s.abort_flag, polls)))
+                                break;
+                            tc_fence_after();
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc) {
                                 float ov[32];
-                                tmem_ld32(o_col + cc * 32, ov);
+                                tmem_ld32(lanes + kColO + cc * 32, ov);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                                tmem_st32(o_col + cc * 32, ov);
+                                tmem_st32(lanes + kColO + cc * 32, ov);
                             }
                         }
                         exp_pass(m_run == -INFINITY ? 0.f : -m_run);
                     }
                     l_run += sum;
-                    // P over the first 64 columns of S
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float pf[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) pf[e] = __uint_as_float(pw[half * 32 + e]);
-                        tmem_st32(s_col + half * 32, pf);
-                    }
                     tmem_wait_st();
                 }
-                if (!whole && (!pair || g == 0)) {
-                    // V rows of keys that do not count may hold anything: thread i clears
-                    // row i (both groups of a pair use the same tile, the first clears it)
-                    const uint32_t fill = 2 * t + 1, slot = fill % kSlots;
-                    if (!(ok = warp_wait(&s.kv_full[slot], (fill / kSlots) & 1, &s.abort_flag,
-                                         polls)))
+                if (!whole) {
+                    // V rows of keys that do not count may hold anything: thread i clears row i
+                    if (!(ok = warp_wait(&s.v_full[st], (t / kStages) & 1, &s.abort_flag, polls)))
                         break;
-                    if (!((mask[warp & 3] >> lane) & 1)) {
+                    if (!((mask[warp] >> lane) & 1)) {
 #pragma unroll
                         for (int hf = 0; hf < kBlocks; ++hf)
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
-                                *reinterpret_cast<uint4*>(s.kv[slot] + hf * kHalf + i * 128 +
-                                                          c * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(s.v[st] + hf * kHalf + i * 128 + c * 16) =
+                                    make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full[g]);
+                if (lane == 0) mbar_arrive(&s.p_full[st]);
             }
             if (!ok) break;
-            tile_no += x.tiles;
-            // ---- this group's part, or the result where there is no other
-            if (!(ok = warp_wait(&s.pv_done[g], (n - 1) & 1, &s.abort_flag, polls))) break;
+            // ---- this item's part, or the result where there is no other
+            T += x.tiles;
+            if (!(ok = warp_wait(&s.pv_done[(T - 1) % kStages], ((T - 1) / kStages) & 1,
+                                 &s.abort_flag, polls)))
+                break;
             tc_fence_after();
             if (active) {
-                const int32_t b = x.b0 + (pair && g == 1 ? a.tile_seqs : 0) + my_seq;
+                const int32_t b = x.b0 + my_seq;
                 int32_t first = 0, parts = 0;
                 if (mine) {
                     first = a.part_prefix[b];
                     parts = a.part_prefix[b + 1] - first;  // 0: a sequence without keys
                 }
                 const int64_t row = x.kvh * a.G + head;
-                const int64_t at = ((int64_t)first + x.part + j0) * a.Hq + row;
+                const int64_t at = ((int64_t)first + x.part) * a.Hq + row;
                 const bool some = l_run > 0.f || l_run != l_run;
                 const float inv = some ? 1.f / l_run : 0.f;
                 const bool wide = ((uintptr_t)a.out & 31) == 0;
@@ -992,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
                     float ov[32];
-                    tmem_ld32(o_col + cc * 32, ov);
+                    tmem_ld32(lanes + kColO + cc * 32, ov);
                     tmem_wait_ld();
                     if (parts > 1) {
 #pragma unroll
@@ -1025,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.o_free[g]);
+            if (lane == 0) mbar_arrive(&s.o_free);
         }
         if (!ok && lane == 0) give_up(s, a.status);
     }
@@ -1033,25 +1018,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (s.abort_flag && warp == 8 && lane == 0) {
-        // some role gave up: every copy issued lands before the CTA exits
-        for (uint32_t back = 1; back <= (uint32_t)kSlots && back <= fills; ++back) {
+    if (s.abort_flag && lane == 0 && (warp == 4 || warp == 7)) {
+        // some role gave up: every copy this producer issued lands before the CTA exits
+        for (uint32_t back = 1; back <= (uint32_t)kStages && back <= fills; ++back) {
             const uint32_t f = fills - back;
-            mbar_drain(&s.kv_full[f % kSlots], (f / kSlots) & 1);
+            mbar_drain(warp == 4 ? &s.k_full[f % kStages] : &s.v_full[f % kStages],
+                       (f / kStages) & 1);
         }
-        for (uint32_t back = 1; back <= 2 && back <= q_fills; ++back) {
-            const uint32_t f = q_fills - back;
-            mbar_drain(&s.q_full[f & 1], (f / 2) & 1);
-        }
+        if (q_fills > 0) mbar_drain(&s.q_full, (q_fills - 1) & 1);
     }
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 5) tmem_dealloc(tmem, 512);
 }
 
 // ----------------------------------------------------------------------- host
 struct Layout {
     int32_t box, edge_box, tile_keys, tile_heads, head_tiles, tile_seqs;
     int32_t cap_records, cap_parts, common_budget;
-    size_t off_prefix, off_group, off_table, off_records, off_ml, off_o, total;
+    size_t off_prefix, off_sequences, off_table, off_records, off_ml, off_o, total;
 };
 
 // Rows of a TMA box: a run of a cache block (a multiple of 8 rows, what the swizzle
@@ -1083,23 +1066,23 @@ bool layout(int32_t batch, int32_t num_q_heads, int32_t max_ctx, const pkv_cache
     L.tile_heads = G < kRows ? G : kRows;
     L.head_tiles = ceil_div(G, L.tile_heads);
     L.tile_seqs = kRows / L.tile_heads;
-    // Parts.  A run of tiles has two at most.  Own runs are long enough for 16 kSms items in
-    // all, and one more for each sequence; common runs, so long that their items could be
-    // 4 kSms of 2 tile_seqs sequences each, and one more for each sequence.  Neither is more
-    // than the tiles there can be.
+    // Parts, one of a run for each of its sequences.  Own runs are long enough for 16 kSms
+    // items in all, and one more for each sequence; common runs, so long that their items
+    // could be 8 kSms of tile_seqs sequences each, and one more for each sequence.  Neither
+    // is more than the tiles there can be.
     const int64_t units = (int64_t)c.num_kv_heads * L.head_tiles;
     const int64_t tiles = (int64_t)batch * (ceil_div(max_ctx, L.tile_keys) + 1);
     const int64_t own = (16 * kSms + units - 1) / units;
-    const int64_t common = (2 * (int64_t)L.tile_seqs * 4 * kSms + units - 1) / units;
+    const int64_t common = ((int64_t)L.tile_seqs * 8 * kSms + units - 1) / units;
     L.common_budget = (int32_t)(common < tiles ? common : tiles);
     if (L.common_budget < 1) L.common_budget = 1;
-    const int64_t parts = 2 * (L.common_budget + (own < tiles ? own : tiles) + 2 * (int64_t)batch + 2);
+    const int64_t parts = L.common_budget + (own < tiles ? own : tiles) + 2 * (int64_t)batch + 2;
     if (parts > (1 << 30) || parts * units > (1LL << 31)) return false;
     L.cap_parts = L.cap_records = (int32_t)parts;
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
     L.off_prefix = 256;
-    L.off_group = align(L.off_prefix + sizeof(int32_t) * ((size_t)batch + 1));
-    L.off_table = align(L.off_group + sizeof(int32_t) * (size_t)batch);
+    L.off_sequences = align(L.off_prefix + sizeof(int32_t) * ((size_t)batch + 1));
+    L.off_table = align(L.off_sequences + sizeof(int2) * (size_t)batch);
     L.off_records = align(L.off_table + sizeof(int32_t) * (size_t)batch);
     L.off_ml = align(L.off_records + sizeof(Record) * (size_t)L.cap_records);
     L.off_o = align(L.off_ml + sizeof(float2) * (size_t)L.cap_parts * num_q_heads);
@@ -1128,7 +1111,7 @@ int make_plan(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
     a = SharedArgs{};
     a.ctrl = (int32_t*)ws;
     a.part_prefix = (int32_t*)(ws + L.off_prefix);
-    a.group = (int32_t*)(ws + L.off_group);
+    a.sequences = (int2*)(ws + L.off_sequences);
     a.table = (int32_t*)(ws + L.off_table);
     a.records = (Record*)(ws + L.off_records);
     a.part_ml = (float2*)(ws + L.off_ml);
