@@ -275,10 +275,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedArgs a) {
     if (tid < 32) {
         const float common_tiles = (float)sum[0], members = (float)sum[1];
         const int64_t own_tiles = (int64_t)sum[2];
-        // own runs: eight items an SM up to four tiles each, then up to sixteen items
+        // own runs: an item's start and end cost as much as three tiles, so two items an SM up
+        // to six tiles each, then up to sixteen items
         const int64_t work = own_tiles * units;
-        int64_t own = (work + 8 * kSms - 1) / (8 * kSms);
-        own = own < 4 ? own : 4;
+        int64_t own = (work + 2 * kSms - 1) / (2 * kSms);
+        own = own < 6 ? own : 6;
         const int64_t sixteen = (work + 16 * kSms - 1) / (16 * kSms);
         own = own > sixteen ? own : sixteen;
         if (own < 1) own = 1;
@@ -399,15 +400,17 @@ struct __align__(1024) Smem {
     unsigned char q[kTile];
     unsigned char k[kStages][kTile];
     unsigned char v[kStages][kTile];
-    uint64_t q_full, q_free;
+    uint64_t q_full[2], q_free[2];
     uint64_t k_full[kStages], v_full[kStages], k_empty[kStages], v_empty[kStages];
     uint64_t s_full[kStages], p_full[kStages], pv_done[kStages];
     uint64_t o_free, mma_done;
     uint64_t item_full[kItemRing], item_empty[kItemRing];
-    uint64_t mask_full[kMaskRing];
     uint4 mask[kMaskRing];                                 // keys of a tile that count
+    uint32_t masked_from;                                  // the first tile with a mask
     struct Item {
-        int32_t b0, seqs, table, key_lo, key_hi, origin, tiles, kvh, head_tile, part, end;
+        int32_t b0, seqs, table, key_lo, key_hi, origin, tiles, kvh, head_tile, part;
+        int32_t q_slot;                                    // half of the Q tile, 2: all of it
+        int32_t end;
     } items[kItemRing];
     uint32_t tmem_base;
     int abort_flag;
@@ -572,8 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         s.abort_flag = 0;
-        mbar_init(&s.q_full, 1);
-        mbar_init(&s.q_free, 1);
+        s.masked_from = ~0u;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_free[i], 1);
+        }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&s.k_full[i], 1);
             mbar_init(&s.v_full[i], 1);
@@ -588,7 +594,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s.item_full[i], 1);
             mbar_init(&s.item_empty[i], kItemReaders);
         }
-        for (int i = 0; i < kMaskRing; ++i) mbar_init(&s.mask_full[i], 1);
         mbar_init(&s.mma_done, 2);
         mbar_init_fence();
     }
@@ -601,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     pkv::allow_dependent_launch();           // the combine reads the plan's parts at once
     const uint32_t units = (uint32_t)(a.Hkv * a.head_tiles);
     const uint32_t n_items = (uint32_t)a.ctrl[0] * units;
-    uint32_t fills = 0, q_fills = 0;         // a producer's tiles, and Q tiles
+    uint32_t fills = 0;                      // a producer's tiles
+    uint32_t q_uses[2] = {0, 0};             // of the halves of the Q tile
 
     // Item I from the ring; false: none in time.
     auto next_item = [&](uint32_t I, Item& x, bool warp_wide) {
@@ -638,7 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto draw = [&]() {
             return k_side && lane == 0 ? atomicInc((unsigned int*)a.ctrl + 1, wrap) : 0u;
         };
-        bool ok = true, bad_block = false;
+        bool ok = true, bad_block = false, masked = false;
+        int q_next = 0;
         int pend = -1;                       // a gathered stage in flight
         auto land = [&](int st) {
             fence_proxy_async_smem();
@@ -676,6 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x.kvh = unit / a.head_tiles;
                 x.head_tile = unit - x.kvh * a.head_tiles;
                 x.end = 0;
+                // the queries of one sequence take half of the Q tile, so that the next
+                // item's can be loaded meanwhile
+                const bool small = x.seqs == 1 && a.tile_heads <= kRows / 2;
+                x.q_slot = small ? q_next : 2;
+                if (x.tiles > 0 && small) q_next ^= 1;
                 if (lane == 0) {
                     s.items[ring] = x;
                     mbar_arrive(&s.item_full[ring]);
@@ -685,19 +697,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int32_t* table = a.bt + (int64_t)x.table * a.MB;
             if (k_side && x.tiles > 0) {
-                if (q_fills > 0 &&
-                    !(ok = warp_wait(&s.q_free, (q_fills - 1) & 1, &s.abort_flag, polls)))
-                    break;
+                for (int h = 0; h < 2 && ok; ++h)
+                    if ((x.q_slot == h || x.q_slot == 2) && q_uses[h] > 0)
+                        ok = warp_wait(&s.q_free[h], (q_uses[h] - 1) & 1, &s.abort_flag, polls);
+                if (!ok) break;
+                const int first = x.q_slot == 1 ? 1 : 0;
                 if (lane == 0) {
                     const CUtensorMap* m = x.seqs == 1 ? &maps.q_one : &maps.q;
-                    mbar_expect_tx(&s.q_full,
+                    mbar_expect_tx(&s.q_full[first],
                                    (uint32_t)(kBlocks * 128 * a.tile_heads *
                                               (x.seqs == 1 ? 1 : a.tile_seqs)));
                     for (int hf = 0; hf < kBlocks; ++hf)
-                        tma_load_4d(s.q + hf * kHalf, m, &s.q_full, hf * 64,
-                                    x.head_tile * a.tile_heads, x.kvh, x.b0);
+                        tma_load_4d(s.q + hf * kHalf + first * (kHalf / 2), m, &s.q_full[first],
+                                    hf * 64, x.head_tile * a.tile_heads, x.kvh, x.b0);
+                    if (x.q_slot == 2) mbar_arrive(&s.q_full[1]);
                 }
-                ++q_fills;
+                ++q_uses[first];
+                if (x.q_slot == 2) ++q_uses[1];
             }
             for (int32_t j = 0; j < x.tiles; ++j, ++fills) {
                 const int st = fills % kStages;
@@ -707,10 +723,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (fills >= kStages &&
                     !(ok = warp_wait(&empty[st], (fills / kStages - 1) & 1, &s.abort_flag, polls)))
                     break;
-                if (k_side && lane == 0) {
-                    s.mask[fills % kMaskRing] =
-                        make_uint4(src.valid[0], src.valid[1], src.valid[2], src.valid[3]);
-                    mbar_arrive(&s.mask_full[fills % kMaskRing]);
+                if (k_side) {
+                    // from the first tile with a bad block on, every tile gets its mask
+                    const bool first = !masked && __any_sync(0xffffffffu, src.bad);
+                    masked |= first;
+                    if (masked && lane == 0) {
+                        s.mask[fills % kMaskRing] =
+                            make_uint4(src.valid[0], src.valid[1], src.valid[2], src.valid[3]);
+                        if (first) *(volatile uint32_t*)&s.masked_from = fills;
+                    }
                 }
                 unsigned char* dst = k_side ? s.k[st] : s.v[st];
                 if constexpr (kGather) {
@@ -767,7 +788,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = next_item(I, x, false)) || x.end) break;
                 if (x.tiles == 0) continue;
                 if (warp == 5) {
-                    if (!(ok = mbar_wait(&s.q_full, uses & 1, &s.abort_flag, polls))) break;
+                    for (int h = 0; h < 2 && ok; ++h)
+                        if (x.q_slot == h || x.q_slot == 2)
+                            ok = mbar_wait(&s.q_full[h], q_uses[h]++ & 1, &s.abort_flag, polls);
+                    if (!ok) break;
+                    const uint64_t qd = qd0 + (x.q_slot == 1 ? kHalf / 2 >> 4 : 0);
                     for (int32_t j = 0; j < x.tiles; ++j) {
                         const uint32_t t = T + j;
                         const int st = t % kStages;
@@ -785,13 +810,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                            umma_bf16(d_s, qd0 + off, kd + off, id_qk, kk > 0);
+                            umma_bf16(d_s, qd + off, kd + off, id_qk, kk > 0);
                         }
                         umma_commit(&s.s_full[st]);
                         umma_commit(&s.k_empty[st]);
                     }
                     if (!ok) break;
-                    umma_commit(&s.q_free);
+                    for (int h = 0; h < 2; ++h)
+                        if (x.q_slot == h || x.q_slot == 2) umma_commit(&s.q_free[h]);
                 } else {
                     for (int32_t j = 0; j < x.tiles; ++j) {
                         const uint32_t t = T + j;
@@ -840,6 +866,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t head = x.head_tile * a.tile_heads + my_head;
             const bool mine = my_seq < x.seqs && head < a.G;
             const bool active = warp * 32 < x.seqs * a.tile_heads;
+            // asked for ahead of its use behind the tiles
+            const int32_t b = x.b0 + my_seq;
+            const int32_t first = mine ? a.part_prefix[b] : 0;
+            const int32_t parts = mine ? a.part_prefix[b + 1] - first : 0;  // 0: without keys
             float m_run = -INFINITY, l_run = 0.f;
             for (int32_t j = 0; j < x.tiles && ok; ++j) {
                 const uint32_t t = T + j;
@@ -847,13 +877,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t s_col = lanes + st * kKeys;
                 if (!(ok = warp_wait(&s.s_full[st], (t / kStages) & 1, &s.abort_flag, polls)))
                     break;
-                if (!(ok = warp_wait(&s.mask_full[t % kMaskRing], (t / kMaskRing) & 1,
-                                     &s.abort_flag, polls)))
-                    break;
                 tc_fence_after();
-                const uint4 mk = s.mask[t % kMaskRing];
-                const uint32_t mask[4] = {mk.x, mk.y, mk.z, mk.w};
-                const bool whole = (mk.x & mk.y & mk.z & mk.w) == ~0u;
+                // Tiles with a bad block are rare: their masks come through shared memory,
+                // the others' follow from the run.  (The producer wrote them before it
+                // filled the tile's K stage, which Q K^T waited for.)
+                const int32_t key0 = x.origin + j * a.tile_keys;
+                const int32_t lo = max(x.key_lo - key0, 0);
+                const int32_t hi = min(x.key_hi - key0, a.tile_keys);
+                const bool marked = t >= *(volatile uint32_t*)&s.masked_from;
+                const bool whole = !marked && lo == 0 && hi == kKeys;
+                uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
+                if (!whole) {
+                    const uint4 mk = s.mask[t % kMaskRing];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        mask[w] = marked ? pkv::word(mk, w) : range_word(lo, hi, w);
+                }
                 if (active) {
                     float sv[kKeys];
 #pragma unroll
@@ -962,12 +1001,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             tc_fence_after();
             if (active) {
-                const int32_t b = x.b0 + my_seq;
-                int32_t first = 0, parts = 0;
-                if (mine) {
-                    first = a.part_prefix[b];
-                    parts = a.part_prefix[b + 1] - first;  // 0: a sequence without keys
-                }
                 const int64_t row = x.kvh * a.G + head;
                 const int64_t at = ((int64_t)first + x.part) * a.Hq + row;
                 const bool some = l_run > 0.f || l_run != l_run;
@@ -1025,7 +1058,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_drain(warp == 4 ? &s.k_full[f % kStages] : &s.v_full[f % kStages],
                        (f / kStages) & 1);
         }
-        if (q_fills > 0) mbar_drain(&s.q_full, (q_fills - 1) & 1);
+        if (warp == 4)
+            for (int h = 0; h < 2; ++h)
+                if (q_uses[h] > 0) mbar_drain(&s.q_full[h], (q_uses[h] - 1) & 1);
     }
     if (warp == 5) tmem_dealloc(tmem, 512);
 }
