@@ -653,6 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&full[st]);
         };
         uint32_t next = draw(), it = __shfl_sync(0xffffffffu, next, 0);
+        int4 r0 = make_int4(0, 0, 0, 0);     // the record of item `it`
+        int2 r1 = make_int2(0, 0);
+        auto fetch = [&]() {
+            if (it < n_items) {
+                const Record* r = a.records + it / units;
+                r0 = *reinterpret_cast<const int4*>(r);
+                r1 = *reinterpret_cast<const int2*>(&r->key_hi);
+            }
+        };
+        if (k_side) fetch();
         for (uint32_t I = 0; ok; ++I) {
             Item x;
             if (k_side) {
@@ -668,10 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     break;
                 }
-                next = draw();               // needed only behind this item's loads
-                const uint32_t rec = it / units, unit = it - rec * units;
-                const int4 r0 = *reinterpret_cast<const int4*>(a.records + rec);
-                const int2 r1 = *reinterpret_cast<const int2*>(&a.records[rec].key_hi);
+                next = draw();               // needed only at this item's last tile
+                const uint32_t unit = it - it / units * units;
                 x.b0 = r0.x;
                 x.seqs = r0.y;
                 x.table = r0.z;
@@ -720,6 +728,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Source src = find_tile<D, kGather>(
                     a, table, x.key_lo, x.key_hi, x.origin + j * a.tile_keys, x.kvh, lane);
                 bad_block |= src.bad;
+                if (k_side && j == x.tiles - 1) {            // the next item's record
+                    it = __shfl_sync(0xffffffffu, next, 0);
+                    fetch();
+                }
                 if (fills >= kStages &&
                     !(ok = warp_wait(&empty[st], (fills / kStages - 1) & 1, &s.abort_flag, polls)))
                     break;
@@ -760,9 +772,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            it = __shfl_sync(0xffffffffu, next, 0);
+            if (k_side && x.tiles == 0) {
+                it = __shfl_sync(0xffffffffu, next, 0);
+                fetch();
+            }
+            // the next item's queries may wait for this item's last Q K^T, which waits for
+            // its last K tile
+            if (pend >= 0) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                land(pend);
+                pend = -1;
+            }
         }
-        if (pend >= 0) {
+        if (pend >= 0) {                     // on the way out of a wait that gave up
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             land(pend);
         }
@@ -928,50 +950,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                         up2(l2[1], s2, s3);
                         sum = (s0 + s1) + (s2 + s3);
                     };
-                    bool redo = j == 0;
-                    if (!redo) {
-                        exp_pass(-m_run);
-                        redo = __any_sync(0xffffffffu, mine && !(sum <= kSumTrigger));
-                        if (redo) tmem_wait_st();          // before P is stored again
-                    }
-                    if (redo) {
-                        float part[8];
+                    // One pass where P stands against the running maximum; else a second,
+                    // with the maximum taken first (as for an item's first tile).
+                    bool take = j == 0, again;
+                    do {
+                        if (take) {
+                            float part[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) part[e] = fmaxf(sv[e], sv[8 + e]);
+                            for (int e = 0; e < 8; ++e) part[e] = fmaxf(sv[e], sv[8 + e]);
 #pragma unroll
-                        for (int c = 16; c < kKeys; c += 16)
+                            for (int c = 16; c < kKeys; c += 16)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                part[e] = max3(part[e], sv[c + e], sv[c + 8 + e]);
-                        float mx = fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
-                                         fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
-                        mx *= a.scale_log2;                // scale > 0 keeps the order
-                        const bool raise = mine && mx > m_run + kRescaleThreshold;
-                        float alpha = 1.f;
-                        if (raise) {
-                            alpha = m_run == -INFINITY ? 0.f : pkv::fast_exp2(m_run - mx);
-                            m_run = mx;
-                            l_run *= alpha;
-                        }
-                        if (j > 0 && __any_sync(0xffffffffu, raise)) {
-                            // O may only be rescaled once the last P V has finished
-                            const uint32_t tp = t - 1;
-                            if (!(ok = warp_wait(&s.pv_done[tp % kStages], (tp / kStages) & 1,
-                                                 &s.abort_flag, polls)))
-                                break;
-                            tc_fence_after();
+                                for (int e = 0; e < 8; ++e)
+                                    part[e] = max3(part[e], sv[c + e], sv[c + 8 + e]);
+                            float mx =
+                                fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
+                                      fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
+                            mx *= a.scale_log2;            // scale > 0 keeps the order
+                            const bool raise = mine && mx > m_run + kRescaleThreshold;
+                            float alpha = 1.f;
+                            if (raise) {
+                                alpha = m_run == -INFINITY ? 0.f : pkv::fast_exp2(m_run - mx);
+                                m_run = mx;
+                                l_run *= alpha;
+                            }
+                            if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                                // O may only be rescaled once the last P V has finished
+                                const uint32_t tp = t - 1;
+                                if (!(ok = warp_wait(&s.pv_done[tp % kStages], (tp / kStages) & 1,
+                                                     &s.abort_flag, polls)))
+                                    break;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int cc = 0; cc < D / 32; ++cc) {
+                                    float ov[32];
+                                    tmem_ld32(lanes + kColO + cc * 32, ov);
+                                    tmem_wait_ld();
 #pragma unroll
-                            for (int cc = 0; cc < D / 32; ++cc) {
-                                float ov[32];
-                                tmem_ld32(lanes + kColO + cc * 32, ov);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                                tmem_st32(lanes + kColO + cc * 32, ov);
+                                    for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                                    tmem_st32(lanes + kColO + cc * 32, ov);
+                                }
                             }
                         }
-                        exp_pass(m_run == -INFINITY ? 0.f : -m_run);
-                    }
+                        // (without a maximum yet, the sum is infinite or NaN the first time)
+                        exp_pass(take && m_run == -INFINITY ? 0.f : -m_run);
+                        again = !take && __any_sync(0xffffffffu, mine && !(sum <= kSumTrigger));
+                        take = again;
+                        if (again) tmem_wait_st();         // before P is stored again
+                    } while (again);
+                    if (!ok) break;
                     l_run += sum;
                     tmem_wait_st();
                 }
@@ -1007,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv = some ? 1.f / l_run : 0.f;
                 const bool wide = ((uintptr_t)a.out & 31) == 0;
                 __nv_bfloat16* out = a.out + ((int64_t)b * a.Hq + row) * D;
-#pragma unroll
+#pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     float ov[32];
                     tmem_ld32(lanes + kColO + cc * 32, ov);

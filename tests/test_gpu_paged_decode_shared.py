@@ -102,6 +102,10 @@ CASES = [  # sizes, prefixes, suffixes (or a bound for random ones), hq, hkv, d,
     ([2, 3], [200, 300], 50, 160, 1, 64, 16),           # more than 128 heads a kv head
     ([4], [136], 40, 3, 3, 128, 136),
     ([30] + [1] * 8 + [12], [1280] + [50] * 8 + [640], 400, 32, 8, 128, 16),
+    # several items a CTA, whole row tiles and single sequences in turn
+    ([24] * 4, [300, 200, 700, 65], 150, 16, 8, 64, 20),
+    ([30] * 2, [300, 500], 100, 16, 8, 128, 12),
+    ([24] * 4, [300, 200, 700, 65], 150, 16, 8, 64, 16),
 ]
 
 
