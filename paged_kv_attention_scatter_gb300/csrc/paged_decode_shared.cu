@@ -678,7 +678,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     break;
                 }
-                next = draw();               // needed only at this item's last tile
                 const uint32_t unit = it - it / units * units;
                 x.b0 = r0.x;
                 x.seqs = r0.y;
@@ -691,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x.kvh = unit / a.head_tiles;
                 x.head_tile = unit - x.kvh * a.head_tiles;
                 x.end = 0;
+                if (x.tiles == 0) next = draw();
                 // the queries of one sequence take half of the Q tile, so that the next
                 // item's can be loaded meanwhile
                 const bool small = x.seqs == 1 && a.tile_heads <= kRows / 2;
@@ -728,7 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Source src = find_tile<D, kGather>(
                     a, table, x.key_lo, x.key_hi, x.origin + j * a.tile_keys, x.kvh, lane);
                 bad_block |= src.bad;
-                if (k_side && j == x.tiles - 1) {            // the next item's record
+                // the next item, and then its record, late: one that is held is kept from others
+                if (k_side && j == max(x.tiles - 2, 0)) next = draw();
+                if (k_side && j == x.tiles - 1) {
                     it = __shfl_sync(0xffffffffu, next, 0);
                     fetch();
                 }
