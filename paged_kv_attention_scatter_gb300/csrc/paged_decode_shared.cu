@@ -100,7 +100,7 @@ __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) {
 }
 
 // ---------------------------------------------------------------------- plan
-constexpr int kPlanThreads = 1024;
+constexpr int kMaxPlanThreads = 1024;
 constexpr int kStaged = 1024;            // groups held in shared memory
 // Fewer common keys than this are attended by each sequence itself.
 constexpr int kMinShared = 64;
@@ -137,6 +137,7 @@ struct Groups {
     // the group of sequence b among the first n, -1: none
     __device__ __forceinline__ int32_t of(int32_t b, int32_t n) const {
         int32_t lo = 0, hi = n;              // groups that begin at b or before
+#pragma unroll 1
         while (lo < hi) {
             const int32_t mid = (lo + hi) / 2;
             if (offsets[mid] <= b) lo = mid + 1;
@@ -166,7 +167,7 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t& carry, int64
     __syncthreads();
     if (lane == 31) scratch[w] = x;
     __syncthreads();
-    int64_t s = scratch[lane];
+    int64_t s = lane < (int)(blockDim.x >> 5) ? scratch[lane] : 0;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int64_t y = __shfl_up_sync(~0u, s, off);
@@ -179,81 +180,104 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t& carry, int64
     return r;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedArgs a) {
+// One CTA of a thread a sequence, within 256 and kMaxPlanThreads (for small batches more threads
+// cost time: 64 sequences 6.4 us with 256, 8.2 with 1024).  What a thread finds out of its first
+// sequence stays in registers; larger batches go over theirs again.  Loops are not unrolled: a
+// kernel that runs once pays for fetching its instructions (86 KB of them: 16 us).
+__global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
     pkv::allow_dependent_launch();
     __shared__ int64_t scratch[32];
-    // common tiles of row tiles, of sequences; own tiles; row tiles; sequences with own keys;
-    // common records, own records
-    __shared__ unsigned long long sum[7];
+    // common tiles of row tiles, of sequences; own tiles; row tiles; sequences with own keys
+    __shared__ unsigned long long sum[5];
     __shared__ int32_t run_len[2];           // key tiles of a common run, of an own run
-    __shared__ int32_t staged_offsets[kStaged + 1], staged_prefix[kStaged];
-    const int tid = threadIdx.x, lane = tid & 31;
+    __shared__ int32_t staged_offsets[kStaged + 1], staged_prefix[kStaged], staged_table[kStaged];
+    const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
     const int32_t units = a.Hkv * a.head_tiles;
+    const int32_t my_ctx = tid < a.B ? a.ctx[tid] : 0;
 
     // ---- groups: increasing offsets within the batch, or none is used
     const bool staged = a.groups <= kStaged;
-    if (tid < 7) sum[tid] = 0;
-    if (staged && a.groups > 0) {
-        for (int32_t g = tid; g <= a.groups; g += kPlanThreads) staged_offsets[g] = a.offsets[g];
-        for (int32_t g = tid; g < a.groups; g += kPlanThreads) staged_prefix[g] = a.prefix[g];
-    }
+    if (tid < 5) sum[tid] = 0;
+    if (staged && a.groups > 0)
+#pragma unroll 1
+        for (int32_t g = tid; g <= a.groups; g += threads) {
+            staged_offsets[g] = a.offsets[g];
+            if (g < a.groups) {
+                staged_prefix[g] = a.prefix[g];
+                staged_table[g] = INT32_MAX;
+            }
+        }
     __syncthreads();
     const Groups of{a, staged ? staged_offsets : a.offsets, staged ? staged_prefix : a.prefix};
+    int32_t* table = staged ? staged_table : a.table;      // by group, or its first sequence
     bool bad = false;
     if (a.groups > 0)
-        for (int32_t g = tid; g <= a.groups; g += kPlanThreads) {
+#pragma unroll 1
+        for (int32_t g = tid; g <= a.groups; g += threads) {
             const int32_t o = of.offsets[g];
             bad |= o < 0 || o > a.B || (g > 0 && o < of.offsets[g - 1]);
         }
     const int32_t groups = __syncthreads_or(bad) ? 0 : a.groups;
     if (groups != a.groups && tid == 0) pkv::report(a.status, PKV_STATUS_BAD_SEQLENS);
 
+    // this thread's group of a round: neighbours go to different warps
+    const int my_group = lane * (threads / 32) + (tid >> 5);
     // ---- how much there is
     auto add = [&](int which, int32_t v) {   // a warp's values into sum[which]
         v = __reduce_add_sync(~0u, v);
         if (lane == 0 && v != 0) atomicAdd(&sum[which], (unsigned long long)v);
     };
-    for (int32_t base = 0; base < groups; base += kPlanThreads) {
-        const int32_t g = base + tid;
+#pragma unroll 1
+    for (int32_t base = 0; base < groups; base += threads) {
+        const int32_t g = base + my_group;
         Group x{};
         if (g < groups) x = of.at(g, true);
-        int32_t tiles = 0, n = 0;
+        int32_t tiles = 0;
+        int64_t t0 = 0, t1 = 0;              // these may pass 32 bits when added up
         if (x.keys > 0) {
             tiles = ceil_div(x.seqs, a.tile_seqs);
-            n = key_tiles(a, 0, x.keys);
-            a.table[x.first] = INT32_MAX;
-            // these may pass 32 bits when added up
-            atomicAdd(&sum[0], (unsigned long long)tiles * n);
-            atomicAdd(&sum[1], (unsigned long long)x.seqs * n);
+            const int32_t n = key_tiles(a, 0, x.keys);
+            if (!staged) a.table[x.first] = INT32_MAX;
+            t0 = (int64_t)tiles * n;
+            t1 = (int64_t)x.seqs * n;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            t0 += __shfl_xor_sync(~0u, t0, off);
+            t1 += __shfl_xor_sync(~0u, t1, off);
+        }
+        if (lane == 0 && t0 != 0) {
+            atomicAdd(&sum[0], (unsigned long long)t0);
+            atomicAdd(&sum[1], (unsigned long long)t1);
         }
         add(3, tiles);
     }
-    __syncthreads();
+    if (!staged) __syncthreads();
     Sequence mine{};                         // of sequence tid; the others' are noted
-    auto sequence_at = [&](int32_t b) {
-        Sequence s{0, 0};
-        const int32_t c = a.ctx[b];
-        if (c < 0 || c > (int64_t)a.MB * a.bs || c > a.max_ctx) {
-            pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
-            return s;
-        }
-        const int32_t g = c > 0 ? of.of(b, groups) : -1;
-        if (g >= 0) {
-            const Group x = of.at(g, false);
-            if (x.prefix > c) {              // a member without all of its group's keys
-                pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
-                return s;
-            }
-            s.prefix = x.keys;
-            if (x.keys > 0) atomicMin(&a.table[x.first], b);
-        }
-        s.ctx = c;
-        return s;
-    };
-    for (int32_t base = 0; base < a.B; base += kPlanThreads) {
+#pragma unroll 1
+    for (int32_t base = 0; base < a.B; base += threads) {
         const int32_t b = base + tid;
-        Sequence s{};
-        if (b < a.B) s = sequence_at(b);
+        Sequence s{0, 0};
+        if (b < a.B) {
+            const int32_t c = base == 0 ? my_ctx : a.ctx[b];
+            bool use = c > 0;
+            if (c < 0 || c > (int64_t)a.MB * a.bs || c > a.max_ctx) {
+                pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
+                use = false;
+            }
+            const int32_t g = use ? of.of(b, groups) : -1;
+            if (g >= 0) {
+                const Group x = of.at(g, false);
+                if (x.prefix > c) {          // a member without all of its group's keys
+                    pkv::report(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
+                    use = false;
+                } else if (x.keys > 0) {
+                    s.prefix = x.keys;
+                    atomicMin(&table[staged ? g : x.first], b);
+                }
+            }
+            if (use) s.ctx = c;
+        }
         if (base == 0) mine = s;
         else if (b < a.B) a.sequences[b] = make_int2(s.ctx, s.prefix);
         const int32_t own = key_tiles(a, s.prefix, s.ctx);
@@ -263,7 +287,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedArgs a) {
     auto noted = [&](int32_t b) {
         Sequence s = mine;
         if (b >= a.B) s = Sequence{};
-        else if (b >= kPlanThreads) {
+        else if (b >= threads) {
             const int2 n = a.sequences[b];
             s = Sequence{n.x, n.y};
         }
@@ -283,8 +307,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedArgs a) {
         const int64_t sixteen = (work + 16 * kSms - 1) / (16 * kSms);
         own = own > sixteen ? own : sixteen;
         if (own < 1) own = 1;
-        const float own_cost = (own_tiles * kOwnTile +
-                                ((float)own_tiles / own + (float)sum[4]) * kItemCost) * units;
+        const float own_cost = ((float)own_tiles * kOwnTile +
+                                ((float)own_tiles / (float)own + (float)sum[4]) * kItemCost) *
+                               units;
         // lengths 1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, ...
         const int32_t len = lane < 4 ? lane + 1 : (4 + (lane & 3)) << ((lane >> 2) - 1);
         const float items = (common_tiles / len + (float)sum[3]) * units;
@@ -292,104 +317,140 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(SharedArgs a) {
         float cost = fmaxf(ceilf(items / kSms) * item, (items * item + own_cost) / kSms);
         // parts: written once, read once, by all rows
         cost += members / len * a.Hq * a.D * 4 / kPartBytes;
-        if ((int64_t)sum[1] / len > a.common_budget) cost = INFINITY;
+        if (members / len > (float)a.common_budget) cost = INFINITY;
         float best = cost;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             best = fminf(best, __shfl_xor_sync(~0u, best, off));
         const uint32_t who = __ballot_sync(~0u, cost == best);
-        int32_t chosen = __shfl_sync(~0u, len, __ffs(who) - 1);
-        if (best == INFINITY)                            // longer than any of these
-            chosen = (int32_t)(((int64_t)sum[1] + a.common_budget - 1) / a.common_budget);
+        int64_t chosen = __shfl_sync(~0u, len, __ffs(who) - 1);
+        // never more parts than there is room for
+        if (chosen * a.common_budget < (int64_t)sum[1])
+            chosen = ((int64_t)sum[1] + a.common_budget - 1) / a.common_budget;
         if (tid == 0) {
-            run_len[0] = chosen;
+            run_len[0] = (int32_t)chosen;
             run_len[1] = (int32_t)own;
         }
     }
     __syncthreads();
     const int32_t common = run_len[0], own = run_len[1];
 
-    // ---- how many records there are of each kind
-    for (int32_t base = 0; base < groups; base += kPlanThreads) {
-        const int32_t g = base + tid;
-        Group x{};
-        if (g < groups) x = of.at(g, false);
-        add(5, x.keys > 0 ? ceil_div(x.seqs, a.tile_seqs) *
+    // ---- places: each group's first record; each sequence's first part and first record
+    auto records_of = [&](const Group& x) {
+        return x.keys > 0 ? ceil_div(x.seqs, a.tile_seqs) *
                                 ceil_div(key_tiles(a, 0, x.keys), common)
-                          : 0);
-    }
-    for (int32_t base = 0; base < a.B; base += kPlanThreads) {
-        const Sequence s = noted(base + tid);
-        add(6, ceil_div(key_tiles(a, s.prefix, s.ctx), own));
-    }
-    __syncthreads();
-    const int32_t n_common = (int32_t)sum[5], n_own = (int32_t)sum[6];
-    // ---- records: the common ones spread over the first three quarters of the own ones, so
-    // that the two kinds run side by side and short items come last
-    const int32_t spread = max(1, n_own - n_own / 4);
-    auto put = [&](int64_t at, const Record& r) {
-        if (at < a.cap_records) a.records[at] = r;
+                          : 0;
     };
-    int64_t carry = 0;
-    for (int32_t base = 0; base < groups; base += kPlanThreads) {
-        const int32_t g = base + tid;
+    auto places_of = [&](const Sequence& s) {
+        const int32_t n = ceil_div(key_tiles(a, s.prefix, s.ctx), own);
+        return (int64_t)(n + ceil_div(key_tiles(a, 0, s.prefix), common)) << 32 | n;
+    };
+    int64_t common_total = 0, total = 0, my_common = 0, my_place = 0;
+    int64_t common_after = 0, after = 0;     // those of the first round
+#pragma unroll 1
+    for (int32_t base = 0; base < groups; base += threads) {
+        const int64_t at = block_prefix(
+            base + my_group < groups ? records_of(of.at(base + my_group, false)) : 0, common_total,
+            scratch);
+        if (base == 0) {
+            my_common = at;
+            common_after = common_total;
+        }
+    }
+#pragma unroll 1
+    for (int32_t base = 0; base < a.B; base += threads) {
+        const int64_t at = block_prefix(places_of(noted(base + tid)), total, scratch);
+        if (base == 0) {
+            my_place = at;
+            after = total;
+        }
+    }
+    const int32_t n_common = (int32_t)common_total, n_own = (int32_t)total;
+    const int32_t parts = (int32_t)(total >> 32);
+    // cannot be otherwise: the run lengths allow for it
+    const bool fits = common_total + n_own <= a.cap_records && parts <= a.cap_parts;
+    if (tid == 0) {
+        if (!fits) pkv::report(a.status, PKV_STATUS_WORKSPACE_OVERFLOW);
+        a.ctrl[0] = fits ? n_common + n_own : 0;
+        a.ctrl[1] = 0;
+        a.part_prefix[a.B] = fits ? parts : 0;
+    }
+    if (!fits) {
+#pragma unroll 1
+        for (int32_t b = tid; b < a.B; b += threads) a.part_prefix[b] = 0;
+        return;
+    }
+    // ---- records: each common one before `stride` own ones, over the first three quarters of
+    // those, so that the two kinds run side by side and short items come last.  Many records
+    // of one group or sequence are written by its warp together.
+    const int32_t stride = max(1, (n_own - n_own / 4) / max(1, n_common));
+#pragma unroll 1
+    for (int32_t base = 0; base < groups; base += threads) {
+        const int32_t g = base + my_group;
         Group x{};
         if (g < groups) x = of.at(g, false);
-        int32_t tiles = 0, cuts = 0;
-        if (x.keys > 0) {
-            tiles = ceil_div(x.seqs, a.tile_seqs);
-            cuts = ceil_div(key_tiles(a, 0, x.keys), common);
-        }
-        const int32_t first = (int32_t)block_prefix(tiles * cuts, carry, scratch);
-        for (int32_t i = 0; i < tiles * cuts; ++i) {
-            const int32_t cut = i / tiles, tile = i - cut * tiles;
-            Record r{};
-            r.b0 = x.first + tile * a.tile_seqs;
-            r.seqs = min(a.tile_seqs, x.first + x.seqs - r.b0);
-            r.table = a.table[x.first];
-            r.key_lo = cut * common * a.tile_keys;
-            r.key_hi = min(x.keys, (cut + 1) * common * a.tile_keys);
-            r.part = cut;
-            // no member has keys: nobody's table to read
-            if (r.table == INT32_MAX) r.key_hi = r.key_lo;
-            const int64_t at = first + i;
-            put(n_own == 0 ? at : at + at * spread / n_common, r);
+        const int32_t n = records_of(x);
+        const int64_t place = base == 0 ? my_common : block_prefix(n, common_after, scratch);
+        const int32_t from = x.keys > 0 ? table[staged ? g : x.first] : 0;
+#pragma unroll 1
+        for (uint32_t left = __ballot_sync(~0u, n > 0); left; left &= left - 1) {
+            const int o = __ffs(left) - 1;
+            const int32_t first = __shfl_sync(~0u, x.first, o), seqs = __shfl_sync(~0u, x.seqs, o);
+            const int32_t keys = __shfl_sync(~0u, x.keys, o), count = __shfl_sync(~0u, n, o);
+            const int32_t at0 = (int32_t)__shfl_sync(~0u, place, o);
+            const int32_t src = __shfl_sync(~0u, from, o);
+            const int32_t tiles = ceil_div(seqs, a.tile_seqs);
+#pragma unroll 1
+            for (int32_t i = lane; i < count; i += 32) {
+                const int32_t cut = i / tiles, tile = i - cut * tiles;
+                Record r{};
+                r.b0 = first + tile * a.tile_seqs;
+                r.seqs = min(a.tile_seqs, first + seqs - r.b0);
+                r.table = src;
+                r.key_lo = cut * common * a.tile_keys;
+                r.key_hi = min(keys, (cut + 1) * common * a.tile_keys);
+                r.part = cut;
+                // no member has keys: nobody's table to read
+                if (src == INT32_MAX) r.key_hi = r.key_lo;
+                const int64_t at = at0 + i;
+                a.records[at + min(at * stride, (int64_t)n_own)] = r;
+            }
         }
     }
-    // ---- and each sequence's parts: those of its group's runs, then those of its own
-    carry = 0;
-    for (int32_t base = 0; base < a.B; base += kPlanThreads) {
+#pragma unroll 1
+    for (int32_t base = 0; base < a.B; base += threads) {
         const int32_t b = base + tid;
         const Sequence s = noted(b);
+        const int64_t place = base == 0 ? my_place : block_prefix(places_of(s), after, scratch);
+        if (b < a.B) a.part_prefix[b] = (int32_t)(place >> 32);
         const int32_t n = ceil_div(key_tiles(a, s.prefix, s.ctx), own);
         const int32_t before = ceil_div(key_tiles(a, 0, s.prefix), common);
-        const int64_t at = block_prefix((int64_t)(before + n) << 32 | n, carry, scratch);
-        if (b < a.B) a.part_prefix[b] = (int32_t)(at >> 32);
-        const int32_t first = (int32_t)at, origin = tile_origin(a, s.prefix);
-        for (int32_t i = 0; i < n; ++i) {
+        const int32_t origin = tile_origin(a, s.prefix);
+        auto put = [&](int32_t i, int32_t b, int32_t ctx, int32_t prefix, int32_t origin,
+                       int32_t before, int32_t j) {
             Record r{};
             r.b0 = r.table = b;
             r.seqs = 1;
-            r.key_lo = i == 0 ? s.prefix : origin + i * own * a.tile_keys;
-            r.key_hi = min(s.ctx, origin + (i + 1) * own * a.tile_keys);
+            r.key_lo = i == 0 ? prefix : origin + i * own * a.tile_keys;
+            r.key_hi = min(ctx, origin + (i + 1) * own * a.tile_keys);
             r.part = before + i;
-            const int64_t j = first + i;
-            const int64_t ahead = ((j + 1) * n_common + spread - 1) / spread;
-            put(j + min(ahead, (int64_t)n_common), r);
+            j += i;
+            a.records[j + min(j / stride + 1, n_common)] = r;
+        };
+        const bool few = n <= 8;
+#pragma unroll 1
+        for (int32_t i = 0; few && i < n; ++i)
+            put(i, b, s.ctx, s.prefix, origin, before, (int32_t)place);
+#pragma unroll 1
+        for (uint32_t left = __ballot_sync(~0u, !few); left; left &= left - 1) {
+            const int o = __ffs(left) - 1;
+            const int32_t ctx = __shfl_sync(~0u, s.ctx, o), prefix = __shfl_sync(~0u, s.prefix, o);
+            const int32_t from = __shfl_sync(~0u, origin, o), part = __shfl_sync(~0u, before, o);
+            const int32_t at = __shfl_sync(~0u, (int32_t)place, o);
+            const int32_t count = __shfl_sync(~0u, n, o), owner = __shfl_sync(~0u, b, o);
+#pragma unroll 1
+            for (int32_t i = lane; i < count; i += 32) put(i, owner, ctx, prefix, from, part, at);
         }
-    }
-    const int32_t parts = (int32_t)(carry >> 32);
-    if (tid == 0) a.part_prefix[a.B] = parts;
-    // cannot be: the run lengths allow for it
-    const bool fits = (int64_t)n_common + n_own <= a.cap_records && parts <= a.cap_parts;
-    if (!fits) {
-        if (tid == 0) pkv::report(a.status, PKV_STATUS_WORKSPACE_OVERFLOW);
-        __syncthreads();
-        for (int32_t b = tid; b <= a.B; b += kPlanThreads) a.part_prefix[b] = 0;
-    }
-    if (tid == 0) {
-        a.ctrl[0] = fits ? n_common + n_own : 0;
-        a.ctrl[1] = 0;
     }
 }
 
@@ -1235,7 +1296,7 @@ int add_tensors(const void* q, const void* k_cache, const void* v_cache,
 }
 
 int launch_plan(const SharedArgs& a, cudaStream_t s) {
-    plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+    plan_kernel<<<1, a.B <= 256 ? 256 : a.B <= 512 ? 512 : kMaxPlanThreads, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
