@@ -65,7 +65,7 @@ constexpr int kSms = 152;                // of a GB300: sizes follow from the ar
 struct Record {
     int32_t b0, seqs, table, key_lo, key_hi;
     int32_t part;                        // place of its part among a sequence's
-    int32_t pad0, pad1;
+    int32_t origin, tiles;               // its tiles' first key; how many there are
 };
 
 struct SharedArgs {
@@ -83,6 +83,7 @@ struct SharedArgs {
     float* part_o;                       // [cap_parts, Hq, D]
     int32_t B, Hq, Hkv, G, MB, NB, bs, max_ctx, D;
     int32_t box, edge_box, tile_keys;    // rows of a TMA box; in tiles not full; keys of a tile
+    int32_t tile_blocks, tile_rest;      // tile_keys in cache blocks, and keys beyond
     int32_t tile_heads, head_tiles, tile_seqs;
     int32_t cap_records, cap_parts, common_budget;
     float scale_log2;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
             const int32_t keys = __shfl_sync(~0u, x.keys, o), count = __shfl_sync(~0u, n, o);
             const int32_t at0 = (int32_t)__shfl_sync(~0u, place, o);
             const int32_t src = __shfl_sync(~0u, from, o);
-            const int32_t tiles = ceil_div(seqs, a.tile_seqs);
+            const int32_t tiles = ceil_div(seqs, a.tile_seqs), all = key_tiles(a, 0, keys);
 #pragma unroll 1
             for (int32_t i = lane; i < count; i += 32) {
                 const int32_t cut = i / tiles, tile = i - cut * tiles;
@@ -410,8 +411,9 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
                 r.key_lo = cut * common * a.tile_keys;
                 r.key_hi = min(keys, (cut + 1) * common * a.tile_keys);
                 r.part = cut;
+                r.origin = r.key_lo;
                 // no member has keys: nobody's table to read
-                if (src == INT32_MAX) r.key_hi = r.key_lo;
+                r.tiles = src == INT32_MAX ? 0 : min(common, all - cut * common);
                 const int64_t at = at0 + i;
                 a.records[at + min(at * stride, (int64_t)n_own)] = r;
             }
@@ -423,24 +425,26 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
         const Sequence s = noted(b);
         const int64_t place = base == 0 ? my_place : block_prefix(places_of(s), after, scratch);
         if (b < a.B) a.part_prefix[b] = (int32_t)(place >> 32);
-        const int32_t n = ceil_div(key_tiles(a, s.prefix, s.ctx), own);
+        const int32_t all = key_tiles(a, s.prefix, s.ctx), n = ceil_div(all, own);
         const int32_t before = ceil_div(key_tiles(a, 0, s.prefix), common);
         const int32_t origin = tile_origin(a, s.prefix);
         auto put = [&](int32_t i, int32_t b, int32_t ctx, int32_t prefix, int32_t origin,
-                       int32_t before, int32_t j) {
+                       int32_t before, int32_t all, int32_t j) {
             Record r{};
             r.b0 = r.table = b;
             r.seqs = 1;
             r.key_lo = i == 0 ? prefix : origin + i * own * a.tile_keys;
             r.key_hi = min(ctx, origin + (i + 1) * own * a.tile_keys);
             r.part = before + i;
+            r.origin = origin + i * own * a.tile_keys;
+            r.tiles = min(own, all - i * own);
             j += i;
             a.records[j + min(j / stride + 1, n_common)] = r;
         };
         const bool few = n <= 8;
 #pragma unroll 1
         for (int32_t i = 0; few && i < n; ++i)
-            put(i, b, s.ctx, s.prefix, origin, before, (int32_t)place);
+            put(i, b, s.ctx, s.prefix, origin, before, all, (int32_t)place);
 #pragma unroll 1
         for (uint32_t left = __ballot_sync(~0u, !few); left; left &= left - 1) {
             const int o = __ffs(left) - 1;
@@ -448,8 +452,10 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
             const int32_t from = __shfl_sync(~0u, origin, o), part = __shfl_sync(~0u, before, o);
             const int32_t at = __shfl_sync(~0u, (int32_t)place, o);
             const int32_t count = __shfl_sync(~0u, n, o), owner = __shfl_sync(~0u, b, o);
+            const int32_t tiles = __shfl_sync(~0u, all, o);
 #pragma unroll 1
-            for (int32_t i = lane; i < count; i += 32) put(i, owner, ctx, prefix, from, part, at);
+            for (int32_t i = lane; i < count; i += 32)
+                put(i, owner, ctx, prefix, from, part, tiles, at);
         }
     }
 }
@@ -544,81 +550,41 @@ __device__ __forceinline__ uint32_t range_word(int32_t lo, int32_t hi, int w) {
     return upto & ~((1u << lo) - 1);
 }
 
-// The K or V rows of a key tile by cp.async: lane l resolves rows l, l + 32, ...; then
-// D / 8 lanes copy a row, each 16-byte chunk to where a 128-byte-swizzled box would put
-// it.  Rows that do not count are left as they are.
+// The K or V rows lo .. hi - 1 of a key tile by cp.async: lane l resolves rows l, l + 32, ...;
+// then D / 8 lanes copy a row, each 16-byte chunk to where a 128-byte-swizzled box would put
+// it.  Other rows, and those of bad blocks, are left as they are; returns whether there are such
+// blocks, and the rows that were copied in `valid`.
 template <int D>
-__device__ __forceinline__ void gather_rows(const int64_t (&src)[4], const __nv_bfloat16* pool,
-                                            unsigned char* dst, int lane) {
+__device__ __forceinline__ bool gather_rows(const SharedArgs& a, const int32_t* table,
+                                            const __nv_bfloat16* pool, unsigned char* dst,
+                                            int32_t key0, int32_t lo, int32_t hi, int32_t kvh,
+                                            int lane, uint32_t (&valid)[4]) {
     constexpr int kChunks = D / 8, kRowsPer = 32 / kChunks;
     const int c = lane % kChunks, sub = lane / kChunks;
+    bool bad = false;
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+    for (int g = 0; g < 4; ++g) {
+        const int32_t i = g * 32 + lane, key = key0 + i;
+        int64_t src = -1;
+        if (i >= lo && i < hi) {
+            const int32_t blk = __ldg(table + key / a.bs);
+            if ((unsigned)blk < (unsigned)a.NB)
+                src = (((int64_t)blk * a.bs + key % a.bs) * a.Hkv + kvh) * D;
+            else
+                bad = true;
+        }
+        valid[g] = __ballot_sync(0xffffffffu, src >= 0);
 #pragma unroll 4
-        for (int i = 0; i < 32 / kRowsPer; ++i) {
-            const int rl = i * kRowsPer + sub;
-            const int64_t e = __shfl_sync(0xffffffffu, src[g], rl);
+        for (int k = 0; k < 32 / kRowsPer; ++k) {
+            const int rl = k * kRowsPer + sub;
+            const int64_t e = __shfl_sync(0xffffffffu, src, rl);
             const int r = g * 32 + rl;
             if (e >= 0)
                 cp_async16(dst + (c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4),
                            pool + e + c * 8, 16);
         }
-}
-
-// Where a lane finds its part of a key tile.
-struct Source {
-    uint32_t valid[4];                   // keys that count
-    int64_t rows[4];                     // kGather: element offsets of rows l, l + 32, ..., -1: none
-    int32_t row;                         // else: the pool row of this lane's box, -1: none
-    int32_t box, boxes;                  // rows of a box; boxes to load
-    bool full, bad;                      // all keys of the tile are in the run; a bad block id
-};
-
-template <int D, bool kGather>
-__device__ __forceinline__ Source find_tile(const SharedArgs& a, const int32_t* table, int32_t key_lo,
-                                            int32_t key_hi, int32_t key0, int32_t kvh, int lane) {
-    Source s;
-    const int32_t lo = max(key_lo - key0, 0), hi = min(key_hi - key0, a.tile_keys);
-    s.full = lo == 0 && hi == a.tile_keys;
-    s.box = s.full ? a.box : a.edge_box;
-    s.row = -1;
-    s.bad = false;
-    if constexpr (kGather) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int32_t i = g * 32 + lane, key = key0 + i;
-            s.rows[g] = -1;
-            if (i >= lo && i < hi) {
-                const int32_t blk = __ldg(table + key / a.bs);
-                if ((unsigned)blk < (unsigned)a.NB)
-                    s.rows[g] = (((int64_t)blk * a.bs + key % a.bs) * a.Hkv + kvh) * D;
-                else
-                    s.bad = true;
-            }
-            s.valid[g] = __ballot_sync(0xffffffffu, s.rows[g] >= 0);
-        }
-        s.boxes = 0;
-    } else {
-        const int32_t i = lane * s.box, key = key0 + i;
-        const bool wanted = i < hi && i + s.box > lo;
-        if (wanted) {
-            const int32_t blk = __ldg(table + key / a.bs);
-            if ((unsigned)blk < (unsigned)a.NB) s.row = blk * a.bs + key % a.bs;
-            else s.bad = true;
-        }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) s.valid[w] = range_word(lo, hi, w);
-        uint32_t gone = __ballot_sync(0xffffffffu, s.bad);
-        while (gone) {
-            const int u = __ffs(gone) - 1;
-            gone &= gone - 1;
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                s.valid[w] &= ~range_word(u * s.box, (u + 1) * s.box, w);
-        }
-        s.boxes = __popc(__ballot_sync(0xffffffffu, s.row >= 0));
     }
-    return s;
+    return __any_sync(0xffffffffu, bad);
 }
 
 // kGather: rows gathered (block sizes that are no multiple of 8).  kPolls: the waits take
@@ -686,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 4 || warp == 7) {
         // ------------------------------------------------------------ producers
         const bool k_side = warp == 4;
-        uint64_t* full = k_side ? s.k_full : s.v_full;
+        uint64_t* full_bar = k_side ? s.k_full : s.v_full;
         uint64_t* empty = k_side ? s.k_empty : s.v_empty;
         const CUtensorMap* whole_map = k_side ? &maps.k : &maps.v;
         const CUtensorMap* edge_map = k_side ? &maps.k_edge : &maps.v_edge;
@@ -711,16 +677,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto land = [&](int st) {
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
+            if (lane == 0) mbar_arrive(&full_bar[st]);
         };
         uint32_t next = draw(), it = __shfl_sync(0xffffffffu, next, 0);
         int4 r0 = make_int4(0, 0, 0, 0);     // the record of item `it`
-        int2 r1 = make_int2(0, 0);
+        int4 r1 = make_int4(0, 0, 0, 0);
         auto fetch = [&]() {
             if (it < n_items) {
                 const Record* r = a.records + it / units;
                 r0 = *reinterpret_cast<const int4*>(r);
-                r1 = *reinterpret_cast<const int2*>(&r->key_hi);
+                r1 = *reinterpret_cast<const int4*>(&r->key_hi);
             }
         };
         if (k_side) fetch();
@@ -746,10 +712,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x.key_lo = r0.w;
                 x.key_hi = r1.x;
                 x.part = r1.y;
-                x.origin = tile_origin(a, x.key_lo);
-                x.tiles = key_tiles(a, x.key_lo, x.key_hi);
-                x.kvh = unit / a.head_tiles;
-                x.head_tile = unit - x.kvh * a.head_tiles;
+                x.origin = r1.z;
+                x.tiles = r1.w;
+                x.kvh = unit;
+                x.head_tile = 0;
+                if (a.head_tiles > 1) {
+                    x.kvh = unit / a.head_tiles;
+                    x.head_tile = unit - x.kvh * a.head_tiles;
+                }
                 x.end = 0;
                 if (x.tiles == 0) next = draw();
                 // the queries of one sequence take half of the Q tile, so that the next
@@ -784,34 +754,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++q_uses[first];
                 if (x.q_slot == 2) ++q_uses[1];
             }
+            // Where this lane's box of a full tile is: cache block `at` of the table, row `off` of
+            // it; from tile to tile without a division.
+            int32_t at = 0, off = 0;
+            if (!kGather) {
+                const int32_t key = x.origin + lane * a.box;
+                at = key / a.bs;
+                off = key - at * a.bs;
+            }
             for (int32_t j = 0; j < x.tiles; ++j, ++fills) {
                 const int st = fills % kStages;
-                const Source src = find_tile<D, kGather>(
-                    a, table, x.key_lo, x.key_hi, x.origin + j * a.tile_keys, x.kvh, lane);
-                bad_block |= src.bad;
-                // the next item, and then its record, late: one that is held is kept from others
+                const int32_t key0 = x.origin + j * a.tile_keys;
+                const int32_t lo = max(x.key_lo - key0, 0), hi = min(x.key_hi - key0, a.tile_keys);
+                const bool full = lo == 0 && hi == a.tile_keys;
+                const int32_t box = full ? a.box : a.edge_box, i = lane * box;
+                const bool wanted = !kGather && i < hi && i + box > lo;
+                int32_t row = -1;
+                if (wanted) {
+                    int32_t block = at, r = off;
+                    if (!full) {
+                        block = (key0 + i) / a.bs;
+                        r = key0 + i - block * a.bs;
+                    }
+                    const int32_t blk = __ldg(table + block);
+                    if ((unsigned)blk < (unsigned)a.NB) row = blk * a.bs + r;
+                }
+                at += a.tile_blocks;
+                off += a.tile_rest;
+                if (off >= a.bs) {
+                    off -= a.bs;
+                    ++at;
+                }
                 if (k_side && j == max(x.tiles - 2, 0)) next = draw();
                 if (k_side && j == x.tiles - 1) {
                     it = __shfl_sync(0xffffffffu, next, 0);
                     fetch();
                 }
+                const int boxes = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                bool bad = __any_sync(0xffffffffu, wanted && row < 0);
                 if (fills >= kStages &&
                     !(ok = warp_wait(&empty[st], (fills / kStages - 1) & 1, &s.abort_flag, polls)))
                     break;
-                if (k_side) {
-                    // from the first tile with a bad block on, every tile gets its mask
-                    const bool first = !masked && __any_sync(0xffffffffu, src.bad);
-                    masked |= first;
-                    if (masked && lane == 0) {
-                        s.mask[fills % kMaskRing] =
-                            make_uint4(src.valid[0], src.valid[1], src.valid[2], src.valid[3]);
-                        if (first) *(volatile uint32_t*)&s.masked_from = fills;
-                    }
-                }
-                unsigned char* dst = k_side ? s.k[st] : s.v[st];
+                unsigned char* dst = (k_side ? s.k[0] : s.v[0]) + st * kTile;
+                uint32_t valid[4];
                 if constexpr (kGather) {
-                    gather_rows<D>(src.rows, pool, dst, lane);
+                    bad = gather_rows<D>(a, table, pool, dst, key0, lo, hi, x.kvh, lane, valid);
                     asm volatile("cp.async.commit_group;" ::: "memory");
+                }
+                if (bad || masked) {
+                    // from the first tile with a bad block on, every tile gets its mask
+                    bad_block |= bad;
+                    if (!kGather) {
+                        const uint32_t gone = __ballot_sync(0xffffffffu, wanted && row < 0);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int32_t k = w * 32 + lane;
+                            valid[w] = __ballot_sync(
+                                0xffffffffu, k >= lo && k < hi && !((gone >> (k / box)) & 1));
+                        }
+                    }
+                    if (k_side && lane == 0) {
+                        s.mask[fills % kMaskRing] =
+                            make_uint4(valid[0], valid[1], valid[2], valid[3]);
+                        if (!masked) *(volatile uint32_t*)&s.masked_from = fills;
+                    }
+                    masked = true;
+                }
+                if constexpr (kGather) {
                     if (pend >= 0) {         // the tile before this one has landed
                         asm volatile("cp.async.wait_group 1;" ::: "memory");
                         land(pend);
@@ -819,18 +828,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pend = st;
                 } else {
                     if (lane == 0) {
-                        if (src.boxes > 0)
-                            mbar_expect_tx(&full[st],
-                                           (uint32_t)(src.boxes * src.box * 128 * kBlocks));
+                        if (boxes > 0)
+                            mbar_expect_tx(&full_bar[st], (uint32_t)(boxes * box * 128 * kBlocks));
                         else
-                            mbar_arrive(&full[st]);
+                            mbar_arrive(&full_bar[st]);
                     }
                     __syncwarp();
-                    if (src.row >= 0) {
-                        const CUtensorMap* m = src.full ? whole_map : edge_map;
+                    if (row >= 0) {
+                        const CUtensorMap* m = full ? whole_map : edge_map;
                         for (int hf = 0; hf < kBlocks; ++hf)
-                            tma_load_3d(dst + hf * kHalf + lane * src.box * 128, m, &full[st],
-                                        hf * 64, x.kvh, src.row);
+                            tma_load_3d(dst + hf * kHalf + i * 128, m, &full_bar[st], hf * 64,
+                                        x.kvh, row);
                     }
                 }
             }
@@ -855,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k_side)
             for (it = __shfl_sync(0xffffffffu, next, 0); it < n_items;)
                 it = __shfl_sync(0xffffffffu, draw(), 0);
-        if (__any_sync(0xffffffffu, bad_block) && lane == 0)
+        if (bad_block && lane == 0)
             pkv::report(a.status, PKV_STATUS_BAD_BLOCK_ID);
         if (!ok && lane == 0) give_up(s, a.status);
     } else if (warp == 5 || warp == 6) {
@@ -1253,6 +1261,8 @@ int make_plan(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
     a.box = L.box;
     a.edge_box = L.edge_box;
     a.tile_keys = L.tile_keys;
+    a.tile_blocks = L.tile_keys / cache.block_size;
+    a.tile_rest = L.tile_keys % cache.block_size;
     a.tile_heads = L.tile_heads;
     a.head_tiles = L.head_tiles;
     a.tile_seqs = L.tile_seqs;
