@@ -103,11 +103,12 @@ __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) {
 // ---------------------------------------------------------------------- plan
 constexpr int kMaxPlanThreads = 1024;
 constexpr int kStaged = 1024;            // groups held in shared memory
+constexpr int kFew = 4;                  // groups up to which a length's items are counted exactly
 // Fewer common keys than this are attended by each sequence itself.
 constexpr int kMinShared = 64;
 // What the plan expects, in ns: a key tile of common keys and of own ones (which come from
 // HBM), the start and end of an item; and the bytes a ns of parts written and read again.
-constexpr float kCommonTile = 750, kOwnTile = 1450, kItemCost = 2500, kPartBytes = 3500;
+constexpr float kCommonTile = 850, kOwnTile = 1450, kItemCost = 2500, kPartBytes = 3500;
 
 struct Group {
     int32_t first, seqs;
@@ -191,6 +192,8 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
     // common tiles of row tiles, of sequences; own tiles; row tiles; sequences with own keys
     __shared__ unsigned long long sum[5];
     __shared__ int32_t run_len[2];           // key tiles of a common run, of an own run
+    __shared__ int32_t longest;              // key tiles of the longest prefix
+    __shared__ int2 few[kFew];               // (row tiles, key tiles) of the first groups
     __shared__ int32_t staged_offsets[kStaged + 1], staged_prefix[kStaged], staged_table[kStaged];
     const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
     const int32_t units = a.Hkv * a.head_tiles;
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
     // ---- groups: increasing offsets within the batch, or none is used
     const bool staged = a.groups <= kStaged;
     if (tid < 5) sum[tid] = 0;
+    if (tid == 5) longest = 1;
     if (staged && a.groups > 0)
 #pragma unroll 1
         for (int32_t g = tid; g <= a.groups; g += threads) {
@@ -235,9 +239,11 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
         if (g < groups) x = of.at(g, true);
         int32_t tiles = 0;
         int64_t t0 = 0, t1 = 0;              // these may pass 32 bits when added up
+        int32_t n = 0;
         if (x.keys > 0) {
             tiles = ceil_div(x.seqs, a.tile_seqs);
-            const int32_t n = key_tiles(a, 0, x.keys);
+            n = key_tiles(a, 0, x.keys);
+            atomicMax(&longest, n);
             if (!staged) a.table[x.first] = INT32_MAX;
             t0 = (int64_t)tiles * n;
             t1 = (int64_t)x.seqs * n;
@@ -251,6 +257,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
             atomicAdd(&sum[0], (unsigned long long)t0);
             atomicAdd(&sum[1], (unsigned long long)t1);
         }
+        if (g < kFew) few[g] = make_int2(tiles, n);
         add(3, tiles);
     }
     if (!staged) __syncthreads();
@@ -296,35 +303,50 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
     };
     __syncthreads();
 
-    // ---- run lengths: lane l of the first warp weighs common runs of a length
+    // ---- run lengths
     if (tid < 32) {
         const float common_tiles = (float)sum[0], members = (float)sum[1];
         const int64_t own_tiles = (int64_t)sum[2];
         // own runs: an item's start and end cost as much as three tiles, so two items an SM up
-        // to six tiles each, then up to sixteen items
+        // to ten tiles each, then up to sixteen items
         const int64_t work = own_tiles * units;
         int64_t own = (work + 2 * kSms - 1) / (2 * kSms);
-        own = own < 6 ? own : 6;
+        own = own < 10 ? own : 10;
         const int64_t sixteen = (work + 16 * kSms - 1) / (16 * kSms);
         own = own > sixteen ? own : sixteen;
         if (own < 1) own = 1;
         const float own_cost = ((float)own_tiles * kOwnTile +
                                 ((float)own_tiles / (float)own + (float)sum[4]) * kItemCost) *
                                units;
-        // lengths 1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 14, 16, 20, ...
-        const int32_t len = lane < 4 ? lane + 1 : (4 + (lane & 3)) << ((lane >> 2) - 1);
-        const float items = (common_tiles / len + (float)sum[3]) * units;
-        const float item = len * kCommonTile + kItemCost;
-        float cost = fmaxf(ceilf(items / kSms) * item, (items * item + own_cost) / kSms);
-        // parts: written once, read once, by all rows
-        cost += members / len * a.Hq * a.D * 4 / kPartBytes;
-        if (members / len > (float)a.common_budget) cost = INFINITY;
-        float best = cost;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            best = fminf(best, __shfl_xor_sync(~0u, best, off));
-        const uint32_t who = __ballot_sync(~0u, cost == best);
-        int64_t chosen = __shfl_sync(~0u, len, __ffs(who) - 1);
+        // a lane weighs two lengths: the longest prefix in so many runs, or in 1, 2, 3, ... tiles
+        float best = INFINITY;
+        int64_t chosen = 1;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const int32_t len = k == 0 ? ceil_div(longest, lane + 1) : lane < 8 ? lane + 1 : 2 * lane - 6;
+            float items = common_tiles / len + 0.5f * (float)sum[3];
+            if (groups <= kFew) {
+                int32_t count = 0;
+#pragma unroll 1
+                for (int32_t g = 0; g < groups; ++g) count += few[g].x * ceil_div(few[g].y, len);
+                items = (float)count;
+            }
+            items *= units;
+            const float item = len * kCommonTile + kItemCost;
+            // no CTA idle; and the last common run, which is drawn after three quarters of the
+            // own ones and what goes beside them
+            const float all = items * item, beside = all / (all + own_cost + 1.f) * own_cost;
+            float cost = fmaxf((all + own_cost) / kSms, 0.75f * (own_cost + beside) / kSms +
+                                                            ceilf(items / kSms) * item);
+            // parts: written once, read once, by all rows
+            cost += members / len * a.Hq * a.D * 4 / kPartBytes;
+            if (cost < best && members / len <= (float)a.common_budget) {
+                best = cost;
+                chosen = len;
+            }
+        }
+        const float least = __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(best)));
+        chosen = __shfl_sync(~0u, chosen, __ffs(__ballot_sync(~0u, best == least)) - 1);
         // never more parts than there is room for
         if (chosen * a.common_budget < (int64_t)sum[1])
             chosen = ((int64_t)sum[1] + a.common_budget - 1) / a.common_budget;
