@@ -30,8 +30,8 @@
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kBatch = 4;                    // heads a lane has in flight
+constexpr int kThreads = 192;
+constexpr int kBatch = 2;                    // heads a lane has in flight
 constexpr int kMaxDim = 256;
 
 struct HeadArgs {
@@ -164,30 +164,31 @@ struct Tables {
     float a[2][kMaxDim], b[2][kMaxDim];
 };
 
+// Half of the threads fill q's, half k's: each its own cosines and sines, for a token's rows wait
+// for the slowest of them.
 __device__ __forceinline__ void fill_tables(const HeadArgs& g, int32_t token, Tables& t) {
-    const int half = g.rotary_dim / 2;
-    for (int i = threadIdx.x; i < half; i += kThreads) {
+    const int half = g.rotary_dim / 2, which = threadIdx.x >= kThreads / 2;
+    const int first = threadIdx.x - which * (kThreads / 2);
+    float *ta = t.a[which], *tb = t.b[which];
+    if (half > 0) {
         const uint64_t p = (uint64_t)(int64_t)__ldg(g.positions + token);
-        float c, s;
-        turn(p * __ldg((const unsigned long long*)g.turns + i), c, s);
-        c *= g.magnitude;
-        s *= g.magnitude;
-        const int e1 = g.interleaved ? 2 * i : i, e2 = g.interleaved ? 2 * i + 1 : i + half;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
+        for (int i = first; i < half; i += kThreads / 2) {
+            const int e1 = g.interleaved ? 2 * i : i, e2 = g.interleaved ? 2 * i + 1 : i + half;
             const float w1 = weight_at(g, which, e1), w2 = weight_at(g, which, e2);
-            t.a[which][e1] = w1 * c;
-            t.b[which][e1] = -w2 * s;
-            t.a[which][e2] = w2 * c;
-            t.b[which][e2] = w1 * s;
+            float c, s;
+            turn(p * __ldg((const unsigned long long*)g.turns + i), c, s);
+            c *= g.magnitude;
+            s *= g.magnitude;
+            ta[e1] = w1 * c;
+            tb[e1] = -w2 * s;
+            ta[e2] = w2 * c;
+            tb[e2] = w1 * s;
         }
     }
-    for (int e = g.rotary_dim + threadIdx.x; e < g.D; e += kThreads)
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            t.a[which][e] = weight_at(g, which, e);
-            t.b[which][e] = 0.f;
-        }
+    for (int e = g.rotary_dim + first; e < g.D; e += kThreads / 2) {
+        ta[e] = weight_at(g, which, e);
+        tb[e] = 0.f;
+    }
 }
 
 __device__ __forceinline__ Pairs table_at(const float* p) {
