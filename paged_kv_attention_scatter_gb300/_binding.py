@@ -971,6 +971,7 @@ class Rotary:
 
     def __init__(self, turns, rotary_dim, interleaved, magnitude):
         self.turns = turns                              # [rotary_dim / 2] int64 (uint64 bits)
+        self.index = turns.get_device()
         self.rotary_dim = rotary_dim
         self.interleaved = bool(interleaved)
         self.magnitude = float(magnitude)
@@ -1029,11 +1030,11 @@ def _heads(t, name, dtype, index, like=None):
     contiguous (a view of a packed projection, say)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
     if t.get_device() != index or index < 0:
         raise ValueError(f"{name} must be on cuda:{max(index, 0)}, got {t.device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    shape = t.shape
     if len(shape) != 3 or (like is not None and shape != like):
         raise ValueError(f"{name} must be {'[tokens, heads, head_dim]' if like is None else like}"
                          f", got {list(shape)}")
@@ -1044,37 +1045,45 @@ def _heads(t, name, dtype, index, like=None):
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, positions, rope):
-    """What both calls check alike: (index, tokens, the arguments of q and k, of
-    the weights, positions, rotation)."""
+    """What both calls check alike: (index, tokens, heads of q and k, head_dim, the addresses
+    and strides of q and k, of the weights and their type, of the positions; the rotation)."""
     index, dtype = q.get_device(), q.dtype
     if dtype not in _TYPES:
         raise TypeError(f"q must be fp32, bf16 or fp16, got {dtype}")
-    rows = (*_heads(q, "q", dtype, index), *_heads(k, "k", dtype, index))
-    if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+    qp, qs = _heads(q, "q", dtype, index)
+    kp, ks = _heads(k, "k", dtype, index)
+    n, hq, d = q.shape
+    n2, hkv, d2 = k.shape
+    if n2 != n or d2 != d:
         raise ValueError("q and k must have the same tokens and head_dim")
-    n, _, d = q.shape
-    wp, wtype = [None, None], dtype
-    for i, (name, w) in enumerate((("q_weight", q_weight), ("k_weight", k_weight))):
-        if w is None:
-            continue
-        if w.shape != (d,):
-            raise ValueError(f"{name} must be [head_dim]")
-        if wp[0] is not None and w.dtype is not wtype:
-            raise TypeError("q_weight and k_weight must have the same dtype")
-        wtype = w.dtype
+    qwp = kwp = None
+    wtype = dtype
+    if q_weight is not None:
+        wtype = q_weight.dtype
         if wtype not in _TYPES:
-            raise TypeError(f"{name} must be fp32, bf16 or fp16, got {wtype}")
-        wp[i] = _at(w, name, wtype, index)
+            raise TypeError(f"q_weight must be fp32, bf16 or fp16, got {wtype}")
+        if q_weight.shape != (d,):
+            raise ValueError("q_weight must be [head_dim]")
+        qwp = _at(q_weight, "q_weight", wtype, index)
+    if k_weight is not None:
+        if q_weight is not None and k_weight.dtype is not wtype:
+            raise TypeError("q_weight and k_weight must have the same dtype")
+        wtype = k_weight.dtype
+        if wtype not in _TYPES:
+            raise TypeError(f"k_weight must be fp32, bf16 or fp16, got {wtype}")
+        if k_weight.shape != (d,):
+            raise ValueError("k_weight must be [head_dim]")
+        kwp = _at(k_weight, "k_weight", wtype, index)
     if rope is None:
-        return index, n, rows, (*wp, _TYPES[wtype]), None, _NO_ROTARY
+        return index, n, hq, hkv, d, qp, qs, kp, ks, qwp, kwp, _TYPES[wtype], None, _NO_ROTARY
     if not isinstance(rope, Rotary):
         raise TypeError("rope must come from rotary()")
-    if rope.turns.get_device() != index:
+    if rope.index != index:
         raise ValueError(f"rope is on {rope.turns.device}, expected cuda:{index}")
     if positions is None or positions.shape != (n,):
         raise ValueError("positions must be [tokens]")
-    return (index, n, rows, (*wp, _TYPES[wtype]), _at(positions, "positions", torch.int32, index),
-            rope.desc)
+    return (index, n, hq, hkv, d, qp, qs, kp, ks, qwp, kwp, _TYPES[wtype],
+            _at(positions, "positions", torch.int32, index), rope.desc)
 
 
 _NO_ROTARY = RotaryDesc(None, 0, 0, 1.0)
@@ -1086,19 +1095,34 @@ def qk_norm_rope(q, k, q_weight, k_weight, eps, positions, rope, q_out=None, k_o
     None) of every head of q [T, Hq, D] and k [T, Hkv, D], fp32, bf16 or fp16; tokens
     may be strided (views of a packed projection).  positions [T] int32.  Returns
     (q_out, k_out), contiguous unless given; pass q_out=q, k_out=k to work in place."""
-    lib = load()
-    index, n, rows, weights, pos, desc = _norm_rope_args(q, k, q_weight, k_weight, positions, rope)
-    dtype, hq, d = q.dtype, q.shape[1], q.shape[2]
+    f = load().pkv_qk_norm_rope
+    index, n, hq, hkv, d, qp, qs, kp, ks, qwp, kwp, wtype, pos, desc = _norm_rope_args(
+        q, k, q_weight, k_weight, positions, rope)
+    dtype = q.dtype
 
     def call(s):
-        qo = torch.empty(q.shape, dtype=dtype, device=q.device) if q_out is None else q_out
-        ko = torch.empty(k.shape, dtype=dtype, device=q.device) if k_out is None else k_out
-        _check(lib.pkv_qk_norm_rope(*rows, _TYPES[dtype], *weights, float(eps), pos, desc, n, hq,
-                                    k.shape[1], d, *_heads(qo, "q_out", dtype, index, q.shape),
-                                    *_heads(ko, "k_out", dtype, index, k.shape), s),
-               "pkv_qk_norm_rope")
+        if q_out is None:
+            qo, qos = _new_rows(q), hq * d
+            qop = qo.data_ptr()
+        else:
+            qo, (qop, qos) = q_out, _heads(q_out, "q_out", dtype, index, q.shape)
+        if k_out is None:
+            ko, kos = _new_rows(k), hkv * d
+            kop = ko.data_ptr()
+        else:
+            ko, (kop, kos) = k_out, _heads(k_out, "k_out", dtype, index, k.shape)
+        rc = f(qp, qs, kp, ks, _TYPES[dtype], qwp, kwp, wtype, eps, pos, desc, n, hq, hkv, d, qop,
+               qos, kop, kos, s)
+        if rc:
+            _check(rc, "pkv_qk_norm_rope")
         return qo, ko
     return _on(index, stream, call)
+
+
+def _new_rows(t):
+    """A contiguous tensor of t's shape (of one token, its strides are not looked at)."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype,
+                                                                     device=t.device)
 
 
 def qk_norm_rope_kv_store(q, k, v, q_weight, k_weight, eps, positions, rope, k_cache, v_cache,
@@ -1108,29 +1132,34 @@ def qk_norm_rope_kv_store(q, k, v, q_weight, k_weight, eps, positions, rope, k_c
     the paged cache as kv_store stores them (slot_mapping [T] int32, negative =
     skip).  Returns q_out; the k rows are also written to k_out when given (for
     paged_prefill_varlen)."""
-    lib = load()
-    index, n, rows, weights, pos, desc = _norm_rope_args(q, k, q_weight, k_weight, positions, rope)
+    f = load().pkv_qk_norm_rope_kv_store
+    index, n, hq, hkv, d, qp, qs, kp, ks, qwp, kwp, wtype, pos, desc = _norm_rope_args(
+        q, k, q_weight, k_weight, positions, rope)
     bf16 = torch.bfloat16
     if q.dtype is not bf16:
         raise TypeError(f"q must be {bf16}, got {q.dtype}")
-    vrow = _heads(v, "v", bf16, index, k.shape)
+    vp, vs = _heads(v, "v", bf16, index, k.shape)
     shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape or shape[2:] != k.shape[1:]:
+    if len(shape) != 4 or v_cache.shape != shape or shape[2] != hkv or shape[3] != d:
         raise ValueError("k_cache and v_cache must both be [num_blocks, block_size, "
                          "num_kv_heads, head_dim] matching k")
     if slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must hold one slot per token")
     slots = _at(slot_mapping, "slot_mapping", torch.int32, index)
-    caches = _at(k_cache, "k_cache", bf16, index), _at(v_cache, "v_cache", bf16, index)
-    st = _maybe(status, "status", torch.int32, index)
-    ko = (None, 0) if k_out is None else _heads(k_out, "k_out", bf16, index, k.shape)
+    kc, vc = _at(k_cache, "k_cache", bf16, index), _at(v_cache, "v_cache", bf16, index)
+    st = None if status is None else _at(status, "status", torch.int32, index)
+    kop, kos = (None, 0) if k_out is None else _heads(k_out, "k_out", bf16, index, k.shape)
 
     def call(s):
-        qo = torch.empty(q.shape, dtype=bf16, device=q.device) if q_out is None else q_out
-        _check(lib.pkv_qk_norm_rope_kv_store(
-            *rows, *vrow, *weights, float(eps), pos, desc, slots, n, q.shape[1],
-            *_heads(qo, "q_out", bf16, index, q.shape), *ko, *caches, _desc(*shape), st, s),
-            "pkv_qk_norm_rope_kv_store")
+        if q_out is None:
+            qo, qos = _new_rows(q), hq * d
+            qop = qo.data_ptr()
+        else:
+            qo, (qop, qos) = q_out, _heads(q_out, "q_out", bf16, index, q.shape)
+        rc = f(qp, qs, kp, ks, vp, vs, qwp, kwp, wtype, eps, pos, desc, slots, n, hq, qop, qos,
+               kop, kos, kc, vc, _desc(*shape), st, s)
+        if rc:
+            _check(rc, "pkv_qk_norm_rope_kv_store")
         return qo
     return _on(index, stream, call)
 
