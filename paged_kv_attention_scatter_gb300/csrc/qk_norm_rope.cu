@@ -16,13 +16,33 @@
 // nearest quarter turn is taken off as an integer, so that the rest, within 1/8 turn, goes
 // to sincospi with 24 significant bits of its own.
 //
-// Bound: every row is read once and written once.
+// Bound: every row is read once and written once; beside that, the instructions of a head.
 //
-// Layout.  A CTA takes one token.  Its first threads build the tables while the rows'
-// loads are in flight.  A head is D / 8 lanes of a warp (in a group of 8, 16 or 32) of 8
-// entries each: 16 bytes for 16-bit types.  The half layout's partner entries come from
-// the lane R/16 further on by shuffles of the packed rows, or from memory where R is no
-// multiple of 16; the interleaved layout's lie in the same lane.
+// Layout.  A head is 4, 8 or 16 lanes of a warp, with two chunks of eight entries each: for
+// the half layout the two that are each other's partners where the rotated part is whole
+// chunks, so that no entry crosses lanes; the interleaved layout's partners lie in the same
+// chunk, and the others come through shared memory, four in one access where they lie so.
+// Arithmetic is on packed pairs of fp32.
+//
+// head_kernel, for few tokens: a CTA takes one token, all of its heads at once, and builds
+// the tables while the rows' loads are in flight.  One token of 24 heads takes 2.4 us, an
+// empty kernel about as long.  192 threads with two heads each in flight; 128 threads took
+// 8% longer for 8191 tokens of 24 heads in 32 bits, the tables built by half of the threads 15%.
+//
+// row_kernel, for many: an SM's 16 warps each work through a run of pieces (some heads of a
+// token), with A and B in registers, made once for a token's q and once for its k, and rows
+// that arrive through shared memory four pieces ahead.  head_kernel reads A and B from
+// shared memory for every head and waits for its token's angles before any row: it is bound
+// by those reads and by the wait.  Behind row_kernel stands the issue of its instructions
+// and, at 5.7 TB/s, the memory.  head / row kernel, us:
+//   tokens                                      1024        2048        4096        16384
+//   24 heads of 80, 32 bits, partial rotation    7.7/8.4   12.7/10.8   22.6/17.6   83.9/58.2
+//   40 of 128, 16 bits, pairs, half rotated      6.5/7.1    9.2/10.1   17.1/16.1   63.6/59.3
+//   24 of 128, bf16, all rotated                 5.6/6.1    8.0/7.8    13.4/12.0   47.4/39.8
+//   48 of 128, bf16, into the cache              7.8/7.7   11.9/11.3   20.6/20.3   78.5/69.8
+// so kManyTokens is 2048.  20 warps with four stages took 2% less for the first and 3% more
+// for the last; 24 and 32 warps spill and take longer; stages of 4 KB, three of them, alike.
+// Both kernels compute an entry by the same steps: a token's bits are the same in any batch.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -33,6 +53,7 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kBatch = 2;                    // heads a lane has in flight
 constexpr int kMaxDim = 256;
+constexpr int kManyTokens = 2048;            // from here on, row_kernel
 
 struct HeadArgs {
     const void* in[3];                       // q, k, v
@@ -102,15 +123,25 @@ __device__ __forceinline__ uint32_t pack(float2 f, __half) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 16 bytes past the nearest cache, by an ordinary load: the rows may be written in place.
+__device__ __forceinline__ uint4 load16(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+
 // Eight entries as they lie in memory.
 template <typename T>
 struct Eight {
     uint4 v;
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const T* p) { v = pkv::ld_stream16(p); }
+    __device__ __forceinline__ void load(const T* p) { v = load16(p); }
     __device__ __forceinline__ Pairs get() const {
         return {{two(v.x, T()), two(v.y, T()), two(v.z, T()), two(v.w, T())}};
     }
+    __device__ __forceinline__ void take(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
     static __device__ __forceinline__ void store(T* p, const Pairs& y) {
         *reinterpret_cast<uint4*>(p) =
             make_uint4(pack(up2(y.v[0]), T()), pack(up2(y.v[1]), T()), pack(up2(y.v[2]), T()),
@@ -123,11 +154,18 @@ struct Eight<float> {
     float4 a, b;
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float* p) {
-        a = pkv::ld_stream16f(p);
-        b = pkv::ld_stream16f(p + 4);
+        const uint4 u = load16(p), v = load16(p + 4);
+        a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                        __uint_as_float(u.w));
+        b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                        __uint_as_float(v.w));
     }
     __device__ __forceinline__ Pairs get() const {
         return {{pk2(a.x, a.y), pk2(a.z, a.w), pk2(b.x, b.y), pk2(b.z, b.w)}};
+    }
+    __device__ __forceinline__ void take(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
     }
     static __device__ __forceinline__ void store(float* p, const Pairs& y) {
         const float2 f0 = up2(y.v[0]), f1 = up2(y.v[1]), f2 = up2(y.v[2]), f3 = up2(y.v[3]);
@@ -363,15 +401,348 @@ __global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: a warp works through a run of pieces, a piece being some heads of one
+// token's q, k or v.
+// ---------------------------------------------------------------------------
+// A piece holds a pass's heads at least: 2 heads of 256 in 32 bits are 2 KB.
+constexpr int kWarps = 16, kStages = 5, kPieceBytes = 2048;
+
+struct Stage {
+    uint4 rows[kPieceBytes / 16];
+    int32_t position, slot, unused[2];
+};
+
+// One warp's shared memory.
+struct WarpShared {
+    Stage stage[kStages];
+    float c[kMaxDim / 2], s[kMaxDim / 2];    // of the token's pairs
+};
+
+struct RowShared {
+    float weight[2][kMaxDim];
+    WarpShared warp[kWarps];
+};
+
+struct Pieces {
+    int32_t heads, of_q, of_k, per_token;    // heads of a piece; pieces of q, of k, of a token
+    int64_t units;                           // pieces of all tokens
+};
+
+__device__ __forceinline__ void async16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void async4(void* to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+
+// Which rows a piece of a token holds: q, k or v (0, 1, 2), its first head, its heads.
+struct Piece {
+    int32_t which, h0, n;
+};
+__device__ __forceinline__ Piece piece_at(const HeadArgs& g, const Pieces& p, int32_t i) {
+    const int32_t which = i < p.of_q ? 0 : i < p.of_q + p.of_k ? 1 : 2;
+    const int32_t h0 = (i - (which == 0 ? 0 : which == 1 ? p.of_q : p.of_q + p.of_k)) * p.heads;
+    const int32_t left = (which == 0 ? g.Hq : g.Hkv) - h0;
+    return {which, h0, left < p.heads ? left : p.heads};
+}
+
+// Four entries' partners in a row, as two packed pairs.
+__device__ __forceinline__ void four(const float* p, uint64_t& lo, uint64_t& hi) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    lo = v.x;
+    hi = v.y;
+}
+template <typename T>
+__device__ __forceinline__ void four(const T* p, uint64_t& lo, uint64_t& hi) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    lo = two(v.x, T());
+    hi = two(v.y, T());
+}
+
+template <typename T, int kLanes, Partner kPartner, bool kStore>
+__global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, const Pieces p) {
+    constexpr int kHeads = 32 / kLanes, kAhead = kStages - 1;
+    extern __shared__ __align__(16) unsigned char raw[];
+    RowShared& sh = *reinterpret_cast<RowShared*>(raw);
+    for (int i = threadIdx.x; i < 2 * g.D; i += kWarps * 32) {
+        const int which = i >= g.D, e = i - which * g.D;
+        sh.weight[which][e] = weight_at(g, which, e);
+    }
+    __syncthreads();
+    const int lane = threadIdx.x % 32, j = lane % kLanes, head = lane / kLanes;
+    WarpShared& my = sh.warp[threadIdx.x / 32];
+    // this lane's chunks, as in head_kernel
+    const int chunks = g.D / 8, away = kPartner == kChunks ? g.rotary_dim / 16 : 0;
+    const int left = chunks - 2 * away;
+    const int c0 = j < away ? j : j + away, c1 = j < away ? j + away : j + away + (left + 1) / 2;
+    const bool has0 = j < away + (left + 1) / 2;
+    const bool has1 = j < away || (has0 && c1 < chunks);
+    const int e0 = has0 ? c0 * 8 : 0, e1 = has1 ? c1 * 8 : 0;
+    const int half = g.rotary_dim / 2;
+
+    // this warp's run of pieces
+    const int64_t warps = (int64_t)gridDim.x * kWarps;
+    const int64_t w = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+    const int64_t first = p.units * w / warps, last = p.units * (w + 1) / warps;
+    if (first >= last) return;
+    const int32_t count = (int32_t)(last - first);
+    int32_t token = (int32_t)(first / p.per_token), at = (int32_t)(first % p.per_token);
+    int32_t next_token = token, next_at = at;                // the next piece to ask for
+
+    auto ask = [&](int32_t i) {
+        if (i < count) {
+            Stage& st = my.stage[i % kStages];
+            const Piece pc = piece_at(g, p, next_at);
+            const T* from = (const T*)g.in[pc.which] + next_token * g.in_stride[pc.which] +
+                            (int64_t)pc.h0 * g.D;
+            const int32_t vecs = pc.n * g.D * (int32_t)sizeof(T) / 16 - lane;
+            const uint4* mine = (const uint4*)from + lane;
+#pragma unroll
+            for (int v = 0; v < kPieceBytes / 16; v += 32)
+                if (v < vecs) async16(st.rows + lane + v, mine + v);
+            if (lane == 0) {
+                if (kPartner != kNone) async4(&st.position, g.positions + next_token);
+                if (kStore) async4(&st.slot, g.slots + next_token);
+            }
+            if (++next_at == p.per_token) {
+                next_at = 0;
+                ++next_token;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ask(i);
+
+    Pairs a0, a1, b0 = {}, b1 = {};                          // A and B of this lane's chunks
+    int32_t have_token = -1, have = -1;                      // what c, s and A, B are of
+    for (int32_t i = 0; i < count; ++i) {
+        ask(i + kAhead);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+        __syncwarp();
+        Stage& st = my.stage[i % kStages];
+        const Piece pc = piece_at(g, p, at);
+        int32_t slot = -1;
+        if constexpr (kStore) {
+            slot = st.slot;
+            if ((int64_t)slot >= g.num_slots) {
+                if (lane == 0) pkv::report(g.status, PKV_STATUS_SLOT_OUT_OF_RANGE);
+                slot = -1;
+            }
+        }
+        if (kStore && pc.which == 2) {                       // v rows, as they are
+            if (slot >= 0) {
+                uint4* to = (uint4*)(g.cache[1] + ((int64_t)slot * g.Hkv + pc.h0) * g.D);
+                const int32_t vecs = pc.n * g.D * (int32_t)sizeof(T) / 16 - lane;
+#pragma unroll
+                for (int v = 0; v < kPieceBytes / 16; v += 32)
+                    if (v < vecs) to[lane + v] = st.rows[lane + v];
+            }
+        } else {
+            if (token != have_token) {
+                have_token = token;
+                have = -1;
+                if constexpr (kPartner != kNone) {
+                    const uint64_t pos = (uint64_t)(int64_t)st.position;
+                    for (int t = lane; t < half; t += 32) {
+                        float c, s;
+                        turn(pos * __ldg((const unsigned long long*)g.turns + t), c, s);
+                        my.c[t] = c * g.magnitude;
+                        my.s[t] = s * g.magnitude;
+                    }
+                    __syncwarp();
+                }
+            }
+            if (pc.which != have) {
+                have = pc.which;
+                const float* weight = sh.weight[pc.which];
+                a0 = table_at(weight + e0);
+                a1 = table_at(weight + e1);
+                if constexpr (kPartner == kChunks) {
+                    if (j < away) {
+                        const Pairs c = table_at(my.c + e0), s = table_at(my.s + e0);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            b0.v[t] = mul2(mul2(a1.v[t], s.v[t]), pk2(-1.f, -1.f));
+                            b1.v[t] = mul2(a0.v[t], s.v[t]);
+                            a0.v[t] = mul2(a0.v[t], c.v[t]);
+                            a1.v[t] = mul2(a1.v[t], c.v[t]);
+                        }
+                    }
+                } else if constexpr (kPartner == kPairs) {
+                    auto chunk = [&](int e, Pairs& ta, Pairs& tb) {
+                        const float4 c = *reinterpret_cast<const float4*>(my.c + e / 2);
+                        const float4 s = *reinterpret_cast<const float4*>(my.s + e / 2);
+                        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            if (e + 2 * t >= g.rotary_dim) break;
+                            tb.v[t] = mul2(swapped(ta.v[t]), pk2(-ss[t], ss[t]));
+                            ta.v[t] = mul2(ta.v[t], pk2(cc[t], cc[t]));
+                        }
+                    };
+                    chunk(e0, a0, b0);
+                    chunk(e1, a1, b1);
+                } else if constexpr (kPartner == kShared) {
+                    // A (from the weight) and B of entry e
+                    auto entry = [&](int e, float& a, float& b) {
+                        b = 0.f;
+                        if (e >= g.rotary_dim) return;
+                        const int t = e < half ? e : e - half;
+                        a *= my.c[t];
+                        b = e < half ? -weight[e + half] * my.s[t] : weight[t] * my.s[t];
+                    };
+                    auto chunk = [&](int e, Pairs& ta, Pairs& tb) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t, e += 2) {
+                            float2 a = up2(ta.v[t]);
+                            float b, d;
+                            entry(e, a.x, b);
+                            entry(e + 1, a.y, d);
+                            ta.v[t] = pk2(a.x, a.y);
+                            tb.v[t] = pk2(b, d);
+                        }
+                    };
+                    chunk(e0, a0, b0);
+                    chunk(e1, a1, b1);
+                }
+            }
+            const bool norm = g.weight[pc.which] != nullptr;
+            T* out = (T*)g.out[pc.which];
+            if (out) out += token * g.out_stride[pc.which] + (int64_t)pc.h0 * g.D;
+            T* cached = nullptr;
+            if (kStore && pc.which == 1 && slot >= 0)
+                cached = (T*)g.cache[0] + ((int64_t)slot * g.Hkv + pc.h0) * g.D;
+            const T* rows = reinterpret_cast<const T*>(st.rows);
+#pragma unroll 2
+            for (int32_t base = 0; base < pc.n; base += kHeads) {
+                // lanes without a head or a chunk compute on another's, and write nothing
+                const int32_t h = base + head < pc.n ? base + head : 0;
+                const bool in = base + head < pc.n && has0;
+                const T* row = rows + h * g.D;
+                Eight<T> x0, x1;
+                x0.take(row + e0);
+                x1.take(row + e1);
+                const Pairs a = x0.get(), b = x1.get();
+                float r = 1.f;
+                if (norm) {
+                    uint64_t s2 = mul2(a.v[0], a.v[0]);
+#pragma unroll
+                    for (int t = 1; t < 4; ++t) s2 = fma2(a.v[t], a.v[t], s2);
+                    uint64_t both = s2;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) both = fma2(b.v[t], b.v[t], both);
+                    const float2 s = up2(has1 ? both : s2);
+                    float ss = has0 ? s.x + s.y : 0.f;
+#pragma unroll
+                    for (int off = kLanes / 2; off > 0; off >>= 1)
+                        ss += __shfl_xor_sync(~0u, ss, off);
+                    r = rsqrtf(ss * g.inv_dim + g.eps);
+                }
+                const uint64_t r2 = pk2(r, r);
+                Pairs y0, y1;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    y0.v[t] = mul2(a0.v[t], a.v[t]);
+                    y1.v[t] = mul2(a1.v[t], b.v[t]);
+                }
+                if constexpr (kPartner == kPairs) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        if (e0 + 2 * t < g.rotary_dim)
+                            y0.v[t] = fma2(b0.v[t], swapped(a.v[t]), y0.v[t]);
+                        if (e1 + 2 * t < g.rotary_dim)
+                            y1.v[t] = fma2(b1.v[t], swapped(b.v[t]), y1.v[t]);
+                    }
+                } else if constexpr (kPartner == kChunks) {
+                    if (j < away) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            y0.v[t] = fma2(b0.v[t], b.v[t], y0.v[t]);
+                            y1.v[t] = fma2(b1.v[t], a.v[t], y1.v[t]);
+                        }
+                    }
+                } else if constexpr (kPartner == kShared) {
+                    auto chunk = [&](int e, const Pairs& tb, Pairs& y) {
+                        if (half % 4 == 0) {
+#pragma unroll
+                            for (int t = 0; t < 4; t += 2, e += 4) {
+                                if (e >= g.rotary_dim) break;
+                                uint64_t lo, hi;
+                                four(row + (e < half ? e + half : e - half), lo, hi);
+                                y.v[t] = fma2(tb.v[t], lo, y.v[t]);
+                                y.v[t + 1] = fma2(tb.v[t + 1], hi, y.v[t + 1]);
+                            }
+                        } else {
+                            auto one = [&](int e) {
+                                return (float)row[e < half ? e + half : e - half];
+                            };
+#pragma unroll
+                            for (int t = 0; t < 4; ++t, e += 2) {
+                                if (e >= g.rotary_dim) break;
+                                y.v[t] = fma2(tb.v[t], pk2(one(e), one(e + 1)), y.v[t]);
+                            }
+                        }
+                    };
+                    chunk(e0, b0, y0);
+                    chunk(e1, b1, y1);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    y0.v[t] = mul2(y0.v[t], r2);
+                    y1.v[t] = mul2(y1.v[t], r2);
+                }
+                if (in && out) {
+                    Eight<T>::store(out + h * g.D + e0, y0);
+                    if (has1) Eight<T>::store(out + h * g.D + e1, y1);
+                }
+                if (kStore && in && cached) {
+                    Eight<T>::store(cached + h * g.D + e0, y0);
+                    if (has1) Eight<T>::store(cached + h * g.D + e1, y1);
+                }
+            }
+        }
+        __syncwarp();                                        // the stage is read
+        if (++at == p.per_token) {
+            at = 0;
+            ++token;
+        }
+    }
+}
+
+template <typename T, int kLanes, Partner kPartner, bool kStore>
+int launch(const HeadArgs& g, cudaStream_t s) {
+    if (g.num_tokens < kManyTokens) {
+        head_kernel<T, kLanes, kPartner, kStore><<<(unsigned)g.num_tokens, kThreads, 0, s>>>(g);
+    } else {
+        constexpr int kHeads = 32 / kLanes;
+        Pieces p;
+        p.heads = kPieceBytes / (g.D * (int)sizeof(T)) / kHeads * kHeads;
+        p.of_q = (g.Hq + p.heads - 1) / p.heads;
+        p.of_k = (g.Hkv + p.heads - 1) / p.heads;
+        p.per_token = p.of_q + p.of_k * (kStore ? 2 : 1);
+        p.units = (int64_t)p.per_token * g.num_tokens;
+        static std::atomic<uint64_t> done{0};
+        if (!pkv_dynamic_smem_once((const void*)row_kernel<T, kLanes, kPartner, kStore>,
+                                   (int)sizeof(RowShared), done))
+            return PKV_ERR_CUDA;
+        int64_t grid = (p.units + kWarps - 1) / kWarps;
+        if (grid > pkv_num_sms()) grid = pkv_num_sms();
+        row_kernel<T, kLanes, kPartner, kStore>
+            <<<(unsigned)grid, kWarps * 32, sizeof(RowShared), s>>>(g, p);
+    }
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 template <typename T, int kLanes, bool kStore>
 int launch(const HeadArgs& g, cudaStream_t s) {
-    void (*kernel)(const HeadArgs) =
-        g.rotary_dim == 0        ? head_kernel<T, kLanes, kNone, kStore>
-        : g.interleaved          ? head_kernel<T, kLanes, kPairs, kStore>
-        : g.rotary_dim % 16 == 0 ? head_kernel<T, kLanes, kChunks, kStore>
-                                 : head_kernel<T, kLanes, kShared, kStore>;
-    kernel<<<(unsigned)g.num_tokens, kThreads, 0, s>>>(g);
-    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return g.rotary_dim == 0        ? launch<T, kLanes, kNone, kStore>(g, s)
+           : g.interleaved          ? launch<T, kLanes, kPairs, kStore>(g, s)
+           : g.rotary_dim % 16 == 0 ? launch<T, kLanes, kChunks, kStore>(g, s)
+                                    : launch<T, kLanes, kShared, kStore>(g, s);
 }
 
 template <typename T, bool kStore>

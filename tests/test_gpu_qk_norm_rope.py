@@ -239,3 +239,94 @@ def test_empty_other_stream_and_graph(cuda):
     assert torch.equal(kc.view(64, 2, 128)[20:32], ref[1])
     assert torch.equal(vc.view(64, 2, 128)[20:32], v)
     assert (kc.view(64, 2, 128)[:20] == 0).all()
+
+
+MANY = [  # as CASES, of so many tokens that warps work through runs of them
+    (2048, 1, 1, 8, 8, True, FP, FP, False),
+    (2100, 9, 2, 256, 256, False, FP, BF, True),
+    (2049, 3, 3, 80, 20, False, BF, BF, True),
+    (2300, 5, 1, 72, 40, False, FP, None, False),
+    (2077, 4, 2, 24, 10, False, HF, HF, True),
+    (5000, 2, 1, 136, 34, True, HF, FP, True),
+    (2050, 33, 1, 128, 64, False, BF, BF, True),
+    (20000, 1, 1, 64, 64, False, BF, BF, False),
+    (2500, 6, 2, 64, 0, False, BF, BF, True),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_many_tokens(cuda, case):
+    """Against the oracle at both ends, and all of it against calls of fewer tokens:
+    a token's bits do not depend on the batch."""
+    pkv = lib()
+    n, hq, hkv, d, rot, inter, dtype, wtype, packed = case
+    rng = np.random.default_rng(n * 1000 + d)
+    q, k = rows(rng, n, (hq, hkv), d, dtype, cuda, packed, 3.0)
+    qw = kw = None
+    if wtype is not None:
+        qw, kw = (torch.from_numpy(1 + 0.5 * rng.normal(size=d)).to(wtype).to(cuda)
+                  for _ in range(2))
+    pos = rng.integers(0, 1 << 20, n).astype(np.int32)
+    dpos = torch.from_numpy(pos).to(cuda)
+    freq, mag = ohr.frequencies(rot, 1e4, "yarn", 4, 4096) if rot else ([], 1.0)
+    rope = pkv.rotary(rot, frequencies=freq, magnitude=mag, interleaved=inter) if rot else None
+    qo, ko = pkv.qk_norm_rope(q, k, qw, kw, 1e-5, dpos, rope)
+    for at in (slice(0, 20), slice(n - 20, n)):
+        check(qo[at], q[at], qw, 1e-5, pos[at], freq, inter, mag, "q")
+        check(ko[at], k[at], kw, 1e-5, pos[at], freq, inter, mag, "k")
+    for at in range(0, n, 2000):
+        few = slice(at, min(at + 2000, n))
+        qf, kf = pkv.qk_norm_rope(q[few], k[few], qw, kw, 1e-5, dpos[few], rope)
+        assert torch.equal(qo[few], qf) and torch.equal(ko[few], kf)
+    # in place; the same weights for one of the two only
+    ref = pkv.qk_norm_rope(q, k, qw, None, 1e-5, dpos, rope) if qw is not None else (qo, ko)
+    got = pkv.qk_norm_rope(q, k, qw, None, 1e-5, dpos, rope, q_out=q, k_out=k)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,rot,inter", [(2048, 4, 1, 64, 64, False),
+                                                  (2300, 9, 3, 80, 20, False),
+                                                  (3333, 32, 8, 128, 128, True)])
+def test_many_tokens_into_the_cache(cuda, n, hq, hkv, d, rot, inter):
+    pkv = lib()
+    rng = np.random.default_rng(n)
+    q, k, v = rows(rng, n, (hq, hkv, hkv), d, BF, cuda, True)
+    w = torch.from_numpy(1 + 0.5 * rng.normal(size=d)).to(BF).to(cuda)
+    nb = n // 16 + 3
+    kc0 = torch.from_numpy(rng.normal(size=(nb, 16, hkv, d))).to(BF).to(cuda)
+    vc0 = -kc0
+    kc, vc = kc0.clone(), vc0.clone()
+    slots = rng.permutation(nb * 16)[:n].astype(np.int32)
+    slots[::7] = -1 - slots[::7]                       # padding
+    slots[5] = nb * 16                                 # outside
+    pos = torch.from_numpy(rng.integers(0, 100000, n).astype(np.int32)).to(cuda)
+    rope = pkv.rotary(rot, interleaved=inter, base=1e6)
+    qr, kr = pkv.qk_norm_rope(q, k, w, w, 1e-6, pos, rope)
+    st, ko = pkv.new_status(cuda), torch.empty_like(kr)
+    got = pkv.qk_norm_rope_kv_store(q, k, v, w, w, 1e-6, pos, rope, kc, vc,
+                                    torch.from_numpy(slots).to(cuda), k_out=ko, status=st)
+    assert status_word(st) == pkv.STATUS["SLOT_OUT_OF_RANGE"]
+    assert torch.equal(got, qr) and torch.equal(ko, kr)
+    slots[5] = -1
+    real = torch.from_numpy(np.flatnonzero(slots >= 0)).to(cuda)
+    to = torch.from_numpy(slots[slots >= 0].astype(np.int64)).to(cuda)
+    kc0.view(-1, hkv, d)[to], vc0.view(-1, hkv, d)[to] = kr[real], v[real]
+    assert np.array_equal(bits(kc), bits(kc0)) and np.array_equal(bits(vc), bits(vc0))
+
+
+def test_odd_values_of_many_tokens(cuda):
+    """Infinite and NaN entries stay in their rows, and in their entries without a norm."""
+    pkv = lib()
+    q = torch.ones(2200, 2, 64, device=cuda)
+    k = torch.ones(2200, 1, 64, device=cuda) * 2
+    q[7, 0, 3], q[8, 1, 5], q[9, 0, 17] = float("inf"), float("nan"), float("inf")
+    pos = torch.zeros(2200, dtype=torch.int32, device=cuda)
+    w = torch.ones(64, device=cuda)
+    qo, ko = pkv.qk_norm_rope(q, k, w, w, 0.0, pos, pkv.rotary(64))
+    odd = torch.zeros(2200, 2, dtype=torch.bool, device=cuda)
+    odd[7, 0] = odd[8, 1] = odd[9, 0] = True
+    assert torch.equal(qo.isnan().any(-1), odd) and (ko == 1).all() and (qo[~odd] == 1).all()
+    q[7, 0, 3] = q[8, 1, 5] = 1
+    for rot, inter in [(16, False), (16, True), (10, False), (10, True)]:
+        got, _ = pkv.qk_norm_rope(q, k, None, None, 0.0, pos, pkv.rotary(rot, interleaved=inter))
+        assert torch.equal(got, q)
