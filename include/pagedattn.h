@@ -694,7 +694,8 @@ PKV_API size_t pkv_paged_decode_shared_workspace_bytes(int32_t batch, int32_t nu
  * is used; a prefix < 0 or longer than max_context_len or the block table sets it
  * and counts as 0.  Keys in a block id outside the pool are left out.  A query
  * row whose scores are NaN or +inf gives NaN.  num_blocks*block_size must be below
- * 2^31 (PKV_ERR_UNSUPPORTED).
+ * 2^31 and max_context_len at most 2^30 (PKV_ERR_UNSUPPORTED; the workspace's size is
+ * 0 then).
  */
 PKV_API int pkv_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
                                     const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -59,6 +59,7 @@ constexpr uint32_t kColO = 384;
 constexpr float kRescaleThreshold = 8.0f;   // log2 of the tolerated growth of a maximum
 constexpr float kSumTrigger = 65536.0f;
 constexpr int kSms = 152;                // of a GB300: sizes follow from the arguments alone
+constexpr int kMaxContext = 1 << 30;     // keys beyond it would pass 32 bits at a tile's end
 
 // A run of keys for `seqs` sequences from b0 on, read through the table of sequence `table`
 // (own keys: one sequence, and its table).
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
         own = own < 10 ? own : 10;
         const int64_t sixteen = (work + 16 * kSms - 1) / (16 * kSms);
         own = own > sixteen ? own : sixteen;
-        if (own < 1) own = 1;
+        // (no run is longer than the longest there can be)
+        own = own < 1 ? 1 : own < kMaxContext / 8 ? own : kMaxContext / 8;
         const float own_cost = ((float)own_tiles * kOwnTile +
                                 ((float)own_tiles / (float)own + (float)sum[4]) * kItemCost) *
                                units;
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
         // never more parts than there is room for
         if (chosen * a.common_budget < (int64_t)sum[1])
             chosen = ((int64_t)sum[1] + a.common_budget - 1) / a.common_budget;
+        if (chosen > longest) chosen = longest;      // one run a group already
         if (tid == 0) {
             run_len[0] = (int32_t)chosen;
             run_len[1] = (int32_t)own;
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
                 r.seqs = min(a.tile_seqs, first + seqs - r.b0);
                 r.table = src;
                 r.key_lo = cut * common * a.tile_keys;
-                r.key_hi = min(keys, (cut + 1) * common * a.tile_keys);
+                r.key_hi = (cut + 1) * common >= all ? keys : (cut + 1) * common * a.tile_keys;
                 r.part = cut;
                 r.origin = r.key_lo;
                 // no member has keys: nobody's table to read
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
             r.b0 = r.table = b;
             r.seqs = 1;
             r.key_lo = i == 0 ? prefix : origin + i * own * a.tile_keys;
-            r.key_hi = min(ctx, origin + (i + 1) * own * a.tile_keys);
+            r.key_hi = (i + 1) * own >= all ? ctx : origin + (i + 1) * own * a.tile_keys;
             r.part = before + i;
             r.origin = origin + i * own * a.tile_keys;
             r.tiles = min(own, all - i * own);
@@ -1226,13 +1229,14 @@ bool layout(int32_t batch, int32_t num_q_heads, int32_t max_ctx, const pkv_cache
     // could be 8 kSms of tile_seqs sequences each, and one more for each sequence.  Neither
     // is more than the tiles there can be.
     const int64_t units = (int64_t)c.num_kv_heads * L.head_tiles;
+    if (max_ctx > kMaxContext) return false;
     const int64_t tiles = (int64_t)batch * (ceil_div(max_ctx, L.tile_keys) + 1);
     const int64_t own = (16 * kSms + units - 1) / units;
     const int64_t common = ((int64_t)L.tile_seqs * 8 * kSms + units - 1) / units;
     L.common_budget = (int32_t)(common < tiles ? common : tiles);
     if (L.common_budget < 1) L.common_budget = 1;
     const int64_t parts = L.common_budget + (own < tiles ? own : tiles) + 2 * (int64_t)batch + 2;
-    if (parts > (1 << 30) || parts * units > (1LL << 31)) return false;
+    if (parts > (1 << 30) || parts * units >= (1LL << 31)) return false;
     L.cap_parts = L.cap_records = (int32_t)parts;
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
     L.off_prefix = 256;

@@ -324,3 +324,28 @@ def test_waits_that_run_out_are_reported(cuda):
         assert status_word(st) & pkv.STATUS["WAIT_TIMEOUT"]
         got = pkv.paged_decode_run_shared(b.tq, b.tk, b.tv, b.tbt, b.scale, b.max_ctx, ws)
         assert torch.equal(got, ref)
+
+
+PLANS = {  # what the one CTA of the plan does in turns, and runs whose length has a bound
+    "1300 sequences": ([600, 700], [128, 70], 60, 2, 1, 64, 16),
+    "400 sequences": ([390, 10], [130, 256], 40, 2, 1, 64, 16),
+    "1160 groups": ([1] * 1100 + [2] * 60, [70] * 1160, 50, 2, 1, 64, 16),
+    "1160 groups, gathered": ([1] * 500 + [3] * 660, [70] * 1160, 30, 2, 1, 64, 5),
+    "long own keys": ([1, 2], [500, 100], [30000, 9000, 17000], 2, 1, 64, 16),
+    "many rows, no room for short runs": ([40], [6400], 30, 128, 1, 64, 128),
+    "two groups of more rows": ([13, 27], [3200, 5000], 30, 128, 1, 64, 64),
+}
+
+
+@pytest.mark.parametrize("name", PLANS)
+def test_plans(cuda, name):
+    pkv = lib()
+    sizes, prefixes, suffixes, hq, hkv, d, bs = PLANS[name]
+    if isinstance(suffixes, int):
+        suffixes = np.random.default_rng(1).integers(0, suffixes + 1, sum(sizes)).tolist()
+    b = Batch(sizes, prefixes, suffixes, hq, hkv, d, bs, cuda, seed=20)
+    st = pkv.new_status(cuda)
+    got = b.run(pkv, status=st)
+    assert status_word(st) == 0
+    b.check(got)
+    assert torch.equal(got, b.run(pkv))

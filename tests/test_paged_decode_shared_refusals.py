@@ -90,3 +90,15 @@ def test_binding():
         B.paged_decode_shared(q, cache, cache[:4], bt, ctx, None, None, 0.1, 64)
     with pytest.raises(ValueError, match="must be a CUDA tensor"):
         B.paged_decode_run_shared(q, cache, cache, bt, 0.1, 64, None)
+
+
+def test_contexts_beyond_2_30(lib):
+    f = lib.pkv_paged_decode_shared_workspace_bytes
+    d = _desc(hkv=1)
+    assert f(1, 1, 1 << 30, d) > 0
+    for n in ((1 << 30) + 1, 2**31 - 1):
+        assert f(1, 1, n, d) == 0
+        assert lib.pkv_paged_decode_plan_shared(OK, OK, OK, 1, 1, 1, n, 4, OK, BIG, d, None,
+                                                None) == -7
+        assert lib.pkv_paged_decode_run_shared(OK, OK, OK, OK, 4, 1, 1, n, 0.1, OK, OK, BIG, d,
+                                               None, None) == -7
