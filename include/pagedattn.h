@@ -655,8 +655,8 @@ PKV_API int pkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int
  * normed and rotated to their slots of k_cache (and to k_out unless it is
  * NULL, e.g. for pkv_paged_prefill_varlen), v rows [num_tokens, num_kv_heads,
  * head_dim], v_stride elements apart, to their slots of v_cache as they are.
- * slot_mapping as in pkv_kv_store; a token without a slot still gets its q_out
- * and k_out rows.  The caches must not overlap the other tensors.
+ * slot_mapping as in pkv_kv_store, but of tokens with the same slot the last
+ * one's rows are stored; a token without a slot still gets its q_out and k_out rows.  The caches must not overlap the other tensors.
  */
 PKV_API int pkv_qk_norm_rope_kv_store(
     const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

@@ -17,6 +17,14 @@ model and the sampler:
                         block and kv head
   apply_logit_rules     penalties, biases and allowed-token masks on logits
 
+and ahead of the cache, and for batches whose sequences share prompts:
+
+  rotary, qk_norm_rope, qk_norm_rope_kv_store
+                        RMS norm of q and k heads and the rotation of their
+                        positions, alone or with the store of k and v
+  paged_decode_shared   paged_decode with the keys that sequences have in common
+                        read and multiplied once for all of them
+
 PyTorch supplies device memory and streams only.  `workloads` draws the seeded
 synthetic inputs the tests and the benchmark use.
 """

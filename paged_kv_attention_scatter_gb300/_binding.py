@@ -1130,7 +1130,7 @@ def qk_norm_rope_kv_store(q, k, v, q_weight, k_weight, eps, positions, rope, k_c
                           stream=None) -> torch.Tensor:
     """qk_norm_rope of bf16 rows with its k rows, and v [T, Hkv, D] as it is, stored in
     the paged cache as kv_store stores them (slot_mapping [T] int32, negative =
-    skip).  Returns q_out; the k rows are also written to k_out when given (for
+    skip; of equal slots the last token's rows).  Returns q_out; the k rows are also written to k_out when given (for
     paged_prefill_varlen)."""
     f = load().pkv_qk_norm_rope_kv_store
     index, n, hq, hkv, d, qp, qs, kp, ks, qwp, kwp, wtype, pos, desc = _norm_rope_args(

@@ -33,6 +33,19 @@
 //   warp 5, 6  issue Q K^T into one of three S buffers, and P V (tcgen05.mma)
 // TMEM columns: S0 [0,128), S1 [128,256), S2 [256,384), O [384,384+D).
 //
+// What bounds it.  Own keys: the floor is their K and V rows once, but an item is a chain of
+// waits (Q, first K tile, S, softmax, P V, epilogue) of about 2.5 us behind its tiles, and a
+// tile costs one softmax warp about 1500 cycles, whatever few rows it has; with three items'
+// worth of buffers in flight 256 sequences of 1..1500 keys run at 6.2 TB/s (128 us), 64 of 4096
+// at 6.7.  Common keys: the softmax warps' pass over 128 x 128 scores, as in the prefill:
+// 1254 TFLOP/s for 1024 sequences on 8192 keys, 1202 for 32 of 64 heads on 65536.  Both sorts
+// together, 256 sequences with 8192 keys in common and up to 1500 of their own: 149 us, where the
+// bytes take 121 and paged_decode 1160.  The softmax threads hold 255 registers, so an SM has one
+// CTA and four softmax warps.  Forms that shorten an item by more instructions (own rows in
+// quarters, one warp after another; S^T with the keys in lanes) lost 5 to 20 %: of 64 KB of
+// code and more a tile's part no longer stays in the nearest instruction cache (55 KB here),
+// and producers of fewer instructions gained 4 to 10 % everywhere.
+//
 // Keys outside a tile's run and keys of a block id outside the pool have weight 0, and
 // their V rows are zeroed in shared memory, because unused cache slots may hold NaN.
 // Every wait is bounded, as in the other tensor-core kernels: a wait that gives up sets

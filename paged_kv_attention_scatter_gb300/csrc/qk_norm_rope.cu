@@ -43,6 +43,13 @@
 // so kManyTokens is 2048.  20 warps with four stages took 2% less for the first and 3% more
 // for the last; 24 and 32 warps spill and take longer; stages of 4 KB, three of them, alike.
 // Both kernels compute an entry by the same steps: a token's bits are the same in any batch.
+//
+// Equal slots.  Two tokens' rows in one slot could mix, 16 bytes of one and 16 of the other, so
+// that the last token of a slot is found first and alone stores.  head_kernel compares its
+// token's slot with those behind it; row_kernel puts its CTA's slots into a table in shared
+// memory, past which all slots go once, while the first rows arrive: 0.4 us of 512 tokens,
+// 2.7 of 16384 (the last line of the table above is without).  The slots that the table has
+// room for set the tokens of a launch, 150784 on 152 SMs.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -304,8 +311,14 @@ __global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
             }
         }
         if (base == 0) {
+            // of equal slots the last token's rows are stored
+            bool later = false;
+            if (kStore && slot >= 0)
+#pragma unroll 4
+                for (int32_t t = token + 1 + threadIdx.x; t < g.num_tokens; t += kThreads)
+                    later |= __ldg(g.slots + t) == slot;
             fill_tables(g, token, tab);
-            __syncthreads();
+            if (__syncthreads_or(later)) slot = -1;
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -419,14 +432,29 @@ struct WarpShared {
     float c[kMaxDim / 2], s[kMaxDim / 2];    // of the token's pairs
 };
 
+// The slots of a CTA's tokens and the last token of the call that has each: open addressing.
+constexpr int kSlotTable = 2048, kTokensPerCta = kSlotTable / 2 - 32;
+
 struct RowShared {
     float weight[2][kMaxDim];
     WarpShared warp[kWarps];
+    int32_t slot[kSlotTable], token[kSlotTable];
 };
+
+__device__ __forceinline__ int slot_hash(int32_t slot) {
+    static_assert(kSlotTable == 1 << 11, "the product's upper 11 bits");
+    return (int)((uint32_t)slot * 2654435769u >> 21);
+}
+
+// Where a slot is in the table, or its first free place.
+__device__ __forceinline__ int slot_place(const int32_t* table, int32_t slot) {
+    int at = slot_hash(slot);
+    while (table[at] != slot && table[at] >= 0) at = (at + 1) % kSlotTable;
+    return at;
+}
 
 struct Pieces {
     int32_t heads, of_q, of_k, per_token;    // heads of a piece; pieces of q, of k, of a token
-    int64_t units;                           // pieces of all tokens
 };
 
 __device__ __forceinline__ void async16(void* to, const void* from) {
@@ -471,6 +499,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
         const int which = i >= g.D, e = i - which * g.D;
         sh.weight[which][e] = weight_at(g, which, e);
     }
+    if (kStore)
+        for (int i = threadIdx.x; i < kSlotTable; i += kWarps * 32) sh.slot[i] = sh.token[i] = -1;
     __syncthreads();
     const int lane = threadIdx.x % 32, j = lane % kLanes, head = lane / kLanes;
     WarpShared& my = sh.warp[threadIdx.x / 32];
@@ -484,19 +514,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
     const int half = g.rotary_dim / 2;
 
     // this warp's run of pieces
-    const int64_t warps = (int64_t)gridDim.x * kWarps;
-    const int64_t w = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-    const int64_t first = p.units * w / warps, last = p.units * (w + 1) / warps;
-    if (first >= last) return;
-    const int32_t count = (int32_t)(last - first);
-    int32_t token = (int32_t)(first / p.per_token), at = (int32_t)(first % p.per_token);
-    int32_t next_token = token, next_at = at;                // the next piece to ask for
+    const int64_t warps = (int64_t)gridDim.x * kWarps, w0 = (int64_t)blockIdx.x * kWarps;
+    const int64_t w = w0 + threadIdx.x / 32, units = (int64_t)g.num_tokens * p.per_token;
+    const int64_t first = units * w / warps;
+    const int32_t count = (int32_t)(units * (w + 1) / warps - first);
+    struct Cursor {
+        int32_t token, at;
+    };
+    auto advance = [&](Cursor& c) {
+        if (++c.at == p.per_token) {
+            c.at = 0;
+            ++c.token;
+        }
+    };
+    Cursor now{(int32_t)(first / p.per_token), (int32_t)(first % p.per_token)};
+    Cursor next = now;                       // the piece at hand, the next to ask for
 
     auto ask = [&](int32_t i) {
         if (i < count) {
             Stage& st = my.stage[i % kStages];
-            const Piece pc = piece_at(g, p, next_at);
-            const T* from = (const T*)g.in[pc.which] + next_token * g.in_stride[pc.which] +
+            const Piece pc = piece_at(g, p, next.at);
+            const T* from = (const T*)g.in[pc.which] + next.token * g.in_stride[pc.which] +
                             (int64_t)pc.h0 * g.D;
             const int32_t vecs = pc.n * g.D * (int32_t)sizeof(T) / 16 - lane;
             const uint4* mine = (const uint4*)from + lane;
@@ -504,18 +542,53 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
             for (int v = 0; v < kPieceBytes / 16; v += 32)
                 if (v < vecs) async16(st.rows + lane + v, mine + v);
             if (lane == 0) {
-                if (kPartner != kNone) async4(&st.position, g.positions + next_token);
-                if (kStore) async4(&st.slot, g.slots + next_token);
+                if (kPartner != kNone) async4(&st.position, g.positions + next.token);
+                if (kStore) async4(&st.slot, g.slots + next.token);
             }
-            if (++next_at == p.per_token) {
-                next_at = 0;
-                ++next_token;
-            }
+            advance(next);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) ask(i);
+
+    if constexpr (kStore) {
+        // of equal slots the last token's rows are stored: the CTA's slots into the table, then
+        // all tokens past it
+        const int32_t t0 = (int32_t)(units * w0 / warps / p.per_token);
+        const int32_t t1 = (int32_t)((units * (w0 + kWarps) / warps + p.per_token - 1) /
+                                     p.per_token);
+        for (int32_t t = t0 + threadIdx.x; t < t1; t += kWarps * 32) {
+            const int32_t slot = __ldg(g.slots + t);
+            if (slot < 0) continue;
+            for (int at = slot_hash(slot);; at = (at + 1) % kSlotTable) {
+                const int32_t had = atomicCAS(&sh.slot[at], -1, slot);
+                if (had == -1 || had == slot) break;
+            }
+        }
+        __syncthreads();
+        constexpr int kBatchSlots = 8;
+        for (int32_t t = t0 + threadIdx.x; t < g.num_tokens; t += kBatchSlots * kWarps * 32) {
+            int32_t slot[kBatchSlots], at[kBatchSlots], key[kBatchSlots];
+#pragma unroll
+            for (int i = 0; i < kBatchSlots; ++i) {
+                const int32_t u = t + i * kWarps * 32;
+                slot[i] = u < g.num_tokens ? __ldg(g.slots + u) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatchSlots; ++i) {
+                at[i] = slot_hash(slot[i]);
+                key[i] = sh.slot[at[i]];
+            }
+#pragma unroll
+            for (int i = 0; i < kBatchSlots; ++i) {
+                if (slot[i] < 0 || key[i] < 0) continue;     // most are not this CTA's
+                const int place = slot_place(sh.slot, slot[i]);
+                if (sh.slot[place] == slot[i]) atomicMax(&sh.token[place], t + i * kWarps * 32);
+            }
+        }
+        __syncthreads();
+    }
 
     Pairs a0, a1, b0 = {}, b1 = {};                          // A and B of this lane's chunks
     int32_t have_token = -1, have = -1;                      // what c, s and A, B are of
@@ -524,7 +597,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
         __syncwarp();
         Stage& st = my.stage[i % kStages];
-        const Piece pc = piece_at(g, p, at);
+        const int32_t token = now.token;
+        const Piece pc = piece_at(g, p, now.at);
         int32_t slot = -1;
         if constexpr (kStore) {
             slot = st.slot;
@@ -532,6 +606,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
                 if (lane == 0) pkv::report(g.status, PKV_STATUS_SLOT_OUT_OF_RANGE);
                 slot = -1;
             }
+            if (slot >= 0 && sh.token[slot_place(sh.slot, slot)] != token) slot = -1;
         }
         if (kStore && pc.which == 2) {                       // v rows, as they are
             if (slot >= 0) {
@@ -706,10 +781,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
             }
         }
         __syncwarp();                                        // the stage is read
-        if (++at == p.per_token) {
-            at = 0;
-            ++token;
-        }
+        advance(now);
     }
 }
 
@@ -718,21 +790,36 @@ int launch(const HeadArgs& g, cudaStream_t s) {
     if (g.num_tokens < kManyTokens) {
         head_kernel<T, kLanes, kPartner, kStore><<<(unsigned)g.num_tokens, kThreads, 0, s>>>(g);
     } else {
+        static std::atomic<uint64_t> done{0};
+        if (!pkv_dynamic_smem_once((const void*)row_kernel<T, kLanes, kPartner, kStore>,
+                                   (int)sizeof(RowShared), done))
+            return PKV_ERR_CUDA;
         constexpr int kHeads = 32 / kLanes;
         Pieces p;
         p.heads = kPieceBytes / (g.D * (int)sizeof(T)) / kHeads * kHeads;
         p.of_q = (g.Hq + p.heads - 1) / p.heads;
         p.of_k = (g.Hkv + p.heads - 1) / p.heads;
         p.per_token = p.of_q + p.of_k * (kStore ? 2 : 1);
-        p.units = (int64_t)p.per_token * g.num_tokens;
-        static std::atomic<uint64_t> done{0};
-        if (!pkv_dynamic_smem_once((const void*)row_kernel<T, kLanes, kPartner, kStore>,
-                                   (int)sizeof(RowShared), done))
-            return PKV_ERR_CUDA;
-        int64_t grid = (p.units + kWarps - 1) / kWarps;
-        if (grid > pkv_num_sms()) grid = pkv_num_sms();
-        row_kernel<T, kLanes, kPartner, kStore>
-            <<<(unsigned)grid, kWarps * 32, sizeof(RowShared), s>>>(g, p);
+        // as many tokens a launch as the table of slots has room for: later launches, with
+        // later tokens, write later
+        const int32_t room = pkv_num_sms() * (kStore ? kTokensPerCta : 1 << 22);
+        HeadArgs part = g;
+        for (int32_t from = 0; from < g.num_tokens;) {
+            part.num_tokens = g.num_tokens - from < room ? g.num_tokens - from : room;
+            const int64_t units = (int64_t)p.per_token * part.num_tokens;
+            int64_t grid = (units + kWarps - 1) / kWarps;
+            if (grid > pkv_num_sms()) grid = pkv_num_sms();
+            row_kernel<T, kLanes, kPartner, kStore>
+                <<<(unsigned)grid, kWarps * 32, sizeof(RowShared), s>>>(part, p);
+            from += part.num_tokens;
+            for (int i = 0; i < 3; ++i)
+                if (g.in[i])
+                    part.in[i] = (const T*)g.in[i] + (int64_t)from * g.in_stride[i];
+            for (int i = 0; i < 2; ++i)
+                if (g.out[i]) part.out[i] = (T*)g.out[i] + (int64_t)from * g.out_stride[i];
+            if (g.positions) part.positions = g.positions + from;
+            if (g.slots) part.slots = g.slots + from;
+        }
     }
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

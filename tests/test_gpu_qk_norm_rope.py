@@ -330,3 +330,33 @@ def test_odd_values_of_many_tokens(cuda):
     for rot, inter in [(16, False), (16, True), (10, False), (10, True)]:
         got, _ = pkv.qk_norm_rope(q, k, None, None, 0.0, pos, pkv.rotary(rot, interleaved=inter))
         assert torch.equal(got, q)
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,slots", [(2, 2, 1, 64, 1), (300, 4, 2, 64, 40),
+                                              (2047, 2, 1, 128, 900), (2048, 2, 1, 64, 3),
+                                              (5001, 9, 3, 80, 4000), (20000, 4, 2, 64, 15000),
+                                              (160001, 1, 1, 8, 120000)])
+def test_the_last_of_equal_slots_is_stored(cuda, n, hq, hkv, d, slots):
+    """Whatever runs first: of one launch, and of the several that very many tokens take."""
+    pkv = lib()
+    rng = np.random.default_rng(n)
+    q, k, v = rows(rng, n, (hq, hkv, hkv), d, BF, cuda, True)
+    nb = -(-slots // 16)
+    kc0 = torch.from_numpy(rng.normal(size=(nb, 16, hkv, d))).to(BF).to(cuda)
+    kc, vc = kc0.clone(), kc0.clone()
+    to = rng.integers(0, slots, n).astype(np.int32)
+    to[rng.random(n) < 0.1] = -5                       # padding
+    pos = torch.from_numpy(rng.integers(0, 100000, n).astype(np.int32)).to(cuda)
+    rope = pkv.rotary(d)
+    qr, kr = pkv.qk_norm_rope(q, k, None, None, 0.0, pos, rope)
+    st = pkv.new_status(cuda)
+    got = pkv.qk_norm_rope_kv_store(q, k, v, None, None, 0.0, pos, rope, kc, vc,
+                                    torch.from_numpy(to).to(cuda), status=st)
+    assert status_word(st) == 0 and torch.equal(got, qr)
+    last = np.full(nb * 16, -1)
+    last[to[to >= 0]] = np.flatnonzero(to >= 0)        # assignments in order: the last stays
+    have = torch.from_numpy(np.flatnonzero(last >= 0)).to(cuda)
+    src = torch.from_numpy(last[last >= 0]).to(cuda)
+    kw, vw = kc0.clone(), kc0.clone()
+    kw.view(-1, hkv, d)[have], vw.view(-1, hkv, d)[have] = kr[src], v[src]
+    assert np.array_equal(bits(kc), bits(kw)) and np.array_equal(bits(vc), bits(vw))
