@@ -53,7 +53,10 @@ Functions and their pins (all pins are tests under ``tests/`` marked not-gpu):
       once) on tiny pools.
   logit_rules.apply
       pinned to values worked out by hand.
+  head_rotation.frequencies, head_rotation.norm_rope
+      pinned to exact values and identities of the rotation and the norm, and
+      to the frequencies' limits by each scaling.
 
 Every function is pinned.
 """
-from . import attention, fp8_cache, kv_store, logit_rules, sampler, slots  # noqa: F401
+from . import attention, fp8_cache, head_rotation, kv_store, logit_rules, sampler, slots  # noqa: F401
