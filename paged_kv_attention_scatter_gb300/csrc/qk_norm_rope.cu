@@ -31,25 +31,26 @@
 //
 // row_kernel, for many: an SM's 16 warps each work through a run of pieces (some heads of a
 // token), with A and B in registers, made once for a token's q and once for its k, and rows
-// that arrive through shared memory four pieces ahead.  head_kernel reads A and B from
+// that arrive through shared memory two pieces of 4 KB ahead.  head_kernel reads A and B from
 // shared memory for every head and waits for its token's angles before any row: it is bound
 // by those reads and by the wait.  Behind row_kernel stands the issue of its instructions
-// and, at 5.7 TB/s, the memory.  head / row kernel, us:
-//   tokens                                      1024        2048        4096        16384
-//   24 heads of 80, 32 bits, partial rotation    7.7/8.4   12.7/10.8   22.6/17.6   83.9/58.2
-//   40 of 128, 16 bits, pairs, half rotated      6.5/7.1    9.2/10.1   17.1/16.1   63.6/59.3
-//   24 of 128, bf16, all rotated                 5.6/6.1    8.0/7.8    13.4/12.0   47.4/39.8
-//   48 of 128, bf16, into the cache              7.8/7.7   11.9/11.3   20.6/20.3   78.5/69.8
-// so kManyTokens is 2048.  20 warps with four stages took 2% less for the first and 3% more
-// for the last; 24 and 32 warps spill and take longer; stages of 4 KB, three of them, alike.
+// (0.5 to 0.6 of it) and, at 5.6 TB/s, the memory.  head / row kernel, us:
+//   tokens                                        2048        4096        16384
+//   24 heads of 80, 32 bits, partial rotation   12.7/9.3    22.6/14.9   83.9/50.5
+//   40 of 128, 16 bits, pairs, half rotated      9.2/9.6    17.1/15.5   63.6/61.7
+//   24 of 128, bf16, all rotated                 8.0/7.4    13.4/11.8   47.4/39.5
+//   48 of 128, bf16, into the cache             11.9/12.4   20.6/20.5   78.5/72.7
+// so kManyTokens is 2048.  Five stages of 2 KB take 1.6% less for the last and 2 to 8% more for
+// the others at 2048 and 4096 tokens; 20 warps with smaller stages 3% more for the last; 24 and
+// 32 warps spill.
 // Both kernels compute an entry by the same steps: a token's bits are the same in any batch.
 //
 // Equal slots.  Two tokens' rows in one slot could mix, 16 bytes of one and 16 of the other, so
 // that the last token of a slot is found first and alone stores.  head_kernel compares its
 // token's slot with those behind it; row_kernel puts its CTA's slots into a table in shared
 // memory, past which all slots go once, while the first rows arrive: 0.4 us of 512 tokens,
-// 2.7 of 16384 (the last line of the table above is without).  The slots that the table has
-// room for set the tokens of a launch, 150784 on 152 SMs.
+// 2.7 of 16384 (in the table above row_kernel's column is with it, head_kernel's without).
+// The slots that the table has room for set the tokens of a launch, 150784 on 152 SMs.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
 // token's q, k or v.
 // ---------------------------------------------------------------------------
 // A piece holds a pass's heads at least: 2 heads of 256 in 32 bits are 2 KB.
-constexpr int kWarps = 16, kStages = 5, kPieceBytes = 2048;
+constexpr int kWarps = 16, kStages = 3, kPieceBytes = 4096;
 
 struct Stage {
     uint4 rows[kPieceBytes / 16];
@@ -670,7 +671,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
                         a *= my.c[t];
                         b = e < half ? -weight[e + half] * my.s[t] : weight[t] * my.s[t];
                     };
+                    auto quads = [&](int e, Pairs& ta, Pairs& tb) {
+#pragma unroll
+                        for (int t = 0; t < 4; t += 2, e += 4) {
+                            tb.v[t] = tb.v[t + 1] = 0;
+                            if (e >= g.rotary_dim) continue;
+                            const bool second = e >= half;
+                            const int at = second ? e - half : e;
+                            const float sign = second ? 1.f : -1.f;
+                            uint64_t c0, c1, s0, s1, o0, o1;
+                            four(my.c + at, c0, c1);
+                            four(my.s + at, s0, s1);
+                            four(weight + (second ? at : e + half), o0, o1);
+                            tb.v[t] = mul2(mul2(o0, pk2(sign, sign)), s0);
+                            tb.v[t + 1] = mul2(mul2(o1, pk2(sign, sign)), s1);
+                            ta.v[t] = mul2(ta.v[t], c0);
+                            ta.v[t + 1] = mul2(ta.v[t + 1], c1);
+                        }
+                    };
                     auto chunk = [&](int e, Pairs& ta, Pairs& tb) {
+                        if (half % 4 == 0) return quads(e, ta, tb);
 #pragma unroll
                         for (int t = 0; t < 4; ++t, e += 2) {
                             float2 a = up2(ta.v[t]);
