@@ -26,8 +26,9 @@
 //
 // head_kernel, for few tokens: a CTA takes one token, all of its heads at once, and builds
 // the tables while the rows' loads are in flight.  One token of 24 heads takes 2.4 us, an
-// empty kernel about as long.  192 threads with two heads each in flight; 128 threads took
-// 8% longer for 8191 tokens of 24 heads in 32 bits, the tables built by half of the threads 15%.
+// empty kernel about as long.  192 threads with two heads each in flight (in 32 bits one: 2047
+// tokens of 24 heads of 80 11.4 us for 12.7), six CTAs an SM (seven spill: up to 30% longer); 128
+// threads took 8% longer for 8191 such tokens, the tables built by half of the threads 15%.
 //
 // row_kernel, for many: an SM's 16 warps each work through a run of pieces (some heads of a
 // token), with A and B in registers, made once for a token's q and once for its k, and rows
@@ -36,7 +37,7 @@
 // by those reads and by the wait.  Behind row_kernel stands the issue of its instructions
 // (0.5 to 0.6 of it) and, at 5.6 TB/s, the memory.  head / row kernel, us:
 //   tokens                                        2048        4096        16384
-//   24 heads of 80, 32 bits, partial rotation   12.7/9.3    22.6/14.9   83.9/50.5
+//   24 heads of 80, 32 bits, partial rotation   11.4/9.3    22.6/14.9   83.9/50.5
 //   40 of 128, 16 bits, pairs, half rotated      9.2/9.6    17.1/15.5   63.6/61.7
 //   24 of 128, bf16, all rotated                 8.0/7.4    13.4/11.8   47.4/39.5
 //   48 of 128, bf16, into the cache             11.9/12.4   20.6/20.5   78.5/72.7
@@ -59,7 +60,8 @@
 namespace {
 
 constexpr int kThreads = 192;
-constexpr int kBatch = 2;                    // heads a lane has in flight
+template <typename T>
+constexpr int kBatchOf = sizeof(T) == 4 ? 1 : 2;   // heads a lane of head_kernel has in flight
 constexpr int kMaxDim = 256;
 constexpr int kManyTokens = 2048;            // from here on, row_kernel
 
@@ -270,8 +272,9 @@ __device__ __forceinline__ Pairs turned(const float* a, const float* b, const Pa
 // kLanes: lanes of a head (16 kLanes >= D), each with two chunks of eight entries.
 // kStore: k and v rows go into the cache.
 template <typename T, int kLanes, Partner kPartner, bool kStore>
-__global__ void __launch_bounds__(kThreads) head_kernel(const HeadArgs g) {
+__global__ void __launch_bounds__(kThreads, 6) head_kernel(const HeadArgs g) {
     constexpr int kHeads = kThreads / kLanes;            // heads of a pass
+    constexpr int kBatch = kBatchOf<T>;
     __shared__ __align__(16) Tables tab;
     // a pass's rows as fp32, for partners that lie across chunks
     __shared__ __align__(16) float rows[kPartner == kShared ? kThreads * 16 : 1];

@@ -349,3 +349,24 @@ def test_plans(cuda, name):
     assert status_word(st) == 0
     b.check(got)
     assert torch.equal(got, b.run(pkv))
+
+
+def test_nothing_to_attend_and_empty_groups(cuda):
+    pkv = lib()
+    b = Batch([3], [100], [20, 0, 7], 4, 2, 64, 16, cuda, seed=30)
+    zero = torch.zeros(3, dtype=torch.int32, device=cuda)
+    st = pkv.new_status(cuda)
+    for max_len in (0, b.max_ctx):
+        got = pkv.paged_decode_shared(b.tq, b.tk, b.tv, b.tbt, zero, b.toff, zero[:1], b.scale,
+                                      max_len, status=st)
+        assert (got == 0).all() and status_word(st) == 0
+    e = pkv.paged_decode_shared(b.tq[:0], b.tk, b.tv, b.tbt[:0], b.tctx[:0], b.toff[:1],
+                                b.tpre[:0], b.scale, b.max_ctx, status=st)
+    assert e.shape == (0, 4, 64)
+    # groups without sequences, a group of one, the rest without a group
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda)  # noqa: E731
+    for off, pre in ((i(0, 0, 3, 3), i(50, 100, 7)), (i(0, 0, 1, 1), i(9, 100, 120)),
+                     (i(3, 3), i(100)), (i(1, 3), i(100))):
+        b.check(pkv.paged_decode_shared(b.tq, b.tk, b.tv, b.tbt, b.tctx, off, pre, b.scale,
+                                        b.max_ctx, status=st))
+        assert status_word(st) == 0
