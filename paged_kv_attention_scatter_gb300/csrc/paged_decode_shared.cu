@@ -82,6 +82,16 @@ struct Record {
     int32_t origin, tiles;               // its tiles' first key; how many there are
 };
 
+// Division of 0 <= x < 2^31 by a d that the host knows: x m >> s with m = ceil(2^s / d) and
+// s = 31 + ceil(log2 d), where m d - 2^s < d <= 2^(s - 31) makes the quotient exact.
+struct Divisor {
+    uint32_t m;
+    int32_t s;
+    __device__ __forceinline__ int32_t of(int32_t x) const {
+        return (int32_t)(((uint64_t)(uint32_t)x * m) >> s);
+    }
+};
+
 struct SharedArgs {
     const __nv_bfloat16* q;
     const __nv_bfloat16* kc;
@@ -108,6 +118,7 @@ struct SharedArgs {
     const int32_t* offsets;
     const int32_t* prefix;
     int32_t groups;
+    Divisor by_box, by_tile, by_seqs;    // box, tile_keys, tile_seqs
 };
 
 __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) {
@@ -165,11 +176,27 @@ struct Groups {
 
 // The first key tile of a run begins at a box of the cache block that key_lo lies in.
 __device__ __forceinline__ int32_t tile_origin(const SharedArgs& a, int32_t key_lo) {
-    return key_lo / a.box * a.box;
+    return a.by_box.of(key_lo) * a.box;
 }
 __device__ __forceinline__ int32_t key_tiles(const SharedArgs& a, int32_t lo, int32_t hi) {
-    return hi > lo ? ceil_div(hi - tile_origin(a, lo), a.tile_keys) : 0;
+    return hi > lo ? a.by_tile.of(hi - tile_origin(a, lo) + a.tile_keys - 1) : 0;
 }
+__device__ __forceinline__ int32_t row_tiles(const SharedArgs& a, int32_t seqs) {
+    return a.by_seqs.of(seqs + a.tile_seqs - 1);
+}
+
+// Division of tile counts, 0 <= x <= 2^24, by a run length d <= 2^24: x + d - 1 and 1 / d are
+// off by 2^-24 of themselves at most, the quotient by one then.
+struct RunLength {
+    int32_t d;
+    float r;
+    __device__ __forceinline__ explicit RunLength(int32_t n) : d(n), r(1.f / n) {}
+    __device__ __forceinline__ int32_t runs(int32_t x) const {
+        const int32_t y = x + d - 1;
+        const int32_t q = __float2int_rz(__int2float_rn(y) * r), rest = y - q * d;
+        return q + (rest >= d) - (rest < 0);
+    }
+};
 
 // Block-wide exclusive prefix of v, over `carry` (updated to the sum).
 __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t& carry, int64_t* scratch) {
@@ -197,9 +224,10 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t& carry, int64
 }
 
 // One CTA of a thread a sequence, within 256 and kMaxPlanThreads (for small batches more threads
-// cost time: 64 sequences 6.4 us with 256, 8.2 with 1024).  What a thread finds out of its first
-// sequence stays in registers; larger batches go over theirs again.  Loops are not unrolled: a
-// kernel that runs once pays for fetching its instructions (86 KB of them: 16 us).
+// cost time: 64 sequences 6.4 us with 256, 8.2 with 1024, in an earlier form).  What a thread finds
+// out of its first sequence stays in registers; larger batches go over theirs again.  Loops are
+// not unrolled, divisions few and by products: a kernel that runs once pays for fetching its
+// instructions (86 KB of them 16 us, 54 KB 7.0, 39 KB 5.5; two sequences as many as 64).
 __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
     pkv::allow_dependent_launch();
     __shared__ int64_t scratch[32];
@@ -255,7 +283,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
         int64_t t0 = 0, t1 = 0;              // these may pass 32 bits when added up
         int32_t n = 0;
         if (x.keys > 0) {
-            tiles = ceil_div(x.seqs, a.tile_seqs);
+            tiles = row_tiles(a, x.seqs);
             n = key_tiles(a, 0, x.keys);
             atomicMax(&longest, n);
             if (!staged) a.table[x.first] = INT32_MAX;
@@ -319,43 +347,45 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
 
     // ---- run lengths
     if (tid < 32) {
+        // (rounded up a little, so that 32 bits never give a run less than its share)
         const float common_tiles = (float)sum[0], members = (float)sum[1];
-        const int64_t own_tiles = (int64_t)sum[2];
+        const float own_tiles = (float)sum[2], work = own_tiles * units * (1 + 0x1p-20f);
         // own runs: an item's start and end cost as much as three tiles, so two items an SM up
-        // to ten tiles each, then up to sixteen items
-        const int64_t work = own_tiles * units;
-        int64_t own = (work + 2 * kSms - 1) / (2 * kSms);
-        own = own < 10 ? own : 10;
-        const int64_t sixteen = (work + 16 * kSms - 1) / (16 * kSms);
-        own = own > sixteen ? own : sixteen;
-        // (no run is longer than the longest there can be)
-        own = own < 1 ? 1 : own < kMaxContext / 8 ? own : kMaxContext / 8;
-        const float own_cost = ((float)own_tiles * kOwnTile +
-                                ((float)own_tiles / (float)own + (float)sum[4]) * kItemCost) *
+        // to ten tiles each, then up to sixteen items (and no run longer than there can be)
+        const float own_share = fmaxf(fminf(ceilf(work * (1.f / (2 * kSms))), 10.f),
+                                      ceilf(work * (1.f / (16 * kSms))));
+        const int32_t own = (int32_t)fminf(fmaxf(own_share, 1.f), kMaxContext / 64);
+        const float own_cost = (own_tiles * kOwnTile +
+                                (__fdividef(own_tiles, (float)own) + (float)sum[4]) * kItemCost) *
                                units;
         // a lane weighs two lengths: the longest prefix in so many runs, or in 1, 2, 3, ... tiles
         float best = INFINITY;
-        int64_t chosen = 1;
+        int32_t chosen = 1;
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
-            const int32_t len = k == 0 ? ceil_div(longest, lane + 1) : lane < 8 ? lane + 1 : 2 * lane - 6;
-            float items = common_tiles / len + 0.5f * (float)sum[3];
+            const int32_t len =
+                k == 0 ? max(1, (int32_t)__fdividef((float)(longest + lane), lane + 1.f))
+                       : lane < 8 ? lane + 1 : 2 * lane - 6;
+            const float rcp = __fdividef(1.f, (float)len);
+            float items = common_tiles * rcp + 0.5f * (float)sum[3];
             if (groups <= kFew) {
                 int32_t count = 0;
 #pragma unroll 1
-                for (int32_t g = 0; g < groups; ++g) count += few[g].x * ceil_div(few[g].y, len);
+                for (int32_t g = 0; g < groups; ++g)
+                    count += few[g].x * (int32_t)((float)(few[g].y + len - 1) * rcp + 1e-3f);
                 items = (float)count;
             }
             items *= units;
             const float item = len * kCommonTile + kItemCost;
             // no CTA idle; and the last common run, which is drawn after three quarters of the
             // own ones and what goes beside them
-            const float all = items * item, beside = all / (all + own_cost + 1.f) * own_cost;
-            float cost = fmaxf((all + own_cost) / kSms, 0.75f * (own_cost + beside) / kSms +
-                                                            ceilf(items / kSms) * item);
+            const float all = items * item, beside = __fdividef(all, all + own_cost + 1.f) * own_cost;
+            constexpr float kEach = 1.f / kSms;
+            float cost = fmaxf((all + own_cost) * kEach, 0.75f * (own_cost + beside) * kEach +
+                                                             ceilf(items * kEach) * item);
             // parts: written once, read once, by all rows
-            cost += members / len * a.Hq * a.D * 4 / kPartBytes;
-            if (cost < best && members / len <= (float)a.common_budget) {
+            cost += members * rcp * a.Hq * a.D * (4 / kPartBytes);
+            if (cost < best && members * rcp <= (float)a.common_budget) {
                 best = cost;
                 chosen = len;
             }
@@ -363,26 +393,25 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
         const float least = __uint_as_float(__reduce_min_sync(~0u, __float_as_uint(best)));
         chosen = __shfl_sync(~0u, chosen, __ffs(__ballot_sync(~0u, best == least)) - 1);
         // never more parts than there is room for
-        if (chosen * a.common_budget < (int64_t)sum[1])
-            chosen = ((int64_t)sum[1] + a.common_budget - 1) / a.common_budget;
-        if (chosen > longest) chosen = longest;      // one run a group already
+        const float least_len = ceilf(__fdividef(members, (float)a.common_budget) * (1 + 0x1p-20f));
+        chosen = max(chosen, (int32_t)fminf(least_len, (float)longest));
+        chosen = max(1, min(chosen, longest));       // one run a group at most
         if (tid == 0) {
-            run_len[0] = (int32_t)chosen;
-            run_len[1] = (int32_t)own;
+            run_len[0] = chosen;
+            run_len[1] = own;
         }
     }
     __syncthreads();
     const int32_t common = run_len[0], own = run_len[1];
+    const RunLength by_common(common), by_own(own);
 
     // ---- places: each group's first record; each sequence's first part and first record
     auto records_of = [&](const Group& x) {
-        return x.keys > 0 ? ceil_div(x.seqs, a.tile_seqs) *
-                                ceil_div(key_tiles(a, 0, x.keys), common)
-                          : 0;
+        return x.keys > 0 ? row_tiles(a, x.seqs) * by_common.runs(key_tiles(a, 0, x.keys)) : 0;
     };
     auto places_of = [&](const Sequence& s) {
-        const int32_t n = ceil_div(key_tiles(a, s.prefix, s.ctx), own);
-        return (int64_t)(n + ceil_div(key_tiles(a, 0, s.prefix), common)) << 32 | n;
+        const int32_t n = by_own.runs(key_tiles(a, s.prefix, s.ctx));
+        return (int64_t)(n + by_common.runs(key_tiles(a, 0, s.prefix))) << 32 | n;
     };
     int64_t common_total = 0, total = 0, my_common = 0, my_place = 0;
     int64_t common_after = 0, after = 0;     // those of the first round
@@ -438,7 +467,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
             const int32_t keys = __shfl_sync(~0u, x.keys, o), count = __shfl_sync(~0u, n, o);
             const int32_t at0 = (int32_t)__shfl_sync(~0u, place, o);
             const int32_t src = __shfl_sync(~0u, from, o);
-            const int32_t tiles = ceil_div(seqs, a.tile_seqs), all = key_tiles(a, 0, keys);
+            const int32_t tiles = row_tiles(a, seqs), all = key_tiles(a, 0, keys);
 #pragma unroll 1
             for (int32_t i = lane; i < count; i += 32) {
                 const int32_t cut = i / tiles, tile = i - cut * tiles;
@@ -463,37 +492,42 @@ __global__ void __launch_bounds__(kMaxPlanThreads) plan_kernel(SharedArgs a) {
         const Sequence s = noted(b);
         const int64_t place = base == 0 ? my_place : block_prefix(places_of(s), after, scratch);
         if (b < a.B) a.part_prefix[b] = (int32_t)(place >> 32);
-        const int32_t all = key_tiles(a, s.prefix, s.ctx), n = ceil_div(all, own);
-        const int32_t before = ceil_div(key_tiles(a, 0, s.prefix), common);
+        const int32_t all = key_tiles(a, s.prefix, s.ctx), n = by_own.runs(all);
+        const int32_t before = by_common.runs(key_tiles(a, 0, s.prefix));
         const int32_t origin = tile_origin(a, s.prefix);
-        auto put = [&](int32_t i, int32_t b, int32_t ctx, int32_t prefix, int32_t origin,
-                       int32_t before, int32_t all, int32_t j) {
-            Record r{};
-            r.b0 = r.table = b;
-            r.seqs = 1;
-            r.key_lo = i == 0 ? prefix : origin + i * own * a.tile_keys;
-            r.key_hi = (i + 1) * own >= all ? ctx : origin + (i + 1) * own * a.tile_keys;
-            r.part = before + i;
-            r.origin = origin + i * own * a.tile_keys;
-            r.tiles = min(own, all - i * own);
-            j += i;
-            a.records[j + min(j / stride + 1, n_common)] = r;
-        };
-        const bool few = n <= 8;
+        // a sequence of up to eight records is written by its thread, then each of the others by
+        // the warp together
+        uint32_t left = __ballot_sync(~0u, n > 8);
+        int32_t owner = b, ctx = s.ctx, lo = s.prefix, from = origin, part = before, tiles = all;
+        int32_t at = (int32_t)place, i = 0, step = 1, count = n > 8 ? 0 : n;
 #pragma unroll 1
-        for (int32_t i = 0; few && i < n; ++i)
-            put(i, b, s.ctx, s.prefix, origin, before, all, (int32_t)place);
+        for (;;) {
 #pragma unroll 1
-        for (uint32_t left = __ballot_sync(~0u, !few); left; left &= left - 1) {
+            for (; i < count; i += step) {
+                Record r{};
+                r.b0 = r.table = owner;
+                r.seqs = 1;
+                r.origin = from + i * own * a.tile_keys;
+                r.key_lo = i == 0 ? lo : r.origin;
+                r.key_hi = (i + 1) * own >= tiles ? ctx : r.origin + own * a.tile_keys;
+                r.part = part + i;
+                r.tiles = min(own, tiles - i * own);
+                const int32_t j = at + i;
+                a.records[j + min(j / stride + 1, n_common)] = r;
+            }
+            if (left == 0) break;
             const int o = __ffs(left) - 1;
-            const int32_t ctx = __shfl_sync(~0u, s.ctx, o), prefix = __shfl_sync(~0u, s.prefix, o);
-            const int32_t from = __shfl_sync(~0u, origin, o), part = __shfl_sync(~0u, before, o);
-            const int32_t at = __shfl_sync(~0u, (int32_t)place, o);
-            const int32_t count = __shfl_sync(~0u, n, o), owner = __shfl_sync(~0u, b, o);
-            const int32_t tiles = __shfl_sync(~0u, all, o);
-#pragma unroll 1
-            for (int32_t i = lane; i < count; i += 32)
-                put(i, owner, ctx, prefix, from, part, tiles, at);
+            left &= left - 1;
+            owner = __shfl_sync(~0u, b, o);
+            ctx = __shfl_sync(~0u, s.ctx, o);
+            lo = __shfl_sync(~0u, s.prefix, o);
+            from = __shfl_sync(~0u, origin, o);
+            part = __shfl_sync(~0u, before, o);
+            tiles = __shfl_sync(~0u, all, o);
+            at = __shfl_sync(~0u, (int32_t)place, o);
+            count = __shfl_sync(~0u, n, o);
+            i = lane;
+            step = 32;
         }
     }
 }
@@ -1310,6 +1344,14 @@ int make_plan(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
     a.common_budget = L.common_budget;
     a.status = status;
     a.wait_polls = pkv_wait_polls();
+    auto divisor = [](int32_t d) {
+        int32_t l = 0;
+        while ((1 << l) < d) ++l;
+        return Divisor{(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+    };
+    a.by_box = divisor(a.box);
+    a.by_tile = divisor(a.tile_keys);
+    a.by_seqs = divisor(a.tile_seqs);
     return PKV_OK;
 }
 
