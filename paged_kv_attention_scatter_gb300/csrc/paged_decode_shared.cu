@@ -1308,10 +1308,11 @@ int make_plan(int32_t batch, int32_t num_q_heads, int32_t max_context_len,
     if (num_q_heads % cache.num_kv_heads != 0) return PKV_ERR_BAD_DIMENSION;
     if (cache.head_dim != 64 && cache.head_dim != 128) return PKV_ERR_UNSUPPORTED_HEAD_DIM;
     if ((int64_t)cache.num_blocks * cache.block_size >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
-    if (!workspace) return PKV_ERR_NULL_POINTER;
-    if ((uintptr_t)workspace & 15) return PKV_ERR_MISALIGNED;
+    // (first, for there is no workspace of such sizes: the query gives 0)
     Layout L;
     if (!layout(batch, num_q_heads, max_context_len, cache, L)) return PKV_ERR_UNSUPPORTED;
+    if (!workspace) return PKV_ERR_NULL_POINTER;
+    if ((uintptr_t)workspace & 15) return PKV_ERR_MISALIGNED;
     if (workspace_bytes < L.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
     char* ws = (char*)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
     a = SharedArgs{};
