@@ -71,6 +71,12 @@ constexpr int kMaskRing = 8;             // more tiles than are between producer
 constexpr uint32_t kColO = 384;
 constexpr float kRescaleThreshold = 8.0f;   // log2 of the tolerated growth of a maximum
 constexpr float kSumTrigger = 65536.0f;
+// A row whose maximum score is so far from zero (base 2) takes its scores in units of a power of
+// two instead of the scale.  S scale - m in one step differs for the maximum itself by what m was
+// rounded by, half its last place: 32 below 2^30, but 128 at 2^31, so that all weights would
+// be infinite or 0.  With a power of two nothing is rounded, and the weights stay what they
+// are: different scores in 32 bits lie 2^30 2^-24 = 64 and more apart (32 below a power of two).
+constexpr float kFarScore = 1073741824.0f;
 constexpr int kSms = 152;                // of a GB300: sizes follow from the arguments alone
 constexpr int kMaxContext = 1 << 30;     // keys beyond it would pass 32 bits at a tile's end
 
@@ -111,6 +117,7 @@ struct SharedArgs {
     int32_t tile_heads, head_tiles, tile_seqs;
     int32_t cap_records, cap_parts, common_budget;
     float scale_log2;
+    float far_unit;                      // the power of two at or below it (see kFarScore)
     uint32_t* status;
     uint32_t wait_polls;
     // the plan's
@@ -1022,6 +1029,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = tid;                                 // row = TMEM lane
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const int32_t my_seq = i / a.tile_heads, my_head = i - my_seq * a.tile_heads;
+        // a maximum in units of either kind as a score
+        auto in_log2 = [&](float m, float unit) {
+            return unit == a.scale_log2 ? m : m * (a.scale_log2 / unit);
+        };
         uint32_t T = 0;
         bool ok = true;
         for (uint32_t I = 0; ok; ++I) {
@@ -1035,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t b = x.b0 + my_seq;
             const int32_t first = mine ? a.part_prefix[b] : 0;
             const int32_t parts = mine ? a.part_prefix[b + 1] - first : 0;  // 0: without keys
-            float m_run = -INFINITY, l_run = 0.f;
+            float m_run = -INFINITY, l_run = 0.f, unit = a.scale_log2;
             for (int32_t j = 0; j < x.tiles && ok; ++j) {
                 const uint32_t t = T + j;
                 const int st = t % kStages;
@@ -1071,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float sum = 0.f;
                     // P against `neg_m` over the first 64 columns of S, and its sum
                     auto exp_pass = [&](float neg_m) {
-                        const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
+                        const uint64_t scale2 = pk2(unit, unit);
                         const uint64_t neg2 = pk2(neg_m, neg_m);
                         uint64_t l2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
@@ -1109,12 +1120,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float mx =
                                 fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
                                       fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
-                            mx *= a.scale_log2;            // scale > 0 keeps the order
-                            const bool raise = mine && mx > m_run + kRescaleThreshold;
+                            const float score = mx * a.scale_log2;    // scale > 0 keeps the order
+                            const float u = fabsf(score) >= kFarScore ? a.far_unit : a.scale_log2;
+                            mx *= u;
+                            const bool raise =
+                                mine && (u == unit ? mx > m_run + kRescaleThreshold
+                                                   : score > in_log2(m_run, unit));
                             float alpha = 1.f;
                             if (raise) {
-                                alpha = m_run == -INFINITY ? 0.f : pkv::fast_exp2(m_run - mx);
+                                // (maxima of different units are far apart)
+                                alpha = m_run == -INFINITY || u != unit
+                                            ? 0.f
+                                            : pkv::fast_exp2(m_run - mx);
                                 m_run = mx;
+                                unit = u;
                                 l_run *= alpha;
                             }
                             if (j > 0 && __any_sync(0xffffffffu, raise)) {
@@ -1209,7 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (parts > 1) a.part_ml[at] = make_float2(0.5f * m_run, l_run);
+                if (parts > 1) a.part_ml[at] = make_float2(0.5f * in_log2(m_run, unit), l_run);
             }
             tc_fence_before();
             __syncwarp();
@@ -1384,6 +1403,9 @@ int add_tensors(const void* q, const void* k_cache, const void* v_cache,
     a.bt = block_tables;
     a.out = (__nv_bfloat16*)out;
     a.scale_log2 = scale * pkv::kLog2e;
+    int e;
+    frexpf(a.scale_log2, &e);
+    a.far_unit = ldexpf(1.f, e - 1);
     return PKV_OK;
 }
 

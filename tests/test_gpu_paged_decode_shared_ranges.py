@@ -1,0 +1,121 @@
+"""paged_decode_shared at the ends of its ranges: scores far from one."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import f64, lib, status_word
+from test_gpu_paged_decode_shared import Batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("bs,d", [(16, 128), (256, 64), (24, 64), (20, 128)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(cuda, bs, d, sign):
+    """A key's score is q0 K0 scale, K0 one of bf16's values in [1, 2): scores that differ do so by
+    2^-7 of the largest, thousands here, so that the result is the value of the one key ahead,
+    in the first tile or a later one, among the common keys or a sequence's own.  Its weight and
+    its value's product are rounded to bf16: twice 2^-8."""
+    pkv = lib()
+    b = Batch([6, 3, 1], [400, 150, 0], [300, 1, 0, 77, 500, 20, 140, 5, 260, 33], 4, 2, d, bs,
+              cuda, seed=bs)
+    rng = np.random.default_rng(d)
+    nb = b.tk.shape[0]
+    k0 = torch.from_numpy(rng.integers(0, 127, nb * bs) / 128 + 1).to(torch.bfloat16).to(cuda)
+    b.tk[torch.isfinite(b.tk)] = 0
+    rows = lambda i, t: t.view(nb * bs, 2, d)[  # noqa: E731
+        torch.from_numpy(b.bt[i, np.arange(b.ctx[i]) // bs].astype(np.int64) * bs +
+                         np.arange(b.ctx[i]) % bs).to(cuda)]
+    b.tk.view(-1, 2, d)[:, :, 0] = torch.where(b.tk.view(-1, 2, d)[:, :, 0].isnan(),
+                                               b.tk.view(-1, 2, d)[:, :, 0], k0[:, None])
+    for g, p in enumerate(b.prefix):               # the members' copies of a common row stay alike
+        first, last = b.offsets[g], b.offsets[g + 1]
+        if p % bs:
+            head = b.tk[int(b.bt[first, p // bs]), :p % bs].clone()
+            for i in range(first, last):
+                b.tk[int(b.bt[i, p // bs]), :p % bs] = head
+    # one key of each sequence ahead of its others: a common one of the first group, own ones of
+    # the second and third
+    ahead = [int(rng.integers(0, 400))] * 6 + [int(b.ctx[i]) - 1 for i in range(6, 10)]
+    at = {}
+    for i in range(10):
+        j = ahead[i]
+        at[i] = int(b.bt[i, j // bs]) * bs + j % bs
+    lead = 1 + 127 / 128 if sign > 0 else 1 - 2.0 ** -7
+    for i in range(10):
+        b.tk.view(-1, 2, d)[at[i], :, 0] = lead
+    # (its copies in blocks that are common only in part)
+    p = int(b.prefix[0])
+    if ahead[0] >= p // bs * bs:
+        for i in range(6):
+            b.tk[int(b.bt[i, p // bs]), ahead[0] % bs, :, 0] = lead
+    want = torch.stack([rows(i, b.tv)[ahead[i]] for i in range(10)])       # [10, 2, d]
+    want = f64(want)[:, [0, 0, 1, 1]]
+    for top in (2.0 ** 20, 2.0 ** 24 + 2, 1.3 * 2.0 ** 26, 2.0 ** 27, 1.9 * 2.0 ** 28,
+                1.1 * 2.0 ** 30, 1.7 * 2.0 ** 31, 1.3 * 2.0 ** 32, 1.9 * 2.0 ** 33,
+                1.2 * 2.0 ** 40, 1.6 * 2.0 ** 63, 1.4 * 2.0 ** 100):
+        for e in (0, 20):                          # the scale's part in a query's
+            b.tq[:] = 0
+            b.tq[:, :, 0] = sign * 2.0 ** e
+            st = pkv.new_status(cuda)
+            got = f64(pkv.paged_decode_shared(b.tq, b.tk, b.tv, b.tbt, b.tctx, b.toff, b.tpre,
+                                              top * 2.0 ** -e * 0.7, b.max_ctx, status=st))
+            assert status_word(st) == 0
+            assert np.isfinite(got).all(), (top, e)
+            bound = np.abs(want) * (2.0 ** -7 + 2.0 ** -14)
+            assert (np.abs(got - want) <= bound).all(), (top, e)
+
+
+@pytest.mark.parametrize("bs,d", [(16, 64), (64, 128), (20, 64)])
+@pytest.mark.parametrize("scale", [0.7, 2.0 ** -20 / 3, 1.0])
+def test_scores_from_near_to_far(cuda, bs, d, scale):
+    """Scores that cross every power of two from one tile to the next, rising, falling, of both
+    signs, with equal maxima in several tiles.  They are K0's values, exact in 32 bits, so that
+    the exponents are exact but for the product with the scale: weights within 2^-8 by their
+    rounding, and by exponents of at most 126 times 2^-23."""
+    pkv = lib()
+    n = 12
+    suffix = [900, 0, 130, 500, 1, 777, 640, 128, 300, 64, 1000, 250]
+    b = Batch([4, 5, 1, 1, 1], [600, 300, 0, 0, 0], suffix, 2, 1, d, bs, cuda, seed=bs)
+    rng = np.random.default_rng(d + bs)
+    nb = b.tk.shape[0]
+    b.tk[torch.isfinite(b.tk)] = 0
+    flat = b.tk.view(nb * bs, d)
+    logical = np.zeros((n, int(b.ctx.max())))
+    for i in range(n):
+        j = np.arange(b.ctx[i])
+        slots = torch.from_numpy(b.bt[i, j // bs].astype(np.int64) * bs + j % bs).to(cuda)
+        g = int(np.searchsorted(b.offsets, i, "right")) - 1
+        first, p = int(b.offsets[g]), int(b.prefix[g])
+        kind = i % 4
+        e = (j // 16) if kind == 0 else (70 - j // 16) if kind == 1 else rng.integers(0, 80, len(j))
+        v = 2.0 ** e.clip(0, 90) * (1 + rng.integers(0, 128, len(j)) / 128)
+        if kind == 2:
+            v = -v
+        if kind == 3:                              # two maxima alike, of some sign
+            v = np.where(rng.random(len(j)) < 0.5, -v, v)
+            v[len(j) // 3] = v[-1] = 2.0 ** 85
+        if i != first:
+            v[:p] = logical[first, :p]
+        logical[i, :len(j)] = v
+        flat[slots, 0] = torch.from_numpy(v).to(cuda).to(torch.bfloat16)
+    for sign in (1, -1):
+        b.tq[:] = 0
+        b.tq[:, 0, 0] = sign * 1.0
+        b.tq[:, 1, 0] = sign * 2.0 ** -30
+        st = pkv.new_status(cuda)
+        got = f64(pkv.paged_decode_shared(b.tq, b.tk, b.tv, b.tbt, b.tctx, b.toff, b.tpre, scale,
+                                          b.max_ctx, status=st))
+        assert status_word(st) == 0
+        v = f64(b.tv).reshape(nb * bs, d)
+        for i in range(n):
+            j = np.arange(b.ctx[i])
+            rows = v[b.bt[i, j // bs].astype(np.int64) * bs + j % bs]
+            for h, f in enumerate((1.0, 2.0 ** -30)):
+                x = scale * sign * f * logical[i, :len(j)]
+                w = np.exp(x - x.max())
+                w /= w.sum()
+                ref, size = w @ rows, w @ np.abs(rows)
+                bound = 2.0 ** -8 * (np.abs(ref) + size) + (2 * 126 * 2.0 ** -23 + 2.0 ** -14) * size
+                err = np.abs(got[i, h] - ref)
+                assert (err <= bound).all(), (i, h, sign, float((err / bound).max()))
