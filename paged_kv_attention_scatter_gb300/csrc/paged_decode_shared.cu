@@ -24,8 +24,8 @@
 //              computed against the running maximum straight away and goes over S in TMEM
 //              as bf16, unnormalised: its rounding of 2^-8 of itself is that of a bf16
 //              softmax, l is summed from the unrounded values.  Only for an item's first
-//              tile, and where a row's sum passes 2^16, the maximum is taken, O and l are
-//              rescaled and P computed again.
+//              tile, and where a row's sum passes 2^16 times its first weight, the maximum
+//              is taken, O and l are rescaled and P computed again.
 //   warp 4     producer: draws items, loads Q and K tiles (TMA, one box a run of a cache
 //              block, or rows gathered with cp.async where the block size is no multiple
 //              of 8) into a ring of three
@@ -69,8 +69,12 @@ constexpr int kStages = 3;               // K, V and S buffers
 constexpr int kItemRing = 4, kItemReaders = 7;
 constexpr int kMaskRing = 8;             // more tiles than are between producer and softmax
 constexpr uint32_t kColO = 384;
-constexpr float kRescaleThreshold = 8.0f;   // log2 of the tolerated growth of a maximum
-constexpr float kSumTrigger = 65536.0f;
+// P stands 2^-16 below 1 where a maximum is taken, and a maximum may be passed by 2^8 (a tile's
+// sum by 2^16) before the next is: P and a tile's sum are 1 at most, so that P V passes V
+// no further than the sum of a softmax's weights would.
+constexpr float kHeadroom = 16.0f;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kSumTrigger = 1.0f;
 // A row whose maximum score is so far from zero (base 2) takes its scores in units of a power of
 // two instead of the scale.  S scale - m in one step differs for the maximum itself by what m was
 // rounded by, half its last place: 32 below 2^30, but 128 at 2^31, so that all weights would
@@ -1124,15 +1128,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float u = fabsf(score) >= kFarScore ? a.far_unit : a.scale_log2;
                             mx *= u;
                             const bool raise =
-                                mine && (u == unit ? mx > m_run + kRescaleThreshold
+                                mine && (u == unit ? mx > m_run - (kHeadroom - kRescaleThreshold)
                                                    : score > in_log2(m_run, unit));
                             float alpha = 1.f;
                             if (raise) {
                                 // (maxima of different units are far apart)
                                 alpha = m_run == -INFINITY || u != unit
                                             ? 0.f
-                                            : pkv::fast_exp2(m_run - mx);
-                                m_run = mx;
+                                            : pkv::fast_exp2(m_run - (mx + kHeadroom));
+                                m_run = mx + kHeadroom;
                                 unit = u;
                                 l_run *= alpha;
                             }

@@ -119,3 +119,46 @@ def test_scores_from_near_to_far(cuda, bs, d, scale):
                 bound = 2.0 ** -8 * (np.abs(ref) + size) + (2 * 126 * 2.0 ** -23 + 2.0 ** -14) * size
                 err = np.abs(got[i, h] - ref)
                 assert (err <= bound).all(), (i, h, sign, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("bs,d", [(16, 128), (20, 64)])
+@pytest.mark.parametrize("e", [-126, -110, 100, 117, 120])
+def test_values_of_any_size(cuda, bs, d, e):
+    """Values of size 2^e, bf16's own range: with scores that rise from tile to tile by less than
+    a new maximum is taken for, and without.  The sums pass neither end of 32 bits where the
+    results are within bf16's.  Near its smallest each of n products adds 2^-149, the last
+    place there, over a sum of weights of n 2^-18 or more (2^-16 for the first tile's maximum,
+    whose other weights are within 2^-2 of it), and the result's half step is 2^-134."""
+    pkv = lib()
+    n = 100                                        # enough for runs of several tiles
+    b = Batch([3, 2, n - 5], [500, 300, 0], [400, 1, 0, 130, 260] + [900 - i for i in range(n - 5)],
+              4, 2, d, bs, cuda, seed=e + 200)
+    keep = b.tv.isnan()
+    b.tv = torch.where(keep, b.tv, (b.tv.clamp(-2, 2).float() * 2.0 ** e).to(torch.bfloat16))
+    for slope in (0.0, 12 / 900):                  # base 2, over a context
+        nb = b.tk.shape[0]
+        b.tk[torch.isfinite(b.tk)] = 0
+        b.tq[:], b.tq[:, :, 0] = 0, 1.0
+        flat = b.tk.view(nb * bs, 2, d)
+        logical = {}
+        for i in range(n):
+            j = np.arange(b.ctx[i])
+            slots = torch.from_numpy(b.bt[i, j // bs].astype(np.int64) * bs + j % bs).to(cuda)
+            logical[i] = slots
+            flat[slots, :, 0] = torch.from_numpy(slope * j).to(cuda).to(torch.bfloat16)[:, None]
+        st = pkv.new_status(cuda)
+        got = f64(pkv.paged_decode_shared(b.tq, b.tk, b.tv, b.tbt, b.tctx, b.toff, b.tpre,
+                                          float(np.log(2)), b.max_ctx, status=st))
+        assert status_word(st) == 0
+        k, v = f64(flat[:, 0, 0]), f64(b.tv).reshape(nb * bs, 2, d)
+        for i in range(n):
+            at = logical[i].cpu().numpy()
+            w = 2.0 ** k[at]
+            w /= w.sum()
+            for h in range(4):
+                ref, size = w @ v[at, h // 2], w @ np.abs(v[at, h // 2])
+                bound = 2.0 ** -8 * (np.abs(ref) + size) + 2.0 ** -12 * size + \
+                    2.0 ** -131 + 2.0 ** -134
+                err = np.abs(got[i, h] - ref)
+                assert np.isfinite(got[i, h]).all(), (i, h, slope)
+                assert (err <= bound).all(), (i, h, slope, float((err / bound).max()))
