@@ -55,6 +55,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace {
@@ -76,6 +78,7 @@ struct HeadArgs {
     const uint64_t* turns;
     int32_t rotary_dim, interleaved;
     float magnitude, eps, inv_dim;           // inv_dim: 1 / D
+    float tiny_unit;                         // see kLeastSquares
     int32_t num_tokens, Hq, Hkv, D;
     // the cache
     const int32_t* slots;
@@ -187,6 +190,25 @@ struct Eight<float> {
         *reinterpret_cast<float4*>(p + 4) = b;
     }
 };
+
+// Sums of squares that 32 bits hold with all their places.  A head whose sum lies outside (entries
+// beyond 2^59, or all below 2^-50) is multiplied by a power of two first, eps by its
+// square: 2^-70 brings the largest entries to 2^58, tiny_unit the small ones to 2^-49 and more
+// where eps leaves room for it.  Halves cannot be so large or small.
+constexpr float kLeastSquares = 0x1p-100f, kMostSquares = 0x1p126f, kHugeUnit = 0x1p-70f;
+template <typename T>
+constexpr bool kAnySquares = !std::is_same<T, __half>::value;
+
+__device__ __forceinline__ bool odd_squares(float ss) {
+    return !(ss >= kLeastSquares && ss < kMostSquares);
+}
+__device__ __forceinline__ float odd_unit(const HeadArgs& g, float ss) {
+    return ss < kLeastSquares ? g.tiny_unit : kHugeUnit;
+}
+__device__ __forceinline__ void scale(Pairs& x, float f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], pk2(f, f));
+}
 
 __device__ __forceinline__ float weight_at(const HeadArgs& a, int which, int e) {
     const void* w = a.weight[which];
@@ -337,20 +359,34 @@ __global__ void __launch_bounds__(kThreads, 6) head_kernel(const HeadArgs g) {
             }
             if (kStore && __all_sync(~0u, h >= qk)) continue;
             const int which = h < g.Hq ? 0 : 1;
-            const Pairs a = x0[u].get(), b = x1[u].get();
+            Pairs a = x0[u].get(), b = x1[u].get();
             float r = 1.f;
             if (g.weight[0] || g.weight[1]) {
-                uint64_t s2 = mul2(a.v[0], a.v[0]);
+                auto squares = [&] {
+                    uint64_t s2 = mul2(a.v[0], a.v[0]);
 #pragma unroll
-                for (int i = 1; i < 4; ++i) s2 = fma2(a.v[i], a.v[i], s2);
+                    for (int i = 1; i < 4; ++i) s2 = fma2(a.v[i], a.v[i], s2);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s2 = fma2(b.v[i], b.v[i], s2);
-                const float2 s = up2(s2);
-                float ss = s.x + s.y;
+                    for (int i = 0; i < 4; ++i) s2 = fma2(b.v[i], b.v[i], s2);
+                    const float2 s = up2(s2);
+                    float ss = s.x + s.y;
 #pragma unroll
-                for (int off = kLanes / 2; off > 0; off >>= 1)
-                    ss += __shfl_xor_sync(~0u, ss, off);
-                if (g.weight[which]) r = rsqrtf(ss * g.inv_dim + g.eps);
+                    for (int off = kLanes / 2; off > 0; off >>= 1)
+                        ss += __shfl_xor_sync(~0u, ss, off);
+                    return ss;
+                };
+                float ss = squares(), eps = g.eps;
+                if constexpr (kAnySquares<T>) {
+                    const bool odd = h < qk && g.weight[which] && odd_squares(ss);
+                    if (__builtin_expect(__any_sync(~0u, odd), 0)) {
+                        const float f = odd ? odd_unit(g, ss) : 1.f;
+                        scale(a, f);
+                        scale(b, f);
+                        ss = squares();
+                        eps = eps * f * f;
+                    }
+                }
+                if (g.weight[which]) r = rsqrtf(ss * g.inv_dim + eps);
             }
             const uint64_t r2 = pk2(r, r);
             Pairs pa = a, pb = b;                            // partners
@@ -724,21 +760,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
                 Eight<T> x0, x1;
                 x0.take(row + e0);
                 x1.take(row + e1);
-                const Pairs a = x0.get(), b = x1.get();
-                float r = 1.f;
+                Pairs a = x0.get(), b = x1.get();
+                float r = 1.f, unit = 1.f;
+                bool odd = false;
                 if (norm) {
-                    uint64_t s2 = mul2(a.v[0], a.v[0]);
+                    auto squares = [&] {
+                        uint64_t s2 = mul2(a.v[0], a.v[0]);
 #pragma unroll
-                    for (int t = 1; t < 4; ++t) s2 = fma2(a.v[t], a.v[t], s2);
-                    uint64_t both = s2;
+                        for (int t = 1; t < 4; ++t) s2 = fma2(a.v[t], a.v[t], s2);
+                        uint64_t both = s2;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) both = fma2(b.v[t], b.v[t], both);
-                    const float2 s = up2(has1 ? both : s2);
-                    float ss = has0 ? s.x + s.y : 0.f;
+                        for (int t = 0; t < 4; ++t) both = fma2(b.v[t], b.v[t], both);
+                        const float2 s = up2(has1 ? both : s2);
+                        float ss = has0 ? s.x + s.y : 0.f;
 #pragma unroll
-                    for (int off = kLanes / 2; off > 0; off >>= 1)
-                        ss += __shfl_xor_sync(~0u, ss, off);
-                    r = rsqrtf(ss * g.inv_dim + g.eps);
+                        for (int off = kLanes / 2; off > 0; off >>= 1)
+                            ss += __shfl_xor_sync(~0u, ss, off);
+                        return ss;
+                    };
+                    float ss = squares(), eps = g.eps;
+                    if constexpr (kAnySquares<T>) {
+                        odd = __any_sync(~0u, odd_squares(ss));
+                        if (__builtin_expect(odd, 0)) {
+                            if (odd_squares(ss)) unit = odd_unit(g, ss);
+                            scale(a, unit);
+                            scale(b, unit);
+                            ss = squares();
+                            eps = eps * unit * unit;
+                        }
+                    }
+                    r = rsqrtf(ss * g.inv_dim + eps);
                 }
                 const uint64_t r2 = pk2(r, r);
                 Pairs y0, y1;
@@ -764,13 +815,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
                         }
                     }
                 } else if constexpr (kPartner == kShared) {
-                    auto chunk = [&](int e, const Pairs& tb, Pairs& y) {
+                    auto chunk = [&](auto scaled, int e, const Pairs& tb, Pairs& y) {
+                        const uint64_t f2 = pk2(unit, unit);
                         if (half % 4 == 0) {
 #pragma unroll
                             for (int t = 0; t < 4; t += 2, e += 4) {
                                 if (e >= g.rotary_dim) break;
                                 uint64_t lo, hi;
                                 four(row + (e < half ? e + half : e - half), lo, hi);
+                                if (scaled) lo = mul2(lo, f2), hi = mul2(hi, f2);
                                 y.v[t] = fma2(tb.v[t], lo, y.v[t]);
                                 y.v[t + 1] = fma2(tb.v[t + 1], hi, y.v[t + 1]);
                             }
@@ -781,12 +834,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
 #pragma unroll
                             for (int t = 0; t < 4; ++t, e += 2) {
                                 if (e >= g.rotary_dim) break;
-                                y.v[t] = fma2(tb.v[t], pk2(one(e), one(e + 1)), y.v[t]);
+                                uint64_t x2 = pk2(one(e), one(e + 1));
+                                if (scaled) x2 = mul2(x2, f2);
+                                y.v[t] = fma2(tb.v[t], x2, y.v[t]);
                             }
                         }
                     };
-                    chunk(e0, b0, y0);
-                    chunk(e1, b1, y1);
+                    if (kAnySquares<T> && __builtin_expect(odd, 0)) {
+                        chunk(std::true_type(), e0, b0, y0);
+                        chunk(std::true_type(), e1, b1, y1);
+                    } else {
+                        chunk(std::false_type(), e0, b0, y0);
+                        chunk(std::false_type(), e1, b1, y1);
+                    }
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
@@ -948,6 +1008,10 @@ int make_args(const void* q, int64_t q_stride, const void* k, int64_t k_stride, 
     g.magnitude = rotary.magnitude;
     g.eps = eps;
     g.inv_dim = 1.f / (float)head_dim;
+    // eps tiny_unit^2 at most 2^120
+    int e = -126;
+    if (eps > 0.f) frexpf(eps, &e);
+    g.tiny_unit = ldexpf(1.f, e < -80 ? 100 : (120 - e) / 2);
     g.num_tokens = num_tokens;
     g.Hq = num_q_heads;
     g.Hkv = num_kv_heads;
