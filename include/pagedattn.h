@@ -119,8 +119,10 @@ PKV_API int pkv_set_wait_poll_limit(uint32_t polls);
  *   slot_mapping   device, [num_tokens] int32; slot < 0 skips the token (padding
  *                  rows of a fixed-shape batch); slot >= num_blocks*block_size
  *                  sets PKV_STATUS_SLOT_OUT_OF_RANGE and skips it
- * Row i of k and of v is copied bit for bit into slot slot_mapping[i].  Two
- * tokens with the same slot in one call: the surviving row is one of them.
+ * Row i of k and of v is copied bit for bit into slot slot_mapping[i].  The
+ * slots of a call are to be different: rows are stored in 16-byte pieces in no
+ * order, so that a slot of two tokens ends with pieces of both
+ * (pkv_qk_norm_rope_kv_store and pkv_kv_store_fp8 store the last token's row).
  * Needs num_kv_heads*head_dim*2 to be a multiple of 16.  num_tokens == 0 is a
  * no-op.
  */

@@ -240,7 +240,7 @@ def status_names(word: int) -> list[str]:
 def kv_store(k, v, k_cache, v_cache, slot_mapping, status=None, stream=None) -> None:
     """Writes row i of k / v into slot slot_mapping[i] of k_cache / v_cache
     (in place).  k, v: [N, Hkv, D] bf16; caches [NB, bs, Hkv, D] bf16;
-    slot_mapping [N] int32 (negative = skip)."""
+    slot_mapping [N] int32 (negative = skip), all different."""
     lib = load()
     dev = k_cache.device
     n = slot_mapping.numel()
