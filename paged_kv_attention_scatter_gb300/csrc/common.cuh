@@ -3,6 +3,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -107,6 +108,21 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// The tensor-core attention kernels take S scale - m in one step, which differs for the maximum
+// itself by what m was rounded by, half its last place: 32 below 2^30, but 128 at 2^31, so that
+// all weights would be infinite or 0.  A row whose maximum score (base 2) is this far from
+// zero takes its scores in units of a power of two instead of the scale.  Nothing is rounded
+// then, and the weights stay what they are: different scores in 32 bits lie
+// 2^30 2^-24 = 64 and more apart (32 below a power of two).
+constexpr float kFarScore = 1073741824.0f;
+
+// The power of two at or below x > 0.
+inline float power_below(float x) {
+    int e = 0;
+    frexpf(x, &e);
+    return ldexpf(1.f, e - 1);
+}
 
 }  // namespace pkv
 

@@ -75,12 +75,6 @@ constexpr uint32_t kColO = 384;
 constexpr float kHeadroom = 16.0f;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kSumTrigger = 1.0f;
-// A row whose maximum score is so far from zero (base 2) takes its scores in units of a power of
-// two instead of the scale.  S scale - m in one step differs for the maximum itself by what m was
-// rounded by, half its last place: 32 below 2^30, but 128 at 2^31, so that all weights would
-// be infinite or 0.  With a power of two nothing is rounded, and the weights stay what they
-// are: different scores in 32 bits lie 2^30 2^-24 = 64 and more apart (32 below a power of two).
-constexpr float kFarScore = 1073741824.0f;
 constexpr int kSms = 152;                // of a GB300: sizes follow from the arguments alone
 constexpr int kMaxContext = 1 << 30;     // keys beyond it would pass 32 bits at a tile's end
 
@@ -121,7 +115,7 @@ struct SharedArgs {
     int32_t tile_heads, head_tiles, tile_seqs;
     int32_t cap_records, cap_parts, common_budget;
     float scale_log2;
-    float far_unit;                      // the power of two at or below it (see kFarScore)
+    float far_unit, far_ratio;           // the power of two at or below it, their ratio (kFarScore)
     uint32_t* status;
     uint32_t wait_polls;
     // the plan's
@@ -1035,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t my_seq = i / a.tile_heads, my_head = i - my_seq * a.tile_heads;
         // a maximum in units of either kind as a score
         auto in_log2 = [&](float m, float unit) {
-            return unit == a.scale_log2 ? m : m * (a.scale_log2 / unit);
+            return unit == a.scale_log2 ? m : m * a.far_ratio;
         };
         uint32_t T = 0;
         bool ok = true;
@@ -1125,7 +1119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
                                       fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
                             const float score = mx * a.scale_log2;    // scale > 0 keeps the order
-                            const float u = fabsf(score) >= kFarScore ? a.far_unit : a.scale_log2;
+                            const float u =
+                                fabsf(score) >= pkv::kFarScore ? a.far_unit : a.scale_log2;
                             mx *= u;
                             const bool raise =
                                 mine && (u == unit ? mx > m_run - (kHeadroom - kRescaleThreshold)
@@ -1407,9 +1402,8 @@ int add_tensors(const void* q, const void* k_cache, const void* v_cache,
     a.bt = block_tables;
     a.out = (__nv_bfloat16*)out;
     a.scale_log2 = scale * pkv::kLog2e;
-    int e;
-    frexpf(a.scale_log2, &e);
-    a.far_unit = ldexpf(1.f, e - 1);
+    a.far_unit = pkv::power_below(a.scale_log2);
+    a.far_ratio = a.scale_log2 / a.far_unit;
     return PKV_OK;
 }
 

@@ -259,6 +259,8 @@ int pkv_prefill_make_args(const void* q, const void* k, const void* v, const voi
     a.bs = cache.block_size > 0 ? cache.block_size : 1;
     a.max_tiles = L.max_tiles;
     a.scale_log2 = scale * pkv::kLog2e;
+    a.far_unit = pkv::power_below(a.scale_log2);
+    a.far_ratio = a.scale_log2 / a.far_unit;
     a.status = status;
     a.skip_single = 0;
     a.wait_polls = pkv_wait_polls();

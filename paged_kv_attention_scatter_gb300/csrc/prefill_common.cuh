@@ -23,6 +23,7 @@ struct PrefillArgs {
     int32_t B, total_q, max_sq, max_sk, Hq, Hkv, G, MB, NB, bs, max_tiles;
     int32_t tile_m, tile_n;          // tile shape the schedule is built for
     float scale_log2;
+    float far_unit, far_ratio;       // the power of two at or below it, their ratio (kFarScore)
     uint32_t* status;
     int32_t skip_single;             // sequences of one query are left to the decode kernels
     uint32_t wait_polls;             // polls of a bounded mbarrier wait

@@ -689,6 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
         // ------------------------------------------------------------ softmax
         const int i = tid;                          // query row == TMEM lane
         const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+        // a maximum in units of either kind (see kFarScore) as a score
+        auto in_log2 = [&](float m, float unit) {
+            return unit == a.scale_log2 ? m : m * a.far_ratio;
+        };
         uint32_t T = 0, I = 0;
         bool ok = true;
         for (; ok; ++I) {
@@ -696,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
             if (!(ok = next_item(s, I, it, polls, true))) break;
             if (it < 0) break;
             const Item x = item_at<kSplit>(a, it);
-            float m_run = -INFINITY, l_run = 0.f;
+            float m_run = -INFINITY, l_run = 0.f, unit = a.scale_log2;
             for (int32_t j = x.first; j < x.end && ok; ++j) {
                 const uint32_t t = T + (j - x.first);
                 const int st = t % kStages;
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                 // pair).
                 float ls[4];
                 auto exp_pass = [&](float neg_m) {
-                    const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
+                    const uint64_t scale2 = pk2(unit, unit);
                     const uint64_t neg_m2 = pk2(neg_m, neg_m);
                     uint64_t l2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
@@ -774,12 +778,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                             mxp[e] = max3(mxp[e], sv[col + e], sv[col + 8 + e]);
                     float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                      fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
-                    mx *= a.scale_log2;                     // scale > 0 keeps the order
-                    const bool raise = mx > m_run + kRescaleThreshold;
+                    const float score = mx * a.scale_log2;  // scale > 0 keeps the order
+                    const float u = fabsf(score) >= pkv::kFarScore ? a.far_unit : a.scale_log2;
+                    mx *= u;
+                    const bool raise = u == unit ? mx > m_run + kRescaleThreshold
+                                                 : score > in_log2(m_run, unit);
                     float alpha = 1.f;
                     if (raise) {
-                        alpha = (m_run == -INFINITY) ? 0.f : pkv::fast_exp2(m_run - mx);
+                        // (maxima of different units are far apart)
+                        alpha = m_run == -INFINITY || u != unit ? 0.f
+                                                                : pkv::fast_exp2(m_run - mx);
                         m_run = mx;
+                        unit = u;
                         l_run *= alpha;
                     }
                     if (j > x.first && __any_sync(0xffffffffu, raise)) {
@@ -847,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(
                             st_global_32b(a.part_o + at * D + cc * 32 + e, w8);
                         }
                     }
-                    if (i < x.rows) a.part_ml[at] = make_float2(m_run, l_run);
+                    if (i < x.rows) a.part_ml[at] = make_float2(in_log2(m_run, unit), l_run);
                     tc_fence_before();
                     mbar_arrive(&s.o_free);
                     T += x.end - x.first;
