@@ -362,31 +362,28 @@ __global__ void __launch_bounds__(kThreads, 6) head_kernel(const HeadArgs g) {
             Pairs a = x0[u].get(), b = x1[u].get();
             float r = 1.f;
             if (g.weight[0] || g.weight[1]) {
-                auto squares = [&] {
+                float ss, eps = g.eps;
+#pragma unroll 1
+                for (bool scaled = false;; scaled = true) {
                     uint64_t s2 = mul2(a.v[0], a.v[0]);
 #pragma unroll
                     for (int i = 1; i < 4; ++i) s2 = fma2(a.v[i], a.v[i], s2);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s2 = fma2(b.v[i], b.v[i], s2);
                     const float2 s = up2(s2);
-                    float ss = s.x + s.y;
+                    ss = s.x + s.y;
 #pragma unroll
                     for (int off = kLanes / 2; off > 0; off >>= 1)
                         ss += __shfl_xor_sync(~0u, ss, off);
-                    return ss;
-                };
-                float ss = squares(), eps = g.eps;
-                if constexpr (kAnySquares<T>) {
+                    if (!kAnySquares<T> || scaled) break;
                     const bool odd = h < qk && g.weight[which] && odd_squares(ss);
-                    if (__builtin_expect(__any_sync(~0u, odd), 0)) {
-                        const float f = odd ? odd_unit(g, ss) : 1.f;
-                        scale(a, f);
-                        scale(b, f);
-                        ss = squares();
-                        eps = eps * f * f;
-                    }
+                    if (!__any_sync(~0u, odd)) break;
+                    const float f = odd ? odd_unit(g, ss) : 1.f;
+                    scale(a, f);
+                    scale(b, f);
+                    eps = eps * f * f;
                 }
-                if (g.weight[which]) r = rsqrtf(ss * g.inv_dim + eps);
+                if (g.weight[which]) r = rsqrtf(fmaf(ss, g.inv_dim, eps));
             }
             const uint64_t r2 = pk2(r, r);
             Pairs pa = a, pb = b;                            // partners
@@ -751,117 +748,117 @@ __global__ void __launch_bounds__(kWarps * 32, 1) row_kernel(const HeadArgs g, c
             if (kStore && pc.which == 1 && slot >= 0)
                 cached = (T*)g.cache[0] + ((int64_t)slot * g.Hkv + pc.h0) * g.D;
             const T* rows = reinterpret_cast<const T*>(st.rows);
-#pragma unroll 2
-            for (int32_t base = 0; base < pc.n; base += kHeads) {
-                // lanes without a head or a chunk compute on another's, and write nothing
-                const int32_t h = base + head < pc.n ? base + head : 0;
-                const bool in = base + head < pc.n && has0;
-                const T* row = rows + h * g.D;
-                Eight<T> x0, x1;
-                x0.take(row + e0);
-                x1.take(row + e1);
-                Pairs a = x0.get(), b = x1.get();
-                float r = 1.f, unit = 1.f;
-                bool odd = false;
-                if (norm) {
-                    auto squares = [&] {
-                        uint64_t s2 = mul2(a.v[0], a.v[0]);
+            // The piece's heads, and once more where there are some with squares beyond 32 bits.
+            bool odd = false;
+            auto heads = [&](auto scaled) {
+                constexpr bool kScaled = decltype(scaled)::value;
+#pragma unroll (kScaled ? 1 : 2)
+                for (int32_t base = 0; base < pc.n; base += kHeads) {
+                    // lanes without a head or a chunk compute on another's, and write nothing
+                    const int32_t h = base + head < pc.n ? base + head : 0;
+                    const bool in = base + head < pc.n && has0;
+                    const T* row = rows + h * g.D;
+                    Eight<T> x0, x1;
+                    x0.take(row + e0);
+                    x1.take(row + e1);
+                    Pairs a = x0.get(), b = x1.get();
+                    float r = 1.f, unit = 1.f;
+                    if (norm) {
+                        auto squares = [&] {
+                            uint64_t s2 = mul2(a.v[0], a.v[0]);
 #pragma unroll
-                        for (int t = 1; t < 4; ++t) s2 = fma2(a.v[t], a.v[t], s2);
-                        uint64_t both = s2;
+                            for (int t = 1; t < 4; ++t) s2 = fma2(a.v[t], a.v[t], s2);
+                            uint64_t both = s2;
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) both = fma2(b.v[t], b.v[t], both);
-                        const float2 s = up2(has1 ? both : s2);
-                        float ss = has0 ? s.x + s.y : 0.f;
+                            for (int t = 0; t < 4; ++t) both = fma2(b.v[t], b.v[t], both);
+                            const float2 s = up2(has1 ? both : s2);
+                            float ss = has0 ? s.x + s.y : 0.f;
 #pragma unroll
-                        for (int off = kLanes / 2; off > 0; off >>= 1)
-                            ss += __shfl_xor_sync(~0u, ss, off);
-                        return ss;
-                    };
-                    float ss = squares(), eps = g.eps;
-                    if constexpr (kAnySquares<T>) {
-                        odd = __any_sync(~0u, odd_squares(ss));
-                        if (__builtin_expect(odd, 0)) {
+                            for (int off = kLanes / 2; off > 0; off >>= 1)
+                                ss += __shfl_xor_sync(~0u, ss, off);
+                            return ss;
+                        };
+                        float ss = squares(), eps = g.eps;
+                        odd |= odd_squares(ss);
+                        if constexpr (kScaled) {
                             if (odd_squares(ss)) unit = odd_unit(g, ss);
                             scale(a, unit);
                             scale(b, unit);
                             ss = squares();
                             eps = eps * unit * unit;
                         }
+                        r = rsqrtf(fmaf(ss, g.inv_dim, eps));
                     }
-                    r = rsqrtf(ss * g.inv_dim + eps);
-                }
-                const uint64_t r2 = pk2(r, r);
-                Pairs y0, y1;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    y0.v[t] = mul2(a0.v[t], a.v[t]);
-                    y1.v[t] = mul2(a1.v[t], b.v[t]);
-                }
-                if constexpr (kPartner == kPairs) {
+                    const uint64_t r2 = pk2(r, r);
+                    Pairs y0, y1;
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        if (e0 + 2 * t < g.rotary_dim)
-                            y0.v[t] = fma2(b0.v[t], swapped(a.v[t]), y0.v[t]);
-                        if (e1 + 2 * t < g.rotary_dim)
-                            y1.v[t] = fma2(b1.v[t], swapped(b.v[t]), y1.v[t]);
+                        y0.v[t] = mul2(a0.v[t], a.v[t]);
+                        y1.v[t] = mul2(a1.v[t], b.v[t]);
                     }
-                } else if constexpr (kPartner == kChunks) {
-                    if (j < away) {
+                    if constexpr (kPartner == kPairs) {
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
-                            y0.v[t] = fma2(b0.v[t], b.v[t], y0.v[t]);
-                            y1.v[t] = fma2(b1.v[t], a.v[t], y1.v[t]);
+                            if (e0 + 2 * t < g.rotary_dim)
+                                y0.v[t] = fma2(b0.v[t], swapped(a.v[t]), y0.v[t]);
+                            if (e1 + 2 * t < g.rotary_dim)
+                                y1.v[t] = fma2(b1.v[t], swapped(b.v[t]), y1.v[t]);
                         }
-                    }
-                } else if constexpr (kPartner == kShared) {
-                    auto chunk = [&](auto scaled, int e, const Pairs& tb, Pairs& y) {
-                        const uint64_t f2 = pk2(unit, unit);
-                        if (half % 4 == 0) {
+                    } else if constexpr (kPartner == kChunks) {
+                        if (j < away) {
 #pragma unroll
-                            for (int t = 0; t < 4; t += 2, e += 4) {
-                                if (e >= g.rotary_dim) break;
-                                uint64_t lo, hi;
-                                four(row + (e < half ? e + half : e - half), lo, hi);
-                                if (scaled) lo = mul2(lo, f2), hi = mul2(hi, f2);
-                                y.v[t] = fma2(tb.v[t], lo, y.v[t]);
-                                y.v[t + 1] = fma2(tb.v[t + 1], hi, y.v[t + 1]);
-                            }
-                        } else {
-                            auto one = [&](int e) {
-                                return (float)row[e < half ? e + half : e - half];
-                            };
-#pragma unroll
-                            for (int t = 0; t < 4; ++t, e += 2) {
-                                if (e >= g.rotary_dim) break;
-                                uint64_t x2 = pk2(one(e), one(e + 1));
-                                if (scaled) x2 = mul2(x2, f2);
-                                y.v[t] = fma2(tb.v[t], x2, y.v[t]);
+                            for (int t = 0; t < 4; ++t) {
+                                y0.v[t] = fma2(b0.v[t], b.v[t], y0.v[t]);
+                                y1.v[t] = fma2(b1.v[t], a.v[t], y1.v[t]);
                             }
                         }
-                    };
-                    if (kAnySquares<T> && __builtin_expect(odd, 0)) {
-                        chunk(std::true_type(), e0, b0, y0);
-                        chunk(std::true_type(), e1, b1, y1);
-                    } else {
-                        chunk(std::false_type(), e0, b0, y0);
-                        chunk(std::false_type(), e1, b1, y1);
+                    } else if constexpr (kPartner == kShared) {
+                        auto chunk = [&](int e, const Pairs& tb, Pairs& y) {
+                            const uint64_t f2 = pk2(unit, unit);
+                            if (half % 4 == 0) {
+#pragma unroll
+                                for (int t = 0; t < 4; t += 2, e += 4) {
+                                    if (e >= g.rotary_dim) break;
+                                    uint64_t lo, hi;
+                                    four(row + (e < half ? e + half : e - half), lo, hi);
+                                    if (kScaled) lo = mul2(lo, f2), hi = mul2(hi, f2);
+                                    y.v[t] = fma2(tb.v[t], lo, y.v[t]);
+                                    y.v[t + 1] = fma2(tb.v[t + 1], hi, y.v[t + 1]);
+                                }
+                            } else {
+                                auto one = [&](int e) {
+                                    return (float)row[e < half ? e + half : e - half];
+                                };
+#pragma unroll
+                                for (int t = 0; t < 4; ++t, e += 2) {
+                                    if (e >= g.rotary_dim) break;
+                                    uint64_t x2 = pk2(one(e), one(e + 1));
+                                    if (kScaled) x2 = mul2(x2, f2);
+                                    y.v[t] = fma2(tb.v[t], x2, y.v[t]);
+                                }
+                            }
+                        };
+                        chunk(e0, b0, y0);
+                        chunk(e1, b1, y1);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        y0.v[t] = mul2(y0.v[t], r2);
+                        y1.v[t] = mul2(y1.v[t], r2);
+                    }
+                    if (in && out) {
+                        Eight<T>::store(out + h * g.D + e0, y0);
+                        if (has1) Eight<T>::store(out + h * g.D + e1, y1);
+                    }
+                    if (kStore && in && cached) {
+                        Eight<T>::store(cached + h * g.D + e0, y0);
+                        if (has1) Eight<T>::store(cached + h * g.D + e1, y1);
                     }
                 }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    y0.v[t] = mul2(y0.v[t], r2);
-                    y1.v[t] = mul2(y1.v[t], r2);
-                }
-                if (in && out) {
-                    Eight<T>::store(out + h * g.D + e0, y0);
-                    if (has1) Eight<T>::store(out + h * g.D + e1, y1);
-                }
-                if (kStore && in && cached) {
-                    Eight<T>::store(cached + h * g.D + e0, y0);
-                    if (has1) Eight<T>::store(cached + h * g.D + e1, y1);
-                }
-            }
+            };
+            heads(std::false_type());
+            if constexpr (kAnySquares<T>)
+                if (__any_sync(~0u, odd)) heads(std::true_type());
         }
         __syncwarp();                                        // the stage is read
         advance(now);
