@@ -289,8 +289,10 @@ PKV_API size_t pkv_paged_prefill_workspace_bytes(int32_t batch, int32_t total_q,
  *                 16-byte aligned; holds the tile schedule
  * A sequence with inconsistent lengths sets PKV_STATUS_BAD_SEQLENS and is
  * skipped (its output rows are not written).  head_dim 64 or 128, any
- * block_size.  PKV_ERR_UNSUPPORTED: num_blocks*block_size >= 2^31 (no such
- * pool fits in device memory) or a driver without cuTensorMapEncodeTiled.
+ * block_size.  Entries of V are to stay below 2^96 in size: the sums before the
+ * softmax's division may stand 2^32 above them.  PKV_ERR_UNSUPPORTED:
+ * num_blocks*block_size >= 2^31 (no such pool fits in device memory) or a
+ * driver without cuTensorMapEncodeTiled.
  */
 PKV_API int pkv_paged_prefill_varlen(const void* q, const void* k, const void* v,
                              const void* k_cache, const void* v_cache,
@@ -631,7 +633,8 @@ PKV_API int pkv_rotary_turns(const double* frequencies, int32_t count, uint64_t*
  *   y = x * weight / sqrt(mean(x^2) + eps)   (y = x where the weights are NULL),
  *   then y's first rotary_dim entries rotated by its token's position, pairs
  *   (a, b) -> magnitude * (a cos - b sin, b cos + a sin).
- * Computed in fp32 and rounded once to the rows' type.
+ * Computed in fp32 and rounded once to the rows' type; squares beyond fp32 do no
+ * harm (such a head is scaled by a power of two first).
  *
  *   q, k         device, [num_tokens, heads, head_dim] of `type` (PKV_FP32, PKV_BF16
  *                or PKV_FP16), tokens q_stride / k_stride elements apart (a packed
@@ -658,7 +661,8 @@ PKV_API int pkv_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int
  * NULL, e.g. for pkv_paged_prefill_varlen), v rows [num_tokens, num_kv_heads,
  * head_dim], v_stride elements apart, to their slots of v_cache as they are.
  * slot_mapping as in pkv_kv_store, but of tokens with the same slot the last
- * one's rows are stored; a token without a slot still gets its q_out and k_out rows.  The caches must not overlap the other tensors.
+ * one's rows are stored; a token without a slot still gets its q_out and k_out
+ * rows.  The caches must not overlap the other tensors.
  */
 PKV_API int pkv_qk_norm_rope_kv_store(
     const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -674,7 +678,9 @@ PKV_API int pkv_qk_norm_rope_kv_store(
  *
  * Bytes of device workspace the calls below need (a pure host function).  As
  * with pkv_paged_decode_workspace_bytes, a workspace shared by several batch
- * sizes must be as large as the largest of their answers.
+ * sizes must be as large as the largest of their answers.  With 32 q and 8 kv heads
+ * of 128 and contexts of 1500: 4 MB for 8 sequences, 21 for 64, 69 for 256; at most
+ * 95 for 256 of any length.
  */
 PKV_API size_t pkv_paged_decode_shared_workspace_bytes(int32_t batch, int32_t num_q_heads,
                                                        int32_t max_context_len,
@@ -688,7 +694,8 @@ PKV_API size_t pkv_paged_decode_shared_workspace_bytes(int32_t batch, int32_t nu
  *                 Sequences outside every group attend by themselves.
  *   prefix_lens   device, [num_groups] int32: the first prefix_lens[g] keys of every
  *                 sequence of group g (of its context_lens[b] in all) are those that
- *                 any one of its block-table rows names.  Read once for the group.
+ *                 any one of its block-table rows names.  Loaded once for every 128
+ *                 rows (query heads of a kv head, times sequences) of the group.
  * num_groups 0 takes NULL for both.  scale must be positive and finite.
  * A context length of 0 gives zeros.  One below its group's prefix, or out of
  * range as in pkv_paged_decode, sets PKV_STATUS_BAD_CONTEXT_LEN and gives zeros.
@@ -698,6 +705,10 @@ PKV_API size_t pkv_paged_decode_shared_workspace_bytes(int32_t batch, int32_t nu
  * row whose scores are NaN or +inf gives NaN.  num_blocks*block_size must be below
  * 2^31 and max_context_len at most 2^30 (PKV_ERR_UNSUPPORTED; the workspace's size is
  * 0 then).
+ * Its plan takes 5 us where pkv_paged_decode's takes 2: with 32 q and 8 kv heads of 128
+ * and up to 1500 own keys the whole call is as fast as pkv_paged_decode at about
+ * 100 common keys of 256 sequences, 200 of 64, 500 of 8, 2500 of two, and faster from there
+ * on (64 and 1024: 52 us for 81); a run alone at 64, 100, 130 and 2000.
  */
 PKV_API int pkv_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
                                     const int32_t* block_tables, int32_t max_blocks_per_seq,

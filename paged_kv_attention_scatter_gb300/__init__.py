@@ -23,7 +23,7 @@ and ahead of the cache, and for batches whose sequences share prompts:
                         RMS norm of q and k heads and the rotation of their
                         positions, alone or with the store of k and v
   paged_decode_shared   paged_decode with the keys that sequences have in common
-                        read and multiplied once for all of them
+                        read and multiplied once for up to 128 query rows
 
 PyTorch supplies device memory and streams only.  `workloads` draws the seeded
 synthetic inputs the tests and the benchmark use.

@@ -1130,8 +1130,8 @@ def qk_norm_rope_kv_store(q, k, v, q_weight, k_weight, eps, positions, rope, k_c
                           stream=None) -> torch.Tensor:
     """qk_norm_rope of bf16 rows with its k rows, and v [T, Hkv, D] as it is, stored in
     the paged cache as kv_store stores them (slot_mapping [T] int32, negative =
-    skip; of equal slots the last token's rows).  Returns q_out; the k rows are also written to k_out when given (for
-    paged_prefill_varlen)."""
+    skip; of equal slots the last token's rows).  Returns q_out; the k rows are also
+    written to k_out when given (for paged_prefill_varlen)."""
     f = load().pkv_qk_norm_rope_kv_store
     index, n, hq, hkv, d, qp, qs, kp, ks, qwp, kwp, wtype, pos, desc = _norm_rope_args(
         q, k, q_weight, k_weight, positions, rope)
@@ -1201,10 +1201,12 @@ def paged_decode_shared(q, k_cache, v_cache, block_tables, context_lens, group_o
                         prefix_lens, scale, max_context_len, out=None, workspace=None, status=None,
                         stream=None) -> torch.Tensor:
     """paged_decode of sequences in groups with their first keys in common, which are
-    read and multiplied once for a group: sequences group_offsets[g] ..
-    group_offsets[g + 1] - 1 (int32, [groups + 1], increasing) share the first prefix_lens[g]
-    ([groups] int32) of their keys, so that their block tables name the same blocks
-    there.  Other sequences attend by themselves.  Both may be None: no groups."""
+    read and multiplied once for up to 128 query rows of a group: sequences
+    group_offsets[g] .. group_offsets[g + 1] - 1 (int32, [groups + 1], increasing) share the
+    first prefix_lens[g] ([groups] int32) of their keys, so that their block tables name the
+    same blocks there.  Other sequences attend by themselves.  Both may be None: no
+    groups.  Faster than paged_decode from some 100 common keys of 256 sequences, 200 of 64,
+    500 of 8 or 2500 of two on (include/pagedattn.h)."""
     lib = load()
     index, cache, desc = _bf16_cache(k_cache, v_cache)
     B, Hq, width, qp, bt, _ = _decode_batch(q, block_tables, context_lens, desc, index)

@@ -1,14 +1,17 @@
 // paged_decode_shared: decode attention for a batch whose sequences come in groups with
 // their first keys in common (one system prompt, one document, several samples of one
-// prompt), the common keys read and multiplied once for all sequences of a group.
+// prompt), the common keys read and multiplied once for up to 128 rows of a group's
+// sequences, not once for each.
 //
 // What it computes: what paged_decode does,
 //   out[b,h] = sum_{j < ctx_b} softmax_j(scale * q[b,h] . K_j) V_j.
 // For a group of n sequences with P common keys the queries of one kv head are the
 // n G rows of a matrix, so that Q K^T and P V over the common keys are matrix products
-// of n G rows on the tensor cores, and the K and V rows are read once, not n times.  The
-// softmax over a sequence's keys is put together from parts: each part is a maximum m, a
-// sum l and an unnormalised o over some of the keys, and
+// of n G rows on the tensor cores.  A tile of 128 rows loads the common K and V rows; the further
+// tiles of a larger group find most of them in L2 (256 sequences of four rows a head behind
+// 8192 keys: eight tiles a head, 877 MB from DRAM in all where 824 cannot be avoided).  The
+// softmax over a sequence's keys is put together from parts: each part is a maximum m, a sum l
+// and an unnormalised o over some of the keys, and
 //   M = max m,  out = sum 2^(m - M) o / sum 2^(m - M) l.
 //
 // Work item = (record, kv head, tile of q heads).  A record is a run of keys for up to 128
@@ -36,15 +39,20 @@
 // What bounds it.  Own keys: the floor is their K and V rows once, but an item is a chain of
 // waits (Q, first K tile, S, softmax, P V, epilogue) of about 2.5 us behind its tiles, and a
 // tile costs one softmax warp about 1500 cycles, whatever few rows it has; with three items'
-// worth of buffers in flight 256 sequences of 1..1500 keys run at 6.2 TB/s (128 us), 64 of 4096
-// at 6.7.  Common keys: the softmax warps' pass over 128 x 128 scores, as in the prefill:
-// 1254 TFLOP/s for 1024 sequences on 8192 keys, 1202 for 32 of 64 heads on 65536.  Both sorts
-// together, 256 sequences with 8192 keys in common and up to 1500 of their own: 149 us, where the
-// bytes take 121 and paged_decode 1160.  The softmax threads hold 255 registers, so an SM has one
-// CTA and four softmax warps.  Forms that shorten an item by more instructions (own rows in
-// quarters, one warp after another; S^T with the keys in lanes) lost 5 to 20 %: of 64 KB of
-// code and more a tile's part no longer stays in the nearest instruction cache (55 KB here),
-// and producers of fewer instructions gained 4 to 10 % everywhere.
+// worth of buffers in flight 256 sequences of 1..1500 keys run at 6.1 TB/s (129 us), 64 of 4096
+// at 6.5.  Common keys: the softmax warps' pass over 128 x 128 scores, as in the prefill:
+// 1260 TFLOP/s for 1024 sequences on 8192 keys, 1200 for 32 of 64 heads on 65536, 928 for 48 on
+// two documents of 30000 and 65536, where a last wave of items and the parts show.  Both
+// sorts together, 256 sequences with 8192 keys in common and up to 1500 of their own: 150 us,
+// where the bytes take 123 and paged_decode 1160.  The softmax threads hold 255 registers (and
+// spill 8 to 12 bytes), so an SM has one CTA and four softmax warps.  Forms that shorten an
+// item by more instructions lost: own rows in quarters, one warp after another, 7 % (2 % gained
+// for long ones), S^T with the keys in lanes 22 %, block ids asked for a tile ahead 3 to 9 %.
+// What they share is 64 KB of code and more, of which a tile's part no longer stays in the
+// nearest instruction cache (about 55 KB here); producers of fewer instructions gained 4 to
+// 10 % everywhere.  head_dim 64 has the same scores to pass for half the bytes: 3.7 TB/s for 256
+// sequences of 1..1500 keys.  Gathered rows (block sizes that are no multiple of 8) come at the
+// pace of one warp's address arithmetic and copies: 2.6 TB/s there; blocks of 8 at 4.6.
 //
 // Keys outside a tile's run and keys of a block id outside the pool have weight 0, and
 // their V rows are zeroed in shared memory, because unused cache slots may hold NaN.
@@ -134,10 +142,18 @@ __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) {
 constexpr int kMaxPlanThreads = 1024;
 constexpr int kStaged = 1024;            // groups held in shared memory
 constexpr int kFew = 4;                  // groups up to which a length's items are counted exactly
-// Fewer common keys than this are attended by each sequence itself.
+// Fewer common keys than this are attended by each sequence itself.  64 sequences in 1, 8 and 32
+// groups, up to 600 own keys, blocks of 16: 16 and 48 common keys together take 1 to 14 % longer
+// than so; 80 to 240 between 12 % more (32 groups, 80 keys: 31.5 us for 28.1) and 8 % less (one
+// group, 240: 29.9 for 32.5).  Without own keys any number is better together (9 us for 20), but
+// a step's token itself is one.
 constexpr int kMinShared = 64;
 // What the plan expects, in ns: a key tile of common keys and of own ones (which come from
-// HBM), the start and end of an item; and the bytes a ns of parts written and read again.
+// HBM), the start and end of an item; and the bytes a ns of parts written and read again.  Taken
+// from runs of one kind of item alone.  Any of them halved or doubled (the tiles' by 1.4),
+// and the three quarters below as a half or as all, changes eight batches of all kinds by -4
+// to +5 %, but for 256 sequences behind 8192 keys, where a common tile of 600, an own one of
+// 2000, an item of 5000 and the half each choose longer common runs: 163 us for 151.
 constexpr float kCommonTile = 850, kOwnTile = 1450, kItemCost = 2500, kPartBytes = 3500;
 
 struct Group {

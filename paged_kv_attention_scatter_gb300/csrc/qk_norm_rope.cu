@@ -25,33 +25,39 @@
 // Arithmetic is on packed pairs of fp32.
 //
 // head_kernel, for few tokens: a CTA takes one token, all of its heads at once, and builds
-// the tables while the rows' loads are in flight.  One token of 24 heads takes 2.4 us, an
+// the tables while the rows' loads are in flight.  One token of 24 heads takes 2.5 us, an
 // empty kernel about as long.  192 threads with two heads each in flight (in 32 bits one: 2047
-// tokens of 24 heads of 80 11.4 us for 12.7), six CTAs an SM (seven spill: up to 30% longer); 128
-// threads took 8% longer for 8191 such tokens, the tables built by half of the threads 15%.
+// tokens of 24 heads of 80 11.5 us for 12.7), six CTAs an SM (some 16-bit forms spill 8 to 20 bytes
+// there; with seven all spill and take up to 30% longer); 128 threads took 8% longer for
+// 8191 such tokens, the tables built by half of the threads 15%.
 //
 // row_kernel, for many: an SM's 16 warps each work through a run of pieces (some heads of a
 // token), with A and B in registers, made once for a token's q and once for its k, and rows
 // that arrive through shared memory two pieces of 4 KB ahead.  head_kernel reads A and B from
 // shared memory for every head and waits for its token's angles before any row: it is bound
-// by those reads and by the wait.  Behind row_kernel stands the issue of its instructions
-// (0.5 to 0.6 of it) and, at 5.6 TB/s, the memory.  head / row kernel, us:
-//   tokens                                        2048        4096        16384
-//   24 heads of 80, 32 bits, partial rotation   11.4/9.3    22.6/14.9   83.9/50.5
-//   40 of 128, 16 bits, pairs, half rotated      9.2/9.6    17.1/15.5   63.6/61.7
-//   24 of 128, bf16, all rotated                 8.0/7.4    13.4/11.8   47.4/39.5
-//   48 of 128, bf16, into the cache             11.9/12.4   20.6/20.5   78.5/72.7
-// so kManyTokens is 2048.  Five stages of 2 KB take 1.6% less for the last and 2 to 8% more for
-// the others at 2048 and 4096 tokens; 20 warps with smaller stages 3% more for the last; 24 and
-// 32 warps spill.
+// by those reads and by the wait.  row_kernel fills no pipe: it issues in 43 to 57% of the cycles
+// and DRAM is busy for 32 to 63% (the rotation of 8191 tokens in 32 bits, 16384 tokens into
+// the cache, 5.6 TB/s): two pieces in flight for each of 16 warps do not hide their latency.
+// head / row kernel, us:
+//   tokens                                         1024        2048        4096        16384
+//   24 heads of 80, 32 bits, partial rotation    7.1/6.7    11.5/9.4   20.6/15.0   75.6/51.3
+//   24 of 128, 32 bits, all rotated              7.4/7.5   11.3/10.1   18.0/17.6   66.6/71.8
+//   40 of 128, 16 bits, pairs, half rotated      6.4/7.4     9.5/9.8   16.8/15.5   62.1/61.0
+//   24 of 128, bf16, all rotated                 5.5/5.7     7.9/7.5   13.2/11.9   48.4/40.4
+//   9 of 128, 16 bits, pairs, half rotated       4.3/4.4     6.1/5.6     9.9/8.2   35.0/22.3
+//   48 of 128, bf16, into the cache              8.3/9.3   12.7/12.8   23.0/20.6  101.8/71.4
+// One threshold for all, kManyTokens: they cross between 1000 and 2500 tokens, whatever the heads.
+// (Whole rotations in 32 bits cross back: 8% at 16384 tokens are given away there.)
+// Five stages of 2 KB take 1.6% less for the last and 2 to 8% more for the others at 2048 and 4096
+// tokens; 20 warps with smaller stages 3% more for the last; 24 and 32 warps spill.
 // Both kernels compute an entry by the same steps: a token's bits are the same in any batch.
 //
 // Equal slots.  Two tokens' rows in one slot could mix, 16 bytes of one and 16 of the other, so
 // that the last token of a slot is found first and alone stores.  head_kernel compares its
 // token's slot with those behind it; row_kernel puts its CTA's slots into a table in shared
 // memory, past which all slots go once, while the first rows arrive: 0.4 us of 512 tokens,
-// 2.7 of 16384 (in the table above row_kernel's column is with it, head_kernel's without).
-// The slots that the table has room for set the tokens of a launch, 150784 on 152 SMs.
+// 2.7 of 16384.  The slots that the table has room for set the tokens of a launch, 150784 on
+// 152 SMs.
 #include <cuda_fp16.h>
 #include <math.h>
 
