@@ -117,8 +117,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 2^30 2^-24 = 64 and more apart (32 below a power of two).
 constexpr float kFarScore = 1073741824.0f;
 
-// The power of two at or below x > 0.
+// The power of two at or below x > 0; of infinity the largest.
 inline float power_below(float x) {
+    if (!(x < INFINITY)) return 0x1p127f;
     int e = 0;
     frexpf(x, &e);
     return ldexpf(1.f, e - 1);

@@ -1149,7 +1149,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             : pkv::fast_exp2(m_run - (mx + kHeadroom));
                                 m_run = mx + kHeadroom;
                                 unit = u;
-                                l_run *= alpha;
+                                // a score that 32 bits do not hold: the row is NaN
+                                l_run *= score < INFINITY ? alpha : NAN;
                             }
                             if (j > 0 && __any_sync(0xffffffffu, raise)) {
                                 // O may only be rescaled once the last P V has finished

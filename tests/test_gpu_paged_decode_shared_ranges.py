@@ -162,3 +162,42 @@ def test_values_of_any_size(cuda, bs, d, e):
                 err = np.abs(got[i, h] - ref)
                 assert np.isfinite(got[i, h]).all(), (i, h, slope)
                 assert (err <= bound).all(), (i, h, slope, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 126, 2.0 ** 127, 3.4e38])
+def test_scales_whose_scores_pass_32_bits(cuda, scale):
+    """Scores of both signs around the ends of 32 bits, times log2 e as the kernel takes them: NaN
+    where the largest passes them, zeros (no keys) where all are -infinite, else the value
+    of the key ahead."""
+    pkv = lib()
+    for size in (0.25, 1.0, 16.0):
+        b = Batch([3, 1, 1], [200, 0, 0], [40, 1, 90, 300, 100], 2, 1, 64, 16, cuda, seed=70)
+        nb = b.tk.shape[0]
+        rng = np.random.default_rng(1)
+        k0 = torch.from_numpy(rng.integers(-127, 127, nb * 16) / 128 * size).to(torch.bfloat16)
+        b.tk[torch.isfinite(b.tk)] = 0
+        flat = b.tk.view(nb * 16, 64)
+        flat[:, 0] = torch.where(flat[:, 0].isnan(), flat[:, 0], k0.to(cuda))
+        b.tq[:], b.tq[:, :, 0] = 0, 1.0
+        for i in range(3):                           # members' copies of a block common in part
+            b.tk[int(b.bt[i, 12]), :8] = b.tk[int(b.bt[0, 12]), :8]
+        got = f64(pkv.paged_decode_shared(b.tq, b.tk, b.tv, b.tbt, b.tctx, b.toff, b.tpre, scale,
+                                          b.max_ctx))
+        k, v = f64(flat[:, 0]), f64(b.tv).reshape(nb * 16, 64)
+        for i in range(5):
+            j = np.arange(b.ctx[i])
+            at = b.bt[i, j // 16].astype(np.int64) * 16 + j % 16
+            top = k[at] == k[at].max()
+            want = v[at][top].mean(0)
+            size_of = np.abs(v[at][top]).mean(0)
+            for h in range(2):
+                with np.errstate(over="ignore"):
+                    scale2 = float(np.float32(scale) * np.float32(1.4426950408889634))
+                most = k[at].max() * scale2
+                if not most <= 3.4028e38:
+                    assert np.isnan(got[i, h]).all(), (size, i, h)
+                elif most < -3.4028e38:
+                    assert (got[i, h] == 0).all(), (size, i, h)
+                else:
+                    bound = 2.0 ** -7 * (size_of + np.abs(want))
+                    assert (np.abs(got[i, h] - want) <= bound).all(), (size, i, h)
