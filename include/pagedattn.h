@@ -702,13 +702,14 @@ PKV_API size_t pkv_paged_decode_shared_workspace_bytes(int32_t batch, int32_t nu
  * Offsets that decrease or leave the batch set PKV_STATUS_BAD_SEQLENS and no group
  * is used; a prefix < 0 or longer than max_context_len or the block table sets it
  * and counts as 0.  Keys in a block id outside the pool are left out.  A query
- * row whose scores are NaN or, times log2 e, pass 32 bits gives NaN.  num_blocks*block_size must be below
- * 2^31 and max_context_len at most 2^30 (PKV_ERR_UNSUPPORTED; the workspace's size is
- * 0 then).
- * Its plan takes 5 us where pkv_paged_decode's takes 2: with 32 q and 8 kv heads of 128
- * and up to 1500 own keys the whole call is as fast as pkv_paged_decode at about
- * 100 common keys of 256 sequences, 200 of 64, 500 of 8, 2500 of two, and faster from there
- * on (64 and 1024: 52 us for 81); a run alone at 64, 100, 130 and 2000.
+ * row whose scores are NaN or, times log2 e, pass 32 bits gives NaN.
+ * num_blocks*block_size must be below 2^31 and max_context_len at most 2^30
+ * (PKV_ERR_UNSUPPORTED; the workspace's size is 0 then).
+ * Its plan takes 5 us where pkv_paged_decode's takes 2: with 32 q and 8 kv heads of
+ * 128 and up to 1500 own keys the whole call is as fast as pkv_paged_decode at
+ * about 100 common keys of 256 sequences, 200 of 64, 500 of 8, 2500 of two, and
+ * faster from there on (64 and 1024: 52 us for 81); a run alone at 64, 100, 130 and
+ * 2000.
  */
 PKV_API int pkv_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache,
                                     const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -144,7 +144,7 @@ constexpr int kStaged = 1024;            // groups held in shared memory
 constexpr int kFew = 4;                  // groups up to which a length's items are counted exactly
 // Fewer common keys than this are attended by each sequence itself.  64 sequences in 1, 8 and 32
 // groups, up to 600 own keys, blocks of 16: 16 and 48 common keys together take 1 to 14 % longer
-// than so; 80 to 240 between 12 % more (32 groups, 80 keys: 31.5 us for 28.1) and 8 % less (one
+// than so; 80 to 240 between 13 % more (32 groups, 80 keys: 31.5 us for 28.1) and 8 % less (one
 // group, 240: 29.9 for 32.5).  Without own keys any number is better together (9 us for 20), but
 // a step's token itself is one.
 constexpr int kMinShared = 64;
